@@ -537,6 +537,166 @@ typedef struct {
 
 qkv_status qsa_gather_attn_ex(const qsa_gather_desc* desc, void* stream);
 
+/*
+ * qkv_append_rope -- append a step's tokens to the cache: rotate q and K by their positions, and
+ * store K and V in the pool's format, in one launch. The pages' models store rotated keys
+ * [E4M3-PR §Implementation scope: cache writes]; the rotation itself is not on the pages.
+ *   For each token t with position p = token_pos[t] and each pair of head dims (a, b) with its
+ *   angle's c = cos_sin[p, i], s = cos_sin[p, rotary_dim / 2 + i]:
+ *     a' = fl(fl(a c) - fl(b s)),  b' = fl(fl(b c) + fl(a s))      (fp32, every step rounded)
+ *   pair i is (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved; dims from rotary_dim on
+ *   are left as they are. q' is rounded once to q's type into q_out. K' is stored as
+ *   qkv_write_int8 / qkv_write_e4m3 would store the fp32 values, V as they store it; a 16-bit
+ *   pool holds K' rounded once and V as it came. Stored bytes equal a plain fp32 program's.
+ *
+ *   size          sizeof(qkv_append_desc), for the layout check (else QKV_ERR_ARG).
+ *   fmt           any format. QKV_BF16 takes bf16 activations, QKV_F16 IEEE half (else
+ *                 QKV_ERR_ARG); the quantised pools take either.
+ *   act_fp16      0: q, k, v, q_out bf16; 1: IEEE half.
+ *   q, q_out      [num_tokens, num_q_heads, head_dim], token t at element t * q_stride /
+ *                 t * q_out_stride. q_out may be q itself with the same stride (in place), else
+ *                 they must not overlap. Both NULL: keys only (num_q_heads is not looked at).
+ *   k, v          [num_tokens, num_kv_heads, head_dim], token t at element t * kv_stride. So q,
+ *                 k and v may be slices of one packed projection. All strides are multiples of
+ *                 8 and at least one token's heads; bases 16 B-aligned.
+ *   cos_sin       fp32 [num_positions, rotary_dim], 16 B-aligned: the pairs' cosines, then their
+ *                 sines (so any frequency scaling is the caller's).
+ *   rotary_dim    a multiple of 16 in [16, head_dim], else QKV_ERR_ARG.
+ *   token_pos     int32 [num_tokens]. -1 skips the token (nothing of it is written, q_out
+ *                 neither). A position outside [-1, num_positions) sets QKV_DEV_BAD_SLOT and
+ *                 skips it likewise.
+ *   slot_mapping  int64 [num_tokens] slot ids; -1 = K and V are not stored (q is still rotated:
+ *                 a token whose K and V are in the cache already). NULL selects paged
+ *                 addressing: token_seq, block_table, num_seqs, max_blocks and block_size as
+ *                 for qkv_write_ex, token_pos being the position in the sequence too. Giving both is
+ *                 QKV_ERR_ARG. An invalid slot, sequence or block sets QKV_DEV_BAD_SLOT; q is
+ *                 rotated, K and V are not stored. Slots must be distinct (duplicates race).
+ *   k_scale, v_scale            fp32 [S, H] for QKV_INT8_SIDE, else NULL.
+ *   k_scale_layer, v_scale_layer  QKV_E4M3: finite and > 0, else QKV_ERR_SCALE.
+ *   num_tokens * (num_q_heads + 2 num_kv_heads) at most 2^33, else QKV_ERR_ARG.
+ */
+typedef struct {
+  size_t size;
+  qkv_format fmt;
+  int act_fp16;
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  int64_t num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int64_t q_stride;
+  int64_t q_out_stride;
+  int64_t kv_stride;
+  const float* cos_sin;
+  int64_t num_positions;
+  int rotary_dim;
+  int interleaved;
+  const int32_t* token_pos;
+  const int64_t* slot_mapping;
+  const int32_t* token_seq;
+  const int32_t* block_table;
+  int64_t num_seqs;
+  int max_blocks;
+  int block_size;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  uint32_t* dev_status;
+} qkv_append_desc;
+
+qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
+
+/*
+ * qkv_prefix_attn -- dense decode attention over a paged pool for a batch whose sequences share a
+ * prefix: every key of the prefix is read once for all rows, then each sequence's own keys.
+ * The pages attend to selected slots only and cache shared prefixes in the engine; this is the
+ * dense operator over the same pool, scales and block tables [HOIST-PR §Changes: scale hoisting;
+ * E4M3-PR §Implementation scope: paged storage, split-K workspace].
+ *   Row r is a query token of sequence row_seq[r] that sees the positions 0 .. row_len[r] - 1 of it:
+ *     s_j = softmax_scale * q[r,g] . K_j,  o = sum_j softmax(s)_j V_j,  lse = log sum_j exp(s_j),
+ *   KV head g / (num_q_heads / num_kv_heads). Position p sits in the slot
+ *     prefix_blocks[p / block_size] * block_size + p % block_size                for p < prefix_len,
+ *     block_table[row_seq[r], p / block_size] * block_size + p % block_size      for p >= prefix_len.
+ *   The prefix may end inside a block; table entries of blocks that lie wholly in the prefix are
+ *   not read. prefix_len = 0 (prefix_blocks NULL) is plain paged decode attention.
+ *
+ *   size          sizeof(qkv_prefix_desc), for the layout check (else QKV_ERR_ARG).
+ *   fmt, k_cache, v_cache, k_scale_tok, v_scale_tok, k_scale_layer, v_scale_layer, num_slots
+ *                 the pool, as for qsa_gather_attn; QKV_F16 with q_fp16 = 1 and QKV_BF16 with
+ *                 q_fp16 = 0 only.
+ *   q             bf16 or (q_fp16) IEEE half [rows, num_q_heads, head_dim], row r at element
+ *                 r * q_stride (a multiple of 8, at least num_q_heads * head_dim); 16 B-aligned.
+ *   prefix_blocks int32 [ceil(prefix_len / block_size)] block ids.
+ *   block_table   int32 [num_seqs, max_blocks] block ids; max_blocks * block_size < 2^31.
+ *   row_seq       int32 [rows]. -1: a padding row, whose out and lse are left as they were.
+ *                 Rows of one sequence that follow each other (draft tokens, a prompt's chunk)
+ *                 share the reads of its keys.
+ *   row_len       int32 [rows]: 0 (the row sees nothing: o = 0, lse = -inf) or in [prefix_len,
+ *                 max_row_len].
+ *   max_row_len   no row is longer; prefix_len <= max_row_len <= max_blocks * block_size, else
+ *                 QKV_ERR_ARG. It sizes the launch (a captured graph keeps it).
+ *   Flagged with QKV_DEV_BAD_INDEX: a row_seq outside [-1, num_seqs) or a row_len outside its
+ *   range (the row is empty), and an unallocated block (id < 0) or a slot >= num_slots among the
+ *   keys that a row sees (the key is masked for the rows that it serves).
+ *   out           [rows, num_q_heads, head_dim] in q's type, contiguous, 16 B-aligned; rounded
+ *                 once. Must not overlap q.
+ *   lse           fp32 [rows, num_q_heads], or NULL.
+ *   workspace     device scratch of workspace_bytes, 16 B-aligned; its contents need not be set.
+ *                 Too small a workspace is QKV_ERR_ARG. Calls that overlap on the GPU -- on two
+ *                 streams, or replays of two captured graphs -- must not share one.
+ *   rows * num_q_heads at most 2^31 - 1, num_slots * num_kv_heads too.
+ * Results do not depend on other rows of the batch, up to rounding; calls with the same arguments
+ * on the same device give the same bits.
+ *
+ * qkv_prefix_attn_workspace -- the bytes that a call of this shape needs on the current device
+ * (0 where one range of keys is enough). Ask for every shape that a program uses: a smaller batch
+ * is cut into more ranges. Launches nothing; a failed device query is QKV_ERR_CUDA.
+ */
+typedef struct {
+  size_t size;
+  qkv_format fmt;
+  int q_fp16;
+  const void* q;
+  int64_t q_stride;
+  int64_t rows;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale_tok;
+  const float* v_scale_tok;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  const int32_t* prefix_blocks;
+  int prefix_len;
+  const int32_t* block_table;
+  int64_t num_seqs;
+  int max_blocks;
+  int block_size;
+  const int32_t* row_seq;
+  const int32_t* row_len;
+  int max_row_len;
+  float softmax_scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* dev_status;
+} qkv_prefix_desc;
+
+qkv_status qkv_prefix_attn_workspace(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int prefix_len, int max_row_len, size_t* bytes);
+qkv_status qkv_prefix_attn(const qkv_prefix_desc* desc, void* stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* qkv_status_str(qkv_status s);
 

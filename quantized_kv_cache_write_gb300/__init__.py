@@ -488,3 +488,202 @@ def qsa_gather_attn_splitk_noalloc(q, fmt: int, k_cache, v_cache, topk_idx, soft
                                             float(v_scale_layer), S, _ptr(topk_idx), topk, float(softmax_scale),
                                             num_splits, _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream))
     _check("qsa_gather_attn_splitk_noalloc", st)
+
+
+class AppendDesc(ctypes.Structure):
+    """qkv_append_desc of include/qkv.h, field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("fmt", _i32), ("act_fp16", _i32), ("q", _p), ("q_out", _p), ("k", _p),
+                ("v", _p), ("num_tokens", _i64), ("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32),
+                ("q_stride", _i64), ("q_out_stride", _i64), ("kv_stride", _i64), ("cos_sin", _p),
+                ("num_positions", _i64), ("rotary_dim", _i32), ("interleaved", _i32), ("token_pos", _p),
+                ("slot_mapping", _p), ("token_seq", _p), ("block_table", _p), ("num_seqs", _i64),
+                ("max_blocks", _i32), ("block_size", _i32), ("k_cache", _p), ("v_cache", _p), ("k_scale", _p),
+                ("v_scale", _p), ("k_scale_layer", _f32), ("v_scale_layer", _f32), ("num_slots", _i64),
+                ("dev_status", _p)]
+
+
+class PrefixDesc(ctypes.Structure):
+    """qkv_prefix_desc of include/qkv.h, field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("fmt", _i32), ("q_fp16", _i32), ("q", _p), ("q_stride", _i64),
+                ("rows", _i64), ("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("k_cache", _p),
+                ("v_cache", _p), ("k_scale_tok", _p), ("v_scale_tok", _p), ("k_scale_layer", _f32),
+                ("v_scale_layer", _f32), ("num_slots", _i64), ("prefix_blocks", _p), ("prefix_len", _i32),
+                ("block_table", _p), ("num_seqs", _i64), ("max_blocks", _i32), ("block_size", _i32), ("row_seq", _p),
+                ("row_len", _p), ("max_row_len", _i32), ("softmax_scale", _f32), ("out", _p), ("lse", _p),
+                ("workspace", _p), ("workspace_bytes", ctypes.c_size_t), ("dev_status", _p)]
+
+
+lib.qkv_append_rope.argtypes = [ctypes.POINTER(AppendDesc), _p]
+lib.qkv_append_rope.restype = ctypes.c_int
+lib.qkv_prefix_attn.argtypes = [ctypes.POINTER(PrefixDesc), _p]
+lib.qkv_prefix_attn.restype = ctypes.c_int
+lib.qkv_prefix_attn_workspace.argtypes = [_i32, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
+lib.qkv_prefix_attn_workspace.restype = ctypes.c_int
+
+_CACHE_BYTES = {QKV_BF16: 2, QKV_F16: 2, QKV_INT8_SIDE: 1, QKV_INT8_INLINE: 1, QKV_E4M3: 1}
+
+
+def _need_cache(name: str, t, fmt: int, H: int, D: int):
+    """A pool tensor [S, H, D] (inline: [S, H, D + 4]) of the format's element size."""
+    size = _CACHE_BYTES.get(fmt)
+    if size is None:
+        raise ValueError(f"unknown pool format {fmt}")
+    width = D + 4 if fmt == QKV_INT8_INLINE else D
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != width or t.element_size() != size or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [num_slots, {H}, {width}] pool of {size}-byte values, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+
+
+def _strided(name: str, t, T: int, H: int, D: int) -> int:
+    """The token stride of a [T, H, D] tensor with contiguous heads (of no matter where T <= 1)."""
+    if t.dim() != 3 or tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    st = t.stride()
+    if (D != 1 and st[2] != 1) or (H != 1 and st[1] != D):
+        raise ValueError(f"{name} needs contiguous heads")
+    return st[0] if T > 1 else H * D
+
+
+def _same_device(first, *rest):
+    """Every tensor must sit on the CUDA device of the first: the kernels take raw pointers."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {dev}")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    return dev
+
+
+def _call_on(dev, fn: str, desc, stream):
+    """Call a descriptor entry point with `dev` current (the C library launches on the current
+    device) and, where none is given, on that device's current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _check(fn, getattr(lib, fn)(ctypes.byref(desc), _stream(stream)))
+    _check(fn, getattr(lib, fn)(ctypes.byref(desc), _stream(stream)))
+
+
+def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=None, q_out=None, slot_mapping=None,
+                    token_seq=None, block_table=None, block_size: int = 1, k_scale=None, v_scale=None,
+                    k_scale_layer: float = 1.0, v_scale_layer: float = 1.0, interleaved: bool = False,
+                    dev_status=None, stream=None):
+    """Rotate q and K by their tokens' positions and store K and V in the pool, in one launch
+    (see qkv_append_rope in qkv.h).
+
+    k, v bf16 or fp16 [T, Hkv, D] (slices of a packed projection are fine); q the same [T, Hq, D]
+    with q_out its rotation (q itself: in place), or both None; cos_sin fp32 [positions,
+    rotary_dim], cosines then sines; token_pos int32 [T] (-1 skips the token); slot_mapping int64
+    [T], or token_seq int32 [T] with block_table int32 [num_seqs, max_blocks] and block_size.
+    """
+    T, H, D, stride = _tokens(k, v)
+    _need_cache("k_cache", k_cache, fmt, H, D)
+    _need_cache("v_cache", v_cache, fmt, H, D)
+    S = k_cache.shape[0]
+    if v_cache.shape[0] != S:
+        raise ValueError("k_cache and v_cache must hold the same number of slots")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [positions, rotary_dim]")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    _need("cos_sin", cos_sin, _F32)
+    _need("token_pos", token_pos, _I32, T)
+    _need("slot_mapping", slot_mapping, _I64, T)
+    _need("token_seq", token_seq, _I32, T)
+    _need("block_table", block_table, _I32)
+    _need("k_scale", k_scale, _F32, S * H)
+    _need("v_scale", v_scale, _F32, S * H)
+    _need("dev_status", dev_status, _WORD)
+    d = AppendDesc()
+    d.size, d.fmt, d.act_fp16 = ctypes.sizeof(AppendDesc), int(fmt), int(k.dtype == torch.float16)
+    if q is not None:
+        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError(f"q and q_out must be {k.dtype} as k and v are")
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        d.q_stride, d.q_out_stride = _strided("q", q, T, Hq, D), _strided("q_out", q_out, T, Hq, D)
+        d.q, d.q_out, d.num_q_heads = q.data_ptr(), q_out.data_ptr(), Hq
+    dev = _same_device(k, v, q, q_out, k_cache, v_cache, cos_sin, token_pos, slot_mapping, token_seq, block_table,
+                       k_scale, v_scale, dev_status)
+    d.k, d.v, d.num_tokens, d.num_kv_heads, d.head_dim, d.kv_stride = k.data_ptr(), v.data_ptr(), T, H, D, stride
+    d.cos_sin, d.num_positions, d.rotary_dim = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+    d.interleaved, d.token_pos = int(bool(interleaved)), token_pos.data_ptr()
+    d.slot_mapping, d.token_seq, d.block_table = _ptr(slot_mapping), _ptr(token_seq), _ptr(block_table)
+    if block_table is not None:
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [num_seqs, max_blocks]")
+        d.num_seqs, d.max_blocks, d.block_size = block_table.shape[0], block_table.shape[1], int(block_size)
+    d.k_cache, d.v_cache, d.k_scale, d.v_scale = k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale)
+    d.k_scale_layer, d.v_scale_layer = float(k_scale_layer), float(v_scale_layer)
+    d.num_slots, d.dev_status = S, _ptr(dev_status)
+    _call_on(dev, "qkv_append_rope", d, stream)
+
+
+def qkv_prefix_attn_workspace(fmt: int, rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                              prefix_len: int, max_row_len: int) -> int:
+    """Workspace bytes of a qkv_prefix_attn call of this shape on the current device."""
+    out = ctypes.c_size_t(0)
+    _check("qkv_prefix_attn_workspace",
+           lib.qkv_prefix_attn_workspace(fmt, rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len,
+                                         ctypes.byref(out)))
+    return out.value
+
+
+def qkv_prefix_attn(q, fmt: int, k_cache, v_cache, block_table, row_seq, row_len, block_size: int,
+                    softmax_scale: float, *, max_row_len: int, num_kv_heads: int = 1, prefix_blocks=None,
+                    prefix_len: int = 0, k_scale_tok=None, v_scale_tok=None, k_scale_layer: float = 1.0,
+                    v_scale_layer: float = 1.0, out, lse=None, workspace=None, dev_status=None, stream=None):
+    """Dense decode attention over a paged pool for rows that share a prefix (see qkv_prefix_attn
+    in qkv.h).
+
+    q bf16 or fp16 [R, Hq, D]; row r is a token of sequence row_seq[r] (int32 [R], -1 padding) and
+    sees positions 0 .. row_len[r] - 1 (int32 [R]); positions below prefix_len go through
+    prefix_blocks (int32), the others through block_table (int32 [num_seqs, max_blocks]). out is
+    [R, Hq, D] in q's type; workspace any contiguous tensor of at least
+    qkv_prefix_attn_workspace bytes.
+    """
+    if q.dim() != 3 or q.dtype not in _ACT16:
+        raise ValueError("q must be bf16 or fp16 [rows, num_q_heads, head_dim]")
+    R, Hq, D = q.shape
+    stride = _strided("q", q, R, Hq, D)
+    _need_cache("k_cache", k_cache, fmt, num_kv_heads, D)
+    _need_cache("v_cache", v_cache, fmt, num_kv_heads, D)
+    S = k_cache.shape[0]
+    if v_cache.shape[0] != S:
+        raise ValueError("k_cache and v_cache must hold the same number of slots")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_seqs, max_blocks]")
+    _need("block_table", block_table, _I32)
+    _need("row_seq", row_seq, _I32, R)
+    _need("row_len", row_len, _I32, R)
+    _expect_shape("out", out, (R, Hq, D))
+    _expect_shape("lse", lse, (R, Hq))
+    _need("out", out, (q.dtype,))
+    _need("lse", lse, _F32)
+    _need("k_scale_tok", k_scale_tok, _F32, S * num_kv_heads)
+    _need("v_scale_tok", v_scale_tok, _F32, S * num_kv_heads)
+    _need("dev_status", dev_status, _WORD)
+    if prefix_len > 0:
+        if prefix_blocks is None or block_size < 1:
+            raise ValueError("a shared prefix needs prefix_blocks and a block_size")
+        _need("prefix_blocks", prefix_blocks, _I32)
+        if prefix_blocks.numel() * block_size < prefix_len:
+            raise ValueError(f"prefix_blocks must cover {prefix_len} positions, got {prefix_blocks.numel()} blocks")
+    d = PrefixDesc()
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _same_device(q, k_cache, v_cache, block_table, row_seq, row_len, out, lse, k_scale_tok, v_scale_tok,
+                       prefix_blocks, workspace, dev_status)
+    d.size, d.fmt, d.q_fp16 = ctypes.sizeof(PrefixDesc), int(fmt), int(q.dtype == torch.float16)
+    d.q, d.q_stride, d.rows, d.num_q_heads, d.num_kv_heads, d.head_dim = q.data_ptr(), stride, R, Hq, num_kv_heads, D
+    d.k_cache, d.v_cache, d.num_slots = k_cache.data_ptr(), v_cache.data_ptr(), S
+    d.k_scale_tok, d.v_scale_tok = _ptr(k_scale_tok), _ptr(v_scale_tok)
+    d.k_scale_layer, d.v_scale_layer = float(k_scale_layer), float(v_scale_layer)
+    if prefix_len != 0:
+        d.prefix_blocks, d.prefix_len = _ptr(prefix_blocks), int(prefix_len)
+    d.block_table, d.num_seqs, d.max_blocks, d.block_size = block_table.data_ptr(), block_table.shape[0], \
+        block_table.shape[1], int(block_size)
+    d.row_seq, d.row_len, d.max_row_len = row_seq.data_ptr(), row_len.data_ptr(), int(max_row_len)
+    d.softmax_scale, d.out, d.lse, d.dev_status = float(softmax_scale), out.data_ptr(), _ptr(lse), _ptr(dev_status)
+    _call_on(dev, "qkv_prefix_attn", d, stream)

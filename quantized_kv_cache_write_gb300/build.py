@@ -41,8 +41,15 @@ SOURCES = [
     "gather_f16q_int8_inline.cu",
     "gather_f16q_e4m3.cu",
     "gather_f16q_f16.cu",
+    "append.cu",
+    "prefix_int8_side.cu",
+    "prefix_int8_inline.cu",
+    "prefix_e4m3.cu",
+    "prefix_bf16.cu",
+    "prefix_f16.cu",
+    "prefix_merge.cu",
 ]
-HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh"]
+HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "prefix_attn.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -457,3 +457,251 @@ qkv_status qsa_splitk_merge(const float* o_part, const float* lse_part, int64_t 
 }
 
 }  // extern "C"
+
+namespace {
+
+// The descriptor's paged or slot-id addressing, and the inputs of an append.
+qkv_status check_append(const qkv_append_desc* d) {
+  const bool paged = d->slot_mapping == nullptr;
+  if (!paged && (d->token_seq || d->block_table)) return QKV_ERR_ARG;  // one addressing only
+  const bool f16 = d->act_fp16 == 1;
+  switch (d->fmt) {
+    case QKV_BF16: if (f16) return QKV_ERR_ARG; break;  // a 16-bit pool takes activations of its own type
+    case QKV_F16: if (!f16) return QKV_ERR_ARG; break;
+    case QKV_INT8_SIDE:
+    case QKV_INT8_INLINE:
+    case QKV_E4M3: break;
+    default: return QKV_ERR_ARG;
+  }
+  if (d->num_q_heads < 0 || (d->q == nullptr) != (d->q_out == nullptr)) return QKV_ERR_ARG;
+  if (d->q != nullptr && d->num_q_heads < 1) return QKV_ERR_ARG;
+  const int hq = d->q != nullptr ? d->num_q_heads : 0;
+  const qkv::WritePaging pg{d->token_seq, d->token_pos, d->block_table, d->num_seqs, d->max_blocks, d->block_size};
+  qkv_status st = check_write_inputs(d->k, d->v, d->num_tokens, d->num_kv_heads, d->head_dim, d->kv_stride,
+                                     d->slot_mapping, d->k_cache, d->v_cache, d->num_slots, paged ? &pg : nullptr);
+  if (st != QKV_OK) return st;
+  if (d->num_positions < 0 || d->rotary_dim < 16 || d->rotary_dim % 16 != 0 || d->rotary_dim > d->head_dim)
+    return QKV_ERR_ARG;
+  if (d->interleaved != 0 && d->interleaved != 1) return QKV_ERR_ARG;
+  const bool side = d->fmt == QKV_INT8_SIDE;
+  if (side ? (!d->k_scale || !d->v_scale) && d->num_tokens > 0 : d->k_scale || d->v_scale) return QKV_ERR_ARG;
+  if (d->fmt == QKV_E4M3 && (!finite_positive(d->k_scale_layer) || !finite_positive(d->v_scale_layer)))
+    return QKV_ERR_SCALE;
+  if (d->num_tokens == 0) return QKV_OK;
+  // at most one warp per row: T (Hq + 2 H) warps of 32 threads must fit a grid of 2^31 - 1 blocks of 256
+  const int64_t rows = static_cast<int64_t>(hq) + 2 * static_cast<int64_t>(d->num_kv_heads);
+  if (rows > INT32_MAX || d->num_tokens > (int64_t(1) << 33) / rows) return QKV_ERR_ARG;
+  if (!d->token_pos || !d->cos_sin) return QKV_ERR_ARG;
+  if (hq > 0) {
+    const int64_t row = static_cast<int64_t>(hq) * d->head_dim;
+    if (d->q_stride < row || d->q_out_stride < row) return QKV_ERR_ARG;
+    if (d->q_stride % 8 != 0 || d->q_out_stride % 8 != 0 || !aligned(d->q, 16) || !aligned(d->q_out, 16))
+      return QKV_ERR_ALIGN;
+  }
+  if (!aligned(d->token_pos, 4) || !aligned(d->cos_sin, 16)) return QKV_ERR_ALIGN;
+  if (!aligned(d->k_cache, 16) || !aligned(d->v_cache, 16)) return QKV_ERR_ALIGN;
+  if (side && (!aligned(d->k_scale, 4) || !aligned(d->v_scale, 4))) return QKV_ERR_ALIGN;
+  if (d->dev_status && !aligned(d->dev_status, 4)) return QKV_ERR_ALIGN;
+  return QKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qkv_status qkv_append_rope(const qkv_append_desc* d, void* stream) {
+  if (d == nullptr || d->size != sizeof(qkv_append_desc)) return QKV_ERR_ARG;
+  if (d->act_fp16 != 0 && d->act_fp16 != 1) return QKV_ERR_ARG;
+  const qkv_status st = check_append(d);
+  if (st != QKV_OK || d->num_tokens == 0) return st;
+  qkv::AppendArgs a;
+  a.q = static_cast<const uint16_t*>(d->q);
+  a.q_out = static_cast<uint16_t*>(d->q_out);
+  a.k = static_cast<const uint16_t*>(d->k);
+  a.v = static_cast<const uint16_t*>(d->v);
+  a.num_tokens = d->num_tokens;
+  a.num_q_heads = d->q != nullptr ? d->num_q_heads : 0;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.q_stride = d->q_stride;
+  a.q_out_stride = d->q_out_stride;
+  a.kv_stride = d->kv_stride;
+  a.cos_sin = d->cos_sin;
+  a.num_positions = d->num_positions;
+  a.rotary_dim = d->rotary_dim;
+  a.interleaved = d->interleaved == 1;
+  a.token_pos = d->token_pos;
+  a.slot_mapping = d->slot_mapping;
+  a.paging = qkv::WritePaging{d->token_seq, d->token_pos, d->block_table, d->num_seqs, d->max_blocks, d->block_size};
+  a.k_cache = static_cast<uint8_t*>(d->k_cache);
+  a.v_cache = static_cast<uint8_t*>(d->v_cache);
+  a.k_scale = d->k_scale;
+  a.v_scale = d->v_scale;
+  a.k_scale_layer = d->k_scale_layer;
+  a.v_scale_layer = d->v_scale_layer;
+  a.num_slots = d->num_slots;
+  a.dev_status = d->dev_status;
+  return cuda_status(qkv::launch_append_rope(a, d->fmt, d->act_fp16 == 1, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+// How a shared-prefix call is cut into key ranges: enough CTAs to fill the GPU a few times over
+// (ragged rows balance), none with fewer than 256 keys.
+struct PrefixPlan {
+  int prefix_parts, own_parts, prefix_chunk;
+  int64_t prefix_items, own_items;
+  int parts() const { return prefix_parts + own_parts; }
+  int64_t rows_heads;
+  int head_dim;
+  // partial outputs, then partial log-sum-exps; a single part writes the output itself
+  size_t o_bytes() const { return parts() > 1 ? static_cast<size_t>(parts()) * rows_heads * head_dim * 4 : 0; }
+  size_t bytes() const { return o_bytes() + (parts() > 1 ? static_cast<size_t>(parts()) * rows_heads * 4 : 0); }
+};
+
+qkv_status check_prefix_shape(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv_heads, int head_dim,
+                              int prefix_len, int max_row_len) {
+  if (rows < 0 || prefix_len < 0 || max_row_len < prefix_len) return QKV_ERR_ARG;
+  if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0) return QKV_ERR_ARG;
+  if (!qkv::head_dim_ok(head_dim) || num_q_heads / num_kv_heads > kMaxGroup) return QKV_ERR_UNSUPPORTED;
+  if (fmt != QKV_BF16 && fmt != QKV_INT8_SIDE && fmt != QKV_INT8_INLINE && fmt != QKV_E4M3 && fmt != QKV_F16)
+    return QKV_ERR_ARG;
+  if (rows > INT32_MAX / num_q_heads) return QKV_ERR_ARG;  // (row, head) pairs are numbered in 32 bits
+  return QKV_OK;
+}
+
+qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head_dim, int prefix_len,
+                       int max_row_len, PrefixPlan* p) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QKV_ERR_CUDA;
+  const int G = num_q_heads / num_kv_heads, own = max_row_len - prefix_len;
+  p->rows_heads = rows * num_q_heads;
+  p->head_dim = head_dim;
+  const int64_t ptiles = ceil_div(rows * G, 16) * num_kv_heads;
+  const int64_t otiles = rows * ceil_div(G, 16) * num_kv_heads;
+  auto parts_of = [&](int64_t tiles, int keys) -> int {
+    if (keys <= 0 || tiles <= 0) return 0;
+    const int64_t want = ceil_div(8 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, 256);
+    return static_cast<int>(want < most ? want : most);
+  };
+  p->prefix_parts = parts_of(ptiles, prefix_len);
+  p->prefix_chunk = 0;
+  if (p->prefix_parts > 0) {
+    p->prefix_chunk = static_cast<int>(ceil_div(ceil_div(prefix_len, p->prefix_parts), 64) * 64);
+    p->prefix_parts = static_cast<int>(ceil_div(prefix_len, p->prefix_chunk));
+  }
+  p->own_parts = parts_of(otiles, own);
+  p->prefix_items = ptiles * p->prefix_parts;
+  p->own_items = otiles * p->own_parts;
+  if (p->prefix_items > INT32_MAX || p->own_items > INT32_MAX) return QKV_ERR_ARG;
+  return QKV_OK;
+}
+
+cudaError_t launch_prefix_mma(const qkv::PrefixArgs& a, qkv_format fmt, bool own, cudaStream_t s) {
+  switch (fmt) {
+    case QKV_BF16: return qkv::launch_prefix_mma_bf16(a, own, s);
+    case QKV_F16: return qkv::launch_prefix_mma_f16(a, own, s);
+    case QKV_INT8_SIDE: return qkv::launch_prefix_mma_int8_side(a, own, s);
+    case QKV_INT8_INLINE: return qkv::launch_prefix_mma_int8_inline(a, own, s);
+    case QKV_E4M3: return qkv::launch_prefix_mma_e4m3(a, own, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+extern "C" {
+
+qkv_status qkv_prefix_attn_workspace(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int prefix_len, int max_row_len, size_t* bytes) {
+  if (!bytes) return QKV_ERR_ARG;
+  qkv_status st = check_prefix_shape(fmt, rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len);
+  if (st != QKV_OK) return st;
+  PrefixPlan p;
+  st = plan_prefix(rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len, &p);
+  if (st == QKV_OK) *bytes = p.bytes();
+  return st;
+}
+
+qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
+  if (d == nullptr || d->size != sizeof(qkv_prefix_desc)) return QKV_ERR_ARG;
+  if (d->q_fp16 != 0 && d->q_fp16 != 1) return QKV_ERR_ARG;
+  qkv_status st = check_prefix_shape(d->fmt, d->rows, d->num_q_heads, d->num_kv_heads, d->head_dim, d->prefix_len,
+                                     d->max_row_len);
+  if (st != QKV_OK) return st;
+  if ((d->fmt == QKV_F16 && !d->q_fp16) || (d->fmt == QKV_BF16 && d->q_fp16)) return QKV_ERR_ARG;
+  if (!std::isfinite(d->softmax_scale) || d->num_slots < 0) return QKV_ERR_ARG;
+  if (d->fmt == QKV_E4M3 && (!finite_positive(d->k_scale_layer) || !finite_positive(d->v_scale_layer)))
+    return QKV_ERR_SCALE;
+  const bool side = d->fmt == QKV_INT8_SIDE;
+  if (side != (d->k_scale_tok != nullptr) || side != (d->v_scale_tok != nullptr)) return QKV_ERR_ARG;
+  if (d->num_seqs < 1 || d->max_blocks < 1 || d->block_size < 1) return QKV_ERR_ARG;
+  if (static_cast<int64_t>(d->max_blocks) * d->block_size > INT32_MAX) return QKV_ERR_ARG;
+  if (d->max_row_len > static_cast<int64_t>(d->max_blocks) * d->block_size) return QKV_ERR_ARG;
+  if (d->num_slots > INT32_MAX / d->num_kv_heads) return QKV_ERR_UNSUPPORTED;  // records are numbered in 32 bits
+  if (d->q_stride < static_cast<int64_t>(d->num_q_heads) * d->head_dim) return QKV_ERR_ARG;
+  if (d->rows == 0) return QKV_OK;
+  if (!d->q || !d->out || !d->k_cache || !d->v_cache || !d->block_table || !d->row_seq || !d->row_len) return QKV_ERR_ARG;
+  if (d->prefix_len > 0 && !d->prefix_blocks) return QKV_ERR_ARG;
+  if (d->q_stride % 8 != 0 || !aligned(d->q, 16) || !aligned(d->out, 16)) return QKV_ERR_ALIGN;
+  if (!aligned(d->k_cache, 16) || !aligned(d->v_cache, 16)) return QKV_ERR_ALIGN;
+  if (side && (!aligned(d->k_scale_tok, 4) || !aligned(d->v_scale_tok, 4))) return QKV_ERR_ALIGN;
+  if (!aligned(d->prefix_blocks, 4) || !aligned(d->block_table, 4) || !aligned(d->row_seq, 4) ||
+      !aligned(d->row_len, 4) || !aligned(d->lse, 4) || !aligned(d->dev_status, 4) || !aligned(d->workspace, 16))
+    return QKV_ERR_ALIGN;
+
+  PrefixPlan p;
+  st = plan_prefix(d->rows, d->num_q_heads, d->num_kv_heads, d->head_dim, d->prefix_len, d->max_row_len, &p);
+  if (st != QKV_OK) return st;
+  if (p.bytes() > 0 && (!d->workspace || d->workspace_bytes < p.bytes())) return QKV_ERR_ARG;
+
+  qkv::PrefixArgs a;
+  a.q = static_cast<const uint16_t*>(d->q);
+  a.q_stride = d->q_stride;
+  a.q_f16 = d->q_fp16 == 1;
+  a.rows = d->rows;
+  a.num_q_heads = d->num_q_heads;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.k_cache = static_cast<const uint8_t*>(d->k_cache);
+  a.v_cache = static_cast<const uint8_t*>(d->v_cache);
+  a.k_scale_tok = d->k_scale_tok;
+  a.v_scale_tok = d->v_scale_tok;
+  a.k_scale_layer = d->k_scale_layer;
+  a.v_scale_layer = d->v_scale_layer;
+  a.num_slots = d->num_slots;
+  a.prefix_blocks = d->prefix_blocks;
+  a.prefix_len = d->prefix_len;
+  a.block_table = d->block_table;
+  a.num_seqs = d->num_seqs;
+  a.max_blocks = d->max_blocks;
+  a.block_size = d->block_size;
+  a.row_seq = d->row_seq;
+  a.row_len = d->row_len;
+  a.max_row_len = d->max_row_len;
+  a.softmax_scale = d->softmax_scale;
+  a.out = static_cast<uint16_t*>(d->out);
+  a.lse = d->lse;
+  a.dev_status = d->dev_status;
+  const bool direct = p.parts() == 1;
+  a.o_part = direct ? nullptr : static_cast<float*>(d->workspace);
+  a.lse_part = direct ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + p.o_bytes());
+  a.prefix_parts = p.prefix_parts;
+  a.own_parts = p.own_parts;
+  a.prefix_chunk = p.prefix_chunk;
+  a.prefix_items = p.prefix_items;
+  a.own_items = p.own_items;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (p.prefix_parts > 0) e = launch_prefix_mma(a, d->fmt, false, s);
+  if (e == cudaSuccess && p.own_parts > 0) e = launch_prefix_mma(a, d->fmt, true, s);
+  if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, d->fmt == QKV_E4M3 ? d->v_scale_layer : 1.f, s);
+  return cuda_status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,10 @@
+// Shared-prefix decode attention over f16 pools (see prefix_attn.cuh).
+#include "prefix_attn.cuh"
+
+namespace qkv {
+
+cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool own, cudaStream_t stream) {
+  return prefix::launch_mma<QKV_F16>(a, own, stream);
+}
+
+}  // namespace qkv

@@ -1,0 +1,10 @@
+// Shared-prefix decode attention over int8_inline pools (see prefix_attn.cuh).
+#include "prefix_attn.cuh"
+
+namespace qkv {
+
+cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool own, cudaStream_t stream) {
+  return prefix::launch_mma<QKV_INT8_INLINE>(a, own, stream);
+}
+
+}  // namespace qkv

@@ -111,6 +111,84 @@ cudaError_t gather_ctas_per_sm_int8_side(int* n);
 cudaError_t gather_ctas_per_sm_int8_inline(int* n);
 cudaError_t gather_ctas_per_sm_e4m3(int* n);
 
+// Arguments of one append launch (already validated on the host).
+struct AppendArgs {
+  const uint16_t* q;  // 16-bit activations, or null (then num_q_heads is 0)
+  uint16_t* q_out;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int64_t q_stride;  // elements between tokens
+  int64_t q_out_stride;
+  int64_t kv_stride;
+  const float* cos_sin;  // [num_positions, rotary_dim]: cos of the pairs, then sin
+  int64_t num_positions;
+  int rotary_dim;  // a multiple of 16
+  bool interleaved;
+  const int32_t* token_pos;
+  const int64_t* slot_mapping;  // null: paged
+  WritePaging paging;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scale;
+  float* v_scale;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  uint32_t* dev_status;
+};
+cudaError_t launch_append_rope(const AppendArgs& a, qkv_format fmt, bool f16, cudaStream_t stream);
+
+// Arguments of one shared-prefix attention call (already validated on the host).
+struct PrefixArgs {
+  const uint16_t* q;  // [rows, Hq, D], bf16 or (q_f16) IEEE half, rows q_stride elements apart
+  int64_t q_stride;
+  bool q_f16;
+  int64_t rows;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale_tok;
+  const float* v_scale_tok;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  const int32_t* prefix_blocks;
+  int prefix_len;
+  const int32_t* block_table;
+  int64_t num_seqs;
+  int max_blocks;
+  int block_size;
+  const int32_t* row_seq;
+  const int32_t* row_len;
+  int max_row_len;
+  float softmax_scale;
+  uint16_t* out;  // [rows, Hq, D] in q's type
+  float* lse;     // [rows, Hq] or null
+  uint32_t* dev_status;
+  // partial results [prefix_parts + own_parts][rows][Hq] of the key ranges; null where one part
+  // writes out itself
+  float* o_part;
+  float* lse_part;
+  int prefix_parts;  // ranges of prefix_chunk keys of the shared prefix
+  int own_parts;     // ranges of the keys behind it (of a length that goes by the row's)
+  int prefix_chunk;
+  int64_t prefix_items;  // CTAs of each launch
+  int64_t own_items;
+};
+// the mma.sync tiles of 16 (row, head) pairs, over the prefix or (own) the keys behind it
+cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixArgs& a, float v_scale_post, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device helpers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
