@@ -47,9 +47,14 @@ SOURCES = [
     "prefix_e4m3.cu",
     "prefix_bf16.cu",
     "prefix_f16.cu",
+    "prefix_umma_int8_side.cu",
+    "prefix_umma_int8_inline.cu",
+    "prefix_umma_e4m3.cu",
+    "prefix_umma_bf16.cu",
+    "prefix_umma_f16.cu",
     "prefix_merge.cu",
 ]
-HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "prefix_attn.cuh"]
+HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "prefix_attn.cuh", "prefix_umma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -550,10 +550,15 @@ namespace {
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
+// Pairs of (row, query head of a KV head) above which the prefix runs on tcgen05.
+constexpr int64_t kUmmaMinPairs = 32;
+
 // How a shared-prefix call is cut into key ranges: enough CTAs to fill the GPU a few times over
 // (ragged rows balance), none with fewer than 256 keys.
 struct PrefixPlan {
   int prefix_parts, own_parts, prefix_chunk;
+  int umma_cg, umma_pairs, umma_keys, umma_ptiles;
+  int64_t umma_tiles, umma_teams;
   int64_t prefix_items, own_items;
   int parts() const { return prefix_parts + own_parts; }
   int64_t rows_heads;
@@ -595,11 +600,35 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
     p->prefix_chunk = static_cast<int>(ceil_div(ceil_div(prefix_len, p->prefix_parts), 64) * 64);
     p->prefix_parts = static_cast<int>(ceil_div(prefix_len, p->prefix_chunk));
   }
+  p->umma_cg = 0, p->umma_pairs = 0, p->umma_keys = 0, p->umma_ptiles = 0, p->umma_tiles = 0, p->umma_teams = 0;
+  if (prefix_len > 0 && rows * G > kUmmaMinPairs) {
+    p->umma_cg = rows * G > 128 ? 2 : 1;  // one SM's tile holds 128 pairs
+    p->umma_pairs = p->umma_cg == 1 ? 128 : head_dim == 128 ? 512 : 256;
+    p->umma_keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
+    const int64_t nb = ceil_div(prefix_len, p->umma_keys), pt = ceil_div(rows * G, p->umma_pairs);
+    p->umma_ptiles = static_cast<int>(pt);
+    p->umma_tiles = pt * num_kv_heads;
+    const int64_t total = p->umma_tiles * nb, teams = sms / p->umma_cg;
+    p->umma_teams = total < teams ? total : teams;
+    // ranges of at least total / teams units: a tile's nb units touch at most this many
+    p->prefix_parts = static_cast<int>(ceil_div(nb, total / p->umma_teams) + 1);
+  }
   p->own_parts = parts_of(otiles, own);
   p->prefix_items = ptiles * p->prefix_parts;
   p->own_items = otiles * p->own_parts;
   if (p->prefix_items > INT32_MAX || p->own_items > INT32_MAX) return QKV_ERR_ARG;
   return QKV_OK;
+}
+
+cudaError_t launch_prefix_umma(const qkv::PrefixArgs& a, qkv_format fmt, cudaStream_t s) {
+  switch (fmt) {
+    case QKV_BF16: return qkv::launch_prefix_umma_bf16(a, s);
+    case QKV_F16: return qkv::launch_prefix_umma_f16(a, s);
+    case QKV_INT8_SIDE: return qkv::launch_prefix_umma_int8_side(a, s);
+    case QKV_INT8_INLINE: return qkv::launch_prefix_umma_int8_inline(a, s);
+    case QKV_E4M3: return qkv::launch_prefix_umma_e4m3(a, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_prefix_mma(const qkv::PrefixArgs& a, qkv_format fmt, bool own, cudaStream_t s) {
@@ -698,7 +727,13 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.own_items = p.own_items;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (p.prefix_parts > 0) e = launch_prefix_mma(a, d->fmt, false, s);
+  a.umma_cg = p.umma_cg;
+  a.umma_pairs = p.umma_pairs;
+  a.umma_keys = p.umma_keys;
+  a.umma_ptiles = p.umma_ptiles;
+  a.umma_tiles = p.umma_tiles;
+  a.umma_teams = p.umma_teams;
+  if (p.prefix_parts > 0) e = p.umma_cg > 0 ? launch_prefix_umma(a, d->fmt, s) : launch_prefix_mma(a, d->fmt, false, s);
   if (e == cudaSuccess && p.own_parts > 0) e = launch_prefix_mma(a, d->fmt, true, s);
   if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, d->fmt == QKV_E4M3 ? d->v_scale_layer : 1.f, s);
   return cuda_status(e);

@@ -1,0 +1,813 @@
+// The shared prefix of qkv_prefix_attn on the fifth-generation tensor cores: S = Q K^T and O += P V by
+// tcgen05.mma with accumulators in tensor memory, for batches with many (row, query head) pairs.
+//
+// The pairs of all rows (row-major) are the M of both products. A team of CG SMs (a cluster; the
+// MMAs span both SMs of a pair) takes NT tiles of 128 CG pairs: two tiles for 128-wide heads, so that one
+// tile's softmax runs under the other's MMAs; one for 256-wide heads, whose O takes half of tensor
+// memory, with S double-buffered instead. The (tile, KV head) x key-block units of the call are cut
+// into equal contiguous ranges, one per team, one CTA per SM; a range covers part of one tile's keys or
+// the end of one and the start of the next, and every such segment leaves a partial result that the
+// merge joins. A pair's SMs each hold their own 128 pairs' Q, S, P and O, and half of K (by keys)
+// and V (by dims): each converts half of the pool's values, and shared memory is read and written half as
+// often per MMA as with one SM.
+//
+// Warps: softmax (four per tile, one thread per pair), four producers, one for the scales, one MMA issuer
+// (of the team's first SM). Slots (rows of 128 B, 128 B swizzle) pass from the producers to the MMA
+// warp in the order K_0 K_1 V_0 K_2 V_1 ...; K is K-major, V MN-major, and both are stored alike, one
+// 128 B row per key and 64 dims.
+//   producers: block list -> records -> 16 B loads into registers, converted to fp16 (codes are exact) and
+//     stored to the slot once it is free; the registers take the next block's loads at once, so a
+//     K and a V slot are in flight all the time. 16-bit pools skip the registers (cp.async).
+//   scales: K and V scales, the mask of the block's keys and the largest V scale into a small ring.
+//   MMA: one thread. P is the A operand in tensor memory, in the columns of the S it was made from.
+//   softmax: y = S ks fac (log2 units). Reference R = M + E - 7: M follows the row's maximum lazily
+//     (raised when a logit passes it by 2^8), E is a power-of-two bound on the V scales, so p vs 2^-R
+//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both.
+// Arithmetic as in prefix_attn.cuh: exact codes, logits and sums in fp32, p rounded once.
+//
+// Every wait is bounded: a wait that runs out sets QKV_DEV_TIMEOUT, the CTA drains its MMAs, frees its
+// tensor memory and returns.
+#pragma once
+
+#include "prefix_attn.cuh"
+
+namespace qkv {
+namespace prefix {
+
+constexpr int kTileM = 128;  // pairs of a tile on one SM
+constexpr int kProdWarps = 4;
+constexpr uint32_t kWaitLimit = 1u << 22;  // mbarrier polls before a wait is declared lost (about a second)
+constexpr int kScRing = 4;
+// keys of a block: 128; 64 where one SM holds 256-wide heads alone
+constexpr int umma_block_keys(int head_dim, int cg) { return head_dim == 256 && cg == 1 ? 64 : 128; }
+
+template <int FMT, int HD, int NT, int CG>
+struct Umma {
+  using F = Fmt<FMT>;
+  static constexpr int KB = umma_block_keys(HD, CG);
+  static constexpr int kSoftWarps = 4 * NT, kScWarp = kSoftWarps + kProdWarps, kMmaWarp = kScWarp + 1;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kKRows = KB / CG, kVDims = HD / CG;  // this SM's part of a block
+  static constexpr uint32_t kSlotBytes = uint32_t(KB) * HD * 2 / CG;
+  static constexpr uint32_t kQTile = kTileM * HD * 2;
+  static constexpr int kSlots = kSlotBytes == 16384 ? 8 : NT * HD >= 256 ? 4 : 5;
+  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kSc = kRing + kSlots * kSlotBytes;
+  // per block: K scales, V scales, key mask (4 words), largest V scale
+  static constexpr uint32_t kScVs = 4 * KB, kScMask = 8 * KB, kScVmax = kScMask + 16, kScStage = kScVmax + 16;
+  static constexpr uint32_t kBar = kSc + kScRing * kScStage;
+  static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
+                            kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
+                            kQFull = kScEmpty + 8 * kScRing, kDrain = kQFull + 8, kTmemSlot = kDrain + 8,
+                            kFlag = kTmemSlot + 4, kSmem = kFlag + 4 + 1024;
+  static_assert(kSmem <= 232448, "one CTA per SM");
+  // tensor memory columns: O of each tile, then two S buffers
+  static constexpr uint32_t kO = 0, kS = NT * HD;
+  static_assert(kS + 2 * KB <= 512, "tensor memory");
+  // instruction descriptors (kind::f16, fp32 accumulator): A / B type at bits 7 and 10 (0 fp16, 1 bf16),
+  // B MN-major at bit 16, N / 8 at bit 17, M / 16 at bit 24
+  static constexpr uint32_t kType = F::kBf16 ? (1u << 7) | (1u << 10) : 0u;
+  static constexpr uint32_t kM = uint32_t(kTileM * CG / 16) << 24;
+  static constexpr uint32_t kIdS = (1u << 4) | kType | (uint32_t(KB / 8) << 17) | kM;
+  static constexpr uint32_t kIdO = (1u << 4) | kType | (1u << 16) | (uint32_t(HD / 8) << 17) | kM;
+};
+
+// 128 B-swizzled shared-memory matrix descriptor: address, leading and stride byte offsets, version 1.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+template <int CG>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+// Arrive on this barrier (of both SMs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit_to(uint32_t mbar) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(mbar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void team_tmem_alloc(uint32_t smem_dst) {
+  if (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_dst), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  } else {
+    tmem_alloc(smem_dst, 512);
+    tmem_relinquish_alloc_permit();
+  }
+}
+template <int CG>
+__device__ __forceinline__ void team_tmem_dealloc(uint32_t taddr) {
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(512u) : "memory");
+  else
+    tmem_dealloc(taddr, 512);
+}
+// Every thread of the team.
+template <int CG>
+__device__ __forceinline__ void team_sync() {
+  if (CG == 2) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+__device__ __forceinline__ void bar_init(uint32_t mbar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mbar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t mbar) {
+  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(mbar) : "memory");
+}
+// Arrive on the barrier at this offset in the team's first SM.
+template <int CG>
+__device__ __forceinline__ void lead_arrive(uint32_t mbar) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, 0;\n"
+        " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n}\n" ::"r"(mbar)
+        : "memory");
+  else
+    bar_arrive(mbar);
+}
+__device__ __forceinline__ bool bar_try(uint32_t mbar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(mbar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+// Wait for the phase of the given parity; false when the polls ran out or the CTA's stop flag is up.
+__device__ __forceinline__ bool bar_wait(uint32_t mbar, uint32_t parity, uint32_t flag) {
+  for (uint32_t it = 0; it < kWaitLimit; ++it) {
+    if (bar_try(mbar, parity)) return true;
+    if ((it & 255u) == 255u && lds32(flag) != 0u) return false;
+  }
+  sts32(flag, 1u);
+  return false;
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// Four floats times the four that `f` holds the bits of.
+__device__ __forceinline__ void f2scale2(float* v, const uint4& f) {
+  f2scale(v, f2pack(__uint_as_float(f.x), __uint_as_float(f.y)));
+  f2scale(v + 2, f2pack(__uint_as_float(f.z), __uint_as_float(f.w)));
+}
+
+// The team whose range [i total / n, (i + 1) total / n) holds unit x.
+__device__ __forceinline__ int64_t team_of(int64_t x, int64_t total, int64_t n) { return ((x + 1) * n - 1) / total; }
+
+// A team's next segment: the part of its unit range that lies in one (KV head, pair tile).
+struct Segment {
+  int64_t u, end;  // units still to do
+  int64_t total, n;
+  int nb;          // key blocks of the prefix
+  int team;
+  int tile, b0, b1, part;
+  __device__ __forceinline__ bool next() {
+    if (u >= end) return false;
+    tile = static_cast<int>(u / nb);
+    const int64_t t0 = static_cast<int64_t>(tile) * nb;
+    b0 = static_cast<int>(u - t0);
+    b1 = static_cast<int>(min(end - t0, static_cast<int64_t>(nb)));
+    part = static_cast<int>(team - team_of(t0, total, n));
+    u = t0 + b1;
+    return true;
+  }
+};
+template <int CG>
+__device__ __forceinline__ Segment first_segment(const PrefixArgs& a, int keys) {
+  Segment s;
+  s.nb = (a.prefix_len + keys - 1) / keys;
+  s.total = a.umma_tiles * s.nb;
+  s.n = gridDim.x / CG;
+  s.team = blockIdx.x / CG;
+  s.u = s.team * s.total / s.n;
+  s.end = (s.team + 1) * s.total / s.n;
+  return s;
+}
+
+// Positions of the prefix to records of the pool.
+struct Records {
+  const int32_t* blocks;
+  int64_t num_slots;
+  int bsz, shift, len, H, h;
+  bool pow2;
+  __device__ __forceinline__ int block_of(int p) const { return pow2 ? p >> shift : p / bsz; }
+  // block id of position p, -1 past the prefix
+  __device__ __forceinline__ int lookup(int p) const { return p < len ? __ldg(blocks + block_of(p)) : -1; }
+  // record of position p in block blk, -1: none
+  __device__ __forceinline__ int record(int p, int blk) const {
+    const int64_t slot = static_cast<int64_t>(blk) * bsz + (p - block_of(p) * bsz);
+    return (p < len && blk >= 0 && slot < num_slots) ? static_cast<int>(slot) * H + h : -1;
+  }
+};
+
+// One operand's part of a block as the producers move it: ROWS keys of kBytes bytes each, from byte
+// `off` of the record on. Each warp takes a quarter of the rows; a row is kLpr lanes of 16 B. In the slot,
+// 64 dims of one key are a 128 B row, swizzled; columns of 64 dims are ROWS rows apart.
+template <int FMT, int HD, int ROWS, int DIMS>
+struct Operand {
+  using F = Fmt<FMT>;
+  static constexpr int kBytes = F::kBytes ? DIMS : 2 * DIMS, kLpr = kBytes / 16;
+  static constexpr int kPerInstr = 32 / kLpr, kWarpRows = ROWS / kProdWarps, kInstr = kWarpRows / kPerInstr;
+  static constexpr uint32_t kCol = ROWS * 128;
+  static constexpr int kGlobalRow = F::kInline ? HD + 4 : F::kBytes ? HD : 2 * HD;
+  static_assert(kLpr <= 32 && kWarpRows <= 32 && kInstr >= 1, "rows of at most 512 B");
+
+  // bytes pools: instruction u's 16 B of this lane
+  static __device__ __forceinline__ uint4 load(const uint8_t* cache, int u, int lane, int rec, int off) {
+    const int rk = __shfl_sync(0xffffffffu, rec, kPerInstr * u + lane / kLpr);
+    if (rk < 0) return make_uint4(0, 0, 0, 0);
+    const uint8_t* p = cache + static_cast<uint64_t>(static_cast<uint32_t>(rk)) * kGlobalRow + off + 16 * (lane % kLpr);
+    if (F::kInline) {  // records sit on 4 B boundaries
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+      return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+    }
+    return __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  // 16 codes to fp16 and into the slot: two 16 B chunks of the key's 128 B row
+  static __device__ __forceinline__ void store(uint32_t slot, int u, int pw, int lane, const uint4& v) {
+    const int ch = lane % kLpr;
+    // row = kWarpRows pw + kPerInstr u + lane / kLpr; the warp's first row is a multiple of 8
+    const uint32_t lane_off = (ch >> 2) * kCol + (kWarpRows * pw + lane / kLpr) * 128;
+    const uint32_t base = slot + lane_off + kPerInstr * u * 128;
+    const uint32_t x = (lane / kLpr) ^ ((kPerInstr * u) & 7);  // row & 7 (disjoint bits)
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (F::kInt8) {
+        o[2 * k] = i8pair_to_f16x2(w[k]);
+        o[2 * k + 1] = i8pair_to_f16x2(w[k] >> 8);
+      } else {
+        o[2 * k] = e4m3pair_to_f16x2(w[k]);
+        o[2 * k + 1] = e4m3pair_to_f16x2(w[k] >> 16);
+      }
+    }
+    const uint32_t c0 = 2 * (ch & 3);
+    const bool odd = kLpr > 4 && (ch & 4);  // the eight lanes of a store phase fill eight distinct chunks
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    sts128(base + (((c0 + (odd ? 1 : 0)) ^ x) << 4), odd ? hi : lo);
+    sts128(base + (((c0 + (odd ? 0 : 1)) ^ x) << 4), odd ? lo : hi);
+  }
+  // 16-bit pools: the whole part by cp.async; missing keys are zero-filled
+  static __device__ __forceinline__ void copy(uint32_t slot, const uint8_t* cache, int pw, int lane, int rec, int off) {
+    const int ch = lane % kLpr;
+#pragma unroll 4
+    for (int u = 0; u < kInstr; ++u) {
+      const int lr = kPerInstr * u + lane / kLpr;
+      const int rk = __shfl_sync(0xffffffffu, rec, lr);
+      const int row = kWarpRows * pw + lr;
+      cp_async16(slot + (ch >> 3) * kCol + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                 cache + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow + off + 16 * ch, rk >= 0 ? 16 : 0);
+    }
+  }
+};
+
+// Slots of a segment of B blocks in ring order: K_0 K_1 V_0 K_2 V_1 ... K_B-1 V_B-2 V_B-1.
+__device__ __forceinline__ uint32_t k_slot(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ uint32_t v_slot(int j, int B) { return j == B - 1 ? 2 * B - 1 : 2 * j + 2; }
+
+template <int FMT, int HD, int NT, int CG>
+__global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umma_kernel(const PrefixArgs a) {
+  using F = Fmt<FMT>;
+  using U = Umma<FMT, HD, NT, CG>;
+  constexpr int NS = U::kSlots, KB = U::KB;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CG == 2 ? blockIdx.x & 1 : 0;  // this SM in the team
+  const uint32_t sb = (smem_u32(smem) + 1023u) & ~1023u, flag = sb + U::kFlag;  // swizzled rows: 1 KB aligned
+  const int H = a.num_kv_heads, G = a.num_q_heads / H;
+  const int64_t pairs = a.rows * G;
+
+  if (warp == U::kMmaWarp) {
+    team_tmem_alloc<CG>(sb + U::kTmemSlot);
+    if (lane == 0) {
+      for (int s = 0; s < NS; ++s) {
+        bar_init(sb + U::kFull + 8 * s, kProdWarps * CG);
+        bar_init(sb + U::kEmpty + 8 * s, 1);
+      }
+      for (int b = 0; b < 2; ++b) {
+        bar_init(sb + U::kSFull + 8 * b, 1);
+        bar_init(sb + U::kPFull + 8 * b, 4 * CG);
+        bar_init(sb + U::kPvDone + 8 * b, 1);
+      }
+      for (int s = 0; s < kScRing; ++s) {
+        bar_init(sb + U::kScFull + 8 * s, 1);
+        bar_init(sb + U::kScEmpty + 8 * s, U::kSoftWarps);
+      }
+      bar_init(sb + U::kQFull, U::kSoftWarps * CG);
+      bar_init(sb + U::kDrain, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+      sts32(flag, 0u);
+    }
+    __syncwarp();
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  team_sync<CG>();
+  tmem_fence_after_sync();
+  const uint32_t tb = lds32(sb + U::kTmemSlot);
+  Segment seg = first_segment<CG>(a, KB);
+  Records rc;
+  rc.blocks = a.prefix_blocks, rc.num_slots = a.num_slots, rc.bsz = a.block_size, rc.len = a.prefix_len, rc.H = H;
+  rc.pow2 = (rc.bsz & (rc.bsz - 1)) == 0, rc.shift = __ffs(rc.bsz) - 1;
+
+  if (warp < U::kSoftWarps) {
+    // ================================================================ softmax: one thread per pair
+    const int t = warp >> 2, r = tid & 127;  // tile, pair of the tile
+    const uint32_t tl = tb + (static_cast<uint32_t>(32 * (warp & 3)) << 16);  // this warp's lanes
+    const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;
+    uint32_t jb = 0;
+    bool ok = true;
+    while (ok && seg.next()) {
+      const int h = seg.tile / a.umma_ptiles;
+      const int64_t flat = ((static_cast<int64_t>(seg.tile - h * a.umma_ptiles) * NT + t) * CG + rank) * kTileM + r;
+      const bool in = flat < pairs;
+      const int64_t row = in ? flat / G : 0;
+      const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
+      const bool warp_in = __any_sync(0xffffffffu, in);
+      // ---- the pair's query row into the tile (bytes pools: fp16, pre-scaled by a power of two)
+      const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD;
+      float fac = fabsf(a.softmax_scale) * kLog2e, up = sign;
+      if (F::kBytes) {
+        float m = 0.f;
+        if (in) {
+          for (int d = 0; d < HD; d += 8) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + d));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
+              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+        }
+        int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
+        e = max(-112, min(126, e));
+        up = sign * pow2f(e);
+        fac *= pow2f(-e);
+        if (FMT == QKV_E4M3) fac *= a.k_scale_layer;
+      }
+      const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 8) {
+        uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
+        if (F::kBytes) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
+            x[2 * k] = f.x * up;
+            x[2 * k + 1] = f.y * up;
+          }
+          // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
+          v = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
+                       : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+        } else if (sign < 0.f) {
+          v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+        }
+        sts128(qrow + (d >> 6) * (kTileM * 128) + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
+      }
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
+
+      float M = -INFINITY, R = 0.f, l = 0.f;
+      int E = F::kInt8 ? -90 : 0;
+      constexpr float kShift = F::kBf16 ? 0.f : kPShift;
+      for (int j = seg.b0; ok && j < seg.b1; ++j, ++jb) {
+        const uint32_t b = NT == 2 ? t : jb & 1, ph = NT == 2 ? jb & 1 : (jb >> 1) & 1;
+        const uint32_t sc = sb + U::kSc + (jb & (kScRing - 1)) * U::kScStage;
+        ok = bar_wait(sb + U::kScFull + 8 * (jb & (kScRing - 1)), (jb / kScRing) & 1, flag) &&
+             bar_wait(sb + U::kSFull + 8 * b, ph, flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tmem_fence_after_sync();
+        // O of the blocks before this one: with one tile, S runs a block ahead of P V, so P V of the last block
+        // may be in flight still. Waited for at every block (before this block's P is handed over), so that the
+        // barrier is never two phases ahead or behind; with two tiles S was issued after it
+        bool o_ready = NT == 2 || j == seg.b0;
+        if (warp_in) {
+          const uint32_t ts = tl + U::kS + KB * b;
+          const uint4 mw = lds128(sc + U::kScMask);
+          const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
+          // ---- pass 1: the row's largest logit of the block
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < KB / 32; ++c) {
+            float s[32];
+            tmem_ld32(ts + 32 * c, s);
+            tmem_wait_ld(s);
+            const uint32_t mask = c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              if (F::kInt8) {
+                const uint4 ks = lds128(sc + 4 * (32 * c + k));
+                f2scale2(s + k, ks);
+              }
+              if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (!((mask >> (k + i)) & 1)) s[k + i] = -INFINITY;
+              }
+              mx = fmaxf(fmaxf(mx, fmaxf(s[k], s[k + 1])), fmaxf(s[k + 2], s[k + 3]));
+            }
+          }
+          const float tm = mx == -INFINITY ? mx : mx * fac;
+          int En = E;
+          if (F::kInt8) {
+            const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
+            if (e > E) En = e + kEuHeadroom;
+          }
+          const bool up_m = tm > M + kTau;
+          if (__any_sync(0xffffffffu, up_m || En != E)) {
+            const float Mn = up_m ? tm : M;
+            const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
+            const float f = M == -INFINITY ? 1.f : fast_exp2(R - Rn);
+            M = Mn, R = Rn, E = En;
+            l *= f;
+            if (j > seg.b0) {
+              if (!o_ready) {
+                ok = bar_wait(sb + U::kPvDone + 8 * t, (jb - 1) & 1, flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                o_ready = true;
+                tmem_fence_after_sync();
+              }
+              const uint64_t f2 = f2pack(f, f);
+#pragma unroll 1
+              for (int c = 0; c < HD / 32; ++c) {
+                float o[32];
+                tmem_ld32(tl + U::kO + t * HD + 32 * c, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) f2scale(o + k, f2);
+                tmem_st32(tl + U::kO + t * HD + 32 * c, o);
+              }
+            }
+          }
+          // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
+          const uint64_t fac2 = f2pack(fac, fac), ref2 = f2pack(-R, -R);
+          uint64_t sum2 = 0;
+#pragma unroll
+          for (int c = 0; c < KB / 32; ++c) {
+            float s[32];
+            uint32_t p[16];
+            tmem_ld32(ts + 32 * c, s);
+            tmem_wait_ld(s);
+            const uint32_t mask = c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              if (F::kInt8) {
+                const uint4 ks = lds128(sc + 4 * (32 * c + k));
+                f2scale2(s + k, ks);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                float y0, y1;
+                f2unpack(f2fma(f2pack(s[k + i], s[k + i + 1]), fac2, ref2), y0, y1);
+                if (!whole) {
+                  if (!((mask >> (k + i)) & 1)) y0 = -INFINITY;
+                  if (!((mask >> (k + i + 1)) & 1)) y1 = -INFINITY;
+                }
+                s[k + i] = fast_exp2(y0);
+                s[k + i + 1] = fast_exp2(y1);
+                sum2 = f2add(sum2, f2pack(s[k + i], s[k + i + 1]));
+              }
+              if (F::kInt8) {
+                const uint4 vs = lds128(sc + U::kScVs + 4 * (32 * c + k));
+                f2scale2(s + k, vs);  // a masked key's scale is 0
+              }
+              p[k / 2] = F::kBf16 ? pack_bf162(s[k], s[k + 1]) : pack_half2(s[k], s[k + 1]);
+              p[k / 2 + 1] = F::kBf16 ? pack_bf162(s[k + 2], s[k + 3]) : pack_half2(s[k + 2], s[k + 3]);
+            }
+            tmem_st_x16(ts + 16 * c, p);
+          }
+          float s0, s1;
+          f2unpack(sum2, s0, s1);
+          l += s0 + s1;
+          tmem_wait_st();
+        }
+        if (!o_ready) {
+          ok = bar_wait(sb + U::kPvDone + 8 * t, (jb - 1) & 1, flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        tmem_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          lead_arrive<CG>(sb + U::kPFull + 8 * b);
+          bar_arrive(sb + U::kScEmpty + 8 * (jb & (kScRing - 1)));
+        }
+      }
+      if (!ok) break;
+      // ---- the segment's partial result
+      ok = bar_wait(sb + U::kPvDone + 8 * t, (jb - 1) & 1, flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tmem_fence_after_sync();
+      if (warp_in) {
+        const bool any = M != -INFINITY || l != l;
+        const float inv = any ? 1.f / l : 0.f;
+        const int64_t at = (static_cast<int64_t>(seg.part) * a.rows + row) * a.num_q_heads + head;
+        if (in) a.lse_part[at] = any ? (R + log2f(l)) * kLn2 : -INFINITY;
+        float* dst = a.o_part + at * HD;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float o[32];
+          tmem_ld32(tl + U::kO + t * HD + 32 * c, o);
+          tmem_wait_ld(o);
+          if (in && any) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              // int8: the producers store dims 0, 2, 1, 3 of each four
+              const float x1 = F::kInt8 ? o[k + 2] : o[k + 1], x2 = F::kInt8 ? o[k + 1] : o[k + 2];
+              *reinterpret_cast<float4*>(dst + 32 * c + k) = make_float4(o[k] * inv, x1 * inv, x2 * inv, o[k + 3] * inv);
+            }
+          }
+        }
+      }
+      tmem_fence_before_sync();  // ordered before the next segment's first arrival
+    }
+  } else if (warp < U::kScWarp) {
+    // ================================================================ producers
+    using KOp = Operand<FMT, HD, U::kKRows, HD>;
+    using VOp = Operand<FMT, HD, KB, U::kVDims>;
+    const int pw = warp & 3;
+    const int voff = rank * VOp::kBytes;  // this SM's dims
+    uint32_t base = 0;                    // slots of earlier segments
+    bool ok = true;
+    // lane's key of block j (a segment-relative number), for K (this SM's keys) and V (all)
+    auto k_pos = [&](int j) -> int {
+      return lane < KOp::kWarpRows && j < seg.b1 - seg.b0 ? (seg.b0 + j) * KB + rank * U::kKRows + KOp::kWarpRows * pw + lane : INT_MAX;
+    };
+    auto v_pos = [&](int j) -> int {
+      return lane < VOp::kWarpRows && j < seg.b1 - seg.b0 ? (seg.b0 + j) * KB + VOp::kWarpRows * pw + lane : INT_MAX;
+    };
+    auto await = [&](uint32_t s) -> bool {
+      if (s < NS) return true;
+      return __all_sync(0xffffffffu, bar_wait(sb + U::kEmpty + 8 * (s % NS), (s / NS - 1) & 1, flag));
+    };
+    auto hand_over = [&](uint32_t s) {
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) lead_arrive<CG>(sb + U::kFull + 8 * (s % NS));
+    };
+    while (ok && seg.next()) {
+      rc.h = seg.tile / a.umma_ptiles;
+      const int B = seg.b1 - seg.b0;
+      // block ids run two blocks ahead of the loads' use, records one
+      int kblk = rc.lookup(k_pos(0)), vblk = rc.lookup(v_pos(0));
+      int krec = rc.record(k_pos(0), kblk), vrec = rc.record(v_pos(0), vblk);
+      kblk = rc.lookup(k_pos(1)), vblk = rc.lookup(v_pos(1));
+      if (F::kBytes) {
+        uint4 kraw[KOp::kInstr], vraw[VOp::kInstr];
+#pragma unroll
+        for (int u = 0; u < KOp::kInstr; ++u) kraw[u] = KOp::load(a.k_cache, u, lane, krec, 0);
+#pragma unroll
+        for (int u = 0; u < VOp::kInstr; ++u) vraw[u] = VOp::load(a.v_cache, u, lane, vrec, voff);
+        for (int j = 0; j <= B; ++j) {
+          if (j < B) {
+            const uint32_t s = base + k_slot(j), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
+            krec = rc.record(k_pos(j + 1), kblk);
+            kblk = rc.lookup(k_pos(j + 2));
+            if (!(ok = await(s))) break;
+#pragma unroll
+            for (int u = 0; u < KOp::kInstr; ++u) {
+              KOp::store(slot, u, pw, lane, kraw[u]);
+              if (j + 1 < B) kraw[u] = KOp::load(a.k_cache, u, lane, krec, 0);
+            }
+            hand_over(s);
+          }
+          if (j > 0) {
+            const uint32_t s = base + v_slot(j - 1, B), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
+            vrec = rc.record(v_pos(j), vblk);
+            vblk = rc.lookup(v_pos(j + 1));
+            if (!(ok = await(s))) break;
+#pragma unroll
+            for (int u = 0; u < VOp::kInstr; ++u) {
+              VOp::store(slot, u, pw, lane, vraw[u]);
+              if (j < B) vraw[u] = VOp::load(a.v_cache, u, lane, vrec, voff);
+            }
+            hand_over(s);
+          }
+        }
+      } else {
+        // a slot is handed over once the copies of the next one have been issued
+        uint32_t last = 0;
+        bool pending = false;
+        for (int j = 0; ok && j <= B; ++j) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            if (v == 0 ? j >= B : j == 0) continue;
+            const uint32_t s = base + (v ? v_slot(j - 1, B) : k_slot(j)), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
+            if (!(ok = await(s))) break;
+            if (v == 0) {
+              KOp::copy(slot, a.k_cache, pw, lane, krec, 0);
+              krec = rc.record(k_pos(j + 1), kblk);
+              kblk = rc.lookup(k_pos(j + 2));
+            } else {
+              VOp::copy(slot, a.v_cache, pw, lane, vrec, voff);
+              vrec = rc.record(v_pos(j), vblk);
+              vblk = rc.lookup(v_pos(j + 1));
+            }
+            cp_async_commit();
+            if (pending) {
+              cp_async_wait<1>();
+              hand_over(last);
+            }
+            last = s, pending = true;
+          }
+        }
+        cp_async_wait<0>();
+        if (ok && pending) hand_over(last);
+      }
+      base += 2 * B;
+    }
+  } else if (warp == U::kScWarp) {
+    // ================================================================ scales and masks
+    uint32_t jb = 0;
+    bool ok = true;
+    while (ok && seg.next()) {
+      rc.h = seg.tile / a.umma_ptiles;
+      int blk[KB / 32];
+#pragma unroll
+      for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup(seg.b0 * KB + 32 * i + lane);
+      for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
+        const uint32_t n = jb & (kScRing - 1), sc = sb + U::kSc + n * U::kScStage;
+        float ks[KB / 32], vs[KB / 32];
+        uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u}, vmax = 0;  // words past the block count as whole
+#pragma unroll
+        for (int i = 0; i < KB / 32; ++i) {
+          const int p = j * KB + 32 * i + lane, rec = rc.record(p, blk[i]);
+          if (rec < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+          mask[i] = __ballot_sync(0xffffffffu, rec >= 0);
+          ks[i] = vs[i] = 0.f;
+          if (F::kInt8 && rec >= 0) {
+            if (F::kInline) {
+              const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(rec)) * (HD + 4) + HD;
+              ks[i] = __ldg(reinterpret_cast<const float*>(a.k_cache + off));
+              vs[i] = __ldg(reinterpret_cast<const float*>(a.v_cache + off));
+            } else {
+              ks[i] = __ldg(a.k_scale_tok + rec);
+              vs[i] = __ldg(a.v_scale_tok + rec);
+            }
+          }
+          blk[i] = j + 1 < seg.b1 ? rc.lookup(p + KB) : -1;
+        }
+        if (jb >= kScRing) {
+          ok = __all_sync(0xffffffffu, bar_wait(sb + U::kScEmpty + 8 * n, (jb / kScRing - 1) & 1, flag));
+          if (!ok) break;
+        }
+        if (F::kInt8) {
+#pragma unroll
+          for (int i = 0; i < KB / 32; ++i) {
+            sts32(sc + 4 * (32 * i + lane), __float_as_uint(ks[i]));
+            sts32(sc + U::kScVs + 4 * (32 * i + lane), __float_as_uint(vs[i]));
+            vmax = max(vmax, __float_as_uint(vs[i]) & 0x7fffffffu);  // magnitudes: bits order like values
+          }
+          vmax = __reduce_max_sync(0xffffffffu, vmax);
+        }
+        if (lane == 0) {
+          sts128(sc + U::kScMask, make_uint4(mask[0], mask[1], mask[2], mask[3]));
+          sts32(sc + U::kScVmax, vmax);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(sb + U::kScFull + 8 * n);
+      }
+    }
+  } else if (lane == 0 && rank == 0) {
+    // ================================================================ MMA issuer
+    uint32_t base = 0, jb = 0, segs = 0;
+    bool ok = true;
+    auto await_full = [&](uint32_t s) -> bool { return bar_wait(sb + U::kFull + 8 * (s % NS), (s / NS) & 1, flag); };
+    // S of tile t into buffer b, from the K slot s (awaited by the first tile, freed by the last)
+    auto qk = [&](int t, uint32_t b, uint32_t s) {
+      if (t == 0 && !(ok = await_full(s))) return;
+      tmem_fence_after_sync();
+      const uint32_t k = sb + U::kRing + (s % NS) * U::kSlotBytes, q = sb + U::kQ + t * U::kQTile;
+#pragma unroll
+      for (int ks = 0; ks < HD / 16; ++ks)
+        mma_ss<CG>(tb + U::kS + KB * b, sw128_desc(q + (ks >> 2) * (kTileM * 128) + 32 * (ks & 3), 16, 1024),
+                   sw128_desc(k + (ks >> 2) * (U::kKRows * 128) + 32 * (ks & 3), 16, 1024), U::kIdS, ks > 0 ? 1u : 0u);
+      if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
+      commit_to<CG>(sb + U::kSFull + 8 * b);
+    };
+    // O of tile t += P (in buffer b) times the V slot s
+    auto pv = [&](int t, uint32_t b, uint32_t ph, uint32_t s, bool first) {
+      if (!(ok = bar_wait(sb + U::kPFull + 8 * b, ph, flag))) return;
+      if (t == 0 && !(ok = await_full(s))) return;
+      tmem_fence_after_sync();
+      const uint32_t v = sb + U::kRing + (s % NS) * U::kSlotBytes;
+#pragma unroll
+      for (int ks = 0; ks < KB / 16; ++ks)
+        mma_ts<CG>(tb + U::kO + t * HD, tb + U::kS + KB * b + 8 * ks, sw128_desc(v + 2048 * ks, KB * 128, 1024), U::kIdO,
+                   !first || ks > 0 ? 1u : 0u);
+      if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
+      commit_to<CG>(sb + U::kPvDone + 8 * t);
+    };
+    while (ok && seg.next()) {
+      const int B = seg.b1 - seg.b0;
+      ok = bar_wait(sb + U::kQFull, segs & 1, flag);
+      ++segs;
+      if (ok) qk(0, NT == 2 ? 0 : jb & 1, base);
+      if (ok && NT == 2) qk(NT - 1, 1, base);
+      for (int j = 0; ok && j < B; ++j, ++jb) {
+        if (NT == 2) {
+          for (int t = 0; ok && t < NT; ++t) {
+            pv(t, t, jb & 1, base + v_slot(j, B), j == 0);
+            if (ok && j + 1 < B) qk(t, t, base + k_slot(j + 1));
+          }
+        } else {
+          if (j + 1 < B) qk(0, (jb + 1) & 1, base + k_slot(j + 1));
+          if (ok) pv(0, jb & 1, (jb >> 1) & 1, base + v_slot(j, B), j == 0);
+        }
+      }
+      base += 2 * B;
+    }
+    commit_to<CG>(sb + U::kDrain);
+  }
+  if (warp == U::kMmaWarp && lane == 0) {
+    // nothing may still write tensor memory, read a slot or arrive on a barrier when the team leaves
+    bool drained = false;
+    for (uint32_t it = 0; it < kWaitLimit && !drained; ++it) drained = bar_try(sb + U::kDrain, 0);
+    if (!drained) sts32(flag, 1u);
+  }
+  __syncwarp();
+  tmem_fence_before_sync();
+  __syncthreads();
+  team_sync<CG>();
+  tmem_fence_after_sync();
+  if (warp == U::kMmaWarp) team_tmem_dealloc<CG>(tb);
+  if (tid == 0 && lds32(flag) != 0u && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_TIMEOUT);
+}
+
+template <int FMT, int HD, int NT, int CG>
+cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
+  using U = Umma<FMT, HD, NT, CG>;
+  auto kern = prefix_umma_kernel<FMT, HD, NT, CG>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, U::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.umma_teams * CG));
+  cfg.blockDim = dim3(U::kThreads);
+  cfg.dynamicSmemBytes = U::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int FMT>
+cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
+  if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2>(a, stream) : launch_umma<FMT, 256, 1, 1>(a, stream);
+  if (a.umma_cg == 2) return launch_umma<FMT, 128, 2, 2>(a, stream);
+  return launch_umma<FMT, 128, 1, 1>(a, stream);
+}
+
+}  // namespace prefix
+}  // namespace qkv

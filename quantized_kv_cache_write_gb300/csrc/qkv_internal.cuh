@@ -180,13 +180,27 @@ struct PrefixArgs {
   int prefix_chunk;
   int64_t prefix_items;  // CTAs of each launch
   int64_t own_items;
+  // the prefix on tcgen05 (umma_cg > 0: SMs per team): umma_ptiles tiles of umma_pairs pairs per KV
+  // head, key blocks of umma_keys
+  int umma_cg = 0;
+  int umma_pairs = 0;
+  int umma_keys = 0;
+  int umma_ptiles = 0;
+  int64_t umma_tiles = 0;  // umma_ptiles * num_kv_heads
+  int64_t umma_teams = 0;
 };
-// the mma.sync tiles of 16 (row, head) pairs, over the prefix or (own) the keys behind it
+// the mma.sync tiles of 16 (row, head) pairs, over the prefix or (own) the keys behind it; the tcgen05
+// tiles of 128, over the prefix
 cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_umma_bf16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_umma_f16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_umma_int8_side(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_umma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, float v_scale_post, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device helpers

@@ -269,3 +269,79 @@ def test_seeded_random_shapes(seed):
     b, pool, q, scale = case(2000 + seed, fmt, act, D, H, G, prefix, own, per, block)
     out, lse = call(pool, b, dev16(q, act), H, scale)
     check(pool, b, q, act, H, scale, out, lse, what=f"seed {seed}")
+
+
+# Batches whose prefix runs on the tensor-memory tiles: several 128-key blocks per CTA, ranges that end
+# inside a tile's keys and go on in the next tile, tiles whose last pairs do not exist.
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("D,rows,G,H", [(128, 9, 8, 1), (128, 70, 8, 2), (256, 21, 16, 1), (128, 13, 12, 3)])
+def test_many_pairs_behind_a_long_prefix(fmt, act, D, rows, G, H):
+    b, pool, q, scale = case(20, fmt, act, D, H, G, 9001, [1 + 3 * (i % 4) for i in range(rows)], 1, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(pool, b, dev16(q, act), H, scale, status=status)
+    check(pool, b, q, act, H, scale, out, lse, what=f"{fmt} {act} {D} {rows}")
+    assert int(status.item()) == 0
+    for _ in range(2):
+        o2, l2 = call(pool, b, dev16(q, act), H, scale)
+        assert torch.equal(out.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("prefix", [20000, 20001, 40000])
+@pytest.mark.parametrize("D,fmt", [(128, "e4m3"), (256, "int8_side"), (128, "bf16")])
+def test_blocks_of_many_ctas(prefix, D, fmt):
+    b, pool, q, scale = case(21, fmt, "bf16", D, 1, 8, prefix, [2] * 17, 1, 64)
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, scale)
+    check(pool, b, q, "bf16", 1, scale, out, lse, what=f"{prefix} {D} {fmt}")
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("falling", [False, True])
+def test_rising_and_falling_logits_and_scales_over_many_blocks(D, falling):
+    """The row maximum and the int8 V scales grow (or fall) block after block, so that the reference
+    is raised again and again, by the logits and by the scales."""
+    rng = np.random.default_rng(22)
+    P, rows, G = 30000, 12, 16
+    b = Batch(rng, P, [1] * rows, 1, 16)
+    pool = Pool(rng, "int8_side", "bf16", b.live, b.num_slots, 1, D)
+    order = torch.tensor([int(b.prefix_blocks[p // 16]) * 16 + p % 16 for p in range(P)]).cuda()
+    ramp = torch.linspace(0, 1, P, device="cuda")
+    if falling:
+        ramp = ramp.flip(0)
+    pool.kw["k_scale_tok"][order] = 0.002 + 0.05 * ramp[:, None]
+    pool.kw["v_scale_tok"][order] = torch.exp2(-20 + 24 * ramp)[:, None]
+    pool.cache[0][order] = torch.randint(100, 128, (P, 1, D), device="cuda", dtype=torch.int8)
+    for c, x, name in ((0, "K", "k_scale_tok"), (1, "V", "v_scale_tok")):
+        setattr(pool, x, pool.cache[c].cpu().numpy().astype(np.float64) * pool.kw[name].double().cpu().numpy()[..., None])
+    q = bits16(np.abs(rng.standard_normal((rows, G, D))), "bf16")
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, D ** -0.5)
+    check(pool, b, q, "bf16", 1, D ** -0.5, out, lse, what="ramp")
+
+
+def test_blocks_without_any_valid_key_among_many():
+    """Whole 128-key blocks masked at the start, in the middle and at the end of the prefix."""
+    b, pool, q, scale = case(23, "e4m3", "bf16", 128, 1, 16, 12000, [3] * 20, 1, 32)
+    for lo, hi in ((0, 30), (100, 140), (360, 375)):
+        b.prefix_blocks[lo:hi] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, scale, status=status)
+    check(pool, b, q, "bf16", 1, scale, out, lse, what="masked blocks")
+    assert int(status.item()) == 2
+
+
+@pytest.mark.parametrize("fmt,act", [("int8_side", "bf16"), ("e4m3", "f16"), ("bf16", "bf16"), ("int8_inline", "f16")])
+@pytest.mark.parametrize("D,rows,G", [(128, 40, 16), (256, 40, 16), (256, 7, 16), (128, 7, 16)])
+def test_each_row_has_one_heavy_key_somewhere(fmt, act, D, rows, G):
+    """One key of the prefix carries most of a row's weight, at another place for every row (the last
+    key of a range among them): a block whose contribution is dropped or counted twice shows."""
+    P, H = 30001, 1
+    b, pool, _, _ = case(24, fmt, act, D, H, G, P, [2] * rows, 1, 16)
+    rng = np.random.default_rng(25)
+    q = rng.standard_normal((rows, G, D))
+    order = np.array([int(b.prefix_blocks[p // 16]) * 16 + p % 16 for p in range(P)])
+    heavy = np.linspace(0, P - 1, rows).astype(int)
+    heavy[1::3] = np.minimum(heavy[1::3] // 128 * 128 + 127, P - 1)
+    K = pool.K[order[heavy], 0]
+    q = 0.25 * q + 6.0 * (K / np.linalg.norm(K, axis=1, keepdims=True))[:, None]
+    q = bits16(q, act)
+    out, lse = call(pool, b, dev16(q, act), H, 1.0 if D == 128 else 0.7)
+    check(pool, b, q, act, H, 1.0 if D == 128 else 0.7, out, lse, what=f"heavy {fmt} {D}")
