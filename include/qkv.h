@@ -640,8 +640,8 @@ qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
  *                 share the reads of its keys.
  *   row_len       int32 [rows]: 0 (the row sees nothing: o = 0, lse = -inf) or in [prefix_len,
  *                 max_row_len].
- *   max_row_len   no row is longer; prefix_len <= max_row_len <= max_blocks * block_size, else
- *                 QKV_ERR_ARG. It sizes the launch (a captured graph keeps it).
+ *   max_row_len   no row is longer; prefix_len <= max_row_len <= max_blocks * block_size and at most
+ *                 2^30, else QKV_ERR_ARG. It sizes the launch (a captured graph keeps it).
  *   Flagged with QKV_DEV_BAD_INDEX: a row_seq outside [-1, num_seqs) or a row_len outside its
  *   range (the row is empty), and an unallocated block (id < 0) or a slot >= num_slots among the
  *   keys that a row sees (the key is masked for the rows that it serves).

@@ -520,6 +520,7 @@ lib.qkv_prefix_attn.restype = ctypes.c_int
 lib.qkv_prefix_attn_workspace.argtypes = [_i32, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
 lib.qkv_prefix_attn_workspace.restype = ctypes.c_int
 
+_APPEND_SIZE, _PREFIX_SIZE = ctypes.sizeof(AppendDesc), ctypes.sizeof(PrefixDesc)
 _CACHE_BYTES = {QKV_BF16: 2, QKV_F16: 2, QKV_INT8_SIDE: 1, QKV_INT8_INLINE: 1, QKV_E4M3: 1}
 
 
@@ -529,7 +530,7 @@ def _need_cache(name: str, t, fmt: int, H: int, D: int):
     if size is None:
         raise ValueError(f"unknown pool format {fmt}")
     width = D + 4 if fmt == QKV_INT8_INLINE else D
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != width or t.element_size() != size or not t.is_contiguous():
+    if tuple(t.shape[1:]) != (H, width) or t.dim() != 3 or t.element_size() != size or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [num_slots, {H}, {width}] pool of {size}-byte values, "
                          f"got {tuple(t.shape)} {t.dtype}")
 
@@ -544,24 +545,37 @@ def _strided(name: str, t, T: int, H: int, D: int) -> int:
     return st[0] if T > 1 else H * D
 
 
-def _same_device(first, *rest):
-    """Every tensor must sit on the CUDA device of the first: the kernels take raw pointers."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors must be on a CUDA device, got {dev}")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+def _on_cuda(*tensors) -> int:
+    """The one CUDA device that every tensor sits on: the kernels take raw pointers."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError(f"all tensors must be on one CUDA device, got {tensors[0].device} and {t.device}")
     return dev
 
 
-def _call_on(dev, fn: str, desc, stream):
-    """Call a descriptor entry point with `dev` current (the C library launches on the current
-    device) and, where none is given, on that device's current stream."""
-    if dev.index != torch.cuda.current_device():
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the stream without a Stream object
+
+
+def _call_on(dev: int, fn: str, call, desc, stream):
+    """Call a descriptor entry point with device `dev` current (the C library launches on the
+    current device) and, where no stream is given, on that device's current stream."""
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _check(fn, getattr(lib, fn)(ctypes.byref(desc), _stream(stream)))
-    _check(fn, getattr(lib, fn)(ctypes.byref(desc), _stream(stream)))
+            st = call(ctypes.byref(desc), _stream(stream))
+    else:
+        st = call(ctypes.byref(desc), _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream))
+    if st != QKV_OK:
+        raise QKVError(fn, st)
+
+
+def _plain(name: str, t, dtype, numel: int):
+    """_need for one dtype, without its cost where nothing is wrong; the tensor's address."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() != numel:
+        _need(name, t, (dtype,), numel)
+    return t.data_ptr()
 
 
 def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=None, q_out=None, slot_mapping=None,
@@ -586,36 +600,34 @@ def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=N
         raise ValueError("cos_sin must be [positions, rotary_dim]")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    _need("cos_sin", cos_sin, _F32)
-    _need("token_pos", token_pos, _I32, T)
-    _need("slot_mapping", slot_mapping, _I64, T)
-    _need("token_seq", token_seq, _I32, T)
-    _need("block_table", block_table, _I32)
-    _need("k_scale", k_scale, _F32, S * H)
-    _need("v_scale", v_scale, _F32, S * H)
-    _need("dev_status", dev_status, _WORD)
-    d = AppendDesc()
-    d.size, d.fmt, d.act_fp16 = ctypes.sizeof(AppendDesc), int(fmt), int(k.dtype == torch.float16)
+    qp = qop = None
+    Hq = qs = qos = 0
     if q is not None:
         if q.dtype != k.dtype or q_out.dtype != k.dtype:
             raise ValueError(f"q and q_out must be {k.dtype} as k and v are")
         Hq = q.shape[1] if q.dim() == 3 else 0
-        d.q_stride, d.q_out_stride = _strided("q", q, T, Hq, D), _strided("q_out", q_out, T, Hq, D)
-        d.q, d.q_out, d.num_q_heads = q.data_ptr(), q_out.data_ptr(), Hq
-    dev = _same_device(k, v, q, q_out, k_cache, v_cache, cos_sin, token_pos, slot_mapping, token_seq, block_table,
-                       k_scale, v_scale, dev_status)
-    d.k, d.v, d.num_tokens, d.num_kv_heads, d.head_dim, d.kv_stride = k.data_ptr(), v.data_ptr(), T, H, D, stride
-    d.cos_sin, d.num_positions, d.rotary_dim = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
-    d.interleaved, d.token_pos = int(bool(interleaved)), token_pos.data_ptr()
-    d.slot_mapping, d.token_seq, d.block_table = _ptr(slot_mapping), _ptr(token_seq), _ptr(block_table)
+        qs, qos = _strided("q", q, T, Hq, D), _strided("q_out", q_out, T, Hq, D)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    P, rot = cos_sin.shape
+    csp = _plain("cos_sin", cos_sin, torch.float32, P * rot)
+    tpp = _plain("token_pos", token_pos, torch.int32, T)
+    smp = _plain("slot_mapping", slot_mapping, torch.int64, T)
+    tsp = _plain("token_seq", token_seq, torch.int32, T)
+    ksp = _plain("k_scale", k_scale, torch.float32, S * H)
+    vsp = _plain("v_scale", v_scale, torch.float32, S * H)
+    _need("dev_status", dev_status, _WORD)
+    btp, seqs, blocks = None, 0, 0
     if block_table is not None:
         if block_table.dim() != 2:
             raise ValueError("block_table must be [num_seqs, max_blocks]")
-        d.num_seqs, d.max_blocks, d.block_size = block_table.shape[0], block_table.shape[1], int(block_size)
-    d.k_cache, d.v_cache, d.k_scale, d.v_scale = k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale)
-    d.k_scale_layer, d.v_scale_layer = float(k_scale_layer), float(v_scale_layer)
-    d.num_slots, d.dev_status = S, _ptr(dev_status)
-    _call_on(dev, "qkv_append_rope", d, stream)
+        seqs, blocks = block_table.shape
+        btp = _plain("block_table", block_table, torch.int32, seqs * blocks)
+    dev = _on_cuda(k, v, q, q_out, k_cache, v_cache, cos_sin, token_pos, slot_mapping, token_seq, block_table, k_scale,
+                   v_scale, dev_status)
+    d = AppendDesc(_APPEND_SIZE, fmt, k.dtype is torch.float16, qp, qop, k.data_ptr(), v.data_ptr(), T, Hq, H, D, qs, qos,
+                   stride, csp, P, rot, 1 if interleaved else 0, tpp, smp, tsp, btp, seqs, blocks, block_size,
+                   k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S, _ptr(dev_status))
+    _call_on(dev, "qkv_append_rope", lib.qkv_append_rope, d, stream)
 
 
 def qkv_prefix_attn_workspace(fmt: int, rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -652,38 +664,36 @@ def qkv_prefix_attn(q, fmt: int, k_cache, v_cache, block_table, row_seq, row_len
         raise ValueError("k_cache and v_cache must hold the same number of slots")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [num_seqs, max_blocks]")
-    _need("block_table", block_table, _I32)
-    _need("row_seq", row_seq, _I32, R)
-    _need("row_len", row_len, _I32, R)
-    _expect_shape("out", out, (R, Hq, D))
-    _expect_shape("lse", lse, (R, Hq))
-    _need("out", out, (q.dtype,))
-    _need("lse", lse, _F32)
-    _need("k_scale_tok", k_scale_tok, _F32, S * num_kv_heads)
-    _need("v_scale_tok", v_scale_tok, _F32, S * num_kv_heads)
+    seqs, blocks = block_table.shape
+    btp = _plain("block_table", block_table, torch.int32, seqs * blocks)
+    rsp = _plain("row_seq", row_seq, torch.int32, R)
+    rlp = _plain("row_len", row_len, torch.int32, R)
+    if out.shape != q.shape:
+        _expect_shape("out", out, (R, Hq, D))
+    op = _plain("out", out, q.dtype, R * Hq * D)
+    lp = None
+    if lse is not None:
+        _expect_shape("lse", lse, (R, Hq))
+        lp = _plain("lse", lse, torch.float32, R * Hq)
+    ksp = _plain("k_scale_tok", k_scale_tok, torch.float32, S * num_kv_heads)
+    vsp = _plain("v_scale_tok", v_scale_tok, torch.float32, S * num_kv_heads)
     _need("dev_status", dev_status, _WORD)
+    pbp = None
     if prefix_len > 0:
         if prefix_blocks is None or block_size < 1:
             raise ValueError("a shared prefix needs prefix_blocks and a block_size")
-        _need("prefix_blocks", prefix_blocks, _I32)
-        if prefix_blocks.numel() * block_size < prefix_len:
-            raise ValueError(f"prefix_blocks must cover {prefix_len} positions, got {prefix_blocks.numel()} blocks")
-    d = PrefixDesc()
+        n = prefix_blocks.numel()
+        pbp = _plain("prefix_blocks", prefix_blocks, torch.int32, n)
+        if n * block_size < prefix_len:
+            raise ValueError(f"prefix_blocks must cover {prefix_len} positions, got {n} blocks")
+    wsp, wsb = None, 0
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    dev = _same_device(q, k_cache, v_cache, block_table, row_seq, row_len, out, lse, k_scale_tok, v_scale_tok,
-                       prefix_blocks, workspace, dev_status)
-    d.size, d.fmt, d.q_fp16 = ctypes.sizeof(PrefixDesc), int(fmt), int(q.dtype == torch.float16)
-    d.q, d.q_stride, d.rows, d.num_q_heads, d.num_kv_heads, d.head_dim = q.data_ptr(), stride, R, Hq, num_kv_heads, D
-    d.k_cache, d.v_cache, d.num_slots = k_cache.data_ptr(), v_cache.data_ptr(), S
-    d.k_scale_tok, d.v_scale_tok = _ptr(k_scale_tok), _ptr(v_scale_tok)
-    d.k_scale_layer, d.v_scale_layer = float(k_scale_layer), float(v_scale_layer)
-    if prefix_len != 0:
-        d.prefix_blocks, d.prefix_len = _ptr(prefix_blocks), int(prefix_len)
-    d.block_table, d.num_seqs, d.max_blocks, d.block_size = block_table.data_ptr(), block_table.shape[0], \
-        block_table.shape[1], int(block_size)
-    d.row_seq, d.row_len, d.max_row_len = row_seq.data_ptr(), row_len.data_ptr(), int(max_row_len)
-    d.softmax_scale, d.out, d.lse, d.dev_status = float(softmax_scale), out.data_ptr(), _ptr(lse), _ptr(dev_status)
-    _call_on(dev, "qkv_prefix_attn", d, stream)
+        wsp, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _on_cuda(q, k_cache, v_cache, block_table, row_seq, row_len, out, lse, k_scale_tok, v_scale_tok,
+                   prefix_blocks, workspace, dev_status)
+    d = PrefixDesc(_PREFIX_SIZE, fmt, q.dtype is torch.float16, q.data_ptr(), stride, R, Hq, num_kv_heads, D,
+                   k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S, pbp, prefix_len, btp,
+                   seqs, blocks, block_size, rsp, rlp, max_row_len, float(softmax_scale), op, lp, wsp, wsb, _ptr(dev_status))
+    _call_on(dev, "qkv_prefix_attn", lib.qkv_prefix_attn, d, stream)

@@ -570,7 +570,7 @@ struct PrefixPlan {
 
 qkv_status check_prefix_shape(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv_heads, int head_dim,
                               int prefix_len, int max_row_len) {
-  if (rows < 0 || prefix_len < 0 || max_row_len < prefix_len) return QKV_ERR_ARG;
+  if (rows < 0 || prefix_len < 0 || max_row_len < prefix_len || max_row_len > (1 << 30)) return QKV_ERR_ARG;
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0) return QKV_ERR_ARG;
   if (!qkv::head_dim_ok(head_dim) || num_q_heads / num_kv_heads > kMaxGroup) return QKV_ERR_UNSUPPORTED;
   if (fmt != QKV_BF16 && fmt != QKV_INT8_SIDE && fmt != QKV_INT8_INLINE && fmt != QKV_E4M3 && fmt != QKV_F16)
@@ -600,6 +600,7 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
     p->prefix_chunk = static_cast<int>(ceil_div(ceil_div(prefix_len, p->prefix_parts), 64) * 64);
     p->prefix_parts = static_cast<int>(ceil_div(prefix_len, p->prefix_chunk));
   }
+  p->prefix_items = ptiles * p->prefix_parts;
   p->umma_cg = 0, p->umma_pairs = 0, p->umma_keys = 0, p->umma_ptiles = 0, p->umma_tiles = 0, p->umma_teams = 0;
   if (prefix_len > 0 && rows * G > kUmmaMinPairs) {
     p->umma_cg = rows * G > 128 ? 2 : 1;  // one SM's tile holds 128 pairs
@@ -612,11 +613,11 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
     p->umma_teams = total < teams ? total : teams;
     // ranges of at least total / teams units: a tile's nb units touch at most this many
     p->prefix_parts = static_cast<int>(ceil_div(nb, total / p->umma_teams) + 1);
+    p->prefix_items = 0;
   }
   p->own_parts = parts_of(otiles, own);
-  p->prefix_items = ptiles * p->prefix_parts;
   p->own_items = otiles * p->own_parts;
-  if (p->prefix_items > INT32_MAX || p->own_items > INT32_MAX) return QKV_ERR_ARG;
+  if (p->prefix_items + p->own_items > INT32_MAX) return QKV_ERR_ARG;
   return QKV_OK;
 }
 
@@ -631,13 +632,13 @@ cudaError_t launch_prefix_umma(const qkv::PrefixArgs& a, qkv_format fmt, cudaStr
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefix_mma(const qkv::PrefixArgs& a, qkv_format fmt, bool own, cudaStream_t s) {
+cudaError_t launch_prefix_mma(const qkv::PrefixArgs& a, qkv_format fmt, bool overlaps, cudaStream_t s) {
   switch (fmt) {
-    case QKV_BF16: return qkv::launch_prefix_mma_bf16(a, own, s);
-    case QKV_F16: return qkv::launch_prefix_mma_f16(a, own, s);
-    case QKV_INT8_SIDE: return qkv::launch_prefix_mma_int8_side(a, own, s);
-    case QKV_INT8_INLINE: return qkv::launch_prefix_mma_int8_inline(a, own, s);
-    case QKV_E4M3: return qkv::launch_prefix_mma_e4m3(a, own, s);
+    case QKV_BF16: return qkv::launch_prefix_mma_bf16(a, overlaps, s);
+    case QKV_F16: return qkv::launch_prefix_mma_f16(a, overlaps, s);
+    case QKV_INT8_SIDE: return qkv::launch_prefix_mma_int8_side(a, overlaps, s);
+    case QKV_INT8_INLINE: return qkv::launch_prefix_mma_int8_inline(a, overlaps, s);
+    case QKV_E4M3: return qkv::launch_prefix_mma_e4m3(a, overlaps, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -716,8 +717,9 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.softmax_scale = d->softmax_scale;
   a.out = static_cast<uint16_t*>(d->out);
   a.lse = d->lse;
+  a.merge_scale = d->fmt == QKV_E4M3 ? d->v_scale_layer : 1.f;
   a.dev_status = d->dev_status;
-  const bool direct = p.parts() == 1;
+  const bool direct = p.parts() == 1 && p.umma_cg == 0;
   a.o_part = direct ? nullptr : static_cast<float*>(d->workspace);
   a.lse_part = direct ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + p.o_bytes());
   a.prefix_parts = p.prefix_parts;
@@ -733,9 +735,9 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.umma_ptiles = p.umma_ptiles;
   a.umma_tiles = p.umma_tiles;
   a.umma_teams = p.umma_teams;
-  if (p.prefix_parts > 0) e = p.umma_cg > 0 ? launch_prefix_umma(a, d->fmt, s) : launch_prefix_mma(a, d->fmt, false, s);
-  if (e == cudaSuccess && p.own_parts > 0) e = launch_prefix_mma(a, d->fmt, true, s);
-  if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, d->fmt == QKV_E4M3 ? d->v_scale_layer : 1.f, s);
+  if (p.umma_cg > 0) e = launch_prefix_umma(a, d->fmt, s);
+  if (e == cudaSuccess && p.prefix_items + p.own_items > 0) e = launch_prefix_mma(a, d->fmt, p.umma_cg > 0, s);
+  if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, s);
   return cuda_status(e);
 }
 

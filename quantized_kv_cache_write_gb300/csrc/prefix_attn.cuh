@@ -7,17 +7,17 @@
 // in one pass over the keys with a running reference M and sum per pair; M is raised (and the
 // accumulators rescaled) only when a logit exceeds it by 2^8, so p <= 2^8.
 //
-// A CTA of four warps takes one tile of pairs, one KV head and one range of keys. OWN = false: the
-// shared prefix, pairs taken across rows (row-major), so every key that is read serves 16 pairs of
-// whatever rows. OWN = true: the keys behind the prefix, pairs of consecutive rows of one sequence.
-// Each warp streams its own 16-key tiles through a cp.async ring; warps meet once, at the end, to
-// join their sums. Quantised pools are multiplied in fp16: codes are exact fp16 values, the query is
-// pre-scaled by a power of two into fp16 (exact except for values 2^-39 below the row's largest), the K
-// scale multiplies the logit, the V scale p. p (times the V scale and a power of two) is rounded to
-// the 16-bit operand type once: relative 2^-12 (fp16) or 2^-9 (bf16), independent from key to key,
-// so an output has about the rounding error of its own 16-bit type or less.
-// One CTA tile is bound by memory: a tile of 16 keys costs about 500 warp instructions against
-// 8 KB of int8 records.
+// A CTA of four warps takes one tile of pairs, one KV head and one range of keys, either of the shared
+// prefix (pairs taken across rows, row-major, so every key that is read serves 16 pairs of whatever
+// rows) or of the keys behind it (pairs of consecutive rows of one sequence); one launch holds both kinds.
+// Each warp streams its own key tiles through a cp.async ring; warps meet once, at the end, to join
+// their sums. Tiles start at positions that are multiples of their size, so where blocks are such
+// multiples too a tile is one run of slots and costs one table lookup. Quantised pools are multiplied
+// in fp16: codes are exact fp16 values, the query is pre-scaled by a power of two into fp16 (exact except
+// for values 2^-39 below the row's largest), the K scale multiplies the logit, the V scale p. p (times the V
+// scale and a power of two) is rounded to the 16-bit operand type once: relative 2^-12 (fp16) or
+// 2^-9 (bf16), independent from key to key, so an output has about the rounding error of its own
+// 16-bit type or less.
 #pragma once
 
 #include "qkv_internal.cuh"
@@ -25,7 +25,6 @@
 namespace qkv {
 namespace prefix {
 
-constexpr int kKeys = 16;   // keys of a warp tile
 constexpr int kPairs = 16;  // (row, query head) pairs of a CTA: the M of the MMAs
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,12 +46,14 @@ struct Geom {
   using F = Fmt<FMT>;
   static constexpr int kRow = F::kBytes ? HD : 2 * HD;              // bytes of a record's values
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : kRow;     // bytes between records
-  // ring stages: two CTAs per SM (one for 512 B rows), 24 to 48 KB of copies in flight per CTA
-  static constexpr int kStages = kRow == 128 ? 4 : 3;
-  static constexpr int kMinBlocks = kRow == 512 ? 1 : 2;
-  static constexpr int kStage = 2 * kKeys * kRow + (F::kInt8 ? 2 * kKeys * 4 : 0) + 16;  // K, V, scales, key mask
+  // keys of a warp tile (32 where rows are short: the softmax step's fixed cost is shared), ring stages and
+  // CTAs per SM: 64 to 128 KB of copies in flight per SM
+  static constexpr int kKeys = kRow == 128 ? 32 : 16;
+  static constexpr int kStages = kRow == 128 ? 2 : 3;
+  static constexpr int kMinBlocks = kRow == 128 ? 3 : kRow == 256 ? 2 : 1;
   static constexpr int kScales = 2 * kKeys * kRow;
-  static constexpr int kMask = kStage - 16;
+  static constexpr int kMask = kScales + (F::kInt8 ? 2 * kKeys * 4 : 0);
+  static constexpr int kStage = kMask + 16;  // K, V, scales, key mask
   static constexpr int kQPad = F::kBytes ? 16 : 64;  // two rows of a quarter-warp fall on disjoint banks
   static constexpr int kQRow = 2 * HD + kQPad;
   static constexpr int kORow = HD + 4;  // floats per pair of the final join
@@ -62,7 +63,7 @@ struct Geom {
   static constexpr int kSmem = kArea + kPairs * kQRow;
 };
 
-// Tile row feeding column n of N-tile nt of q.K^T, so that the p a lane holds are those of the
+// Row (of 16) feeding column n of N-tile nt (of 2) of q.K^T, so that the p a lane holds are those of the
 // keys its transposed V fragments hold (bytes: keys 4c .. 4c + 3 in one register).
 template <int FMT>
 __device__ __forceinline__ int key_of(int nt, int n) {
@@ -77,10 +78,9 @@ __device__ __forceinline__ int swz(int r) {
   return Fmt<FMT>::kInt8 ? (((r >> 1) & 1) << 2) | (r & 1) | (((r >> 2) & 1) << 1) : ((r & 1) << 2) | ((r >> 1) & 3);
 }
 
-// Keys of its own that row r sees; kEmptyRow: it sees nothing; kPadRow: no row at all.
+// Keys of its own that a row sees; kEmptyRow: it sees nothing; kPadRow: no row at all.
 constexpr int kEmptyRow = -1, kPadRow = -2;
-__device__ __forceinline__ int row_state(const PrefixArgs& a, int64_t r, bool flags) {
-  const int seq = __ldg(a.row_seq + r), len = __ldg(a.row_len + r);
+__device__ __forceinline__ int row_state(const PrefixArgs& a, int seq, int len, bool flags) {
   if (seq == -1) return kPadRow;
   if (seq < 0 || seq >= a.num_seqs || len < 0 || len > a.max_row_len || (len > 0 && len < a.prefix_len)) {
     if (flags && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
@@ -88,154 +88,190 @@ __device__ __forceinline__ int row_state(const PrefixArgs& a, int64_t r, bool fl
   }
   return len == 0 ? kEmptyRow : len - a.prefix_len;
 }
+__device__ __forceinline__ int row_state(const PrefixArgs& a, int64_t r, bool flags) {
+  return row_state(a, __ldg(a.row_seq + r), __ldg(a.row_len + r), flags);
+}
+// A kernel that a later one of the call need not wait for, and the wait itself (programmatic launches).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
 
 // out (16-bit) of one value pair
 __device__ __forceinline__ uint32_t round2(bool f16, float x, float y) { return f16 ? pack_half2(x, y) : pack_bf162(x, y); }
 
-template <int FMT, int HD, bool OWN>
+template <int FMT, int HD>
 __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mma_kernel(const PrefixArgs a) {
   using F = Fmt<FMT>;
   using GM = Geom<FMT, HD>;
-  constexpr int RB = GM::kRow, ST = GM::kStages, CH = RB / 16;
+  constexpr int RB = GM::kRow, ST = GM::kStages, CH = RB / 16, TK = GM::kKeys, NH = TK / 16;
+  constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int sRow[kPairs], sHead[kPairs], sOwn[kPairs];
   __shared__ float sFac[kPairs], sM[kWarps][kPairs], sL[kWarps][kPairs];
   __shared__ int sEu[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, hn = lane >> 2;
   const int H = a.num_kv_heads, G = a.num_q_heads / H;
-  const int parts = OWN ? a.own_parts : a.prefix_parts;
-  uint32_t item = blockIdx.x;
-  const int part = static_cast<int>(item % static_cast<uint32_t>(parts));
-  item /= static_cast<uint32_t>(parts);
+  let_next_start();
+  const bool own_part = blockIdx.x >= a.prefix_items;
+  uint32_t item = own_part ? blockIdx.x - static_cast<uint32_t>(a.prefix_items) : blockIdx.x;
+  const uint32_t parts = own_part ? a.own_parts : a.prefix_parts;
+  const int part = static_cast<int>(item % parts);
+  item /= parts;
   const int h = static_cast<int>(item % static_cast<uint32_t>(H));
   const uint32_t tile = item / static_cast<uint32_t>(H);
 
-  // ---------------- the tile's pairs
-  int64_t r0 = 0;   // OWN: its first row
-  int nrows = 0;    // OWN: its rows, all of one sequence
-  if (OWN) {
+  // ---------------- the tile's pairs: lane i < 16 holds pair i (row, head of the group, keys of its own)
+  int my_row = -1, my_g = 0, my_own = kPadRow;
+  int64_t r0 = 0;   // own part: its first row
+  int nrows = 0;    //           its rows, all of one sequence
+  int seq = 0;
+  if (own_part) {
     const int T = G >= kPairs ? 1 : kPairs / G, chunks = (G + kPairs - 1) / kPairs;
     r0 = tile / static_cast<uint32_t>(chunks);
     const int ch = static_cast<int>(tile % static_cast<uint32_t>(chunks));
-    const int seq = __ldg(a.row_seq + r0);
+    // lane t holds row r0 + t, lane 31 the row before
+    const int64_t rr = lane == 31 ? r0 - 1 : r0 + lane;
+    const bool there = rr >= 0 && rr < a.rows && (lane == 31 || lane < T);
+    const int rs = there ? __ldg(a.row_seq + rr) : 0, rl = there ? __ldg(a.row_len + rr) : 0;
+    seq = __shfl_sync(0xffffffffu, rs, 0);
+    const uint32_t same = __ballot_sync(0xffffffffu, there && rs == seq);
     // rows [r0, r0 + n) up to the next multiple of T, while the sequence stays the same; a row that
     // continues such a run is in its first row's tile
-    if (r0 % T != 0 && __ldg(a.row_seq + r0 - 1) == seq) return;
-    nrows = 1;
-    while ((r0 + nrows) % T != 0 && r0 + nrows < a.rows && __ldg(a.row_seq + r0 + nrows) == seq) ++nrows;
-    if (tid < kPairs) {
-      const int t = G >= kPairs ? 0 : tid / G, g = G >= kPairs ? ch * kPairs + tid : tid % G;
-      const bool in = t < nrows && g < G;
-      sRow[tid] = in ? static_cast<int>(r0 + t) : -1;
-      sHead[tid] = h * G + g;
-      sOwn[tid] = in ? row_state(a, r0 + t, false) : kPadRow;
-    }
-  } else if (tid < kPairs) {
-    const int64_t flat = static_cast<int64_t>(tile) * kPairs + tid;
-    const int64_t row = flat / G;
-    const bool in = row < a.rows;
-    sRow[tid] = in ? static_cast<int>(row) : -1;
-    sHead[tid] = h * G + static_cast<int>(flat - row * G);
-    sOwn[tid] = 0;
+    const int into = static_cast<int>(r0 % T);
+    if (into != 0 && (same >> 31)) return;
+    nrows = min(__ffs(~same) - 1, T - into);
+    const int state = row_state(a, rs, rl, false);
+    const int t = G >= kPairs ? 0 : lane / G;
+    my_g = G >= kPairs ? ch * kPairs + lane : lane - t * G;
+    const int st = __shfl_sync(0xffffffffu, state, t & 31);
+    if (lane < kPairs && t < nrows && my_g < G) my_row = static_cast<int>(r0) + t, my_own = st;
+  } else {
+    const int64_t flat = static_cast<int64_t>(tile) * kPairs + lane, row = flat / G;
+    my_g = static_cast<int>(flat - row * G);
+    if (lane < kPairs && row < a.rows) my_row = static_cast<int>(row), my_own = 0;
   }
-  __syncthreads();
 
-  // ---------------- its keys [k0, k1), counted from the prefix's or the own part's first
-  int k0, k1, own_min = 0;
-  if (OWN) {
-    int n = 0;
-    own_min = INT_MAX;
-    for (int i = 0; i < kPairs; ++i) {
-      if (sRow[i] < 0) continue;
-      n = max(n, sOwn[i]);
-      own_min = min(own_min, max(sOwn[i], 0));
+  // ---------------- query rows into registers, each warp four pairs
+  constexpr int kPer = HD / 32, kQPairs = kPairs / kWarps;  // dims per lane, pairs per warp
+  uint32_t qw[kQPairs][kPer / 2];
+#pragma unroll
+  for (int i = 0; i < kQPairs; ++i) {
+    const int row = __shfl_sync(0xffffffffu, my_row, warp * kQPairs + i), g = __shfl_sync(0xffffffffu, my_g, warp * kQPairs + i);
+    const uint16_t* src = a.q + static_cast<int64_t>(max(row, 0)) * a.q_stride + static_cast<int64_t>(row >= 0 ? h * G + g : 0) * HD;
+    if (kPer == 8) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+      qw[i][0] = v.x, qw[i][1] = v.y, qw[i][kPer / 2 - 2] = v.z, qw[i][kPer / 2 - 1] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+      qw[i][0] = v.x, qw[i][1] = v.y;
     }
-    const int per = ((n + parts - 1) / parts + kKeys * kWarps - 1) / (kKeys * kWarps) * (kKeys * kWarps);
-    k0 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(part) * per));
-    k1 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(k0) + per));
+  }
+
+  // ---------------- its keys: positions [k0, k1) in tiles from a0 (a multiple of TK) on
+  int k0, k1, own_min = INT_MAX;  // own_min: the shortest row's end
+  if (own_part) {
+    const int n = max(0, __reduce_max_sync(0xffffffffu, my_own));
+    own_min = a.prefix_len + __reduce_min_sync(0xffffffffu, my_row >= 0 ? max(my_own, 0) : INT_MAX - a.prefix_len);
+    // ranges end at multiples of a CTA's step
+    const int first = a.prefix_len & ~(TK - 1), len = a.prefix_len + n - first, np = static_cast<int>(parts);
+    const int per = ((len + np - 1) / np + TK * kWarps - 1) / (TK * kWarps) * (TK * kWarps);
+    const int64_t lo = first + static_cast<int64_t>(part) * per;
+    k0 = static_cast<int>(max(static_cast<int64_t>(a.prefix_len), min(lo, static_cast<int64_t>(a.prefix_len) + n)));
+    k1 = static_cast<int>(min(lo + per, static_cast<int64_t>(a.prefix_len) + n));
+    if (n == 0) k1 = k0;
   } else {
     k0 = static_cast<int>(min(static_cast<int64_t>(a.prefix_len), static_cast<int64_t>(part) * a.prefix_chunk));
     k1 = static_cast<int>(min(static_cast<int64_t>(a.prefix_len), static_cast<int64_t>(k0) + a.prefix_chunk));
   }
-  const int ntiles = (k1 - k0 + kKeys - 1) / kKeys;
+  const int a0 = k0 & ~(TK - 1);
+  const int ntiles = k1 > k0 ? (k1 - a0 + TK - 1) / TK : 0;
   const int my = ntiles > warp ? (ntiles - warp + kWarps - 1) / kWarps : 0;
 
   // ---------------- block lookups and copies
   const int32_t* table = a.prefix_blocks;
-  const int pos0 = OWN ? a.prefix_len : 0;  // position of key 0
-  if (OWN) {
-    const int seq = __ldg(a.row_seq + r0);
-    table = a.block_table + static_cast<int64_t>(seq >= 0 && seq < a.num_seqs ? seq : 0) * a.max_blocks;
-  }
+  if (own_part) table = a.block_table + static_cast<int64_t>(seq >= 0 && seq < a.num_seqs ? seq : 0) * a.max_blocks;
   const int bsz = a.block_size;
-  const bool pow2 = (bsz & (bsz - 1)) == 0;
+  const bool pow2 = (bsz & (bsz - 1)) == 0, runs = bsz % TK == 0;  // runs: a tile never leaves its block
   const int shift = __ffs(bsz) - 1;
   auto block_of = [&](int pos) -> int { return pow2 ? pos >> shift : pos / bsz; };
+  auto tile_pos = [&](int i) -> int { return a0 + (warp + kWarps * i) * TK; };
   // block id of key `lane` of this warp's tile i (loaded a tile ahead of its use)
   auto load_blk = [&](int i) -> int {
-    const int key = k0 + (warp + kWarps * i) * kKeys + lane;
-    return (i < my && lane < kKeys && key < k1) ? __ldg(table + block_of(pos0 + key)) : -1;
+    const int pos = tile_pos(i) + lane;
+    return (i < my && lane < TK && pos >= k0 && pos < k1) ? __ldg(table + block_of(pos)) : -1;
   };
   uint8_t* ring = smem + warp * ST * GM::kStage;
   const int key_sub = lane >> 3, chunk_sub = lane & 7;
+  const int64_t rec_bytes = static_cast<int64_t>(H) * GM::kGlobalRow;  // bytes between slots
   auto issue = [&](int i, int blk) {
     if (i < my) {
       uint8_t* st = ring + (i % ST) * GM::kStage;
-      const uint32_t sk = smem_u32(st), sv = sk + kKeys * RB;
-      const int key = k0 + (warp + kWarps * i) * kKeys + lane;
+      const uint32_t sk = smem_u32(st), sv = sk + TK * RB;
+      const int p0 = tile_pos(i);
+      // all keys wanted and one run of slots: no lookups per key
+      const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
+      const int64_t slot0 = static_cast<int64_t>(blk0) * bsz + (p0 - block_of(p0) * bsz);
+      const bool run = runs && p0 >= k0 && p0 + TK <= k1 && blk0 >= 0 && slot0 + TK <= a.num_slots;
       int rec_l = -1;  // record of key `lane`, -1: none
-      if (lane < kKeys && key < k1) {
-        const int pos = pos0 + key;
-        const int64_t slot = static_cast<int64_t>(blk) * bsz + (pos - block_of(pos) * bsz);
-        if (blk < 0 || slot >= a.num_slots) {
-          if (a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
-        } else {
-          rec_l = static_cast<int>(slot) * H + h;  // the host keeps num_slots * H below 2^31
+      uint32_t mask = kAll;
+      if (!run) {
+        const int pos = p0 + lane;
+        if (lane < TK && pos >= k0 && pos < k1) {
+          const int64_t slot = static_cast<int64_t>(blk) * bsz + (pos - block_of(pos) * bsz);
+          if (blk < 0 || slot >= a.num_slots) {
+            if (a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+          } else {
+            rec_l = static_cast<int>(slot) * H + h;  // the host keeps num_slots * H below 2^31
+          }
         }
+        mask = __ballot_sync(0xffffffffu, rec_l >= 0);
+      } else {
+        rec_l = (static_cast<int>(slot0) + lane) * H + h;  // lanes past the tile: not used
       }
-      const uint32_t mask = __ballot_sync(0xffffffffu, rec_l >= 0);
       if (lane == 0) sts32(sk + GM::kMask, mask);
       if (!F::kInline) {
         // four keys per instruction, one 128 B line of each; a masked key zero-fills its rows
+        const int64_t run_off = run ? (static_cast<int64_t>(slot0 + key_sub) * H + h) * RB + 16 * chunk_sub : 0;
 #pragma unroll
-        for (int t = 0; t < kKeys / 4; ++t) {
+        for (int t = 0; t < TK / 4; ++t) {
           const int kr = key_sub + 4 * t;
-          const int rec = __shfl_sync(0xffffffffu, rec_l, kr);
-          const int nb = rec >= 0 ? 16 : 0;
-          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(max(rec, 0))) * RB;
+          int nb = 16;
+          int64_t off = run_off + 4 * t * rec_bytes;
+          if (!run) {
+            const int rec = __shfl_sync(0xffffffffu, rec_l, kr);
+            nb = rec >= 0 ? 16 : 0;
+            off = static_cast<int64_t>(max(rec, 0)) * RB + 16 * chunk_sub;
+          }
 #pragma unroll
           for (int u = 0; u < CH / 8; ++u) {
-            const int ch = chunk_sub + 8 * u;
-            const uint32_t d = kr * RB + ((ch ^ swz<FMT>(kr)) << 4);
-            cp_async16(sk + d, a.k_cache + off + 16 * ch, nb);
-            cp_async16(sv + d, a.v_cache + off + 16 * ch, nb);
+            const uint32_t d = kr * RB + (((chunk_sub + 8 * u) ^ swz<FMT>(kr & 15)) << 4);
+            cp_async16(sk + d, a.k_cache + off + 128 * u, nb);
+            cp_async16(sv + d, a.v_cache + off + 128 * u, nb);
           }
         }
-        if (F::kInt8 && lane < kKeys) {
+        if (F::kInt8 && lane < TK) {
           cp_async4(sk + GM::kScales + 4 * lane, a.k_scale_tok + max(rec_l, 0), rec_l >= 0 ? 4 : 0);
-          cp_async4(sk + GM::kScales + 4 * (kKeys + lane), a.v_scale_tok + max(rec_l, 0), rec_l >= 0 ? 4 : 0);
+          cp_async4(sk + GM::kScales + 4 * (TK + lane), a.v_scale_tok + max(rec_l, 0), rec_l >= 0 ? 4 : 0);
         }
       } else {
         // inline records sit on 4 B boundaries: 4 B copies, one key per instruction
 #pragma unroll 4
-        for (int kr = 0; kr < kKeys; ++kr) {
+        for (int kr = 0; kr < TK; ++kr) {
           const int rec = __shfl_sync(0xffffffffu, rec_l, kr);
           const int nb = rec >= 0 ? 4 : 0;
           const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(max(rec, 0))) * GM::kGlobalRow;
 #pragma unroll
           for (int u = 0; u < HD / 128; ++u) {
             const int w = lane + 32 * u;
-            const uint32_t d = kr * RB + (((w >> 2) ^ swz<FMT>(kr)) << 4) + 4 * (w & 3);
+            const uint32_t d = kr * RB + (((w >> 2) ^ swz<FMT>(kr & 15)) << 4) + 4 * (w & 3);
             cp_async4(sk + d, a.k_cache + off + 4 * w, nb);
             cp_async4(sv + d, a.v_cache + off + 4 * w, nb);
           }
         }
-        if (lane < kKeys) {
+        if (lane < TK) {
           const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(max(rec_l, 0))) * GM::kGlobalRow + HD;
           cp_async4(sk + GM::kScales + 4 * lane, a.k_cache + off, rec_l >= 0 ? 4 : 0);
-          cp_async4(sk + GM::kScales + 4 * (kKeys + lane), a.v_cache + off, rec_l >= 0 ? 4 : 0);
+          cp_async4(sk + GM::kScales + 4 * (TK + lane), a.v_cache + off, rec_l >= 0 ? 4 : 0);
         }
       }
     }
@@ -250,25 +286,16 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     blk = next;
   }
 
-  // ---------------- stage the query: each warp four pairs; bytes pools in the fragments' dim order
+  // ---------------- the query into shared memory; bytes pools: fp16, in the fragments' dim order
   uint8_t* sQ = smem + GM::kArea;
-  for (int i = warp * (kPairs / kWarps); i < (warp + 1) * (kPairs / kWarps); ++i) {
-    const bool in = sRow[i] >= 0;
-    const uint16_t* src = a.q + (in ? static_cast<int64_t>(sRow[i]) * a.q_stride : 0) + static_cast<int64_t>(in ? sHead[i] : 0) * HD;
-    constexpr int kPer = HD / 32;  // dims per lane: 4 or 8
+#pragma unroll
+  for (int i = 0; i < kQPairs; ++i) {
+    const int pair = warp * kQPairs + i;
+    const bool in = __shfl_sync(0xffffffffu, my_row, pair) >= 0;
     uint32_t w[kPer / 2];
 #pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) w[k] = 0u;
-    if (in) {
-      if (kPer == 8) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-        w[0] = v.x, w[1] = v.y, w[kPer / 2 - 2] = v.z, w[kPer / 2 - 1] = v.w;
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + lane);
-        w[0] = v.x, w[1] = v.y;
-      }
-    }
-    uint8_t* row = sQ + i * GM::kQRow;
+    for (int k = 0; k < kPer / 2; ++k) w[k] = in ? qw[i][k] : 0u;
+    uint8_t* row = sQ + pair * GM::kQRow;
     float fac = fabsf(a.softmax_scale) * kLog2e;
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;  // into the query: the logit factor stays >= 0
     if (F::kBytes) {
@@ -284,8 +311,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
         }
         m = fmaxf(m, fabsf(x[k]));
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // magnitudes: bits order like values
       // largest magnitude into [2^14, 2^15): e = 14 - floor(log2 m), kept where 2^e and 2^-e are normal
       int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
       e = max(-112, min(126, e));
@@ -306,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
       for (int k = 0; k < kPer; k += 4)
         *reinterpret_cast<uint2*>(row + (lane * kPer + k) * 2) = make_uint2(w[k / 2] ^ flip, w[k / 2 + 1] ^ flip);
     }
-    if (lane == 0) sFac[i] = fac;
+    if (lane == 0) sFac[pair] = fac;
   }
   __syncthreads();
 
@@ -318,112 +344,133 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
   float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   int eu = -120;  // int8: the accumulators hold values times 2^-eu
   const float fac[2] = {sFac[hn], sFac[hn + 8]};
-  const int own[2] = {sOwn[hn], sOwn[hn + 8]};
-  const int row_of[2] = {sRow[hn], sRow[hn + 8]};
+  // first position past each of the lane's two rows
+  int end[2], row_of[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int ow = __shfl_sync(0xffffffffu, my_own, hn + 8 * p);
+    end[p] = own_part ? a.prefix_len + max(ow, 0) : INT_MAX;
+    row_of[p] = __shfl_sync(0xffffffffu, my_row, hn + 8 * p);
+  }
   const uint32_t qa = smem_u32(sQ) + hn * GM::kQRow, qb = qa + 8 * GM::kQRow;
-  int kr[2];  // tile rows of this lane's K fragments
-  kr[0] = key_of<FMT>(0, hn);
-  kr[1] = key_of<FMT>(1, hn);
+  // 128-wide heads: the query's fragments stay in registers
+  constexpr bool kQReg = HD == 128;
+  uint4 qf[kQReg ? HD / 32 : 1][2];
+  if (kQReg) {
+#pragma unroll
+    for (int j = 0; j < HD / 32; ++j) {
+      const uint32_t qo = F::kBytes ? 128 * (j >> 1) + 32 * c + 16 * (j & 1) : 64 * j + 16 * c;
+      qf[j % (kQReg ? HD / 32 : 1)][0] = lds128(qa + qo);
+      qf[j % (kQReg ? HD / 32 : 1)][1] = lds128(qb + qo);
+    }
+  }
 
 #pragma unroll 1
   for (int i = 0; i < my; ++i) {
     const int next = load_blk(i + ST);
     cp_async_wait<ST - 2>();
     __syncwarp();
-    const uint32_t sk = smem_u32(ring + (i % ST) * GM::kStage), sv = sk + kKeys * RB;
+    const uint32_t sk = smem_u32(ring + (i % ST) * GM::kStage), sv = sk + TK * RB;
     const uint32_t mask = lds32(sk + GM::kMask);
+    const int base = tile_pos(i);
+    // every key wanted by every row: no masks
+    const bool whole = mask == kAll && base + TK <= own_min;
 
-    // ---- logits: two N-tiles of eight keys, two chains each
-    float s[2][2][4];
+    // ---- logits: N-tiles of eight keys
+    float s[2 * NH][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][0][k] = s[n][1][k] = 0.f;
-    if (F::kBytes) {
+      for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+    uint4 kb[2 * NH];  // bytes pools: 16 dims per lane, for two j
 #pragma unroll
-      for (int jb = 0; jb < HD / 64; ++jb) {
-        uint4 kw[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) kw[n] = lds128(sk + kr[n] * RB + (((4 * jb + c) ^ swz<FMT>(kr[n])) << 4));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t qo = 128 * jb + 32 * c + 16 * half;
-          const uint4 x = lds128(qa + qo), y = lds128(qb + qo);
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t af[4] = {w ? x.z : x.x, w ? y.z : y.x, w ? x.w : x.y, w ? y.w : y.y};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t kk = half ? (w ? kw[n].w : kw[n].z) : (w ? kw[n].y : kw[n].x);
-              uint32_t b0, b1;
-              if (F::kInt8) {
-                b0 = i8pair_to_f16x2(kk);
-                b1 = i8pair_to_f16x2(kk >> 8);
-              } else {
-                b0 = e4m3pair_to_f16x2(kk);
-                b1 = e4m3pair_to_f16x2(kk >> 16);
-              }
-              mma_f16(s[n][w], af, b0, b1);
-            }
-          }
-        }
+    for (int j = 0; j < HD / 32; ++j) {  // two k-steps of 16 dims
+      uint4 x, y;
+      if (kQReg) {
+        x = qf[j % (kQReg ? HD / 32 : 1)][0], y = qf[j % (kQReg ? HD / 32 : 1)][1];
+      } else {
+        const uint32_t qo = F::kBytes ? 128 * (j >> 1) + 32 * c + 16 * (j & 1) : 64 * j + 16 * c;
+        x = lds128(qa + qo), y = lds128(qb + qo);
       }
-    } else {
+      const uint32_t a0f[4] = {x.x, y.x, x.y, y.y}, a1f[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
-      for (int jb = 0; jb < HD / 32; ++jb) {
-        uint4 kw[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) kw[n] = lds128(sk + kr[n] * RB + (((4 * jb + c) ^ swz<FMT>(kr[n])) << 4));
-        const uint4 x = lds128(qa + 64 * jb + 16 * c), y = lds128(qb + 64 * jb + 16 * c);
-        const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          if (F::kBf16) {
-            mma_bf16(s[n][0], a0, kw[n].x, kw[n].y);
-            mma_bf16(s[n][1], a1, kw[n].z, kw[n].w);
+      for (int n = 0; n < 2 * NH; ++n) {
+        const int kr = key_of<FMT>(n & 1, hn);
+        const uint32_t krow = sk + (kr + 16 * (n >> 1)) * RB;
+        if (F::kBytes) {
+          if ((j & 1) == 0) kb[n] = lds128(krow + (((4 * (j >> 1) + c) ^ swz<FMT>(kr)) << 4));
+          const uint2 kw = (j & 1) ? make_uint2(kb[n].z, kb[n].w) : make_uint2(kb[n].x, kb[n].y);  // four dims per k-step
+          if (F::kInt8) {
+            mma_f16(s[n], a0f, i8pair_to_f16x2(kw.x), i8pair_to_f16x2(kw.x >> 8));
+            mma_f16(s[n], a1f, i8pair_to_f16x2(kw.y), i8pair_to_f16x2(kw.y >> 8));
           } else {
-            mma_f16(s[n][0], a0, kw[n].x, kw[n].y);
-            mma_f16(s[n][1], a1, kw[n].z, kw[n].w);
+            mma_f16(s[n], a0f, e4m3pair_to_f16x2(kw.x), e4m3pair_to_f16x2(kw.x >> 16));
+            mma_f16(s[n], a1f, e4m3pair_to_f16x2(kw.y), e4m3pair_to_f16x2(kw.y >> 16));
+          }
+        } else {
+          const uint4 kw = lds128(krow + (((4 * j + c) ^ swz<FMT>(kr)) << 4));
+          if (F::kBf16) {
+            mma_bf16(s[n], a0f, kw.x, kw.y);
+            mma_bf16(s[n], a1f, kw.z, kw.w);
+          } else {
+            mma_f16(s[n], a0f, kw.x, kw.y);
+            mma_f16(s[n], a1f, kw.z, kw.w);
           }
         }
       }
     }
 
-    // ---- softmax step. Lane's columns: keys key_of(n, 2c + {0, 1}); rows hn, hn + 8
-    const int base = k0 + (warp + kWarps * i) * kKeys;
-    float y[2][2][2];  // [pair][n][column]
-    float vs[2][2];    // int8: V scales of the lane's keys, times 2^-eu below
+    // ---- softmax step. Lane's columns of N-tile n: keys 16 (n / 2) + key_of(n % 2, 2c + {0, 1}); rows hn, hn + 8
+    float vs[NH][4];  // int8: V scales of the lane's keys 4c .. 4c + 3 of each 16
     float vmax = 0.f;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int key = key_of<FMT>(n, 2 * c + k);
-        const bool valid = (mask >> key) & 1;
-        float ks = 1.f;
-        if (F::kInt8) {
-          ks = __uint_as_float(lds32(sk + GM::kScales + 4 * key));
-          vs[n][k] = __uint_as_float(lds32(sk + GM::kScales + 4 * (kKeys + key)));
-          vmax = fmaxf(vmax, fabsf(vs[n][k]));
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float z = (s[n][0][2 * p + k] + s[n][1][2 * p + k]) * ks * fac[p];
-          y[p][n][k] = (valid && (!OWN || base + key < own[p])) ? z : -INFINITY;
-        }
+    for (int g = 0; g < NH; ++g) {
+      float4 ks = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (F::kInt8) {
+        const uint4 kb = lds128(sk + GM::kScales + 4 * (16 * g + 4 * c)), vb = lds128(sk + GM::kScales + 4 * (TK + 16 * g + 4 * c));
+        ks = make_float4(__uint_as_float(kb.x), __uint_as_float(kb.y), __uint_as_float(kb.z), __uint_as_float(kb.w));
+        vs[g][0] = __uint_as_float(vb.x), vs[g][1] = __uint_as_float(vb.y);
+        vs[g][2] = __uint_as_float(vb.z), vs[g][3] = __uint_as_float(vb.w);
+        vmax = fmaxf(fmaxf(vmax, fmaxf(fabsf(vs[g][0]), fabsf(vs[g][1]))), fmaxf(fabsf(vs[g][2]), fabsf(vs[g][3])));
       }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            float& z = s[2 * g + n][2 * p + k];
+            // int8: key 4c + 2k + n
+            z *= F::kInt8 ? (k == 0 ? (n == 0 ? ks.x : ks.y) : (n == 0 ? ks.z : ks.w)) * fac[p] : fac[p];
+          }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int key = 16 * (n >> 1) + key_of<FMT>(n & 1, 2 * c + k);
+          const bool valid = (mask >> key) & 1;
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            if (!valid || base + key >= end[p]) s[n][2 * p + k] = -INFINITY;
+        }
     }
     float tm[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      tm[p] = fmaxf(fmaxf(y[p][0][0], y[p][0][1]), fmaxf(y[p][1][0], y[p][1][1]));
-      tm[p] = fmaxf(tm[p], __shfl_xor_sync(0xffffffffu, tm[p], 1));
-      tm[p] = fmaxf(tm[p], __shfl_xor_sync(0xffffffffu, tm[p], 2));
+      tm[p] = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 2 * NH; ++n) tm[p] = fmaxf(tm[p], fmaxf(s[n][2 * p], s[n][2 * p + 1]));
+    }
+#pragma unroll
+    for (int off = 1; off <= 2; off <<= 1) {
+      tm[0] = fmaxf(tm[0], __shfl_xor_sync(0xffffffffu, tm[0], off));
+      tm[1] = fmaxf(tm[1], __shfl_xor_sync(0xffffffffu, tm[1], off));
+      if (F::kInt8) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
     }
     int eu_new = eu;
     if (F::kInt8) {
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
       const int e = min(120, static_cast<int>(__float_as_uint(vmax) >> 23) - 126);  // vmax < 2^e
       if (e > eu) eu_new = min(120, e + kEuHeadroom);
     }
@@ -451,87 +498,108 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
       eu = eu_new;
     }
     const float vdown = F::kInt8 ? pow2f(-eu) : 1.f;
-    uint32_t pa[4];
+    uint32_t pa[NH][4];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const float ref = M[p] == -INFINITY ? 0.f : M[p] - (F::kBf16 ? 0.f : kPShift);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        float e0 = fast_exp2(y[p][n][0] - ref), e1 = fast_exp2(y[p][n][1] - ref);
+      for (int n = 0; n < 2 * NH; ++n) {
+        const float y0 = s[n][2 * p], y1 = s[n][2 * p + 1];
+        float e0 = fast_exp2(y0 - ref), e1 = fast_exp2(y1 - ref);
         l[p] += e0 + e1;
         if (F::kInt8) {
-          // a masked key's scale may be anything (0 x inf): its p stays 0
-          e0 = y[p][n][0] == -INFINITY ? 0.f : e0 * (vs[n][0] * vdown);
-          e1 = y[p][n][1] == -INFINITY ? 0.f : e1 * (vs[n][1] * vdown);
+          e0 *= vs[n >> 1][n & 1] * vdown;
+          e1 *= vs[n >> 1][2 + (n & 1)] * vdown;
+          if (!whole) {  // a masked key's scale may be anything (0 x inf): its p stays 0
+            if (y0 == -INFINITY) e0 = 0.f;
+            if (y1 == -INFINITY) e1 = 0.f;
+          }
         }
-        pa[2 * n + p] = F::kBf16 ? pack_bf162(e0, e1) : pack_half2(e0, e1);
+        pa[n >> 1][2 * (n & 1) + p] = F::kBf16 ? pack_bf162(e0, e1) : pack_half2(e0, e1);
       }
     }
 
-    // ---- p V. Rows of different lengths in one tile: a key that one row sees and another does not
-    // may hold anything there (0 x NaN), so such a tile goes row by row, each with its own keys only, and
-    // only that row's sums are taken.
-    const bool ragged = OWN && !F::kInt8 && nrows > 1 && base + kKeys > own_min;
-    const int passes = ragged ? nrows : 1;
-#pragma unroll 1
-    for (int t = 0; t < passes; ++t) {
-      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // halves of b0 / b1 (the lane's keys) that the row sees
-      if (ragged) {
-        const int n = sOwn[t * G];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          keep[k] = (base + key_of<FMT>(k, 2 * c) < n ? 0x0000ffffu : 0u) | (base + key_of<FMT>(k, 2 * c + 1) < n ? 0xffff0000u : 0u);
-      }
-#pragma unroll
-      for (int q = 0; q < HD / 32; ++q) {
-        uint32_t v[8];  // b0, b1 of four N-tiles of eight dims
-        if (F::kBytes) {
-          // matrices of 16 keys x 16 dims: chunk 2q for lanes 0-15's addresses, 2q + 1 for the others
-          uint32_t m[4];
-          const int r = lane & 15;
-          ldmatrix_x2_trans_b8(sv + r * RB + (((2 * q + (lane >> 4)) ^ swz<FMT>(r)) << 4), m[0], m[1], m[2], m[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (F::kInt8) {
-              v[2 * k] = i8pair_to_f16x2(m[k]);
-              v[2 * k + 1] = i8pair_to_f16x2(m[k] >> 8);
-            } else {
-              v[2 * k] = e4m3pair_to_f16x2(m[k]);
-              v[2 * k + 1] = e4m3pair_to_f16x2(m[k] >> 16);
-            }
-          }
-        } else {
-          // four 8 x 8 matrices: keys 0-7 and 8-15 of chunks ch and ch + 1
-          const int r = (lane & 7) + (lane & 8), chs = lane >> 4;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int ch = 4 * q + 2 * k + chs;
-            const uint32_t addr = sv + r * RB + ((ch ^ swz<FMT>(r)) << 4);
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                         : "=r"(v[4 * k]), "=r"(v[4 * k + 1]), "=r"(v[4 * k + 2]), "=r"(v[4 * k + 3])
-                         : "r"(addr));
-          }
-        }
+    // ---- p V
+    // b0, b1 of the four N-tiles of eight dims from 32 q on, 16 keys from 16 g on
+    auto v_frags = [&](int g, int q, uint32_t (&v)[8]) {
+      const uint32_t sg = sv + 16 * g * RB;
+      if (F::kBytes) {
+        // matrices of 16 keys x 16 dims: chunk 2q for lanes 0-15's addresses, 2q + 1 for the others
+        uint32_t m[4];
+        const int r = lane & 15;
+        ldmatrix_x2_trans_b8(sg + r * RB + (((2 * q + (lane >> 4)) ^ swz<FMT>(r)) << 4), m[0], m[1], m[2], m[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float* acc = o[4 * q + k];
-          if (!ragged) {
-            if (F::kBf16)
-              mma_bf16(acc, pa, v[2 * k], v[2 * k + 1]);
-            else
-              mma_f16(acc, pa, v[2 * k], v[2 * k + 1]);
+          if (F::kInt8) {
+            v[2 * k] = i8pair_to_f16x2(m[k]);
+            v[2 * k + 1] = i8pair_to_f16x2(m[k] >> 8);
           } else {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (F::kBf16)
-              mma_bf16(x, pa, v[2 * k] & keep[0], v[2 * k + 1] & keep[1]);
-            else
-              mma_f16(x, pa, v[2 * k] & keep[0], v[2 * k + 1] & keep[1]);
-            const int row = static_cast<int>(r0) + t;
-            if (row_of[0] == row) acc[0] += x[0], acc[1] += x[1];
-            if (row_of[1] == row) acc[2] += x[2], acc[3] += x[3];
+            v[2 * k] = e4m3pair_to_f16x2(m[k]);
+            v[2 * k + 1] = e4m3pair_to_f16x2(m[k] >> 16);
+          }
+        }
+      } else {
+        // four 8 x 8 matrices: keys 0-7 and 8-15 of chunks ch and ch + 1
+        const int r = (lane & 7) + (lane & 8), chs = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int ch = 4 * q + 2 * k + chs;
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                       : "=r"(v[4 * k]), "=r"(v[4 * k + 1]), "=r"(v[4 * k + 2]), "=r"(v[4 * k + 3])
+                       : "r"(sg + r * RB + ((ch ^ swz<FMT>(r)) << 4)));
+        }
+      }
+    };
+    // Rows of different lengths in one tile: a key that one row sees and another does not may hold
+    // anything there (0 x NaN), so such a tile goes row by row, each with its own keys only, and only
+    // that row's sums are taken.
+    if (!F::kInt8 && own_part && nrows > 1 && base + TK > own_min) {
+#pragma unroll 1
+      for (int t = 0; t < nrows; ++t) {
+        const int row = static_cast<int>(r0) + t;
+        const int n_end = a.prefix_len + max(0, __shfl_sync(0xffffffffu, my_own, t * G));
+#pragma unroll 1
+        for (int g = 0; g < NH; ++g) {
+          uint32_t keep[2], pg[4];  // halves of b0 / b1 (the lane's keys) that the row sees
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            keep[k] = (base + 16 * g + key_of<FMT>(k, 2 * c) < n_end ? 0x0000ffffu : 0u) |
+                      (base + 16 * g + key_of<FMT>(k, 2 * c + 1) < n_end ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pg[k] = g == 0 ? pa[0][k] : pa[NH - 1][k];
+#pragma unroll
+          for (int q = 0; q < HD / 32; ++q) {
+            uint32_t v[8];
+            v_frags(g, q, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x[4] = {0.f, 0.f, 0.f, 0.f};
+              if (F::kBf16)
+                mma_bf16(x, pg, v[2 * k] & keep[0], v[2 * k + 1] & keep[1]);
+              else
+                mma_f16(x, pg, v[2 * k] & keep[0], v[2 * k + 1] & keep[1]);
+              float* acc = o[4 * q + k];
+              if (row_of[0] == row) acc[0] += x[0], acc[1] += x[1];
+              if (row_of[1] == row) acc[2] += x[2], acc[3] += x[3];
+            }
           }
         }
       }
+    } else {
+#pragma unroll
+      for (int g = 0; g < NH; ++g)
+#pragma unroll
+        for (int q = 0; q < HD / 32; ++q) {
+          uint32_t v[8];
+          v_frags(g, q, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (F::kBf16)
+              mma_bf16(o[4 * q + k], pa[g], v[2 * k], v[2 * k + 1]);
+            else
+              mma_f16(o[4 * q + k], pa[g], v[2 * k], v[2 * k + 1]);
+          }
+        }
     }
     __syncwarp();
     issue(i + ST - 1, blk);
@@ -552,20 +620,24 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
   if (lane == 0) sEu[warp] = eu;
   __syncthreads();  // every ring is drained
   float* sO = reinterpret_cast<float*>(smem);
+  if (my > 0) {
 #pragma unroll
-  for (int t = 0; t < HD / 8; ++t)
+    for (int t = 0; t < HD / 8; ++t)
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-      *reinterpret_cast<float2*>(sO + (warp * kPairs + hn + 8 * p) * GM::kORow + 8 * t + 2 * c) =
-          make_float2(o[t][2 * p], o[t][2 * p + 1]);
+      for (int p = 0; p < 2; ++p)
+        *reinterpret_cast<float2*>(sO + (warp * kPairs + hn + 8 * p) * GM::kORow + 8 * t + 2 * c) =
+            make_float2(o[t][2 * p], o[t][2 * p + 1]);
+  }
   __syncthreads();
   const bool direct = a.o_part == nullptr;  // the only part: its result is the row's
+#pragma unroll 1
   for (int i = warp; i < kPairs; i += kWarps) {
-    const int row = sRow[i];
+    const int row = __shfl_sync(0xffffffffu, my_row, i), g = __shfl_sync(0xffffffffu, my_g, i);
     if (row < 0) continue;
+    const int head = h * G + g;
     bool empty = false;
     if (direct) {
-      const int state = row_state(a, row, lane == 0 && sHead[i] == 0);
+      const int state = row_state(a, static_cast<int64_t>(row), lane == 0 && head == 0);
       if (state == kPadRow) continue;
       empty = state == kEmptyRow;
     }
@@ -582,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     }
     const bool any = !empty && (m != -INFINITY || sum != sum);
     const float inv = any ? (direct && FMT == QKV_E4M3 ? a.v_scale_layer : 1.f) / sum : 0.f;
-    const int64_t at = static_cast<int64_t>(row) * a.num_q_heads + sHead[i];
-    const int64_t part_at = (static_cast<int64_t>(OWN ? a.prefix_parts + part : part) * a.rows) * a.num_q_heads + at;
+    const int64_t at = static_cast<int64_t>(row) * a.num_q_heads + head;
+    const int64_t part_at = (static_cast<int64_t>(own_part ? a.prefix_parts + part : part) * a.rows) * a.num_q_heads + at;
     if (lane == 0) {
       const float v = any ? (m - (F::kBf16 ? 0.f : kPShift) + log2f(sum)) * kLn2 : -INFINITY;
       if (!direct) a.lse_part[part_at] = v;
@@ -595,10 +667,9 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
+        if (f[w] == 0.f) continue;  // a warp without keys left no values
         const float4 x = *reinterpret_cast<const float4*>(sO + (w * kPairs + i) * GM::kORow + d);
-        if (f[w] != 0.f) {
-          acc.x += f[w] * x.x, acc.y += f[w] * x.y, acc.z += f[w] * x.z, acc.w += f[w] * x.w;
-        }
+        acc.x += f[w] * x.x, acc.y += f[w] * x.y, acc.z += f[w] * x.z, acc.w += f[w] * x.w;
       }
       acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
       if (direct) {
@@ -608,21 +679,39 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
       }
     }
   }
+  // the prefix's launch is over before this one is, so what waits for this one need not wait for both
+  if (blockIdx.x == 0 && tid == 0) await_previous();
 }
 
-template <int FMT, int HD, bool OWN>
-cudaError_t launch_mma(const PrefixArgs& a, cudaStream_t stream) {
+// A launch that may start while the call's previous kernel still runs (`overlaps`).
+template <typename K>
+cudaError_t launch_after(K kern, unsigned grid, unsigned block, int smem, bool overlaps, cudaStream_t stream,
+                         const PrefixArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = overlaps ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int FMT, int HD>
+cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
   constexpr int smem = Geom<FMT, HD>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(prefix_mma_kernel<FMT, HD, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = prefix_mma_kernel<FMT, HD>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prefix_mma_kernel<FMT, HD, OWN><<<static_cast<unsigned>(OWN ? a.own_items : a.prefix_items), kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, static_cast<unsigned>(a.prefix_items + a.own_items), kThreads, smem, overlaps, stream, a);
 }
 
 template <int FMT>
-cudaError_t launch_mma(const PrefixArgs& a, bool own, cudaStream_t stream) {
-  if (a.head_dim == 256) return own ? launch_mma<FMT, 256, true>(a, stream) : launch_mma<FMT, 256, false>(a, stream);
-  return own ? launch_mma<FMT, 128, true>(a, stream) : launch_mma<FMT, 128, false>(a, stream);
+cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
+  return a.head_dim == 256 ? launch_mma<FMT, 256>(a, overlaps, stream) : launch_mma<FMT, 128>(a, overlaps, stream);
 }
 
 }  // namespace prefix

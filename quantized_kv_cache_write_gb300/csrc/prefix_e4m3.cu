@@ -3,8 +3,8 @@
 
 namespace qkv {
 
-cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool own, cudaStream_t stream) {
-  return prefix::launch_mma<QKV_E4M3>(a, own, stream);
+cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
+  return prefix::launch_mma<QKV_E4M3>(a, overlaps, stream);
 }
 
 }  // namespace qkv

@@ -3,8 +3,8 @@
 
 namespace qkv {
 
-cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool own, cudaStream_t stream) {
-  return prefix::launch_mma<QKV_INT8_SIDE>(a, own, stream);
+cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
+  return prefix::launch_mma<QKV_INT8_SIDE>(a, overlaps, stream);
 }
 
 }  // namespace qkv

@@ -1,23 +1,26 @@
-// Join of the partial results of a shared-prefix attention call: one (row, query head) per warp,
-//   lse = log sum_s exp(lse_s),  o = v_scale_post sum_s exp(lse_s - lse) o_s,
+// Join of the partial results of a shared-prefix attention call, one (row, query head) pair at a time:
+//   lse = log sum_s exp(lse_s),  o = v_scale sum_s exp(lse_s - lse) o_s   (v_scale: E4M3's layer scale),
 // over the parts of the prefix and of the row's own keys, rounded once to the output's 16-bit type.
 // Rows that see nothing get o = 0, lse = -inf; padding rows are left as they were.
-// The partials come out of L2 (they were written just before).
+// The partials come out of L2 (they were written just before). With many parts four warps share a
+// pair: each takes every fourth part, and shared memory joins them.
 #include "prefix_umma.cuh"
 
 namespace qkv {
 namespace prefix {
 namespace {
 
-template <int HD>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a, float v_scale_post) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);  // (row, head)
+constexpr int kMergeWarps = 4;
+
+// WP: warps per pair (1 or 4).
+template <int HD, int WP>
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PrefixArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = WP == 1 ? 0 : warp;
+  const int64_t unit = WP == 1 ? static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp : blockIdx.x;  // pair
   const int64_t stride = a.rows * a.num_q_heads;
   if (unit >= stride) return;
   const int64_t row = unit / a.num_q_heads;
-  const int state = row_state(a, row, lane == 0 && unit == row * a.num_q_heads);
-  if (state == kPadRow) return;
+  const int state = row_state(a, row, lane == 0 && sub == 0 && unit == row * a.num_q_heads);
   // the parts of the prefix that this pair's tile was cut into, then those of its own keys
   int pre = a.prefix_parts;
   if (a.umma_cg > 0) {
@@ -26,6 +29,8 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a, f
     const int64_t tile = static_cast<int64_t>(h) * a.umma_ptiles + (row * G + (head - h * G)) / a.umma_pairs;
     pre = static_cast<int>(team_of((tile + 1) * nb - 1, total, a.umma_teams) - team_of(tile * nb, total, a.umma_teams)) + 1;
   }
+  await_previous();
+  if (state == kPadRow) return;
   const int skip = a.prefix_parts - pre;  // part numbers that this pair does not have
   const int parts = state == kEmptyRow ? 0 : pre + a.own_parts;
   auto at = [&](int s) -> int64_t { return (s < pre ? s : s + skip) * stride; };
@@ -49,15 +54,17 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a, f
   const bool any = m != -INFINITY || nan;
   const float ref = m == -INFINITY ? 0.f : m;
   if (any) {
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      const float mine = s0 + lane < parts ? expf(__ldcg(lp + at(s0 + lane)) - ref) : 0.f;
-      const int n = min(32, parts - s0);
+    // this warp's parts are sub + WP i; lane i holds the weight of the i-th of 32
+    for (int s0 = sub; s0 < parts; s0 += 32 * WP) {
+      const int mine_at = s0 + WP * lane;
+      const float mine = mine_at < parts ? expf(__ldcg(lp + at(mine_at)) - ref) : 0.f;
+      const int n = min(32, (parts - s0 + WP - 1) / WP);
 #pragma unroll 4
-      for (int s = 0; s < n; ++s) {
-        const float w = __shfl_sync(0xffffffffu, mine, s);
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xffffffffu, mine, i);
         if (w == 0.f) continue;  // a part without keys wrote no values
         sum += w;
-        const float4* src = reinterpret_cast<const float4*>(op + at(s0 + s) * HD);
+        const float4* src = reinterpret_cast<const float4*>(op + at(s0 + WP * i) * HD);
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
           const float4 x = __ldcg(src + lane + 32 * v);
@@ -66,24 +73,50 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixArgs a, f
       }
     }
   }
-  const float f = any ? v_scale_post / sum : 0.f;
+  if (WP > 1) {
+    __shared__ float4 sAcc[kMergeWarps][HD / 4];
+    __shared__ float sSum[kMergeWarps];
 #pragma unroll
-  for (int v = 0; v < kVec; ++v)
-    *reinterpret_cast<uint2*>(a.out + unit * HD + 4 * (lane + 32 * v)) =
+    for (int v = 0; v < kVec; ++v) sAcc[warp][lane + 32 * v] = acc[v];
+    if (lane == 0) sSum[warp] = sum;
+    __syncthreads();
+    if (warp >= kVec) return;
+    sum = (sSum[0] + sSum[1]) + (sSum[2] + sSum[3]);
+    const int col = lane + 32 * warp;
+    float4 t = sAcc[0][col];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) {
+      const float4 x = sAcc[w][col];
+      t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+    }
+    acc[0] = t;
+  }
+  const float f = any ? (a.merge_scale / sum) : 0.f;
+#pragma unroll
+  for (int v = 0; v < (WP > 1 ? 1 : kVec); ++v)
+    *reinterpret_cast<uint2*>(a.out + unit * HD + 4 * (lane + 32 * (WP > 1 ? warp : v))) =
         make_uint2(round2(a.q_f16, acc[v].x * f, acc[v].y * f), round2(a.q_f16, acc[v].z * f, acc[v].w * f));
-  if (lane == 0 && a.lse != nullptr) a.lse[unit] = any ? ref + logf(sum) : -INFINITY;
+  if (lane == 0 && (WP == 1 || warp == 0) && a.lse != nullptr) a.lse[unit] = any ? ref + logf(sum) : -INFINITY;
+}
+
+// Parts from which four warps share a pair.
+constexpr int kSharedParts = 8;
+
+template <int HD>
+cudaError_t launch_merge(const PrefixArgs& a, cudaStream_t stream) {
+  const int64_t pairs = a.rows * a.num_q_heads;
+  const bool overlaps = a.prefix_parts + a.own_parts > 0;
+  if (a.prefix_parts + a.own_parts >= kSharedParts)
+    return launch_after(prefix_merge_kernel<HD, 4>, static_cast<unsigned>(pairs), 32 * kMergeWarps, 0, overlaps, stream, a);
+  return launch_after(prefix_merge_kernel<HD, 1>, static_cast<unsigned>((pairs + kMergeWarps - 1) / kMergeWarps),
+                      32 * kMergeWarps, 0, overlaps, stream, a);
 }
 
 }  // namespace
 }  // namespace prefix
 
-cudaError_t launch_prefix_merge(const PrefixArgs& a, float v_scale_post, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>((a.rows * a.num_q_heads + 3) / 4);
-  if (a.head_dim == 256)
-    prefix::prefix_merge_kernel<256><<<blocks, 128, 0, stream>>>(a, v_scale_post);
-  else
-    prefix::prefix_merge_kernel<128><<<blocks, 128, 0, stream>>>(a, v_scale_post);
-  return cudaGetLastError();
+cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream) {
+  return a.head_dim == 256 ? prefix::launch_merge<256>(a, stream) : prefix::launch_merge<128>(a, stream);
 }
 
 }  // namespace qkv

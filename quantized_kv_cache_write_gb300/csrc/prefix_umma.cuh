@@ -184,10 +184,19 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// Four floats times the four that `f` holds the bits of.
-__device__ __forceinline__ void f2scale2(float* v, const uint4& f) {
-  f2scale(v, f2pack(__uint_as_float(f.x), __uint_as_float(f.y)));
-  f2scale(v + 2, f2pack(__uint_as_float(f.z), __uint_as_float(f.w)));
+// 32 columns times their keys' scales; 32 columns whose key is missing to -inf.
+__device__ __forceinline__ void scale32(float* v, const float4* f) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float4 x = f[k];
+    f2scale(v + 4 * k, f2pack(x.x, x.y));
+    f2scale(v + 4 * k + 2, f2pack(x.z, x.w));
+  }
+}
+__device__ __forceinline__ void mask32(float* v, uint32_t mask) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!((mask >> k) & 1)) v[k] = -INFINITY;
 }
 
 // The team whose range [i total / n, (i + 1) total / n) holds unit x.
@@ -251,41 +260,52 @@ struct Operand {
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : F::kBytes ? HD : 2 * HD;
   static_assert(kLpr <= 32 && kWarpRows <= 32 && kInstr >= 1, "rows of at most 512 B");
 
-  // bytes pools: instruction u's 16 B of this lane
-  static __device__ __forceinline__ uint4 load(const uint8_t* cache, int u, int lane, int rec, int off) {
-    const int rk = __shfl_sync(0xffffffffu, rec, kPerInstr * u + lane / kLpr);
-    if (rk < 0) return make_uint4(0, 0, 0, 0);
-    const uint8_t* p = cache + static_cast<uint64_t>(static_cast<uint32_t>(rk)) * kGlobalRow + off + 16 * (lane % kLpr);
-    if (F::kInline) {  // records sit on 4 B boundaries
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-      return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
-    }
-    return __ldg(reinterpret_cast<const uint4*>(p));
-  }
-  // 16 codes to fp16 and into the slot: two 16 B chunks of the key's 128 B row
-  static __device__ __forceinline__ void store(uint32_t slot, int u, int pw, int lane, const uint4& v) {
-    const int ch = lane % kLpr;
-    // row = kWarpRows pw + kPerInstr u + lane / kLpr; the warp's first row is a multiple of 8
-    const uint32_t lane_off = (ch >> 2) * kCol + (kWarpRows * pw + lane / kLpr) * 128;
-    const uint32_t base = slot + lane_off + kPerInstr * u * 128;
-    const uint32_t x = (lane / kLpr) ^ ((kPerInstr * u) & 7);  // row & 7 (disjoint bits)
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[8];
+  // bytes pools: this lane's 16 B of every instruction. A missing key (record -1) reads record 0 instead:
+  // its p is 0, so only its V must be finite (`store` clears it where a code can be NaN)
+  static __device__ __forceinline__ void load(uint4 (&raw)[kInstr], const uint8_t* cache, int lane, int rec, int off) {
+    const uint8_t* p0 = cache + off + 16 * (lane % kLpr);
+    const int rc = max(rec, 0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (F::kInt8) {
-        o[2 * k] = i8pair_to_f16x2(w[k]);
-        o[2 * k + 1] = i8pair_to_f16x2(w[k] >> 8);
+    for (int u = 0; u < kInstr; ++u) {
+      const int rk = __shfl_sync(0xffffffffu, rc, kPerInstr * u + lane / kLpr);
+      const uint8_t* p = p0 + static_cast<uint64_t>(static_cast<uint32_t>(rk)) * kGlobalRow;
+      if (F::kInline) {  // records sit on 4 B boundaries
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+        raw[u] = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
       } else {
-        o[2 * k] = e4m3pair_to_f16x2(w[k]);
-        o[2 * k + 1] = e4m3pair_to_f16x2(w[k] >> 16);
+        raw[u] = __ldg(reinterpret_cast<const uint4*>(p));
       }
     }
+  }
+  // codes to fp16 and into the slot: two 16 B chunks of the key's 128 B row per instruction
+  static __device__ __forceinline__ void store(uint32_t slot, int pw, int lane, const uint4 (&raw)[kInstr], uint32_t missing) {
+    const int ch = lane % kLpr;
+    // row = kWarpRows pw + kPerInstr u + lane / kLpr; the warp's first row is a multiple of 8
     const uint32_t c0 = 2 * (ch & 3);
-    const bool odd = kLpr > 4 && (ch & 4);  // the eight lanes of a store phase fill eight distinct chunks
-    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-    sts128(base + (((c0 + (odd ? 1 : 0)) ^ x) << 4), odd ? hi : lo);
-    sts128(base + (((c0 + (odd ? 0 : 1)) ^ x) << 4), odd ? lo : hi);
+    const uint32_t odd = kLpr > 4 && (ch & 4) ? 1 : 0;  // the eight lanes of a store phase fill eight distinct chunks
+    const uint32_t at = slot + (ch >> 2) * kCol + (kWarpRows * pw + lane / kLpr) * 128;
+    const uint32_t first = ((c0 + odd) ^ (lane / kLpr)) << 4;
+#pragma unroll
+    for (int u = 0; u < kInstr; ++u) {
+      uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      if (!F::kInt8 && missing != 0u && ((missing >> (kPerInstr * u + lane / kLpr)) & 1)) w[0] = w[1] = w[2] = w[3] = 0u;
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (F::kInt8) {
+          o[2 * k] = i8pair_to_f16x2(w[k]);
+          o[2 * k + 1] = i8pair_to_f16x2(w[k] >> 8);
+        } else {
+          o[2 * k] = e4m3pair_to_f16x2(w[k]);
+          o[2 * k + 1] = e4m3pair_to_f16x2(w[k] >> 16);
+        }
+      }
+      const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+      const uint32_t x = (kPerInstr * u) & 7;  // the rest of row & 7
+      const uint32_t a0 = at + kPerInstr * u * 128 + (first ^ (x << 4));
+      sts128(a0, odd ? hi : lo);
+      sts128(a0 ^ 16, odd ? lo : hi);
+    }
   }
   // 16-bit pools: the whole part by cp.async; missing keys are zero-filled
   static __device__ __forceinline__ void copy(uint32_t slot, const uint8_t* cache, int pw, int lane, int rec, int off) {
@@ -313,9 +333,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = CG == 2 ? blockIdx.x & 1 : 0;  // this SM in the team
-  const uint32_t sb = (smem_u32(smem) + 1023u) & ~1023u, flag = sb + U::kFlag;  // swizzled rows: 1 KB aligned
+  const uint32_t sb = (smem_u32(smem) + 1023u) & ~1023u, smem0 = smem_u32(smem), flag = sb + U::kFlag;  // swizzled rows: 1 KB aligned
   const int H = a.num_kv_heads, G = a.num_q_heads / H;
   const int64_t pairs = a.rows * G;
+  let_next_start();
 
   if (warp == U::kMmaWarp) {
     team_tmem_alloc<CG>(sb + U::kTmemSlot);
@@ -386,6 +407,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         fac *= pow2f(-e);
         if (FMT == QKV_E4M3) fac *= a.k_scale_layer;
       }
+      fac = fmaxf(fac, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
       const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
 #pragma unroll 4
       for (int d = 0; d < HD; d += 8) {
@@ -430,28 +452,26 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           const uint32_t ts = tl + U::kS + KB * b;
           const uint4 mw = lds128(sc + U::kScMask);
           const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
-          // ---- pass 1: the row's largest logit of the block
-          float mx = -INFINITY;
+          const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0));
+          const float4* vsp = reinterpret_cast<const float4*>(smem + (sc - smem0) + U::kScVs);
+          // ---- pass 1: the row's largest logit of the block. The next 32 columns load while these are
+          // worked on; four chains of maxima (sums, in pass 2) keep the warp's latency covered
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          {
+            float s[2][32];
+            tmem_ld32(ts, s[0]);
 #pragma unroll
-          for (int c = 0; c < KB / 32; ++c) {
-            float s[32];
-            tmem_ld32(ts + 32 * c, s);
-            tmem_wait_ld(s);
-            const uint32_t mask = c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w;
+            for (int c = 0; c < KB / 32; ++c) {
+              float* x = s[c & 1];
+              tmem_wait_ld(s[c & 1]);
+              if (c + 1 < KB / 32) tmem_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
+              if (F::kInt8) scale32(x, ksp + 8 * c);
+              if (!whole) mask32(x, c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              if (F::kInt8) {
-                const uint4 ks = lds128(sc + 4 * (32 * c + k));
-                f2scale2(s + k, ks);
-              }
-              if (!whole) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (!((mask >> (k + i)) & 1)) s[k + i] = -INFINITY;
-              }
-              mx = fmaxf(fmaxf(mx, fmaxf(s[k], s[k + 1])), fmaxf(s[k + 2], s[k + 3]));
+              for (int k = 0; k < 32; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
             }
           }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float tm = mx == -INFINITY ? mx : mx * fac;
           int En = E;
           if (F::kInt8) {
@@ -475,55 +495,50 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
               }
               const uint64_t f2 = f2pack(f, f);
 #pragma unroll 1
-              for (int c = 0; c < HD / 32; ++c) {
-                float o[32];
-                tmem_ld32(tl + U::kO + t * HD + 32 * c, o);
-                tmem_wait_ld(o);
+              for (int c = 0; c < HD / 32; c += 2) {
+                float o0[32], o1[32];
+                const uint32_t to = tl + U::kO + t * HD + 32 * c;
+                tmem_ld32(to, o0);
+                tmem_ld32(to + 32, o1);
+                tmem_wait_ld(o0);
+                tmem_wait_ld(o1);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) f2scale(o + k, f2);
-                tmem_st32(tl + U::kO + t * HD + 32 * c, o);
+                for (int k = 0; k < 32; k += 2) f2scale(o0 + k, f2), f2scale(o1 + k, f2);
+                tmem_st32(to, o0);
+                tmem_st32(to + 32, o1);
               }
             }
           }
           // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
           const uint64_t fac2 = f2pack(fac, fac), ref2 = f2pack(-R, -R);
-          uint64_t sum2 = 0;
+          uint64_t sum[4] = {0, 0, 0, 0};
+          {
+            float s[2][32];
+            tmem_ld32(ts, s[0]);
 #pragma unroll
-          for (int c = 0; c < KB / 32; ++c) {
-            float s[32];
-            uint32_t p[16];
-            tmem_ld32(ts + 32 * c, s);
-            tmem_wait_ld(s);
-            const uint32_t mask = c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w;
+            for (int c = 0; c < KB / 32; ++c) {
+              float* x = s[c & 1];
+              tmem_wait_ld(s[c & 1]);
+              if (c + 1 < KB / 32) tmem_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
+              if (F::kInt8) scale32(x, ksp + 8 * c);
+              if (!whole) mask32(x, c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w);
+              uint32_t p[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              if (F::kInt8) {
-                const uint4 ks = lds128(sc + 4 * (32 * c + k));
-                f2scale2(s + k, ks);
-              }
-#pragma unroll
-              for (int i = 0; i < 4; i += 2) {
+              for (int k = 0; k < 32; k += 2) {
                 float y0, y1;
-                f2unpack(f2fma(f2pack(s[k + i], s[k + i + 1]), fac2, ref2), y0, y1);
-                if (!whole) {
-                  if (!((mask >> (k + i)) & 1)) y0 = -INFINITY;
-                  if (!((mask >> (k + i + 1)) & 1)) y1 = -INFINITY;
-                }
-                s[k + i] = fast_exp2(y0);
-                s[k + i + 1] = fast_exp2(y1);
-                sum2 = f2add(sum2, f2pack(s[k + i], s[k + i + 1]));
+                f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, ref2), y0, y1);
+                x[k] = fast_exp2(y0);
+                x[k + 1] = fast_exp2(y1);
+                sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
               }
-              if (F::kInt8) {
-                const uint4 vs = lds128(sc + U::kScVs + 4 * (32 * c + k));
-                f2scale2(s + k, vs);  // a masked key's scale is 0
-              }
-              p[k / 2] = F::kBf16 ? pack_bf162(s[k], s[k + 1]) : pack_half2(s[k], s[k + 1]);
-              p[k / 2 + 1] = F::kBf16 ? pack_bf162(s[k + 2], s[k + 3]) : pack_half2(s[k + 2], s[k + 3]);
+              if (F::kInt8) scale32(x, vsp + 8 * c);  // a masked key's scale is 0
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
+              tmem_st_x16(ts + 16 * c, p);
             }
-            tmem_st_x16(ts + 16 * c, p);
           }
           float s0, s1;
-          f2unpack(sum2, s0, s1);
+          f2unpack(f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3])), s0, s1);
           l += s0 + s1;
           tmem_wait_st();
         }
@@ -574,6 +589,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     using VOp = Operand<FMT, HD, KB, U::kVDims>;
     const int pw = warp & 3;
     const int voff = rank * VOp::kBytes;  // this SM's dims
+    // missing keys read record 0; where the pool has none, the query stands in (it has a record's bytes)
+    const uint8_t* kc = a.num_slots > 0 ? a.k_cache : reinterpret_cast<const uint8_t*>(a.q);
+    const uint8_t* vc = a.num_slots > 0 ? a.v_cache : reinterpret_cast<const uint8_t*>(a.q);
     uint32_t base = 0;                    // slots of earlier segments
     bool ok = true;
     // lane's key of block j (a segment-relative number), for K (this SM's keys) and V (all)
@@ -601,33 +619,26 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       kblk = rc.lookup(k_pos(1)), vblk = rc.lookup(v_pos(1));
       if (F::kBytes) {
         uint4 kraw[KOp::kInstr], vraw[VOp::kInstr];
-#pragma unroll
-        for (int u = 0; u < KOp::kInstr; ++u) kraw[u] = KOp::load(a.k_cache, u, lane, krec, 0);
-#pragma unroll
-        for (int u = 0; u < VOp::kInstr; ++u) vraw[u] = VOp::load(a.v_cache, u, lane, vrec, voff);
+        KOp::load(kraw, kc, lane, krec, 0);
+        VOp::load(vraw, vc, lane, vrec, voff);
         for (int j = 0; j <= B; ++j) {
           if (j < B) {
             const uint32_t s = base + k_slot(j), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
             krec = rc.record(k_pos(j + 1), kblk);
             kblk = rc.lookup(k_pos(j + 2));
             if (!(ok = await(s))) break;
-#pragma unroll
-            for (int u = 0; u < KOp::kInstr; ++u) {
-              KOp::store(slot, u, pw, lane, kraw[u]);
-              if (j + 1 < B) kraw[u] = KOp::load(a.k_cache, u, lane, krec, 0);
-            }
+            KOp::store(slot, pw, lane, kraw, 0u);
+            if (j + 1 < B) KOp::load(kraw, kc, lane, krec, 0);
             hand_over(s);
           }
           if (j > 0) {
             const uint32_t s = base + v_slot(j - 1, B), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
+            const uint32_t missing = __ballot_sync(0xffffffffu, vrec < 0);
             vrec = rc.record(v_pos(j), vblk);
             vblk = rc.lookup(v_pos(j + 1));
             if (!(ok = await(s))) break;
-#pragma unroll
-            for (int u = 0; u < VOp::kInstr; ++u) {
-              VOp::store(slot, u, pw, lane, vraw[u]);
-              if (j < B) vraw[u] = VOp::load(a.v_cache, u, lane, vrec, voff);
-            }
+            VOp::store(slot, pw, lane, vraw, missing);
+            if (j < B) VOp::load(vraw, vc, lane, vrec, voff);
             hand_over(s);
           }
         }
@@ -642,11 +653,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
             const uint32_t s = base + (v ? v_slot(j - 1, B) : k_slot(j)), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
             if (!(ok = await(s))) break;
             if (v == 0) {
-              KOp::copy(slot, a.k_cache, pw, lane, krec, 0);
+              KOp::copy(slot, kc, pw, lane, krec, 0);
               krec = rc.record(k_pos(j + 1), kblk);
               kblk = rc.lookup(k_pos(j + 2));
             } else {
-              VOp::copy(slot, a.v_cache, pw, lane, vrec, voff);
+              VOp::copy(slot, vc, pw, lane, vrec, voff);
               vrec = rc.record(v_pos(j), vblk);
               vblk = rc.lookup(v_pos(j + 1));
             }

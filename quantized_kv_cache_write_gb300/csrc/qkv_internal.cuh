@@ -170,6 +170,7 @@ struct PrefixArgs {
   float softmax_scale;
   uint16_t* out;  // [rows, Hq, D] in q's type
   float* lse;     // [rows, Hq] or null
+  float merge_scale;  // the join's factor: E4M3's V scale, else 1
   uint32_t* dev_status;
   // partial results [prefix_parts + own_parts][rows][Hq] of the key ranges; null where one part
   // writes out itself
@@ -178,7 +179,7 @@ struct PrefixArgs {
   int prefix_parts;  // ranges of prefix_chunk keys of the shared prefix
   int own_parts;     // ranges of the keys behind it (of a length that goes by the row's)
   int prefix_chunk;
-  int64_t prefix_items;  // CTAs of each launch
+  int64_t prefix_items;  // CTAs of the mma.sync tiles
   int64_t own_items;
   // the prefix on tcgen05 (umma_cg > 0: SMs per team): umma_ptiles tiles of umma_pairs pairs per KV
   // head, key blocks of umma_keys
@@ -189,19 +190,19 @@ struct PrefixArgs {
   int64_t umma_tiles = 0;  // umma_ptiles * num_kv_heads
   int64_t umma_teams = 0;
 };
-// the mma.sync tiles of 16 (row, head) pairs, over the prefix or (own) the keys behind it; the tcgen05
-// tiles of 128, over the prefix
-cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool own, cudaStream_t stream);
+// the mma.sync tiles of 16 (row, head) pairs over prefix_items ranges of the prefix and own_items of the
+// keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
+cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_prefix_umma_bf16(const PrefixArgs& a, cudaStream_t stream);
-cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_prefix_umma_f16(const PrefixArgs& a, cudaStream_t stream);
-cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_prefix_umma_int8_side(const PrefixArgs& a, cudaStream_t stream);
-cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_prefix_umma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
-cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_prefix_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
-cudaError_t launch_prefix_merge(const PrefixArgs& a, float v_scale_post, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device helpers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -3,7 +3,8 @@
     python -m quantized_kv_cache_write_gb300.profile_cases <case> [--launches N]
 
 Each case builds its slot pool with the library's own write kernels from the seeded
-generator's inputs, then launches the case's gather N times (default 3), each after an L2
+generator's inputs (the append and prefix cases: from seeded random values on the device), then launches
+the case's call N times (default 3), each after an L2
 flush (a 256 MiB write), and synchronises. Profile the last launch with
 `-k regex:<kernel> -s <N - 1> -c 1`. Cases:
 
@@ -27,6 +28,12 @@ flush (a 256 MiB write), and synchronises. Profile the last launch with
                      fmt = int8 (side tensors) or e4m3 (calibrated scales)
   merge_e4m3_layer   qsa_splitk_merge of the E4M3 layer's split partials (64 rows, 16 heads, P
                      from qsa_suggest_num_splits), the separate-merge path
+  append_<fmt>       qkv_append_rope of an 8192-token chunk: int8 (16 + 1 heads of 256, side scales,
+                     524288-slot pool) or bf16 (32 + 8 heads of 128)
+  prefix_<fmt>       qkv_prefix_attn of a batch behind a shared prefix: int8 (64 rows x 16 heads of 256
+                     behind 65536 keys), e4m3 (64 rows x 64 heads of 128, 8 KV heads, 32768 keys) or
+                     bf16 (128 rows x 32 heads of 128, 4 KV heads, 8191 keys, up to 2048 of their own)
+  dense_e4m3         the same call without a prefix: 64 rows x 64 heads of 128, up to 8192 keys each
 """
 
 from __future__ import annotations
@@ -46,7 +53,8 @@ from gen import (chunked_prefill, e4m3_splitk_layer, long_context_decode, mixed_
 
 CASES = ["page1_int8_side", "page1_int8_inline", "page1_e4m3", "page1_bf16", "page1_tcgen05", "page1_gqa32",
          "page1_hd128", "e4m3_layer", "long_context", "mixed_default", "mixed_persistent", "chunked_prefill",
-         "write_int8_fill", "write_e4m3_fill", "merge_e4m3_layer"]
+         "write_int8_fill", "write_e4m3_fill", "merge_e4m3_layer", "append_int8", "append_bf16", "prefix_int8",
+         "prefix_e4m3", "prefix_bf16", "dense_e4m3"]
 
 
 def _dev(bits):
@@ -82,6 +90,55 @@ def _pool(wl, fmt):
     vc = torch.zeros_like(kc)
     q.qkv_write_e4m3(k, v, slots, kc, vc, ksl, vsl)
     return kc, vc, dict(k_scale_layer=ksl, v_scale_layer=vsl)
+
+
+def _append(case: str):
+    fmt, Hq, H, D, S = ("int8_side", 16, 1, 256, 524288) if case == "append_int8" else ("bf16", 32, 8, 128, 65536)
+    T, gen = 8192, torch.Generator(device="cuda").manual_seed(1)
+    packed = torch.randn((T, Hq + 2 * H, D), device="cuda", generator=gen).to(torch.bfloat16)
+    ang = torch.arange(131072, device="cuda", dtype=torch.float64)[:, None] * 1e6 ** (
+        -torch.arange(D // 2, device="cuda", dtype=torch.float64) / (D // 2))
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    pos = torch.randint(0, 131072, (T,), device="cuda", generator=gen).int()
+    slots = torch.randperm(S, device="cuda", generator=gen)[:T]
+    kc = torch.zeros((S, H, D), dtype=torch.bfloat16 if fmt == "bf16" else torch.int8, device="cuda")
+    vc, q_out = torch.zeros_like(kc), torch.empty((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    kw = {} if fmt == "bf16" else {n: torch.zeros((S, H), device="cuda") for n in ("k_scale", "v_scale")}
+    return lambda: q.qkv_append_rope(packed[:, Hq:Hq + H], packed[:, Hq + H:], q.FORMATS[fmt], kc, vc, cs, pos,
+                                     q=packed[:, :Hq], q_out=q_out, slot_mapping=slots, **kw)
+
+
+def _prefix(case: str):
+    fmt, rows, Hq, H, D, P, own, block = {
+        "prefix_int8": ("int8_side", 64, 16, 1, 256, 65536, 64, 16),
+        "prefix_e4m3": ("e4m3", 64, 64, 8, 128, 32768, 512, 64),
+        "prefix_bf16": ("bf16", 128, 32, 4, 128, 8191, 2048, 32),
+        "dense_e4m3": ("e4m3", 64, 64, 8, 128, 0, 8192, 64)}[case]
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    lens = [P + 1 + (own - 1) * i // (rows - 1) for i in range(rows)]
+    wide = -(-max(lens) // block)
+    shared, mine = -(-P // block), wide - P // block
+    S = (shared + rows * mine) * block
+    ids = torch.randperm(shared + rows * mine, device="cuda", generator=gen).int()
+    table = torch.full((rows, wide), -1, dtype=torch.int32, device="cuda")
+    table[:, P // block:] = ids[shared:].view(rows, mine)
+    kw = {}
+    if fmt == "bf16":
+        kc, vc = (torch.randn((S, H, D), device="cuda", generator=gen).to(torch.bfloat16) for _ in "kv")
+    elif fmt == "e4m3":
+        kc, vc = (torch.randn((S, H, D), device="cuda", generator=gen).to(torch.float8_e4m3fn).view(torch.uint8)
+                  for _ in "kv")
+    else:
+        kc, vc = (torch.randint(-127, 128, (S, H, D), device="cuda", generator=gen, dtype=torch.int8) for _ in "kv")
+        kw = {n: torch.full((S, H), 0.02, device="cuda") for n in ("k_scale_tok", "v_scale_tok")}
+    qd = torch.randn((rows, Hq, D), device="cuda", generator=gen).to(torch.bfloat16)
+    out = torch.empty_like(qd)
+    seq, ln = torch.arange(rows, device="cuda").int(), torch.tensor(lens, device="cuda").int()
+    ws = torch.empty(q.qkv_prefix_attn_workspace(q.FORMATS[fmt], rows, Hq, H, D, P, max(lens)), dtype=torch.uint8,
+                     device="cuda")
+    return lambda: q.qkv_prefix_attn(qd, q.FORMATS[fmt], kc, vc, table, seq, ln, block, D ** -0.5, max_row_len=max(lens),
+                                     num_kv_heads=H, prefix_blocks=ids[:shared], prefix_len=P, out=out, workspace=ws,
+                                     **kw)
 
 
 def build(case: str):
@@ -168,6 +225,10 @@ def build(case: str):
         out = torch.empty((R, Hq, D), dtype=torch.float32, device="cuda")
         lse = torch.empty((R, Hq), dtype=torch.float32, device="cuda")
         return lambda: q.qsa_splitk_merge(o_part, lse_part, out, lse, v_scale_post=float(kw["v_scale_layer"]))
+    if case in ("append_int8", "append_bf16"):
+        return _append(case)
+    if case in ("prefix_int8", "prefix_e4m3", "prefix_bf16", "dense_e4m3"):
+        return _prefix(case)
     raise SystemExit(f"unknown case {case!r}; one of {', '.join(CASES)}")
 
 

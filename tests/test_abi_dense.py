@@ -118,6 +118,7 @@ def test_prefix_refusals(lib):
     assert prefix(lib, prefix_len=-1) == E.QKV_ERR_ARG
     assert prefix(lib, max_row_len=19) == E.QKV_ERR_ARG  # below the prefix
     assert prefix(lib, max_row_len=65) == E.QKV_ERR_ARG  # past the table
+    assert prefix(lib, max_row_len=(1 << 30) + 1, max_blocks=1 << 28, block_size=7) == E.QKV_ERR_ARG
     for name in ("num_seqs", "max_blocks", "block_size"):
         assert prefix(lib, **{name: 0}) == E.QKV_ERR_ARG, name
     assert prefix(lib, block_size=1 << 30) == E.QKV_ERR_ARG

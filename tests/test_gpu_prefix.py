@@ -345,3 +345,29 @@ def test_each_row_has_one_heavy_key_somewhere(fmt, act, D, rows, G):
     q = bits16(q, act)
     out, lse = call(pool, b, dev16(q, act), H, 1.0 if D == 128 else 0.7)
     check(pool, b, q, act, H, 1.0 if D == 128 else 0.7, out, lse, what=f"heavy {fmt} {D}")
+
+
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("rows", [1, 20])
+def test_empty_pool(fmt, act, rows):
+    """num_slots = 0 (through the C ABI): every key is masked and flagged, nothing of the pool is read."""
+    import ctypes
+    import quantized_kv_cache_write_gb300 as qkv
+    b, pool, q, scale = case(26, fmt, act, 128, 1, 16, 40, [2] * rows, 1, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qd = dev16(q, act)
+    out, lse = torch.full_like(qd, 7.0), torch.full((rows, 16), 7.0, device="cuda")
+    ws = torch.empty(qkv.qkv_prefix_attn_workspace(qkv.FORMATS[fmt], rows, 16, 1, 128, 40, 42), dtype=torch.uint8, device="cuda")
+    keep = [torch.from_numpy(x).cuda() for x in (b.prefix_blocks, b.table, b.row_seq, b.row_len)]
+    ptr = lambda n: pool.kw[n].data_ptr() if torch.is_tensor(pool.kw.get(n)) else None
+    d = qkv.PrefixDesc(size=ctypes.sizeof(qkv.PrefixDesc), fmt=qkv.FORMATS[fmt], q_fp16=int(act == "f16"), q=qd.data_ptr(),
+                       q_stride=16 * 128, rows=rows, num_q_heads=16, num_kv_heads=1, head_dim=128,
+                       k_cache=pool.cache[0].data_ptr(), v_cache=pool.cache[1].data_ptr(), k_scale_tok=ptr("k_scale_tok"),
+                       v_scale_tok=ptr("v_scale_tok"), k_scale_layer=1.0, v_scale_layer=1.0, num_slots=0,
+                       prefix_blocks=keep[0].data_ptr(), prefix_len=40, block_table=keep[1].data_ptr(), num_seqs=rows,
+                       max_blocks=b.table.shape[1], block_size=16, row_seq=keep[2].data_ptr(), row_len=keep[3].data_ptr(),
+                       max_row_len=42, softmax_scale=scale, out=out.data_ptr(), lse=lse.data_ptr(),
+                       workspace=ws.data_ptr(), workspace_bytes=ws.numel(), dev_status=status.data_ptr())
+    assert qkv.lib.qkv_prefix_attn(ctypes.byref(d), torch.cuda.current_stream().cuda_stream) == qkv.QKV_OK
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all() and int(status.item()) == 2
