@@ -11,19 +11,27 @@
 // and V (by dims): each converts half of the pool's values, and shared memory is read and written half as
 // often per MMA as with one SM.
 //
-// Warps: softmax (four per tile, one thread per pair), four producers, one for the scales, one MMA issuer
-// (of the team's first SM). Slots (rows of 128 B, 128 B swizzle) pass from the producers to the MMA
-// warp in the order K_0 K_1 V_0 K_2 V_1 ...; K is K-major, V MN-major, and both are stored alike, one
-// 128 B row per key and 64 dims.
-//   producers: block list -> records -> 16 B loads into registers, converted to fp16 (codes are exact) and
-//     stored to the slot once it is free; the registers take the next block's loads at once, so a
-//     K and a V slot are in flight all the time. 16-bit pools skip the registers (cp.async).
+// Warps: eight for the softmax (one thread per pair), four producers, one for the records, one for the
+// scales, one MMA issuer (of the team's first SM). Slots (rows of 128 B, 128 B swizzle) pass from the producers
+// to the MMA warp in the order K_0 K_1 V_0 K_2 V_1 ...; K is K-major, V MN-major, and both are stored
+// alike, one 128 B row per key and 64 dims.
+//   records: block list -> record numbers of a block's keys, into a ring, eight blocks ahead.
+//   producers: 16 B copies (cp.async) into a staging ring three slots deep, then, by the lane that copied
+//     them, converted to fp16 (codes are exact) and stored to the slot once it is free. 16-bit pools are copied
+//     straight into the slot.
 //   scales: K and V scales, the mask of the block's keys and the largest V scale into a small ring.
 //   MMA: one thread. P is the A operand in tensor memory, in the columns of the S it was made from.
 //   softmax: y = S ks fac (log2 units). Reference R = M + E - 7: M follows the row's maximum lazily
 //     (raised when a logit passes it by 2^8), E is a power-of-two bound on the V scales, so p vs 2^-R
-//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both.
+//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. With two tiles
+//     each has four warps; with one tile four warps take the even blocks and four the odd ones: a row's
+//     two threads pass (M, E) on as soon as a block's maxima are known, so one block's exponentials run
+//     under the next one's maxima, and join their sums at a segment's end.
 // Arithmetic as in prefix_attn.cuh: exact codes, logits and sums in fp32, p rounded once.
+//
+// The roles' loops are kept rolled: five of them run at once on each scheduler, and fully unrolled they
+// outgrow the instruction cache (measured: 5.3 stalled warps per issue on instruction fetch, 256 rows x 16
+// heads behind 65536 int8 keys 549 us against 394 us).
 //
 // Every wait is bounded: a wait that runs out sets QKV_DEV_TIMEOUT, the CTA drains its MMAs, frees its
 // tensor memory and returns.
@@ -36,8 +44,8 @@ namespace prefix {
 
 constexpr int kTileM = 128;  // pairs of a tile on one SM
 constexpr int kProdWarps = 4;
-constexpr uint32_t kWaitLimit = 1u << 22;  // mbarrier polls before a wait is declared lost (about a second)
-constexpr int kScRing = 4;
+constexpr uint64_t kWaitNs = 2000000000;  // after which a wait is declared lost
+constexpr int kScRing = 4, kRecRing = 8;
 // keys of a block: 128; 64 where one SM holds 256-wide heads alone
 constexpr int umma_block_keys(int head_dim, int cg) { return head_dim == 256 && cg == 1 ? 64 : 128; }
 
@@ -45,20 +53,27 @@ template <int FMT, int HD, int NT, int CG>
 struct Umma {
   using F = Fmt<FMT>;
   static constexpr int KB = umma_block_keys(HD, CG);
-  static constexpr int kSoftWarps = 4 * NT, kScWarp = kSoftWarps + kProdWarps, kMmaWarp = kScWarp + 1;
+  static constexpr int kSoftWarps = 8, kRecWarp = kSoftWarps + kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kKRows = KB / CG, kVDims = HD / CG;  // this SM's part of a block
   static constexpr uint32_t kSlotBytes = uint32_t(KB) * HD * 2 / CG;
   static constexpr uint32_t kQTile = kTileM * HD * 2;
-  static constexpr int kSlots = kSlotBytes == 16384 ? 8 : NT * HD >= 256 ? 4 : 5;
-  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kSc = kRing + kSlots * kSlotBytes;
+  // bytes pools: staged slots beside fewer converted ones
+  static constexpr int kStaged = !F::kBytes ? 0 : kSlotBytes == 16384 ? 6 : 3;
+  static constexpr uint32_t kStageBytes = kSlotBytes / 2;
+  static constexpr int kSlots = kSlotBytes == 16384 ? (F::kBytes ? 6 : 8) : NT * HD >= 256 ? (F::kBytes ? 3 : 4) : (F::kBytes ? 4 : 5);
+  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kStage = kRing + kSlots * kSlotBytes, kSc = kStage + kStaged * kStageBytes;
   // per block: K scales, V scales, key mask (4 words), largest V scale
   static constexpr uint32_t kScVs = 4 * KB, kScMask = 8 * KB, kScVmax = kScMask + 16, kScStage = kScVmax + 16;
-  static constexpr uint32_t kBar = kSc + kScRing * kScStage;
+  static constexpr uint32_t kRec = kSc + kScRing * kScStage;       // record numbers of a block's keys
+  static constexpr uint32_t kRow = kRec + kRecRing * 4 * KB;       // per row: (M, E) of the last even and odd block
+  static constexpr uint32_t kSum = kRow + 2 * 8 * kTileM;          // and (l, R) of the two threads of a row
+  static constexpr uint32_t kBar = kSum + 2 * 8 * kTileM;
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
-                            kQFull = kScEmpty + 8 * kScRing, kDrain = kQFull + 8, kTmemSlot = kDrain + 8,
-                            kFlag = kTmemSlot + 4, kSmem = kFlag + 4 + 1024;
+                            kRecFull = kScEmpty + 8 * kScRing, kRecEmpty = kRecFull + 8 * kRecRing,
+                            kRowSet = kRecEmpty + 8 * kRecRing, kSegEnd = kRowSet + 64, kQFull = kSegEnd + 16,
+                            kDrain = kQFull + 8, kTmemSlot = kDrain + 8, kFlag = kTmemSlot + 4, kSmem = kFlag + 4 + 1024;
   static_assert(kSmem <= 232448, "one CTA per SM");
   // tensor memory columns: O of each tile, then two S buffers
   static constexpr uint32_t kO = 0, kS = NT * HD;
@@ -146,31 +161,46 @@ __device__ __forceinline__ void bar_init(uint32_t mbar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t mbar) {
   asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(mbar) : "memory");
 }
-// Arrive on the barrier at this offset in the team's first SM.
+// Arrive on the barrier at this offset in the team's first SM. What it hands over lies in this SM's own
+// shared or tensor memory and is read there by the MMAs, so the proxy (or tensor-memory) fence before it is
+// the order that is needed; a release at cluster scope would wait for the thread's global loads too (measured:
+// about 750 cycles an arrival, twice per block and producer).
 template <int CG>
 __device__ __forceinline__ void lead_arrive(uint32_t mbar) {
   if (CG == 2)
     asm volatile(
         "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, 0;\n"
-        " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n}\n" ::"r"(mbar)
+        " mbarrier.arrive.shared::cluster.b64 _, [ra];\n}\n" ::"r"(mbar)
         : "memory");
   else
     bar_arrive(mbar);
 }
+// One poll: the hardware may suspend the thread until the phase is over, for up to a millisecond here.
 __device__ __forceinline__ bool bar_try(uint32_t mbar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(mbar), "r"(parity)
+      : "r"(mbar), "r"(parity), "r"(1000000u)
       : "memory");
   return ok != 0u;
 }
-// Wait for the phase of the given parity; false when the polls ran out or the CTA's stop flag is up.
-__device__ __forceinline__ bool bar_wait(uint32_t mbar, uint32_t parity, uint32_t flag) {
-  for (uint32_t it = 0; it < kWaitLimit; ++it) {
-    if (bar_try(mbar, parity)) return true;
-    if ((it & 255u) == 255u && lds32(flag) != 0u) return false;
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  return t;
+}
+// Wait for the phase of the given parity; false when the time ran out or (where it `stops` a wait)
+// the CTA's stop flag is up.
+__device__ __forceinline__ bool bar_wait(uint32_t mbar, uint32_t parity, uint32_t flag, bool stops = true) {
+  if (bar_try(mbar, parity)) return true;
+  const uint64_t start = now_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(mbar, parity)) return true;
+    if (stops && lds32(flag) != 0u) return false;
+    if (now_ns() - start > kWaitNs) break;
   }
   sts32(flag, 1u);
   return false;
@@ -184,13 +214,19 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
 // 32 columns times their keys' scales; 32 columns whose key is missing to -inf.
-__device__ __forceinline__ void scale32(float* v, const float4* f) {
+__device__ __forceinline__ void load8(float4 (&f)[8], const float4* src) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = src[k];
+}
+__device__ __forceinline__ void scale32(float* v, const float4 (&f)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float4 x = f[k];
-    f2scale(v + 4 * k, f2pack(x.x, x.y));
-    f2scale(v + 4 * k + 2, f2pack(x.z, x.w));
+    f2scale(v + 4 * k, f2pack(f[k].x, f[k].y));
+    f2scale(v + 4 * k + 2, f2pack(f[k].z, f[k].w));
   }
 }
 __device__ __forceinline__ void mask32(float* v, uint32_t mask) {
@@ -260,35 +296,37 @@ struct Operand {
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : F::kBytes ? HD : 2 * HD;
   static_assert(kLpr <= 32 && kWarpRows <= 32 && kInstr >= 1, "rows of at most 512 B");
 
-  // bytes pools: this lane's 16 B of every instruction. A missing key (record -1) reads record 0 instead:
-  // its p is 0, so only its V must be finite (`store` clears it where a code can be NaN)
-  static __device__ __forceinline__ void load(uint4 (&raw)[kInstr], const uint8_t* cache, int lane, int rec, int off) {
+  // bytes pools: this lane's 16 B of every instruction into the staging slot (missing keys: zeros); `rec`: the ring's
+  // entry of the warp's first row
+  static __device__ __forceinline__ void stage(uint32_t stage, const uint8_t* cache, int pw, int lane, uint32_t rec, int off) {
     const uint8_t* p0 = cache + off + 16 * (lane % kLpr);
-    const int rc = max(rec, 0);
-#pragma unroll
+    const uint32_t d0 = stage + pw * kInstr * 512 + lane * 16;
+    rec += 4 * (lane / kLpr);
+#pragma unroll 4
     for (int u = 0; u < kInstr; ++u) {
-      const int rk = __shfl_sync(0xffffffffu, rc, kPerInstr * u + lane / kLpr);
-      const uint8_t* p = p0 + static_cast<uint64_t>(static_cast<uint32_t>(rk)) * kGlobalRow;
+      const int rk = static_cast<int>(lds32(rec + 4 * kPerInstr * u));
+      const uint8_t* p = p0 + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow;
       if (F::kInline) {  // records sit on 4 B boundaries
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-        raw[u] = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) cp_async4(d0 + u * 512 + 4 * w, p + 4 * w, rk >= 0 ? 4 : 0);
       } else {
-        raw[u] = __ldg(reinterpret_cast<const uint4*>(p));
+        cp_async16(d0 + u * 512, p, rk >= 0 ? 16 : 0);
       }
     }
   }
-  // codes to fp16 and into the slot: two 16 B chunks of the key's 128 B row per instruction
-  static __device__ __forceinline__ void store(uint32_t slot, int pw, int lane, const uint4 (&raw)[kInstr], uint32_t missing) {
+  // a staged slot's codes to fp16 and into the slot: two 16 B chunks of the key's 128 B row per instruction
+  static __device__ __forceinline__ void convert(uint32_t slot, uint32_t stage, int pw, int lane) {
     const int ch = lane % kLpr;
     // row = kWarpRows pw + kPerInstr u + lane / kLpr; the warp's first row is a multiple of 8
     const uint32_t c0 = 2 * (ch & 3);
     const uint32_t odd = kLpr > 4 && (ch & 4) ? 1 : 0;  // the eight lanes of a store phase fill eight distinct chunks
     const uint32_t at = slot + (ch >> 2) * kCol + (kWarpRows * pw + lane / kLpr) * 128;
     const uint32_t first = ((c0 + odd) ^ (lane / kLpr)) << 4;
-#pragma unroll
+    const uint32_t d0 = stage + pw * kInstr * 512 + lane * 16;
+#pragma unroll 4
     for (int u = 0; u < kInstr; ++u) {
-      uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-      if (!F::kInt8 && missing != 0u && ((missing >> (kPerInstr * u + lane / kLpr)) & 1)) w[0] = w[1] = w[2] = w[3] = 0u;
+      const uint4 v = lds128(d0 + u * 512);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t o[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -308,12 +346,12 @@ struct Operand {
     }
   }
   // 16-bit pools: the whole part by cp.async; missing keys are zero-filled
-  static __device__ __forceinline__ void copy(uint32_t slot, const uint8_t* cache, int pw, int lane, int rec, int off) {
+  static __device__ __forceinline__ void copy(uint32_t slot, const uint8_t* cache, int pw, int lane, uint32_t rec, int off) {
     const int ch = lane % kLpr;
 #pragma unroll 4
     for (int u = 0; u < kInstr; ++u) {
       const int lr = kPerInstr * u + lane / kLpr;
-      const int rk = __shfl_sync(0xffffffffu, rec, lr);
+      const int rk = static_cast<int>(lds32(rec + 4 * lr));
       const int row = kWarpRows * pw + lr;
       cp_async16(slot + (ch >> 3) * kCol + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                  cache + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow + off + 16 * ch, rk >= 0 ? 16 : 0);
@@ -352,8 +390,14 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       }
       for (int s = 0; s < kScRing; ++s) {
         bar_init(sb + U::kScFull + 8 * s, 1);
-        bar_init(sb + U::kScEmpty + 8 * s, U::kSoftWarps);
+        bar_init(sb + U::kScEmpty + 8 * s, 4 * NT);
       }
+      for (int s = 0; s < kRecRing; ++s) {
+        bar_init(sb + U::kRecFull + 8 * s, 1);
+        bar_init(sb + U::kRecEmpty + 8 * s, kProdWarps + 1);  // producers and scales
+      }
+      for (int s = 0; s < 8; ++s) bar_init(sb + U::kRowSet + 8 * s, 1);
+      for (int s = 0; s < 2; ++s) bar_init(sb + U::kSegEnd + 8 * s, 4);
       bar_init(sb + U::kQFull, U::kSoftWarps * CG);
       bar_init(sb + U::kDrain, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -373,11 +417,18 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
 
   if (warp < U::kSoftWarps) {
     // ================================================================ softmax: one thread per pair
-    const int t = warp >> 2, r = tid & 127;  // tile, pair of the tile
-    const uint32_t tl = tb + (static_cast<uint32_t>(32 * (warp & 3)) << 16);  // this warp's lanes
+    const int wg = warp >> 2, t = NT == 2 ? wg : 0, q4 = warp & 3, r = tid & 127;  // tile, quarter, pair of the tile
+    const uint32_t tl = tb + (static_cast<uint32_t>(32 * q4) << 16);  // this warp's lanes
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;
-    uint32_t jb = 0;
+    uint32_t jb = 0, segs = 0;
     bool ok = true;
+    // the barrier and phase of P V of running block n
+    auto await_pv = [&](uint32_t n) -> bool {
+      const uint32_t b = NT == 2 ? t : n & 1, ph = NT == 2 ? n & 1 : (n >> 1) & 1;
+      const bool done = __all_sync(0xffffffffu, bar_wait(sb + U::kPvDone + 8 * b, ph, flag));
+      tmem_fence_after_sync();
+      return done;
+    };
     while (ok && seg.next()) {
       const int h = seg.tile / a.umma_ptiles;
       const int64_t flat = ((static_cast<int64_t>(seg.tile - h * a.umma_ptiles) * NT + t) * CG + rank) * kTileM + r;
@@ -385,49 +436,60 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       const int64_t row = in ? flat / G : 0;
       const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
       const bool warp_in = __any_sync(0xffffffffu, in);
-      // ---- the pair's query row into the tile (bytes pools: fp16, pre-scaled by a power of two)
+      // ---- the pair's query row into the tile (bytes pools: fp16, pre-scaled by a power of two); one tile: half
+      // of the dims by each of the row's threads
       const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD;
       float fac = fabsf(a.softmax_scale) * kLog2e, up = sign;
-      if (F::kBytes) {
-        float m = 0.f;
-        if (in) {
-          for (int d = 0; d < HD; d += 8) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + d));
+      {
+        constexpr int kQVec = (NT == 2 ? HD : HD / 2) / 8;
+        const int d0 = NT == 2 ? 0 : wg * (HD / 2);
+        uint4 qv[kQVec];
+#pragma unroll
+        for (int i = 0; i < kQVec; ++i) qv[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + d0) + i) : make_uint4(0, 0, 0, 0);
+        if (F::kBytes) {
+          // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
+          uint32_t mb = 0;
+          auto take = [&](const uint4& v) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          };
+#pragma unroll
+          for (int i = 0; i < kQVec; ++i) take(qv[i]);
+          if (NT == 1 && in) {  // the other thread's half
+#pragma unroll 8
+            for (int i = 0; i < kQVec; ++i) take(__ldg(reinterpret_cast<const uint4*>(src + HD / 2 - d0) + i));
+          }
+          const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
+          int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
+          e = max(-112, min(126, e));
+          up = sign * pow2f(e);
+          fac *= pow2f(-e);
+          if (FMT == QKV_E4M3) fac *= a.k_scale_layer;
+        }
+        fac = fmaxf(fac, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
+        const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
+#pragma unroll
+        for (int i = 0; i < kQVec; ++i) {
+          uint4 v = qv[i];
+          if (F::kBytes) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float x[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
-              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+              x[2 * k] = f.x * up;
+              x[2 * k + 1] = f.y * up;
             }
+            // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
+            v = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
+                         : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+          } else if (sign < 0.f) {
+            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
           }
+          const int d = d0 + 8 * i;
+          sts128(qrow + (d >> 6) * (kTileM * 128) + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
         }
-        int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
-        e = max(-112, min(126, e));
-        up = sign * pow2f(e);
-        fac *= pow2f(-e);
-        if (FMT == QKV_E4M3) fac *= a.k_scale_layer;
-      }
-      fac = fmaxf(fac, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
-      const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
-#pragma unroll 4
-      for (int d = 0; d < HD; d += 8) {
-        uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
-        if (F::kBytes) {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
-            x[2 * k] = f.x * up;
-            x[2 * k + 1] = f.y * up;
-          }
-          // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
-          v = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
-                       : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
-        } else if (sign < 0.f) {
-          v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-        }
-        sts128(qrow + (d >> 6) * (kTileM * 128) + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
       }
       proxy_fence();
       __syncwarp();
@@ -437,6 +499,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       int E = F::kInt8 ? -90 : 0;
       constexpr float kShift = F::kBf16 ? 0.f : kPShift;
       for (int j = seg.b0; ok && j < seg.b1; ++j, ++jb) {
+        if (NT == 1 && static_cast<int>(jb & 1) != wg) continue;  // the other warps' block
         const uint32_t b = NT == 2 ? t : jb & 1, ph = NT == 2 ? jb & 1 : (jb >> 1) & 1;
         const uint32_t sc = sb + U::kSc + (jb & (kScRing - 1)) * U::kScStage;
         ok = bar_wait(sb + U::kScFull + 8 * (jb & (kScRing - 1)), (jb / kScRing) & 1, flag) &&
@@ -444,108 +507,112 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tmem_fence_after_sync();
-        // O of the blocks before this one: with one tile, S runs a block ahead of P V, so P V of the last block
-        // may be in flight still. Waited for at every block (before this block's P is handed over), so that the
-        // barrier is never two phases ahead or behind; with two tiles S was issued after it
-        bool o_ready = NT == 2 || j == seg.b0;
+        const uint32_t ts = tl + U::kS + KB * b;
+        const uint4 mw = lds128(sc + U::kScMask);
+        const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
+        const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0));
+        const float4* vsp = reinterpret_cast<const float4*>(smem + (sc - smem0) + U::kScVs);
+        // ---- pass 1: the row's largest logit of the block
+        float tm = -INFINITY;
         if (warp_in) {
-          const uint32_t ts = tl + U::kS + KB * b;
-          const uint4 mw = lds128(sc + U::kScMask);
-          const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
-          const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0));
-          const float4* vsp = reinterpret_cast<const float4*>(smem + (sc - smem0) + U::kScVs);
-          // ---- pass 1: the row's largest logit of the block. The next 32 columns load while these are
-          // worked on; four chains of maxima (sums, in pass 2) keep the warp's latency covered
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          {
-            float s[2][32];
-            tmem_ld32(ts, s[0]);
+#pragma unroll 1
+          for (int c = 0; c < KB / 32; ++c) {
+            float x[32];
+            float4 f[8];
+            tmem_ld32(ts + 32 * c, x);
+            if (F::kInt8) load8(f, ksp + 8 * c);  // under the tensor-memory load
+            tmem_wait_ld(x);
+            if (F::kInt8) scale32(x, f);
+            if (__builtin_expect(!whole, 0)) mask32(x, lds32(sc + U::kScMask + 4 * c));
 #pragma unroll
-            for (int c = 0; c < KB / 32; ++c) {
-              float* x = s[c & 1];
-              tmem_wait_ld(s[c & 1]);
-              if (c + 1 < KB / 32) tmem_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
-              if (F::kInt8) scale32(x, ksp + 8 * c);
-              if (!whole) mask32(x, c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
-            }
+            for (int k = 0; k < 32; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
           }
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          const float tm = mx == -INFINITY ? mx : mx * fac;
-          int En = E;
-          if (F::kInt8) {
-            const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
-            if (e > E) En = e + kEuHeadroom;
+          tm = mx == -INFINITY ? mx : mx * fac;
+        }
+        // ---- the reference after the block before (one tile: from the row's other thread)
+        float f = 1.f;  // 2^(this thread's last R - the new one)
+        if (NT == 1 && jb > 0) {
+          const uint32_t n = jb - 1;
+          ok = __all_sync(0xffffffffu, bar_wait(sb + U::kRowSet + 8 * (2 * q4 + (n & 1)), (n >> 1) & 1, flag));
+          if (!ok) break;
+          if (j > seg.b0) {
+            const uint2 st = lds64(sb + U::kRow + 8 * ((n & 1) * kTileM + r));
+            M = __uint_as_float(st.x);
+            E = static_cast<int>(st.y);
           }
-          const bool up_m = tm > M + kTau;
-          if (__any_sync(0xffffffffu, up_m || En != E)) {
-            const float Mn = up_m ? tm : M;
-            const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
-            const float f = M == -INFINITY ? 1.f : fast_exp2(R - Rn);
-            M = Mn, R = Rn, E = En;
-            l *= f;
-            if (j > seg.b0) {
-              if (!o_ready) {
-                ok = bar_wait(sb + U::kPvDone + 8 * t, (jb - 1) & 1, flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                o_ready = true;
-                tmem_fence_after_sync();
-              }
-              const uint64_t f2 = f2pack(f, f);
+        }
+        int En = E;
+        if (F::kInt8) {
+          const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
+          if (e > E) En = e + kEuHeadroom;
+        }
+        const bool up_m = tm > M + kTau, first = M == -INFINITY;
+        const float Mn = up_m ? tm : M;
+        const float Rp = first ? 0.f : M + static_cast<float>(E) - kShift;  // the reference of O so far
+        const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
+        const bool raised = __any_sync(0xffffffffu, up_m || En != E);
+        if (l != 0.f) l *= fast_exp2(R - Rn);
+        f = first ? 1.f : fast_exp2(Rp - Rn);
+        M = Mn, E = En, R = Rn;
+        if (NT == 1) {
+          sts64(sb + U::kRow + 8 * ((jb & 1) * kTileM + r), make_uint2(__float_as_uint(M), static_cast<uint32_t>(E)));
+          __syncwarp();
+          if (lane == 0) bar_arrive(sb + U::kRowSet + 8 * (2 * q4 + (jb & 1)));
+        }
+        if (raised && warp_in && j > seg.b0) {
+          // O of the blocks before: with two tiles S was issued after the last P V
+          if (NT == 1 && !(ok = await_pv(jb - 1))) break;
+          const uint64_t f2 = f2pack(f, f);
 #pragma unroll 1
-              for (int c = 0; c < HD / 32; c += 2) {
-                float o0[32], o1[32];
-                const uint32_t to = tl + U::kO + t * HD + 32 * c;
-                tmem_ld32(to, o0);
-                tmem_ld32(to + 32, o1);
-                tmem_wait_ld(o0);
-                tmem_wait_ld(o1);
+          for (int c = 0; c < HD / 32; c += 2) {
+            float o0[32], o1[32];
+            const uint32_t to = tl + U::kO + t * HD + 32 * c;
+            tmem_ld32(to, o0);
+            tmem_ld32(to + 32, o1);
+            tmem_wait_ld(o0);
+            tmem_wait_ld(o1);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) f2scale(o0 + k, f2), f2scale(o1 + k, f2);
-                tmem_st32(to, o0);
-                tmem_st32(to + 32, o1);
-              }
-            }
+            for (int k = 0; k < 32; k += 2) f2scale(o0 + k, f2), f2scale(o1 + k, f2);
+            tmem_st32(to, o0);
+            tmem_st32(to + 32, o1);
           }
-          // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
+        }
+        // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
+        if (warp_in) {
           const uint64_t fac2 = f2pack(fac, fac), ref2 = f2pack(-R, -R);
           uint64_t sum[4] = {0, 0, 0, 0};
-          {
-            float s[2][32];
-            tmem_ld32(ts, s[0]);
-#pragma unroll
-            for (int c = 0; c < KB / 32; ++c) {
-              float* x = s[c & 1];
-              tmem_wait_ld(s[c & 1]);
-              if (c + 1 < KB / 32) tmem_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
-              if (F::kInt8) scale32(x, ksp + 8 * c);
-              if (!whole) mask32(x, c == 0 ? mw.x : c == 1 ? mw.y : c == 2 ? mw.z : mw.w);
-              uint32_t p[16];
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                float y0, y1;
-                f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, ref2), y0, y1);
-                x[k] = fast_exp2(y0);
-                x[k + 1] = fast_exp2(y1);
-                sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
-              }
-              if (F::kInt8) scale32(x, vsp + 8 * c);  // a masked key's scale is 0
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
-              tmem_st_x16(ts + 16 * c, p);
+#pragma unroll 1
+          for (int c = 0; c < KB / 32; ++c) {
+            float x[32];
+            float4 f4[8];
+            tmem_ld32(ts + 32 * c, x);
+            if (F::kInt8) load8(f4, ksp + 8 * c);
+            tmem_wait_ld(x);
+            if (F::kInt8) {
+              scale32(x, f4);
+              load8(f4, vsp + 8 * c);
             }
+            if (__builtin_expect(!whole, 0)) mask32(x, lds32(sc + U::kScMask + 4 * c));
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float y0, y1;
+              f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, ref2), y0, y1);
+              x[k] = fast_exp2(y0);
+              x[k + 1] = fast_exp2(y1);
+              sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
+            }
+            if (F::kInt8) scale32(x, f4);  // a masked key's scale is 0
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
+            tmem_st_x16(ts + 16 * c, p);
           }
           float s0, s1;
           f2unpack(f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3])), s0, s1);
           l += s0 + s1;
           tmem_wait_st();
-        }
-        if (!o_ready) {
-          ok = bar_wait(sb + U::kPvDone + 8 * t, (jb - 1) & 1, flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
         }
         tmem_fence_before_sync();
         __syncwarp();
@@ -556,18 +623,36 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       }
       if (!ok) break;
       // ---- the segment's partial result
-      ok = bar_wait(sb + U::kPvDone + 8 * t, (jb - 1) & 1, flag);
-      ok = __all_sync(0xffffffffu, ok);
+      const bool mine = NT == 2 || static_cast<int>((jb - 1) & 1) == wg;  // the last block was this thread's
+      auto await_other = [&]() -> bool {
+        return __all_sync(0xffffffffu, bar_wait(sb + U::kSegEnd + 8 * (1 - wg), segs & 1, flag));
+      };
+      // one tile: the warps of the last block go first, the others answer (so neither can be a segment ahead)
+      ok = mine ? await_pv(jb - 1) : await_other();
       if (!ok) break;
-      tmem_fence_after_sync();
+      if (NT == 1) {
+        // both threads of a row: the sums at the last block's reference
+        sts64(sb + U::kSum + 8 * (wg * kTileM + r), make_uint2(__float_as_uint(l), __float_as_uint(R)));
+        __syncwarp();
+        if (lane == 0) bar_arrive(sb + U::kSegEnd + 8 * wg);
+        if (mine && !(ok = await_other())) break;
+        tmem_fence_after_sync();
+        const uint2 ot = lds64(sb + U::kSum + 8 * ((1 - wg) * kTileM + r));
+        const float lo = __uint_as_float(ot.x), Ro = __uint_as_float(ot.y);
+        const float Rf = mine ? R : Ro;
+        l = (l == 0.f ? 0.f : l * fast_exp2(R - Rf)) + (lo == 0.f ? 0.f : lo * fast_exp2(Ro - Rf));
+        R = Rf;
+      }
+      ++segs;
       if (warp_in) {
-        const bool any = M != -INFINITY || l != l;
+        const bool any = l != 0.f;  // NaN too
         const float inv = any ? 1.f / l : 0.f;
         const int64_t at = (static_cast<int64_t>(seg.part) * a.rows + row) * a.num_q_heads + head;
-        if (in) a.lse_part[at] = any ? (R + log2f(l)) * kLn2 : -INFINITY;
+        if (in && (NT == 2 || wg == 0)) a.lse_part[at] = any ? (R + log2f(l)) * kLn2 : -INFINITY;
         float* dst = a.o_part + at * HD;
+        constexpr int kCols = NT == 2 ? HD / 32 : HD / 64;  // one tile: half of the dims by each of the row's threads
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
+        for (int c = NT == 2 ? 0 : wg * kCols; c < (NT == 2 ? kCols : (wg + 1) * kCols); ++c) {
           float o[32];
           tmem_ld32(tl + U::kO + t * HD + 32 * c, o);
           tmem_wait_ld(o);
@@ -583,24 +668,15 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       }
       tmem_fence_before_sync();  // ordered before the next segment's first arrival
     }
-  } else if (warp < U::kScWarp) {
+  } else if (warp < U::kRecWarp) {
     // ================================================================ producers
     using KOp = Operand<FMT, HD, U::kKRows, HD>;
     using VOp = Operand<FMT, HD, KB, U::kVDims>;
     const int pw = warp & 3;
     const int voff = rank * VOp::kBytes;  // this SM's dims
-    // missing keys read record 0; where the pool has none, the query stands in (it has a record's bytes)
-    const uint8_t* kc = a.num_slots > 0 ? a.k_cache : reinterpret_cast<const uint8_t*>(a.q);
-    const uint8_t* vc = a.num_slots > 0 ? a.v_cache : reinterpret_cast<const uint8_t*>(a.q);
-    uint32_t base = 0;                    // slots of earlier segments
+    const uint32_t krow = 4 * (rank * U::kKRows + KOp::kWarpRows * pw), vrow = 4 * VOp::kWarpRows * pw;  // of a ring entry
+    uint32_t base = 0, jb = 0;            // slots and blocks of earlier segments
     bool ok = true;
-    // lane's key of block j (a segment-relative number), for K (this SM's keys) and V (all)
-    auto k_pos = [&](int j) -> int {
-      return lane < KOp::kWarpRows && j < seg.b1 - seg.b0 ? (seg.b0 + j) * KB + rank * U::kKRows + KOp::kWarpRows * pw + lane : INT_MAX;
-    };
-    auto v_pos = [&](int j) -> int {
-      return lane < VOp::kWarpRows && j < seg.b1 - seg.b0 ? (seg.b0 + j) * KB + VOp::kWarpRows * pw + lane : INT_MAX;
-    };
     auto await = [&](uint32_t s) -> bool {
       if (s < NS) return true;
       return __all_sync(0xffffffffu, bar_wait(sb + U::kEmpty + 8 * (s % NS), (s / NS - 1) & 1, flag));
@@ -610,38 +686,49 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kFull + 8 * (s % NS));
     };
+    // the records of running block n; given back once its V has been loaded (K is loaded before)
+    auto records = [&](uint32_t n) -> uint32_t { return sb + U::kRec + (n % kRecRing) * 4 * KB; };
+    auto await_records = [&](uint32_t n) -> bool {
+      return __all_sync(0xffffffffu, bar_wait(sb + U::kRecFull + 8 * (n % kRecRing), (n / kRecRing) & 1, flag));
+    };
+    auto free_records = [&](uint32_t n) {
+      __syncwarp();
+      if (lane == 0) bar_arrive(sb + U::kRecEmpty + 8 * (n % kRecRing));
+    };
     while (ok && seg.next()) {
-      rc.h = seg.tile / a.umma_ptiles;
       const int B = seg.b1 - seg.b0;
-      // block ids run two blocks ahead of the loads' use, records one
-      int kblk = rc.lookup(k_pos(0)), vblk = rc.lookup(v_pos(0));
-      int krec = rc.record(k_pos(0), kblk), vrec = rc.record(v_pos(0), vblk);
-      kblk = rc.lookup(k_pos(1)), vblk = rc.lookup(v_pos(1));
+      if (!(ok = await_records(jb))) break;
       if (F::kBytes) {
-        uint4 kraw[KOp::kInstr], vraw[VOp::kInstr];
-        KOp::load(kraw, kc, lane, krec, 0);
-        VOp::load(vraw, vc, lane, vrec, voff);
-        for (int j = 0; j <= B; ++j) {
-          if (j < B) {
-            const uint32_t s = base + k_slot(j), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
-            krec = rc.record(k_pos(j + 1), kblk);
-            kblk = rc.lookup(k_pos(j + 2));
-            if (!(ok = await(s))) break;
-            KOp::store(slot, pw, lane, kraw, 0u);
-            if (j + 1 < B) KOp::load(kraw, kc, lane, krec, 0);
-            hand_over(s);
+        // staging runs kStaged - 1 slots ahead of the conversion; slot e is K of block (e + 1) / 2 or V
+        auto is_v = [&](int e) -> bool { return e == 2 * B - 1 || (e > 0 && !(e & 1)); };
+        auto stage = [&](int e) {
+          if (e < 2 * B) {
+            const uint32_t st = sb + U::kStage + ((base + e) % U::kStaged) * U::kStageBytes;
+            if (is_v(e)) {
+              const uint32_t n = jb + (e == 2 * B - 1 ? B - 1 : e / 2 - 1);
+              VOp::stage(st, a.v_cache, pw, lane, records(n) + vrow, voff);
+              free_records(n);
+            } else {
+              const uint32_t n = jb + (e + 1) / 2;
+              if (e > 0 && !(ok = await_records(n))) return;
+              KOp::stage(st, a.k_cache, pw, lane, records(n) + krow, 0);
+            }
           }
-          if (j > 0) {
-            const uint32_t s = base + v_slot(j - 1, B), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
-            const uint32_t missing = __ballot_sync(0xffffffffu, vrec < 0);
-            vrec = rc.record(v_pos(j), vblk);
-            vblk = rc.lookup(v_pos(j + 1));
-            if (!(ok = await(s))) break;
-            VOp::store(slot, pw, lane, vraw, missing);
-            if (j < B) VOp::load(vraw, vc, lane, vrec, voff);
-            hand_over(s);
-          }
+          cp_async_commit();
+        };
+        for (int e = 0; ok && e < U::kStaged - 1; ++e) stage(e);
+        for (int e = 0; ok && e < 2 * B; ++e) {
+          stage(e + U::kStaged - 1);
+          if (!ok) break;
+          const uint32_t n = base + e, slot = sb + U::kRing + (n % NS) * U::kSlotBytes;
+          const uint32_t st = sb + U::kStage + (n % U::kStaged) * U::kStageBytes;
+          if (!(ok = await(n))) break;
+          cp_async_wait<U::kStaged - 1>();
+          if (is_v(e)) VOp::convert(slot, st, pw, lane);
+          else KOp::convert(slot, st, pw, lane);
+          hand_over(n);
         }
+        cp_async_wait<0>();
       } else {
         // a slot is handed over once the copies of the next one have been issued
         uint32_t last = 0;
@@ -653,13 +740,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
             const uint32_t s = base + (v ? v_slot(j - 1, B) : k_slot(j)), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
             if (!(ok = await(s))) break;
             if (v == 0) {
-              KOp::copy(slot, kc, pw, lane, krec, 0);
-              krec = rc.record(k_pos(j + 1), kblk);
-              kblk = rc.lookup(k_pos(j + 2));
+              if (j > 0 && !(ok = await_records(jb + j))) break;
+              KOp::copy(slot, a.k_cache, pw, lane, records(jb + j) + krow, 0);
             } else {
-              VOp::copy(slot, vc, pw, lane, vrec, voff);
-              vrec = rc.record(v_pos(j), vblk);
-              vblk = rc.lookup(v_pos(j + 1));
+              VOp::copy(slot, a.v_cache, pw, lane, records(jb + j - 1) + vrow, voff);
+              free_records(jb + j - 1);
             }
             cp_async_commit();
             if (pending) {
@@ -673,9 +758,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         if (ok && pending) hand_over(last);
       }
       base += 2 * B;
+      jb += B;
     }
-  } else if (warp == U::kScWarp) {
-    // ================================================================ scales and masks
+  } else if (warp == U::kRecWarp) {
+    // ================================================================ records
     uint32_t jb = 0;
     bool ok = true;
     while (ok && seg.next()) {
@@ -684,13 +770,39 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
 #pragma unroll
       for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup(seg.b0 * KB + 32 * i + lane);
       for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
-        const uint32_t n = jb & (kScRing - 1), sc = sb + U::kSc + n * U::kScStage;
-        float ks[KB / 32], vs[KB / 32];
-        uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u}, vmax = 0;  // words past the block count as whole
+        const uint32_t n = jb % kRecRing;
+        int rec[KB / 32];
 #pragma unroll
         for (int i = 0; i < KB / 32; ++i) {
-          const int p = j * KB + 32 * i + lane, rec = rc.record(p, blk[i]);
-          if (rec < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+          const int p = j * KB + 32 * i + lane;
+          rec[i] = rc.record(p, blk[i]);
+          if (rec[i] < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+          blk[i] = j + 1 < seg.b1 ? rc.lookup(p + KB) : -1;  // the next block's, a block ahead of its use
+        }
+        if (jb >= kRecRing) {
+          ok = __all_sync(0xffffffffu, bar_wait(sb + U::kRecEmpty + 8 * n, (jb / kRecRing - 1) & 1, flag));
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int i = 0; i < KB / 32; ++i) sts32(sb + U::kRec + n * 4 * KB + 4 * (32 * i + lane), static_cast<uint32_t>(rec[i]));
+        __syncwarp();
+        if (lane == 0) bar_arrive(sb + U::kRecFull + 8 * n);
+      }
+    }
+  } else if (warp == U::kScWarp) {
+    // ================================================================ scales and masks
+    uint32_t jb = 0;
+    bool ok = true;
+    while (ok && seg.next()) {
+      for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
+        const uint32_t n = jb & (kScRing - 1), sc = sb + U::kSc + n * U::kScStage, rn = jb % kRecRing;
+        float ks[KB / 32], vs[KB / 32];
+        uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u}, vmax = 0;  // words past the block count as whole
+        ok = __all_sync(0xffffffffu, bar_wait(sb + U::kRecFull + 8 * rn, (jb / kRecRing) & 1, flag));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < KB / 32; ++i) {
+          const int rec = static_cast<int>(lds32(sb + U::kRec + rn * 4 * KB + 4 * (32 * i + lane)));
           mask[i] = __ballot_sync(0xffffffffu, rec >= 0);
           ks[i] = vs[i] = 0.f;
           if (F::kInt8 && rec >= 0) {
@@ -703,8 +815,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
               vs[i] = __ldg(a.v_scale_tok + rec);
             }
           }
-          blk[i] = j + 1 < seg.b1 ? rc.lookup(p + KB) : -1;
         }
+        __syncwarp();
+        if (lane == 0) bar_arrive(sb + U::kRecEmpty + 8 * rn);
         if (jb >= kScRing) {
           ok = __all_sync(0xffffffffu, bar_wait(sb + U::kScEmpty + 8 * n, (jb / kScRing - 1) & 1, flag));
           if (!ok) break;
@@ -735,11 +848,16 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     auto qk = [&](int t, uint32_t b, uint32_t s) {
       if (t == 0 && !(ok = await_full(s))) return;
       tmem_fence_after_sync();
-      const uint32_t k = sb + U::kRing + (s % NS) * U::kSlotBytes, q = sb + U::kQ + t * U::kQTile;
+      const uint32_t d = tb + U::kS + KB * b;
+      uint64_t qd = sw128_desc(sb + U::kQ + t * U::kQTile, 16, 1024);
+      uint64_t kd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, 16, 1024);
+#pragma unroll 1
+      for (int i = 0; i < HD / 64; ++i) {  // 64 dims: one column of 128 B rows
 #pragma unroll
-      for (int ks = 0; ks < HD / 16; ++ks)
-        mma_ss<CG>(tb + U::kS + KB * b, sw128_desc(q + (ks >> 2) * (kTileM * 128) + 32 * (ks & 3), 16, 1024),
-                   sw128_desc(k + (ks >> 2) * (U::kKRows * 128) + 32 * (ks & 3), 16, 1024), U::kIdS, ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < 4; ++ks) mma_ss<CG>(d, qd + 2 * ks, kd + 2 * ks, U::kIdS, i > 0 || ks > 0 ? 1u : 0u);
+        qd += (kTileM * 128) >> 4;
+        kd += (U::kKRows * 128) >> 4;
+      }
       if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
       commit_to<CG>(sb + U::kSFull + 8 * b);
     };
@@ -748,40 +866,43 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       if (!(ok = bar_wait(sb + U::kPFull + 8 * b, ph, flag))) return;
       if (t == 0 && !(ok = await_full(s))) return;
       tmem_fence_after_sync();
-      const uint32_t v = sb + U::kRing + (s % NS) * U::kSlotBytes;
+      const uint32_t d = tb + U::kO + t * HD;
+      uint32_t p = tb + U::kS + KB * b;
+      uint64_t vd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, KB * 128, 1024);
+#pragma unroll 1
+      for (int i = 0; i < KB / 64; ++i) {  // 64 keys
 #pragma unroll
-      for (int ks = 0; ks < KB / 16; ++ks)
-        mma_ts<CG>(tb + U::kO + t * HD, tb + U::kS + KB * b + 8 * ks, sw128_desc(v + 2048 * ks, KB * 128, 1024), U::kIdO,
-                   !first || ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < 4; ++ks) mma_ts<CG>(d, p + 8 * ks, vd + 128 * ks, U::kIdO, !first || i > 0 || ks > 0 ? 1u : 0u);
+        p += 32;
+        vd += 512;
+      }
       if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
-      commit_to<CG>(sb + U::kPvDone + 8 * t);
+      commit_to<CG>(sb + U::kPvDone + 8 * b);
     };
     while (ok && seg.next()) {
       const int B = seg.b1 - seg.b0;
       ok = bar_wait(sb + U::kQFull, segs & 1, flag);
       ++segs;
-      if (ok) qk(0, NT == 2 ? 0 : jb & 1, base);
-      if (ok && NT == 2) qk(NT - 1, 1, base);
-      for (int j = 0; ok && j < B; ++j, ++jb) {
-        if (NT == 2) {
-          for (int t = 0; ok && t < NT; ++t) {
-            pv(t, t, jb & 1, base + v_slot(j, B), j == 0);
-            if (ok && j + 1 < B) qk(t, t, base + k_slot(j + 1));
-          }
-        } else {
-          if (j + 1 < B) qk(0, (jb + 1) & 1, base + k_slot(j + 1));
-          if (ok) pv(0, jb & 1, (jb >> 1) & 1, base + v_slot(j, B), j == 0);
+      // two tiles: P V of block j of a tile, then its S of block j + 1; one tile: S of block j + 1, then P V of j
+#pragma unroll 1
+      for (int j = -1; ok && j < B; ++j) {
+        const uint32_t n = jb + j;
+#pragma unroll 1
+        for (int i = 0; ok && i < 2; ++i) {
+          const int t = NT == 2 ? i : 0;
+          if (j >= 0 && (NT == 2 || i == 1))
+            pv(t, NT == 2 ? t : n & 1, NT == 2 ? n & 1 : (n >> 1) & 1, base + v_slot(j, B), j == 0);
+          if (ok && j + 1 < B && (NT == 2 || i == 0)) qk(t, NT == 2 ? t : (n + 1) & 1, base + k_slot(j + 1));
         }
       }
+      jb += B;
       base += 2 * B;
     }
     commit_to<CG>(sb + U::kDrain);
   }
   if (warp == U::kMmaWarp && lane == 0) {
     // nothing may still write tensor memory, read a slot or arrive on a barrier when the team leaves
-    bool drained = false;
-    for (uint32_t it = 0; it < kWaitLimit && !drained; ++it) drained = bar_try(sb + U::kDrain, 0);
-    if (!drained) sts32(flag, 1u);
+    bar_wait(sb + U::kDrain, 0, flag, false);
   }
   __syncwarp();
   tmem_fence_before_sync();
