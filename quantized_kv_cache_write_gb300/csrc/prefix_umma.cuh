@@ -11,22 +11,22 @@
 // and V (by dims): each converts half of the pool's values, and shared memory is read and written half as
 // often per MMA as with one SM.
 //
-// Warps: eight for the softmax (one thread per pair), four producers, one for the records, one for the
-// scales, one MMA issuer (of the team's first SM). Slots (rows of 128 B, 128 B swizzle) pass from the producers
-// to the MMA warp in the order K_0 K_1 V_0 K_2 V_1 ...; K is K-major, V MN-major, and both are stored
-// alike, one 128 B row per key and 64 dims.
+// Warps: eight for the softmax (two threads per pair, half of a block's columns each), two groups of four
+// producers, one for the records, one for the scales, one MMA issuer (of the team's first SM). Slots
+// (rows of 128 B, 128 B swizzle) pass from the producers to the MMA warp in the order
+// K_0 K_1 V_0 K_2 V_1 ..., one group every second one; K is K-major, V MN-major, and both are stored alike, one
+// 128 B row per key and 64 dims.
 //   records: block list -> record numbers of a block's keys, into a ring, eight blocks ahead.
-//   producers: 16 B copies (cp.async) into a staging ring three slots deep, then, by the lane that copied
-//     them, converted to fp16 (codes are exact) and stored to the slot once it is free. 16-bit pools are copied
-//     straight into the slot.
+//   producers: 16 B copies (cp.async) into the group's staging slot, then, by the lane that copied them,
+//     converted to fp16 (codes are exact) and stored to the slot once it is free; each 16 B read makes room for
+//     the copy of the group's next slot. 16-bit pools are copied straight into the slot.
 //   scales: K and V scales, the mask of the block's keys and the largest V scale into a small ring.
 //   MMA: one thread. P is the A operand in tensor memory, in the columns of the S it was made from.
 //   softmax: y = S ks fac (log2 units). Reference R = M + E - 7: M follows the row's maximum lazily
 //     (raised when a logit passes it by 2^8), E is a power-of-two bound on the V scales, so p vs 2^-R
-//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. With two tiles
-//     each has four warps; with one tile four warps take the even blocks and four the odd ones: a row's
-//     two threads pass (M, E) on as soon as a block's maxima are known, so one block's exponentials run
-//     under the next one's maxima, and join their sums at a segment's end.
+//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. A first pass over
+//     the thread's columns finds their maximum, the row's two threads exchange it, a second takes p; each
+//     thread's half of P goes over its own half of S.
 // Arithmetic as in prefix_attn.cuh: exact codes, logits and sums in fp32, p rounded once.
 //
 // The roles' loops are kept rolled: five of them run at once on each scheduler, and fully unrolled they
@@ -43,7 +43,7 @@ namespace qkv {
 namespace prefix {
 
 constexpr int kTileM = 128;  // pairs of a tile on one SM
-constexpr int kProdWarps = 4;
+constexpr int kProdWarps = 4;  // of a group; two groups
 constexpr uint64_t kWaitNs = 2000000000;  // after which a wait is declared lost
 constexpr int kScRing = 4, kRecRing = 8;
 // keys of a block: 128; 64 where one SM holds 256-wide heads alone
@@ -53,26 +53,24 @@ template <int FMT, int HD, int NT, int CG>
 struct Umma {
   using F = Fmt<FMT>;
   static constexpr int KB = umma_block_keys(HD, CG);
-  static constexpr int kSoftWarps = 8, kRecWarp = kSoftWarps + kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
+  static constexpr int kSoftWarps = 8, kRecWarp = kSoftWarps + 2 * kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kKRows = KB / CG, kVDims = HD / CG;  // this SM's part of a block
   static constexpr uint32_t kSlotBytes = uint32_t(KB) * HD * 2 / CG;
   static constexpr uint32_t kQTile = kTileM * HD * 2;
-  // bytes pools: staged slots beside fewer converted ones
-  static constexpr int kStaged = !F::kBytes ? 0 : kSlotBytes == 16384 ? 6 : 3;
-  static constexpr uint32_t kStageBytes = kSlotBytes / 2;
-  static constexpr int kSlots = kSlotBytes == 16384 ? (F::kBytes ? 6 : 8) : NT * HD >= 256 ? (F::kBytes ? 3 : 4) : (F::kBytes ? 4 : 5);
-  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kStage = kRing + kSlots * kSlotBytes, kSc = kStage + kStaged * kStageBytes;
+  // bytes pools: one staging slot per producer group beside the converted ones
+  static constexpr uint32_t kStageBytes = F::kBytes ? kSlotBytes / 2 : 0;
+  static constexpr int kSlots = kSlotBytes == 16384 ? (F::kBytes ? 7 : 8) : NT * HD >= 256 ? (F::kBytes ? 3 : 4) : 4;
+  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kStage = kRing + kSlots * kSlotBytes, kSc = kStage + 2 * kStageBytes;
   // per block: K scales, V scales, key mask (4 words), largest V scale
   static constexpr uint32_t kScVs = 4 * KB, kScMask = 8 * KB, kScVmax = kScMask + 16, kScStage = kScVmax + 16;
   static constexpr uint32_t kRec = kSc + kScRing * kScStage;       // record numbers of a block's keys
-  static constexpr uint32_t kRow = kRec + kRecRing * 4 * KB;       // per row: (M, E) of the last even and odd block
-  static constexpr uint32_t kSum = kRow + 2 * 8 * kTileM;          // and (l, R) of the two threads of a row
-  static constexpr uint32_t kBar = kSum + 2 * 8 * kTileM;
+  static constexpr uint32_t kRow = kRec + kRecRing * 4 * KB;       // per row: its two threads' maxima (sums), two phases
+  static constexpr uint32_t kBar = kRow + 2 * 2 * 4 * kTileM;
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
                             kRecFull = kScEmpty + 8 * kScRing, kRecEmpty = kRecFull + 8 * kRecRing,
-                            kRowSet = kRecEmpty + 8 * kRecRing, kSegEnd = kRowSet + 64, kQFull = kSegEnd + 16,
+                            kRowSet = kRecEmpty + 8 * kRecRing, kQFull = kRowSet + 32,
                             kDrain = kQFull + 8, kTmemSlot = kDrain + 8, kFlag = kTmemSlot + 4, kSmem = kFlag + 4 + 1024;
   static_assert(kSmem <= 232448, "one CTA per SM");
   // tensor memory columns: O of each tile, then two S buffers
@@ -217,22 +215,46 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
 __device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
-// 32 columns times their keys' scales; 32 columns whose key is missing to -inf.
-__device__ __forceinline__ void load8(float4 (&f)[8], const float4* src) {
+// N columns' scales; N columns times them; N columns whose key is missing to -inf.
+template <int N>
+__device__ __forceinline__ void load_scales(float4 (&f)[N], const float4* src) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = src[k];
+  for (int k = 0; k < N; ++k) f[k] = src[k];
 }
-__device__ __forceinline__ void scale32(float* v, const float4 (&f)[8]) {
+template <int N, int M>
+__device__ __forceinline__ void scale_by(float (&v)[N], const float4 (&f)[M]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < M; ++k) {
     f2scale(v + 4 * k, f2pack(f[k].x, f[k].y));
     f2scale(v + 4 * k + 2, f2pack(f[k].z, f[k].w));
   }
 }
-__device__ __forceinline__ void mask32(float* v, uint32_t mask) {
+template <int N>
+__device__ __forceinline__ void mask_by(float (&v)[N], uint32_t mask) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k)
+  for (int k = 0; k < N; ++k)
     if (!((mask >> k) & 1)) v[k] = -INFINITY;
+}
+// 16 or 32 columns of this thread's tensor-memory lane; 8 or 16 packed ones
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
+__device__ __forceinline__ void tmem_loaded(float (&v)[32]) { tmem_wait_ld(v); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st_x16(taddr, v); }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_loaded(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // The team whose range [i total / n, (i + 1) total / n) holds unit x.
@@ -285,7 +307,7 @@ struct Records {
 };
 
 // One operand's part of a block as the producers move it: ROWS keys of kBytes bytes each, from byte
-// `off` of the record on. Each warp takes a quarter of the rows; a row is kLpr lanes of 16 B. In the slot,
+// `off` of the record on. Each warp of a group takes a quarter of the rows; a row is kLpr lanes of 16 B. In the slot,
 // 64 dims of one key are a 128 B row, swizzled; columns of 64 dims are ROWS rows apart.
 template <int FMT, int HD, int ROWS, int DIMS>
 struct Operand {
@@ -296,34 +318,27 @@ struct Operand {
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : F::kBytes ? HD : 2 * HD;
   static_assert(kLpr <= 32 && kWarpRows <= 32 && kInstr >= 1, "rows of at most 512 B");
 
-  // bytes pools: this lane's 16 B of every instruction into the staging slot (missing keys: zeros); `rec`: the ring's
-  // entry of the warp's first row
-  static __device__ __forceinline__ void stage(uint32_t stage, const uint8_t* cache, int pw, int lane, uint32_t rec, int off) {
-    const uint8_t* p0 = cache + off + 16 * (lane % kLpr);
-    const uint32_t d0 = stage + pw * kInstr * 512 + lane * 16;
-    rec += 4 * (lane / kLpr);
-#pragma unroll 4
-    for (int u = 0; u < kInstr; ++u) {
-      const int rk = static_cast<int>(lds32(rec + 4 * kPerInstr * u));
-      const uint8_t* p = p0 + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow;
-      if (F::kInline) {  // records sit on 4 B boundaries
+  // Bytes pools. This lane's 16 B of instruction u into the staging slot (a missing key: zeros); `rec`: the ring's
+  // entry of the lane's first row, p0: its bytes of record 0, d0: its place in the staging slot.
+  static __device__ __forceinline__ void stage1(uint32_t d0, const uint8_t* p0, int u, uint32_t rec) {
+    const int rk = static_cast<int>(lds32(rec + 4 * kPerInstr * u));
+    const uint8_t* p = p0 + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow;
+    if (F::kInline) {  // records sit on 4 B boundaries
 #pragma unroll
-        for (int w = 0; w < 4; ++w) cp_async4(d0 + u * 512 + 4 * w, p + 4 * w, rk >= 0 ? 4 : 0);
-      } else {
-        cp_async16(d0 + u * 512, p, rk >= 0 ? 16 : 0);
-      }
+      for (int w = 0; w < 4; ++w) cp_async4(d0 + u * 512 + 4 * w, p + 4 * w, rk >= 0 ? 4 : 0);
+    } else {
+      cp_async16(d0 + u * 512, p, rk >= 0 ? 16 : 0);
     }
   }
-  // a staged slot's codes to fp16 and into the slot: two 16 B chunks of the key's 128 B row per instruction
-  static __device__ __forceinline__ void convert(uint32_t slot, uint32_t stage, int pw, int lane) {
+  // The staged codes to fp16 and into the slot, two 16 B chunks of the key's 128 B row per instruction.
+  static __device__ __forceinline__ void convert(uint32_t slot, uint32_t d0, int pw, int lane) {
     const int ch = lane % kLpr;
     // row = kWarpRows pw + kPerInstr u + lane / kLpr; the warp's first row is a multiple of 8
     const uint32_t c0 = 2 * (ch & 3);
     const uint32_t odd = kLpr > 4 && (ch & 4) ? 1 : 0;  // the eight lanes of a store phase fill eight distinct chunks
     const uint32_t at = slot + (ch >> 2) * kCol + (kWarpRows * pw + lane / kLpr) * 128;
     const uint32_t first = ((c0 + odd) ^ (lane / kLpr)) << 4;
-    const uint32_t d0 = stage + pw * kInstr * 512 + lane * 16;
-#pragma unroll 4
+#pragma unroll 2
     for (int u = 0; u < kInstr; ++u) {
       const uint4 v = lds128(d0 + u * 512);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -385,19 +400,18 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       }
       for (int b = 0; b < 2; ++b) {
         bar_init(sb + U::kSFull + 8 * b, 1);
-        bar_init(sb + U::kPFull + 8 * b, 4 * CG);
+        bar_init(sb + U::kPFull + 8 * b, U::kSoftWarps * CG);
         bar_init(sb + U::kPvDone + 8 * b, 1);
       }
       for (int s = 0; s < kScRing; ++s) {
         bar_init(sb + U::kScFull + 8 * s, 1);
-        bar_init(sb + U::kScEmpty + 8 * s, 4 * NT);
+        bar_init(sb + U::kScEmpty + 8 * s, U::kSoftWarps);
       }
       for (int s = 0; s < kRecRing; ++s) {
         bar_init(sb + U::kRecFull + 8 * s, 1);
-        bar_init(sb + U::kRecEmpty + 8 * s, kProdWarps + 1);  // producers and scales
+        bar_init(sb + U::kRecEmpty + 8 * s, 2 * kProdWarps + 1);  // a K and a V group, and scales
       }
-      for (int s = 0; s < 8; ++s) bar_init(sb + U::kRowSet + 8 * s, 1);
-      for (int s = 0; s < 2; ++s) bar_init(sb + U::kSegEnd + 8 * s, 4);
+      for (int s = 0; s < 4; ++s) bar_init(sb + U::kRowSet + 8 * s, 2);
       bar_init(sb + U::kQFull, U::kSoftWarps * CG);
       bar_init(sb + U::kDrain, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -416,62 +430,74 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   rc.pow2 = (rc.bsz & (rc.bsz - 1)) == 0, rc.shift = __ffs(rc.bsz) - 1;
 
   if (warp < U::kSoftWarps) {
-    // ================================================================ softmax: one thread per pair
-    const int wg = warp >> 2, t = NT == 2 ? wg : 0, q4 = warp & 3, r = tid & 127;  // tile, quarter, pair of the tile
+    // ================================================================ softmax: two threads per pair
+    const int wg = warp >> 2, q4 = warp & 3, r = tid & 127;  // half of the columns, quarter of the lanes, lane
     const uint32_t tl = tb + (static_cast<uint32_t>(32 * q4) << 16);  // this warp's lanes
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;
-    uint32_t jb = 0, segs = 0;
+    const uint32_t row_bar = sb + U::kRowSet + 8 * q4;
+    constexpr int HB = KB / 2;                    // this thread's columns of a block
+    constexpr int CC = F::kInt8 ? 16 : 32;        // at a time: with their scales they have to fit the registers
+    constexpr float kShift = F::kBf16 ? 0.f : kPShift;
+    uint32_t jb = 0, meet = 0;  // blocks so far; exchanges so far of the row's two threads
     bool ok = true;
-    // the barrier and phase of P V of running block n
+    // both threads of each of the warp's rows leave a value, and take the other's
+    auto exchange = [&](float mine, float& other) -> bool {
+      const uint32_t at = sb + U::kRow + 4 * ((meet & 1) * 2 * kTileM + r);
+      sts32(at + 4 * wg * kTileM, __float_as_uint(mine));
+      __syncwarp();
+      if (lane == 0) bar_arrive(row_bar);
+      const bool met = __all_sync(0xffffffffu, bar_wait(row_bar, meet & 1, flag));
+      other = __uint_as_float(lds32(at + 4 * (1 - wg) * kTileM));
+      ++meet;
+      return met;
+    };
+    // P V of sub-iteration n (block, tile)
     auto await_pv = [&](uint32_t n) -> bool {
-      const uint32_t b = NT == 2 ? t : n & 1, ph = NT == 2 ? n & 1 : (n >> 1) & 1;
-      const bool done = __all_sync(0xffffffffu, bar_wait(sb + U::kPvDone + 8 * b, ph, flag));
+      const bool done = __all_sync(0xffffffffu, bar_wait(sb + U::kPvDone + 8 * (n & 1), (n >> 1) & 1, flag));
       tmem_fence_after_sync();
       return done;
     };
     while (ok && seg.next()) {
       const int h = seg.tile / a.umma_ptiles;
-      const int64_t flat = ((static_cast<int64_t>(seg.tile - h * a.umma_ptiles) * NT + t) * CG + rank) * kTileM + r;
-      const bool in = flat < pairs;
-      const int64_t row = in ? flat / G : 0;
-      const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
-      const bool warp_in = __any_sync(0xffffffffu, in);
-      // ---- the pair's query row into the tile (bytes pools: fp16, pre-scaled by a power of two); one tile: half
-      // of the dims by each of the row's threads
-      const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD;
-      float fac = fabsf(a.softmax_scale) * kLog2e, up = sign;
-      {
-        constexpr int kQVec = (NT == 2 ? HD : HD / 2) / 8;
-        const int d0 = NT == 2 ? 0 : wg * (HD / 2);
-        uint4 qv[kQVec];
+      const int64_t flat0 = (static_cast<int64_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
+      float fac[NT];
+      bool warp_in[NT];
+      // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), half of the
+      // dims by each of a row's threads
 #pragma unroll
-        for (int i = 0; i < kQVec; ++i) qv[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + d0) + i) : make_uint4(0, 0, 0, 0);
+      for (int t = 0; t < NT; ++t) {
+        const int64_t flat = flat0 + t * CG * kTileM;
+        const bool in = flat < pairs;
+        const int64_t row = in ? flat / G : 0;
+        const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
+        warp_in[t] = __any_sync(0xffffffffu, in);
+        const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD;
+        float fc = fabsf(a.softmax_scale) * kLog2e, up = sign;
+        constexpr int kQVec = HD / 16;
+        const int d0 = wg * (HD / 2);
+        uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
+        auto take = [&](const uint4& v) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+        };
         if (F::kBytes) {
-          // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
-          uint32_t mb = 0;
-          auto take = [&](const uint4& v) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-          };
-#pragma unroll
-          for (int i = 0; i < kQVec; ++i) take(qv[i]);
-          if (NT == 1 && in) {  // the other thread's half
+          if (in) {
 #pragma unroll 8
-            for (int i = 0; i < kQVec; ++i) take(__ldg(reinterpret_cast<const uint4*>(src + HD / 2 - d0) + i));
+            for (int i = 0; i < 2 * kQVec; ++i) take(__ldg(reinterpret_cast<const uint4*>(src) + i));
           }
           const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
           int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
           e = max(-112, min(126, e));
           up = sign * pow2f(e);
-          fac *= pow2f(-e);
-          if (FMT == QKV_E4M3) fac *= a.k_scale_layer;
+          fc *= pow2f(-e);
+          if (FMT == QKV_E4M3) fc *= a.k_scale_layer;
         }
-        fac = fmaxf(fac, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
+        fac[t] = fmaxf(fc, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
         const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < kQVec; ++i) {
-          uint4 v = qv[i];
+          uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(src + d0) + i) : make_uint4(0, 0, 0, 0);
           if (F::kBytes) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             float x[8];
@@ -495,173 +521,157 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
 
-      float M = -INFINITY, R = 0.f, l = 0.f;
-      int E = F::kInt8 ? -90 : 0;
-      constexpr float kShift = F::kBf16 ? 0.f : kPShift;
-      for (int j = seg.b0; ok && j < seg.b1; ++j, ++jb) {
-        if (NT == 1 && static_cast<int>(jb & 1) != wg) continue;  // the other warps' block
-        const uint32_t b = NT == 2 ? t : jb & 1, ph = NT == 2 ? jb & 1 : (jb >> 1) & 1;
-        const uint32_t sc = sb + U::kSc + (jb & (kScRing - 1)) * U::kScStage;
-        ok = bar_wait(sb + U::kScFull + 8 * (jb & (kScRing - 1)), (jb / kScRing) & 1, flag) &&
-             bar_wait(sb + U::kSFull + 8 * b, ph, flag);
+      // state of the tile at hand; with two tiles the other one's waits in the second element
+      float M[2] = {-INFINITY, -INFINITY}, R[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+      int E[2] = {F::kInt8 ? -90 : 0, F::kInt8 ? -90 : 0};
+      auto other_tile = [&]() {
+        if (NT == 2) {
+          float x;
+          x = M[0], M[0] = M[1], M[1] = x;
+          x = R[0], R[0] = R[1], R[1] = x;
+          x = l[0], l[0] = l[1], l[1] = x;
+          x = fac[0], fac[0] = fac[NT - 1], fac[NT - 1] = x;
+          const int e = E[0];
+          E[0] = E[1], E[1] = e;
+          const bool w = warp_in[0];
+          warp_in[0] = warp_in[NT - 1], warp_in[NT - 1] = w;
+        }
+      };
+      const int subs = (seg.b1 - seg.b0) * NT;
+#pragma unroll 1
+      for (int i = 0; i < subs; ++i) {
+        const int t = NT == 2 ? i & 1 : 0;
+        const uint32_t blk = jb + i / NT, n = jb * NT + i, b = n & 1;
+        const uint32_t sc = sb + U::kSc + (blk & (kScRing - 1)) * U::kScStage;
+        if (t == 0) ok = bar_wait(sb + U::kScFull + 8 * (blk & (kScRing - 1)), (blk / kScRing) & 1, flag);
+        ok = ok && bar_wait(sb + U::kSFull + 8 * b, (n >> 1) & 1, flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tmem_fence_after_sync();
-        const uint32_t ts = tl + U::kS + KB * b;
-        const uint4 mw = lds128(sc + U::kScMask);
-        const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
-        const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0));
-        const float4* vsp = reinterpret_cast<const float4*>(smem + (sc - smem0) + U::kScVs);
-        // ---- pass 1: the row's largest logit of the block
-        float tm = -INFINITY;
-        if (warp_in) {
+        if (warp_in[0]) {
+          const uint4 mw = lds128(sc + U::kScMask);
+          const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
+          const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0)) + wg * (HB / 4);
+          const float4* vsp = ksp + U::kScVs / 16;
+          const uint32_t ts = tl + U::kS + KB * b + wg * HB;  // this thread's columns of S, and its half of P over them
+          // ---- pass 1: the columns' largest logit
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < KB / 32; ++c) {
-            float x[32];
-            float4 f[8];
-            tmem_ld32(ts + 32 * c, x);
-            if (F::kInt8) load8(f, ksp + 8 * c);  // under the tensor-memory load
-            tmem_wait_ld(x);
-            if (F::kInt8) scale32(x, f);
-            if (__builtin_expect(!whole, 0)) mask32(x, lds32(sc + U::kScMask + 4 * c));
+          for (int c = 0; c < HB; c += CC) {
+            float x[CC];
+            float4 f[CC / 4];
+            tmem_load(ts + c, x);
+            if (F::kInt8) load_scales(f, ksp + c / 4);  // under the tensor-memory load
+            tmem_loaded(x);
+            if (F::kInt8) scale_by(x, f);
+            if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB + c) >> 5)) >> ((wg * HB + c) & 31));
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
+            for (int k = 0; k < CC; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
           }
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          tm = mx == -INFINITY ? mx : mx * fac;
-        }
-        // ---- the reference after the block before (one tile: from the row's other thread)
-        float f = 1.f;  // 2^(this thread's last R - the new one)
-        if (NT == 1 && jb > 0) {
-          const uint32_t n = jb - 1;
-          ok = __all_sync(0xffffffffu, bar_wait(sb + U::kRowSet + 8 * (2 * q4 + (n & 1)), (n >> 1) & 1, flag));
-          if (!ok) break;
-          if (j > seg.b0) {
-            const uint2 st = lds64(sb + U::kRow + 8 * ((n & 1) * kTileM + r));
-            M = __uint_as_float(st.x);
-            E = static_cast<int>(st.y);
+          float tm = mx == -INFINITY ? mx : mx * fac[0], other;
+          if (!(ok = exchange(tm, other))) break;
+          tm = fmaxf(tm, other);
+          int En = E[0];
+          if (F::kInt8) {
+            const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
+            if (e > En) En = e + kEuHeadroom;
           }
-        }
-        int En = E;
-        if (F::kInt8) {
-          const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
-          if (e > E) En = e + kEuHeadroom;
-        }
-        const bool up_m = tm > M + kTau, first = M == -INFINITY;
-        const float Mn = up_m ? tm : M;
-        const float Rp = first ? 0.f : M + static_cast<float>(E) - kShift;  // the reference of O so far
-        const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
-        const bool raised = __any_sync(0xffffffffu, up_m || En != E);
-        if (l != 0.f) l *= fast_exp2(R - Rn);
-        f = first ? 1.f : fast_exp2(Rp - Rn);
-        M = Mn, E = En, R = Rn;
-        if (NT == 1) {
-          sts64(sb + U::kRow + 8 * ((jb & 1) * kTileM + r), make_uint2(__float_as_uint(M), static_cast<uint32_t>(E)));
-          __syncwarp();
-          if (lane == 0) bar_arrive(sb + U::kRowSet + 8 * (2 * q4 + (jb & 1)));
-        }
-        if (raised && warp_in && j > seg.b0) {
-          // O of the blocks before: with two tiles S was issued after the last P V
-          if (NT == 1 && !(ok = await_pv(jb - 1))) break;
-          const uint64_t f2 = f2pack(f, f);
+          const bool up_m = tm > M[0] + kTau;  // the same for the row's two threads
+          if (__any_sync(0xffffffffu, up_m || En != E[0])) {
+            // ---- raise the reference: the sums and O so far go down by f
+            const float Mn = up_m ? tm : M[0];
+            const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
+            const float f = M[0] == -INFINITY ? 1.f : fast_exp2(R[0] - Rn);
+            l[0] *= f;
+            M[0] = Mn, R[0] = Rn, E[0] = En;
+            if (i >= NT) {
+              // O of the blocks before; with two tiles S was issued after the tile's last P V
+              if (NT == 1 && !(ok = await_pv(n - 1))) break;
+              const uint64_t f2 = f2pack(f, f);
 #pragma unroll 1
-          for (int c = 0; c < HD / 32; c += 2) {
-            float o0[32], o1[32];
-            const uint32_t to = tl + U::kO + t * HD + 32 * c;
-            tmem_ld32(to, o0);
-            tmem_ld32(to + 32, o1);
-            tmem_wait_ld(o0);
-            tmem_wait_ld(o1);
+              for (int c = wg * (HD / 2); c < (wg + 1) * (HD / 2); c += 32) {  // half of the dims each
+                float o[32];
+                tmem_ld32(tl + U::kO + t * HD + c, o);
+                tmem_wait_ld(o);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) f2scale(o0 + k, f2), f2scale(o1 + k, f2);
-            tmem_st32(to, o0);
-            tmem_st32(to + 32, o1);
+                for (int k = 0; k < 32; k += 2) f2scale(o + k, f2);
+                tmem_st32(tl + U::kO + t * HD + c, o);
+              }
+            }
           }
-        }
-        // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
-        if (warp_in) {
-          const uint64_t fac2 = f2pack(fac, fac), ref2 = f2pack(-R, -R);
+          // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
+          const uint64_t fac2 = f2pack(fac[0], fac[0]), ref2 = f2pack(-R[0], -R[0]);
           uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
-          for (int c = 0; c < KB / 32; ++c) {
-            float x[32];
-            float4 f4[8];
-            tmem_ld32(ts + 32 * c, x);
-            if (F::kInt8) load8(f4, ksp + 8 * c);
-            tmem_wait_ld(x);
+          for (int c = 0; c < HB; c += CC) {
+            float x[CC];
+            float4 f4[CC / 4];
+            tmem_load(ts + c, x);
+            if (F::kInt8) load_scales(f4, ksp + c / 4);
+            tmem_loaded(x);
             if (F::kInt8) {
-              scale32(x, f4);
-              load8(f4, vsp + 8 * c);
+              scale_by(x, f4);
+              load_scales(f4, vsp + c / 4);
             }
-            if (__builtin_expect(!whole, 0)) mask32(x, lds32(sc + U::kScMask + 4 * c));
-            uint32_t p[16];
+            if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB + c) >> 5)) >> ((wg * HB + c) & 31));
+            uint32_t p[CC / 2];
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
+            for (int k = 0; k < CC; k += 2) {
               float y0, y1;
               f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, ref2), y0, y1);
               x[k] = fast_exp2(y0);
               x[k + 1] = fast_exp2(y1);
               sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
             }
-            if (F::kInt8) scale32(x, f4);  // a masked key's scale is 0
+            if (F::kInt8) scale_by(x, f4);  // a masked key's scale is 0
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
-            tmem_st_x16(ts + 16 * c, p);
+            for (int k = 0; k < CC; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
+            tmem_store(ts + c / 2, p);
           }
           float s0, s1;
           f2unpack(f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3])), s0, s1);
-          l += s0 + s1;
+          l[0] += s0 + s1;
           tmem_wait_st();
         }
         tmem_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           lead_arrive<CG>(sb + U::kPFull + 8 * b);
-          bar_arrive(sb + U::kScEmpty + 8 * (jb & (kScRing - 1)));
+          if (t == NT - 1) bar_arrive(sb + U::kScEmpty + 8 * (blk & (kScRing - 1)));
         }
+        other_tile();
       }
+      jb += seg.b1 - seg.b0;
       if (!ok) break;
-      // ---- the segment's partial result
-      const bool mine = NT == 2 || static_cast<int>((jb - 1) & 1) == wg;  // the last block was this thread's
-      auto await_other = [&]() -> bool {
-        return __all_sync(0xffffffffu, bar_wait(sb + U::kSegEnd + 8 * (1 - wg), segs & 1, flag));
-      };
-      // one tile: the warps of the last block go first, the others answer (so neither can be a segment ahead)
-      ok = mine ? await_pv(jb - 1) : await_other();
-      if (!ok) break;
-      if (NT == 1) {
-        // both threads of a row: the sums at the last block's reference
-        sts64(sb + U::kSum + 8 * (wg * kTileM + r), make_uint2(__float_as_uint(l), __float_as_uint(R)));
-        __syncwarp();
-        if (lane == 0) bar_arrive(sb + U::kSegEnd + 8 * wg);
-        if (mine && !(ok = await_other())) break;
-        tmem_fence_after_sync();
-        const uint2 ot = lds64(sb + U::kSum + 8 * ((1 - wg) * kTileM + r));
-        const float lo = __uint_as_float(ot.x), Ro = __uint_as_float(ot.y);
-        const float Rf = mine ? R : Ro;
-        l = (l == 0.f ? 0.f : l * fast_exp2(R - Rf)) + (lo == 0.f ? 0.f : lo * fast_exp2(Ro - Rf));
-        R = Rf;
-      }
-      ++segs;
-      if (warp_in) {
-        const bool any = l != 0.f;  // NaN too
-        const float inv = any ? 1.f / l : 0.f;
-        const int64_t at = (static_cast<int64_t>(seg.part) * a.rows + row) * a.num_q_heads + head;
-        if (in && (NT == 2 || wg == 0)) a.lse_part[at] = any ? (R + log2f(l)) * kLn2 : -INFINITY;
-        float* dst = a.o_part + at * HD;
-        constexpr int kCols = NT == 2 ? HD / 32 : HD / 64;  // one tile: half of the dims by each of the row's threads
+      // ---- the segment's partial results
 #pragma unroll 1
-        for (int c = NT == 2 ? 0 : wg * kCols; c < (NT == 2 ? kCols : (wg + 1) * kCols); ++c) {
+      for (int t = 0; t < NT; ++t, other_tile()) {
+        if (!(ok = await_pv((jb - 1) * NT + t))) break;
+        if (!warp_in[0]) continue;
+        float other;
+        if (!(ok = exchange(l[0], other))) break;
+        const int64_t flat = flat0 + t * CG * kTileM;
+        const bool in = flat < pairs;
+        const int64_t row = in ? flat / G : 0;
+        const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
+        const float sum = wg == 0 ? l[0] + other : other + l[0];  // the same order in both threads
+        const bool any = sum != 0.f;  // NaN too
+        const float inv = any ? 1.f / sum : 0.f;
+        const int64_t at = (static_cast<int64_t>(seg.part) * a.rows + row) * a.num_q_heads + head;
+        if (in && wg == 0) a.lse_part[at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
+        float* dst = a.o_part + at * HD;
+#pragma unroll 1
+        for (int c = wg * (HD / 2); c < (wg + 1) * (HD / 2); c += 32) {
           float o[32];
-          tmem_ld32(tl + U::kO + t * HD + 32 * c, o);
+          tmem_ld32(tl + U::kO + t * HD + c, o);
           tmem_wait_ld(o);
           if (in && any) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
               // int8: the producers store dims 0, 2, 1, 3 of each four
               const float x1 = F::kInt8 ? o[k + 2] : o[k + 1], x2 = F::kInt8 ? o[k + 1] : o[k + 2];
-              *reinterpret_cast<float4*>(dst + 32 * c + k) = make_float4(o[k] * inv, x1 * inv, x2 * inv, o[k + 3] * inv);
+              *reinterpret_cast<float4*>(dst + c + k) = make_float4(o[k] * inv, x1 * inv, x2 * inv, o[k + 3] * inv);
             }
           }
         }
@@ -672,7 +682,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     // ================================================================ producers
     using KOp = Operand<FMT, HD, U::kKRows, HD>;
     using VOp = Operand<FMT, HD, KB, U::kVDims>;
-    const int pw = warp & 3;
+    const int pg = (warp - U::kSoftWarps) >> 2, pw = warp & 3;  // group, warp of the group
     const int voff = rank * VOp::kBytes;  // this SM's dims
     const uint32_t krow = 4 * (rank * U::kKRows + KOp::kWarpRows * pw), vrow = 4 * VOp::kWarpRows * pw;  // of a ring entry
     uint32_t base = 0, jb = 0;            // slots and blocks of earlier segments
@@ -686,76 +696,66 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kFull + 8 * (s % NS));
     };
-    // the records of running block n; given back once its V has been loaded (K is loaded before)
-    auto records = [&](uint32_t n) -> uint32_t { return sb + U::kRec + (n % kRecRing) * 4 * KB; };
-    auto await_records = [&](uint32_t n) -> bool {
-      return __all_sync(0xffffffffu, bar_wait(sb + U::kRecFull + 8 * (n % kRecRing), (n / kRecRing) & 1, flag));
-    };
-    auto free_records = [&](uint32_t n) {
-      __syncwarp();
-      if (lane == 0) bar_arrive(sb + U::kRecEmpty + 8 * (n % kRecRing));
-    };
     while (ok && seg.next()) {
       const int B = seg.b1 - seg.b0;
-      if (!(ok = await_records(jb))) break;
+      // what the segment's slot e holds
+      auto is_v = [&](int e) -> bool { return e == 2 * B - 1 || (e > 0 && !(e & 1)); };
+      auto block_of = [&](int e) -> int { return is_v(e) ? (e == 2 * B - 1 ? B - 1 : e / 2 - 1) : (e + 1) / 2; };
+      // the records of slot e's block, awaited; each group takes a block's once for K and once for V
+      uint32_t rec = 0;
+      auto await_records = [&](int e) -> bool {
+        const uint32_t n = jb + block_of(e);
+        rec = sb + U::kRec + (n % kRecRing) * 4 * KB;
+        return __all_sync(0xffffffffu, bar_wait(sb + U::kRecFull + 8 * (n % kRecRing), (n / kRecRing) & 1, flag));
+      };
+      auto free_records = [&](int e) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(sb + U::kRecEmpty + 8 * ((jb + block_of(e)) % kRecRing));
+      };
       if (F::kBytes) {
-        // staging runs kStaged - 1 slots ahead of the conversion; slot e is K of block (e + 1) / 2 or V
-        auto is_v = [&](int e) -> bool { return e == 2 * B - 1 || (e > 0 && !(e & 1)); };
-        auto stage = [&](int e) {
-          if (e < 2 * B) {
-            const uint32_t st = sb + U::kStage + ((base + e) % U::kStaged) * U::kStageBytes;
-            if (is_v(e)) {
-              const uint32_t n = jb + (e == 2 * B - 1 ? B - 1 : e / 2 - 1);
-              VOp::stage(st, a.v_cache, pw, lane, records(n) + vrow, voff);
-              free_records(n);
-            } else {
-              const uint32_t n = jb + (e + 1) / 2;
-              if (e > 0 && !(ok = await_records(n))) return;
-              KOp::stage(st, a.k_cache, pw, lane, records(n) + krow, 0);
-            }
+        const uint32_t stage0 = sb + U::kStage + pg * U::kStageBytes;
+        const uint32_t kd = stage0 + pw * KOp::kInstr * 512 + lane * 16, vd = stage0 + pw * VOp::kInstr * 512 + lane * 16;
+        const uint8_t* kp = a.k_cache + 16 * (lane % KOp::kLpr);
+        const uint8_t* vp = a.v_cache + voff + 16 * (lane % VOp::kLpr);
+        auto stage = [&](int e) -> bool {
+          if (e >= 2 * B) return true;
+          if (!await_records(e)) return false;
+          if (is_v(e)) {
+            rec += vrow + 4 * (lane / VOp::kLpr);
+#pragma unroll 4
+            for (int u = 0; u < VOp::kInstr; ++u) VOp::stage1(vd, vp, u, rec);
+          } else {
+            rec += krow + 4 * (lane / KOp::kLpr);
+#pragma unroll 4
+            for (int u = 0; u < KOp::kInstr; ++u) KOp::stage1(kd, kp, u, rec);
           }
-          cp_async_commit();
+          free_records(e);
+          return true;
         };
-        for (int e = 0; ok && e < U::kStaged - 1; ++e) stage(e);
-        for (int e = 0; ok && e < 2 * B; ++e) {
-          stage(e + U::kStaged - 1);
-          if (!ok) break;
+        ok = stage(pg);
+        cp_async_commit();
+        for (int e = pg; ok && e < 2 * B; e += 2) {
           const uint32_t n = base + e, slot = sb + U::kRing + (n % NS) * U::kSlotBytes;
-          const uint32_t st = sb + U::kStage + (n % U::kStaged) * U::kStageBytes;
           if (!(ok = await(n))) break;
-          cp_async_wait<U::kStaged - 1>();
-          if (is_v(e)) VOp::convert(slot, st, pw, lane);
-          else KOp::convert(slot, st, pw, lane);
+          cp_async_wait<0>();
+          if (is_v(e)) VOp::convert(slot, vd, pw, lane);
+          else KOp::convert(slot, kd, pw, lane);
           hand_over(n);
+          ok = stage(e + 2);
+          cp_async_commit();
         }
         cp_async_wait<0>();
       } else {
-        // a slot is handed over once the copies of the next one have been issued
-        uint32_t last = 0;
-        bool pending = false;
-        for (int j = 0; ok && j <= B; ++j) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            if (v == 0 ? j >= B : j == 0) continue;
-            const uint32_t s = base + (v ? v_slot(j - 1, B) : k_slot(j)), slot = sb + U::kRing + (s % NS) * U::kSlotBytes;
-            if (!(ok = await(s))) break;
-            if (v == 0) {
-              if (j > 0 && !(ok = await_records(jb + j))) break;
-              KOp::copy(slot, a.k_cache, pw, lane, records(jb + j) + krow, 0);
-            } else {
-              VOp::copy(slot, a.v_cache, pw, lane, records(jb + j - 1) + vrow, voff);
-              free_records(jb + j - 1);
-            }
-            cp_async_commit();
-            if (pending) {
-              cp_async_wait<1>();
-              hand_over(last);
-            }
-            last = s, pending = true;
-          }
+        for (int e = pg; ok && e < 2 * B; e += 2) {
+          const uint32_t n = base + e, slot = sb + U::kRing + (n % NS) * U::kSlotBytes;
+          if (!(ok = await_records(e)) || !(ok = await(n))) break;
+          if (is_v(e)) VOp::copy(slot, a.v_cache, pw, lane, rec + vrow, voff);
+          else KOp::copy(slot, a.k_cache, pw, lane, rec + krow, 0);
+          free_records(e);
+          cp_async_commit();
+          cp_async_wait<0>();
+          hand_over(n);
         }
-        cp_async_wait<0>();
-        if (ok && pending) hand_over(last);
       }
       base += 2 * B;
       jb += B;
@@ -870,11 +870,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       uint32_t p = tb + U::kS + KB * b;
       uint64_t vd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, KB * 128, 1024);
 #pragma unroll 1
-      for (int i = 0; i < KB / 64; ++i) {  // 64 keys
+      for (int i = 0; i < 2; ++i) {  // half of the keys: their P lies over their S
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_ts<CG>(d, p + 8 * ks, vd + 128 * ks, U::kIdO, !first || i > 0 || ks > 0 ? 1u : 0u);
-        p += 32;
-        vd += 512;
+        for (int ks = 0; ks < KB / 32; ++ks) mma_ts<CG>(d, p + 8 * ks, vd + 128 * ks, U::kIdO, !first || i > 0 || ks > 0 ? 1u : 0u);
+        p += KB / 2;
+        vd += 128 * (KB / 32);
       }
       if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
       commit_to<CG>(sb + U::kPvDone + 8 * b);
@@ -891,8 +891,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         for (int i = 0; ok && i < 2; ++i) {
           const int t = NT == 2 ? i : 0;
           if (j >= 0 && (NT == 2 || i == 1))
-            pv(t, NT == 2 ? t : n & 1, NT == 2 ? n & 1 : (n >> 1) & 1, base + v_slot(j, B), j == 0);
-          if (ok && j + 1 < B && (NT == 2 || i == 0)) qk(t, NT == 2 ? t : (n + 1) & 1, base + k_slot(j + 1));
+            pv(t, (n * NT + t) & 1, ((n * NT + t) >> 1) & 1, base + v_slot(j, B), j == 0);
+          if (ok && j + 1 < B && (NT == 2 || i == 0)) qk(t, ((n + 1) * NT + t) & 1, base + k_slot(j + 1));
         }
       }
       jb += B;
