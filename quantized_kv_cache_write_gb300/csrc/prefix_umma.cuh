@@ -11,22 +11,25 @@
 // and V (by dims): each converts half of the pool's values, and shared memory is read and written half as
 // often per MMA as with one SM.
 //
-// Warps: eight for the softmax (two threads per pair, half of a block's columns each), two groups of four
+// Warps: sixteen for the softmax (four threads per pair, a quarter of a block's columns each), two groups of four
 // producers, one for the records, one for the scales, one MMA issuer (of the team's first SM). Slots
 // (rows of 128 B, 128 B swizzle) pass from the producers to the MMA warp in the order
 // K_0 K_1 V_0 K_2 V_1 ..., one group every second one; K is K-major, V MN-major, and both are stored alike, one
 // 128 B row per key and 64 dims.
 //   records: block list -> record numbers of a block's keys, into a ring, eight blocks ahead.
-//   producers: 16 B copies (cp.async) into the group's staging slot, then, by the lane that copied them,
-//     converted to fp16 (codes are exact) and stored to the slot once it is free; each 16 B read makes room for
-//     the copy of the group's next slot. 16-bit pools are copied straight into the slot.
+//   producers: 16 B loads into registers, converted to fp16 (codes are exact) and stored to the slot once it is
+//     free; then the registers take the group's next slot. 16-bit pools are copied straight into the slot
+//     (cp.async).
 //   scales: K and V scales, the mask of the block's keys and the largest V scale into a small ring.
 //   MMA: one thread. P is the A operand in tensor memory, in the columns of the S it was made from.
 //   softmax: y = S ks fac (log2 units). Reference R = M + E - 7: M follows the row's maximum lazily
 //     (raised when a logit passes it by 2^8), E is a power-of-two bound on the V scales, so p vs 2^-R
-//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. A first pass over
-//     the thread's columns finds their maximum, the row's two threads exchange it, a second takes p; each
-//     thread's half of P goes over its own half of S.
+//     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. The thread's columns
+//     stay in registers from the one load of S on: their maximum is exchanged between the row's four threads,
+//     then p replaces them, and each thread's part of P goes over its own part of S. A raise rescales O after P
+//     is stored, when those registers are free (measured, 64 rows x 64 heads behind 32768 e4m3 keys: 131 us for
+//     the call with two threads per pair and the columns read twice, 163 us with O rescaled before P, 130 us
+//     like this; 256 rows x 16 heads behind 65536 int8 keys 269, 269 and 264 us).
 // Arithmetic as in prefix_attn.cuh: exact codes, logits and sums in fp32, p rounded once.
 //
 // The roles' loops are kept rolled: five of them run at once on each scheduler, and fully unrolled they
@@ -44,6 +47,7 @@ namespace prefix {
 
 constexpr int kTileM = 128;  // pairs of a tile on one SM
 constexpr int kProdWarps = 4;  // of a group; two groups
+constexpr int kParts = 4;      // threads of a pair: each takes a part of a block's columns
 constexpr uint64_t kWaitNs = 2000000000;  // after which a wait is declared lost
 constexpr int kScRing = 4, kRecRing = 8;
 // keys of a block: 128; 64 where one SM holds 256-wide heads alone
@@ -53,20 +57,18 @@ template <int FMT, int HD, int NT, int CG>
 struct Umma {
   using F = Fmt<FMT>;
   static constexpr int KB = umma_block_keys(HD, CG);
-  static constexpr int kSoftWarps = 8, kRecWarp = kSoftWarps + 2 * kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
+  static constexpr int kSoftWarps = 4 * kParts, kRecWarp = kSoftWarps + 2 * kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kKRows = KB / CG, kVDims = HD / CG;  // this SM's part of a block
   static constexpr uint32_t kSlotBytes = uint32_t(KB) * HD * 2 / CG;
   static constexpr uint32_t kQTile = kTileM * HD * 2;
-  // bytes pools: one staging slot per producer group beside the converted ones
-  static constexpr uint32_t kStageBytes = F::kBytes ? kSlotBytes / 2 : 0;
-  static constexpr int kSlots = kSlotBytes == 16384 ? (F::kBytes ? 7 : 8) : NT * HD >= 256 ? (F::kBytes ? 3 : 4) : 4;
-  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kStage = kRing + kSlots * kSlotBytes, kSc = kStage + 2 * kStageBytes;
+  static constexpr int kSlots = kSlotBytes == 16384 ? 8 : NT * HD >= 256 ? 4 : 5;
+  static constexpr uint32_t kQ = 0, kRing = NT * kQTile, kSc = kRing + kSlots * kSlotBytes;
   // per block: K scales, V scales, key mask (4 words), largest V scale
   static constexpr uint32_t kScVs = 4 * KB, kScMask = 8 * KB, kScVmax = kScMask + 16, kScStage = kScVmax + 16;
   static constexpr uint32_t kRec = kSc + kScRing * kScStage;       // record numbers of a block's keys
-  static constexpr uint32_t kRow = kRec + kRecRing * 4 * KB;       // per row: its two threads' maxima (sums), two phases
-  static constexpr uint32_t kBar = kRow + 2 * 2 * 4 * kTileM;
+  static constexpr uint32_t kRow = kRec + kRecRing * 4 * KB;       // per row: its threads' maxima (sums), two phases
+  static constexpr uint32_t kBar = kRow + 2 * kParts * 4 * kTileM;
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
                             kRecFull = kScEmpty + 8 * kScRing, kRecEmpty = kRecFull + 8 * kRecRing,
@@ -89,32 +91,30 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
   return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
+// The MMAs' issuing warp runs its loop with all lanes, so that descriptors stay in uniform registers; one
+// elected lane (`lead`) issues. acc: add to D, else overwrite it.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+#define QKV_PREFIX_MMA(GROUP, A, AC)                                                                                    \
+  asm volatile(                                                                                                         \
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"                                         \
+      " @q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], " A ", %2, %3, p;\n}\n" ::"r"(d), AC(a), "l"(b), "r"(id),   \
+      "r"(acc), "r"(lead)                                                                                               \
+      : "memory")
 template <int CG>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  if (CG == 2)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  if (CG == 2) QKV_PREFIX_MMA("2", "%1", "l");
+  else QKV_PREFIX_MMA("1", "%1", "l");
 }
 template <int CG>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  if (CG == 2)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  if (CG == 2) QKV_PREFIX_MMA("2", "[%1]", "r");
+  else QKV_PREFIX_MMA("1", "[%1]", "r");
 }
+#undef QKV_PREFIX_MMA
 // Arrive on this barrier (of both SMs of a pair) when the MMAs issued so far are done.
 template <int CG>
 __device__ __forceinline__ void commit_to(uint32_t mbar) {
@@ -212,21 +212,14 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-// N columns' scales; N columns times them; N columns whose key is missing to -inf.
+// N columns times their scales; N columns whose key is missing to -inf.
 template <int N>
-__device__ __forceinline__ void load_scales(float4 (&f)[N], const float4* src) {
+__device__ __forceinline__ void scale_by(float (&v)[N], const float4* src) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) f[k] = src[k];
-}
-template <int N, int M>
-__device__ __forceinline__ void scale_by(float (&v)[N], const float4 (&f)[M]) {
-#pragma unroll
-  for (int k = 0; k < M; ++k) {
-    f2scale(v + 4 * k, f2pack(f[k].x, f[k].y));
-    f2scale(v + 4 * k + 2, f2pack(f[k].z, f[k].w));
+  for (int k = 0; k < N / 4; ++k) {
+    const float4 f = src[k];
+    f2scale(v + 4 * k, f2pack(f.x, f.y));
+    f2scale(v + 4 * k + 2, f2pack(f.z, f.w));
   }
 }
 template <int N>
@@ -318,48 +311,6 @@ struct Operand {
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : F::kBytes ? HD : 2 * HD;
   static_assert(kLpr <= 32 && kWarpRows <= 32 && kInstr >= 1, "rows of at most 512 B");
 
-  // Bytes pools. This lane's 16 B of instruction u into the staging slot (a missing key: zeros); `rec`: the ring's
-  // entry of the lane's first row, p0: its bytes of record 0, d0: its place in the staging slot.
-  static __device__ __forceinline__ void stage1(uint32_t d0, const uint8_t* p0, int u, uint32_t rec) {
-    const int rk = static_cast<int>(lds32(rec + 4 * kPerInstr * u));
-    const uint8_t* p = p0 + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow;
-    if (F::kInline) {  // records sit on 4 B boundaries
-#pragma unroll
-      for (int w = 0; w < 4; ++w) cp_async4(d0 + u * 512 + 4 * w, p + 4 * w, rk >= 0 ? 4 : 0);
-    } else {
-      cp_async16(d0 + u * 512, p, rk >= 0 ? 16 : 0);
-    }
-  }
-  // The staged codes to fp16 and into the slot, two 16 B chunks of the key's 128 B row per instruction.
-  static __device__ __forceinline__ void convert(uint32_t slot, uint32_t d0, int pw, int lane) {
-    const int ch = lane % kLpr;
-    // row = kWarpRows pw + kPerInstr u + lane / kLpr; the warp's first row is a multiple of 8
-    const uint32_t c0 = 2 * (ch & 3);
-    const uint32_t odd = kLpr > 4 && (ch & 4) ? 1 : 0;  // the eight lanes of a store phase fill eight distinct chunks
-    const uint32_t at = slot + (ch >> 2) * kCol + (kWarpRows * pw + lane / kLpr) * 128;
-    const uint32_t first = ((c0 + odd) ^ (lane / kLpr)) << 4;
-#pragma unroll 2
-    for (int u = 0; u < kInstr; ++u) {
-      const uint4 v = lds128(d0 + u * 512);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (F::kInt8) {
-          o[2 * k] = i8pair_to_f16x2(w[k]);
-          o[2 * k + 1] = i8pair_to_f16x2(w[k] >> 8);
-        } else {
-          o[2 * k] = e4m3pair_to_f16x2(w[k]);
-          o[2 * k + 1] = e4m3pair_to_f16x2(w[k] >> 16);
-        }
-      }
-      const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-      const uint32_t x = (kPerInstr * u) & 7;  // the rest of row & 7
-      const uint32_t a0 = at + kPerInstr * u * 128 + (first ^ (x << 4));
-      sts128(a0, odd ? hi : lo);
-      sts128(a0 ^ 16, odd ? lo : hi);
-    }
-  }
   // 16-bit pools: the whole part by cp.async; missing keys are zero-filled
   static __device__ __forceinline__ void copy(uint32_t slot, const uint8_t* cache, int pw, int lane, uint32_t rec, int off) {
     const int ch = lane % kLpr;
@@ -373,6 +324,76 @@ struct Operand {
     }
   }
 };
+
+// Bytes pools: a slot's rows of one operand as a lane sees them. K's and V's parts differ only in these
+// numbers, so one copy of the code serves both.
+struct Rows {
+  const uint8_t* src;  // the lane's 16 B of record 0
+  uint32_t rec;        // the ring entry's offset of the lane's first row
+  uint32_t at, first;  // the lane's place in a slot: column and row, and its first chunk (16 B)
+  uint32_t odd;        // whether that is the odd chunk of the pair: the eight lanes of a store phase fill eight
+  int per;             // keys per instruction
+};
+template <typename OP>
+__device__ __forceinline__ Rows rows_of(const uint8_t* src, int pw, int lane, int first_row) {
+  constexpr int L = OP::kLpr;
+  const int ch = lane % L;  // the lane's 16 dims: two chunks of the key's 128 B row
+  Rows r;
+  r.src = src + 16 * ch;
+  r.rec = 4 * (first_row + OP::kWarpRows * pw + lane / L);
+  r.odd = L > 4 && (ch & 4) ? 1 : 0;
+  r.at = (ch >> 2) * OP::kCol + (OP::kWarpRows * pw + lane / L) * 128;  // the warp's first row is a multiple of 8
+  r.first = ((2 * (ch & 3) + r.odd) ^ (lane / L)) << 4;
+  r.per = OP::kPerInstr;
+  return r;
+}
+// N instructions' 16 B (a missing key's: zeros) into registers.
+template <int FMT, int HD, int N>
+__device__ __forceinline__ void load_rows(uint4 (&raw)[N], const Rows& r, uint32_t ring) {
+  using F = Fmt<FMT>;
+  constexpr int kGlobalRow = F::kInline ? HD + 4 : HD;
+  int rk[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) rk[u] = static_cast<int>(lds32(ring + r.rec + 4 * r.per * u));
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    raw[u] = make_uint4(0, 0, 0, 0);
+    if (rk[u] >= 0) {
+      const uint8_t* p = r.src + static_cast<uint64_t>(static_cast<uint32_t>(rk[u])) * kGlobalRow;
+      if (F::kInline) {  // records sit on 4 B boundaries
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+        raw[u] = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+      } else {
+        raw[u] = __ldg(reinterpret_cast<const uint4*>(p));
+      }
+    }
+  }
+}
+// The codes to fp16 and into the slot.
+template <int FMT, int N>
+__device__ __forceinline__ void convert_rows(uint32_t slot, const Rows& r, const uint4 (&raw)[N]) {
+  using F = Fmt<FMT>;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (F::kInt8) {
+        o[2 * k] = i8pair_to_f16x2(w[k]);
+        o[2 * k + 1] = i8pair_to_f16x2(w[k] >> 8);
+      } else {
+        o[2 * k] = e4m3pair_to_f16x2(w[k]);
+        o[2 * k + 1] = e4m3pair_to_f16x2(w[k] >> 16);
+      }
+    }
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    const uint32_t row = r.per * u;  // row & 7: these bits and the lane's, which are disjoint
+    const uint32_t a0 = slot + r.at + row * 128 + (r.first ^ ((row & 7) << 4));
+    sts128(a0, r.odd ? hi : lo);
+    sts128(a0 ^ 16, r.odd ? lo : hi);
+  }
+}
 
 // Slots of a segment of B blocks in ring order: K_0 K_1 V_0 K_2 V_1 ... K_B-1 V_B-2 V_B-1.
 __device__ __forceinline__ uint32_t k_slot(int j) { return j == 0 ? 0 : 2 * j - 1; }
@@ -411,7 +432,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         bar_init(sb + U::kRecFull + 8 * s, 1);
         bar_init(sb + U::kRecEmpty + 8 * s, 2 * kProdWarps + 1);  // a K and a V group, and scales
       }
-      for (int s = 0; s < 4; ++s) bar_init(sb + U::kRowSet + 8 * s, 2);
+      for (int s = 0; s < 4; ++s) bar_init(sb + U::kRowSet + 8 * s, kParts);
       bar_init(sb + U::kQFull, U::kSoftWarps * CG);
       bar_init(sb + U::kDrain, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -430,24 +451,24 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   rc.pow2 = (rc.bsz & (rc.bsz - 1)) == 0, rc.shift = __ffs(rc.bsz) - 1;
 
   if (warp < U::kSoftWarps) {
-    // ================================================================ softmax: two threads per pair
-    const int wg = warp >> 2, q4 = warp & 3, r = tid & 127;  // half of the columns, quarter of the lanes, lane
+    // ================================================================ softmax: kParts threads per pair
+    const int wg = warp >> 2, q4 = warp & 3, r = tid & 127;  // part of the columns, quarter of the lanes, lane
     const uint32_t tl = tb + (static_cast<uint32_t>(32 * q4) << 16);  // this warp's lanes
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;
     const uint32_t row_bar = sb + U::kRowSet + 8 * q4;
-    constexpr int HB = KB / 2;                    // this thread's columns of a block
-    constexpr int CC = F::kInt8 ? 16 : 32;        // at a time: with their scales they have to fit the registers
+    constexpr int HB = KB / kParts;  // this thread's columns of a block
     constexpr float kShift = F::kBf16 ? 0.f : kPShift;
-    uint32_t jb = 0, meet = 0;  // blocks so far; exchanges so far of the row's two threads
+    uint32_t jb = 0, meet = 0;  // blocks so far; exchanges so far of the row's threads
     bool ok = true;
-    // both threads of each of the warp's rows leave a value, and take the other's
-    auto exchange = [&](float mine, float& other) -> bool {
-      const uint32_t at = sb + U::kRow + 4 * ((meet & 1) * 2 * kTileM + r);
+    // the threads of each of the warp's rows leave a value, and take all of them in the same order
+    auto exchange = [&](float mine, float (&all)[kParts]) -> bool {
+      const uint32_t at = sb + U::kRow + 4 * ((meet & 1) * kParts * kTileM + r);
       sts32(at + 4 * wg * kTileM, __float_as_uint(mine));
       __syncwarp();
       if (lane == 0) bar_arrive(row_bar);
       const bool met = __all_sync(0xffffffffu, bar_wait(row_bar, meet & 1, flag));
-      other = __uint_as_float(lds32(at + 4 * (1 - wg) * kTileM));
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) all[i] = __uint_as_float(lds32(at + 4 * i * kTileM));
       ++meet;
       return met;
     };
@@ -462,7 +483,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       const int64_t flat0 = (static_cast<int64_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
       float fac[NT];
       bool warp_in[NT];
-      // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), half of the
+      // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), a part of the
       // dims by each of a row's threads
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -471,21 +492,25 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         const int64_t row = in ? flat / G : 0;
         const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
         warp_in[t] = __any_sync(0xffffffffu, in);
-        const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD;
+        const int d0 = wg * (HD / kParts);
+        const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD + d0;
         float fc = fabsf(a.softmax_scale) * kLog2e, up = sign;
-        constexpr int kQVec = HD / 16;
-        const int d0 = wg * (HD / 2);
-        uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
-        auto take = [&](const uint4& v) {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-        };
+        constexpr int kQVec = HD / kParts / 8;
         if (F::kBytes) {
+          uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
           if (in) {
-#pragma unroll 8
-            for (int i = 0; i < 2 * kQVec; ++i) take(__ldg(reinterpret_cast<const uint4*>(src) + i));
+#pragma unroll
+            for (int i = 0; i < kQVec; ++i) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+            }
           }
+          float all[kParts];
+          if (!(ok = exchange(__uint_as_float(mb), all))) break;
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) mb = max(mb, __float_as_uint(all[i]));
           const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
           int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
           e = max(-112, min(126, e));
@@ -495,9 +520,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         }
         fac[t] = fmaxf(fc, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
         const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
-#pragma unroll 8
+#pragma unroll
         for (int i = 0; i < kQVec; ++i) {
-          uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(src + d0) + i) : make_uint4(0, 0, 0, 0);
+          uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
           if (F::kBytes) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             float x[8];
@@ -517,6 +542,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           sts128(qrow + (d >> 6) * (kTileM * 128) + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
         }
       }
+      if (!ok) break;
       proxy_fence();
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
@@ -554,84 +580,70 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0)) + wg * (HB / 4);
           const float4* vsp = ksp + U::kScVs / 16;
           const uint32_t ts = tl + U::kS + KB * b + wg * HB;  // this thread's columns of S, and its half of P over them
-          // ---- pass 1: the columns' largest logit
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < HB; c += CC) {
-            float x[CC];
-            float4 f[CC / 4];
-            tmem_load(ts + c, x);
-            if (F::kInt8) load_scales(f, ksp + c / 4);  // under the tensor-memory load
-            tmem_loaded(x);
-            if (F::kInt8) scale_by(x, f);
-            if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB + c) >> 5)) >> ((wg * HB + c) & 31));
+          // ---- the columns' logits (before fac) and their largest
+          float x[HB];
+          tmem_load(ts, x);
+          tmem_loaded(x);
+          if (F::kInt8) scale_by(x, ksp);
+          if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB) >> 5)) >> ((wg * HB) & 31));
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, all[kParts];
 #pragma unroll
-            for (int k = 0; k < CC; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
-          }
+          for (int k = 0; k < HB; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          float tm = mx == -INFINITY ? mx : mx * fac[0], other;
-          if (!(ok = exchange(tm, other))) break;
-          tm = fmaxf(tm, other);
+          float tm = mx == -INFINITY ? mx : mx * fac[0];
+          if (!(ok = exchange(tm, all))) break;
+          tm = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
           int En = E[0];
           if (F::kInt8) {
             const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
             if (e > En) En = e + kEuHeadroom;
           }
-          const bool up_m = tm > M[0] + kTau;  // the same for the row's two threads
-          if (__any_sync(0xffffffffu, up_m || En != E[0])) {
+          const bool up_m = tm > M[0] + kTau;  // the same for the row's threads
+          const bool raise = __any_sync(0xffffffffu, up_m || En != E[0]);
+          float f = 1.f;
+          if (raise) {
             // ---- raise the reference: the sums and O so far go down by f
             const float Mn = up_m ? tm : M[0];
             const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
-            const float f = M[0] == -INFINITY ? 1.f : fast_exp2(R[0] - Rn);
+            if (M[0] != -INFINITY) f = fast_exp2(R[0] - Rn);
             l[0] *= f;
             M[0] = Mn, R[0] = Rn, E[0] = En;
-            if (i >= NT) {
-              // O of the blocks before; with two tiles S was issued after the tile's last P V
-              if (NT == 1 && !(ok = await_pv(n - 1))) break;
-              const uint64_t f2 = f2pack(f, f);
-#pragma unroll 1
-              for (int c = wg * (HD / 2); c < (wg + 1) * (HD / 2); c += 32) {  // half of the dims each
-                float o[32];
-                tmem_ld32(tl + U::kO + t * HD + c, o);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) f2scale(o + k, f2);
-                tmem_st32(tl + U::kO + t * HD + c, o);
-              }
-            }
           }
-          // ---- pass 2: p = 2^(y - R), its sum, and (times the V scale) the operand
+          // ---- p = 2^(y - R), its sum, and (times the V scale) the operand
           const uint64_t fac2 = f2pack(fac[0], fac[0]), ref2 = f2pack(-R[0], -R[0]);
           uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll 1
-          for (int c = 0; c < HB; c += CC) {
-            float x[CC];
-            float4 f4[CC / 4];
-            tmem_load(ts + c, x);
-            if (F::kInt8) load_scales(f4, ksp + c / 4);
-            tmem_loaded(x);
-            if (F::kInt8) {
-              scale_by(x, f4);
-              load_scales(f4, vsp + c / 4);
-            }
-            if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB + c) >> 5)) >> ((wg * HB + c) & 31));
-            uint32_t p[CC / 2];
 #pragma unroll
-            for (int k = 0; k < CC; k += 2) {
-              float y0, y1;
-              f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, ref2), y0, y1);
-              x[k] = fast_exp2(y0);
-              x[k + 1] = fast_exp2(y1);
-              sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
-            }
-            if (F::kInt8) scale_by(x, f4);  // a masked key's scale is 0
-#pragma unroll
-            for (int k = 0; k < CC; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
-            tmem_store(ts + c / 2, p);
+          for (int k = 0; k < HB; k += 2) {
+            float y0, y1;
+            f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, ref2), y0, y1);
+            x[k] = fast_exp2(y0);
+            x[k + 1] = fast_exp2(y1);
+            sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
           }
+          if (F::kInt8) scale_by(x, vsp);  // a masked key's scale is 0
+          uint32_t p[HB / 2];
+#pragma unroll
+          for (int k = 0; k < HB; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
+          tmem_store(ts, p);
           float s0, s1;
           f2unpack(f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3])), s0, s1);
           l[0] += s0 + s1;
+          if (raise && i >= NT) {
+            // O of the blocks before, once their P V is done (with two tiles S was issued after it); last, when the
+            // columns' registers are free for a part of the dims at once
+            if (NT == 1 && !(ok = await_pv(n - 1))) break;
+            const uint64_t f2 = f2pack(f, f);
+            const uint32_t to = tl + U::kO + t * HD + wg * (HD / kParts);
+#pragma unroll 1
+            for (int c = 0; c < HD / kParts; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) f2scale(o + k, f2);
+              tmem_st32(to + c, o);
+            }
+          }
           tmem_wait_st();
         }
         tmem_fence_before_sync();
@@ -649,26 +661,26 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       for (int t = 0; t < NT; ++t, other_tile()) {
         if (!(ok = await_pv((jb - 1) * NT + t))) break;
         if (!warp_in[0]) continue;
-        float other;
-        if (!(ok = exchange(l[0], other))) break;
+        float all[kParts];
+        if (!(ok = exchange(l[0], all))) break;
         const int64_t flat = flat0 + t * CG * kTileM;
         const bool in = flat < pairs;
         const int64_t row = in ? flat / G : 0;
         const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
-        const float sum = wg == 0 ? l[0] + other : other + l[0];  // the same order in both threads
+        const float sum = (all[0] + all[1]) + (all[2] + all[3]);
         const bool any = sum != 0.f;  // NaN too
         const float inv = any ? 1.f / sum : 0.f;
         const int64_t at = (static_cast<int64_t>(seg.part) * a.rows + row) * a.num_q_heads + head;
         if (in && wg == 0) a.lse_part[at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
         float* dst = a.o_part + at * HD;
 #pragma unroll 1
-        for (int c = wg * (HD / 2); c < (wg + 1) * (HD / 2); c += 32) {
-          float o[32];
-          tmem_ld32(tl + U::kO + t * HD + c, o);
-          tmem_wait_ld(o);
+        for (int c = wg * (HD / kParts); c < (wg + 1) * (HD / kParts); c += 16) {
+          float o[16];
+          tmem_load(tl + U::kO + t * HD + c, o);
+          tmem_loaded(o);
           if (in && any) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
+            for (int k = 0; k < 16; k += 4) {
               // int8: the producers store dims 0, 2, 1, 3 of each four
               const float x1 = F::kInt8 ? o[k + 2] : o[k + 1], x2 = F::kInt8 ? o[k + 1] : o[k + 2];
               *reinterpret_cast<float4*>(dst + c + k) = make_float4(o[k] * inv, x1 * inv, x2 * inv, o[k + 3] * inv);
@@ -685,6 +697,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     const int pg = (warp - U::kSoftWarps) >> 2, pw = warp & 3;  // group, warp of the group
     const int voff = rank * VOp::kBytes;  // this SM's dims
     const uint32_t krow = 4 * (rank * U::kKRows + KOp::kWarpRows * pw), vrow = 4 * VOp::kWarpRows * pw;  // of a ring entry
+    Rows kr, vr;
+    if (F::kBytes) {
+      kr = rows_of<KOp>(a.k_cache, pw, lane, rank * U::kKRows);
+      vr = rows_of<VOp>(a.v_cache + voff, pw, lane, 0);
+    }
     uint32_t base = 0, jb = 0;            // slots and blocks of earlier segments
     bool ok = true;
     auto await = [&](uint32_t s) -> bool {
@@ -713,38 +730,25 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         if (lane == 0) bar_arrive(sb + U::kRecEmpty + 8 * ((jb + block_of(e)) % kRecRing));
       };
       if (F::kBytes) {
-        const uint32_t stage0 = sb + U::kStage + pg * U::kStageBytes;
-        const uint32_t kd = stage0 + pw * KOp::kInstr * 512 + lane * 16, vd = stage0 + pw * VOp::kInstr * 512 + lane * 16;
-        const uint8_t* kp = a.k_cache + 16 * (lane % KOp::kLpr);
-        const uint8_t* vp = a.v_cache + voff + 16 * (lane % VOp::kLpr);
-        auto stage = [&](int e) -> bool {
+        static_assert(KOp::kInstr == VOp::kInstr, "one code for both");
+        constexpr int N = KOp::kInstr;
+        uint4 raw[N];
+        auto load = [&](int e) -> bool {
           if (e >= 2 * B) return true;
           if (!await_records(e)) return false;
-          if (is_v(e)) {
-            rec += vrow + 4 * (lane / VOp::kLpr);
-#pragma unroll 4
-            for (int u = 0; u < VOp::kInstr; ++u) VOp::stage1(vd, vp, u, rec);
-          } else {
-            rec += krow + 4 * (lane / KOp::kLpr);
-#pragma unroll 4
-            for (int u = 0; u < KOp::kInstr; ++u) KOp::stage1(kd, kp, u, rec);
-          }
+          load_rows<FMT, HD, N>(raw, is_v(e) ? vr : kr, rec);
           free_records(e);
           return true;
         };
-        ok = stage(pg);
-        cp_async_commit();
+        ok = load(pg);
+#pragma unroll 1
         for (int e = pg; ok && e < 2 * B; e += 2) {
-          const uint32_t n = base + e, slot = sb + U::kRing + (n % NS) * U::kSlotBytes;
+          const uint32_t n = base + e;
           if (!(ok = await(n))) break;
-          cp_async_wait<0>();
-          if (is_v(e)) VOp::convert(slot, vd, pw, lane);
-          else KOp::convert(slot, kd, pw, lane);
+          convert_rows<FMT, N>(sb + U::kRing + (n % NS) * U::kSlotBytes, is_v(e) ? vr : kr, raw);
           hand_over(n);
-          ok = stage(e + 2);
-          cp_async_commit();
+          ok = load(e + 2);
         }
-        cp_async_wait<0>();
       } else {
         for (int e = pg; ok && e < 2 * B; e += 2) {
           const uint32_t n = base + e, slot = sb + U::kRing + (n % NS) * U::kSlotBytes;
@@ -839,49 +843,51 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         if (lane == 0) bar_arrive(sb + U::kScFull + 8 * n);
       }
     }
-  } else if (lane == 0 && rank == 0) {
+  } else if (rank == 0) {
     // ================================================================ MMA issuer
     uint32_t base = 0, jb = 0, segs = 0;
     bool ok = true;
-    auto await_full = [&](uint32_t s) -> bool { return bar_wait(sb + U::kFull + 8 * (s % NS), (s / NS) & 1, flag); };
+    const uint32_t lead = elect_one();
+    const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);  // warp-uniform
+    auto wait = [&](uint32_t bar, uint32_t ph) -> bool { return __all_sync(0xffffffffu, bar_wait(bar, ph, flag)); };
+    auto await_full = [&](uint32_t s) -> bool { return wait(sb + U::kFull + 8 * (s % NS), (s / NS) & 1); };
     // S of tile t into buffer b, from the K slot s (awaited by the first tile, freed by the last)
     auto qk = [&](int t, uint32_t b, uint32_t s) {
       if (t == 0 && !(ok = await_full(s))) return;
       tmem_fence_after_sync();
-      const uint32_t d = tb + U::kS + KB * b;
-      uint64_t qd = sw128_desc(sb + U::kQ + t * U::kQTile, 16, 1024);
-      uint64_t kd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, 16, 1024);
-#pragma unroll 1
-      for (int i = 0; i < HD / 64; ++i) {  // 64 dims: one column of 128 B rows
+      const uint32_t d = tu + U::kS + KB * b;
+      const uint64_t qd = sw128_desc(sb + U::kQ + t * U::kQTile, 16, 1024);
+      const uint64_t kd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, 16, 1024);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_ss<CG>(d, qd + 2 * ks, kd + 2 * ks, U::kIdS, i > 0 || ks > 0 ? 1u : 0u);
-        qd += (kTileM * 128) >> 4;
-        kd += (U::kKRows * 128) >> 4;
+      for (int ks = 0; ks < HD / 16; ++ks)  // 64 dims are one column of 128 B rows
+        mma_ss<CG>(d, qd + (ks >> 2) * ((kTileM * 128) >> 4) + 2 * (ks & 3), kd + (ks >> 2) * ((U::kKRows * 128) >> 4) + 2 * (ks & 3),
+                   U::kIdS, ks > 0 ? 1u : 0u, lead);
+      if (lead) {
+        if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
+        commit_to<CG>(sb + U::kSFull + 8 * b);
       }
-      if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
-      commit_to<CG>(sb + U::kSFull + 8 * b);
+      __syncwarp();
     };
     // O of tile t += P (in buffer b) times the V slot s
     auto pv = [&](int t, uint32_t b, uint32_t ph, uint32_t s, bool first) {
-      if (!(ok = bar_wait(sb + U::kPFull + 8 * b, ph, flag))) return;
+      if (!(ok = wait(sb + U::kPFull + 8 * b, ph))) return;
       if (t == 0 && !(ok = await_full(s))) return;
       tmem_fence_after_sync();
-      const uint32_t d = tb + U::kO + t * HD;
-      uint32_t p = tb + U::kS + KB * b;
-      uint64_t vd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, KB * 128, 1024);
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {  // half of the keys: their P lies over their S
+      constexpr int kPer = KB / kParts / 16;  // 16 keys a step
+      const uint32_t d = tu + U::kO + t * HD, p = tu + U::kS + KB * b;
+      const uint64_t vd = sw128_desc(sb + U::kRing + (s % NS) * U::kSlotBytes, KB * 128, 1024);
 #pragma unroll
-        for (int ks = 0; ks < KB / 32; ++ks) mma_ts<CG>(d, p + 8 * ks, vd + 128 * ks, U::kIdO, !first || i > 0 || ks > 0 ? 1u : 0u);
-        p += KB / 2;
-        vd += 128 * (KB / 32);
+      for (int ks = 0; ks < KB / 16; ++ks)  // each part of the keys' P lies over its S
+        mma_ts<CG>(d, p + (ks / kPer) * (KB / kParts) + 8 * (ks % kPer), vd + 128 * ks, U::kIdO, !first || ks > 0 ? 1u : 0u, lead);
+      if (lead) {
+        if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
+        commit_to<CG>(sb + U::kPvDone + 8 * b);
       }
-      if (t == NT - 1) commit_to<CG>(sb + U::kEmpty + 8 * (s % NS));
-      commit_to<CG>(sb + U::kPvDone + 8 * b);
+      __syncwarp();
     };
     while (ok && seg.next()) {
       const int B = seg.b1 - seg.b0;
-      ok = bar_wait(sb + U::kQFull, segs & 1, flag);
+      ok = wait(sb + U::kQFull, segs & 1);
       ++segs;
       // two tiles: P V of block j of a tile, then its S of block j + 1; one tile: S of block j + 1, then P V of j
 #pragma unroll 1
@@ -898,7 +904,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       jb += B;
       base += 2 * B;
     }
-    commit_to<CG>(sb + U::kDrain);
+    if (lead) commit_to<CG>(sb + U::kDrain);
+    __syncwarp();
   }
   if (warp == U::kMmaWarp && lane == 0) {
     // nothing may still write tensor memory, read a slot or arrive on a barrier when the team leaves
