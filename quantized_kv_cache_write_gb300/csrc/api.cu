@@ -557,8 +557,8 @@ constexpr int64_t kUmmaMinPairs = 32;
 // (ragged rows balance), none with fewer than 256 keys.
 struct PrefixPlan {
   int prefix_parts, own_parts, prefix_chunk;
-  int umma_cg, umma_pairs, umma_keys, umma_ptiles;
-  int64_t umma_tiles, umma_teams;
+  int umma_cg, umma_pairs, umma_ptiles;
+  uint32_t umma_blocks, umma_teams, umma_share, umma_extra;
   int64_t prefix_items, own_items;
   int parts() const { return prefix_parts + own_parts; }
   int64_t rows_heads;
@@ -601,18 +601,22 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
     p->prefix_parts = static_cast<int>(ceil_div(prefix_len, p->prefix_chunk));
   }
   p->prefix_items = ptiles * p->prefix_parts;
-  p->umma_cg = 0, p->umma_pairs = 0, p->umma_keys = 0, p->umma_ptiles = 0, p->umma_tiles = 0, p->umma_teams = 0;
+  p->umma_cg = 0, p->umma_pairs = 0, p->umma_ptiles = 0;
+  p->umma_blocks = 0, p->umma_teams = 0, p->umma_share = 0, p->umma_extra = 0;
   if (prefix_len > 0 && rows * G > kUmmaMinPairs) {
     p->umma_cg = rows * G > 128 ? 2 : 1;  // one SM's tile holds 128 pairs
     p->umma_pairs = p->umma_cg == 1 ? 128 : head_dim == 128 ? 512 : 256;
-    p->umma_keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
-    const int64_t nb = ceil_div(prefix_len, p->umma_keys), pt = ceil_div(rows * G, p->umma_pairs);
+    const int keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
+    const int64_t nb = ceil_div(prefix_len, keys), pt = ceil_div(rows * G, p->umma_pairs);
+    const int64_t total = pt * num_kv_heads * nb, teams = total < sms / p->umma_cg ? total : sms / p->umma_cg;
+    if (total > INT32_MAX) return QKV_ERR_UNSUPPORTED;  // units are numbered in 32 bits
     p->umma_ptiles = static_cast<int>(pt);
-    p->umma_tiles = pt * num_kv_heads;
-    const int64_t total = p->umma_tiles * nb, teams = sms / p->umma_cg;
-    p->umma_teams = total < teams ? total : teams;
-    // ranges of at least total / teams units: a tile's nb units touch at most this many
-    p->prefix_parts = static_cast<int>(ceil_div(nb, total / p->umma_teams) + 1);
+    p->umma_blocks = static_cast<uint32_t>(nb);
+    p->umma_teams = static_cast<uint32_t>(teams);
+    p->umma_share = static_cast<uint32_t>(total / teams);
+    p->umma_extra = static_cast<uint32_t>(total % teams);
+    // a tile's nb units touch at most this many ranges
+    p->prefix_parts = static_cast<int>(ceil_div(nb, p->umma_share) + 1);
     p->prefix_items = 0;
   }
   p->own_parts = parts_of(otiles, own);
@@ -731,10 +735,11 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   cudaError_t e = cudaSuccess;
   a.umma_cg = p.umma_cg;
   a.umma_pairs = p.umma_pairs;
-  a.umma_keys = p.umma_keys;
   a.umma_ptiles = p.umma_ptiles;
-  a.umma_tiles = p.umma_tiles;
+  a.umma_blocks = p.umma_blocks;
   a.umma_teams = p.umma_teams;
+  a.umma_share = p.umma_share;
+  a.umma_extra = p.umma_extra;
   if (p.umma_cg > 0) e = launch_prefix_umma(a, d->fmt, s);
   if (e == cudaSuccess && p.prefix_items + p.own_items > 0) e = launch_prefix_mma(a, d->fmt, p.umma_cg > 0, s);
   if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, s);

@@ -25,9 +25,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
   int pre = a.prefix_parts;
   if (a.umma_cg > 0) {
     const int G = a.num_q_heads / a.num_kv_heads, head = static_cast<int>(unit - row * a.num_q_heads), h = head / G;
-    const int64_t nb = (a.prefix_len + a.umma_keys - 1) / a.umma_keys, total = a.umma_tiles * nb;
-    const int64_t tile = static_cast<int64_t>(h) * a.umma_ptiles + (row * G + (head - h * G)) / a.umma_pairs;
-    pre = static_cast<int>(team_of((tile + 1) * nb - 1, total, a.umma_teams) - team_of(tile * nb, total, a.umma_teams)) + 1;
+    const uint32_t pair = static_cast<uint32_t>(row) * G + (head - h * G);
+    const uint32_t first = (static_cast<uint32_t>(h) * a.umma_ptiles + pair / a.umma_pairs) * a.umma_blocks;
+    pre = static_cast<int>(team_of(a, first + a.umma_blocks - 1) - team_of(a, first)) + 1;
   }
   await_previous();
   if (state == kPadRow) return;

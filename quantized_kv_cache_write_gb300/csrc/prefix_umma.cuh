@@ -22,14 +22,14 @@
 //     (cp.async).
 //   scales: K and V scales, the mask of the block's keys and the largest V scale into a small ring.
 //   MMA: one thread. P is the A operand in tensor memory, in the columns of the S it was made from.
-//   softmax: y = S ks fac (log2 units). Reference R = M + E - 7: M follows the row's maximum lazily
-//     (raised when a logit passes it by 2^8), E is a power-of-two bound on the V scales, so p vs 2^-R
+//   softmax: y = S ks fac (log2 units). Reference R = M + E - kShift: M follows the row's maximum lazily
+//     (raised when a logit passes it by 2^kRaise), E is a power-of-two bound on the V scales, so p vs 2^-R
 //     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. The thread's columns
 //     stay in registers from the one load of S on: their maximum is exchanged between the row's four threads,
 //     then p replaces them, and each thread's part of P goes over its own part of S. A raise rescales O after P
-//     is stored, when those registers are free (measured, 64 rows x 64 heads behind 32768 e4m3 keys: 131 us for
-//     the call with two threads per pair and the columns read twice, 163 us with O rescaled before P, 130 us
-//     like this; 256 rows x 16 heads behind 65536 int8 keys 269, 269 and 264 us).
+//     is stored, when those registers are free (measured, 64 rows x 64 heads behind 32768 e4m3 keys: 165 thousand
+//     cycles, 265 with O rescaled before P; 256 rows x 16 heads behind 65536 int8 keys: 264 us for the call, 269
+//     with O rescaled before P and 269 with two threads per pair that read their columns twice).
 // Arithmetic as in prefix_attn.cuh: exact codes, logits and sums in fp32, p rounded once.
 //
 // The roles' loops are kept rolled: five of them run at once on each scheduler, and fully unrolled they
@@ -59,6 +59,12 @@ struct Umma {
   static constexpr int KB = umma_block_keys(HD, CG);
   static constexpr int kSoftWarps = 4 * kParts, kRecWarp = kSoftWarps + 2 * kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  // The softmax's window: a logit may pass its reference by 2^kRaise, and p there is 2^kShift (int8: times a V scale
+  // over its bound, which sits up to 2^kHeadroom above the largest seen). fp16 operands stay below 2^15, and
+  // a p below fp16's normal range is off by at most 2^-25 2^-kShift, int8 2^(1 + kHeadroom) of that: 2^-28 of the largest
+  // V. bf16 operands have fp32's range.
+  static constexpr float kRaise = F::kBf16 ? 16.f : F::kInt8 ? 10.f : 12.f, kShift = F::kBf16 ? 0.f : 15.f - kRaise;
+  static constexpr int kHeadroom = 1;
   static constexpr int kKRows = KB / CG, kVDims = HD / CG;  // this SM's part of a block
   static constexpr uint32_t kSlotBytes = uint32_t(KB) * HD * 2 / CG;
   static constexpr uint32_t kQTile = kTileM * HD * 2;
@@ -250,36 +256,34 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[8
                : "memory");
 }
 
-// The team whose range [i total / n, (i + 1) total / n) holds unit x.
-__device__ __forceinline__ int64_t team_of(int64_t x, int64_t total, int64_t n) { return ((x + 1) * n - 1) / total; }
+// The team whose range holds unit x.
+__device__ __forceinline__ uint32_t team_of(const PrefixArgs& a, uint32_t x) {
+  const uint32_t cut = a.umma_extra * (a.umma_share + 1);
+  return x < cut ? x / (a.umma_share + 1) : a.umma_extra + (x - cut) / a.umma_share;
+}
 
 // A team's next segment: the part of its unit range that lies in one (KV head, pair tile).
 struct Segment {
-  int64_t u, end;  // units still to do
-  int64_t total, n;
-  int nb;          // key blocks of the prefix
-  int team;
+  uint32_t u, end;  // units still to do
+  uint32_t team;
   int tile, b0, b1, part;
-  __device__ __forceinline__ bool next() {
+  __device__ __forceinline__ bool next(const PrefixArgs& a) {
     if (u >= end) return false;
-    tile = static_cast<int>(u / nb);
-    const int64_t t0 = static_cast<int64_t>(tile) * nb;
+    const uint32_t nb = a.umma_blocks, t = u / nb, t0 = t * nb;
+    tile = static_cast<int>(t);
     b0 = static_cast<int>(u - t0);
-    b1 = static_cast<int>(min(end - t0, static_cast<int64_t>(nb)));
-    part = static_cast<int>(team - team_of(t0, total, n));
+    b1 = static_cast<int>(min(end - t0, nb));
+    part = b0 > 0 ? static_cast<int>(team - team_of(a, t0)) : 0;  // a tile's first units: its first part
     u = t0 + b1;
     return true;
   }
 };
 template <int CG>
-__device__ __forceinline__ Segment first_segment(const PrefixArgs& a, int keys) {
+__device__ __forceinline__ Segment first_segment(const PrefixArgs& a) {
   Segment s;
-  s.nb = (a.prefix_len + keys - 1) / keys;
-  s.total = a.umma_tiles * s.nb;
-  s.n = gridDim.x / CG;
   s.team = blockIdx.x / CG;
-  s.u = s.team * s.total / s.n;
-  s.end = (s.team + 1) * s.total / s.n;
+  s.u = s.team * a.umma_share + min(s.team, a.umma_extra);
+  s.end = s.u + a.umma_share + (s.team < a.umma_extra ? 1 : 0);
   return s;
 }
 
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   const int rank = CG == 2 ? blockIdx.x & 1 : 0;  // this SM in the team
   const uint32_t sb = (smem_u32(smem) + 1023u) & ~1023u, smem0 = smem_u32(smem), flag = sb + U::kFlag;  // swizzled rows: 1 KB aligned
   const int H = a.num_kv_heads, G = a.num_q_heads / H;
-  const int64_t pairs = a.rows * G;
+  const uint32_t pairs = static_cast<uint32_t>(a.rows) * G;
   let_next_start();
 
   if (warp == U::kMmaWarp) {
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   team_sync<CG>();
   tmem_fence_after_sync();
   const uint32_t tb = lds32(sb + U::kTmemSlot);
-  Segment seg = first_segment<CG>(a, KB);
+  Segment seg = first_segment<CG>(a);
   Records rc;
   rc.blocks = a.prefix_blocks, rc.num_slots = a.num_slots, rc.bsz = a.block_size, rc.len = a.prefix_len, rc.H = H;
   rc.pow2 = (rc.bsz & (rc.bsz - 1)) == 0, rc.shift = __ffs(rc.bsz) - 1;
@@ -457,7 +461,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;
     const uint32_t row_bar = sb + U::kRowSet + 8 * q4;
     constexpr int HB = KB / kParts;  // this thread's columns of a block
-    constexpr float kShift = F::kBf16 ? 0.f : kPShift;
+    // this thread's part of the dims, and the place of this warp's rows of it in a query tile
+    constexpr int kVec = HD / kParts / 8;
+    const int d0 = wg * (HD / kParts), c0 = (d0 >> 3) & 7;
+    const uint32_t own_part = sb + U::kQ + (d0 >> 6) * (kTileM * 128) + 32 * q4 * 128;
     uint32_t jb = 0, meet = 0;  // blocks so far; exchanges so far of the row's threads
     bool ok = true;
     // the threads of each of the warp's rows leave a value, and take all of them in the same order
@@ -478,78 +485,13 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       tmem_fence_after_sync();
       return done;
     };
-    while (ok && seg.next()) {
+    while (ok && seg.next(a)) {
       const int h = seg.tile / a.umma_ptiles;
-      const int64_t flat0 = (static_cast<int64_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
-      float fac[NT];
-      bool warp_in[NT];
-      // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), a part of the
-      // dims by each of a row's threads
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int64_t flat = flat0 + t * CG * kTileM;
-        const bool in = flat < pairs;
-        const int64_t row = in ? flat / G : 0;
-        const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
-        warp_in[t] = __any_sync(0xffffffffu, in);
-        const int d0 = wg * (HD / kParts);
-        const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(head) * HD + d0;
-        float fc = fabsf(a.softmax_scale) * kLog2e, up = sign;
-        constexpr int kQVec = HD / kParts / 8;
-        if (F::kBytes) {
-          uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
-          if (in) {
-#pragma unroll
-            for (int i = 0; i < kQVec; ++i) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-            }
-          }
-          float all[kParts];
-          if (!(ok = exchange(__uint_as_float(mb), all))) break;
-#pragma unroll
-          for (int i = 0; i < kParts; ++i) mb = max(mb, __float_as_uint(all[i]));
-          const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
-          int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
-          e = max(-112, min(126, e));
-          up = sign * pow2f(e);
-          fc *= pow2f(-e);
-          if (FMT == QKV_E4M3) fc *= a.k_scale_layer;
-        }
-        fac[t] = fmaxf(fc, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
-        const uint32_t qrow = sb + U::kQ + t * U::kQTile + r * 128;
-#pragma unroll
-        for (int i = 0; i < kQVec; ++i) {
-          uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
-          if (F::kBytes) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
-              x[2 * k] = f.x * up;
-              x[2 * k + 1] = f.y * up;
-            }
-            // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
-            v = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
-                         : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
-          } else if (sign < 0.f) {
-            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-          }
-          const int d = d0 + 8 * i;
-          sts128(qrow + (d >> 6) * (kTileM * 128) + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
-        }
-      }
-      if (!ok) break;
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
-
+      const uint32_t flat0 = (static_cast<uint32_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
       // state of the tile at hand; with two tiles the other one's waits in the second element
-      float M[2] = {-INFINITY, -INFINITY}, R[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+      float M[2] = {-INFINITY, -INFINITY}, R[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, fac[NT] = {};
       int E[2] = {F::kInt8 ? -90 : 0, F::kInt8 ? -90 : 0};
+      bool warp_in[NT] = {};
       auto other_tile = [&]() {
         if (NT == 2) {
           float x;
@@ -563,6 +505,74 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           warp_in[0] = warp_in[NT - 1], warp_in[NT - 1] = w;
         }
       };
+      // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), a part of the
+      // dims by each of a row's threads; kVec lanes fetch a row's part together, 32 / kVec rows at a time
+#pragma unroll 1
+      for (int t = 0; t < NT; ++t, other_tile()) {
+        const uint32_t flat = flat0 + t * CG * kTileM;
+        const bool in = flat < pairs;
+        const uint32_t row = in ? flat / G : 0;
+        warp_in[0] = __any_sync(0xffffffffu, in);
+        const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(in ? h * G + (flat - row * G) : 0) * HD + d0;
+        const uint32_t part = own_part + t * U::kQTile;
+        uint4 v[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const int rr = 32 / kVec * i + lane / kVec;
+          const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), rr);
+          const bool there = __shfl_sync(0xffffffffu, in, rr);
+          v[i] = there ? __ldg(reinterpret_cast<const uint4*>(from) + lane % kVec) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const int rr = 32 / kVec * i + lane / kVec;
+          if (!F::kBytes && sign < 0.f) v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
+          sts128(part + rr * 128 + (((c0 + lane % kVec) ^ (rr & 7)) << 4), v[i]);
+        }
+        float fc = fabsf(a.softmax_scale) * kLog2e;
+        if (F::kBytes) {
+          __syncwarp();
+          uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            v[i] = lds128(part + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4));
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          }
+          float all[kParts];
+          if (!(ok = exchange(__uint_as_float(mb), all))) break;
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) mb = max(mb, __float_as_uint(all[i]));
+          const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
+          int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
+          e = max(-112, min(126, e));
+          const float up = sign * pow2f(e);
+          fc *= pow2f(-e);
+          if (FMT == QKV_E4M3) fc *= a.k_scale_layer;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
+              x[2 * k] = f.x * up;
+              x[2 * k + 1] = f.y * up;
+            }
+            // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
+            v[i] = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
+                            : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+            sts128(part + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4), v[i]);
+          }
+        }
+        fac[0] = fmaxf(fc, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
+      }
+      if (!ok) break;
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
+
       const int subs = (seg.b1 - seg.b0) * NT;
 #pragma unroll 1
       for (int i = 0; i < subs; ++i) {
@@ -596,15 +606,15 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           int En = E[0];
           if (F::kInt8) {
             const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
-            if (e > En) En = e + kEuHeadroom;
+            if (e > En) En = e + U::kHeadroom;
           }
-          const bool up_m = tm > M[0] + kTau;  // the same for the row's threads
+          const bool up_m = tm > M[0] + U::kRaise;  // the same for the row's threads
           const bool raise = __any_sync(0xffffffffu, up_m || En != E[0]);
           float f = 1.f;
           if (raise) {
             // ---- raise the reference: the sums and O so far go down by f
             const float Mn = up_m ? tm : M[0];
-            const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - kShift;
+            const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - U::kShift;
             if (M[0] != -INFINITY) f = fast_exp2(R[0] - Rn);
             l[0] *= f;
             M[0] = Mn, R[0] = Rn, E[0] = En;
@@ -663,29 +673,41 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         if (!warp_in[0]) continue;
         float all[kParts];
         if (!(ok = exchange(l[0], all))) break;
-        const int64_t flat = flat0 + t * CG * kTileM;
+        const uint32_t flat = flat0 + t * CG * kTileM;
         const bool in = flat < pairs;
-        const int64_t row = in ? flat / G : 0;
-        const int head = h * G + static_cast<int>(in ? flat - row * G : 0);
+        const uint32_t row = in ? flat / G : 0;
         const float sum = (all[0] + all[1]) + (all[2] + all[3]);
         const bool any = sum != 0.f;  // NaN too
         const float inv = any ? 1.f / sum : 0.f;
-        const int64_t at = (static_cast<int64_t>(seg.part) * a.rows + row) * a.num_q_heads + head;
-        if (in && wg == 0) a.lse_part[at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
-        float* dst = a.o_part + at * HD;
+        const int64_t part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
+        const int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
+        if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
+        // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer needs: four
+        // lanes write 64 B of a row
+        const int to = in && any ? at : -1;
+        const uint32_t part = own_part + t * U::kQTile;
 #pragma unroll 1
-        for (int c = wg * (HD / kParts); c < (wg + 1) * (HD / kParts); c += 16) {
+        for (int c = 0; c < HD / kParts; c += 16) {
           float o[16];
-          tmem_load(tl + U::kO + t * HD + c, o);
+          tmem_load(tl + U::kO + t * HD + d0 + c, o);
           tmem_loaded(o);
-          if (in && any) {
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              // int8: the producers store dims 0, 2, 1, 3 of each four
-              const float x1 = F::kInt8 ? o[k + 2] : o[k + 1], x2 = F::kInt8 ? o[k + 1] : o[k + 2];
-              *reinterpret_cast<float4*>(dst + c + k) = make_float4(o[k] * inv, x1 * inv, x2 * inv, o[k + 3] * inv);
-            }
+          for (int k = 0; k < 4; ++k) {
+            // int8: the producers store dims 0, 2, 1, 3 of each four
+            const float x1 = F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], x2 = F::kInt8 ? o[4 * k + 1] : o[4 * k + 2];
+            sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(o[4 * k] * inv), __float_as_uint(x1 * inv), __float_as_uint(x2 * inv),
+                              __float_as_uint(o[4 * k + 3] * inv)));
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 8 * k + (lane >> 3) + (lane & 4);
+            const int rr_to = __shfl_sync(0xffffffffu, to, rr);
+            const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
+            if (rr_to >= 0) *reinterpret_cast<uint4*>(a.o_part + (part_at + rr_to) * HD + d0 + c + 4 * (lane & 3)) = x;
+          }
+          __syncwarp();
         }
       }
       tmem_fence_before_sync();  // ordered before the next segment's first arrival
@@ -713,7 +735,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kFull + 8 * (s % NS));
     };
-    while (ok && seg.next()) {
+    while (ok && seg.next(a)) {
       const int B = seg.b1 - seg.b0;
       // what the segment's slot e holds
       auto is_v = [&](int e) -> bool { return e == 2 * B - 1 || (e > 0 && !(e & 1)); };
@@ -768,7 +790,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     // ================================================================ records
     uint32_t jb = 0;
     bool ok = true;
-    while (ok && seg.next()) {
+    while (ok && seg.next(a)) {
       rc.h = seg.tile / a.umma_ptiles;
       int blk[KB / 32];
 #pragma unroll
@@ -797,7 +819,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     // ================================================================ scales and masks
     uint32_t jb = 0;
     bool ok = true;
-    while (ok && seg.next()) {
+    while (ok && seg.next(a)) {
       for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
         const uint32_t n = jb & (kScRing - 1), sc = sb + U::kSc + n * U::kScStage, rn = jb % kRecRing;
         float ks[KB / 32], vs[KB / 32];
@@ -885,7 +907,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       }
       __syncwarp();
     };
-    while (ok && seg.next()) {
+    while (ok && seg.next(a)) {
       const int B = seg.b1 - seg.b0;
       ok = wait(sb + U::kQFull, segs & 1);
       ++segs;

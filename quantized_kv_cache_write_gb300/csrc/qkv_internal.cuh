@@ -182,13 +182,12 @@ struct PrefixArgs {
   int64_t prefix_items;  // CTAs of the mma.sync tiles
   int64_t own_items;
   // the prefix on tcgen05 (umma_cg > 0: SMs per team): umma_ptiles tiles of umma_pairs pairs per KV
-  // head, key blocks of umma_keys
+  // head by umma_blocks key blocks are the units, in that order; of umma_teams teams each takes umma_share, and the
+  // first umma_extra one more
   int umma_cg = 0;
   int umma_pairs = 0;
-  int umma_keys = 0;
   int umma_ptiles = 0;
-  int64_t umma_tiles = 0;  // umma_ptiles * num_kv_heads
-  int64_t umma_teams = 0;
+  uint32_t umma_blocks = 0, umma_teams = 0, umma_share = 0, umma_extra = 0;
 };
 // the mma.sync tiles of 16 (row, head) pairs over prefix_items ranges of the prefix and own_items of the
 // keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
