@@ -1,6 +1,7 @@
 // extern "C" entry points of libqkv.so: host-side validation, then one launch each on the
 // caller's stream. Nothing here allocates, frees or synchronises. The declarations, with
 // argument meaning, layout, ownership and error behaviour, are in qkv.h.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -550,6 +551,17 @@ namespace {
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
+// SMs of the current device, 0: none.
+int sm_count() {
+  static std::atomic<int> count[64] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    count[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // Pairs of (row, query head of a KV head) above which the prefix runs on tcgen05.
 constexpr int64_t kUmmaMinPairs = 32;
 
@@ -581,9 +593,8 @@ qkv_status check_prefix_shape(qkv_format fmt, int64_t rows, int num_q_heads, int
 
 qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head_dim, int prefix_len,
                        int max_row_len, PrefixPlan* p) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return QKV_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms < 1) return QKV_ERR_CUDA;
   const int G = num_q_heads / num_kv_heads, own = max_row_len - prefix_len;
   p->rows_heads = rows * num_q_heads;
   p->head_dim = head_dim;

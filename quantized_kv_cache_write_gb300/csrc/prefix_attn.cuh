@@ -20,6 +20,8 @@
 // 16-bit type or less.
 #pragma once
 
+#include <atomic>
+
 #include "qkv_internal.cuh"
 
 namespace qkv {
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
 
   // ---------------- the tile's pairs: lane i < 16 holds pair i (row, head of the group, keys of its own)
   int my_row = -1, my_g = 0, my_own = kPadRow;
-  int64_t r0 = 0;   // own part: its first row
+  uint32_t r0 = 0;  // own part: its first row
   int nrows = 0;    //           its rows, all of one sequence
   int seq = 0;
   if (own_part) {
@@ -130,14 +132,14 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     r0 = tile / static_cast<uint32_t>(chunks);
     const int ch = static_cast<int>(tile % static_cast<uint32_t>(chunks));
     // lane t holds row r0 + t, lane 31 the row before
-    const int64_t rr = lane == 31 ? r0 - 1 : r0 + lane;
+    const int64_t rr = static_cast<int64_t>(r0) + (lane == 31 ? -1 : lane);
     const bool there = rr >= 0 && rr < a.rows && (lane == 31 || lane < T);
     const int rs = there ? __ldg(a.row_seq + rr) : 0, rl = there ? __ldg(a.row_len + rr) : 0;
     seq = __shfl_sync(0xffffffffu, rs, 0);
     const uint32_t same = __ballot_sync(0xffffffffu, there && rs == seq);
     // rows [r0, r0 + n) up to the next multiple of T, while the sequence stays the same; a row that
     // continues such a run is in its first row's tile
-    const int into = static_cast<int>(r0 % T);
+    const int into = static_cast<int>(r0 % static_cast<uint32_t>(T));
     if (into != 0 && (same >> 31)) return;
     nrows = min(__ffs(~same) - 1, T - into);
     const int state = row_state(a, rs, rl, false);
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     const int st = __shfl_sync(0xffffffffu, state, t & 31);
     if (lane < kPairs && t < nrows && my_g < G) my_row = static_cast<int>(r0) + t, my_own = st;
   } else {
-    const int64_t flat = static_cast<int64_t>(tile) * kPairs + lane, row = flat / G;
+    const uint32_t flat = tile * kPairs + lane, row = flat / static_cast<uint32_t>(G);  // below 2^31 + 32
     my_g = static_cast<int>(flat - row * G);
     if (lane < kPairs && row < a.rows) my_row = static_cast<int>(row), my_own = 0;
   }
@@ -700,11 +702,26 @@ cudaError_t launch_after(K kern, unsigned grid, unsigned block, int smem, bool o
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// Opt a kernel into its dynamic shared memory, once per device (`done`: the kernel's own flags). Host threads may
+// race here on a device's first call: both set the same attribute, and the flags are atomic.
+template <typename K>
+cudaError_t allow_smem(K kern, int smem, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 template <int FMT, int HD>
 cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
+  static std::atomic<bool> done[64] = {};
   constexpr int smem = Geom<FMT, HD>::kSmem;
   auto kern = prefix_mma_kernel<FMT, HD>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_after(kern, static_cast<unsigned>(a.prefix_items + a.own_items), kThreads, smem, overlaps, stream, a);
 }

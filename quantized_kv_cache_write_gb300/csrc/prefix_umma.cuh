@@ -946,7 +946,8 @@ template <int FMT, int HD, int NT, int CG>
 cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
   using U = Umma<FMT, HD, NT, CG>;
   auto kern = prefix_umma_kernel<FMT, HD, NT, CG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, U::kSmem);
+  static std::atomic<bool> done[64] = {};
+  cudaError_t e = allow_smem(kern, U::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.umma_teams * CG));
