@@ -571,7 +571,7 @@ struct PrefixPlan {
   int prefix_parts, own_parts, prefix_chunk;
   int umma_cg, umma_pairs, umma_ptiles;
   uint32_t umma_blocks, umma_teams, umma_share, umma_extra;
-  int64_t prefix_items, own_items;
+  int64_t ptiles, otiles;  // mma.sync tiles of the prefix (none: it runs on tcgen05) and of the rows' own keys
   int parts() const { return prefix_parts + own_parts; }
   int64_t rows_heads;
   int head_dim;
@@ -598,20 +598,19 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
   const int G = num_q_heads / num_kv_heads, own = max_row_len - prefix_len;
   p->rows_heads = rows * num_q_heads;
   p->head_dim = head_dim;
-  const int64_t ptiles = ceil_div(rows * G, 16) * num_kv_heads;
-  const int64_t otiles = rows * ceil_div(G, 16) * num_kv_heads;
+  p->ptiles = ceil_div(rows * G, 16) * num_kv_heads;
+  p->otiles = rows * ceil_div(G, 16) * num_kv_heads;
   auto parts_of = [&](int64_t tiles, int keys) -> int {
     if (keys <= 0 || tiles <= 0) return 0;
     const int64_t want = ceil_div(8 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, 256);
     return static_cast<int>(want < most ? want : most);
   };
-  p->prefix_parts = parts_of(ptiles, prefix_len);
+  p->prefix_parts = parts_of(p->ptiles, prefix_len);
   p->prefix_chunk = 0;
   if (p->prefix_parts > 0) {
     p->prefix_chunk = static_cast<int>(ceil_div(ceil_div(prefix_len, p->prefix_parts), 64) * 64);
     p->prefix_parts = static_cast<int>(ceil_div(prefix_len, p->prefix_chunk));
   }
-  p->prefix_items = ptiles * p->prefix_parts;
   p->umma_cg = 0, p->umma_pairs = 0, p->umma_ptiles = 0;
   p->umma_blocks = 0, p->umma_teams = 0, p->umma_share = 0, p->umma_extra = 0;
   if (prefix_len > 0 && rows * G > kUmmaMinPairs) {
@@ -628,11 +627,11 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
     p->umma_extra = static_cast<uint32_t>(total % teams);
     // a tile's nb units touch at most this many ranges
     p->prefix_parts = static_cast<int>(ceil_div(nb, p->umma_share) + 1);
-    p->prefix_items = 0;
+    p->ptiles = 0;
   }
-  p->own_parts = parts_of(otiles, own);
-  p->own_items = otiles * p->own_parts;
-  if (p->prefix_items + p->own_items > INT32_MAX) return QKV_ERR_ARG;
+  p->own_parts = parts_of(p->otiles, own);
+  // tiles of 8 pairs: at most twice as many
+  if (2 * p->ptiles * p->prefix_parts + p->otiles * p->own_parts > INT32_MAX) return QKV_ERR_ARG;
   return QKV_OK;
 }
 
@@ -740,8 +739,11 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.prefix_parts = p.prefix_parts;
   a.own_parts = p.own_parts;
   a.prefix_chunk = p.prefix_chunk;
-  a.prefix_items = p.prefix_items;
-  a.own_items = p.own_items;
+  const int G = d->num_q_heads / d->num_kv_heads;
+  a.mma_pairs = G <= 8 && d->rows * G <= 8 * static_cast<int64_t>(d->num_seqs) ? 8 : 16;
+  if (a.mma_pairs == 8 && p.ptiles > 0) p.ptiles = ceil_div(d->rows * G, 8) * d->num_kv_heads;
+  a.prefix_items = p.ptiles * p.prefix_parts;
+  a.own_items = p.otiles * p.own_parts;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   a.umma_cg = p.umma_cg;
@@ -752,7 +754,7 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.umma_share = p.umma_share;
   a.umma_extra = p.umma_extra;
   if (p.umma_cg > 0) e = launch_prefix_umma(a, d->fmt, s);
-  if (e == cudaSuccess && p.prefix_items + p.own_items > 0) e = launch_prefix_mma(a, d->fmt, p.umma_cg > 0, s);
+  if (e == cudaSuccess && a.prefix_items + a.own_items > 0) e = launch_prefix_mma(a, d->fmt, p.umma_cg > 0, s);
   if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, s);
   return cuda_status(e);
 }

@@ -1,5 +1,5 @@
 // Dense decode attention over a paged pool for a batch whose sequences share a prefix: the part of
-// the work that runs on mma.sync tiles of 16 (row, query head) pairs.
+// the work that runs on mma.sync tiles of 16 or 8 (row, query head) pairs.
 //
 // For row r, query head h and the keys j the row sees (positions 0 .. row_len - 1 of its sequence;
 // those below prefix_len through the shared block list, the others through its own table row):
@@ -27,7 +27,6 @@
 namespace qkv {
 namespace prefix {
 
-constexpr int kPairs = 16;  // (row, query head) pairs of a CTA: the M of the MMAs
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -43,16 +42,18 @@ struct Fmt {
   static constexpr bool kBf16 = FMT == QKV_BF16;            // multiplied as bf16; every other pool as fp16
 };
 
-template <int FMT, int HD>
+// NP: (row, query head) pairs of a CTA. 16: they are the M of the MMAs, keys (dims) the N; 8: keys (dims) are the M,
+// pairs the N.
+template <int FMT, int HD, int NP>
 struct Geom {
   using F = Fmt<FMT>;
   static constexpr int kRow = F::kBytes ? HD : 2 * HD;              // bytes of a record's values
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : kRow;     // bytes between records
-  // keys of a warp tile (32 where rows are short: the softmax step's fixed cost is shared), ring stages and
-  // CTAs per SM: 64 to 128 KB of copies in flight per SM
-  static constexpr int kKeys = kRow == 128 ? 32 : 16;
-  static constexpr int kStages = kRow == 128 ? 2 : 3;
-  static constexpr int kMinBlocks = kRow == 128 ? 3 : kRow == 256 ? 2 : 1;
+  // keys of a warp tile (32 where rows are short and the tile holds 16 pairs: the softmax step's fixed cost is
+  // shared), ring stages and CTAs per SM: 64 to 128 KB of copies in flight per SM
+  static constexpr int kKeys = kRow == 128 && NP == 16 ? 32 : 16;
+  static constexpr int kStages = kRow == 128 ? (NP == 16 ? 2 : 3) : kRow == 256 ? (NP == 16 ? 3 : 2) : 3;
+  static constexpr int kMinBlocks = kRow == 128 ? (NP == 16 ? 3 : 4) : kRow == 256 ? (NP == 16 ? 2 : 3) : 1;
   static constexpr int kScales = 2 * kKeys * kRow;
   static constexpr int kMask = kScales + (F::kInt8 ? 2 * kKeys * 4 : 0);
   static constexpr int kStage = kMask + 16;  // K, V, scales, key mask
@@ -60,9 +61,9 @@ struct Geom {
   static constexpr int kQRow = 2 * HD + kQPad;
   static constexpr int kORow = HD + 4;  // floats per pair of the final join
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kJoin = kWarps * kPairs * kORow * 4;
+  static constexpr int kJoin = kWarps * NP * kORow * 4;
   static constexpr int kArea = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kSmem = kArea + kPairs * kQRow;
+  static constexpr int kSmem = kArea + NP * kQRow;
 };
 
 // Row (of 16) feeding column n of N-tile nt (of 2) of q.K^T, so that the p a lane holds are those of the
@@ -102,14 +103,28 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 // out (16-bit) of one value pair
 __device__ __forceinline__ uint32_t round2(bool f16, float x, float y) { return f16 ? pack_half2(x, y) : pack_bf162(x, y); }
 
-template <int FMT, int HD>
-__global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mma_kernel(const PrefixArgs a) {
+// The 8 x 8 matrix of 16-bit values that the warp holds (row lane / 4, columns 2 (lane % 4) and the next), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16) mma_bf16(d, a, b0, b1);
+  else mma_f16(d, a, b0, b1);
+}
+
+template <int FMT, int HD, int NP>
+__global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefix_mma_kernel(const PrefixArgs a) {
   using F = Fmt<FMT>;
-  using GM = Geom<FMT, HD>;
+  using GM = Geom<FMT, HD, NP>;
+  constexpr bool kWide = NP == 16;     // pairs are the MMAs' M
+  constexpr int KL = kWide ? 2 : 1;    // keys of eight whose logits a lane holds, for each of its two pairs
   constexpr int RB = GM::kRow, ST = GM::kStages, CH = RB / 16, TK = GM::kKeys, NH = TK / 16;
   constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sFac[kPairs], sM[kWarps][kPairs], sL[kWarps][kPairs];
+  __shared__ float sFac[NP], sM[kWarps][NP], sL[kWarps][NP];
   __shared__ int sEu[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, hn = lane >> 2;
   const int H = a.num_kv_heads, G = a.num_q_heads / H;
@@ -122,13 +137,13 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
   const int h = static_cast<int>(item % static_cast<uint32_t>(H));
   const uint32_t tile = item / static_cast<uint32_t>(H);
 
-  // ---------------- the tile's pairs: lane i < 16 holds pair i (row, head of the group, keys of its own)
+  // ---------------- the tile's pairs: lane i < NP holds pair i (row, head of the group, keys of its own)
   int my_row = -1, my_g = 0, my_own = kPadRow;
   uint32_t r0 = 0;  // own part: its first row
   int nrows = 0;    //           its rows, all of one sequence
   int seq = 0;
   if (own_part) {
-    const int T = G >= kPairs ? 1 : kPairs / G, chunks = (G + kPairs - 1) / kPairs;
+    const int T = G >= NP ? 1 : NP / G, chunks = (G + NP - 1) / NP;
     r0 = tile / static_cast<uint32_t>(chunks);
     const int ch = static_cast<int>(tile % static_cast<uint32_t>(chunks));
     // lane t holds row r0 + t, lane 31 the row before
@@ -143,18 +158,18 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     if (into != 0 && (same >> 31)) return;
     nrows = min(__ffs(~same) - 1, T - into);
     const int state = row_state(a, rs, rl, false);
-    const int t = G >= kPairs ? 0 : lane / G;
-    my_g = G >= kPairs ? ch * kPairs + lane : lane - t * G;
+    const int t = G >= NP ? 0 : lane / G;
+    my_g = G >= NP ? ch * NP + lane : lane - t * G;
     const int st = __shfl_sync(0xffffffffu, state, t & 31);
-    if (lane < kPairs && t < nrows && my_g < G) my_row = static_cast<int>(r0) + t, my_own = st;
+    if (lane < NP && t < nrows && my_g < G) my_row = static_cast<int>(r0) + t, my_own = st;
   } else {
-    const uint32_t flat = tile * kPairs + lane, row = flat / static_cast<uint32_t>(G);  // below 2^31 + 32
+    const uint32_t flat = tile * NP + lane, row = flat / static_cast<uint32_t>(G);  // below 2^31 + 32
     my_g = static_cast<int>(flat - row * G);
-    if (lane < kPairs && row < a.rows) my_row = static_cast<int>(row), my_own = 0;
+    if (lane < NP && row < a.rows) my_row = static_cast<int>(row), my_own = 0;
   }
 
-  // ---------------- query rows into registers, each warp four pairs
-  constexpr int kPer = HD / 32, kQPairs = kPairs / kWarps;  // dims per lane, pairs per warp
+  // ---------------- query rows into registers, each warp a quarter of the pairs
+  constexpr int kPer = HD / 32, kQPairs = NP / kWarps;  // dims per lane, pairs per warp
   uint32_t qw[kQPairs][kPer / 2];
 #pragma unroll
   for (int i = 0; i < kQPairs; ++i) {
@@ -338,32 +353,35 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
   }
   __syncthreads();
 
-  float o[HD / 8][4];
+  // kWide: pairs hn, hn + 8 (rows) by dims 8t + 2c, 2c + 1 (columns) of tile t; else dims 16t + hn, hn + 8 by pairs 2c, 2c + 1
+  constexpr int kOTiles = kWide ? HD / 8 : HD / 16;
+  float o[kOTiles][4];
 #pragma unroll
-  for (int t = 0; t < HD / 8; ++t)
+  for (int t = 0; t < kOTiles; ++t)
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[t][k] = 0.f;
   float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   int eu = -120;  // int8: the accumulators hold values times 2^-eu
-  const float fac[2] = {sFac[hn], sFac[hn + 8]};
+  const int pr[2] = {kWide ? hn : 2 * c, kWide ? hn + 8 : 2 * c + 1};  // the lane's two pairs
+  const float fac[2] = {sFac[pr[0]], sFac[pr[1]]};
   // first position past each of the lane's two rows
   int end[2], row_of[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const int ow = __shfl_sync(0xffffffffu, my_own, hn + 8 * p);
+    const int ow = __shfl_sync(0xffffffffu, my_own, pr[p]);
     end[p] = own_part ? a.prefix_len + max(ow, 0) : INT_MAX;
-    row_of[p] = __shfl_sync(0xffffffffu, my_row, hn + 8 * p);
+    row_of[p] = __shfl_sync(0xffffffffu, my_row, pr[p]);
   }
-  const uint32_t qa = smem_u32(sQ) + hn * GM::kQRow, qb = qa + 8 * GM::kQRow;
+  const uint32_t qa = smem_u32(sQ) + hn * GM::kQRow, qb = qa + (kWide ? 8 * GM::kQRow : 0);
   // 128-wide heads: the query's fragments stay in registers
   constexpr bool kQReg = HD == 128;
-  uint4 qf[kQReg ? HD / 32 : 1][2];
+  uint4 qf[kQReg ? HD / 32 : 1][KL];
   if (kQReg) {
 #pragma unroll
     for (int j = 0; j < HD / 32; ++j) {
       const uint32_t qo = F::kBytes ? 128 * (j >> 1) + 32 * c + 16 * (j & 1) : 64 * j + 16 * c;
       qf[j % (kQReg ? HD / 32 : 1)][0] = lds128(qa + qo);
-      qf[j % (kQReg ? HD / 32 : 1)][1] = lds128(qb + qo);
+      if (kWide) qf[j % (kQReg ? HD / 32 : 1)][KL - 1] = lds128(qb + qo);
     }
   }
 
@@ -378,23 +396,26 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     // every key wanted by every row: no masks
     const bool whole = mask == kAll && base + TK <= own_min;
 
-    // ---- logits: N-tiles of eight keys
-    float s[2 * NH][4];
+    // ---- logits of 2 NH groups of eight keys. kWide: N-tiles, s[n][2p + k]: pair p, key 2c + k of the group; else halves
+    // of M-tiles, s[n / 2][2 (n % 2) + p]: key hn of the group, pair p
+    float s[KL * NH][4];
 #pragma unroll
-    for (int n = 0; n < 2 * NH; ++n)
+    for (int n = 0; n < KL * NH; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+    auto S = [&](int n, int p, int k) -> float& { return kWide ? s[n % (KL * NH)][2 * p + k] : s[(n >> 1) % (KL * NH)][2 * (n & 1) + p]; };
+    auto key_at = [&](int n, int k) -> int { return 16 * (n >> 1) + key_of<FMT>(n & 1, kWide ? 2 * c + k : hn); };
     uint4 kb[2 * NH];  // bytes pools: 16 dims per lane, for two j
 #pragma unroll
     for (int j = 0; j < HD / 32; ++j) {  // two k-steps of 16 dims
       uint4 x, y;
       if (kQReg) {
-        x = qf[j % (kQReg ? HD / 32 : 1)][0], y = qf[j % (kQReg ? HD / 32 : 1)][1];
+        x = qf[j % (kQReg ? HD / 32 : 1)][0], y = qf[j % (kQReg ? HD / 32 : 1)][KL - 1];
       } else {
         const uint32_t qo = F::kBytes ? 128 * (j >> 1) + 32 * c + 16 * (j & 1) : 64 * j + 16 * c;
-        x = lds128(qa + qo), y = lds128(qb + qo);
+        x = lds128(qa + qo), y = kWide ? lds128(qb + qo) : x;
       }
-      const uint32_t a0f[4] = {x.x, y.x, x.y, y.y}, a1f[4] = {x.z, y.z, x.w, y.w};
+      uint32_t kf[2 * NH][4];  // a key's dims of the two k-steps
 #pragma unroll
       for (int n = 0; n < 2 * NH; ++n) {
         const int kr = key_of<FMT>(n & 1, hn);
@@ -402,60 +423,70 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
         if (F::kBytes) {
           if ((j & 1) == 0) kb[n] = lds128(krow + (((4 * (j >> 1) + c) ^ swz<FMT>(kr)) << 4));
           const uint2 kw = (j & 1) ? make_uint2(kb[n].z, kb[n].w) : make_uint2(kb[n].x, kb[n].y);  // four dims per k-step
-          if (F::kInt8) {
-            mma_f16(s[n], a0f, i8pair_to_f16x2(kw.x), i8pair_to_f16x2(kw.x >> 8));
-            mma_f16(s[n], a1f, i8pair_to_f16x2(kw.y), i8pair_to_f16x2(kw.y >> 8));
-          } else {
-            mma_f16(s[n], a0f, e4m3pair_to_f16x2(kw.x), e4m3pair_to_f16x2(kw.x >> 16));
-            mma_f16(s[n], a1f, e4m3pair_to_f16x2(kw.y), e4m3pair_to_f16x2(kw.y >> 16));
-          }
+          kf[n][0] = F::kInt8 ? i8pair_to_f16x2(kw.x) : e4m3pair_to_f16x2(kw.x);
+          kf[n][1] = F::kInt8 ? i8pair_to_f16x2(kw.x >> 8) : e4m3pair_to_f16x2(kw.x >> 16);
+          kf[n][2] = F::kInt8 ? i8pair_to_f16x2(kw.y) : e4m3pair_to_f16x2(kw.y);
+          kf[n][3] = F::kInt8 ? i8pair_to_f16x2(kw.y >> 8) : e4m3pair_to_f16x2(kw.y >> 16);
         } else {
           const uint4 kw = lds128(krow + (((4 * j + c) ^ swz<FMT>(kr)) << 4));
-          if (F::kBf16) {
-            mma_bf16(s[n], a0f, kw.x, kw.y);
-            mma_bf16(s[n], a1f, kw.z, kw.w);
-          } else {
-            mma_f16(s[n], a0f, kw.x, kw.y);
-            mma_f16(s[n], a1f, kw.z, kw.w);
-          }
+          kf[n][0] = kw.x, kf[n][1] = kw.y, kf[n][2] = kw.z, kf[n][3] = kw.w;
+        }
+        if (kWide) {
+          const uint32_t a0f[4] = {x.x, y.x, x.y, y.y}, a1f[4] = {x.z, y.z, x.w, y.w};
+          mma16<F::kBf16>(s[n % (KL * NH)], a0f, kf[n][0], kf[n][1]);
+          mma16<F::kBf16>(s[n % (KL * NH)], a1f, kf[n][2], kf[n][3]);
+        } else if (n & 1) {
+          const uint32_t a0f[4] = {kf[n - 1][0], kf[n][0], kf[n - 1][1], kf[n][1]};
+          const uint32_t a1f[4] = {kf[n - 1][2], kf[n][2], kf[n - 1][3], kf[n][3]};
+          mma16<F::kBf16>(s[(n >> 1) % (KL * NH)], a0f, x.x, x.y);
+          mma16<F::kBf16>(s[(n >> 1) % (KL * NH)], a1f, x.z, x.w);
         }
       }
     }
 
-    // ---- softmax step. Lane's columns of N-tile n: keys 16 (n / 2) + key_of(n % 2, 2c + {0, 1}); rows hn, hn + 8
-    float vs[NH][4];  // int8: V scales of the lane's keys 4c .. 4c + 3 of each 16
+    // ---- softmax step
+    float vs[2 * NH][KL];  // int8: V scales of the lane's keys
     float vmax = 0.f;
 #pragma unroll
     for (int g = 0; g < NH; ++g) {
-      float4 ks = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (F::kInt8) {
-        const uint4 kb = lds128(sk + GM::kScales + 4 * (16 * g + 4 * c)), vb = lds128(sk + GM::kScales + 4 * (TK + 16 * g + 4 * c));
-        ks = make_float4(__uint_as_float(kb.x), __uint_as_float(kb.y), __uint_as_float(kb.z), __uint_as_float(kb.w));
-        vs[g][0] = __uint_as_float(vb.x), vs[g][1] = __uint_as_float(vb.y);
-        vs[g][2] = __uint_as_float(vb.z), vs[g][3] = __uint_as_float(vb.w);
-        vmax = fmaxf(fmaxf(vmax, fmaxf(fabsf(vs[g][0]), fabsf(vs[g][1]))), fmaxf(fabsf(vs[g][2]), fabsf(vs[g][3])));
+      float ks[2][KL];
+      if (F::kInt8) {  // the lane's keys of 16: 4c .. 4c + 3 (kWide), 2 hn and the next
+        const uint32_t at = sk + GM::kScales + 4 * (16 * g + 2 * KL * (kWide ? c : hn));
+        uint32_t kw[4], vw[4];
+        if (kWide) {
+          const uint4 k4 = lds128(at), v4 = lds128(at + 4 * TK);
+          kw[0] = k4.x, kw[1] = k4.y, kw[2] = k4.z, kw[3] = k4.w;
+          vw[0] = v4.x, vw[1] = v4.y, vw[2] = v4.z, vw[3] = v4.w;
+        } else {
+          kw[0] = lds32(at), kw[1] = lds32(at + 4);
+          vw[0] = lds32(at + 4 * TK), vw[1] = lds32(at + 4 * TK + 4);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < KL; ++k) {  // key 2 (2c + k) + n, or 2 hn + n
+            ks[n][k] = __uint_as_float(kw[2 * k + n]);
+            vs[2 * g + n][k] = __uint_as_float(vw[2 * k + n]);
+            vmax = fmaxf(vmax, fabsf(vs[2 * g + n][k]));
+          }
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < KL; ++k)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            float& z = s[2 * g + n][2 * p + k];
-            // int8: key 4c + 2k + n
-            z *= F::kInt8 ? (k == 0 ? (n == 0 ? ks.x : ks.y) : (n == 0 ? ks.z : ks.w)) * fac[p] : fac[p];
-          }
+          for (int p = 0; p < 2; ++p) S(2 * g + n, p, k) *= F::kInt8 ? ks[n][k] * fac[p] : fac[p];
     }
     if (!whole) {
 #pragma unroll
       for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int key = 16 * (n >> 1) + key_of<FMT>(n & 1, 2 * c + k);
+        for (int k = 0; k < KL; ++k) {
+          const int key = key_at(n, k);
           const bool valid = (mask >> key) & 1;
 #pragma unroll
           for (int p = 0; p < 2; ++p)
-            if (!valid || base + key >= end[p]) s[n][2 * p + k] = -INFINITY;
+            if (!valid || base + key >= end[p]) S(n, p, k) = -INFINITY;
         }
     }
     float tm[2];
@@ -463,10 +494,13 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
     for (int p = 0; p < 2; ++p) {
       tm[p] = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < 2 * NH; ++n) tm[p] = fmaxf(tm[p], fmaxf(s[n][2 * p], s[n][2 * p + 1]));
-    }
+      for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
-    for (int off = 1; off <= 2; off <<= 1) {
+        for (int k = 0; k < KL; ++k) tm[p] = fmaxf(tm[p], S(n, p, k));
+    }
+    // over the lanes that hold the pairs' other keys: four (c) or eight (hn)
+#pragma unroll
+    for (int off = kWide ? 1 : 4; off <= (kWide ? 2 : 16); off <<= 1) {
       tm[0] = fmaxf(tm[0], __shfl_xor_sync(0xffffffffu, tm[0], off));
       tm[1] = fmaxf(tm[1], __shfl_xor_sync(0xffffffffu, tm[1], off));
       if (F::kInt8) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
@@ -491,35 +525,42 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
         f[p] = al * down;
       }
 #pragma unroll
-      for (int t = 0; t < HD / 8; ++t) {
+      for (int t = 0; t < kOTiles; ++t) {
         o[t][0] *= f[0];
-        o[t][1] *= f[0];
-        o[t][2] *= f[1];
+        o[t][1] *= f[kWide ? 0 : 1];
+        o[t][2] *= f[kWide ? 1 : 0];
         o[t][3] *= f[1];
       }
       eu = eu_new;
     }
     const float vdown = F::kInt8 ? pow2f(-eu) : 1.f;
-    uint32_t pa[NH][4];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const float ref = M[p] == -INFINITY ? 0.f : M[p] - (F::kBf16 ? 0.f : kPShift);
 #pragma unroll
-      for (int n = 0; n < 2 * NH; ++n) {
-        const float y0 = s[n][2 * p], y1 = s[n][2 * p + 1];
-        float e0 = fast_exp2(y0 - ref), e1 = fast_exp2(y1 - ref);
-        l[p] += e0 + e1;
-        if (F::kInt8) {
-          e0 *= vs[n >> 1][n & 1] * vdown;
-          e1 *= vs[n >> 1][2 + (n & 1)] * vdown;
-          if (!whole) {  // a masked key's scale may be anything (0 x inf): its p stays 0
-            if (y0 == -INFINITY) e0 = 0.f;
-            if (y1 == -INFINITY) e1 = 0.f;
+      for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+        for (int k = 0; k < KL; ++k) {
+          const float y = S(n, p, k);
+          float e = fast_exp2(y - ref);
+          l[p] += e;
+          if (F::kInt8) {
+            e *= vs[n][k] * vdown;
+            if (!whole && y == -INFINITY) e = 0.f;  // a masked key's scale may be anything (0 x inf): its p stays 0
           }
+          S(n, p, k) = e;
         }
-        pa[n >> 1][2 * (n & 1) + p] = F::kBf16 ? pack_bf162(e0, e1) : pack_half2(e0, e1);
-      }
     }
+    // kWide: the A operand, pairs by keys; else the B operand, keys by pairs (a lane's pairs were the columns)
+    uint32_t pa[NH][2 * KL];
+#pragma unroll
+    for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+      for (int p = 0; p < KL; ++p) {
+        const float e0 = S(n, p, 0), e1 = kWide ? S(n, p, KL - 1) : S(n, 1, 0);
+        const uint32_t w = F::kBf16 ? pack_bf162(e0, e1) : pack_half2(e0, e1);
+        pa[n >> 1][KL * (n & 1) + p] = kWide ? w : transpose8x8(w);
+      }
 
     // ---- p V
     // b0, b1 of the four N-tiles of eight dims from 32 q on, 16 keys from 16 g on
@@ -552,6 +593,15 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
         }
       }
     };
+    // tile k of the four of 8 dims (kWide) or the two of 16 that v holds
+    auto pv = [&](float (&d)[4], const uint32_t (&pw)[2 * KL], const uint32_t (&v)[8], int k) {
+      if constexpr (kWide) {
+        mma16<F::kBf16>(d, pw, v[2 * k], v[2 * k + 1]);
+      } else {
+        const uint32_t av[4] = {v[4 * k], v[4 * k + 2], v[4 * k + 1], v[4 * k + 3]};
+        mma16<F::kBf16>(d, av, pw[0], pw[1]);
+      }
+    };
     // Rows of different lengths in one tile: a key that one row sees and another does not may hold
     // anything there (0 x NaN), so such a tile goes row by row, each with its own keys only, and only
     // that row's sums are taken.
@@ -562,27 +612,26 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
         const int n_end = a.prefix_len + max(0, __shfl_sync(0xffffffffu, my_own, t * G));
 #pragma unroll 1
         for (int g = 0; g < NH; ++g) {
-          uint32_t keep[2], pg[4];  // halves of b0 / b1 (the lane's keys) that the row sees
+          uint32_t keep[2], pg[2 * KL];  // halves of b0 / b1 (the lane's keys) that the row sees
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             keep[k] = (base + 16 * g + key_of<FMT>(k, 2 * c) < n_end ? 0x0000ffffu : 0u) |
                       (base + 16 * g + key_of<FMT>(k, 2 * c + 1) < n_end ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) pg[k] = g == 0 ? pa[0][k] : pa[NH - 1][k];
+          for (int k = 0; k < 2 * KL; ++k) pg[k] = g == 0 ? pa[0][k] : pa[NH - 1][k];
 #pragma unroll
           for (int q = 0; q < HD / 32; ++q) {
             uint32_t v[8];
             v_frags(g, q, v);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 8; ++k) v[k] &= keep[k & 1];
+#pragma unroll
+            for (int k = 0; k < 2 * KL; ++k) {
               float x[4] = {0.f, 0.f, 0.f, 0.f};
-              if (F::kBf16)
-                mma_bf16(x, pg, v[2 * k] & keep[0], v[2 * k + 1] & keep[1]);
-              else
-                mma_f16(x, pg, v[2 * k] & keep[0], v[2 * k + 1] & keep[1]);
-              float* acc = o[4 * q + k];
-              if (row_of[0] == row) acc[0] += x[0], acc[1] += x[1];
-              if (row_of[1] == row) acc[2] += x[2], acc[3] += x[3];
+              pv(x, pg, v, k);
+              float* acc = o[2 * KL * q + k];
+              if (row_of[0] == row) acc[0] += x[0], acc[kWide ? 1 : 2] += x[kWide ? 1 : 2];
+              if (row_of[1] == row) acc[kWide ? 2 : 1] += x[kWide ? 2 : 1], acc[3] += x[3];
             }
           }
         }
@@ -595,12 +644,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
           uint32_t v[8];
           v_frags(g, q, v);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (F::kBf16)
-              mma_bf16(o[4 * q + k], pa[g], v[2 * k], v[2 * k + 1]);
-            else
-              mma_f16(o[4 * q + k], pa[g], v[2 * k], v[2 * k + 1]);
-          }
+          for (int k = 0; k < 2 * KL; ++k) pv(o[2 * KL * q + k], pa[g], v, k);
         }
     }
     __syncwarp();
@@ -612,11 +656,11 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
   cp_async_wait<0>();
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    l[p] += __shfl_xor_sync(0xffffffffu, l[p], 1);
-    l[p] += __shfl_xor_sync(0xffffffffu, l[p], 2);
-    if (c == 0) {
-      sM[warp][hn + 8 * p] = M[p];
-      sL[warp][hn + 8 * p] = l[p];
+#pragma unroll
+    for (int off = kWide ? 1 : 4; off <= (kWide ? 2 : 16); off <<= 1) l[p] += __shfl_xor_sync(0xffffffffu, l[p], off);
+    if ((kWide ? c : hn) == 0) {
+      sM[warp][pr[p]] = M[p];
+      sL[warp][pr[p]] = l[p];
     }
   }
   if (lane == 0) sEu[warp] = eu;
@@ -624,16 +668,18 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
   float* sO = reinterpret_cast<float*>(smem);
   if (my > 0) {
 #pragma unroll
-    for (int t = 0; t < HD / 8; ++t)
+    for (int t = 0; t < kOTiles; ++t)
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        *reinterpret_cast<float2*>(sO + (warp * kPairs + hn + 8 * p) * GM::kORow + 8 * t + 2 * c) =
-            make_float2(o[t][2 * p], o[t][2 * p + 1]);
+      for (int p = 0; p < 2; ++p) {
+        float* row = sO + (warp * NP + pr[p]) * GM::kORow;
+        if (kWide) *reinterpret_cast<float2*>(row + 8 * t + 2 * c) = make_float2(o[t][2 * p], o[t][2 * p + 1]);
+        else row[16 * t + hn] = o[t][p], row[16 * t + 8 + hn] = o[t][2 + p];
+      }
   }
   __syncthreads();
   const bool direct = a.o_part == nullptr;  // the only part: its result is the row's
 #pragma unroll 1
-  for (int i = warp; i < kPairs; i += kWarps) {
+  for (int i = warp; i < NP; i += kWarps) {
     const int row = __shfl_sync(0xffffffffu, my_row, i), g = __shfl_sync(0xffffffffu, my_g, i);
     if (row < 0) continue;
     const int head = h * G + g;
@@ -670,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD>::kMinBlocks) prefix_mm
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (f[w] == 0.f) continue;  // a warp without keys left no values
-        const float4 x = *reinterpret_cast<const float4*>(sO + (w * kPairs + i) * GM::kORow + d);
+        const float4 x = *reinterpret_cast<const float4*>(sO + (w * NP + i) * GM::kORow + d);
         acc.x += f[w] * x.x, acc.y += f[w] * x.y, acc.z += f[w] * x.z, acc.w += f[w] * x.w;
       }
       acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
@@ -716,11 +762,11 @@ cudaError_t allow_smem(K kern, int smem, std::atomic<bool> (&done)[64]) {
   return e;
 }
 
-template <int FMT, int HD>
+template <int FMT, int HD, int NP>
 cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
   static std::atomic<bool> done[64] = {};
-  constexpr int smem = Geom<FMT, HD>::kSmem;
-  auto kern = prefix_mma_kernel<FMT, HD>;
+  constexpr int smem = Geom<FMT, HD, NP>::kSmem;
+  auto kern = prefix_mma_kernel<FMT, HD, NP>;
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_after(kern, static_cast<unsigned>(a.prefix_items + a.own_items), kThreads, smem, overlaps, stream, a);
@@ -728,7 +774,9 @@ cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) 
 
 template <int FMT>
 cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
-  return a.head_dim == 256 ? launch_mma<FMT, 256>(a, overlaps, stream) : launch_mma<FMT, 128>(a, overlaps, stream);
+  if (a.head_dim == 256)
+    return a.mma_pairs == 8 ? launch_mma<FMT, 256, 8>(a, overlaps, stream) : launch_mma<FMT, 256, 16>(a, overlaps, stream);
+  return a.mma_pairs == 8 ? launch_mma<FMT, 128, 8>(a, overlaps, stream) : launch_mma<FMT, 128, 16>(a, overlaps, stream);
 }
 
 }  // namespace prefix

@@ -179,6 +179,7 @@ struct PrefixArgs {
   int prefix_parts;  // ranges of prefix_chunk keys of the shared prefix
   int own_parts;     // ranges of the keys behind it (of a length that goes by the row's)
   int prefix_chunk;
+  int mma_pairs;         // pairs of an mma.sync tile, 8 or 16
   int64_t prefix_items;  // CTAs of the mma.sync tiles
   int64_t own_items;
   // the prefix on tcgen05 (umma_cg > 0: SMs per team): umma_ptiles tiles of umma_pairs pairs per KV
@@ -189,7 +190,7 @@ struct PrefixArgs {
   int umma_ptiles = 0;
   uint32_t umma_blocks = 0, umma_teams = 0, umma_share = 0, umma_extra = 0;
 };
-// the mma.sync tiles of 16 (row, head) pairs over prefix_items ranges of the prefix and own_items of the
+// the mma.sync tiles of (row, head) pairs over prefix_items ranges of the prefix and own_items of the
 // keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
 cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_prefix_umma_bf16(const PrefixArgs& a, cudaStream_t stream);

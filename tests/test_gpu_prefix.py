@@ -133,6 +133,34 @@ def test_draft_rows_of_one_sequence_with_leftovers_behind_the_shorter_ones(fmt, 
     assert not torch.isfinite(out.float()[torch.from_numpy(~first).cuda()]).any()
 
 
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("D,G", [(128, 1), (128, 4), (256, 2)])
+def test_draft_rows_in_a_large_table(fmt, act, D, G):
+    """Few rows and many sequences (tiles of eight pairs): draft rows of one sequence share a tile, and the key that
+    only the last of them sees holds a NaN of its own."""
+    b, pool, q, scale = case(16, fmt, act, D, 2, G, 40, [7, 150, 4], 4, 16)
+    b.table = np.concatenate([b.table, np.full((30, b.table.shape[1]), -1, dtype=np.int32)])
+    for i in range(3):
+        n = int(b.row_len[4 * i + 3])
+        slot = int(b.table[i, (n - 1) // 16]) * 16 + (n - 1) % 16
+        if fmt == "int8_side":
+            pool.kw["v_scale_tok"][slot] = float("nan")
+        elif fmt == "int8_inline":
+            pool.cache[1].view(torch.uint8)[slot, :, D:] = 0xFF  # a NaN scale
+        elif fmt == "e4m3":
+            pool.cache[1].view(torch.uint8)[slot] = 0x7F
+        else:
+            pool.cache[1][slot] = float("nan")
+    out, lse = call(pool, b, dev16(q, act), 2, scale)
+    first = np.arange(12) % 4 != 3
+    slots, _ = dense.row_slots(b.row_seq[first], b.row_len[first], b.prefix_blocks, b.prefix, b.table, b.block, pool.num_slots)
+    ref, rlse, wabs, big = dense.prefix_attention(q[first], pool.K, pool.V, slots, scale, act)
+    tol, ltol = attention_bounds(ref, rlse, wabs, big, 190, float(np.abs(pool.V[b.live]).max()), act, fmt, D)
+    assert_within(out.float().cpu().numpy()[first], ref, tol, "rows before the leftovers")
+    assert_within(lse.cpu().numpy()[first], rlse, ltol, "lse before the leftovers")
+    assert torch.isnan(out.float()[torch.from_numpy(~first).cuda()]).all()
+
+
 def test_empty_padding_and_bad_rows():
     b, pool, q, scale = case(7, "int8_side", "bf16", 256, 1, 16, 50, [20, 30, 10, 5, 8, 9], 1, 16)
     for max_parts in (False, True):  # with and without keys of their own
