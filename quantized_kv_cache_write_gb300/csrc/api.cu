@@ -562,11 +562,17 @@ int sm_count() {
   return n;
 }
 
-// Pairs of (row, query head of a KV head) above which the prefix runs on tcgen05.
-constexpr int64_t kUmmaMinPairs = 32;
+// K bytes that tiles of 16 pairs would read above which the prefix runs on tcgen05: its tiles read them once per 128
+// pairs or more, but a call costs some 6 us before the first key and after the last. In us, mma.sync | tcgen05: one KV
+// head of 256, int8, 16 pairs of 65536 keys (17 MB) 28 | 35, 24 pairs (34 MB) 36 | 34, 128 pairs of 8192 (17 MB)
+// 22 | 26; 8 heads of 128, e4m3, 8192 keys, 32 pairs (17 MB) 19.4 | 18.8, 48 pairs (25 MB) 29 | 19; 4 heads of 128, bf16, 8192
+// keys, 32 pairs (17 MB) 17.0 | 18.5, 48 pairs (25 MB) 20.3 | 19.5, 64 pairs (34 MB) 30 | 19.
+constexpr int64_t kUmmaMinBytes = 20 << 20;
 
-// How a shared-prefix call is cut into key ranges: enough CTAs to fill the GPU a few times over
-// (ragged rows balance), none with fewer than 256 keys.
+// How a shared-prefix call is cut into key ranges: up to 16 CTAs per SM, so that ragged rows balance (64 rows x 64 heads
+// of 0 to 8192 e4m3 keys: 118 us, 121 with 8, 130 with 4), but none with fewer than 512 keys, since a CTA's start and its
+// join cost as much as about 300 (8 x 5 drafts behind 126976 int8 keys: 131 us, 135 with 256, 144 with 1024; one row of
+// 65536: 31 us, 40, 37), and 256 while those do not fill the SMs once (one row of 8192: 19 us, 23 with 512, 33 with 1024).
 struct PrefixPlan {
   int prefix_parts, own_parts, prefix_chunk;
   int umma_cg, umma_pairs, umma_ptiles;
@@ -591,7 +597,7 @@ qkv_status check_prefix_shape(qkv_format fmt, int64_t rows, int num_q_heads, int
   return QKV_OK;
 }
 
-qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head_dim, int prefix_len,
+qkv_status plan_prefix(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv_heads, int head_dim, int prefix_len,
                        int max_row_len, PrefixPlan* p) {
   const int sms = sm_count();
   if (sms < 1) return QKV_ERR_CUDA;
@@ -602,7 +608,8 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
   p->otiles = rows * ceil_div(G, 16) * num_kv_heads;
   auto parts_of = [&](int64_t tiles, int keys) -> int {
     if (keys <= 0 || tiles <= 0) return 0;
-    const int64_t want = ceil_div(8 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, 256);
+    const int least = tiles * ceil_div(keys, 256) <= sms ? 256 : 512;
+    const int64_t want = ceil_div(16 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, least);
     return static_cast<int>(want < most ? want : most);
   };
   p->prefix_parts = parts_of(p->ptiles, prefix_len);
@@ -613,8 +620,12 @@ qkv_status plan_prefix(int64_t rows, int num_q_heads, int num_kv_heads, int head
   }
   p->umma_cg = 0, p->umma_pairs = 0, p->umma_ptiles = 0;
   p->umma_blocks = 0, p->umma_teams = 0, p->umma_share = 0, p->umma_extra = 0;
-  if (prefix_len > 0 && rows * G > kUmmaMinPairs) {
-    p->umma_cg = rows * G > 128 ? 2 : 1;  // one SM's tile holds 128 pairs
+  const int64_t row_bytes = fmt == QKV_BF16 || fmt == QKV_F16 ? 2 * head_dim : head_dim;
+  if (prefix_len > 0 && p->ptiles > kUmmaMinBytes / (prefix_len * row_bytes)) {
+    // Two SMs per team where their tiles (512 pairs of 128-wide heads, 256 of 256-wide ones) are at least half full. In us, one
+    // SM | two: 8 heads of 128, e4m3, 65536 keys, 256 pairs 99 | 118, 512 pairs 180 | 145; 4 heads of 128, bf16, 256 pairs
+    // 64.6 | 65.5, 512 pairs 113 | 81; one head of 256, int8, 128 pairs 40 | 38, 192 pairs 44 | 40, 256 pairs 46 | 42.
+    p->umma_cg = rows * G > (head_dim == 128 ? 256 : 128) ? 2 : 1;
     p->umma_pairs = p->umma_cg == 1 ? 128 : head_dim == 128 ? 512 : 256;
     const int keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
     const int64_t nb = ceil_div(prefix_len, keys), pt = ceil_div(rows * G, p->umma_pairs);
@@ -667,7 +678,7 @@ qkv_status qkv_prefix_attn_workspace(qkv_format fmt, int64_t rows, int num_q_hea
   qkv_status st = check_prefix_shape(fmt, rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len);
   if (st != QKV_OK) return st;
   PrefixPlan p;
-  st = plan_prefix(rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len, &p);
+  st = plan_prefix(fmt, rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len, &p);
   if (st == QKV_OK) *bytes = p.bytes();
   return st;
 }
@@ -700,7 +711,7 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
     return QKV_ERR_ALIGN;
 
   PrefixPlan p;
-  st = plan_prefix(d->rows, d->num_q_heads, d->num_kv_heads, d->head_dim, d->prefix_len, d->max_row_len, &p);
+  st = plan_prefix(d->fmt, d->rows, d->num_q_heads, d->num_kv_heads, d->head_dim, d->prefix_len, d->max_row_len, &p);
   if (st != QKV_OK) return st;
   if (p.bytes() > 0 && (!d->workspace || d->workspace_bytes < p.bytes())) return QKV_ERR_ARG;
 
@@ -739,6 +750,9 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.prefix_parts = p.prefix_parts;
   a.own_parts = p.own_parts;
   a.prefix_chunk = p.prefix_chunk;
+  // Tiles of 8 pairs where a sequence's rows bring no more than that on average: half of a 16-pair tile would be empty. In us, 8 |
+  // 16: e4m3, 32 sequences of 1400 keys, 4 heads of 128, groups of 8, one row each 17 | 23, two rows 28 | 27, four rows 46 | 40;
+  // bf16 28 | 28, 37 | 31, 61 | 48.
   const int G = d->num_q_heads / d->num_kv_heads;
   a.mma_pairs = G <= 8 && d->rows * G <= 8 * static_cast<int64_t>(d->num_seqs) ? 8 : 16;
   if (a.mma_pairs == 8 && p.ptiles > 0) p.ptiles = ceil_div(d->rows * G, 8) * d->num_kv_heads;

@@ -62,12 +62,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
         const float w = __shfl_sync(0xffffffffu, mine, i);
-        if (w == 0.f) continue;  // a part without keys wrote no values
         sum += w;
         const float4* src = reinterpret_cast<const float4*>(op + at(s0 + WP * i) * HD);
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-          const float4 x = __ldcg(src + lane + 32 * v);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w != 0.f) x = __ldcg(src + lane + 32 * v);  // a part without keys wrote no values
           acc[v].x += w * x.x, acc[v].y += w * x.y, acc[v].z += w * x.z, acc[v].w += w * x.w;
         }
       }
@@ -99,14 +99,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
   if (lane == 0 && (WP == 1 || warp == 0) && a.lse != nullptr) a.lse[unit] = any ? ref + logf(sum) : -INFINITY;
 }
 
-// Parts from which four warps share a pair.
+// Four warps share a pair where there are at least so many parts and not enough pairs to fill the GPU with one warp each.
+// 640 pairs, 18 parts: 128 us for the call, 137 with one warp; 888 pairs, 8 parts: 23.3 us, 24.6; 4096 pairs: 105, 102.
 constexpr int kSharedParts = 8;
+constexpr int64_t kSharedPairs = 2048;
 
 template <int HD>
 cudaError_t launch_merge(const PrefixArgs& a, cudaStream_t stream) {
   const int64_t pairs = a.rows * a.num_q_heads;
   const bool overlaps = a.prefix_parts + a.own_parts > 0;
-  if (a.prefix_parts + a.own_parts >= kSharedParts)
+  if (a.prefix_parts + a.own_parts >= kSharedParts && pairs <= kSharedPairs)
     return launch_after(prefix_merge_kernel<HD, 4>, static_cast<unsigned>(pairs), 32 * kMergeWarps, 0, overlaps, stream, a);
   return launch_after(prefix_merge_kernel<HD, 1>, static_cast<unsigned>((pairs + kMergeWarps - 1) / kMergeWarps),
                       32 * kMergeWarps, 0, overlaps, stream, a);

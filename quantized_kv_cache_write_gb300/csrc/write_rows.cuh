@@ -90,18 +90,15 @@ __device__ __forceinline__ int64_t paged_slot(const WritePaging& pg, int64_t t, 
   return static_cast<int64_t>(blk) * pg.block_size + (pos - b * pg.block_size);
 }
 
-// int8 codes and scale of one head row into record `rec` of `cache` (and `scale_out`, side layout).
-// W lanes hold the row, `lane` counts them; the whole warp takes part, rows that are not stored too.
-template <bool kInline, int W = 32>
-__device__ __forceinline__ void store_int8_row(const HeadVec& hv, int lane, bool act, int head_dim, int64_t rec,
-                                               uint8_t* __restrict__ cache, float* __restrict__ scale_out,
-                                               bool stored = true) {
+// int8 codes (four to a word) and the scale of one head row. W lanes hold the row; the whole warp takes part.
+template <int W>
+__device__ __forceinline__ float int8_codes(const HeadVec& hv, uint32_t (&word)[2]) {
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(hv.x[i]));
   a = warp_max<W>(a);
   const float scale = __fdiv_rn(a, 127.0f);
-  uint32_t word[2] = {0u, 0u};
+  word[0] = word[1] = 0u;
   if (scale > 0.f) {
     // |x| <= amax and scale = fl(amax / 127) keep |x / scale| below 127.5, so the clamp never
     // acts on a finite value (a NaN value fails the bracket test and takes the clamped division)
@@ -121,6 +118,17 @@ __device__ __forceinline__ void store_int8_row(const HeadVec& hv, int lane, bool
       word[w] = __byte_perm(__byte_perm(c[4 * w], c[4 * w + 1], 0x0040), __byte_perm(c[4 * w + 2], c[4 * w + 3], 0x0040),
                             0x5410);
   }
+  return scale;
+}
+
+// int8 codes and scale of one head row into record `rec` of `cache` (and `scale_out`, side layout).
+// W lanes hold the row, `lane` counts them; the whole warp takes part, rows that are not stored too.
+template <bool kInline, int W = 32>
+__device__ __forceinline__ void store_int8_row(const HeadVec& hv, int lane, bool act, int head_dim, int64_t rec,
+                                               uint8_t* __restrict__ cache, float* __restrict__ scale_out,
+                                               bool stored = true) {
+  uint32_t word[2];
+  const float scale = int8_codes<W>(hv, word);
   if (!stored) return;
   if (kInline) {
     uint8_t* base = cache + rec * (head_dim + 4);  // head_dim codes, then the fp32 scale
@@ -136,9 +144,8 @@ __device__ __forceinline__ void store_int8_row(const HeadVec& hv, int lane, bool
   }
 }
 
-// E4M3 codes of one head row (lanes that own dims only) into record `rec` of `cache`.
-__device__ __forceinline__ void store_e4m3_row(const HeadVec& hv, int lane, int head_dim, int64_t rec, float s,
-                                               uint8_t* __restrict__ cache) {
+// E4M3 codes of eight values, four to a word.
+__device__ __forceinline__ uint2 e4m3_codes(const HeadVec& hv, float s) {
   uint32_t p[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -147,8 +154,13 @@ __device__ __forceinline__ void store_e4m3_row(const HeadVec& hv, int lane, int 
     p[j] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
   }
   // code pairs 2w, 2w + 1 into word w (low halves), one byte permute each
-  *reinterpret_cast<uint2*>(cache + rec * head_dim + lane * 8) =
-      make_uint2(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410));
+  return make_uint2(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410));
+}
+
+// E4M3 codes of one head row (lanes that own dims only) into record `rec` of `cache`.
+__device__ __forceinline__ void store_e4m3_row(const HeadVec& hv, int lane, int head_dim, int64_t rec, float s,
+                                               uint8_t* __restrict__ cache) {
+  *reinterpret_cast<uint2*>(cache + rec * head_dim + lane * 8) = e4m3_codes(hv, s);
 }
 
 }  // namespace

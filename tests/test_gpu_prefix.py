@@ -299,8 +299,7 @@ def test_seeded_random_shapes(seed):
     check(pool, b, q, act, H, scale, out, lse, what=f"seed {seed}")
 
 
-# Batches whose prefix runs on the tensor-memory tiles: several 128-key blocks per CTA, ranges that end
-# inside a tile's keys and go on in the next tile, tiles whose last pairs do not exist.
+# Batches behind long prefixes: several ranges of keys, tiles whose last pairs do not exist.
 @pytest.mark.parametrize("fmt,act", FMTS)
 @pytest.mark.parametrize("D,rows,G,H", [(128, 9, 8, 1), (128, 70, 8, 2), (256, 21, 16, 1), (128, 13, 12, 3)])
 def test_many_pairs_behind_a_long_prefix(fmt, act, D, rows, G, H):
@@ -312,6 +311,48 @@ def test_many_pairs_behind_a_long_prefix(fmt, act, D, rows, G, H):
     for _ in range(2):
         o2, l2 = call(pool, b, dev16(q, act), H, scale)
         assert torch.equal(out.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, l2)
+
+
+# The tcgen05 tiles: one SM or two per tile, tiles with few pairs, many tiles of one block, more tiles than SMs.
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("D,rows,G,H,prefix", [(128, 9, 8, 1, 33001), (128, 70, 8, 2, 2401), (256, 21, 16, 1, 4001), (128, 13, 12, 3, 5601),
+                                               (128, 40, 128, 8, 65), (256, 8, 16, 1, 10301), (128, 300, 1, 2, 4401), (256, 64, 128, 1, 161)])
+def test_tcgen05_tiles(fmt, act, D, rows, G, H, prefix):
+    assert -(-rows * G // 16) * H * prefix * D > 20 << 20  # of one byte each: K bytes that mma.sync tiles would read
+    b, pool, q, scale = case(30, fmt, act, D, H, G, prefix, [1 + 3 * (i % 4) for i in range(rows)], 1, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(pool, b, dev16(q, act), H, scale, status=status)
+    check(pool, b, q, act, H, scale, out, lse, what=f"{fmt} {act} {D} {rows}")
+    assert int(status.item()) == 0
+    o2, l2 = call(pool, b, dev16(q, act), H, scale)
+    assert torch.equal(out.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("D", [128, 256])
+def test_tcgen05_tiles_with_bad_blocks_empty_rows_and_padding(fmt, act, D):
+    b, pool, q, scale = case(31, fmt, act, D, 2, 8, 7001, [1 + i % 3 for i in range(24)], 1, 16)
+    b.prefix_blocks[5], b.prefix_blocks[100:140], b.prefix_blocks[-1] = 1 << 26, -1, -7
+    seq, ln = b.row_seq.copy(), b.row_len.copy()
+    seq[3], seq[23], ln[5], ln[6] = -1, -1, 0, 6999  # padding twice, nothing, and a length inside the prefix: bad
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = torch.full((24, 16, D), 7.0, dtype=ACT[act], device="cuda"), torch.full((24, 16), 7.0, device="cuda")
+    call(pool, b, dev16(q, act), 2, scale, row_seq=seq, row_len=ln, out=out, lse=lse, status=status)
+    assert int(status.item()) == 2
+    for r in (3, 23):
+        assert (out[r] == 7).all() and (lse[r] == 7).all()
+    for r in (5, 6):
+        assert (out[r] == 0).all() and torch.isneginf(lse[r]).all()
+    keep = np.array([r for r in range(24) if r not in (3, 5, 6, 23)])
+    slots, _ = dense.row_slots(seq[keep], ln[keep], b.prefix_blocks, b.prefix, b.table, b.block, pool.num_slots)
+    ref, rlse, wabs, big = dense.prefix_attention(q[keep], pool.K, pool.V, slots, scale, act)
+    tol, ltol = attention_bounds(ref, rlse, wabs, big, 7004, float(np.abs(pool.V[b.live]).max()), act, fmt, D)
+    assert_within(out.float().cpu().numpy()[keep], ref, tol, "out")
+    assert_within(lse.cpu().numpy()[keep], rlse, ltol, "lse")
+    # no block at all: the rows see their own keys alone
+    b.prefix_blocks[:] = -1
+    out, lse = call(pool, b, dev16(q, act), 2, scale)
+    check(pool, b, q, act, 2, scale, out, lse, what="no prefix block")
 
 
 @pytest.mark.parametrize("prefix", [20000, 20001, 40000])
