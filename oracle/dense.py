@@ -45,15 +45,14 @@ def row_slots(row_seq, row_len, prefix_blocks, prefix_len, block_table, block_si
             flagged = True
             got.append([])
             continue
-        slots = []
-        for p in range(n):
-            blk = prefix_blocks[p // block_size] if p < prefix_len else block_table[seq, p // block_size]
-            slot = int(blk) * block_size + p % block_size
-            if blk < 0 or slot >= num_slots:
-                flagged = True
-            else:
-                slots.append(slot)
-        got.append(slots)
+        p = np.arange(n)
+        blk = np.empty(n, dtype=np.int64)
+        blk[:prefix_len] = np.asarray(prefix_blocks)[p[:prefix_len] // block_size] if prefix_len else 0
+        blk[prefix_len:] = block_table[seq, p[prefix_len:] // block_size]
+        slot = blk * block_size + p % block_size
+        ok = (blk >= 0) & (slot < num_slots)
+        flagged |= not ok.all()
+        got.append(slot[ok].tolist())
     return got, flagged
 
 
@@ -70,17 +69,29 @@ def prefix_attention(q_bits: np.ndarray, K: np.ndarray, V: np.ndarray, slots, sc
     for r, sl in enumerate(slots):
         if sl is None:
             out[r], lse[r] = np.nan, np.nan
-            continue
-        if not sl:
-            continue
-        for h in range(K.shape[1]):
-            k, v = K[sl, h], V[sl, h]
-            for g in range(h * G, (h + 1) * G):
-                s = scale * (k @ q[r, g])
-                m = s.max()
-                e = np.exp(s - m)
-                w = e / e.sum()
-                out[r, g], wabs[r, g] = w @ v, w @ np.abs(v)
-                lse[r, g] = m + np.log(e.sum())
-                big[r, g] = abs(scale) * (np.abs(k) @ np.abs(q[r, g])).max()
+    rows = [r for r, sl in enumerate(slots) if sl]
+    if not rows:
+        return out, lse, wabs, big
+    # the keys that all rows see first, gathered once
+    n = min(len(slots[r]) for r in rows)
+    lists = np.array([slots[r][:n] for r in rows])
+    differ = np.flatnonzero((lists != lists[0]).any(0))
+    n = int(differ[0]) if len(differ) else n
+    for h in range(K.shape[1]):
+        heads = slice(h * G, (h + 1) * G)
+        k0, v0 = K[slots[rows[0]][:n], h], V[slots[rows[0]][:n], h]
+        ak0, av0 = np.abs(k0), np.abs(v0)
+        for r in rows:
+            k1, v1 = K[slots[r][n:], h], V[slots[r][n:], h]
+            qr = q[r, heads]
+            s = scale * np.concatenate([qr @ k0.T, qr @ k1.T], 1)
+            m = s.max(1, keepdims=True)
+            e = np.exp(s - m)
+            total = e.sum(1, keepdims=True)
+            w = e / total
+            out[r, heads] = w[:, :n] @ v0 + w[:, n:] @ v1
+            wabs[r, heads] = w[:, :n] @ av0 + w[:, n:] @ np.abs(v1)
+            lse[r, heads] = (m + np.log(total))[:, 0]
+            mags = np.concatenate([np.abs(qr) @ ak0.T, np.abs(qr) @ np.abs(k1).T], 1)
+            big[r, heads] = abs(scale) * mags.max(1)
     return out, lse, wabs, big
