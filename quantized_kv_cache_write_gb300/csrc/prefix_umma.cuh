@@ -25,8 +25,9 @@
 //   softmax: y = S ks fac (log2 units). Reference R = M + E - kShift: M follows the row's maximum lazily
 //     (raised when a logit passes it by 2^kRaise), E is a power-of-two bound on the V scales, so p vs 2^-R
 //     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. The thread's columns
-//     stay in registers from the one load of S on: their maximum is exchanged between the row's four threads,
-//     then p replaces them, and each thread's part of P goes over its own part of S. A raise rescales O after P
+//     stay in registers from the one load of S on: the row's four threads vote whether any column passes the
+//     reference by too much (exchanging the maxima in every block instead: 253 us for the call on 256 rows x 16
+//     heads behind 65536 int8 keys, 235 us with the vote), then p replaces them, and each thread's part of P goes over its own part of S. A raise rescales O after P
 //     is stored, when those registers are free (measured, 64 rows x 64 heads behind 32768 e4m3 keys: 165 thousand
 //     cycles, 265 with O rescaled before P; 256 rows x 16 heads behind 65536 int8 keys: 264 us for the call, 269
 //     with O rescaled before P and 269 with two threads per pair that read their columns twice).
@@ -78,7 +79,7 @@ struct Umma {
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
                             kRecFull = kScEmpty + 8 * kScRing, kRecEmpty = kRecFull + 8 * kRecRing,
-                            kRowSet = kRecEmpty + 8 * kRecRing, kQFull = kRowSet + 32,
+                            kQFull = kRecEmpty + 8 * kRecRing,
                             kDrain = kQFull + 8, kTmemSlot = kDrain + 8, kFlag = kTmemSlot + 4, kSmem = kFlag + 4 + 1024;
   static_assert(kSmem <= 232448, "one CTA per SM");
   // tensor memory columns: O of each tile, then two S buffers
@@ -436,7 +437,6 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         bar_init(sb + U::kRecFull + 8 * s, 1);
         bar_init(sb + U::kRecEmpty + 8 * s, 2 * kProdWarps + 1);  // a K and a V group, and scales
       }
-      for (int s = 0; s < 4; ++s) bar_init(sb + U::kRowSet + 8 * s, kParts);
       bar_init(sb + U::kQFull, U::kSoftWarps * CG);
       bar_init(sb + U::kDrain, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -459,7 +459,6 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     const int wg = warp >> 2, q4 = warp & 3, r = tid & 127;  // part of the columns, quarter of the lanes, lane
     const uint32_t tl = tb + (static_cast<uint32_t>(32 * q4) << 16);  // this warp's lanes
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;
-    const uint32_t row_bar = sb + U::kRowSet + 8 * q4;
     constexpr int HB = KB / kParts;  // this thread's columns of a block
     // this thread's part of the dims, and the place of this warp's rows of it in a query tile
     constexpr int kVec = HD / kParts / 8;
@@ -467,17 +466,26 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     const uint32_t own_part = sb + U::kQ + (d0 >> 6) * (kTileM * 128) + 32 * q4 * 128;
     uint32_t jb = 0, meet = 0;  // blocks so far; exchanges so far of the row's threads
     bool ok = true;
+    // Whether any thread of the kParts warps that share rows says so. They meet at a hardware barrier, which has no time
+    // limit: so none of them ever leaves alone. One whose own wait ran out (!ok) goes on without its work to the next
+    // vote or exchange, where all of them learn it and leave together.
+    auto vote = [&](bool x) -> bool {
+      uint32_t any;
+      asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                   : "=r"(any)
+                   : "r"(static_cast<uint32_t>(x)), "r"(1 + q4), "n"(32 * kParts)
+                   : "memory");
+      return any != 0u;
+    };
     // the threads of each of the warp's rows leave a value, and take all of them in the same order
     auto exchange = [&](float mine, float (&all)[kParts]) -> bool {
       const uint32_t at = sb + U::kRow + 4 * ((meet & 1) * kParts * kTileM + r);
       sts32(at + 4 * wg * kTileM, __float_as_uint(mine));
-      __syncwarp();
-      if (lane == 0) bar_arrive(row_bar);
-      const bool met = __all_sync(0xffffffffu, bar_wait(row_bar, meet & 1, flag));
+      ok = !vote(!ok);
 #pragma unroll
       for (int i = 0; i < kParts; ++i) all[i] = __uint_as_float(lds32(at + 4 * i * kTileM));
       ++meet;
-      return met;
+      return ok;
     };
     // P V of sub-iteration n (block, tile)
     auto await_pv = [&](uint32_t n) -> bool {
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       tmem_fence_after_sync();
       return done;
     };
-    while (ok && seg.next(a)) {
+    while (seg.next(a)) {
       const int h = seg.tile / a.umma_ptiles;
       const uint32_t flat0 = (static_cast<uint32_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
       // state of the tile at hand; with two tiles the other one's waits in the second element
@@ -541,7 +549,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
             for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
           }
           float all[kParts];
-          if (!(ok = exchange(__uint_as_float(mb), all))) break;
+          if (!exchange(__uint_as_float(mb), all)) break;
 #pragma unroll
           for (int i = 0; i < kParts; ++i) mb = max(mb, __float_as_uint(all[i]));
           const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
@@ -579,12 +587,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         const int t = NT == 2 ? i & 1 : 0;
         const uint32_t blk = jb + i / NT, n = jb * NT + i, b = n & 1;
         const uint32_t sc = sb + U::kSc + (blk & (kScRing - 1)) * U::kScStage;
-        if (t == 0) ok = bar_wait(sb + U::kScFull + 8 * (blk & (kScRing - 1)), (blk / kScRing) & 1, flag);
+        if (t == 0) ok = ok && bar_wait(sb + U::kScFull + 8 * (blk & (kScRing - 1)), (blk / kScRing) & 1, flag);
         ok = ok && bar_wait(sb + U::kSFull + 8 * b, (n >> 1) & 1, flag);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         tmem_fence_after_sync();
-        if (warp_in[0]) {
+        if (warp_in[0]) {  // the same in the kParts warps
           const uint4 mw = lds128(sc + U::kScMask);
           const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
           const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0)) + wg * (HB / 4);
@@ -601,18 +608,19 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           for (int k = 0; k < HB; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           float tm = mx == -INFINITY ? mx : mx * fac[0];
-          if (!(ok = exchange(tm, all))) break;
-          tm = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
           int En = E[0];
           if (F::kInt8) {
             const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
             if (e > En) En = e + U::kHeadroom;
           }
-          const bool up_m = tm > M[0] + U::kRaise;  // the same for the row's threads
-          const bool raise = __any_sync(0xffffffffu, up_m || En != E[0]);
+          // most blocks need no more than the answer that no thread's columns pass the reference by too much
+          const bool raise = vote(!ok || tm > M[0] + U::kRaise || En != E[0]);
           float f = 1.f;
           if (raise) {
             // ---- raise the reference: the sums and O so far go down by f
+            if (!exchange(tm, all)) break;
+            tm = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+            const bool up_m = tm > M[0] + U::kRaise;  // the same for the row's threads
             const float Mn = up_m ? tm : M[0];
             const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - U::kShift;
             if (M[0] != -INFINITY) f = fast_exp2(R[0] - Rn);
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           if (raise && i >= NT) {
             // O of the blocks before, once their P V is done (with two tiles S was issued after it); last, when the
             // columns' registers are free for a part of the dims at once
-            if (NT == 1 && !(ok = await_pv(n - 1))) break;
+            if (NT == 1) ok = await_pv(n - 1);
             const uint64_t f2 = f2pack(f, f);
             const uint32_t to = tl + U::kO + t * HD + wg * (HD / kParts);
 #pragma unroll 1
@@ -658,21 +666,20 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         }
         tmem_fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
+        if (ok && lane == 0) {
           lead_arrive<CG>(sb + U::kPFull + 8 * b);
           if (t == NT - 1) bar_arrive(sb + U::kScEmpty + 8 * (blk & (kScRing - 1)));
         }
         other_tile();
       }
       jb += seg.b1 - seg.b0;
-      if (!ok) break;
       // ---- the segment's partial results
 #pragma unroll 1
       for (int t = 0; t < NT; ++t, other_tile()) {
-        if (!(ok = await_pv((jb - 1) * NT + t))) break;
+        ok = ok && await_pv((jb - 1) * NT + t);
         if (!warp_in[0]) continue;
         float all[kParts];
-        if (!(ok = exchange(l[0], all))) break;
+        if (!exchange(l[0], all)) break;
         const uint32_t flat = flat0 + t * CG * kTileM;
         const bool in = flat < pairs;
         const uint32_t row = in ? flat / G : 0;
@@ -711,6 +718,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         }
       }
       tmem_fence_before_sync();  // ordered before the next segment's first arrival
+      if (vote(!ok)) break;
     }
   } else if (warp < U::kRecWarp) {
     // ================================================================ producers
