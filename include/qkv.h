@@ -651,7 +651,8 @@ qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
  *   workspace     device scratch of workspace_bytes, 16 B-aligned; its contents need not be set.
  *                 Too small a workspace is QKV_ERR_ARG. Calls that overlap on the GPU -- on two
  *                 streams, or replays of two captured graphs -- must not share one.
- *   rows * num_q_heads at most 2^31 - 1, num_slots * num_kv_heads too.
+ *   rows * num_q_heads at most 2^31 - 1 (else QKV_ERR_ARG), num_slots * num_kv_heads too, and fewer than 2^31 pieces
+ *                 of 128 (row, head) pairs x 64 keys of the prefix (else QKV_ERR_UNSUPPORTED).
  * Results do not depend on other rows of the batch, up to rounding; calls with the same arguments
  * on the same device give the same bits.
  *

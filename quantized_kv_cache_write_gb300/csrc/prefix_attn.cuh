@@ -125,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sFac[NP], sM[kWarps][NP], sL[kWarps][NP];
-  __shared__ int sEu[kWarps];
+  __shared__ float sW[kWarps][NP], sInv[NP];
+  __shared__ int64_t sAt[NP];
+  __shared__ int sEu[kWarps][NP];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, hn = lane >> 2;
   const int H = a.num_kv_heads, G = a.num_q_heads / H;
   let_next_start();
@@ -166,22 +168,6 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     const uint32_t flat = tile * NP + lane, row = flat / static_cast<uint32_t>(G);  // below 2^31 + 32
     my_g = static_cast<int>(flat - row * G);
     if (lane < NP && row < a.rows) my_row = static_cast<int>(row), my_own = 0;
-  }
-
-  // ---------------- query rows into registers, each warp a quarter of the pairs
-  constexpr int kPer = HD / 32, kQPairs = NP / kWarps;  // dims per lane, pairs per warp
-  uint32_t qw[kQPairs][kPer / 2];
-#pragma unroll
-  for (int i = 0; i < kQPairs; ++i) {
-    const int row = __shfl_sync(0xffffffffu, my_row, warp * kQPairs + i), g = __shfl_sync(0xffffffffu, my_g, warp * kQPairs + i);
-    const uint16_t* src = a.q + static_cast<int64_t>(max(row, 0)) * a.q_stride + static_cast<int64_t>(row >= 0 ? h * G + g : 0) * HD;
-    if (kPer == 8) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-      qw[i][0] = v.x, qw[i][1] = v.y, qw[i][kPer / 2 - 2] = v.z, qw[i][kPer / 2 - 1] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + lane);
-      qw[i][0] = v.x, qw[i][1] = v.y;
-    }
   }
 
   // ---------------- its keys: positions [k0, k1) in tiles from a0 (a multiple of TK) on
@@ -295,10 +281,27 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     cp_async_commit();
   };
 
-  int blk = load_blk(0);
+  int blk = load_blk(0), next0 = load_blk(1);  // before the query's loads: the copies wait for them
+
+  // ---------------- query rows into registers, each warp a quarter of the pairs
+  constexpr int kPer = HD / 32, kQPairs = NP / kWarps;  // dims per lane, pairs per warp
+  uint32_t qw[kQPairs][kPer / 2];
+#pragma unroll
+  for (int i = 0; i < kQPairs; ++i) {
+    const int row = __shfl_sync(0xffffffffu, my_row, warp * kQPairs + i), g = __shfl_sync(0xffffffffu, my_g, warp * kQPairs + i);
+    const uint16_t* src = a.q + static_cast<int64_t>(max(row, 0)) * a.q_stride + static_cast<int64_t>(row >= 0 ? h * G + g : 0) * HD;
+    if (kPer == 8) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+      qw[i][0] = v.x, qw[i][1] = v.y, qw[i][kPer / 2 - 2] = v.z, qw[i][kPer / 2 - 1] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+      qw[i][0] = v.x, qw[i][1] = v.y;
+    }
+  }
+
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) {
-    const int next = load_blk(i + 1);
+    const int next = i == 0 ? next0 : load_blk(i + 1);
     issue(i, blk);
     blk = next;
   }
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[t][k] = 0.f;
   float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  int eu = -120;  // int8: the accumulators hold values times 2^-eu
+  int eu[2] = {-120, -120};  // int8: a pair's accumulators hold values times 2^-eu
   const int pr[2] = {kWide ? hn : 2 * c, kWide ? hn + 8 : 2 * c + 1};  // the lane's two pairs
   const float fac[2] = {sFac[pr[0]], sFac[pr[1]]};
   // first position past each of the lane's two rows
@@ -446,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 
     // ---- softmax step
     float vs[2 * NH][KL];  // int8: V scales of the lane's keys
-    float vmax = 0.f;
+    float vmax[2] = {0.f, 0.f};  // the largest that a pair sees: what lies behind its row's end is not its own
 #pragma unroll
     for (int g = 0; g < NH; ++g) {
       float ks[2][KL];
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
           for (int k = 0; k < KL; ++k) {  // key 2 (2c + k) + n, or 2 hn + n
             ks[n][k] = __uint_as_float(kw[2 * k + n]);
             vs[2 * g + n][k] = __uint_as_float(vw[2 * k + n]);
-            vmax = fmaxf(vmax, fabsf(vs[2 * g + n][k]));
+            vmax[0] = fmaxf(vmax[0], fabsf(vs[2 * g + n][k]));
           }
       }
 #pragma unroll
@@ -477,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 #pragma unroll
           for (int p = 0; p < 2; ++p) S(2 * g + n, p, k) *= F::kInt8 ? ks[n][k] * fac[p] : fac[p];
     }
+    vmax[1] = vmax[0];
     if (!whole) {
+      vmax[0] = vmax[1] = 0.f;
 #pragma unroll
       for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
@@ -485,8 +490,10 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
           const int key = key_at(n, k);
           const bool valid = (mask >> key) & 1;
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
+          for (int p = 0; p < 2; ++p) {
             if (!valid || base + key >= end[p]) S(n, p, k) = -INFINITY;
+            else if (F::kInt8) vmax[p] = fmaxf(vmax[p], fabsf(vs[n][k]));
+          }
         }
     }
     float tm[2];
@@ -503,18 +510,23 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     for (int off = kWide ? 1 : 4; off <= (kWide ? 2 : 16); off <<= 1) {
       tm[0] = fmaxf(tm[0], __shfl_xor_sync(0xffffffffu, tm[0], off));
       tm[1] = fmaxf(tm[1], __shfl_xor_sync(0xffffffffu, tm[1], off));
-      if (F::kInt8) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+      if (F::kInt8) {
+        vmax[0] = fmaxf(vmax[0], __shfl_xor_sync(0xffffffffu, vmax[0], off));
+        vmax[1] = whole ? vmax[0] : fmaxf(vmax[1], __shfl_xor_sync(0xffffffffu, vmax[1], off));
+      }
     }
-    int eu_new = eu;
+    int eu_new[2] = {eu[0], eu[1]};
     if (F::kInt8) {
-      const int e = min(120, static_cast<int>(__float_as_uint(vmax) >> 23) - 126);  // vmax < 2^e
-      if (e > eu) eu_new = min(120, e + kEuHeadroom);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int e = min(120, static_cast<int>(__float_as_uint(vmax[p]) >> 23) - 126);  // vmax < 2^e
+        if (e > eu[p]) eu_new[p] = min(120, e + kEuHeadroom);
+      }
     }
     // a first finite logit has no reference to be compared with: M = -inf lies below any
     const bool raise0 = tm[0] > M[0] + kTau, raise1 = tm[1] > M[1] + kTau;
-    if (__any_sync(0xffffffffu, raise0 || raise1 || eu_new != eu)) {
+    if (__any_sync(0xffffffffu, raise0 || raise1 || eu_new[0] != eu[0] || eu_new[1] != eu[1])) {
       float f[2];
-      const float down = F::kInt8 ? pow2f(max(eu - eu_new, -126)) : 1.f;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const bool up = p ? raise1 : raise0;
@@ -522,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         const float al = (up && M[p] != -INFINITY) ? fast_exp2(M[p] - m) : 1.f;
         M[p] = m;
         l[p] *= al;
-        f[p] = al * down;
+        f[p] = F::kInt8 ? al * pow2f(max(eu[p] - eu_new[p], -126)) : al;
+        eu[p] = eu_new[p];
       }
 #pragma unroll
       for (int t = 0; t < kOTiles; ++t) {
@@ -531,12 +544,11 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         o[t][2] *= f[kWide ? 1 : 0];
         o[t][3] *= f[1];
       }
-      eu = eu_new;
     }
-    const float vdown = F::kInt8 ? pow2f(-eu) : 1.f;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const float ref = M[p] == -INFINITY ? 0.f : M[p] - (F::kBf16 ? 0.f : kPShift);
+      const float vdown = F::kInt8 ? pow2f(-eu[p]) : 1.f;
 #pragma unroll
       for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
@@ -661,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     if ((kWide ? c : hn) == 0) {
       sM[warp][pr[p]] = M[p];
       sL[warp][pr[p]] = l[p];
+      if (F::kInt8) sEu[warp][pr[p]] = eu[p];
     }
   }
-  if (lane == 0) sEu[warp] = eu;
   __syncthreads();  // every ring is drained
   float* sO = reinterpret_cast<float*>(smem);
   if (my > 0) {
@@ -678,53 +690,62 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   }
   __syncthreads();
   const bool direct = a.o_part == nullptr;  // the only part: its result is the row's
-#pragma unroll 1
-  for (int i = warp; i < NP; i += kWarps) {
-    const int row = __shfl_sync(0xffffffffu, my_row, i), g = __shfl_sync(0xffffffffu, my_g, i);
-    if (row < 0) continue;
-    const int head = h * G + g;
-    bool empty = false;
-    if (direct) {
-      const int state = row_state(a, static_cast<int64_t>(row), lane == 0 && head == 0);
-      if (state == kPadRow) continue;
-      empty = state == kEmptyRow;
-    }
-    float m = -INFINITY;
+  // one thread per pair: the warps' weights, log-sum-exp and where the result goes
+  if (tid < NP) {
+    const int head = h * G + my_g;
+    int64_t at = -1;
+    if (my_row >= 0) {
+      const int state = direct ? row_state(a, static_cast<int64_t>(my_row), head == 0) : 0;
+      const int64_t pair = static_cast<int64_t>(my_row) * a.num_q_heads + head;
+      float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sM[w][i]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float f[kWarps], sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sM[w][lane]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float al = fast_exp2(sM[w][i] - ref);  // 2^-inf = 0 for a warp without keys
-      sum += al * sL[w][i];
-      f[w] = F::kInt8 ? al * pow2f(sEu[w]) : al;
+      for (int w = 0; w < kWarps; ++w) {
+        const float al = fast_exp2(sM[w][lane] - ref);  // 2^-inf = 0 for a warp without keys
+        sum += al * sL[w][lane];
+        sW[w][lane] = F::kInt8 ? al * pow2f(sEu[w][lane]) : al;
+      }
+      const bool any = state != kEmptyRow && (m != -INFINITY || sum != sum);
+      sInv[lane] = any ? (direct && FMT == QKV_E4M3 ? a.v_scale_layer : 1.f) / sum : 0.f;
+      if (state != kPadRow) {
+        const int64_t part_at = static_cast<int64_t>(own_part ? a.prefix_parts + part : part) * a.rows * a.num_q_heads + pair;
+        const float v = any ? (m - (F::kBf16 ? 0.f : kPShift) + log2f(sum)) * kLn2 : -INFINITY;
+        if (!direct) a.lse_part[part_at] = v;
+        else if (a.lse != nullptr) a.lse[pair] = v;
+        if (direct) at = pair;
+        else if (any) at = part_at;  // a part without keys leaves no values
+        if (!any) {
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) sW[w][lane] = 0.f;
+        }
+      }
     }
-    const bool any = !empty && (m != -INFINITY || sum != sum);
-    const float inv = any ? (direct && FMT == QKV_E4M3 ? a.v_scale_layer : 1.f) / sum : 0.f;
-    const int64_t at = static_cast<int64_t>(row) * a.num_q_heads + head;
-    const int64_t part_at = (static_cast<int64_t>(own_part ? a.prefix_parts + part : part) * a.rows) * a.num_q_heads + at;
-    if (lane == 0) {
-      const float v = any ? (m - (F::kBf16 ? 0.f : kPShift) + log2f(sum)) * kLn2 : -INFINITY;
-      if (!direct) a.lse_part[part_at] = v;
-      else if (a.lse != nullptr) a.lse[at] = v;
-    }
-    if (!any && !direct) continue;
+    sAt[lane] = at;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i0 = 0; i0 < NP; i0 += kWarps) {
+    const int i = i0 + warp;
+    const int64_t at = sAt[i];
+    const float inv = sInv[i];
 #pragma unroll
     for (int d = 4 * lane; d < HD; d += 128) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (f[w] == 0.f) continue;  // a warp without keys left no values
-        const float4 x = *reinterpret_cast<const float4*>(sO + (w * NP + i) * GM::kORow + d);
-        acc.x += f[w] * x.x, acc.y += f[w] * x.y, acc.z += f[w] * x.z, acc.w += f[w] * x.w;
+        const float f = sW[w][i];
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (f != 0.f && at >= 0) x = *reinterpret_cast<const float4*>(sO + (w * NP + i) * GM::kORow + d);  // else none there
+        acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
       }
       acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-      if (direct) {
+      if (at >= 0 && direct)
         *reinterpret_cast<uint2*>(a.out + at * HD + d) = make_uint2(round2(a.q_f16, acc.x, acc.y), round2(a.q_f16, acc.z, acc.w));
-      } else {
-        *reinterpret_cast<float4*>(a.o_part + part_at * HD + d) = acc;
-      }
+      else if (at >= 0)
+        *reinterpret_cast<float4*>(a.o_part + at * HD + d) = acc;
     }
   }
   // the prefix's launch is over before this one is, so what waits for this one need not wait for both

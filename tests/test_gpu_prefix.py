@@ -299,6 +299,30 @@ def test_seeded_random_shapes(seed):
     check(pool, b, q, act, H, scale, out, lse, what=f"seed {seed}")
 
 
+@pytest.mark.parametrize("fmt", ["int8_side", "int8_inline"])
+@pytest.mark.parametrize("leftover", [float("inf"), 3e38, 1e30, -1e30, float("nan")])
+@pytest.mark.parametrize("spare", [0, 30])
+def test_a_huge_scale_behind_a_shorter_row_of_the_tile(fmt, leftover, spare):
+    """The V scale of the key that only a sequence's last draft row sees bounds that row's weights alone: the others
+    keep theirs (with 30 unused sequences in the table: tiles of eight pairs)."""
+    b, pool, q, scale = case(17, fmt, "bf16", 128, 1, 4, 40, [7, 30, 4], 4, 16)
+    b.table = np.concatenate([b.table, np.full((spare, b.table.shape[1]), -1, dtype=np.int32)])
+    for i in range(3):
+        n = int(b.row_len[4 * i + 3])
+        slot = int(b.table[i, (n - 1) // 16]) * 16 + (n - 1) % 16
+        if fmt == "int8_side":
+            pool.kw["v_scale_tok"][slot] = leftover
+        else:
+            pool.cache[1].view(torch.uint8)[slot, :, 128:] = torch.tensor(np.array([leftover], np.float32).view(np.uint8)).cuda()
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, scale)
+    first = np.arange(12) % 4 != 3
+    slots, _ = dense.row_slots(b.row_seq[first], b.row_len[first], b.prefix_blocks, b.prefix, b.table, b.block, pool.num_slots)
+    ref, rlse, wabs, big = dense.prefix_attention(q[first], pool.K, pool.V, slots, scale)
+    tol, ltol = attention_bounds(ref, rlse, wabs, big, 70, float(np.abs(pool.V[b.live]).max()), "bf16", fmt, 128)
+    assert_within(out.float().cpu().numpy()[first], ref, tol, "rows before the leftovers")
+    assert_within(lse.cpu().numpy()[first], rlse, ltol, "lse before the leftovers")
+
+
 # Batches behind long prefixes: several ranges of keys, tiles whose last pairs do not exist.
 @pytest.mark.parametrize("fmt,act", FMTS)
 @pytest.mark.parametrize("D,rows,G,H", [(128, 9, 8, 1), (128, 70, 8, 2), (256, 21, 16, 1), (128, 13, 12, 3)])
