@@ -562,17 +562,19 @@ int sm_count() {
   return n;
 }
 
-// K bytes that tiles of 16 pairs would read above which the prefix runs on tcgen05: its tiles read them once per 128
-// pairs or more, but a call costs some 6 us before the first key and after the last. In us, mma.sync | tcgen05: one KV
-// head of 256, int8, 16 pairs of 65536 keys (17 MB) 28 | 35, 24 pairs (34 MB) 36 | 34, 128 pairs of 8192 (17 MB)
-// 22 | 26; 8 heads of 128, e4m3, 8192 keys, 32 pairs (17 MB) 19.4 | 18.8, 48 pairs (25 MB) 29 | 19; 4 heads of 128, bf16, 8192
-// keys, 32 pairs (17 MB) 17.0 | 18.5, 48 pairs (25 MB) 20.3 | 19.5, 64 pairs (34 MB) 30 | 19.
+// K bytes that tiles of 16 pairs would read above which the prefix runs on tcgen05: its tiles read them once per
+// 128 pairs or more, but a call costs some 6 us before the first key and after the last. In us, mma.sync |
+// tcgen05: one KV head of 256, int8, 16 pairs of 65536 keys (17 MB) 28 | 35, 24 pairs (34 MB) 36 | 34, 128 pairs
+// of 8192 (17 MB) 22 | 26; 8 heads of 128, e4m3, 8192 keys, 32 pairs (17 MB) 19.4 | 18.8, 48 pairs (25 MB) 29 |
+// 19; 4 heads of 128, bf16, 8192 keys, 32 pairs (17 MB) 17.0 | 18.5, 48 pairs (25 MB) 20.3 | 19.5, 64 pairs (34
+// MB) 30 | 19.
 constexpr int64_t kUmmaMinBytes = 20 << 20;
 
-// How a shared-prefix call is cut into key ranges: up to 16 CTAs per SM, so that ragged rows balance (64 rows x 64 heads
-// of 0 to 8192 e4m3 keys: 118 us, 121 with 8, 130 with 4), but none with fewer than 512 keys, since a CTA's start and its
-// join cost as much as about 300 (8 x 5 drafts behind 126976 int8 keys: 131 us, 135 with 256, 144 with 1024; one row of
-// 65536: 31 us, 40, 37), and 256 while those do not fill the SMs once (one row of 8192: 19 us, 23 with 512, 33 with 1024).
+// How a shared-prefix call is cut into key ranges: up to 16 CTAs per SM, so that ragged rows balance (64 rows x 64
+// heads of 0 to 8192 e4m3 keys: 118 us, 121 with 8, 130 with 4), but none with fewer than 512 keys, since a CTA's
+// start and its join cost as much as about 300 (8 x 5 drafts behind 126976 int8 keys: 131 us, 135 with 256, 144
+// with 1024; one row of 65536: 31 us, 40, 37), and 256 while those do not fill the SMs once (one row of 8192: 19
+// us, 23 with 512, 33 with 1024).
 struct PrefixPlan {
   int prefix_parts, own_parts, prefix_chunk;
   int umma_cg, umma_pairs, umma_ptiles;
@@ -622,9 +624,10 @@ qkv_status plan_prefix(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv
   p->umma_blocks = 0, p->umma_teams = 0, p->umma_share = 0, p->umma_extra = 0;
   const int64_t row_bytes = fmt == QKV_BF16 || fmt == QKV_F16 ? 2 * head_dim : head_dim;
   if (prefix_len > 0 && p->ptiles > kUmmaMinBytes / (prefix_len * row_bytes)) {
-    // Two SMs per team where their tiles (512 pairs of 128-wide heads, 256 of 256-wide ones) are at least half full. In us, one
-    // SM | two: 8 heads of 128, e4m3, 65536 keys, 256 pairs 99 | 118, 512 pairs 180 | 145; 4 heads of 128, bf16, 256 pairs
-    // 64.6 | 65.5, 512 pairs 113 | 81; one head of 256, int8, 128 pairs 40 | 38, 192 pairs 44 | 40, 256 pairs 46 | 42.
+    // Two SMs per team where their tiles (512 pairs of 128-wide heads, 256 of 256-wide ones) are at least half
+    // full. In us, one SM | two: 8 heads of 128, e4m3, 65536 keys, 256 pairs 99 | 118, 512 pairs 180 | 145; 4
+    // heads of 128, bf16, 256 pairs 64.6 | 65.5, 512 pairs 113 | 81; one head of 256, int8, 128 pairs 40 | 38, 192
+    // pairs 44 | 40, 256 pairs 46 | 42.
     p->umma_cg = rows * G > (head_dim == 128 ? 256 : 128) ? 2 : 1;
     p->umma_pairs = p->umma_cg == 1 ? 128 : head_dim == 128 ? 512 : 256;
     const int keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
@@ -750,9 +753,9 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.prefix_parts = p.prefix_parts;
   a.own_parts = p.own_parts;
   a.prefix_chunk = p.prefix_chunk;
-  // Tiles of 8 pairs where a sequence's rows bring no more than that on average: half of a 16-pair tile would be empty. In us, 8 |
-  // 16: e4m3, 32 sequences of 1400 keys, 4 heads of 128, groups of 8, one row each 17 | 23, two rows 28 | 27, four rows 46 | 40;
-  // bf16 28 | 28, 37 | 31, 61 | 48.
+  // Tiles of 8 pairs where a sequence's rows bring no more than that on average: half of a 16-pair tile would be
+  // empty. In us, 8 | 16: e4m3, 32 sequences of 1400 keys, 4 heads of 128, groups of 8, one row each 17 | 23, two
+  // rows 28 | 27, four rows 46 | 40; bf16 28 | 28, 37 | 31, 61 | 48.
   const int G = d->num_q_heads / d->num_kv_heads;
   a.mma_pairs = G <= 8 && d->rows * G <= 8 * static_cast<int64_t>(d->num_seqs) ? 8 : 16;
   if (a.mma_pairs == 8 && p.ptiles > 0) p.ptiles = ceil_div(d->rows * G, 8) * d->num_kv_heads;

@@ -7,14 +7,18 @@
 // every stored byte -- is the one a plain fp32 program gives. q' is rounded once to q's type; K' goes
 // through the writes' own quantisers (write_rows.cuh), V unrotated.
 //
-// A row (one head of q, K or V) is held by head_dim / 8 lanes, two runs of four dims each: dims 4j of the rotated
-// part's first half and of its second, which are partners, so that a lane rotates what it holds with four cosines and
-// four sines and no exchange (adjacent pairs, and dims past the rotated part: four dims of each half of what is left). A warp
-// takes kRows rows of one token for each of its lane groups, so the token's cos and sin are loaded once into registers
-// for all of them; the row loads are issued before the position's dependent loads return.
-// Bound by memory: 2 B in and 2 B out per q value, 2 B in and a record out per K and V value. Measured: 8192 tokens x
-// 18 heads of 256 into an int8 pool 32.5 us (4.8 TB/s), 16384 x 48 heads of 128 into a bf16 pool 74 us (5.5 TB/s); with 16 B
-// per lane and partners exchanged by shuffles 37.6 and 92 us (twice the cosines and sines per lane, twice the widening).
+// A row (one head of q, K or V) is held by head_dim / 8 lanes, two runs of four dims each: dims 4j of
+// the rotated part's first half and of its second, which are partners, so that a lane rotates what it
+// holds with four cosines and four sines and no exchange (adjacent pairs, and dims past the rotated
+// part: four dims of each half of what is left). A warp takes kRows rows of one token for each of its
+// lane groups, so the token's cos and sin are loaded once into registers for all of them; the row
+// loads are issued before the position's dependent loads return.
+//
+// Bound by memory: 2 B in and 2 B out per q value, 2 B in and a record out per K and V value. Measured:
+// 8192 tokens x 18 heads of 256 into an int8 pool 32.5 us (4.8 TB/s), 16384 x 48 heads of 128 into a
+// bf16 pool 74 us (5.5 TB/s); with 16 B per lane and partners exchanged by shuffles 37.6 and 92 us
+// (twice the cosines and sines per lane, twice the widening). Issue slots are 60 % busy there and warps
+// wait for the rows' loads.
 #include "write_rows.cuh"
 
 namespace qkv {
@@ -36,8 +40,8 @@ template <bool F16>
 __device__ __forceinline__ uint2 round4(const float* x) {
   return F16 ? make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3])) : make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
 }
-// (a, b) of a pair by its cosine and sine, every product and sum rounded. Scalar: packed pairs of products and sums are
-// fused by the compiler, with one rounding less (seen as changed bytes).
+// (a, b) of a pair by its cosine and sine, every product and sum rounded. Scalar: packed pairs of products and
+// sums are fused by the compiler, with one rounding less (seen as changed bytes).
 __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   const float x = a;
   a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(b, s));
@@ -166,8 +170,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const Appen
 }
 
 // Rows per lane group: one while the launch is too small to fill the GPU (each row's loads then start in a warp of
-// their own), four above. Tokens x (16 + 2 heads of 256), int8, in us with one | four: 64: 3.0 | 3.7, 256 (4608 warps with
-// one): 3.4 | 3.9, 512 (9216): 4.3 | 4.2, 8192: 42 | 32.
+// their own), four above. Tokens x (16 + 2 heads of 256), int8, in us with one | four: 64: 3.0 | 3.7, 256 (4608
+// warps with one): 3.4 | 3.9, 512 (9216): 4.3 | 4.2, 8192: 42 | 32.
 constexpr int64_t kSmallWarps = 8192;
 
 template <int FMT, bool F16, int HD, bool PAIRS>

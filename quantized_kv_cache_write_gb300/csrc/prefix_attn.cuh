@@ -18,6 +18,13 @@
 // scale and a power of two) is rounded to the 16-bit operand type once: relative 2^-12 (fp16) or
 // 2^-9 (bf16), independent from key to key, so an output has about the rounding error of its own
 // 16-bit type or less.
+//
+// Measured: 64 rows x 64 heads of 128 over 0 to 8192 e4m3 keys of their own, no prefix (539 MB), 110 us in this
+// kernel (4.9 TB/s); 128 rows x 32 heads over 16 to 2048 bf16 keys (270 MB) 63 us (4.3 TB/s). Between its start and
+// its join a CTA streams at more than its share of the memory rate; the block list, table and query that it waits for
+// before the first key, and the join, are 40 to 60 % of a short range's time and are hidden by the SM's two or
+// three other CTAs only in part. Deeper rings with fewer CTAs, shallower ones with more, and longer ranges all
+// measured the same or slower.
 #pragma once
 
 #include <atomic>
@@ -103,7 +110,8 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 // out (16-bit) of one value pair
 __device__ __forceinline__ uint32_t round2(bool f16, float x, float y) { return f16 ? pack_half2(x, y) : pack_bf162(x, y); }
 
-// The 8 x 8 matrix of 16-bit values that the warp holds (row lane / 4, columns 2 (lane % 4) and the next), transposed.
+// The 8 x 8 matrix of 16-bit values that the warp holds (row lane / 4, columns 2 (lane % 4) and the next),
+// transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
@@ -356,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   }
   __syncthreads();
 
-  // kWide: pairs hn, hn + 8 (rows) by dims 8t + 2c, 2c + 1 (columns) of tile t; else dims 16t + hn, hn + 8 by pairs 2c, 2c + 1
+  // kWide: pairs hn, hn + 8 (rows) by dims 8t + 2c, 2c + 1 (columns) of tile t; else dims 16t + hn, hn + 8 by
+  // pairs 2c, 2c + 1
   constexpr int kOTiles = kWide ? HD / 8 : HD / 16;
   float o[kOTiles][4];
 #pragma unroll
@@ -399,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     // every key wanted by every row: no masks
     const bool whole = mask == kAll && base + TK <= own_min;
 
-    // ---- logits of 2 NH groups of eight keys. kWide: N-tiles, s[n][2p + k]: pair p, key 2c + k of the group; else halves
-    // of M-tiles, s[n / 2][2 (n % 2) + p]: key hn of the group, pair p
+    // ---- logits of 2 NH groups of eight keys. kWide: N-tiles, s[n][2p + k]: pair p, key 2c + k of the group;
+    // else halves of M-tiles, s[n / 2][2 (n % 2) + p]: key hn of the group, pair p
     float s[KL * NH][4];
 #pragma unroll
     for (int n = 0; n < KL * NH; ++n)

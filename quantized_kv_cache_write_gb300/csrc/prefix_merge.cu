@@ -99,8 +99,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
   if (lane == 0 && (WP == 1 || warp == 0) && a.lse != nullptr) a.lse[unit] = any ? ref + logf(sum) : -INFINITY;
 }
 
-// Four warps share a pair where there are at least so many parts and not enough pairs to fill the GPU with one warp each.
-// 640 pairs, 18 parts: 128 us for the call, 137 with one warp; 888 pairs, 8 parts: 23.3 us, 24.6; 4096 pairs: 105, 102.
+// Four warps share a pair where there are at least so many parts and not enough pairs to fill the GPU with one
+// warp each. 640 pairs, 18 parts: 128 us for the call, 137 with one warp; 888 pairs, 8 parts: 23.3 us, 24.6; 4096
+// pairs: 105, 102.
 constexpr int kSharedParts = 8;
 constexpr int64_t kSharedPairs = 2048;
 

@@ -25,12 +25,12 @@
 //   softmax: y = S ks fac (log2 units). Reference R = M + E - kShift: M follows the row's maximum lazily
 //     (raised when a logit passes it by 2^kRaise), E is a power-of-two bound on the V scales, so p vs 2^-R
 //     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. The thread's columns
-//     stay in registers from the one load of S on: the row's four threads vote whether any column passes the
-//     reference by too much (exchanging the maxima in every block instead: 253 us for the call on 256 rows x 16
-//     heads behind 65536 int8 keys, 235 us with the vote), then p replaces them, and each thread's part of P goes over its own part of S. A raise rescales O after P
-//     is stored, when those registers are free (measured, 64 rows x 64 heads behind 32768 e4m3 keys: 165 thousand
-//     cycles, 265 with O rescaled before P; 256 rows x 16 heads behind 65536 int8 keys: 264 us for the call, 269
-//     with O rescaled before P and 269 with two threads per pair that read their columns twice).
+//     stay in registers from the one load of S on; the row's four threads vote whether any column passes the
+//     reference by too much; then p replaces the columns, and each thread's part of P goes over its own part of S.
+//     A raise rescales O last, after P is stored, when those registers are free. Measured, 256 rows x 16 heads
+//     behind 65536 int8 keys, us for the call: 235; 253 with the maxima exchanged in every block instead of the
+//     vote; 269 with O rescaled before P besides. 64 rows x 64 heads behind 32768 e4m3 keys, thousands of cycles:
+//     142; 165 with the maxima exchanged; 265 with O rescaled before P besides.
 // Arithmetic as in prefix_attn.cuh: exact codes, logits and sums in fp32, p rounded once.
 //
 // The roles' loops are kept rolled: five of them run at once on each scheduler, and fully unrolled they
@@ -60,10 +60,10 @@ struct Umma {
   static constexpr int KB = umma_block_keys(HD, CG);
   static constexpr int kSoftWarps = 4 * kParts, kRecWarp = kSoftWarps + 2 * kProdWarps, kScWarp = kRecWarp + 1, kMmaWarp = kScWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  // The softmax's window: a logit may pass its reference by 2^kRaise, and p there is 2^kShift (int8: times a V scale
-  // over its bound, which sits up to 2^kHeadroom above the largest seen). fp16 operands stay below 2^15, and
-  // a p below fp16's normal range is off by at most 2^-25 2^-kShift, int8 2^(1 + kHeadroom) of that: 2^-28 of the largest
-  // V. bf16 operands have fp32's range.
+  // The softmax's window: a logit may pass its reference by 2^kRaise, and p there is 2^kShift (int8: times a V
+  // scale over its bound, which sits up to 2^kHeadroom above the largest seen). fp16 operands stay below 2^15, and
+  // a p below fp16's normal range is off by at most 2^-25 2^-kShift, int8 2^(1 + kHeadroom) of that: 2^-28 of the
+  // largest V. bf16 operands have fp32's range.
   static constexpr float kRaise = F::kBf16 ? 16.f : F::kInt8 ? 10.f : 12.f, kShift = F::kBf16 ? 0.f : 15.f - kRaise;
   static constexpr int kHeadroom = 1;
   static constexpr int kKRows = KB / CG, kVDims = HD / CG;  // this SM's part of a block
@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     const uint32_t own_part = sb + U::kQ + (d0 >> 6) * (kTileM * 128) + 32 * q4 * 128;
     uint32_t jb = 0, meet = 0;  // blocks so far; exchanges so far of the row's threads
     bool ok = true;
-    // Whether any thread of the kParts warps that share rows says so. They meet at a hardware barrier, which has no time
-    // limit: so none of them ever leaves alone. One whose own wait ran out (!ok) goes on without its work to the next
-    // vote or exchange, where all of them learn it and leave together.
+    // Whether any thread of the kParts warps that share rows says so. They meet at a hardware barrier, which has
+    // no time limit: so none of them ever leaves alone. One whose own wait ran out (!ok) goes on without its work
+    // to the next vote or exchange, where all of them learn it and leave together.
     auto vote = [&](bool x) -> bool {
       uint32_t any;
       asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
@@ -689,8 +689,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         const int64_t part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
         const int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
         if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
-        // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer needs: four
-        // lanes write 64 B of a row
+        // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer
+        // needs: four lanes write 64 B of a row
         const int to = in && any ? at : -1;
         const uint32_t part = own_part + t * U::kQTile;
 #pragma unroll 1
