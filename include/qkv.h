@@ -653,6 +653,7 @@ qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
  *                 streams, or replays of two captured graphs -- must not share one.
  *   rows * num_q_heads at most 2^31 - 1 (else QKV_ERR_ARG), num_slots * num_kv_heads too, and fewer than 2^31 pieces
  *                 of 128 (row, head) pairs x 64 keys of the prefix (else QKV_ERR_UNSUPPORTED).
+ *   int8 V scales of keys that a row sees: magnitudes up to 2^98 (an output past that may come out infinite).
  * Results do not depend on other rows of the batch, up to rounding; calls with the same arguments
  * on the same device give the same bits.
  *

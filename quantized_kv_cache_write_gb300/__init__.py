@@ -540,7 +540,7 @@ def _packer(desc, fn: str):
     def call(dev, stream, *fields):
         try:
             packed = pack(*fields)
-        except struct.error as e:
+        except (struct.error, OverflowError) as e:
             raise ValueError(f"{fn}: a size or scalar out of range: {e}") from None
         _call_on(dev, fn, entry, packed, stream)
     return call

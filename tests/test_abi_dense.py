@@ -227,3 +227,24 @@ def test_descriptors_match_the_header(lib):
             t, n = re.match(r"\s*((?:const )?\w+\*?)\s+(\w+);", line).groups()
             want.append((n, ctypes.c_void_p if t.endswith("*") else c[t]))
         assert [(n, t) for n, t in struct._fields_] == want
+
+
+@pytest.mark.parametrize("field,value", [("max_row_len", 1 << 31), ("max_blocks", -(1 << 40)), ("softmax_scale", 1e300),
+                                         ("workspace_bytes", -1), ("q", 1 << 64), ("head_dim", 128.5)])
+def test_scalars_that_do_not_fit_the_descriptor_are_refused(lib, field, value):
+    """Before anything is called: a size is never cut to its field's width."""
+    import quantized_kv_cache_write_gb300 as qkv
+    fields = [value if name == field else 0 for name, _ in qkv.PrefixDesc._fields_]
+    with pytest.raises(ValueError, match="out of range"):
+        qkv._call_prefix(0, None, *fields)
+
+
+def test_packed_descriptors_equal_the_structures(lib):
+    """The bytes that the binding passes are those of the structure, field for field."""
+    import ctypes
+    import struct
+    import quantized_kv_cache_write_gb300 as qkv
+    for desc, call in ((qkv.AppendDesc, qkv._call_append), (qkv.PrefixDesc, qkv._call_prefix)):
+        pack = next(c.cell_contents for c in call.__closure__ if getattr(c.cell_contents, "__name__", "") == "pack")
+        values = [float(i) if kind is ctypes.c_float else i + 1 for i, (_, kind) in enumerate(desc._fields_)]
+        assert pack(*values) == bytes(desc(*values)) and isinstance(pack.__self__, struct.Struct)
