@@ -130,16 +130,14 @@ _ACT16 = (torch.bfloat16, torch.float16)
 def _tokens(k: torch.Tensor, v: torch.Tensor):
     """[T, Hkv, D] views sharing one token stride; heads and dims contiguous. (The stride of a
     dimension of size 1 is never used, so it may be anything.)"""
-    if k.dim() != 3 or k.shape != v.shape or k.dtype not in _ACT16 or v.dtype != k.dtype:
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or k.dtype not in _ACT16 or v.dtype != k.dtype:
         raise ValueError("k and v must be bf16 (or both fp16) [num_tokens, num_kv_heads, head_dim] of equal shape")
-    T, H, D = k.shape
-
-    def heads_contiguous(t):
-        return (D == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == D)
-
-    if not (heads_contiguous(k) and heads_contiguous(v)) or (T > 1 and k.stride(0) != v.stride(0)):
+    T, H, D = shape
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    if (D != 1 and (kd != 1 or vd != 1)) or (H != 1 and (kh != D or vh != D)) or (T > 1 and kt != vt):
         raise ValueError("k and v need contiguous heads and one shared token stride")
-    return T, H, D, (k.stride(0) if T > 1 else H * D)
+    return T, H, D, (kt if T > 1 else H * D)
 
 
 def qkv_write_int8(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, *,
@@ -546,36 +544,42 @@ def _packer(desc, fn: str):
     return call
 
 
+_f32, _half, _int32, _int64 = torch.float32, torch.float16, torch.int32, torch.int64
 _call_append, _call_prefix = _packer(AppendDesc, "qkv_append_rope"), _packer(PrefixDesc, "qkv_prefix_attn")
 _CACHE_BYTES = {QKV_BF16: 2, QKV_F16: 2, QKV_INT8_SIDE: 1, QKV_INT8_INLINE: 1, QKV_E4M3: 1}
 
 
-def _need_cache(name: str, t, fmt: int, H: int, D: int):
-    """A pool tensor [S, H, D] (inline: [S, H, D + 4]) of the format's element size."""
+def _need_caches(k_cache, v_cache, fmt: int, H: int, D: int) -> int:
+    """The pool's tensors, contiguous [S, H, D] (inline: [S, H, D + 4]) of the format's element size; S."""
     size = _CACHE_BYTES.get(fmt)
     if size is None:
         raise ValueError(f"unknown pool format {fmt}")
-    width = D + 4 if fmt == QKV_INT8_INLINE else D
-    if tuple(t.shape[1:]) != (H, width) or t.dim() != 3 or t.element_size() != size or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [num_slots, {H}, {width}] pool of {size}-byte values, "
-                         f"got {tuple(t.shape)} {t.dtype}")
+    want = (H, D + 4 if fmt == QKV_INT8_INLINE else D)
+    shape = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.shape[1:] != want or t.element_size() != size or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [num_slots, {H}, {want[1]}] pool of {size}-byte values, "
+                             f"got {tuple(t.shape)} {t.dtype}")
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must hold the same number of slots")
+    return shape[0]
 
 
 def _strided(name: str, t, T: int, H: int, D: int) -> int:
     """The token stride of a [T, H, D] tensor with contiguous heads (of no matter where T <= 1)."""
-    if t.dim() != 3 or tuple(t.shape) != (T, H, D):
+    if t.shape != (T, H, D):
         raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
-    st = t.stride()
-    if (D != 1 and st[2] != 1) or (H != 1 and st[1] != D):
+    token, head, dim = t.stride()
+    if (D != 1 and dim != 1) or (H != 1 and head != D):
         raise ValueError(f"{name} needs contiguous heads")
-    return st[0] if T > 1 else H * D
+    return token if T > 1 else H * D
 
 
 def _on_cuda(*tensors) -> int:
     """The one CUDA device that every tensor sits on: the kernels take raw pointers."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
+        if t is not None and t.get_device() != dev or dev < 0:
             raise ValueError(f"all tensors must be on one CUDA device, got {tensors[0].device} and {t.device}")
     return dev
 
@@ -597,9 +601,9 @@ def _call_on(dev: int, fn: str, call, desc, stream):
 
 
 def _plain(name: str, t, dtype, numel: int):
-    """_need for one dtype, without its cost where nothing is wrong; the tensor's address."""
+    """_need for one dtype, without its cost where nothing is wrong; the tensor's address (None: 0)."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or not t.is_contiguous() or t.numel() != numel:
         _need(name, t, (dtype,), numel)
     return t.data_ptr()
@@ -618,43 +622,42 @@ def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=N
     [T], or token_seq int32 [T] with block_table int32 [num_seqs, max_blocks] and block_size.
     """
     T, H, D, stride = _tokens(k, v)
-    _need_cache("k_cache", k_cache, fmt, H, D)
-    _need_cache("v_cache", v_cache, fmt, H, D)
-    S = k_cache.shape[0]
-    if v_cache.shape[0] != S:
-        raise ValueError("k_cache and v_cache must hold the same number of slots")
-    if cos_sin.dim() != 2:
+    S = _need_caches(k_cache, v_cache, fmt, H, D)
+    angles = cos_sin.shape
+    if len(angles) != 2:
         raise ValueError("cos_sin must be [positions, rotary_dim]")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    qp = qop = None
-    Hq = qs = qos = 0
+    qp = qop = Hq = qs = qos = 0
     if q is not None:
-        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+        if q.dtype is not k.dtype or q_out.dtype is not k.dtype:
             raise ValueError(f"q and q_out must be {k.dtype} as k and v are")
-        Hq = q.shape[1] if q.dim() == 3 else 0
+        heads = q.shape
+        Hq = heads[1] if len(heads) == 3 else 0
         qs, qos = _strided("q", q, T, Hq, D), _strided("q_out", q_out, T, Hq, D)
         qp, qop = q.data_ptr(), q_out.data_ptr()
-    P, rot = cos_sin.shape
-    csp = _plain("cos_sin", cos_sin, torch.float32, P * rot)
-    tpp = _plain("token_pos", token_pos, torch.int32, T)
-    smp = _plain("slot_mapping", slot_mapping, torch.int64, T)
-    tsp = _plain("token_seq", token_seq, torch.int32, T)
-    ksp = _plain("k_scale", k_scale, torch.float32, S * H)
-    vsp = _plain("v_scale", v_scale, torch.float32, S * H)
-    _need("dev_status", dev_status, _WORD)
-    btp, seqs, blocks = None, 0, 0
+    P, rot = angles
+    csp = _plain("cos_sin", cos_sin, _f32, P * rot)
+    tpp = _plain("token_pos", token_pos, _int32, T)
+    smp = _plain("slot_mapping", slot_mapping, _int64, T)
+    tsp = _plain("token_seq", token_seq, _int32, T)
+    ksp = _plain("k_scale", k_scale, _f32, S * H)
+    vsp = _plain("v_scale", v_scale, _f32, S * H)
+    if dev_status is not None:
+        _need("dev_status", dev_status, _WORD)
+    btp = seqs = blocks = 0
     if block_table is not None:
-        if block_table.dim() != 2:
+        table = block_table.shape
+        if len(table) != 2:
             raise ValueError("block_table must be [num_seqs, max_blocks]")
-        seqs, blocks = block_table.shape
-        btp = _plain("block_table", block_table, torch.int32, seqs * blocks)
+        seqs, blocks = table
+        btp = _plain("block_table", block_table, _int32, seqs * blocks)
     dev = _on_cuda(k, v, q, q_out, k_cache, v_cache, cos_sin, token_pos, slot_mapping, token_seq, block_table, k_scale,
                    v_scale, dev_status)
-    _call_append(dev, stream, _APPEND_SIZE, fmt, k.dtype is torch.float16, qp or 0, qop or 0, k.data_ptr(), v.data_ptr(), T,
-                 Hq, H, D, qs, qos, stride, csp or 0, P, rot, 1 if interleaved else 0, tpp or 0, smp or 0, tsp or 0, btp or 0,
-                 seqs, blocks, block_size, k_cache.data_ptr(), v_cache.data_ptr(), ksp or 0, vsp or 0, float(k_scale_layer),
-                 float(v_scale_layer), S, _ptr(dev_status) or 0)
+    _call_append(dev, stream, _APPEND_SIZE, fmt, k.dtype is _half, qp, qop, k.data_ptr(), v.data_ptr(), T, Hq, H, D, qs,
+                 qos, stride, csp, P, rot, 1 if interleaved else 0, tpp, smp, tsp, btp, seqs, blocks, block_size,
+                 k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S,
+                 0 if dev_status is None else dev_status.data_ptr())
 
 
 def qkv_prefix_attn_workspace(fmt: int, rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -680,47 +683,46 @@ def qkv_prefix_attn(q, fmt: int, k_cache, v_cache, block_table, row_seq, row_len
     [R, Hq, D] in q's type; workspace any contiguous tensor of at least
     qkv_prefix_attn_workspace bytes.
     """
-    if q.dim() != 3 or q.dtype not in _ACT16:
+    shape, table = q.shape, block_table.shape
+    if len(shape) != 3 or q.dtype not in _ACT16:
         raise ValueError("q must be bf16 or fp16 [rows, num_q_heads, head_dim]")
-    R, Hq, D = q.shape
+    R, Hq, D = shape
     stride = _strided("q", q, R, Hq, D)
-    _need_cache("k_cache", k_cache, fmt, num_kv_heads, D)
-    _need_cache("v_cache", v_cache, fmt, num_kv_heads, D)
-    S = k_cache.shape[0]
-    if v_cache.shape[0] != S:
-        raise ValueError("k_cache and v_cache must hold the same number of slots")
-    if block_table.dim() != 2:
+    S = _need_caches(k_cache, v_cache, fmt, num_kv_heads, D)
+    if len(table) != 2:
         raise ValueError("block_table must be [num_seqs, max_blocks]")
-    seqs, blocks = block_table.shape
-    btp = _plain("block_table", block_table, torch.int32, seqs * blocks)
-    rsp = _plain("row_seq", row_seq, torch.int32, R)
-    rlp = _plain("row_len", row_len, torch.int32, R)
-    if out.shape != q.shape:
+    seqs, blocks = table
+    btp = _plain("block_table", block_table, _int32, seqs * blocks)
+    rsp = _plain("row_seq", row_seq, _int32, R)
+    rlp = _plain("row_len", row_len, _int32, R)
+    if out.shape != shape:
         _expect_shape("out", out, (R, Hq, D))
     op = _plain("out", out, q.dtype, R * Hq * D)
-    lp = None
+    lp = 0
     if lse is not None:
-        _expect_shape("lse", lse, (R, Hq))
-        lp = _plain("lse", lse, torch.float32, R * Hq)
-    ksp = _plain("k_scale_tok", k_scale_tok, torch.float32, S * num_kv_heads)
-    vsp = _plain("v_scale_tok", v_scale_tok, torch.float32, S * num_kv_heads)
-    _need("dev_status", dev_status, _WORD)
-    pbp = None
+        if lse.shape != (R, Hq):
+            _expect_shape("lse", lse, (R, Hq))
+        lp = _plain("lse", lse, _f32, R * Hq)
+    ksp = _plain("k_scale_tok", k_scale_tok, _f32, S * num_kv_heads)
+    vsp = _plain("v_scale_tok", v_scale_tok, _f32, S * num_kv_heads)
+    if dev_status is not None:
+        _need("dev_status", dev_status, _WORD)
+    pbp = 0
     if prefix_len > 0:
         if prefix_blocks is None or block_size < 1:
             raise ValueError("a shared prefix needs prefix_blocks and a block_size")
         n = prefix_blocks.numel()
-        pbp = _plain("prefix_blocks", prefix_blocks, torch.int32, n)
+        pbp = _plain("prefix_blocks", prefix_blocks, _int32, n)
         if n * block_size < prefix_len:
             raise ValueError(f"prefix_blocks must cover {prefix_len} positions, got {n} blocks")
-    wsp, wsb = None, 0
+    wsp = wsb = 0
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wsp, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     dev = _on_cuda(q, k_cache, v_cache, block_table, row_seq, row_len, out, lse, k_scale_tok, v_scale_tok,
                    prefix_blocks, workspace, dev_status)
-    _call_prefix(dev, stream, _PREFIX_SIZE, fmt, q.dtype is torch.float16, q.data_ptr(), stride, R, Hq, num_kv_heads, D,
-                 k_cache.data_ptr(), v_cache.data_ptr(), ksp or 0, vsp or 0, float(k_scale_layer), float(v_scale_layer), S,
-                 pbp or 0, prefix_len, btp or 0, seqs, blocks, block_size, rsp or 0, rlp or 0, max_row_len,
-                 float(softmax_scale), op or 0, lp or 0, wsp or 0, wsb, _ptr(dev_status) or 0)
+    _call_prefix(dev, stream, _PREFIX_SIZE, fmt, q.dtype is _half, q.data_ptr(), stride, R, Hq, num_kv_heads, D,
+                 k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S, pbp,
+                 prefix_len, btp, seqs, blocks, block_size, rsp, rlp, max_row_len, float(softmax_scale), op, lp, wsp, wsb,
+                 0 if dev_status is None else dev_status.data_ptr())
