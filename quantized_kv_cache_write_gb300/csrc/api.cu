@@ -573,8 +573,11 @@ constexpr int64_t kUmmaMinBytes = 20 << 20;
 // How a shared-prefix call is cut into key ranges: up to 16 CTAs per SM, so that ragged rows balance (64 rows x 64
 // heads of 0 to 8192 e4m3 keys: 118 us, 121 with 8, 130 with 4), but none with fewer than 512 keys, since a CTA's
 // start and its join cost as much as about 300 (8 x 5 drafts behind 126976 int8 keys: 131 us, 135 with 256, 144
-// with 1024; one row of 65536: 31 us, 40, 37), and 256 while those do not fill the SMs once (one row of 8192: 19
-// us, 23 with 512, 33 with 1024).
+// with 1024; one row of 65536: 31 us, 40, 37). Ranges of 64, 128 or 256 keys where all CTAs then run at once (with
+// a tenth to spare) and the merge has at most 32 ranges to join. In us, ranges of at least 512 | 256 | 128 | 64:
+// one row x 16 heads of 256, int8, 500 keys 17 | 13 | 11 | 9, 2000 keys 19 | 14 | 11 | 11, 8192 keys 20 | 15 | 15
+// | 17; one row x 64 heads (8 KV heads) of 128, bf16, 1000 keys 14 | 11 | 8 | 7, 8192 keys 15 | 13 | 18 | 22; four
+// such rows, e4m3, 1000 keys 13 | 10 | 9 | 9, 4096 keys 15 | 14 | 18 | 26.
 struct PrefixPlan {
   int prefix_parts, own_parts, prefix_chunk;
   int umma_cg, umma_pairs, umma_ptiles;
@@ -608,9 +611,12 @@ qkv_status plan_prefix(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv
   p->head_dim = head_dim;
   p->ptiles = ceil_div(rows * G, 16) * num_kv_heads;
   p->otiles = rows * ceil_div(G, 16) * num_kv_heads;
+  const int64_t row_bytes = fmt == QKV_BF16 || fmt == QKV_F16 ? 2 * head_dim : head_dim;
+  const int64_t slots = static_cast<int64_t>(sms) * (row_bytes == 128 ? 3 : row_bytes == 256 ? 2 : 1);  // resident CTAs
   auto parts_of = [&](int64_t tiles, int keys) -> int {
     if (keys <= 0 || tiles <= 0) return 0;
-    const int least = tiles * ceil_div(keys, 256) <= sms ? 256 : 512;
+    int least = 64;
+    while (least < 512 && (ceil_div(keys, least) > 32 || 10 * tiles * ceil_div(keys, least) > 9 * slots)) least *= 2;
     const int64_t want = ceil_div(16 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, least);
     return static_cast<int>(want < most ? want : most);
   };
@@ -622,7 +628,6 @@ qkv_status plan_prefix(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv
   }
   p->umma_cg = 0, p->umma_pairs = 0, p->umma_ptiles = 0;
   p->umma_blocks = 0, p->umma_teams = 0, p->umma_share = 0, p->umma_extra = 0;
-  const int64_t row_bytes = fmt == QKV_BF16 || fmt == QKV_F16 ? 2 * head_dim : head_dim;
   if (prefix_len > 0 && p->ptiles > kUmmaMinBytes / (prefix_len * row_bytes)) {
     // Two SMs per team where their tiles (512 pairs of 128-wide heads, 256 of 256-wide ones) are at least half
     // full. In us, one SM | two: 8 heads of 128, e4m3, 65536 keys, 256 pairs 99 | 118, 512 pairs 180 | 145; 4
