@@ -68,7 +68,8 @@ typedef enum {
 #define QKV_DEV_TIMEOUT 4u   /* a gather CTA's bounded wait for its own copies or tensor-core
                                 work ran out (not expected on a healthy GPU): the CTA stopped
                                 early, its outputs are incomplete; the kernel returns instead of
-                                hanging. Only the tcgen05 engine waits. A test can make it happen:
+                                hanging. Only the tcgen05 engine and qkv_prefix_attn's tcgen05
+                                tiles wait. A test can make it happen in the engine:
                                 QKV_TEST_TCGEN05_DROP_HANDOFF=<block> in the environment drops
                                 that block's hand-off inside each CTA (never set it otherwise) */
 

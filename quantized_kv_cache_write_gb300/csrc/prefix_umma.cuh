@@ -944,13 +944,13 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     if (lead) commit_to<CG>(sb + U::kDrain);
     __syncwarp();
   }
-  if (warp == U::kMmaWarp && lane == 0) {
-    // nothing may still write tensor memory, read a slot or arrive on a barrier when the team leaves
-    bar_wait(sb + U::kDrain, 0, flag, false);
-  }
   __syncwarp();
   tmem_fence_before_sync();
   __syncthreads();
+  // Nothing may still write tensor memory, read a slot or arrive on a barrier when the team leaves. (After the others are
+  // done: the second SM's MMA warp has nothing to do until here, and a call may be longer than a wait's limit.)
+  if (warp == U::kMmaWarp && lane == 0) bar_wait(sb + U::kDrain, 0, flag, false);
+  __syncwarp();
   team_sync<CG>();
   tmem_fence_after_sync();
   if (warp == U::kMmaWarp) team_tmem_dealloc<CG>(tb);
