@@ -352,6 +352,27 @@ def test_tcgen05_tiles(fmt, act, D, rows, G, H, prefix):
     assert torch.equal(out.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_seeded_random_tcgen05_shapes(seed):
+    rng = np.random.default_rng(3000 + seed)
+    fmt, act = FMTS[seed % len(FMTS)]
+    D, H, per = int(rng.choice([128, 256])), int(rng.choice([1, 2, 4])), int(rng.choice([1, 1, 2, 5]))
+    G, seqs = int(rng.choice([1, 3, 8, 12, 16, 32, 128])), int(rng.integers(1, 40))
+    tiles = -(-seqs * per * G // 16) * H
+    prefix = (20 << 20) // (tiles * D) + int(rng.integers(1, 300))  # just past the rule, for one byte per value
+    if prefix * seqs * per * G * H > 1 << 25:
+        prefix = max(1, (1 << 25) // (seqs * per * G * H))
+    own = [int(rng.integers(per, 60)) for _ in range(seqs)]
+    b, pool, q, scale = case(4000 + seed, fmt, act, D, H, G, prefix, own, per, int(rng.choice([1, 7, 16, 64, 128])))
+    seq, ln = b.row_seq.copy(), b.row_len.copy()
+    idle = rng.random(len(seq)) < 0.1
+    seq[idle] = -1
+    out, lse = torch.full((len(seq), H * G, D), 7.0, dtype=ACT[act], device="cuda"), torch.full((len(seq), H * G), 7.0, device="cuda")
+    call(pool, b, dev16(q, act), H, scale, row_seq=seq, row_len=ln, out=out, lse=lse)
+    check(pool, b, q, act, H, scale, out, lse, row_seq=seq, row_len=ln, what=f"seed {seed}")
+    assert (out[torch.from_numpy(idle).cuda()] == 7).all() and (lse[torch.from_numpy(idle).cuda()] == 7).all()
+
+
 @pytest.mark.parametrize("fmt,act", FMTS)
 @pytest.mark.parametrize("D", [128, 256])
 def test_tcgen05_tiles_with_bad_blocks_empty_rows_and_padding(fmt, act, D):
