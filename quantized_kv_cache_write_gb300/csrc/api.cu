@@ -563,12 +563,12 @@ int sm_count() {
 }
 
 // K bytes that tiles of 16 pairs would read above which the prefix runs on tcgen05: its tiles read them once per
-// 128 pairs or more, but a call costs some 6 us before the first key and after the last. In us, mma.sync |
-// tcgen05: one KV head of 256, int8, 16 pairs of 65536 keys (17 MB) 28 | 35, 24 pairs (34 MB) 36 | 34, 128 pairs
-// of 8192 (17 MB) 22 | 26; 8 heads of 128, e4m3, 8192 keys, 32 pairs (17 MB) 19.4 | 18.8, 48 pairs (25 MB) 29 |
-// 19; 4 heads of 128, bf16, 8192 keys, 32 pairs (17 MB) 17.0 | 18.5, 48 pairs (25 MB) 20.3 | 19.5, 64 pairs (34
-// MB) 30 | 19.
-constexpr int64_t kUmmaMinBytes = 20 << 20;
+// 128 pairs or more, but a call costs some 6 us before the first key and after the last. In us, mma.sync | tcgen05:
+// one KV head of 256, int8: 16 pairs at 12 MB 28 | 31, at 20 MB 37 | 35, at 32 MB 58 | 44; 128 pairs 18 | 21, 28 | 29,
+// 39 | 29. 8 heads of 128, e4m3: 32 pairs at 6 MB 15 | 16, at 12 MB 20 | 17, at 20 MB 26 | 19. 4 heads of 128, bf16:
+// 32 pairs at 12 MB 14 | 17, at 20 MB 19 | 17; 2048 pairs 23 | 19, 25 | 20. 2 heads of 256, fp16: 32 pairs at 12 MB
+// 22 | 22, at 20 MB 33 | 21.
+constexpr int64_t kUmmaMinBytes = 16 << 20;
 
 // How a shared-prefix call is cut into key ranges: up to 16 CTAs per SM, so that ragged rows balance (64 rows x 64
 // heads of 0 to 8192 e4m3 keys: 118 us, 121 with 8, 130 with 4), but none with fewer than 512 keys, since a CTA's
