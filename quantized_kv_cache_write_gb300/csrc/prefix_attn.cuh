@@ -20,7 +20,7 @@
 // 16-bit type or less.
 //
 // Measured: 64 rows x 64 heads of 128 over 0 to 8192 e4m3 keys of their own, no prefix (539 MB), 110 us in this
-// kernel (4.9 TB/s); 128 rows x 32 heads over 16 to 2048 bf16 keys (270 MB) 63 us (4.3 TB/s). Between its start and
+// kernel (4.9 TB/s); 128 rows x 32 heads over 16 to 2048 bf16 keys (270 MB) 57 us (4.7 TB/s). Between its start and
 // its join a CTA streams at more than its share of the memory rate; the block list, table and query that it waits for
 // before the first key, and the join, are 40 to 60 % of a short range's time and are hidden by the SM's two or
 // three other CTAs only in part. Deeper rings with fewer CTAs, shallower ones with more, and longer ranges all
@@ -61,6 +61,10 @@ struct Geom {
   static constexpr int kKeys = kRow == 128 && NP == 16 ? 32 : 16;
   static constexpr int kStages = kRow == 128 ? (NP == 16 ? 2 : 3) : kRow == 256 ? (NP == 16 ? 3 : 2) : 3;
   static constexpr int kMinBlocks = kRow == 128 ? (NP == 16 ? 3 : 4) : kRow == 256 ? (NP == 16 ? 2 : 3) : 1;
+  // the next tile fetched into L2 ahead of its copy, where the ring holds two tiles of 8 KB: 128 rows x 32 heads over
+  // 16 to 2048 own keys, heads of 128 in bf16 64 -> 60 us, of 256 in e4m3 90 -> 83, in inline int8 118 -> 104; with
+  // the other rings it costs (64 rows x 64 heads of 128, e4m3: 110 -> 114 us)
+  static constexpr bool kAhead = kRow == 256 && kStages == 2;
   static constexpr int kScales = 2 * kKeys * kRow;
   static constexpr int kMask = kScales + (F::kInt8 ? 2 * kKeys * 4 : 0);
   static constexpr int kStage = kMask + 16;  // K, V, scales, key mask
@@ -289,6 +293,21 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     cp_async_commit();
   };
 
+  // The tile after the ring's into L2: one more tile in flight per warp than the ring has room for.
+  auto prefetch = [&](int i, int blk) {
+    if (!GM::kAhead || i >= my) return;
+    const int key = lane & (TK - 1), pos = tile_pos(i) + key;
+    const int b = __shfl_sync(0xffffffffu, blk, key);
+    const int64_t slot = static_cast<int64_t>(b) * bsz + (pos - block_of(pos) * bsz);
+    if (b < 0 || slot >= a.num_slots) return;
+    const int64_t off = (slot * H + h) * GM::kGlobalRow;
+#pragma unroll
+    for (int u = 0; u < RB / 128; ++u) {
+      if (TK == 32 || lane < TK) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(a.k_cache + off + 128 * u));
+      if (TK == 32 || lane >= TK) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(a.v_cache + off + 128 * u));
+    }
+  };
+
   int blk = load_blk(0), next0 = load_blk(1);  // before the query's loads: the copies wait for them
 
   // ---------------- query rows into registers, each warp a quarter of the pairs
@@ -313,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     issue(i, blk);
     blk = next;
   }
+  prefetch(ST - 1, blk);
 
   // ---------------- the query into shared memory; bytes pools: fp16, in the fragments' dim order
   uint8_t* sQ = smem + GM::kArea;
@@ -670,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     }
     __syncwarp();
     issue(i + ST - 1, blk);
+    prefetch(i + ST, next);
     blk = next;
   }
 

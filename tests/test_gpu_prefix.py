@@ -285,6 +285,13 @@ def test_workspace_too_small_is_refused():
                                 **pool.kw)
 
 
+def test_a_call_of_more_units_than_32_bits_number_is_refused():
+    import quantized_kv_cache_write_gb300 as qkv
+    with pytest.raises(qkv.QKVError) as e:
+        qkv.qkv_prefix_attn_workspace(qkv.QKV_E4M3, 1 << 20, 64, 8, 128, 1 << 29, 1 << 29)
+    assert e.value.status == qkv.QKV_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_seeded_random_shapes(seed):
     rng = np.random.default_rng(1000 + seed)
