@@ -56,15 +56,19 @@ struct Geom {
   using F = Fmt<FMT>;
   static constexpr int kRow = F::kBytes ? HD : 2 * HD;              // bytes of a record's values
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : kRow;     // bytes between records
-  // keys of a warp tile (32 where rows are short and the tile holds 16 pairs: the softmax step's fixed cost is
-  // shared), ring stages and CTAs per SM: 64 to 128 KB of copies in flight per SM
-  static constexpr int kKeys = kRow == 128 && NP == 16 ? 32 : 16;
-  static constexpr int kStages = kRow == 128 ? (NP == 16 ? 2 : 3) : kRow == 256 ? (NP == 16 ? 3 : 2) : 3;
-  static constexpr int kMinBlocks = kRow == 128 ? (NP == 16 ? 3 : 4) : kRow == 256 ? (NP == 16 ? 2 : 3) : 1;
-  // the next tile fetched into L2 ahead of its copy, where the ring holds two tiles of 8 KB: 128 rows x 32 heads over
-  // 16 to 2048 own keys, heads of 128 in bf16 64 -> 60 us, of 256 in e4m3 90 -> 83, in inline int8 118 -> 104; with
-  // the other rings it costs (64 rows x 64 heads of 128, e4m3: 110 -> 114 us)
-  static constexpr bool kAhead = kRow == 256 && kStages == 2;
+  // Keys of a warp tile (32 where rows are short: the softmax step's fixed cost is shared), ring stages and CTAs
+  // per SM: 64 to 128 KB of copies in flight per SM. Tiles of 8 pairs with rows of 128 B, us with 16 keys in three
+  // stages on four CTAs | 32 keys in two on three, the next tile ahead in L2: e4m3, 64 rows x 64 heads of 0 to
+  // 8192 keys 114 | 105, 4 rows of 1000 9.0 | 8.3, 256 rows of 50 to 300 35 | 37; inline int8, 64 rows of 0 to
+  // 4096 131 | 125; int8 with side scales 79 | 86, so that one keeps the former.
+  static constexpr bool kShort = kRow == 128 && (NP == 16 || FMT != QKV_INT8_SIDE);
+  static constexpr int kKeys = kShort ? 32 : 16;
+  static constexpr int kStages = kShort || (kRow == 256 && NP == 8) ? 2 : 3;
+  static constexpr int kMinBlocks = kShort ? 3 : kRow == 128 ? 4 : kRow == 256 ? (NP == 16 ? 2 : 3) : 1;
+  // The next tile fetched into L2 ahead of its copy, where the ring holds two tiles of 8 KB and the tile has 8
+  // pairs: 128 rows x 32 heads over 16 to 2048 own keys, heads of 128 in bf16 64 -> 60 us, of 256 in e4m3 90 ->
+  // 83, in inline int8 118 -> 104; with the other rings it costs (e4m3, 16 keys in three stages: 110 -> 114 us).
+  static constexpr bool kAhead = NP == 8 && kStages == 2;
   static constexpr int kScales = 2 * kKeys * kRow;
   static constexpr int kMask = kScales + (F::kInt8 ? 2 * kKeys * 4 : 0);
   static constexpr int kStage = kMask + 16;  // K, V, scales, key mask
