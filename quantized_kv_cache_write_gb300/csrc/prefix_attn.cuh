@@ -19,12 +19,11 @@
 // 2^-9 (bf16), independent from key to key, so an output has about the rounding error of its own
 // 16-bit type or less.
 //
-// Measured: 64 rows x 64 heads of 128 over 0 to 8192 e4m3 keys of their own, no prefix (539 MB), 110 us in this
-// kernel (4.9 TB/s); 128 rows x 32 heads over 16 to 2048 bf16 keys (270 MB) 57 us (4.7 TB/s). Between its start and
+// Measured: 64 rows x 64 heads of 128 over 0 to 8192 e4m3 keys of their own, no prefix (539 MB), 101 us in this
+// kernel (5.3 TB/s); 128 rows x 32 heads over 16 to 2048 bf16 keys (270 MB) 58 us (4.7 TB/s). Between its start and
 // its join a CTA streams at more than its share of the memory rate; the block list, table and query that it waits for
-// before the first key, and the join, are 40 to 60 % of a short range's time and are hidden by the SM's two or
-// three other CTAs only in part. Deeper rings with fewer CTAs, shallower ones with more, and longer ranges all
-// measured the same or slower.
+// before the first key, and the join, are 40 to 60 % of a short range's time and are hidden by the SM's other one
+// to three CTAs only in part.
 #pragma once
 
 #include <atomic>
