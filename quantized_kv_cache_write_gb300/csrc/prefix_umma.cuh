@@ -888,8 +888,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);  // warp-uniform
     auto wait = [&](uint32_t bar, uint32_t ph) -> bool { return __all_sync(0xffffffffu, bar_wait(bar, ph, flag)); };
     auto await_full = [&](uint32_t s) -> bool { return wait(sb + U::kFull + 8 * (s % NS), (s / NS) & 1); };
-    // S of tile t into buffer b, from the K slot s (awaited by the first tile, freed by the last)
-    auto qk = [&](int t, uint32_t b, uint32_t s) {
+    // S of sub-iteration n (of tile t) into its buffer, from the K slot s (awaited by the first tile, freed by the
+    // last). The buffer holds P of sub-iteration n - 2. MMAs are only sure to run in the order of their issue where
+    // they have the same shape and accumulator, which S and O are not, so that P V has to be over first.
+    auto qk = [&](int t, uint32_t n, uint32_t s) {
+      const uint32_t b = n & 1;
+      if (n >= 2 && !(ok = wait(sb + U::kPvDone + 8 * b, ((n >> 1) - 1) & 1))) return;
       if (t == 0 && !(ok = await_full(s))) return;
       tmem_fence_after_sync();
       const uint32_t d = tu + U::kS + KB * b;
@@ -935,7 +939,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           const int t = NT == 2 ? i : 0;
           if (j >= 0 && (NT == 2 || i == 1))
             pv(t, (n * NT + t) & 1, ((n * NT + t) >> 1) & 1, base + v_slot(j, B), j == 0);
-          if (ok && j + 1 < B && (NT == 2 || i == 0)) qk(t, ((n + 1) * NT + t) & 1, base + k_slot(j + 1));
+          if (ok && j + 1 < B && (NT == 2 || i == 0)) qk(t, (n + 1) * NT + t, base + k_slot(j + 1));
         }
       }
       jb += B;
