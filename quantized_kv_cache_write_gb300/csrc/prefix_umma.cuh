@@ -630,8 +630,17 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
             const bool up_m = tm > M[0] + U::kRaise;  // the same for the row's threads
             const float Mn = up_m ? tm : M[0];
             const float Rn = Mn == -INFINITY ? 0.f : Mn + static_cast<float>(En) - U::kShift;
-            if (M[0] != -INFINITY) f = fast_exp2(R[0] - Rn);
-            l[0] *= f;
+            if (F::kInt8) {
+              // the reference may rise by more than fp32's exponents go down, by E alone: the sum carries E from
+              // -90 to 99 and stays in range, so it is scaled in two steps (O then held V scales 2^-126 of the
+              // new one's, and is lost)
+              const float half = M[0] != -INFINITY ? fast_exp2(0.5f * (R[0] - Rn)) : 1.f;
+              l[0] = l[0] * half * half;
+              f = half * half;
+            } else {
+              if (M[0] != -INFINITY) f = fast_exp2(R[0] - Rn);
+              l[0] *= f;
+            }
             M[0] = Mn, R[0] = Rn, E[0] = En;
           }
           // ---- p = 2^(y - R), its sum, and (times the V scale) the operand

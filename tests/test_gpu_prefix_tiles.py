@@ -43,3 +43,34 @@ def test_score_buffers_used_again_and_again(fmt, act, D, rows, prefix):
     for _ in range(10):
         o2, l2 = call(pool, b, dev16(q, act), 1, 0.25 * D ** -0.5)
         assert torch.equal(out.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, l2)
+
+
+def set_v(pool, codes, scale_bits):
+    """V of an int8 pool: codes [S, H, D] and fp32 scales [S, H] into its layout, and their values into pool.V."""
+    if pool.fmt == "int8_side":
+        pool.cache[1].copy_(codes)
+        pool.kw["v_scale_tok"].copy_(scale_bits)
+    else:
+        D = codes.shape[2]
+        pool.cache[1][..., :D] = codes.view(torch.uint8)
+        pool.cache[1][..., D:] = scale_bits.contiguous().view(torch.uint8).view(*scale_bits.shape, 4)
+    pool.V = codes.cpu().numpy().astype(np.float64) * scale_bits.cpu().numpy().astype(np.float64)[..., None]
+
+
+@pytest.mark.parametrize("fmt", ["int8_side", "int8_inline"])
+@pytest.mark.parametrize("D,rows", [(128, 8), (128, 32), (256, 8), (256, 16)])
+@pytest.mark.parametrize("low,high", [(0.0, 2.0 ** 50), (2.0 ** -80, 2.0 ** 98), (2.0 ** -140, 2.0 ** 40)])
+def test_blocks_of_tiny_and_huge_v_scales_in_turn(fmt, D, rows, low, high):
+    """tcgen05 tiles: runs of 1024 keys whose V scales lie more than 2^126 apart. The weights of the tiny ones' keys
+    count in the sum all the same."""
+    P = 70001
+    rng = np.random.default_rng(41)
+    b = Batch(rng, P, [1] * rows, 1, 64)
+    pool = Pool(rng, fmt, "bf16", b.live, b.num_slots, 1, D)
+    scale = torch.full((b.num_slots, 1), high, device="cuda")
+    scale[torch.from_numpy(prefix_slots(b)[np.arange(P) // 1024 % 2 == 0]).cuda()] = low
+    codes = torch.from_numpy(rng.integers(64, 128, (b.num_slots, 1, D)).astype(np.int8)).cuda()
+    set_v(pool, codes, scale)
+    q = bits16(rng.standard_normal((rows, 16, D)), "bf16")
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, 0.25 * D ** -0.5)
+    check(pool, b, q, "bf16", 1, 0.25 * D ** -0.5, out, lse, what=f"{fmt} {D} {low} {high}")
