@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sFac[NP], sM[kWarps][NP], sL[kWarps][NP];
-  __shared__ float sW[kWarps][NP], sInv[NP];
+  __shared__ float sW[kWarps][NP], sInv[NP], sUp[NP];
   __shared__ int64_t sAt[NP];
   __shared__ int sEu[kWarps][NP];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, hn = lane >> 2;
@@ -734,12 +734,20 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sM[w][lane]);
       const float ref = m == -INFINITY ? 0.f : m;
+      // int8: the warps' outputs are joined as values times 2^-top, and get 2^top last, after the division: sums of
+      // keys with V scales up to 2^98 would not fit otherwise
+      int top = -126;
+      if (F::kInt8) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = max(top, sEu[w][lane]);
+      }
+      sUp[lane] = F::kInt8 ? pow2f(top) : 1.f;
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float al = fast_exp2(sM[w][lane] - ref);  // 2^-inf = 0 for a warp without keys
         sum += al * sL[w][lane];
-        sW[w][lane] = F::kInt8 ? al * pow2f(sEu[w][lane]) : al;
+        sW[w][lane] = F::kInt8 ? al * pow2f(max(sEu[w][lane] - top, -126)) : al;
       }
       const bool any = state != kEmptyRow && (m != -INFINITY || sum != sum);
       sInv[lane] = any ? (direct && FMT == QKV_E4M3 ? a.v_scale_layer : 1.f) / sum : 0.f;
@@ -763,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   for (int i0 = 0; i0 < NP; i0 += kWarps) {
     const int i = i0 + warp;
     const int64_t at = sAt[i];
-    const float inv = sInv[i];
+    const float inv = sInv[i], up = sUp[i];
 #pragma unroll
     for (int d = 4 * lane; d < HD; d += 128) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -775,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
       }
       acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+      if (F::kInt8) acc.x *= up, acc.y *= up, acc.z *= up, acc.w *= up;
       if (at >= 0 && direct)
         *reinterpret_cast<uint2*>(a.out + at * HD + d) = make_uint2(round2(a.q_f16, acc.x, acc.y), round2(a.q_f16, acc.z, acc.w));
       else if (at >= 0)

@@ -74,3 +74,36 @@ def test_blocks_of_tiny_and_huge_v_scales_in_turn(fmt, D, rows, low, high):
     q = bits16(rng.standard_normal((rows, 16, D)), "bf16")
     out, lse = call(pool, b, dev16(q, "bf16"), 1, 0.25 * D ** -0.5)
     check(pool, b, q, "bf16", 1, 0.25 * D ** -0.5, out, lse, what=f"{fmt} {D} {low} {high}")
+
+
+@pytest.mark.parametrize("fmt", ["int8_side", "int8_inline"])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("keys", [512, 4100])
+@pytest.mark.parametrize("spare", [0, 900])
+def test_sums_of_keys_with_the_largest_v_scales(fmt, D, keys, spare):
+    """mma.sync tiles of 16 pairs and (with unused sequences in the table) of 8: V scales of 2^98, and weights that rise
+    within the softmax's window. The outputs are 127 2^98, the sums on the way there are 2^30 times that."""
+    rng = np.random.default_rng(42)
+    rows, G = 420, 16 if spare == 0 else 8
+    b = Batch(rng, 0, [keys], 1, 64)
+    pool = Pool(rng, fmt, "bf16", b.live, b.num_slots, 1, D)
+    b.row_seq, b.row_len = np.zeros(rows, np.int32), np.full(rows, keys, np.int32)
+    b.table = np.concatenate([b.table, np.full((spare, b.table.shape[1]), -1, dtype=np.int32)])
+    # K = the key's code in every dim, q = 1: logits of code D; the first 128 keys' 5.4 below the others'
+    code = np.where(np.arange(keys) < 128, 1, 2)
+    p = np.arange(keys)
+    slots = torch.from_numpy(b.table[0, p // 64].astype(np.int64) * 64 + p % 64).cuda()
+    k = torch.ones((b.num_slots, 1, D), dtype=torch.int8, device="cuda")
+    k[slots] = torch.from_numpy(np.broadcast_to(code[:, None, None], (keys, 1, D)).astype(np.int8)).cuda()
+    one = torch.ones((b.num_slots, 1), device="cuda")
+    if fmt == "int8_side":
+        pool.cache[0].copy_(k)
+        pool.kw["k_scale_tok"].copy_(one)
+    else:
+        pool.cache[0][..., :D] = k.view(torch.uint8)
+        pool.cache[0][..., D:] = one.view(torch.uint8).view(-1, 1, 4)
+    pool.K = k.cpu().numpy().astype(np.float64)
+    set_v(pool, torch.full((b.num_slots, 1, D), 127, dtype=torch.int8, device="cuda"), one * 2.0 ** 98)
+    q = bits16(np.ones((rows, G, D)), "bf16")
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, 5.4 / D)
+    check(pool, b, q, "bf16", 1, 5.4 / D, out, lse, what=f"{fmt} {D} {keys}")
