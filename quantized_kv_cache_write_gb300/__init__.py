@@ -546,20 +546,23 @@ def _packer(desc, fn: str):
 
 _f32, _half, _int32, _int64 = torch.float32, torch.float16, torch.int32, torch.int64
 _call_append, _call_prefix = _packer(AppendDesc, "qkv_append_rope"), _packer(PrefixDesc, "qkv_prefix_attn")
-_CACHE_BYTES = {QKV_BF16: 2, QKV_F16: 2, QKV_INT8_SIDE: 1, QKV_INT8_INLINE: 1, QKV_E4M3: 1}
+# the tensor types that hold a pool: its values' own, or integers of their size (raw bits)
+_CACHE_TYPES = {QKV_BF16: (torch.bfloat16, torch.int16, torch.uint16), QKV_F16: (torch.float16, torch.int16, torch.uint16),
+                QKV_INT8_SIDE: (torch.int8, torch.uint8), QKV_INT8_INLINE: (torch.int8, torch.uint8),
+                QKV_E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8)}
 
 
 def _need_caches(k_cache, v_cache, fmt: int, H: int, D: int) -> int:
-    """The pool's tensors, contiguous [S, H, D] (inline: [S, H, D + 4]) of the format's element size; S."""
-    size = _CACHE_BYTES.get(fmt)
-    if size is None:
+    """The pool's tensors, contiguous [S, H, D] (inline: [S, H, D + 4]) of a type that holds the format; S."""
+    types = _CACHE_TYPES.get(fmt)
+    if types is None:
         raise ValueError(f"unknown pool format {fmt}")
     want = (H, D + 4 if fmt == QKV_INT8_INLINE else D)
     shape = k_cache.shape
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.shape[1:] != want or t.element_size() != size or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [num_slots, {H}, {want[1]}] pool of {size}-byte values, "
-                             f"got {tuple(t.shape)} {t.dtype}")
+        if t.shape[1:] != want or t.dtype not in types or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [num_slots, {H}, {want[1]}] pool of "
+                             f"{' or '.join(str(d).replace('torch.', '') for d in types)}, got {tuple(t.shape)} {t.dtype}")
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must hold the same number of slots")
     return shape[0]
