@@ -636,6 +636,9 @@ qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
  *                 r * q_stride (a multiple of 8, at least num_q_heads * head_dim); 16 B-aligned.
  *   prefix_blocks int32 [ceil(prefix_len / block_size)] block ids.
  *   block_table   int32 [num_seqs, max_blocks] block ids; max_blocks * block_size < 2^31.
+ *                 rows / num_seqs is taken for the rows per sequence where the tiles' width is chosen
+ *                 (never for what is computed): with several rows per sequence a table cut to the
+ *                 batch's sequences is faster than one with many unused rows (up to 1.5 times).
  *   row_seq       int32 [rows]. -1: a padding row, whose out and lse are left as they were.
  *                 Rows of one sequence that follow each other (draft tokens, a prompt's chunk)
  *                 share the reads of its keys.

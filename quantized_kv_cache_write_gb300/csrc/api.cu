@@ -758,11 +758,16 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   a.prefix_parts = p.prefix_parts;
   a.own_parts = p.own_parts;
   a.prefix_chunk = p.prefix_chunk;
-  // Tiles of 8 pairs where a sequence's rows bring no more than that on average: half of a 16-pair tile would be
-  // empty. In us, 8 | 16: e4m3, 32 sequences of 1400 keys, 4 heads of 128, groups of 8, one row each 17 | 23, two
-  // rows 28 | 27, four rows 46 | 40; bf16 28 | 28, 37 | 31, 61 | 48.
+  // Tiles of 8 pairs where a sequence's rows bring no more than that on average: half of a 16-pair tile of own keys
+  // would be empty. What stands for the sequences is the block table's rows; row_seq is not read here. In us, 8 | 16:
+  // e4m3, 32 sequences of 1400 keys, 4 heads of 128, groups of 8, one row each 16 | 18, four rows 45 | 34; int8 20 |
+  // 22, 51 | 40; bf16 24 | 29, 64 | 43. Tiles of the prefix take pairs of any rows and are full either way, so that 16
+  // reads it half as often: 8 only where mma.sync has no prefix or one of at most twice the rows' own keys. Single
+  // rows behind 2000 shared keys, 8 | 16: 32 rows with 300 of their own, e4m3 24 | 18, int8 25 | 21, with 1400 29 |
+  // 31, 33 | 36; behind 500, 8 rows with 300 8.9 | 10.0, 8.9 | 10.7.
   const int G = d->num_q_heads / d->num_kv_heads;
-  a.mma_pairs = G <= 8 && d->rows * G <= 8 * static_cast<int64_t>(d->num_seqs) ? 8 : 16;
+  const bool prefix_rules = p.ptiles > 0 && d->prefix_len > 2 * static_cast<int64_t>(d->max_row_len - d->prefix_len);
+  a.mma_pairs = G <= 8 && d->rows * G <= 8 * static_cast<int64_t>(d->num_seqs) && !prefix_rules ? 8 : 16;
   if (a.mma_pairs == 8 && p.ptiles > 0) p.ptiles = ceil_div(d->rows * G, 8) * d->num_kv_heads;
   a.prefix_items = p.ptiles * p.prefix_parts;
   a.own_items = p.otiles * p.own_parts;

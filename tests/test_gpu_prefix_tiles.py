@@ -107,3 +107,21 @@ def test_sums_of_keys_with_the_largest_v_scales(fmt, D, keys, spare):
     q = bits16(np.ones((rows, G, D)), "bf16")
     out, lse = call(pool, b, dev16(q, "bf16"), 1, 5.4 / D)
     check(pool, b, q, "bf16", 1, 5.4 / D, out, lse, what=f"{fmt} {D} {keys}")
+
+
+@pytest.mark.parametrize("fmt,act", [("e4m3", "bf16"), ("int8_side", "f16"), ("int8_inline", "bf16"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("prefix,own", [(200, [99, 100, 30]), (201, [100, 99, 3]), (0, [40, 1, 7]), (64, [0, 0, 0])])
+@pytest.mark.parametrize("per,spare", [(1, 0), (1, 40), (3, 0), (3, 40)])
+def test_both_tile_widths_with_and_without_a_prefix(fmt, act, prefix, own, per, spare):
+    """Groups of 4 on mma.sync: prefixes of up to twice the rows' own keys and of more, exact tables and tall ones."""
+    rng = np.random.default_rng(43)
+    b = Batch(rng, prefix, [max(n, per) if n else 0 for n in own], per, 16)
+    if 0 in own:
+        b.row_len = np.full_like(b.row_len, prefix)
+    pool = Pool(rng, fmt, act, b.live, b.num_slots, 2, 128)
+    b.table = np.concatenate([b.table, np.full((spare, b.table.shape[1]), -1, dtype=np.int32)])
+    q = bits16(rng.standard_normal((3 * per, 8, 128)), act)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(pool, b, dev16(q, act), 2, 128 ** -0.5, status=status)
+    check(pool, b, q, act, 2, 128 ** -0.5, out, lse, what=f"{fmt} {prefix} {own} {per} {spare}")
+    assert int(status.item()) == 0
