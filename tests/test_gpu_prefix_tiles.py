@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from dense_harness import Batch, Pool, bits16, dev16
+from dense_harness import ACT, Batch, Pool, bits16, dev16
 from test_gpu_prefix import FMTS, call, check
 
 pytestmark = pytest.mark.gpu
@@ -124,4 +124,39 @@ def test_both_tile_widths_with_and_without_a_prefix(fmt, act, prefix, own, per, 
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     out, lse = call(pool, b, dev16(q, act), 2, 128 ** -0.5, status=status)
     check(pool, b, q, act, 2, 128 ** -0.5, out, lse, what=f"{fmt} {prefix} {own} {per} {spare}")
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("D,G,spare", [(256, 16, 0), (128, 4, 0), (128, 4, 40)])
+def test_padding_empty_and_bad_rows_without_a_merge(fmt, act, shared, D, G, spare):
+    """One range of keys, of the prefix or of the rows' own: its tiles write the outputs themselves, and leave padding
+    rows as they were."""
+    import quantized_kv_cache_write_gb300 as qkv
+    rng = np.random.default_rng(44)
+    b = Batch(rng, 50 if shared else 0, [0] * 7 if shared else [50, 1, 49, 50, 7, 50, 33], 1, 16)
+    pool = Pool(rng, fmt, act, b.live, b.num_slots, 2, D)
+    b.table = np.concatenate([b.table, np.full((spare, b.table.shape[1]), -1, dtype=np.int32)])
+    q = bits16(rng.standard_normal((7, 2 * G, D)), act)
+    assert qkv.qkv_prefix_attn_workspace(qkv.FORMATS[fmt], 7, 2 * G, 2, D, b.prefix, b.max_row_len) == 0
+    seq, ln = b.row_seq.copy(), b.row_len.copy()
+    seq[1] = seq[6] = -1     # padding
+    seq[2] = 7 + spare       # no such sequence
+    ln[3] = 0                # sees nothing
+    ln[4] = 49 if shared else 51  # ends inside the prefix; longer than a row may be
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = torch.full((7, 2 * G, D), 7.0, dtype=ACT[act], device="cuda"), torch.full((7, 2 * G), 7.0, device="cuda")
+    call(pool, b, dev16(q, act), 2, D ** -0.5, row_seq=seq, row_len=ln, out=out, lse=lse, status=status)
+    assert int(status.item()) == 2
+    for r in (1, 6):
+        assert (out[r] == 7).all() and (lse[r] == 7).all(), r
+    for r in (2, 3, 4):
+        assert (out[r] == 0).all() and torch.isneginf(lse[r]).all(), r
+    check(pool, b, q, act, 2, D ** -0.5, out, lse, row_seq=seq, row_len=np.minimum(ln, b.max_row_len) * np.isin(np.arange(7), (0, 1, 5, 6)),
+          what=f"{fmt} {shared} {D} {spare}")
+    # without the bad rows nothing is flagged
+    seq[2], ln[4] = 2, 0
+    status.zero_()
+    call(pool, b, dev16(q, act), 2, D ** -0.5, row_seq=seq, row_len=ln, out=out, lse=lse, status=status)
     assert int(status.item()) == 0
