@@ -69,9 +69,11 @@ typedef enum {
                                 work ran out (not expected on a healthy GPU): the CTA stopped
                                 early, its outputs are incomplete; the kernel returns instead of
                                 hanging. Only the tcgen05 engine and qkv_prefix_attn's tcgen05
-                                tiles wait. A test can make it happen in the engine:
+                                tiles wait. Tests make it happen:
                                 QKV_TEST_TCGEN05_DROP_HANDOFF=<block> in the environment drops
-                                that block's hand-off inside each CTA (never set it otherwise) */
+                                that block's hand-off inside each CTA of the engine,
+                                QKV_TEST_PREFIX_DROP_HANDOFF=<block> inside each CTA of the tiles
+                                (never set them otherwise) */
 
 /*
  * qkv_write_int8 -- quantize new K/V tokens to int8 with one absmax scale per (token, head)

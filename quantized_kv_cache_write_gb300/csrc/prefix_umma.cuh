@@ -41,6 +41,8 @@
 // tensor memory and returns.
 #pragma once
 
+#include <cstdlib>
+
 #include "prefix_attn.cuh"
 
 namespace qkv {
@@ -836,7 +838,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
 #pragma unroll
         for (int i = 0; i < KB / 32; ++i) sts32(sb + U::kRec + n * 4 * KB + 4 * (32 * i + lane), static_cast<uint32_t>(rec[i]));
         __syncwarp();
-        if (lane == 0) bar_arrive(sb + U::kRecFull + 8 * n);
+        if (lane == 0 && jb != a.umma_drop) bar_arrive(sb + U::kRecFull + 8 * n);
       }
     }
   } else if (warp == U::kScWarp) {
@@ -993,7 +995,14 @@ cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
 }
 
 template <int FMT>
-cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
+cudaError_t launch_umma(PrefixArgs a, cudaStream_t stream) {
+  // Test of the lost-wait path: QKV_TEST_PREFIX_DROP_HANDOFF=<block> makes the records' warp leave out the hand-off of
+  // that block in each CTA (read at each launch; unset in any other use).
+  if (const char* t = std::getenv("QKV_TEST_PREFIX_DROP_HANDOFF")) {
+    char* end = nullptr;
+    const long n = std::strtol(t, &end, 10);
+    if (end != t && n >= 0 && n < (1 << 30)) a.umma_drop = static_cast<uint32_t>(n);
+  }
   if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2>(a, stream) : launch_umma<FMT, 256, 1, 1>(a, stream);
   if (a.umma_cg == 2) return launch_umma<FMT, 128, 2, 2>(a, stream);
   return launch_umma<FMT, 128, 1, 1>(a, stream);

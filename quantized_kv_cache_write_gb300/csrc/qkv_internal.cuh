@@ -189,6 +189,7 @@ struct PrefixArgs {
   int umma_pairs = 0;
   int umma_ptiles = 0;
   uint32_t umma_blocks = 0, umma_teams = 0, umma_share = 0, umma_extra = 0;
+  uint32_t umma_drop = UINT32_MAX;  // the block whose records' hand-off a test leaves out; none
 };
 // the mma.sync tiles of (row, head) pairs over prefix_items ranges of the prefix and own_items of the
 // keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
