@@ -10,6 +10,7 @@ package fails loudly if libqkv.so has not been built
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -664,12 +665,13 @@ def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=N
 
 
 def qkv_prefix_attn_workspace(fmt: int, rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
-                              prefix_len: int, max_row_len: int) -> int:
-    """Workspace bytes of a qkv_prefix_attn call of this shape on the current device."""
+                              prefix_len: int, max_row_len: int, device=None) -> int:
+    """Workspace bytes of a qkv_prefix_attn call of this shape on `device`, which is the tensors' (None: the current one)."""
     out = ctypes.c_size_t(0)
-    _check("qkv_prefix_attn_workspace",
-           lib.qkv_prefix_attn_workspace(fmt, rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len,
-                                         ctypes.byref(out)))
+    with contextlib.nullcontext() if device is None else torch.cuda.device(device):
+        _check("qkv_prefix_attn_workspace",
+               lib.qkv_prefix_attn_workspace(fmt, rows, num_q_heads, num_kv_heads, head_dim, prefix_len, max_row_len,
+                                             ctypes.byref(out)))
     return out.value
 
 

@@ -1,5 +1,5 @@
-"""More refusals of the dense cache operators' binding, without a GPU: pools whose tensors hold another type than the
-format's, which the kernels would misread."""
+"""More of the dense cache operators' binding, without a GPU: pools whose tensors hold another type than the format's,
+which the kernels would misread, and the device that a workspace is asked for."""
 
 import pytest
 import torch
@@ -48,3 +48,30 @@ def test_every_type_that_holds_the_format_passes_the_check(lib, fmt, held, other
         for f in _calls(lib, fmt, _pool(fmt, dtype), _pool(fmt, held[0])):
             with pytest.raises(ValueError, match="CUDA device"):
                 f()
+
+
+def test_the_workspace_is_asked_for_on_the_given_device(lib, monkeypatch):  # noqa: F811
+    """The size goes by the device's SMs, and the call runs on its tensors' device."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.device
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Library:
+        def qkv_prefix_attn_workspace(self, *args):
+            seen.append(current[0])
+            return lib.QKV_OK
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(lib, "lib", Library())
+    shape = (lib.QKV_E4M3, 4, 8, 2, 128, 20, 40)
+    lib.qkv_prefix_attn_workspace(*shape)
+    lib.qkv_prefix_attn_workspace(*shape, device=3)
+    assert seen == [0, 3] and current == [0]
