@@ -160,3 +160,81 @@ def test_padding_empty_and_bad_rows_without_a_merge(fmt, act, shared, D, G, spar
     status.zero_()
     call(pool, b, dev16(q, act), 2, D ** -0.5, row_seq=seq, row_len=ln, out=out, lse=lse, status=status)
     assert int(status.item()) == 0
+
+
+# (head dim, rows, groups, prefix): mma.sync tiles of 16 pairs and of 8 (rows alone), tcgen05 tiles on one SM and on two
+KINDS = [(128, 6, 16, 90), (128, 6, 4, 0), (256, 6, 16, 0), (128, 8, 16, 70001), (128, 32, 16, 70001), (256, 8, 16, 70001), (256, 16, 16, 70001)]
+
+
+@pytest.mark.parametrize("fmt,act", FMTS)
+@pytest.mark.parametrize("D,rows,G,prefix", KINDS)
+def test_a_query_that_is_not_finite_spoils_its_own_outputs_only(fmt, act, D, rows, G, prefix):
+    rng = np.random.default_rng(45)
+    b = Batch(rng, prefix, [30 + i for i in range(rows)], 1, 16)
+    pool = Pool(rng, fmt, act, b.live, b.num_slots, 1, D)
+    q = bits16(rng.standard_normal((rows, G, D)), act)
+    qd = dev16(q, act)
+    qd[1, 2] = float("nan")
+    qd[3, 0, 5] = float("inf")
+    qd[4, G - 1, D - 1] = float("-inf")
+    out, lse = call(pool, b, qd, 1, D ** -0.5)
+    bad = np.zeros((rows, G), dtype=bool)
+    bad[1, 2] = bad[3, 0] = bad[4, G - 1] = True
+    at = torch.from_numpy(bad).cuda()
+    assert not torch.isfinite(out.float()[at]).any() and not torch.isfinite(lse[at]).any()
+    ref, ref_lse = call(pool, b, dev16(q, act), 1, D ** -0.5)  # the others as without them, in the last bits too
+    assert torch.equal(out.view(torch.int16)[~at], ref.view(torch.int16)[~at]) and torch.equal(lse[~at], ref_lse[~at])
+    check(pool, b, q, act, 1, D ** -0.5, ref, ref_lse, what=f"{fmt} {D} {rows}")
+
+
+@pytest.mark.parametrize("D,rows,G,prefix", KINDS)
+def test_values_of_a_bf16_pool_up_to_2_to_the_80(D, rows, G, prefix):
+    rng = np.random.default_rng(46)
+    b = Batch(rng, prefix, [700 + i for i in range(rows)], 1, 16)
+    pool = Pool(rng, "bf16", "bf16", b.live, b.num_slots, 1, D)
+    live = torch.from_numpy(b.live).cuda()
+    pool.cache[1][live] = (pool.cache[1][live].float().sign() * 2.0 ** 80).to(torch.bfloat16)
+    pool.V = np.sign(pool.V) * 2.0 ** 80
+    q = bits16(rng.standard_normal((rows, G, D)), "bf16")
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, 2 * D ** -0.5)
+    check(pool, b, q, "bf16", 1, 2 * D ** -0.5, out, lse, what=f"{D} {rows}")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8_side", "int8_inline", "bf16"])
+@pytest.mark.parametrize("D,rows,G,prefix", KINDS)
+@pytest.mark.parametrize("up", [40, -60])
+def test_queries_of_any_magnitude(fmt, D, rows, G, prefix, up):
+    """The query is scaled by a power of two into fp16 for byte pools: rows of other magnitudes, in one tile."""
+    rng = np.random.default_rng(47)
+    b = Batch(rng, prefix, [30 + i for i in range(rows)], 1, 16)
+    pool = Pool(rng, fmt, "bf16", b.live, b.num_slots, 1, D)
+    x = rng.standard_normal((rows, G, D)) * 2.0 ** -rng.integers(0, 12, (rows, G, 1)) * 2.0 ** -rng.integers(0, 12, (rows, G, D))
+    x[0, 0] = 0.0
+    x[2, 1, 1:] *= 2.0 ** -30
+    q = bits16(x * 2.0 ** up, "bf16")
+    scale = 4 * D ** -0.5 * 2.0 ** -up
+    out, lse = call(pool, b, dev16(q, "bf16"), 1, scale)
+    check(pool, b, q, "bf16", 1, scale, out, lse, what=f"{fmt} {D} {rows} {up}")
+
+
+@pytest.mark.parametrize("fmt,act", [("e4m3", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("D,rows,G,prefix", KINDS)
+def test_a_strided_query_and_no_lse(fmt, act, D, rows, G, prefix):
+    """The query as a slice of a packed projection whose other columns hold NaN; the log-sum-exps are not asked for."""
+    import quantized_kv_cache_write_gb300 as qkv
+    rng = np.random.default_rng(48)
+    b = Batch(rng, prefix, [30 + i for i in range(rows)], 1, 16)
+    pool = Pool(rng, fmt, act, b.live, b.num_slots, 1, D)
+    q = bits16(rng.standard_normal((rows, G, D)), act)
+    want, _ = call(pool, b, dev16(q, act), 1, D ** -0.5)
+    wide = torch.full((rows, G + 5, D), float("nan"), dtype=ACT[act], device="cuda")
+    wide[:, 3:3 + G] = dev16(q, act)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    out = torch.full((rows, G, D), float("nan"), dtype=ACT[act], device="cuda")
+    need = qkv.qkv_prefix_attn_workspace(qkv.FORMATS[fmt], rows, G, 1, D, prefix, b.max_row_len, device="cuda:0")
+    qkv.qkv_prefix_attn(wide[:, 3:3 + G], qkv.FORMATS[fmt], *pool.cache, dev(b.table), dev(b.row_seq), dev(b.row_len), 16,
+                        D ** -0.5, max_row_len=b.max_row_len, num_kv_heads=1,
+                        prefix_blocks=dev(b.prefix_blocks) if prefix else None, prefix_len=prefix, out=out,
+                        workspace=torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"), **pool.kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
