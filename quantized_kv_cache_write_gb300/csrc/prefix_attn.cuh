@@ -747,7 +747,9 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
       for (int w = 0; w < kWarps; ++w) {
         const float al = fast_exp2(sM[w][lane] - ref);  // 2^-inf = 0 for a warp without keys
         sum += al * sL[w][lane];
-        sW[w][lane] = F::kInt8 ? al * pow2f(max(sEu[w][lane] - top, -126)) : al;
+        // no keys, no values: -1. A warp with keys counts though its weight is 0: its values may be NaN
+        const bool none = sM[w][lane] == -INFINITY && sL[w][lane] == 0.f;
+        sW[w][lane] = none ? -1.f : F::kInt8 ? al * pow2f(max(sEu[w][lane] - top, -126)) : al;
       }
       const bool any = state != kEmptyRow && (m != -INFINITY || sum != sum);
       sInv[lane] = any ? (direct && FMT == QKV_E4M3 ? a.v_scale_layer : 1.f) / sum : 0.f;
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         else if (any) at = part_at;  // a part without keys leaves no values
         if (!any) {
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) sW[w][lane] = 0.f;
+          for (int w = 0; w < kWarps; ++w) sW[w][lane] = -1.f;
         }
       }
     }
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
       for (int w = 0; w < kWarps; ++w) {
         const float f = sW[w][i];
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (f != 0.f && at >= 0) x = *reinterpret_cast<const float4*>(sO + (w * NP + i) * GM::kORow + d);  // else none there
+        if (f >= 0.f && at >= 0) x = *reinterpret_cast<const float4*>(sO + (w * NP + i) * GM::kORow + d);  // else none there
         acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
       }
       acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;

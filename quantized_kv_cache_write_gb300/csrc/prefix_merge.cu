@@ -57,17 +57,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
     // this warp's parts are sub + WP i; lane i holds the weight of the i-th of 32
     for (int s0 = sub; s0 < parts; s0 += 32 * WP) {
       const int mine_at = s0 + WP * lane;
-      const float mine = mine_at < parts ? expf(__ldcg(lp + at(mine_at)) - ref) : 0.f;
+      const float v = mine_at < parts ? __ldcg(lp + at(mine_at)) : -INFINITY;
+      // a part without keys wrote no values: -1. One with keys counts though its weight is 0: its values may be NaN
+      const float mine = v == -INFINITY ? -1.f : expf(v - ref);
       const int n = min(32, (parts - s0 + WP - 1) / WP);
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
-        const float w = __shfl_sync(0xffffffffu, mine, i);
+        const float got = __shfl_sync(0xffffffffu, mine, i);
+        const bool there = !(got < 0.f);
+        const float w = there ? got : 0.f;
         sum += w;
         const float4* src = reinterpret_cast<const float4*>(op + at(s0 + WP * i) * HD);
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (w != 0.f) x = __ldcg(src + lane + 32 * v);  // a part without keys wrote no values
+          if (there) x = __ldcg(src + lane + 32 * v);
           acc[v].x += w * x.x, acc[v].y += w * x.y, acc[v].z += w * x.z, acc[v].w += w * x.w;
         }
       }

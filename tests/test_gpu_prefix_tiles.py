@@ -238,3 +238,25 @@ def test_a_strided_query_and_no_lse(fmt, act, D, rows, G, prefix):
                         workspace=torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"), **pool.kw)
     torch.cuda.synchronize()
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt,act", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("int8_side", "f16")])
+@pytest.mark.parametrize("D,rows,G,prefix,at", [(*k, at) for k in KINDS for at in ("own", "prefix") if k[3] or at == "own"])
+def test_a_value_that_is_not_finite_shows_though_its_weight_vanishes(fmt, act, D, rows, G, prefix, at):
+    """A key that a row sees with a logit far below the others and a V of NaN: 0 x NaN is NaN, wherever the key falls in
+    the split of the call into ranges and warps."""
+    rng = np.random.default_rng(49)
+    b = Batch(rng, prefix, [300 + i for i in range(rows)], 1, 16)
+    pool = Pool(rng, fmt, act, b.live, b.num_slots, 1, D)
+    p = prefix + 5 if at == "own" else 40
+    slots = [int((b.table[i] if at == "own" else b.prefix_blocks)[p // 16]) * 16 + p % 16 for i in range(rows)]
+    for s in set(slots):
+        if fmt == "int8_side":
+            pool.cache[0][s], pool.kw["k_scale_tok"][s], pool.kw["v_scale_tok"][s] = -127, 10.0, float("nan")
+        elif fmt == "e4m3":
+            pool.cache[0][s], pool.cache[1][s] = 0xFE, 0x7F
+        else:
+            pool.cache[0][s], pool.cache[1][s] = -64.0, float("nan")
+    q = dev16(bits16(np.abs(rng.standard_normal((rows, G, D))) + 0.5, act), act)
+    out, lse = call(pool, b, q, 1, 1.0)
+    assert torch.isnan(out.float()).all() and torch.isfinite(lse).all()
