@@ -643,14 +643,15 @@ qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
  *                 batch's sequences is faster than one with many unused rows (up to 1.5 times).
  *   row_seq       int32 [rows]. -1: a padding row, whose out and lse are left as they were.
  *                 Rows of one sequence that follow each other (draft tokens, a prompt's chunk)
- *                 share the reads of its keys.
+ *                 share the reads of its keys while a tile of 16 (row, head) pairs has room:
+ *                 16 / G rows for G query heads per KV head, none from G = 9 on.
  *   row_len       int32 [rows]: 0 (the row sees nothing: o = 0, lse = -inf) or in [prefix_len,
  *                 max_row_len].
  *   max_row_len   no row is longer; prefix_len <= max_row_len <= max_blocks * block_size and at most
  *                 2^30, else QKV_ERR_ARG. It sizes the launch (a captured graph keeps it).
  *   Flagged with QKV_DEV_BAD_INDEX: a row_seq outside [-1, num_seqs) or a row_len outside its
  *   range (the row is empty), and an unallocated block (id < 0) or a slot >= num_slots among the
- *   keys that a row sees (the key is masked for the rows that it serves).
+ *   prefix's keys, or those behind it that a row sees (the key is masked for the rows that it serves).
  *   out           [rows, num_q_heads, head_dim] in q's type, contiguous, 16 B-aligned; rounded
  *                 once. Must not overlap q.
  *   lse           fp32 [rows, num_q_heads], or NULL.
@@ -659,7 +660,13 @@ qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
  *                 streams, or replays of two captured graphs -- must not share one.
  *   rows * num_q_heads at most 2^31 - 1 (else QKV_ERR_ARG), num_slots * num_kv_heads too, and fewer than 2^31 pieces
  *                 of 128 (row, head) pairs x 64 keys of the prefix (else QKV_ERR_UNSUPPORTED).
- *   int8 V scales of keys that a row sees: magnitudes up to 2^98 (an output past that may come out infinite).
+ *   Numbers: logits, sums and accumulators are fp32; each weight is rounded once to fp16 (bf16 for a bf16 pool)
+ *   before it meets V, relative 2^-11 (2^-8). An int8 key's V scale is multiplied into its weight before that, against a
+ *   bound on the scales seen so far: such a product below fp16's normal range is off by up to 2^-28 of the largest V
+ *   scale that the row sees, its weight there or not. Magnitudes up to 2^98 for int8 V scales, up to 2^80 for the
+ *   values of a bf16 pool (an output past that may come out infinite). With byte pools the query is rounded to fp16
+ *   after a power of two that brings its row's largest value to 2^14 or more: parts below 2^-28 of that lose bits.
+ *   With dev_status NULL a wait that ran out (QKV_DEV_TIMEOUT) leaves incomplete outputs without a sign.
  * Results do not depend on other rows of the batch, up to rounding; calls with the same arguments
  * on the same device give the same bits.
  *

@@ -13,11 +13,14 @@
 // Each warp streams its own key tiles through a cp.async ring; warps meet once, at the end, to join
 // their sums. Tiles start at positions that are multiples of their size, so where blocks are such
 // multiples too a tile is one run of slots and costs one table lookup. Quantised pools are multiplied
-// in fp16: codes are exact fp16 values, the query is pre-scaled by a power of two into fp16 (exact except
-// for values 2^-39 below the row's largest), the K scale multiplies the logit, the V scale p. p (times the V
-// scale and a power of two) is rounded to the 16-bit operand type once: relative 2^-12 (fp16) or
-// 2^-9 (bf16), independent from key to key, so an output has about the rounding error of its own
-// 16-bit type or less.
+// in fp16: codes are exact fp16 values, the query is pre-scaled by a power of two into fp16 (its largest
+// value between 2^14 and 2^15, so that bf16 values lose bits from 2^-31 of it on and fp16 values from 2^-28; both
+// vanish below 2^-39), the K scale multiplies the logit, the V scale p. p (times the V
+// scale and a power of two) is rounded to the 16-bit operand type once: relative 2^-11 (fp16) or
+// 2^-8 (bf16) at most, independent from key to key. The sum is that of the unrounded p, so a single heavy key's
+// rounding stays in the output: at most as much again as the output's own rounding. Measured against 64 bits
+// (relative, root mean square; a plain fp32 form in brackets): bf16 pool 0.0022 (0.0017), fp16 outputs behind 65536
+// int8 keys 0.00029 (0.00021), the other cases as the plain form.
 //
 // Measured: 64 rows x 64 heads of 128 over 0 to 8192 e4m3 keys of their own, no prefix (539 MB), 101 us in this
 // kernel (5.3 TB/s); 128 rows x 32 heads over 16 to 2048 bf16 keys (270 MB) 58 us (4.7 TB/s). Between its start and
@@ -56,10 +59,14 @@ struct Geom {
   static constexpr int kRow = F::kBytes ? HD : 2 * HD;              // bytes of a record's values
   static constexpr int kGlobalRow = F::kInline ? HD + 4 : kRow;     // bytes between records
   // Keys of a warp tile (32 where rows are short: the softmax step's fixed cost is shared), ring stages and CTAs
-  // per SM: 64 to 128 KB of copies in flight per SM. Tiles of 8 pairs with rows of 128 B, us with 16 keys in three
-  // stages on four CTAs | 32 keys in two on three, the next tile ahead in L2: e4m3, 64 rows x 64 heads of 0 to
-  // 8192 keys 114 | 105, 4 rows of 1000 9.0 | 8.3, 256 rows of 50 to 300 35 | 37; inline int8, 64 rows of 0 to
-  // 4096 131 | 125; int8 with side scales 79 | 86, so that one keeps the former.
+  // per SM. A warp starts the copy of a tile when it is done with the one before: kStages - 1 tiles are in flight while
+  // it waits, kStages - 2 while it computes, and the SM's other warps cover that (8 to 16 of them; up to 128 KB in
+  // flight). Started before the tile at hand is computed instead, us after that | before: heads of 128, 8 pairs, e4m3
+  // 106 | 105, inline int8 127 | 129, bf16 59.6 | 58.4, 16 pairs, int8 66 | 62.5; heads of 256, 8 pairs, e4m3 83 | 78,
+  // bf16 78 | 81, 16 pairs, int8 61.5 | 63; drafts 42.6 | 44: no gain on the whole. Tiles of 8 pairs with rows of
+  // 128 B, us with 16 keys in three stages on four CTAs | 32 keys in two on three, the next tile ahead in L2: e4m3, 64
+  // rows x 64 heads of 0 to 8192 keys 114 | 105, 4 rows of 1000 9.0 | 8.3, 256 rows of 50 to 300 35 | 37; inline int8,
+  // 64 rows of 0 to 4096 131 | 125; int8 with side scales 79 | 86 (the cause is not known), so that one keeps the former.
   static constexpr bool kShort = kRow == 128 && (NP == 16 || FMT != QKV_INT8_SIDE);
   static constexpr int kKeys = kShort ? 32 : 16;
   static constexpr int kStages = kShort || (kRow == 256 && NP == 8) ? 2 : 3;
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     cp_async_commit();
   };
 
-  // The tile after the ring's into L2: one more tile in flight per warp than the ring has room for.
+  // The tile after the one whose copy has just been started into L2, while that one is copied and computed.
   auto prefetch = [&](int i, int blk) {
     if (!GM::kAhead || i >= my) return;
     const int key = lane & (TK - 1), pos = tile_pos(i) + key;
