@@ -104,8 +104,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
 }
 
 // Four warps share a pair where there are at least so many parts and not enough pairs to fill the GPU with one
-// warp each. 640 pairs, 18 parts: 128 us for the call, 137 with one warp; 888 pairs, 8 parts: 23.3 us, 24.6; 4096
-// pairs: 105, 102.
+// warp each. us for the call, one warp | four: int8, 16 heads of 256, 8192 own keys: 16 pairs of 32 parts 20.5 | 15.0,
+// 128 of 32 26.2 | 19.7, 512 of 16 51 | 48, 2048 of 16 161 | 158, 4096 of 10 276 | 278; one row of 65536, 16 of 128 parts
+// 49 | 27. e4m3, 64 heads of 128, 4096 own keys: 256 pairs of 8 parts 15.1 | 13.8, 2048 of 8 67.7 | 67.1, 4096 of 5 108 |
+// 111; behind 32768 shared keys 512 of 23 39.8 | 35.5, 2048 of 12 57.5 | 57.7, 4096 of 12 82.3 | 85.7. bf16, 16 heads of
+// 256 behind 20000: 128 of 86 49.5 | 31.8, 2048 of 13 95.2 | 94.6.
 constexpr int kSharedParts = 8;
 constexpr int64_t kSharedPairs = 2048;
 
