@@ -43,30 +43,30 @@ def _read(name, seqs, lo, hi, hkv, d, fmt, out, block, rot=0, pairs=False):
 def listed():
     return [
         # a decode step of a model with image positions: nothing but latency
-        _append("append one token, 3 axes", 1, 16, 1, 256, 128, "int8_side", False),
+        _append("append one token 3 axes", 1, 16, 1, 256, 128, "int8_side", False),
         # an odd batch of image patches: half activations, inline records, adjacent pairs, woven axes
-        _append("append 1369 patches, inline", 1369, 16, 2, 128, 96, "int8_inline", True, act="f16", pairs=True, block=5),
+        _append("append 1369 patches inline", 1369, 16, 2, 128, 96, "int8_inline", True, act="f16", pairs=True, block=5),
         # a packed video prompt into an unquantised pool, the repository's largest append
-        _append("append 16384 video, bf16", 16384, 32, 8, 128, 128, "bf16", False, block=64),
+        _append("append 16384 video bf16", 16384, 32, 8, 128, 128, "bf16", False, block=64),
         # one request decodes one token in a layer with a sliding window and capped scores: latency
-        _attn("decode, 1 row, capped window", 1, (1, 1), (8191, 8191), 16, 1, 256, "int8_side", 16, window=4096, cap=50.0),
+        _attn("decode 1 row capped window", 1, (1, 1), (8191, 8191), 16, 1, 256, "int8_side", 16, window=4096, cap=50.0),
         # a serving batch of ragged lengths, capped scores
-        _attn("decode, 64 rows, capped, e4m3", 64, (1, 1), (0, 8191), 64, 8, 128, "e4m3", 64, cap=30.0),
+        _attn("decode 64 rows capped e4m3", 64, (1, 1), (0, 8191), 64, 8, 128, "e4m3", 64, cap=30.0),
         # draft tokens of a model with a distance bias, unquantised pool
-        _attn("decode, 8 x 5 drafts, bias, bf16", 8, (5, 5), (1000, 30000), 32, 4, 128, "bf16", 32, bias=True),
+        _attn("decode 8 x 5 drafts bias bf16", 8, (5, 5), (1000, 30000), 32, 4, 128, "bf16", 32, bias=True),
         # a whole prompt, the repository's chunked-prefill length, capped scores
-        _attn("prompt 8192, capped, int8", 1, (8192, 8192), (0, 0), 16, 1, 256, "int8_side", 16, cap=50.0),
+        _attn("prompt 8192 capped int8", 1, (8192, 8192), (0, 0), 16, 1, 256, "int8_side", 16, cap=50.0),
         # prompts packed of documents that do not see one another, with a window
-        _attn("prompts, documents, bf16", 6, (300, 4000), (0, 0), 32, 8, 128, "bf16", 32, mask="docs", doc=700, window=1024),
+        _attn("prompts documents bf16", 6, (300, 4000), (0, 0), 32, 8, 128, "bf16", 32, mask="docs", doc=700, window=1024),
         # odd sizes everywhere: prefix mask, distance bias, half activations, groups of 12, blocks of 7, empty rows
-        _attn("prompts, prefix mask, bias, odd", 3, (77, 1501), (0, 999), 24, 2, 256, "e4m3", 7, mask="prefix", bias=True,
+        _attn("prompts prefix mask bias odd", 3, (77, 1501), (0, 999), 24, 2, 256, "e4m3", 7, mask="prefix", bias=True,
               hole=29, act="f16"),
         # the largest: the last chunk of the long context
-        _attn("chunk 2048 behind 129024, int8", 1, (2048, 2048), (129024, 129024), 16, 1, 256, "int8_side", 64),
+        _attn("chunk 2048 behind 129024 int8", 1, (2048, 2048), (129024, 129024), 16, 1, 256, "int8_side", 64),
         # a short document's keys turned back, to be appended at another place
-        _read("read 333 turned back, f16", 1, 333, 333, 2, 128, "int8_inline", "f16", 5, rot=96, pairs=True),
+        _read("read 333 turned back f16", 1, 333, 333, 2, 128, "int8_inline", "f16", 5, rot=96, pairs=True),
         # a long conversation handed to another program
-        _read("read 131072, int8 to bf16", 1, 131072, 131072, 1, 256, "int8_side", "bf16", 16),
+        _read("read 131072 int8 to bf16", 1, 131072, 131072, 1, 256, "int8_side", "bf16", 16),
     ]
 
 
