@@ -64,7 +64,8 @@ typedef enum {
 /* Bits OR-ed into *dev_status by the kernels. */
 #define QKV_DEV_BAD_SLOT 1u  /* a write's slot is invalid (a slot_mapping entry >= num_slots or
                                  < -1, or a bad paged entry, see qkv_write_ex): token skipped */
-#define QKV_DEV_BAD_INDEX 2u /* top-k entry >= num_slots or < -1: treated as padding (-1) */
+#define QKV_DEV_BAD_INDEX 2u /* top-k entry >= num_slots or < -1: treated as padding (-1); the other
+                                reads say in their own text what they flag with it */
 #define QKV_DEV_TIMEOUT 4u   /* a gather CTA's bounded wait for its own copies or tensor-core
                                 work ran out (not expected on a healthy GPU): the CTA stopped
                                 early, its outputs are incomplete; the kernel returns instead of
@@ -615,6 +616,95 @@ typedef struct {
 } qkv_append_desc;
 
 qkv_status qkv_append_rope(const qkv_append_desc* desc, void* stream);
+
+/*
+ * qkv_append_axes -- qkv_append_rope for tokens whose rotary positions have several axes (time, height and width of an
+ * image's or a video's patches): each pair of head dims turns by its own axis's position.
+ *   Pair i of token t turns by the angle of cos_sin[p, i], cos_sin[p, rotary_dim / 2 + i] at
+ *     p = axis_pos[pair_axis[i], t]
+ *   with the arithmetic, storage and errors of qkv_append_rope, which this call equals where all axes hold the same position.
+ *
+ *   append        qkv_append_rope's fields with its meanings, but for
+ *     size        sizeof(qkv_append_axes_desc).
+ *     token_pos   only where K and V go: with paged addressing the token's position in its sequence, as for
+ *                 qkv_write_ex (-1: K and V are not stored, q is still rotated); NULL with slot_mapping, else QKV_ERR_ARG.
+ *   axis_pos      int32 [num_axes, num_tokens], 4 B-aligned. A token whose position on axis 0 is -1 is skipped (nothing of
+ *                 it is written); one with a position outside [0, num_positions) on any axis sets QKV_DEV_BAD_SLOT and
+ *                 is skipped likewise.
+ *   num_axes      1 to QKV_MAX_AXES, else QKV_ERR_ARG.
+ *   pair_axis     HOST array uint8 [rotary_dim / 2], read before the call returns: the axis of each pair, below num_axes
+ *                 (else QKV_ERR_ARG), in any order (runs of pairs, or axes that take turns). NULL: axis 0 for all.
+ */
+#define QKV_MAX_AXES 4
+typedef struct {
+  qkv_append_desc append;
+  const int32_t* axis_pos;
+  int num_axes;
+  const uint8_t* pair_axis;
+} qkv_append_axes_desc;
+
+qkv_status qkv_append_axes(const qkv_append_axes_desc* desc, void* stream);
+
+/*
+ * qkv_read -- the pool read back: K and V rows of given tokens, dequantised into contiguous tensors; with cos_sin, K
+ * turned back to before its rotation, so that it can be appended at other positions.
+ *   value = code * scale in fp32 (E4M3: the layer's scale; 16-bit pools: the value itself); turned back, for pair i of
+ *   token t (paired as for qkv_append_rope) with c, s of cos_sin at p = axis_pos[pair_axis[i], t]:
+ *     a' = fl(fl(a c) + fl(b s)),  b' = fl(fl(b c) - fl(a s));
+ *   then rounded once to the output's type. A 16-bit pool's rows into their own type are copied bit for bit.
+ *
+ *   size          sizeof(qkv_read_desc), for the layout check (else QKV_ERR_ARG).
+ *   fmt, k_cache, v_cache, k_scale, v_scale, k_scale_layer, v_scale_layer, num_slots, num_kv_heads, head_dim
+ *                 the pool, as for qkv_append_rope.
+ *   num_tokens    num_tokens * num_kv_heads at most 2^32, else QKV_ERR_ARG.
+ *   slot_mapping  int64 [num_tokens] slot ids, or NULL: token_seq, token_pos, block_table, num_seqs, max_blocks and
+ *                 block_size as for qkv_write_ex. A slot (position) of -1 skips the token: its rows of k_out and v_out are
+ *                 left as they were. An invalid slot, position, sequence or block sets QKV_DEV_BAD_INDEX and skips it
+ *                 likewise. A slot may be read more than once.
+ *   k_out, v_out  [num_tokens, num_kv_heads, head_dim] of out_type, token t at element t * out_stride (a multiple of 8,
+ *                 at least one token's heads); 16 B-aligned. Either may be NULL, and is then not read; both: QKV_ERR_ARG.
+ *                 They must not overlap the pool or each other.
+ *   cos_sin       fp32 [num_positions, rotary_dim], 16 B-aligned, or NULL: K as it is stored. rotary_dim, interleaved,
+ *                 axis_pos, num_axes and pair_axis as for qkv_append_axes (a plain rotation: num_axes 1, pair_axis NULL);
+ *                 a token whose position on axis 0 is -1 is skipped, one with an invalid position sets
+ *                 QKV_DEV_BAD_INDEX and is skipped. Without k_out nothing is turned and no position looked at.
+ */
+typedef enum { QKV_OUT_BF16 = 0, QKV_OUT_F16 = 1, QKV_OUT_F32 = 2 } qkv_out_type;
+typedef struct {
+  size_t size;
+  qkv_format fmt;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  int num_kv_heads;
+  int head_dim;
+  int64_t num_tokens;
+  const int64_t* slot_mapping;
+  const int32_t* token_seq;
+  const int32_t* token_pos;
+  const int32_t* block_table;
+  int64_t num_seqs;
+  int max_blocks;
+  int block_size;
+  qkv_out_type out_type;
+  void* k_out;
+  void* v_out;
+  int64_t out_stride;
+  const float* cos_sin;
+  int64_t num_positions;
+  int rotary_dim;
+  int interleaved;
+  const int32_t* axis_pos;
+  int num_axes;
+  const uint8_t* pair_axis;
+  uint32_t* dev_status;
+} qkv_read_desc;
+
+qkv_status qkv_read(const qkv_read_desc* desc, void* stream);
 
 /*
  * qkv_prefix_attn -- dense decode attention over a paged pool for a batch whose sequences share a

@@ -25,6 +25,8 @@ QKV_BF16, QKV_INT8_SIDE, QKV_INT8_INLINE, QKV_E4M3, QKV_F16 = range(5)
 QKV_DEV_BAD_SLOT = 1
 QKV_DEV_BAD_INDEX = 2
 QKV_DEV_TIMEOUT = 4
+QKV_OUT_BF16, QKV_OUT_F16, QKV_OUT_F32 = range(3)
+QKV_MAX_AXES = 4
 QSA_ENGINE_DEFAULT, QSA_ENGINE_TCGEN05, QSA_ENGINE_PERSISTENT = 0, 1, 2
 HEAD_DIM = 256
 FORMATS = {"bf16": QKV_BF16, "int8_side": QKV_INT8_SIDE, "int8_inline": QKV_INT8_INLINE, "e4m3": QKV_E4M3,
@@ -130,13 +132,13 @@ _ACT16 = (torch.bfloat16, torch.float16)
 
 def _tokens(k: torch.Tensor, v: torch.Tensor):
     """[T, Hkv, D] views sharing one token stride; heads and dims contiguous. (The stride of a
-    dimension of size 1 is never used, so it may be anything.)"""
+    dimension of size 1 is never used, so it may be anything, as any may without tokens.)"""
     shape = k.shape
     if len(shape) != 3 or v.shape != shape or k.dtype not in _ACT16 or v.dtype != k.dtype:
         raise ValueError("k and v must be bf16 (or both fp16) [num_tokens, num_kv_heads, head_dim] of equal shape")
     T, H, D = shape
     (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
-    if (D != 1 and (kd != 1 or vd != 1)) or (H != 1 and (kh != D or vh != D)) or (T > 1 and kt != vt):
+    if T > 0 and ((D != 1 and (kd != 1 or vd != 1)) or (H != 1 and (kh != D or vh != D)) or (T > 1 and kt != vt)):
         raise ValueError("k and v need contiguous heads and one shared token stride")
     return T, H, D, (kt if T > 1 else H * D)
 
@@ -502,6 +504,22 @@ class AppendDesc(ctypes.Structure):
                 ("dev_status", _p)]
 
 
+class AppendAxesDesc(ctypes.Structure):
+    """qkv_append_axes_desc of include/qkv.h, field for field (its first member's fields in place)."""
+    _fields_ = [*AppendDesc._fields_, ("axis_pos", _p), ("num_axes", _i32), ("pair_axis", _p)]
+
+
+class ReadDesc(ctypes.Structure):
+    """qkv_read_desc of include/qkv.h, field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("fmt", _i32), ("k_cache", _p), ("v_cache", _p), ("k_scale", _p),
+                ("v_scale", _p), ("k_scale_layer", _f32), ("v_scale_layer", _f32), ("num_slots", _i64),
+                ("num_kv_heads", _i32), ("head_dim", _i32), ("num_tokens", _i64), ("slot_mapping", _p),
+                ("token_seq", _p), ("token_pos", _p), ("block_table", _p), ("num_seqs", _i64), ("max_blocks", _i32),
+                ("block_size", _i32), ("out_type", _i32), ("k_out", _p), ("v_out", _p), ("out_stride", _i64),
+                ("cos_sin", _p), ("num_positions", _i64), ("rotary_dim", _i32), ("interleaved", _i32),
+                ("axis_pos", _p), ("num_axes", _i32), ("pair_axis", _p), ("dev_status", _p)]
+
+
 class PrefixDesc(ctypes.Structure):
     """qkv_prefix_desc of include/qkv.h, field for field."""
     _fields_ = [("size", ctypes.c_size_t), ("fmt", _i32), ("q_fp16", _i32), ("q", _p), ("q_stride", _i64),
@@ -515,12 +533,17 @@ class PrefixDesc(ctypes.Structure):
 
 lib.qkv_append_rope.argtypes = [ctypes.POINTER(AppendDesc), _p]
 lib.qkv_append_rope.restype = ctypes.c_int
+lib.qkv_append_axes.argtypes = [ctypes.POINTER(AppendAxesDesc), _p]
+lib.qkv_append_axes.restype = ctypes.c_int
+lib.qkv_read.argtypes = [ctypes.POINTER(ReadDesc), _p]
+lib.qkv_read.restype = ctypes.c_int
 lib.qkv_prefix_attn.argtypes = [ctypes.POINTER(PrefixDesc), _p]
 lib.qkv_prefix_attn.restype = ctypes.c_int
 lib.qkv_prefix_attn_workspace.argtypes = [_i32, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
 lib.qkv_prefix_attn_workspace.restype = ctypes.c_int
 
 _APPEND_SIZE, _PREFIX_SIZE = ctypes.sizeof(AppendDesc), ctypes.sizeof(PrefixDesc)
+_AXES_SIZE, _READ_SIZE = ctypes.sizeof(AppendAxesDesc), ctypes.sizeof(ReadDesc)
 
 
 def _packer(desc, fn: str):
@@ -547,6 +570,7 @@ def _packer(desc, fn: str):
 
 _f32, _half, _int32, _int64 = torch.float32, torch.float16, torch.int32, torch.int64
 _call_append, _call_prefix = _packer(AppendDesc, "qkv_append_rope"), _packer(PrefixDesc, "qkv_prefix_attn")
+_call_axes, _call_read = _packer(AppendAxesDesc, "qkv_append_axes"), _packer(ReadDesc, "qkv_read")
 # the tensor types that hold a pool: its values' own, or integers of their size (raw bits)
 _CACHE_TYPES = {QKV_BF16: (torch.bfloat16, torch.int16, torch.uint16), QKV_F16: (torch.float16, torch.int16, torch.uint16),
                 QKV_INT8_SIDE: (torch.int8, torch.uint8), QKV_INT8_INLINE: (torch.int8, torch.uint8),
@@ -574,7 +598,7 @@ def _strided(name: str, t, T: int, H: int, D: int) -> int:
     if t.shape != (T, H, D):
         raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
     token, head, dim = t.stride()
-    if (D != 1 and dim != 1) or (H != 1 and head != D):
+    if T > 0 and ((D != 1 and dim != 1) or (H != 1 and head != D)):
         raise ValueError(f"{name} needs contiguous heads")
     return token if T > 1 else H * D
 
@@ -613,18 +637,9 @@ def _plain(name: str, t, dtype, numel: int):
     return t.data_ptr()
 
 
-def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=None, q_out=None, slot_mapping=None,
-                    token_seq=None, block_table=None, block_size: int = 1, k_scale=None, v_scale=None,
-                    k_scale_layer: float = 1.0, v_scale_layer: float = 1.0, interleaved: bool = False,
-                    dev_status=None, stream=None):
-    """Rotate q and K by their tokens' positions and store K and V in the pool, in one launch
-    (see qkv_append_rope in qkv.h).
-
-    k, v bf16 or fp16 [T, Hkv, D] (slices of a packed projection are fine); q the same [T, Hq, D]
-    with q_out its rotation (q itself: in place), or both None; cos_sin fp32 [positions,
-    rotary_dim], cosines then sines; token_pos int32 [T] (-1 skips the token); slot_mapping int64
-    [T], or token_seq int32 [T] with block_table int32 [num_seqs, max_blocks] and block_size.
-    """
+def _append(k, v, fmt, k_cache, v_cache, cos_sin, token_pos, q, q_out, slot_mapping, token_seq, block_table, block_size,
+            k_scale, v_scale, k_scale_layer, v_scale_layer, interleaved, dev_status, size, axis_pos=None, pair_axis=None):
+    """The checks of an append's tensors: the device, the descriptor's fields, and what holds its host array."""
     T, H, D, stride = _tokens(k, v)
     S = _need_caches(k_cache, v_cache, fmt, H, D)
     angles = cos_sin.shape
@@ -656,12 +671,125 @@ def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=N
             raise ValueError("block_table must be [num_seqs, max_blocks]")
         seqs, blocks = table
         btp = _plain("block_table", block_table, _int32, seqs * blocks)
+    more, held = (), None
+    if size == _AXES_SIZE:
+        *more, held = _axes(axis_pos, pair_axis, rot, T)
     dev = _on_cuda(k, v, q, q_out, k_cache, v_cache, cos_sin, token_pos, slot_mapping, token_seq, block_table, k_scale,
-                   v_scale, dev_status)
-    _call_append(dev, stream, _APPEND_SIZE, fmt, k.dtype is _half, qp, qop, k.data_ptr(), v.data_ptr(), T, Hq, H, D, qs,
-                 qos, stride, csp, P, rot, 1 if interleaved else 0, tpp, smp, tsp, btp, seqs, blocks, block_size,
-                 k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S,
-                 0 if dev_status is None else dev_status.data_ptr())
+                   v_scale, dev_status, axis_pos)
+    return dev, held, (size, fmt, k.dtype is _half, qp, qop, k.data_ptr(), v.data_ptr(), T, Hq, H, D, qs, qos, stride, csp, P,
+                 rot, 1 if interleaved else 0, tpp, smp, tsp, btp, seqs, blocks, block_size, k_cache.data_ptr(),
+                 v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S,
+                 0 if dev_status is None else dev_status.data_ptr(), *more)
+
+
+def qkv_append_rope(k, v, fmt: int, k_cache, v_cache, cos_sin, token_pos, *, q=None, q_out=None, slot_mapping=None,
+                    token_seq=None, block_table=None, block_size: int = 1, k_scale=None, v_scale=None,
+                    k_scale_layer: float = 1.0, v_scale_layer: float = 1.0, interleaved: bool = False,
+                    dev_status=None, stream=None):
+    """Rotate q and K by their tokens' positions and store K and V in the pool, in one launch
+    (see qkv_append_rope in qkv.h).
+
+    k, v bf16 or fp16 [T, Hkv, D] (slices of a packed projection are fine); q the same [T, Hq, D]
+    with q_out its rotation (q itself: in place), or both None; cos_sin fp32 [positions,
+    rotary_dim], cosines then sines; token_pos int32 [T] (-1 skips the token); slot_mapping int64
+    [T], or token_seq int32 [T] with block_table int32 [num_seqs, max_blocks] and block_size.
+    """
+    dev, _, fields = _append(k, v, fmt, k_cache, v_cache, cos_sin, token_pos, q, q_out, slot_mapping, token_seq, block_table,
+                             block_size, k_scale, v_scale, k_scale_layer, v_scale_layer, interleaved, dev_status,
+                             _APPEND_SIZE)
+    _call_append(dev, stream, *fields)
+
+
+def _axes(axis_pos, pair_axis, rot: int, T: int):
+    """Addresses of the positions by axis and of the pairs' axes, the number of axes, and what holds the latter."""
+    shape = axis_pos.shape
+    if len(shape) != 2 or shape[1] != T:
+        raise ValueError(f"axis_pos must be [num_axes, {T}], got {tuple(shape)}")
+    app = _plain("axis_pos", axis_pos, _int32, shape[0] * T)
+    if pair_axis is None:
+        return app, shape[0], 0, None
+    held = bytearray(pair_axis)  # a value that is no byte: ValueError
+    if len(held) != rot // 2 or not held:
+        raise ValueError(f"pair_axis must hold an axis for each of the {rot // 2} pairs, got {len(held)}")
+    return app, shape[0], ctypes.addressof(ctypes.c_char.from_buffer(held)), held
+
+
+def qkv_append_axes(k, v, fmt: int, k_cache, v_cache, cos_sin, axis_pos, pair_axis=None, *, q=None, q_out=None,
+                    slot_mapping=None, token_seq=None, token_pos=None, block_table=None, block_size: int = 1, k_scale=None,
+                    v_scale=None, k_scale_layer: float = 1.0, v_scale_layer: float = 1.0, interleaved: bool = False,
+                    dev_status=None, stream=None):
+    """qkv_append_rope for tokens whose positions have several axes (see qkv_append_axes in qkv.h).
+
+    axis_pos int32 [axes, T] (-1 on axis 0 skips the token); pair_axis the axis of each of the
+    rotary_dim / 2 pairs, a sequence of integers on the host (None: axis 0 for all); slot_mapping, or
+    token_seq, token_pos (int32 [T], the positions in the sequence) and block_table; the rest as for
+    qkv_append_rope.
+    """
+    dev, held, fields = _append(k, v, fmt, k_cache, v_cache, cos_sin, token_pos, q, q_out, slot_mapping, token_seq,
+                                block_table, block_size, k_scale, v_scale, k_scale_layer, v_scale_layer, interleaved,
+                                dev_status, _AXES_SIZE, axis_pos, pair_axis)
+    _call_axes(dev, stream, *fields)
+    del held  # read by the call
+
+
+_OUT_TYPES = {torch.bfloat16: QKV_OUT_BF16, torch.float16: QKV_OUT_F16, torch.float32: QKV_OUT_F32}
+
+
+def qkv_read(fmt: int, k_cache, v_cache, *, k_out=None, v_out=None, slot_mapping=None, token_seq=None, token_pos=None,
+             block_table=None, block_size: int = 1, k_scale=None, v_scale=None, k_scale_layer: float = 1.0,
+             v_scale_layer: float = 1.0, cos_sin=None, axis_pos=None, pair_axis=None, interleaved: bool = False,
+             dev_status=None, stream=None):
+    """The pool read back: K and V rows of given tokens, dequantised, K turned back to before its rotation
+    where cos_sin is given (see qkv_read in qkv.h).
+
+    k_out, v_out bf16, fp16 or fp32 [T, Hkv, D] of one type and token stride (either may be None);
+    slot_mapping int64 [T], or token_seq, token_pos int32 [T] with block_table and block_size; cos_sin
+    fp32 [positions, rotary_dim] with axis_pos int32 [axes, T] and pair_axis as for qkv_append_axes.
+    """
+    one = k_out if k_out is not None else v_out
+    if one is None:
+        raise ValueError("k_out or v_out must be given")
+    shape = one.shape
+    kind = _OUT_TYPES.get(one.dtype)
+    if len(shape) != 3 or kind is None:
+        raise ValueError("k_out and v_out must be bf16, fp16 or fp32 [tokens, num_kv_heads, head_dim]")
+    T, H, D = shape
+    stride = _strided("k_out" if k_out is not None else "v_out", one, T, H, D)
+    if k_out is not None and v_out is not None:
+        if v_out.dtype is not k_out.dtype or _strided("v_out", v_out, T, H, D) != stride:
+            raise ValueError("k_out and v_out must have one type and one token stride")
+    S = _need_caches(k_cache, v_cache, fmt, H, D)
+    smp = _plain("slot_mapping", slot_mapping, _int64, T)
+    tsp = _plain("token_seq", token_seq, _int32, T)
+    tpp = _plain("token_pos", token_pos, _int32, T)
+    ksp = _plain("k_scale", k_scale, _f32, S * H)
+    vsp = _plain("v_scale", v_scale, _f32, S * H)
+    if dev_status is not None:
+        _need("dev_status", dev_status, _WORD)
+    btp = seqs = blocks = 0
+    if block_table is not None:
+        table = block_table.shape
+        if len(table) != 2:
+            raise ValueError("block_table must be [num_seqs, max_blocks]")
+        seqs, blocks = table
+        btp = _plain("block_table", block_table, _int32, seqs * blocks)
+    csp = P = rot = app = axes = pap = 0
+    held = None
+    if (cos_sin is None) != (axis_pos is None):
+        raise ValueError("cos_sin and axis_pos come together")
+    if cos_sin is not None:
+        if len(cos_sin.shape) != 2:
+            raise ValueError("cos_sin must be [positions, rotary_dim]")
+        P, rot = cos_sin.shape
+        csp = _plain("cos_sin", cos_sin, _f32, P * rot)
+        app, axes, pap, held = _axes(axis_pos, pair_axis, rot, T)
+    dev = _on_cuda(one, k_out, v_out, k_cache, v_cache, slot_mapping, token_seq, token_pos, block_table, k_scale, v_scale,
+                   cos_sin, axis_pos, dev_status)
+    _call_read(dev, stream, _READ_SIZE, fmt, k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer),
+               float(v_scale_layer), S, H, D, T, smp, tsp, tpp, btp, seqs, blocks, block_size, kind,
+               0 if k_out is None else k_out.data_ptr(), 0 if v_out is None else v_out.data_ptr(), stride, csp, P, rot,
+               1 if interleaved else 0, app, axes, pap, 0 if dev_status is None else dev_status.data_ptr())
+    del held  # read by the call
 
 
 def qkv_prefix_attn_workspace(fmt: int, rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -42,6 +42,8 @@ SOURCES = [
     "gather_f16q_e4m3.cu",
     "gather_f16q_f16.cu",
     "append.cu",
+    "append_axes.cu",
+    "read.cu",
     "prefix_int8_side.cu",
     "prefix_int8_inline.cu",
     "prefix_e4m3.cu",
@@ -54,7 +56,7 @@ SOURCES = [
     "prefix_umma_f16.cu",
     "prefix_merge.cu",
 ]
-HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "prefix_attn.cuh", "prefix_umma.cuh"]
+HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "rope.cuh", "append.cuh", "prefix_attn.cuh", "prefix_umma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

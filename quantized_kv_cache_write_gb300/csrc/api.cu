@@ -461,10 +461,10 @@ qkv_status qsa_splitk_merge(const float* o_part, const float* lse_part, int64_t 
 
 namespace {
 
-// The descriptor's paged or slot-id addressing, and the inputs of an append.
-qkv_status check_append(const qkv_append_desc* d) {
+// The descriptor's paged or slot-id addressing, and the inputs of an append. axes: token_pos belongs to the paged addressing.
+qkv_status check_append(const qkv_append_desc* d, bool axes = false) {
   const bool paged = d->slot_mapping == nullptr;
-  if (!paged && (d->token_seq || d->block_table)) return QKV_ERR_ARG;  // one addressing only
+  if (!paged && (d->token_seq || d->block_table || (axes && d->token_pos))) return QKV_ERR_ARG;  // one addressing only
   const bool f16 = d->act_fp16 == 1;
   switch (d->fmt) {
     case QKV_BF16: if (f16) return QKV_ERR_ARG; break;  // a 16-bit pool takes activations of its own type
@@ -493,7 +493,7 @@ qkv_status check_append(const qkv_append_desc* d) {
   // fewer, which is at most T rows / 2 (rows is 3 or more, or 2: one unit), so 2^32 warps, 2^30 blocks of four.
   const int64_t rows = static_cast<int64_t>(hq) + 2 * static_cast<int64_t>(d->num_kv_heads);
   if (rows > INT32_MAX || d->num_tokens > (int64_t(1) << 33) / rows) return QKV_ERR_ARG;
-  if (!d->token_pos || !d->cos_sin) return QKV_ERR_ARG;
+  if ((!axes && !d->token_pos) || !d->cos_sin) return QKV_ERR_ARG;
   if (hq > 0) {
     const int64_t row = static_cast<int64_t>(hq) * d->head_dim;
     if (d->q_stride < row || d->q_out_stride < row) return QKV_ERR_ARG;
@@ -507,16 +507,9 @@ qkv_status check_append(const qkv_append_desc* d) {
   return QKV_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-qkv_status qkv_append_rope(const qkv_append_desc* d, void* stream) {
-  if (d == nullptr || d->size != sizeof(qkv_append_desc)) return QKV_ERR_ARG;
-  if (d->act_fp16 != 0 && d->act_fp16 != 1) return QKV_ERR_ARG;
-  const qkv_status st = check_append(d);
-  if (st != QKV_OK || d->num_tokens == 0) return st;
-  qkv::AppendArgs a;
+// A checked descriptor's fields.
+qkv::AppendArgs append_args(const qkv_append_desc* d) {
+  qkv::AppendArgs a = {};
   a.q = static_cast<const uint16_t*>(d->q);
   a.q_out = static_cast<uint16_t*>(d->q_out);
   a.k = static_cast<const uint16_t*>(d->k);
@@ -543,7 +536,112 @@ qkv_status qkv_append_rope(const qkv_append_desc* d, void* stream) {
   a.v_scale_layer = d->v_scale_layer;
   a.num_slots = d->num_slots;
   a.dev_status = d->dev_status;
-  return cuda_status(qkv::launch_append_rope(a, d->fmt, d->act_fp16 == 1, static_cast<cudaStream_t>(stream)));
+  return a;
+}
+
+// Positions of several axes, and each pair's axis packed from the host's array. The positions' pointer is checked
+// where there are tokens.
+qkv_status check_axes(const int32_t* axis_pos, int num_axes, const uint8_t* pair_axis, int rotary_dim, int64_t num_tokens,
+                      qkv::RopeAxes* out) {
+  if (num_axes < 1 || num_axes > qkv::kMaxAxes) return QKV_ERR_ARG;
+  *out = qkv::RopeAxes{axis_pos, num_axes, {}};
+  for (int i = 0; pair_axis != nullptr && i < rotary_dim / 2; ++i) {
+    if (pair_axis[i] >= num_axes) return QKV_ERR_ARG;
+    out->pair_axis[i >> 4] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i & 15));
+  }
+  if (num_tokens > 0 && !axis_pos) return QKV_ERR_ARG;
+  return aligned(axis_pos, 4) ? QKV_OK : QKV_ERR_ALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+qkv_status qkv_append_rope(const qkv_append_desc* d, void* stream) {
+  if (d == nullptr || d->size != sizeof(qkv_append_desc)) return QKV_ERR_ARG;
+  if (d->act_fp16 != 0 && d->act_fp16 != 1) return QKV_ERR_ARG;
+  const qkv_status st = check_append(d);
+  if (st != QKV_OK || d->num_tokens == 0) return st;
+  return cuda_status(qkv::launch_append_rope(append_args(d), d->fmt, d->act_fp16 == 1, static_cast<cudaStream_t>(stream)));
+}
+
+qkv_status qkv_append_axes(const qkv_append_axes_desc* d, void* stream) {
+  if (d == nullptr || d->append.size != sizeof(qkv_append_axes_desc)) return QKV_ERR_ARG;
+  const qkv_append_desc* p = &d->append;
+  if (p->act_fp16 != 0 && p->act_fp16 != 1) return QKV_ERR_ARG;
+  qkv_status st = check_append(p, true);
+  if (st != QKV_OK) return st;
+  qkv::RopeAxes axes;
+  st = check_axes(d->axis_pos, d->num_axes, d->pair_axis, p->rotary_dim, p->num_tokens, &axes);
+  if (st != QKV_OK || p->num_tokens == 0) return st;
+  qkv::AppendArgs a = append_args(p);
+  a.axes = axes;
+  return cuda_status(qkv::launch_append_axes(a, p->fmt, p->act_fp16 == 1, static_cast<cudaStream_t>(stream)));
+}
+
+qkv_status qkv_read(const qkv_read_desc* d, void* stream) {
+  if (d == nullptr || d->size != sizeof(qkv_read_desc)) return QKV_ERR_ARG;
+  if (d->num_tokens < 0 || d->num_slots < 0 || d->num_kv_heads < 1) return QKV_ERR_ARG;
+  if (!qkv::head_dim_ok(d->head_dim)) return QKV_ERR_UNSUPPORTED;
+  if (d->fmt != QKV_BF16 && d->fmt != QKV_INT8_SIDE && d->fmt != QKV_INT8_INLINE && d->fmt != QKV_E4M3 && d->fmt != QKV_F16)
+    return QKV_ERR_ARG;
+  if (d->out_type != QKV_OUT_BF16 && d->out_type != QKV_OUT_F16 && d->out_type != QKV_OUT_F32) return QKV_ERR_ARG;
+  if (d->fmt == QKV_E4M3 && (!finite_positive(d->k_scale_layer) || !finite_positive(d->v_scale_layer))) return QKV_ERR_SCALE;
+  const bool side = d->fmt == QKV_INT8_SIDE, paged = d->slot_mapping == nullptr;
+  if (!side && (d->k_scale || d->v_scale)) return QKV_ERR_ARG;
+  if (!paged && (d->token_seq || d->token_pos || d->block_table)) return QKV_ERR_ARG;  // one addressing only
+  // four rows per lane group in large launches: T ceil(2 H / 4) <= T H warps or fewer, in blocks of four
+  if (d->num_tokens > (int64_t(1) << 32) / d->num_kv_heads) return QKV_ERR_ARG;
+  qkv::RopeAxes axes = {};
+  if (d->cos_sin != nullptr) {
+    if (d->num_positions < 0 || d->rotary_dim < 16 || d->rotary_dim % 16 != 0 || d->rotary_dim > d->head_dim) return QKV_ERR_ARG;
+    if (d->interleaved != 0 && d->interleaved != 1) return QKV_ERR_ARG;
+    const qkv_status st = check_axes(d->axis_pos, d->num_axes, d->pair_axis, d->rotary_dim, d->num_tokens, &axes);
+    if (st != QKV_OK) return st;
+    if (!aligned(d->cos_sin, 16)) return QKV_ERR_ALIGN;
+  } else if (d->axis_pos != nullptr) {
+    return QKV_ERR_ARG;  // positions without a table
+  }
+  if (d->num_tokens == 0) return QKV_OK;
+  if (!d->k_cache || !d->v_cache || (!d->k_out && !d->v_out)) return QKV_ERR_ARG;
+  if (side && (!d->k_scale || !d->v_scale)) return QKV_ERR_ARG;
+  if (paged) {
+    if (!d->token_seq || !d->token_pos || !d->block_table) return QKV_ERR_ARG;
+    if (d->block_size < 1 || d->max_blocks < 1 || d->num_seqs < 1) return QKV_ERR_ARG;
+    if (static_cast<int64_t>(d->max_blocks) * d->block_size > INT32_MAX) return QKV_ERR_ARG;
+    if (!aligned(d->token_seq, 4) || !aligned(d->token_pos, 4) || !aligned(d->block_table, 4)) return QKV_ERR_ALIGN;
+  } else if (!aligned(d->slot_mapping, 8)) {
+    return QKV_ERR_ALIGN;
+  }
+  if (d->out_stride < static_cast<int64_t>(d->num_kv_heads) * d->head_dim) return QKV_ERR_ARG;
+  if (d->out_stride % 8 != 0 || !aligned(d->k_out, 16) || !aligned(d->v_out, 16)) return QKV_ERR_ALIGN;
+  if (!aligned(d->k_cache, 16) || !aligned(d->v_cache, 16)) return QKV_ERR_ALIGN;
+  if (side && (!aligned(d->k_scale, 4) || !aligned(d->v_scale, 4))) return QKV_ERR_ALIGN;
+  if (!aligned(d->dev_status, 4)) return QKV_ERR_ALIGN;
+  qkv::ReadArgs a = {};
+  a.k_cache = static_cast<const uint8_t*>(d->k_cache);
+  a.v_cache = static_cast<const uint8_t*>(d->v_cache);
+  a.k_scale = d->k_scale;
+  a.v_scale = d->v_scale;
+  a.k_scale_layer = d->k_scale_layer;
+  a.v_scale_layer = d->v_scale_layer;
+  a.num_slots = d->num_slots;
+  a.num_tokens = d->num_tokens;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.slot_mapping = d->slot_mapping;
+  a.paging = qkv::WritePaging{d->token_seq, d->token_pos, d->block_table, d->num_seqs, d->max_blocks, d->block_size};
+  a.k_out = d->k_out;
+  a.v_out = d->v_out;
+  a.out_stride = d->out_stride;
+  a.out_type = d->out_type;
+  a.cos_sin = d->cos_sin;
+  a.num_positions = d->num_positions;
+  a.rotary_dim = d->rotary_dim;
+  a.interleaved = d->interleaved == 1;
+  a.axes = axes;
+  a.dev_status = d->dev_status;
+  return cuda_status(qkv::launch_read(a, d->fmt, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

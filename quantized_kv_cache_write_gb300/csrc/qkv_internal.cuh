@@ -111,6 +111,14 @@ cudaError_t gather_ctas_per_sm_int8_side(int* n);
 cudaError_t gather_ctas_per_sm_int8_inline(int* n);
 cudaError_t gather_ctas_per_sm_e4m3(int* n);
 
+// Positions of several axes (time, height, width) and each pair's axis.
+constexpr int kMaxAxes = QKV_MAX_AXES;
+struct RopeAxes {
+  const int32_t* axis_pos;  // [num_axes, num_tokens]
+  int num_axes;
+  uint32_t pair_axis[8];  // two bits per pair
+};
+
 // Arguments of one append launch (already validated on the host).
 struct AppendArgs {
   const uint16_t* q;  // 16-bit activations, or null (then num_q_heads is 0)
@@ -128,7 +136,7 @@ struct AppendArgs {
   int64_t num_positions;
   int rotary_dim;  // a multiple of 16
   bool interleaved;
-  const int32_t* token_pos;
+  const int32_t* token_pos;     // one axis
   const int64_t* slot_mapping;  // null: paged
   WritePaging paging;
   uint8_t* k_cache;
@@ -139,8 +147,37 @@ struct AppendArgs {
   float v_scale_layer;
   int64_t num_slots;
   uint32_t* dev_status;
+  RopeAxes axes;  // several axes
 };
 cudaError_t launch_append_rope(const AppendArgs& a, qkv_format fmt, bool f16, cudaStream_t stream);
+cudaError_t launch_append_axes(const AppendArgs& a, qkv_format fmt, bool f16, cudaStream_t stream);
+
+// Arguments of one read of the pool (already validated on the host).
+struct ReadArgs {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  int64_t num_tokens;
+  int num_kv_heads;
+  int head_dim;
+  const int64_t* slot_mapping;  // null: paged
+  WritePaging paging;
+  void* k_out;  // null: not read
+  void* v_out;
+  int64_t out_stride;  // elements between tokens
+  int out_type;        // qkv_out_type
+  const float* cos_sin;  // null: K as it is stored
+  int64_t num_positions;
+  int rotary_dim;
+  bool interleaved;
+  RopeAxes axes;
+  uint32_t* dev_status;
+};
+cudaError_t launch_read(const ReadArgs& a, qkv_format fmt, cudaStream_t stream);
 
 // Arguments of one shared-prefix attention call (already validated on the host).
 struct PrefixArgs {
