@@ -802,6 +802,93 @@ qkv_status qkv_prefix_attn_workspace(qkv_format fmt, int64_t rows, int num_q_hea
                                      int prefix_len, int max_row_len, size_t* bytes);
 qkv_status qkv_prefix_attn(const qkv_prefix_desc* desc, void* stream);
 
+/*
+ * qkv_masked_attn -- dense attention over a paged pool whose scores may be capped, get a bias that depends on distance, and
+ * are masked to a range of keys per row: a causal prompt or a chunk of one, a sliding window, packed documents, a prefix that
+ * its own tokens see whole, and single tokens of any of these. Prompts run on tcgen05 tiles that take up to 512
+ * (row, head) pairs of one sequence, single tokens on tiles of 16 or 8 whose keys are split over the GPU.
+ * The pages attend to selected slots only; this is the dense operator over the same pool, scales and block tables
+ * [HOIST-PR §Changes: scale hoisting; E4M3-PR §Implementation scope: paged storage].
+ *   Row r is a query token of sequence row_seq[r] at position p = row_pos[r] of it. It sees the positions
+ *     row_start[r] <= j < row_end[r], and with a window only those with j > p - window;
+ *   position j sits in slot block_table[row_seq[r], j / block_size] * block_size + j % block_size. Over them
+ *     z_j = softmax_scale * q[r,g] . K_j,  s_j = c(z_j) - slopes[g] |p - j|,  o = sum_j softmax(s)_j V_j,  lse = log sum_j exp(s_j)
+ *   with KV head g / (num_q_heads / num_kv_heads) and c(z) = softcap tanh(z / softcap) (softcap 0: z).
+ *   Masks: causal: row_end = p + 1; documents: row_start = the first position of p's document; a prefix of n tokens that see
+ *   one another: row_end = max(p + 1, n) for p < n.
+ *
+ *   size, fmt, q, q_fp16, q_stride, rows, num_q_heads, num_kv_heads, head_dim, k_cache, v_cache, k_scale_tok, v_scale_tok,
+ *   k_scale_layer, v_scale_layer, num_slots, block_table, num_seqs, max_blocks, block_size, softmax_scale, out, lse,
+ *   dev_status    as for qkv_prefix_attn, size being sizeof(qkv_masked_desc).
+ *   row_seq       int32 [rows]. -1: a padding row, whose out and lse are left as they were. Rows of one sequence that
+ *                 follow each other share the reads of its keys; other orders give the same results, slower.
+ *   row_start     int32 [rows], at least 0, or NULL: 0. row_start >= row_end: the row sees nothing (o = 0, lse = -inf).
+ *   row_end       int32 [rows] in [0, max_row_end].
+ *   row_pos       int32 [rows] in [0, 2^30], or NULL: row_end - 1. Looked at for the window and the bias only, and not for
+ *                 rows that see nothing.
+ *   max_row_end   no row ends later; 0 <= max_row_end <= max_blocks * block_size and at most 2^30, else QKV_ERR_ARG. With
+ *                 num_seqs and window it sizes the launch (a captured graph keeps it).
+ *   window        0: none; else at least 1.
+ *   softcap       0: none; else in [2^-20, 2^20] (else QKV_ERR_ARG).
+ *   slopes        fp32 [num_q_heads], 4 B-aligned, or NULL: no bias.
+ *   Flagged with QKV_DEV_BAD_INDEX: a row_seq outside [-1, num_seqs), a row_start, row_end or row_pos outside its range (the
+ *   row is empty), and an unallocated block (id < 0) or a slot >= num_slots among the keys that a row sees (the key is masked).
+ *   Blocks that no row sees may hold anything in the table.
+ *   workspace     device scratch of workspace_bytes, 16 B-aligned; its contents need not be set. Too small a workspace is
+ *                 QKV_ERR_ARG. Calls that overlap on the GPU -- on two streams, or replays of two captured graphs -- must
+ *                 not share one.
+ *   Limits as for qkv_prefix_attn: rows * num_q_heads and num_slots * num_kv_heads at most 2^31 - 1.
+ *   Numbers: as for qkv_prefix_attn. A capped score is off by up to 2^-19 of itself besides. The bias
+ *   counts from the seen key that is nearest to p (only differences matter to the weights), so that a row far from its keys
+ *   loses no bits; a key at distance d from that one has a score off by up to 2^-23 slopes[g] d. A value that is not finite
+ *   in a key that a row does not see leaves that row as it was.
+ * Results do not depend on other rows of the batch, up to rounding; calls with the same arguments on the same device give the
+ * same bits.
+ *
+ * qkv_masked_attn_workspace -- the bytes that a call of this shape needs on the current device. Ask for every shape that a
+ * program uses. Launches nothing; a failed device query is QKV_ERR_CUDA.
+ */
+typedef struct {
+  size_t size;
+  qkv_format fmt;
+  int q_fp16;
+  const void* q;
+  int64_t q_stride;
+  int64_t rows;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale_tok;
+  const float* v_scale_tok;
+  float k_scale_layer;
+  float v_scale_layer;
+  int64_t num_slots;
+  const int32_t* block_table;
+  int64_t num_seqs;
+  int max_blocks;
+  int block_size;
+  const int32_t* row_seq;
+  const int32_t* row_start;
+  const int32_t* row_end;
+  const int32_t* row_pos;
+  int max_row_end;
+  int window;
+  float softmax_scale;
+  float softcap;
+  const float* slopes;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* dev_status;
+} qkv_masked_desc;
+
+qkv_status qkv_masked_attn_workspace(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads,
+                                     int head_dim, int max_row_end, int window, size_t* bytes);
+qkv_status qkv_masked_attn(const qkv_masked_desc* desc, void* stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* qkv_status_str(qkv_status s);
 

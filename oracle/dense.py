@@ -1,5 +1,6 @@
 """Oracle of the dense cache operators (test infrastructure; see the package docstring): the position
-rotation of new tokens and attention of a batch over a shared prefix and its rows' own keys.
+rotation of new tokens, attention of a batch over a shared prefix and its rows' own keys, and attention of rows
+that each see a range of their sequence's keys, with capped scores and a distance bias.
 
 Rotation, for a pair of head dims (a, b) with cosine c and sine s, all fp32:
     a' = fl(fl(a c) - fl(b s)),  b' = fl(fl(b c) + fl(a s))
@@ -95,3 +96,89 @@ def prefix_attention(q_bits: np.ndarray, K: np.ndarray, V: np.ndarray, slots, sc
             mags = np.concatenate([np.abs(qr) @ ak0.T, np.abs(qr) @ np.abs(k1).T], 1)
             big[r, heads] = abs(scale) * mags.max(1)
     return out, lse, wabs, big
+
+
+def masked_rows(row_seq, row_start, row_end, row_pos, window, num_seqs, max_row_end):
+    """Per row the range [lo, hi) of positions it sees and its position p ([0, 0), 0: none), whether it is a padding row,
+    and whether any row is invalid (it sees nothing)."""
+    n = len(row_seq)
+    lo, hi, pos = np.zeros(n, np.int64), np.zeros(n, np.int64), np.zeros(n, np.int64)
+    pad, flagged = np.asarray(row_seq) == -1, False
+    for r in range(n):
+        a, e = (0 if row_start is None else int(row_start[r])), int(row_end[r])
+        p = e - 1 if row_pos is None else int(row_pos[r])
+        if pad[r]:
+            continue
+        if not 0 <= row_seq[r] < num_seqs or not 0 <= e <= max_row_end or a < 0 or (a < e and not 0 <= p <= 1 << 30):
+            flagged = True
+        elif a < e:
+            a = max(a, p - window + 1) if window else a
+            if a < e:
+                lo[r], hi[r], pos[r] = a, e, p
+    return lo, hi, pos, pad, flagged
+
+
+def masked_attention(q_bits, K, V, row_seq, lo, hi, pos, pad, block_table, block_size, scale, softcap=0.0, slopes=None,
+                     q_dtype: str = "bf16"):
+    """fp64 attention of rows q_bits [R, Hq, D] over the positions [lo, hi) of their sequences in pools K, V [S, Hkv, D]:
+    scores softcap tanh(scale q . K / softcap) - slopes |pos - j|; keys without a slot are masked.
+
+    Returns out, lse and, for error bounds, sum_j w_j |V_j|, max_j |scale| sum_d |q_d K_jd|, the largest |slope| times
+    distance from the nearest seen key, and whether a row sees a key without a slot. Values that are not finite reach only
+    the rows that see their key. Padding rows give NaN."""
+    q = act_bits_to_f32(q_bits, q_dtype).astype(np.float64)
+    R, Hq, D = q.shape
+    S, H, _ = K.shape
+    G = Hq // H
+    out, wabs = np.zeros((R, Hq, D)), np.zeros((R, Hq, D))
+    lse, big, far = np.full((R, Hq), -np.inf), np.zeros((R, Hq)), np.zeros((R, Hq))
+    out[pad], lse[pad] = np.nan, np.nan
+    flagged = False
+    sl = np.zeros(Hq) if slopes is None else np.asarray(slopes, np.float64)
+    live = [r for r in range(R) if lo[r] < hi[r]]
+    for seq in sorted({int(row_seq[r]) for r in live}):
+        rows = np.array([r for r in live if row_seq[r] == seq])
+        a, e = int(lo[rows].min()), int(hi[rows].max())
+        j = np.arange(a, e)
+        blk = block_table[seq, j // block_size].astype(np.int64)
+        slot = blk * block_size + j % block_size
+        ok = (blk >= 0) & (slot < S)
+        inside = (j >= lo[rows, None]) & (j < hi[rows, None])
+        flagged |= bool((inside & ~ok).any())
+        j, slot, sees = j[ok], slot[ok], (inside & ok)[:, ok]
+        seen = sees.any(0)
+        j, slot, sees = j[seen], slot[seen], sees[:, seen]
+        if not len(j):
+            continue
+        near = np.minimum(np.maximum(pos[rows], lo[rows]), hi[rows] - 1)
+        for h in range(H):
+            heads = slice(h * G, (h + 1) * G)
+            k, v = K[slot, h], V[slot, h]
+            qr = q[rows, heads]  # [r, G, D]
+            with np.errstate(invalid="ignore", over="ignore"):
+                z = scale * np.einsum("rgd,jd->rgj", qr, k)
+                if softcap:
+                    z = softcap * np.tanh(z / softcap)
+                dist = np.abs(pos[rows, None] - j).astype(np.float64)
+                z = z - sl[heads][None, :, None] * dist[:, None]
+                z = np.where(sees[:, None], z, -np.inf)
+                m = z.max(-1, keepdims=True)
+                ex = np.where(sees[:, None], np.exp(z - np.where(np.isfinite(m), m, 0.0)), 0.0)
+                total = ex.sum(-1, keepdims=True)
+                w = ex / np.where(total > 0, total, 1.0)
+                w = np.where(np.isnan(total), np.nan, w)
+                fin = np.isfinite(v)
+                v0 = np.where(fin, v, 0.0)
+                o = w @ v0
+                bad = np.flatnonzero(~fin.all(1))
+                for b in bad:
+                    rr = np.flatnonzero(sees[:, b])
+                    o[rr] += np.where(fin[b], 0.0, v[b])
+                out[rows, heads] = o
+                wabs[rows, heads] = w @ np.abs(v0)
+                lse[rows, heads] = np.where(total[..., 0] > 0, (m + np.log(total))[..., 0], np.where(np.isnan(total[..., 0]), np.nan, -np.inf))
+                mags = np.einsum("rgd,jd->rgj", np.abs(qr), np.abs(np.where(np.isfinite(k), k, 0.0)))
+                big[rows, heads] = abs(scale) * np.where(sees[:, None], mags, 0.0).max(-1)
+                reach = np.where(sees, np.abs(near[:, None] - j), 0).max(-1)
+                far[rows, heads] = np.abs(sl[heads])[None] * reach[:, None]
+    return out, lse, wabs, big, far, flagged

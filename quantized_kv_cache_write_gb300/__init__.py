@@ -531,6 +531,18 @@ class PrefixDesc(ctypes.Structure):
                 ("workspace", _p), ("workspace_bytes", ctypes.c_size_t), ("dev_status", _p)]
 
 
+class MaskedDesc(ctypes.Structure):
+    """qkv_masked_desc of include/qkv.h, field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("fmt", _i32), ("q_fp16", _i32), ("q", _p), ("q_stride", _i64),
+                ("rows", _i64), ("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("k_cache", _p),
+                ("v_cache", _p), ("k_scale_tok", _p), ("v_scale_tok", _p), ("k_scale_layer", _f32),
+                ("v_scale_layer", _f32), ("num_slots", _i64), ("block_table", _p), ("num_seqs", _i64),
+                ("max_blocks", _i32), ("block_size", _i32), ("row_seq", _p), ("row_start", _p), ("row_end", _p),
+                ("row_pos", _p), ("max_row_end", _i32), ("window", _i32), ("softmax_scale", _f32), ("softcap", _f32),
+                ("slopes", _p), ("out", _p), ("lse", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+                ("dev_status", _p)]
+
+
 lib.qkv_append_rope.argtypes = [ctypes.POINTER(AppendDesc), _p]
 lib.qkv_append_rope.restype = ctypes.c_int
 lib.qkv_append_axes.argtypes = [ctypes.POINTER(AppendAxesDesc), _p]
@@ -542,8 +554,13 @@ lib.qkv_prefix_attn.restype = ctypes.c_int
 lib.qkv_prefix_attn_workspace.argtypes = [_i32, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
 lib.qkv_prefix_attn_workspace.restype = ctypes.c_int
 
+lib.qkv_masked_attn.argtypes = [ctypes.POINTER(MaskedDesc), _p]
+lib.qkv_masked_attn.restype = ctypes.c_int
+lib.qkv_masked_attn_workspace.argtypes = [_i32, _i64, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
+lib.qkv_masked_attn_workspace.restype = ctypes.c_int
+
 _APPEND_SIZE, _PREFIX_SIZE = ctypes.sizeof(AppendDesc), ctypes.sizeof(PrefixDesc)
-_AXES_SIZE, _READ_SIZE = ctypes.sizeof(AppendAxesDesc), ctypes.sizeof(ReadDesc)
+_AXES_SIZE, _READ_SIZE, _MASKED_SIZE = ctypes.sizeof(AppendAxesDesc), ctypes.sizeof(ReadDesc), ctypes.sizeof(MaskedDesc)
 
 
 def _packer(desc, fn: str):
@@ -571,6 +588,7 @@ def _packer(desc, fn: str):
 _f32, _half, _int32, _int64 = torch.float32, torch.float16, torch.int32, torch.int64
 _call_append, _call_prefix = _packer(AppendDesc, "qkv_append_rope"), _packer(PrefixDesc, "qkv_prefix_attn")
 _call_axes, _call_read = _packer(AppendAxesDesc, "qkv_append_axes"), _packer(ReadDesc, "qkv_read")
+_call_masked = _packer(MaskedDesc, "qkv_masked_attn")
 # the tensor types that hold a pool: its values' own, or integers of their size (raw bits)
 _CACHE_TYPES = {QKV_BF16: (torch.bfloat16, torch.int16, torch.uint16), QKV_F16: (torch.float16, torch.int16, torch.uint16),
                 QKV_INT8_SIDE: (torch.int8, torch.uint8), QKV_INT8_INLINE: (torch.int8, torch.uint8),
@@ -859,3 +877,67 @@ def qkv_prefix_attn(q, fmt: int, k_cache, v_cache, block_table, row_seq, row_len
                  k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S, pbp,
                  prefix_len, btp, seqs, blocks, block_size, rsp, rlp, max_row_len, float(softmax_scale), op, lp, wsp, wsb,
                  0 if dev_status is None else dev_status.data_ptr())
+
+
+def qkv_masked_attn_workspace(fmt: int, rows: int, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                              max_row_end: int, window: int = 0, device=None) -> int:
+    """Workspace bytes of a qkv_masked_attn call of this shape on `device`, which is the tensors' (None: the current one)."""
+    out = ctypes.c_size_t(0)
+    with contextlib.nullcontext() if device is None else torch.cuda.device(device):
+        _check("qkv_masked_attn_workspace",
+               lib.qkv_masked_attn_workspace(fmt, rows, num_seqs, num_q_heads, num_kv_heads, head_dim, max_row_end, window,
+                                             ctypes.byref(out)))
+    return out.value
+
+
+def qkv_masked_attn(q, fmt: int, k_cache, v_cache, block_table, row_seq, row_end, block_size: int, softmax_scale: float, *,
+                    max_row_end: int, num_kv_heads: int = 1, row_start=None, row_pos=None, window: int = 0,
+                    softcap: float = 0.0, slopes=None, k_scale_tok=None, v_scale_tok=None, k_scale_layer: float = 1.0,
+                    v_scale_layer: float = 1.0, out, lse=None, workspace=None, dev_status=None, stream=None):
+    """Dense attention over a paged pool with capped scores, a distance bias and masks, for prompts' chunks and
+    single tokens (see qkv_masked_attn in qkv.h).
+
+    q bf16 or fp16 [R, Hq, D]; row r is a token of sequence row_seq[r] (int32 [R], -1 padding) and sees
+    positions row_start[r] (None: 0) .. row_end[r] - 1, with a window only those less than `window`
+    before row_pos[r] (None: row_end - 1); slopes fp32 [Hq]; block_table int32 [num_seqs, max_blocks].
+    out is [R, Hq, D] in q's type; workspace any contiguous tensor of at least
+    qkv_masked_attn_workspace bytes.
+    """
+    shape, table = q.shape, block_table.shape
+    if len(shape) != 3 or q.dtype not in _ACT16:
+        raise ValueError("q must be bf16 or fp16 [rows, num_q_heads, head_dim]")
+    R, Hq, D = shape
+    stride = _strided("q", q, R, Hq, D)
+    S = _need_caches(k_cache, v_cache, fmt, num_kv_heads, D)
+    if len(table) != 2:
+        raise ValueError("block_table must be [num_seqs, max_blocks]")
+    seqs, blocks = table
+    btp = _plain("block_table", block_table, _int32, seqs * blocks)
+    rsp = _plain("row_seq", row_seq, _int32, R)
+    rap = _plain("row_start", row_start, _int32, R)
+    rep = _plain("row_end", row_end, _int32, R)
+    rpp = _plain("row_pos", row_pos, _int32, R)
+    slp = _plain("slopes", slopes, _f32, Hq)
+    if out.shape != shape:
+        _expect_shape("out", out, (R, Hq, D))
+    op = _plain("out", out, q.dtype, R * Hq * D)
+    lp = 0
+    if lse is not None:
+        if lse.shape != (R, Hq):
+            _expect_shape("lse", lse, (R, Hq))
+        lp = _plain("lse", lse, _f32, R * Hq)
+    ksp = _plain("k_scale_tok", k_scale_tok, _f32, S * num_kv_heads)
+    vsp = _plain("v_scale_tok", v_scale_tok, _f32, S * num_kv_heads)
+    if dev_status is not None:
+        _need("dev_status", dev_status, _WORD)
+    wsp = wsb = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        wsp, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _on_cuda(q, k_cache, v_cache, block_table, row_seq, row_start, row_end, row_pos, slopes, out, lse, k_scale_tok,
+                   v_scale_tok, workspace, dev_status)
+    _call_masked(dev, stream, _MASKED_SIZE, fmt, q.dtype is _half, q.data_ptr(), stride, R, Hq, num_kv_heads, D,
+                 k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, float(k_scale_layer), float(v_scale_layer), S, btp, seqs,
+                 blocks, block_size, rsp, rap, rep, rpp, max_row_end, window, float(softmax_scale), float(softcap), slp, op, lp,
+                 wsp, wsb, 0 if dev_status is None else dev_status.data_ptr())

@@ -55,6 +55,11 @@ SOURCES = [
     "prefix_umma_bf16.cu",
     "prefix_umma_f16.cu",
     "prefix_merge.cu",
+    "masked_int8_side.cu",
+    "masked_int8_inline.cu",
+    "masked_e4m3.cu",
+    "masked_bf16.cu",
+    "masked_f16.cu",
 ]
 HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "rope.cuh", "append.cuh", "prefix_attn.cuh", "prefix_umma.cuh"]
 

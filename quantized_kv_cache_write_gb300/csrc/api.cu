@@ -590,7 +590,7 @@ qkv_status qkv_read(const qkv_read_desc* d, void* stream) {
   const bool side = d->fmt == QKV_INT8_SIDE, paged = d->slot_mapping == nullptr;
   if (!side && (d->k_scale || d->v_scale)) return QKV_ERR_ARG;
   if (!paged && (d->token_seq || d->token_pos || d->block_table)) return QKV_ERR_ARG;  // one addressing only
-  // four rows per lane group in large launches: T ceil(2 H / 4) <= T H warps or fewer, in blocks of four
+  // 2 T H rows, four per warp or more in large launches, four warps per block
   if (d->num_tokens > (int64_t(1) << 32) / d->num_kv_heads) return QKV_ERR_ARG;
   qkv::RopeAxes axes = {};
   if (d->cos_sin != nullptr) {
@@ -701,6 +701,18 @@ qkv_status check_prefix_shape(qkv_format fmt, int64_t rows, int num_q_heads, int
   return QKV_OK;
 }
 
+int64_t row_bytes_of(qkv_format fmt, int head_dim) { return fmt == QKV_BF16 || fmt == QKV_F16 ? 2 * head_dim : head_dim; }
+
+// Ranges that the keys of mma.sync tiles are cut into, as PrefixPlan's comment says.
+int key_parts(int64_t tiles, int keys, int64_t row_bytes, int sms) {
+  if (keys <= 0 || tiles <= 0) return 0;
+  const int64_t slots = static_cast<int64_t>(sms) * (row_bytes == 128 ? 3 : row_bytes == 256 ? 2 : 1);  // resident CTAs
+  int least = 64;
+  while (least < 512 && (ceil_div(keys, least) > 32 || 10 * tiles * ceil_div(keys, least) > 9 * slots)) least *= 2;
+  const int64_t want = ceil_div(16 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, least);
+  return static_cast<int>(want < most ? want : most);
+}
+
 qkv_status plan_prefix(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv_heads, int head_dim, int prefix_len,
                        int max_row_len, PrefixPlan* p) {
   const int sms = sm_count();
@@ -710,15 +722,8 @@ qkv_status plan_prefix(qkv_format fmt, int64_t rows, int num_q_heads, int num_kv
   p->head_dim = head_dim;
   p->ptiles = ceil_div(rows * G, 16) * num_kv_heads;
   p->otiles = rows * ceil_div(G, 16) * num_kv_heads;
-  const int64_t row_bytes = fmt == QKV_BF16 || fmt == QKV_F16 ? 2 * head_dim : head_dim;
-  const int64_t slots = static_cast<int64_t>(sms) * (row_bytes == 128 ? 3 : row_bytes == 256 ? 2 : 1);  // resident CTAs
-  auto parts_of = [&](int64_t tiles, int keys) -> int {
-    if (keys <= 0 || tiles <= 0) return 0;
-    int least = 64;
-    while (least < 512 && (ceil_div(keys, least) > 32 || 10 * tiles * ceil_div(keys, least) > 9 * slots)) least *= 2;
-    const int64_t want = ceil_div(16 * static_cast<int64_t>(sms), tiles), most = ceil_div(keys, least);
-    return static_cast<int>(want < most ? want : most);
-  };
+  const int64_t row_bytes = row_bytes_of(fmt, head_dim);
+  auto parts_of = [&](int64_t tiles, int keys) { return key_parts(tiles, keys, row_bytes, sms); };
   p->prefix_parts = parts_of(p->ptiles, prefix_len);
   p->prefix_chunk = 0;
   if (p->prefix_parts > 0) {
@@ -882,6 +887,146 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
   if (p.umma_cg > 0) e = launch_prefix_umma(a, d->fmt, s);
   if (e == cudaSuccess && a.prefix_items + a.own_items > 0) e = launch_prefix_mma(a, d->fmt, p.umma_cg > 0, s);
   if (e == cudaSuccess && !direct) e = qkv::launch_prefix_merge(a, s);
+  return cuda_status(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+struct MaskedPlan {
+  int64_t tiles;  // mma.sync tiles
+  int parts;      // ranges of their keys
+  int64_t rows_heads;
+  int head_dim;
+  // partial outputs, then partial log-sum-exps; a single part writes the output itself
+  size_t o_bytes() const { return parts > 1 ? static_cast<size_t>(parts) * rows_heads * head_dim * 4 : 0; }
+  size_t bytes() const { return o_bytes() + (parts > 1 ? static_cast<size_t>(parts) * rows_heads * 4 : 0); }
+};
+
+qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                              int max_row_end, int window) {
+  if (num_seqs < 1 || window < 0) return QKV_ERR_ARG;
+  return check_prefix_shape(fmt, rows, num_q_heads, num_kv_heads, head_dim, 0, max_row_end);
+}
+
+qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                       int max_row_end, int window, MaskedPlan* p) {
+  const int sms = sm_count();
+  if (sms < 1) return QKV_ERR_CUDA;
+  const int G = num_q_heads / num_kv_heads;
+  p->rows_heads = rows * num_q_heads;
+  p->head_dim = head_dim;
+  p->tiles = rows * ceil_div(G, 16) * num_kv_heads;
+  // a tile's rows that follow each other see a window's keys and a few more
+  const int64_t keys = window > 0 && window < max_row_end - 16 ? window + 16 : max_row_end;
+  p->parts = key_parts(p->tiles, static_cast<int>(keys > 0 ? keys : 1), row_bytes_of(fmt, head_dim), sms);
+  if (p->tiles * p->parts > INT32_MAX) return QKV_ERR_ARG;
+  return QKV_OK;
+}
+
+cudaError_t launch_masked_mma(const qkv::PrefixArgs& a, qkv_format fmt, cudaStream_t s) {
+  switch (fmt) {
+    case QKV_BF16: return qkv::launch_masked_mma_bf16(a, s);
+    case QKV_F16: return qkv::launch_masked_mma_f16(a, s);
+    case QKV_INT8_SIDE: return qkv::launch_masked_mma_int8_side(a, s);
+    case QKV_INT8_INLINE: return qkv::launch_masked_mma_int8_inline(a, s);
+    case QKV_E4M3: return qkv::launch_masked_mma_e4m3(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+extern "C" {
+
+qkv_status qkv_masked_attn_workspace(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads,
+                                     int head_dim, int max_row_end, int window, size_t* bytes) {
+  if (!bytes) return QKV_ERR_ARG;
+  qkv_status st = check_masked_shape(fmt, rows, num_seqs, num_q_heads, num_kv_heads, head_dim, max_row_end, window);
+  if (st != QKV_OK) return st;
+  MaskedPlan p;
+  st = plan_masked(fmt, rows, num_seqs, num_q_heads, num_kv_heads, head_dim, max_row_end, window, &p);
+  if (st == QKV_OK) *bytes = p.bytes();
+  return st;
+}
+
+qkv_status qkv_masked_attn(const qkv_masked_desc* d, void* stream) {
+  if (d == nullptr || d->size != sizeof(qkv_masked_desc)) return QKV_ERR_ARG;
+  if (d->q_fp16 != 0 && d->q_fp16 != 1) return QKV_ERR_ARG;
+  qkv_status st = check_masked_shape(d->fmt, d->rows, d->num_seqs, d->num_q_heads, d->num_kv_heads, d->head_dim, d->max_row_end,
+                                     d->window);
+  if (st != QKV_OK) return st;
+  if ((d->fmt == QKV_F16 && !d->q_fp16) || (d->fmt == QKV_BF16 && d->q_fp16)) return QKV_ERR_ARG;
+  if (!std::isfinite(d->softmax_scale) || d->num_slots < 0) return QKV_ERR_ARG;
+  if (!(d->softcap == 0.f || (d->softcap >= 0x1p-20f && d->softcap <= 0x1p20f))) return QKV_ERR_ARG;
+  if (d->fmt == QKV_E4M3 && (!finite_positive(d->k_scale_layer) || !finite_positive(d->v_scale_layer)))
+    return QKV_ERR_SCALE;
+  const bool side = d->fmt == QKV_INT8_SIDE;
+  if (side != (d->k_scale_tok != nullptr) || side != (d->v_scale_tok != nullptr)) return QKV_ERR_ARG;
+  if (d->max_blocks < 1 || d->block_size < 1) return QKV_ERR_ARG;
+  if (static_cast<int64_t>(d->max_blocks) * d->block_size > INT32_MAX) return QKV_ERR_ARG;
+  if (d->max_row_end > static_cast<int64_t>(d->max_blocks) * d->block_size) return QKV_ERR_ARG;
+  if (d->num_slots > INT32_MAX / d->num_kv_heads) return QKV_ERR_UNSUPPORTED;  // records are numbered in 32 bits
+  if (d->q_stride < static_cast<int64_t>(d->num_q_heads) * d->head_dim) return QKV_ERR_ARG;
+  if (d->rows == 0) return QKV_OK;
+  if (!d->q || !d->out || !d->k_cache || !d->v_cache || !d->block_table || !d->row_seq || !d->row_end) return QKV_ERR_ARG;
+  if (d->q_stride % 8 != 0 || !aligned(d->q, 16) || !aligned(d->out, 16)) return QKV_ERR_ALIGN;
+  if (!aligned(d->k_cache, 16) || !aligned(d->v_cache, 16)) return QKV_ERR_ALIGN;
+  if (side && (!aligned(d->k_scale_tok, 4) || !aligned(d->v_scale_tok, 4))) return QKV_ERR_ALIGN;
+  if (!aligned(d->block_table, 4) || !aligned(d->row_seq, 4) || !aligned(d->row_start, 4) || !aligned(d->row_end, 4) ||
+      !aligned(d->row_pos, 4) || !aligned(d->slopes, 4) || !aligned(d->lse, 4) || !aligned(d->dev_status, 4) ||
+      !aligned(d->workspace, 16))
+    return QKV_ERR_ALIGN;
+
+  MaskedPlan p;
+  st = plan_masked(d->fmt, d->rows, d->num_seqs, d->num_q_heads, d->num_kv_heads, d->head_dim, d->max_row_end, d->window, &p);
+  if (st != QKV_OK) return st;
+  if (p.bytes() > 0 && (!d->workspace || d->workspace_bytes < p.bytes())) return QKV_ERR_ARG;
+
+  qkv::PrefixArgs a = {};
+  a.q = static_cast<const uint16_t*>(d->q);
+  a.q_stride = d->q_stride;
+  a.q_f16 = d->q_fp16 == 1;
+  a.rows = d->rows;
+  a.num_q_heads = d->num_q_heads;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.k_cache = static_cast<const uint8_t*>(d->k_cache);
+  a.v_cache = static_cast<const uint8_t*>(d->v_cache);
+  a.k_scale_tok = d->k_scale_tok;
+  a.v_scale_tok = d->v_scale_tok;
+  a.k_scale_layer = d->k_scale_layer;
+  a.v_scale_layer = d->v_scale_layer;
+  a.num_slots = d->num_slots;
+  a.block_table = d->block_table;
+  a.num_seqs = d->num_seqs;
+  a.max_blocks = d->max_blocks;
+  a.block_size = d->block_size;
+  a.row_seq = d->row_seq;
+  a.row_len = d->row_end;
+  a.max_row_len = d->max_row_end;
+  a.row_start = d->row_start;
+  a.row_pos = d->row_pos;
+  a.window = d->window;
+  a.softcap = d->softcap;
+  a.slopes = d->slopes;
+  a.softmax_scale = d->softmax_scale;
+  a.out = static_cast<uint16_t*>(d->out);
+  a.lse = d->lse;
+  a.merge_scale = d->fmt == QKV_E4M3 ? d->v_scale_layer : 1.f;
+  a.dev_status = d->dev_status;
+  const bool direct = p.parts == 1;
+  a.o_part = direct ? nullptr : static_cast<float*>(d->workspace);
+  a.lse_part = direct ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + p.o_bytes());
+  a.own_parts = p.parts;
+  a.own_items = p.tiles * p.parts;
+  // tiles of 8 pairs where a sequence's rows bring no more than that on average, as for qkv_prefix_attn's own keys
+  const int G = d->num_q_heads / d->num_kv_heads;
+  a.mma_pairs = G <= 8 && d->rows * G <= 8 * d->num_seqs ? 8 : 16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_masked_mma(a, d->fmt, s);
+  if (e == cudaSuccess && !direct) e = qkv::launch_masked_merge(a, s);
   return cuda_status(e);
 }
 

@@ -104,6 +104,7 @@ __device__ __forceinline__ int swz(int r) {
 
 // Keys of its own that a row sees; kEmptyRow: it sees nothing; kPadRow: no row at all.
 constexpr int kEmptyRow = -1, kPadRow = -2;
+constexpr int kMaxRowPos = 1 << 30;
 __device__ __forceinline__ int row_state(const PrefixArgs& a, int seq, int len, bool flags) {
   if (seq == -1) return kPadRow;
   if (seq < 0 || seq >= a.num_seqs || len < 0 || len > a.max_row_len || (len > 0 && len < a.prefix_len)) {
@@ -115,6 +116,47 @@ __device__ __forceinline__ int row_state(const PrefixArgs& a, int seq, int len, 
 __device__ __forceinline__ int row_state(const PrefixArgs& a, int64_t r, bool flags) {
   return row_state(a, __ldg(a.row_seq + r), __ldg(a.row_len + r), flags);
 }
+// The keys that a row of qkv_masked_attn sees, positions [lo, hi); empty and padding rows: lo = hi = 0. near is the
+// seen position next to the row's own, from which the distance bias counts: only differences of the bias matter to the
+// weights, and those from the row's own position would cost a far row bits.
+struct RowRange {
+  int state;  // 0, kEmptyRow or kPadRow
+  int lo, hi, pos, near;
+};
+__device__ __forceinline__ RowRange row_range(const PrefixArgs& a, int64_t r, bool flags) {
+  const int seq = __ldg(a.row_seq + r), end = __ldg(a.row_len + r);
+  const int start = a.row_start != nullptr ? __ldg(a.row_start + r) : 0;
+  const int pos = a.row_pos != nullptr ? __ldg(a.row_pos + r) : end - 1;
+  RowRange x = {kEmptyRow, 0, 0, 0, 0};
+  if (seq == -1) {
+    x.state = kPadRow;
+  } else if (seq < 0 || seq >= a.num_seqs || end < 0 || end > a.max_row_len || start < 0 ||
+             (start < end && (pos < 0 || pos > kMaxRowPos))) {
+    if (flags && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+  } else if (start < end) {
+    const int lo = a.window > 0 ? max(start, pos - a.window + 1) : start;
+    if (lo < end) x.state = 0, x.lo = lo, x.hi = end, x.pos = pos, x.near = min(max(pos, lo), end - 1);
+  }
+  return x;
+}
+// tanh, off by less than 2^-20 of itself: near 0 its series (the first term left out is below 2^-23 of the value),
+// elsewhere one exponential and one reciprocal, 1 - 2 / (1 + e^2z), off by less than 2^-21, with the limits at infinities.
+constexpr float kTanhSmall = 0.4f;
+__device__ __forceinline__ float tanh_series(float z) {
+  const float x = z * z;
+  float s = fmaf(x, -8.8632355e-3f, 2.1869488e-2f);  // -1382 / 155925, 62 / 2835
+  s = fmaf(x, s, -5.3968254e-2f);                    // -17 / 315
+  s = fmaf(x, s, 1.3333333e-1f);                     // 2 / 15
+  s = fmaf(x, s, -3.3333333e-1f);                    // -1 / 3
+  return fmaf(x * s, z, z);
+}
+__device__ __forceinline__ float tanh_exp(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + fast_exp2(z * (2.f * kLog2e))));
+  return fmaf(-2.f, r, 1.f);
+}
+__device__ __forceinline__ float tanh_of(float z) { return fabsf(z) < kTanhSmall ? tanh_series(z) : tanh_exp(z); }
+
 // A kernel that a later one of the call need not wait for, and the wait itself (programmatic launches).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
@@ -137,7 +179,9 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
   else mma_f16(d, a, b0, b1);
 }
 
-template <int FMT, int HD, int NP>
+// MASK: qkv_masked_attn, whose rows see ranges of their sequence's keys, with capped scores and a distance bias. All
+// keys are the rows' own then.
+template <int FMT, int HD, int NP, bool MASK = false>
 __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefix_mma_kernel(const PrefixArgs a) {
   using F = Fmt<FMT>;
   using GM = Geom<FMT, HD, NP>;
@@ -150,10 +194,13 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   __shared__ float sW[kWarps][NP], sInv[NP], sUp[NP];
   __shared__ int64_t sAt[NP];
   __shared__ int sEu[kWarps][NP];
+  // MASK: a pair's range and nearest key, its bias per position (log2 units), and what the bias adds to its log-sum-exp
+  __shared__ int sLo[NP], sHi[NP], sNear[NP];
+  __shared__ float sSlope[NP], sFar[NP];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, hn = lane >> 2;
   const int H = a.num_kv_heads, G = a.num_q_heads / H;
   let_next_start();
-  const bool own_part = blockIdx.x >= a.prefix_items;
+  const bool own_part = MASK || blockIdx.x >= a.prefix_items;
   uint32_t item = own_part ? blockIdx.x - static_cast<uint32_t>(a.prefix_items) : blockIdx.x;
   const uint32_t parts = own_part ? a.own_parts : a.prefix_parts;
   const int part = static_cast<int>(item % parts);
@@ -166,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   uint32_t r0 = 0;  // own part: its first row
   int nrows = 0;    //           its rows, all of one sequence
   int seq = 0;
+  int my_lo = 0, my_hi = 0;  // MASK: the pair's range
   if (own_part) {
     const int T = G >= NP ? 1 : NP / G, chunks = (G + NP - 1) / NP;
     r0 = tile / static_cast<uint32_t>(chunks);
@@ -181,11 +229,24 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     const int into = static_cast<int>(r0 % static_cast<uint32_t>(T));
     if (into != 0 && (same >> 31)) return;
     nrows = min(__ffs(~same) - 1, T - into);
-    const int state = row_state(a, rs, rl, false);
     const int t = G >= NP ? 0 : lane / G;
+    RowRange range;
+    if (MASK) range = row_range(a, there ? rr : static_cast<int64_t>(r0), false);
+    const int state = MASK ? range.state : row_state(a, rs, rl, false);
     my_g = G >= NP ? ch * NP + lane : lane - t * G;
     const int st = __shfl_sync(0xffffffffu, state, t & 31);
     if (lane < NP && t < nrows && my_g < G) my_row = static_cast<int>(r0) + t, my_own = st;
+    if (MASK) {
+      my_lo = __shfl_sync(0xffffffffu, range.lo, t & 31), my_hi = __shfl_sync(0xffffffffu, range.hi, t & 31);
+      const int near = __shfl_sync(0xffffffffu, range.near, t & 31), pos = __shfl_sync(0xffffffffu, range.pos, t & 31);
+      if (my_row < 0) my_lo = my_hi = 0;
+      if (warp == 0 && lane < NP) {
+        const float slope = my_row >= 0 && a.slopes != nullptr ? __ldg(a.slopes + h * G + my_g) : 0.f;
+        sLo[lane] = my_lo, sHi[lane] = my_hi, sNear[lane] = near;
+        sSlope[lane] = -slope * kLog2e;
+        sFar[lane] = near == pos ? 0.f : -slope * fabsf(static_cast<float>(pos - near));
+      }
+    }
   } else {
     const uint32_t flat = tile * NP + lane, row = flat / static_cast<uint32_t>(G);  // below 2^31 + 32
     my_g = static_cast<int>(flat - row * G);
@@ -194,7 +255,18 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 
   // ---------------- its keys: positions [k0, k1) in tiles from a0 (a multiple of TK) on
   int k0, k1, own_min = INT_MAX;  // own_min: the shortest row's end
-  if (own_part) {
+  int own_max = 0;                // MASK: the last row's start
+  if (MASK) {
+    const bool sees = my_lo < my_hi;
+    const int lo = __reduce_min_sync(0xffffffffu, sees ? my_lo : INT_MAX), hi = __reduce_max_sync(0xffffffffu, my_hi);
+    own_min = __reduce_min_sync(0xffffffffu, my_row >= 0 ? my_hi : INT_MAX);
+    own_max = __reduce_max_sync(0xffffffffu, my_lo);
+    const int first = lo < hi ? lo & ~(TK - 1) : 0, np = static_cast<int>(parts);
+    const int per = ((hi - first + np - 1) / np + TK * kWarps - 1) / (TK * kWarps) * (TK * kWarps);
+    const int64_t at = first + static_cast<int64_t>(part) * per;
+    k0 = static_cast<int>(lo < hi ? max(static_cast<int64_t>(lo), min(at, static_cast<int64_t>(hi))) : 0);
+    k1 = static_cast<int>(lo < hi ? min(at + per, static_cast<int64_t>(hi)) : 0);
+  } else if (own_part) {
     const int n = max(0, __reduce_max_sync(0xffffffffu, my_own));
     own_min = a.prefix_len + __reduce_min_sync(0xffffffffu, my_row >= 0 ? max(my_own, 0) : INT_MAX - a.prefix_len);
     // ranges end at multiples of a CTA's step
@@ -244,7 +316,9 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         if (lane < TK && pos >= k0 && pos < k1) {
           const int64_t slot = static_cast<int64_t>(blk) * bsz + (pos - block_of(pos) * bsz);
           if (blk < 0 || slot >= a.num_slots) {
-            if (a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+            bool seen = !MASK;  // rows with ranges apart leave keys between them that none sees
+            for (int p = 0; MASK && p < NP; ++p) seen |= pos >= sLo[p] && pos < sHi[p];
+            if (seen && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
           } else {
             rec_l = static_cast<int>(slot) * H + h;  // the host keeps num_slots * H below 2^31
           }
@@ -319,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   };
 
   int blk = load_blk(0), next0 = load_blk(1);  // before the query's loads: the copies wait for them
+  if (MASK) __syncthreads();  // the pairs' ranges
 
   // ---------------- query rows into registers, each warp a quarter of the pairs
   constexpr int kPer = HD / 32, kQPairs = NP / kWarps;  // dims per lane, pairs per warp
@@ -354,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 #pragma unroll
     for (int k = 0; k < kPer / 2; ++k) w[k] = in ? qw[i][k] : 0u;
     uint8_t* row = sQ + pair * GM::kQRow;
-    float fac = fabsf(a.softmax_scale) * kLog2e;
+    const bool capped = MASK && a.softcap > 0.f;
+    float fac = fabsf(a.softmax_scale) * (capped ? 1.f / a.softcap : kLog2e);
     const float sign = a.softmax_scale < 0.f ? -1.f : 1.f;  // into the query: the logit factor stays >= 0
     if (F::kBytes) {
       float x[kPer], m = 0.f;
@@ -411,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int ow = __shfl_sync(0xffffffffu, my_own, pr[p]);
-    end[p] = own_part ? a.prefix_len + max(ow, 0) : INT_MAX;
+    end[p] = MASK ? sHi[pr[p]] : own_part ? a.prefix_len + max(ow, 0) : INT_MAX;
     row_of[p] = __shfl_sync(0xffffffffu, my_row, pr[p]);
   }
   const uint32_t qa = smem_u32(sQ) + hn * GM::kQRow, qb = qa + (kWide ? 8 * GM::kQRow : 0);
@@ -436,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     const uint32_t mask = lds32(sk + GM::kMask);
     const int base = tile_pos(i);
     // every key wanted by every row: no masks
-    const bool whole = mask == kAll && base + TK <= own_min;
+    const bool whole = mask == kAll && base + TK <= own_min && (!MASK || base >= own_max);
 
     // ---- logits of 2 NH groups of eight keys. kWide: N-tiles, s[n][2p + k]: pair p, key 2c + k of the group;
     // else halves of M-tiles, s[n / 2][2 (n % 2) + p]: key hn of the group, pair p
@@ -519,8 +595,29 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
 #pragma unroll
           for (int p = 0; p < 2; ++p) S(2 * g + n, p, k) *= F::kInt8 ? ks[n][k] * fac[p] : fac[p];
     }
+    if (MASK && a.softcap > 0.f) {
+      const float up = a.softcap * kLog2e;
+#pragma unroll
+      for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int k = 0; k < KL; ++k) S(n, p, k) = up * tanh_of(S(n, p, k));
+    }
+    if (MASK && a.slopes != nullptr) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float slope = sSlope[pr[p]], from = static_cast<float>(base - sNear[pr[p]]);
+#pragma unroll
+        for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+          for (int k = 0; k < KL; ++k) S(n, p, k) = fmaf(slope, fabsf(from + static_cast<float>(key_at(n, k))), S(n, p, k));
+      }
+    }
     vmax[1] = vmax[0];
     if (!whole) {
+      int lo[2] = {0, 0};
+      if (MASK) lo[0] = sLo[pr[0]], lo[1] = sLo[pr[1]];
       vmax[0] = vmax[1] = 0.f;
 #pragma unroll
       for (int n = 0; n < 2 * NH; ++n)
@@ -530,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
           const bool valid = (mask >> key) & 1;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            if (!valid || base + key >= end[p]) S(n, p, k) = -INFINITY;
+            if (!valid || base + key >= end[p] || (MASK && base + key < lo[p])) S(n, p, k) = -INFINITY;
             else if (F::kInt8) vmax[p] = fmaxf(vmax[p], fabsf(vs[n][k]));
           }
         }
@@ -656,18 +753,20 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     // Rows of different lengths in one tile: a key that one row sees and another does not may hold
     // anything there (0 x NaN), so such a tile goes row by row, each with its own keys only, and only
     // that row's sums are taken.
-    if (!F::kInt8 && own_part && nrows > 1 && base + TK > own_min) {
+    if (!F::kInt8 && own_part && nrows > 1 && (base + TK > own_min || (MASK && base < own_max))) {
 #pragma unroll 1
       for (int t = 0; t < nrows; ++t) {
         const int row = static_cast<int>(r0) + t;
-        const int n_end = a.prefix_len + max(0, __shfl_sync(0xffffffffu, my_own, t * G));
+        const int n_end = MASK ? sHi[t * G] : a.prefix_len + max(0, __shfl_sync(0xffffffffu, my_own, t * G));
+        const int n_lo = MASK ? sLo[t * G] : 0;
+        auto sees = [&](int key) -> bool { return base + key < n_end && (!MASK || base + key >= n_lo); };
 #pragma unroll 1
         for (int g = 0; g < NH; ++g) {
           uint32_t keep[2], pg[2 * KL];  // halves of b0 / b1 (the lane's keys) that the row sees
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            keep[k] = (base + 16 * g + key_of<FMT>(k, 2 * c) < n_end ? 0x0000ffffu : 0u) |
-                      (base + 16 * g + key_of<FMT>(k, 2 * c + 1) < n_end ? 0xffff0000u : 0u);
+            keep[k] = (sees(16 * g + key_of<FMT>(k, 2 * c)) ? 0x0000ffffu : 0u) |
+                      (sees(16 * g + key_of<FMT>(k, 2 * c + 1)) ? 0xffff0000u : 0u);
 #pragma unroll
           for (int k = 0; k < 2 * KL; ++k) pg[k] = g == 0 ? pa[0][k] : pa[NH - 1][k];
 #pragma unroll
@@ -735,7 +834,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
     const int head = h * G + my_g;
     int64_t at = -1;
     if (my_row >= 0) {
-      const int state = direct ? row_state(a, static_cast<int64_t>(my_row), head == 0) : 0;
+      int state = 0;
+      if (direct) state = MASK ? row_range(a, my_row, head == 0).state : row_state(a, static_cast<int64_t>(my_row), head == 0);
       const int64_t pair = static_cast<int64_t>(my_row) * a.num_q_heads + head;
       float m = -INFINITY;
 #pragma unroll
@@ -764,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         const int64_t part_at = static_cast<int64_t>(own_part ? a.prefix_parts + part : part) * a.rows * a.num_q_heads + pair;
         const float v = any ? (m - (F::kBf16 ? 0.f : kPShift) + log2f(sum)) * kLn2 : -INFINITY;
         if (!direct) a.lse_part[part_at] = v;
-        else if (a.lse != nullptr) a.lse[pair] = v;
+        else if (a.lse != nullptr) a.lse[pair] = MASK ? v + sFar[lane] : v;
         if (direct) at = pair;
         else if (any) at = part_at;  // a part without keys leaves no values
         if (!any) {
@@ -834,21 +934,21 @@ cudaError_t allow_smem(K kern, int smem, std::atomic<bool> (&done)[64]) {
   return e;
 }
 
-template <int FMT, int HD, int NP>
+template <int FMT, int HD, int NP, bool MASK>
 cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
   static std::atomic<bool> done[64] = {};
   constexpr int smem = Geom<FMT, HD, NP>::kSmem;
-  auto kern = prefix_mma_kernel<FMT, HD, NP>;
+  auto kern = prefix_mma_kernel<FMT, HD, NP, MASK>;
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_after(kern, static_cast<unsigned>(a.prefix_items + a.own_items), kThreads, smem, overlaps, stream, a);
 }
 
-template <int FMT>
+template <int FMT, bool MASK = false>
 cudaError_t launch_mma(const PrefixArgs& a, bool overlaps, cudaStream_t stream) {
   if (a.head_dim == 256)
-    return a.mma_pairs == 8 ? launch_mma<FMT, 256, 8>(a, overlaps, stream) : launch_mma<FMT, 256, 16>(a, overlaps, stream);
-  return a.mma_pairs == 8 ? launch_mma<FMT, 128, 8>(a, overlaps, stream) : launch_mma<FMT, 128, 16>(a, overlaps, stream);
+    return a.mma_pairs == 8 ? launch_mma<FMT, 256, 8, MASK>(a, overlaps, stream) : launch_mma<FMT, 256, 16, MASK>(a, overlaps, stream);
+  return a.mma_pairs == 8 ? launch_mma<FMT, 128, 8, MASK>(a, overlaps, stream) : launch_mma<FMT, 128, 16, MASK>(a, overlaps, stream);
 }
 
 }  // namespace prefix

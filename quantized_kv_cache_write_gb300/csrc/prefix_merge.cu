@@ -12,15 +12,25 @@ namespace {
 
 constexpr int kMergeWarps = 4;
 
-// WP: warps per pair (1 or 4).
-template <int HD, int WP>
+// WP: warps per pair (1 or 4). MASK: qkv_masked_attn, whose parts' log-sum-exps leave out the bias of the row's nearest key.
+template <int HD, int WP, bool MASK>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PrefixArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = WP == 1 ? 0 : warp;
   const int64_t unit = WP == 1 ? static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp : blockIdx.x;  // pair
   const int64_t stride = a.rows * a.num_q_heads;
   if (unit >= stride) return;
   const int64_t row = unit / a.num_q_heads;
-  const int state = row_state(a, row, lane == 0 && sub == 0 && unit == row * a.num_q_heads);
+  const bool flags = lane == 0 && sub == 0 && unit == row * a.num_q_heads;
+  int state;
+  float far = 0.f;
+  if (MASK) {
+    const RowRange x = row_range(a, row, flags);
+    state = x.state;
+    if (a.slopes != nullptr && x.pos != x.near)
+      far = -__ldg(a.slopes + (unit - row * a.num_q_heads)) * fabsf(static_cast<float>(x.pos - x.near));
+  } else {
+    state = row_state(a, row, flags);
+  }
   // the parts of the prefix that this pair's tile was cut into, then those of its own keys
   int pre = a.prefix_parts;
   if (a.umma_cg > 0) {
@@ -100,7 +110,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
   for (int v = 0; v < (WP > 1 ? 1 : kVec); ++v)
     *reinterpret_cast<uint2*>(a.out + unit * HD + 4 * (lane + 32 * (WP > 1 ? warp : v))) =
         make_uint2(round2(a.q_f16, acc[v].x * f, acc[v].y * f), round2(a.q_f16, acc[v].z * f, acc[v].w * f));
-  if (lane == 0 && (WP == 1 || warp == 0) && a.lse != nullptr) a.lse[unit] = any ? ref + logf(sum) : -INFINITY;
+  if (lane == 0 && (WP == 1 || warp == 0) && a.lse != nullptr) a.lse[unit] = any ? ref + logf(sum) + far : -INFINITY;
 }
 
 // Four warps share a pair where there are at least so many parts and not enough pairs to fill the GPU with one
@@ -112,13 +122,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pr
 constexpr int kSharedParts = 8;
 constexpr int64_t kSharedPairs = 2048;
 
-template <int HD>
+template <int HD, bool MASK>
 cudaError_t launch_merge(const PrefixArgs& a, cudaStream_t stream) {
   const int64_t pairs = a.rows * a.num_q_heads;
   const bool overlaps = a.prefix_parts + a.own_parts > 0;
   if (a.prefix_parts + a.own_parts >= kSharedParts && pairs <= kSharedPairs)
-    return launch_after(prefix_merge_kernel<HD, 4>, static_cast<unsigned>(pairs), 32 * kMergeWarps, 0, overlaps, stream, a);
-  return launch_after(prefix_merge_kernel<HD, 1>, static_cast<unsigned>((pairs + kMergeWarps - 1) / kMergeWarps),
+    return launch_after(prefix_merge_kernel<HD, 4, MASK>, static_cast<unsigned>(pairs), 32 * kMergeWarps, 0, overlaps, stream, a);
+  return launch_after(prefix_merge_kernel<HD, 1, MASK>, static_cast<unsigned>((pairs + kMergeWarps - 1) / kMergeWarps),
                       32 * kMergeWarps, 0, overlaps, stream, a);
 }
 
@@ -126,7 +136,10 @@ cudaError_t launch_merge(const PrefixArgs& a, cudaStream_t stream) {
 }  // namespace prefix
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream) {
-  return a.head_dim == 256 ? prefix::launch_merge<256>(a, stream) : prefix::launch_merge<128>(a, stream);
+  return a.head_dim == 256 ? prefix::launch_merge<256, false>(a, stream) : prefix::launch_merge<128, false>(a, stream);
+}
+cudaError_t launch_masked_merge(const PrefixArgs& a, cudaStream_t stream) {
+  return a.head_dim == 256 ? prefix::launch_merge<256, true>(a, stream) : prefix::launch_merge<128, true>(a, stream);
 }
 
 }  // namespace qkv

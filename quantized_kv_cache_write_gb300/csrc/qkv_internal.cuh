@@ -227,20 +227,32 @@ struct PrefixArgs {
   int umma_ptiles = 0;
   uint32_t umma_blocks = 0, umma_teams = 0, umma_share = 0, umma_extra = 0;
   uint32_t umma_drop = UINT32_MAX;  // the block whose records' hand-off a test leaves out; none
+  // qkv_masked_attn: row_len holds the rows' ends, prefix_len is 0
+  const int32_t* row_start = nullptr;  // null: 0
+  const int32_t* row_pos = nullptr;    // null: the row's end - 1
+  int window = 0;                      // 0: none
+  float softcap = 0.f;                 // 0: none
+  const float* slopes = nullptr;       // [Hq], null: no bias
 };
 // the mma.sync tiles of (row, head) pairs over prefix_items ranges of the prefix and own_items of the
 // keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
 cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
+cudaError_t launch_masked_mma_bf16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_bf16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
+cudaError_t launch_masked_mma_f16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_f16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
+cudaError_t launch_masked_mma_int8_side(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_int8_side(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
+cudaError_t launch_masked_mma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
+cudaError_t launch_masked_mma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_merge(const PrefixArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device helpers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
