@@ -60,8 +60,14 @@ SOURCES = [
     "masked_e4m3.cu",
     "masked_bf16.cu",
     "masked_f16.cu",
+    "masked_umma_int8_side.cu",
+    "masked_umma_int8_inline.cu",
+    "masked_umma_e4m3.cu",
+    "masked_umma_bf16.cu",
+    "masked_umma_f16.cu",
+    "masked_plan.cu",
 ]
-HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "rope.cuh", "append.cuh", "prefix_attn.cuh", "prefix_umma.cuh"]
+HEADERS = ["qkv_internal.cuh", "gather_attn.cuh", "gather_umma.cuh", "write_rows.cuh", "rope.cuh", "append.cuh", "prefix_attn.cuh", "prefix_umma.cuh", "masked_tiles.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

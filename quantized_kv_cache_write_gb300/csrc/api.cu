@@ -894,14 +894,21 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* d, void* stream) {
 
 namespace {
 
+// How a masked call runs: on mma.sync tiles of the rows over `parts` ranges of their keys, or on tcgen05 tiles of
+// tile_rows rows (umma_cg > 0) that teams of umma_cg SMs take from the work list.
 struct MaskedPlan {
   int64_t tiles;  // mma.sync tiles
   int parts;      // ranges of their keys
-  int64_t rows_heads;
+  int umma_cg, umma_pairs, tile_rows, block_keys;
+  uint32_t umma_teams;
+  int64_t rows, rows_heads;
   int head_dim;
-  // partial outputs, then partial log-sum-exps; a single part writes the output itself
-  size_t o_bytes() const { return parts > 1 ? static_cast<size_t>(parts) * rows_heads * head_dim * 4 : 0; }
-  size_t bytes() const { return o_bytes() + (parts > 1 ? static_cast<size_t>(parts) * rows_heads * 4 : 0); }
+  // Partial outputs, then partial log-sum-exps, then the work list. Of mma.sync tiles a single part writes the output
+  // itself; a team of SMs leaves at most two partial tiles.
+  int64_t part_rows() const { return umma_cg > 0 ? 2 * static_cast<int64_t>(umma_teams) * umma_pairs : parts > 1 ? parts * rows_heads : 0; }
+  size_t o_bytes() const { return static_cast<size_t>(part_rows()) * head_dim * 4; }
+  size_t list_at() const { return o_bytes() + (static_cast<size_t>(part_rows()) * 4 + 15) / 16 * 16; }
+  size_t bytes() const { return list_at() + (umma_cg > 0 ? qkv::masked_plan_bytes(rows) : 0); }
 };
 
 qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
@@ -909,6 +916,9 @@ qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, in
   if (num_seqs < 1 || window < 0) return QKV_ERR_ARG;
   return check_prefix_shape(fmt, rows, num_q_heads, num_kv_heads, head_dim, 0, max_row_end);
 }
+
+// Pairs of a sequence, on average, from which a masked call runs on tcgen05 tiles.
+constexpr int64_t kMaskedUmmaPairs = 64;
 
 qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                        int max_row_end, int window, MaskedPlan* p) {
@@ -921,8 +931,32 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   // a tile's rows that follow each other see a window's keys and a few more
   const int64_t keys = window > 0 && window < max_row_end - 16 ? window + 16 : max_row_end;
   p->parts = key_parts(p->tiles, static_cast<int>(keys > 0 ? keys : 1), row_bytes_of(fmt, head_dim), sms);
-  if (p->tiles * p->parts > INT32_MAX) return QKV_ERR_ARG;
+  p->rows = rows;
+  p->umma_cg = 0, p->umma_pairs = 0, p->tile_rows = 0, p->block_keys = 0, p->umma_teams = 0;
+  const int64_t pairs = rows * G / num_seqs;  // of a sequence
+  if (pairs >= kMaskedUmmaPairs && max_row_end <= (1 << 27)) {
+    p->umma_cg = pairs > (head_dim == 128 ? 256 : 128) ? 2 : 1;
+    p->umma_pairs = p->umma_cg == 1 ? 128 : head_dim == 128 ? 512 : 256;
+    p->tile_rows = p->umma_pairs / G;
+    p->block_keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
+    p->umma_teams = static_cast<uint32_t>(sms / p->umma_cg);
+    // a team's share is counted in 32 bits, however the rows are cut into tiles
+    const int64_t blocks = max_row_end / p->block_keys + 2;
+    if (rows > (int64_t(1) << 31) / blocks / num_kv_heads * p->umma_teams) p->umma_cg = 0;
+  }
+  if (p->umma_cg == 0 && p->tiles * p->parts > INT32_MAX) return QKV_ERR_ARG;
   return QKV_OK;
+}
+
+cudaError_t launch_masked_umma(const qkv::PrefixArgs& a, qkv_format fmt, cudaStream_t s) {
+  switch (fmt) {
+    case QKV_BF16: return qkv::launch_masked_umma_bf16(a, s);
+    case QKV_F16: return qkv::launch_masked_umma_f16(a, s);
+    case QKV_INT8_SIDE: return qkv::launch_masked_umma_int8_side(a, s);
+    case QKV_INT8_INLINE: return qkv::launch_masked_umma_int8_inline(a, s);
+    case QKV_E4M3: return qkv::launch_masked_umma_e4m3(a, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_masked_mma(const qkv::PrefixArgs& a, qkv_format fmt, cudaStream_t s) {
@@ -1016,17 +1050,31 @@ qkv_status qkv_masked_attn(const qkv_masked_desc* d, void* stream) {
   a.lse = d->lse;
   a.merge_scale = d->fmt == QKV_E4M3 ? d->v_scale_layer : 1.f;
   a.dev_status = d->dev_status;
-  const bool direct = p.parts == 1;
-  a.o_part = direct ? nullptr : static_cast<float*>(d->workspace);
-  a.lse_part = direct ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + p.o_bytes());
-  a.own_parts = p.parts;
-  a.own_items = p.tiles * p.parts;
-  // tiles of 8 pairs where a sequence's rows bring no more than that on average, as for qkv_prefix_attn's own keys
-  const int G = d->num_q_heads / d->num_kv_heads;
-  a.mma_pairs = G <= 8 && d->rows * G <= 8 * d->num_seqs ? 8 : 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_masked_mma(a, d->fmt, s);
-  if (e == cudaSuccess && !direct) e = qkv::launch_masked_merge(a, s);
+  uint8_t* ws = static_cast<uint8_t*>(d->workspace);
+  const bool direct = p.part_rows() == 0;
+  a.o_part = direct ? nullptr : reinterpret_cast<float*>(ws);
+  a.lse_part = direct ? nullptr : reinterpret_cast<float*>(ws + p.o_bytes());
+  cudaError_t e;
+  if (p.umma_cg > 0) {
+    a.plan = ws + p.list_at();
+    a.umma_cg = p.umma_cg;
+    a.umma_pairs = p.umma_pairs;
+    a.umma_teams = p.umma_teams;
+    a.tile_rows = p.tile_rows;
+    a.block_keys = p.block_keys;
+    e = qkv::launch_masked_plan(a, s);
+    if (e == cudaSuccess) e = launch_masked_umma(a, d->fmt, s);
+    if (e == cudaSuccess) e = qkv::launch_masked_join(a, s);
+  } else {
+    a.own_parts = p.parts;
+    a.own_items = p.tiles * p.parts;
+    // tiles of 8 pairs where a sequence's rows bring no more than that on average, as for qkv_prefix_attn's own keys
+    const int G = d->num_q_heads / d->num_kv_heads;
+    a.mma_pairs = G <= 8 && d->rows * G <= 8 * d->num_seqs ? 8 : 16;
+    e = launch_masked_mma(a, d->fmt, s);
+    if (e == cudaSuccess && !direct) e = qkv::launch_masked_merge(a, s);
+  }
   return cuda_status(e);
 }
 

@@ -1,0 +1,209 @@
+// The work list of qkv_masked_attn's tcgen05 tiles, and the join of the tiles that teams share (masked_tiles.cuh).
+#include "prefix_umma.cuh"
+
+namespace qkv {
+namespace prefix {
+namespace {
+
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+
+// Inclusive sum over the block's threads; `total` is the last one's.
+__device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* sums, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t s = sums[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, s, off);
+      if (lane >= off) s += y;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  if (warp > 0) x += sums[warp - 1];
+  total = sums[kPlanWarps - 1];
+  __syncthreads();
+  return x;
+}
+
+// One block; a thread per row, as many whole groups of tile_rows rows at a time as it has threads.
+__global__ void __launch_bounds__(kPlanThreads) masked_plan_kernel(const PrefixArgs a) {
+  __shared__ int sSeq[kPlanThreads], sLo[kPlanThreads], sHi[kPlanThreads];
+  __shared__ int tLo[kPlanThreads], tHi[kPlanThreads], tAllLo[kPlanThreads], tAllHi[kPlanThreads], tRow[kPlanThreads], tRows[kPlanThreads];
+  __shared__ uint32_t sums[kPlanWarps];
+  let_next_start();
+  const int tid = threadIdx.x, T = a.tile_rows, KB = a.block_keys, step = kPlanThreads / T * T;
+  MaskedHead* head = static_cast<MaskedHead*>(a.plan);
+  MaskedTile* tiles = reinterpret_cast<MaskedTile*>(head + 1);
+  uint64_t units = 0;
+  uint32_t count = 0;
+  for (int64_t r0 = 0; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + tid;
+    const bool there = tid < step && row < a.rows;
+    RowRange x = {kPadRow, 0, 0, 0, 0};
+    int seq = -1;
+    if (there) x = row_range(a, row, true), seq = __ldg(a.row_seq + row);
+    const bool live = x.state != kPadRow, sees = x.lo < x.hi;
+    sSeq[tid] = live ? seq : -1, sLo[tid] = x.lo, sHi[tid] = x.hi;
+    tLo[tid] = INT_MAX, tHi[tid] = 0, tAllLo[tid] = 0, tAllHi[tid] = INT_MAX, tRows[tid] = 0;
+    __syncthreads();
+    bool first = live;
+    if (live && tid % T != 0) {
+      const int lo = sLo[tid - 1], hi = sHi[tid - 1];
+      const bool apart = sees && lo < hi && max(lo, x.lo) > min(hi, x.hi);
+      first = sSeq[tid - 1] != seq || apart;  // a padding row before: another sequence (-1)
+    }
+    uint32_t n;
+    const uint32_t i = scan(first ? 1 : 0, sums, n) - 1;  // the row's tile of these
+    // a tile's rows of the warp to the first of them, and from there into the tile
+    const int tile = live ? static_cast<int>(i) : -1, lane = tid & 31;
+    int rows = 1, lo = sees ? x.lo : INT_MAX, hi = x.hi, all_lo = x.lo, all_hi = sees ? x.hi : INT_MAX;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o_tile = __shfl_down_sync(0xffffffffu, tile, off), o_rows = __shfl_down_sync(0xffffffffu, rows, off);
+      const int o_lo = __shfl_down_sync(0xffffffffu, lo, off), o_hi = __shfl_down_sync(0xffffffffu, hi, off);
+      const int o_all_lo = __shfl_down_sync(0xffffffffu, all_lo, off), o_all_hi = __shfl_down_sync(0xffffffffu, all_hi, off);
+      if (lane + off < 32 && o_tile == tile) {
+        rows += o_rows, lo = min(lo, o_lo), hi = max(hi, o_hi), all_lo = max(all_lo, o_all_lo), all_hi = min(all_hi, o_all_hi);
+      }
+    }
+    const int before = __shfl_up_sync(0xffffffffu, tile, 1);
+    if (live && first) tRow[i] = static_cast<int>(row);
+    if (live && (lane == 0 || before != tile)) {
+      atomicAdd(tRows + i, rows);
+      atomicMin(tLo + i, lo), atomicMax(tHi + i, hi);
+      atomicMax(tAllLo + i, all_lo), atomicMin(tAllHi + i, all_hi);
+    }
+    __syncthreads();
+    MaskedTile t = {};
+    uint32_t blocks = 0, sum;
+    if (tid < n) {
+      t.row0 = tRow[tid], t.nrows = tRows[tid], t.seq = sSeq[t.row0 - r0];
+      if (tHi[tid] > 0) t.lo = tLo[tid], t.hi = tHi[tid], t.all_lo = tAllLo[tid], t.all_hi = tAllHi[tid];
+      blocks = max(1, (t.hi + KB - 1) / KB - t.lo / KB);  // rows that see nothing have a block without keys
+    }
+    t.first = units + scan(blocks, sums, sum) - blocks;  // the host keeps 1024 tiles' blocks below 2^32
+    if (tid < n) tiles[count + tid] = t;
+    count += n;
+    units += sum;
+  }
+  if (tid == 0) {
+    tiles[count].first = units;
+    head->units = units, head->tiles = count;
+  }
+}
+
+// A tile that teams share: its (row, head) pairs, one warp each, from the parts that the teams left.
+constexpr int kJoinWarps = 8;
+template <int HD>
+__global__ void __launch_bounds__(32 * kJoinWarps) masked_join_kernel(const PrefixArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  await_previous();
+  // the tile that team blockIdx.x begins and does not finish
+  const MaskedHead head = *plan_head(a);
+  const MaskedTile* tiles = plan_tiles(a);
+  const Shares s(head.units * a.num_kv_heads, a.umma_teams);
+  const uint32_t team = blockIdx.x;
+  const uint64_t from = s.first(team), end = from + s.of(team);
+  if (end == from || end == head.units * a.num_kv_heads) return;
+  const int h = static_cast<int>((end - 1) / head.units);
+  const uint64_t h0 = h * head.units, rem = end - 1 - h0;
+  int lo = 0, hi = static_cast<int>(head.tiles);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tiles[mid].first <= rem) lo = mid;
+    else hi = mid;
+  }
+  const MaskedTile t = tiles[lo];
+  const uint64_t begin = h0 + t.first, stop = h0 + tiles[lo + 1].first;
+  if (begin < from || stop <= end) return;  // begun by a team before, or finished
+  uint32_t parts = 1;
+  for (uint64_t u = end; u < stop; ++parts) u += s.of(team + parts);
+  const int G = a.num_q_heads / a.num_kv_heads;
+  const int flat = static_cast<int>(blockIdx.y) * kJoinWarps + warp;
+  if (flat >= t.nrows * G) return;
+  const int64_t row = t.row0 + flat / G, at = row * a.num_q_heads + h * G + flat % G;
+  // part i: place 1 of the team that begins, place 0 of those after it
+  auto place = [&](uint32_t i) -> int64_t { return static_cast<int64_t>(i == 0 ? 2 * team + 1 : 2 * (team + i)) * a.umma_pairs + flat; };
+  float m = -INFINITY;
+  bool nan = false;
+  for (uint32_t i = lane; i < parts; i += 32) {
+    const float v = __ldcg(a.lse_part + place(i));
+    nan |= v != v;
+    m = fmaxf(m, v);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  nan = __any_sync(0xffffffffu, nan);
+  constexpr int kVec = HD / 128;
+  float4 acc[kVec];
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const bool any = m != -INFINITY || nan;
+  const float ref = m == -INFINITY ? 0.f : m;
+  if (any) {
+#pragma unroll 4
+    for (uint32_t i = 0; i < parts; ++i) {
+      const float l = __ldcg(a.lse_part + place(i));
+      const bool none = l == -INFINITY;  // a part without keys wrote no values; one with keys counts, its values may be NaN
+      const float w = none ? 0.f : expf(l - ref);
+      sum += w;
+      const float4* src = reinterpret_cast<const float4*>(a.o_part + place(i) * HD);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!none) x = __ldcg(src + lane + 32 * v);
+        acc[v].x += w * x.x, acc[v].y += w * x.y, acc[v].z += w * x.z, acc[v].w += w * x.w;
+      }
+    }
+  }
+  const float f = any ? a.merge_scale / sum : 0.f;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v)
+    *reinterpret_cast<uint2*>(a.out + at * HD + 4 * (lane + 32 * v)) =
+        make_uint2(round2(a.q_f16, acc[v].x * f, acc[v].y * f), round2(a.q_f16, acc[v].z * f, acc[v].w * f));
+  if (lane == 0 && a.lse != nullptr) {
+    const RowRange x = row_range(a, row, false);
+    float far = 0.f;
+    if (a.slopes != nullptr && x.pos != x.near) far = -__ldg(a.slopes + h * G + flat % G) * fabsf(static_cast<float>(x.pos - x.near));
+    a.lse[at] = any ? ref + logf(sum) + far : -INFINITY;
+  }
+}
+
+template <int HD>
+cudaError_t launch_join(const PrefixArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.umma_teams, (a.umma_pairs + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, masked_join_kernel<HD>, a);
+}
+
+}  // namespace
+}  // namespace prefix
+
+size_t masked_plan_bytes(int64_t rows) {
+  return sizeof(prefix::MaskedHead) + static_cast<size_t>(rows + 1) * sizeof(prefix::MaskedTile);
+}
+cudaError_t launch_masked_plan(const PrefixArgs& a, cudaStream_t stream) {
+  prefix::masked_plan_kernel<<<1, prefix::kPlanThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+cudaError_t launch_masked_join(const PrefixArgs& a, cudaStream_t stream) {
+  return a.head_dim == 256 ? prefix::launch_join<256>(a, stream) : prefix::launch_join<128>(a, stream);
+}
+
+}  // namespace qkv

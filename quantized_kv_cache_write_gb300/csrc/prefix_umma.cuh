@@ -43,7 +43,7 @@
 
 #include <cstdlib>
 
-#include "prefix_attn.cuh"
+#include "masked_tiles.cuh"
 
 namespace qkv {
 namespace prefix {
@@ -56,7 +56,7 @@ constexpr int kScRing = 4, kRecRing = 8;
 // keys of a block: 128; 64 where one SM holds 256-wide heads alone
 constexpr int umma_block_keys(int head_dim, int cg) { return head_dim == 256 && cg == 1 ? 64 : 128; }
 
-template <int FMT, int HD, int NT, int CG>
+template <int FMT, int HD, int NT, int CG, bool MASK = false>
 struct Umma {
   using F = Fmt<FMT>;
   static constexpr int KB = umma_block_keys(HD, CG);
@@ -77,7 +77,11 @@ struct Umma {
   static constexpr uint32_t kScVs = 4 * KB, kScMask = 8 * KB, kScVmax = kScMask + 16, kScStage = kScVmax + 16;
   static constexpr uint32_t kRec = kSc + kScRing * kScStage;       // record numbers of a block's keys
   static constexpr uint32_t kRow = kRec + kRecRing * 4 * KB;       // per row: its threads' maxima (sums), two phases
-  static constexpr uint32_t kBar = kRow + 2 * kParts * 4 * kTileM;
+  // MASK: each pair's range, nearest position and slope; each softmax warp's positions that all its rows see; blocks whose
+  // values that are not finite were left out (a bit for each block modulo 32)
+  static constexpr uint32_t kTab = kRow + 2 * kParts * 4 * kTileM, kAll = kTab + (MASK ? NT * kTileM * 16 : 0);
+  static constexpr uint32_t kOdd = kAll + (MASK ? NT * kSoftWarps * 8 : 0);
+  static constexpr uint32_t kBar = kOdd + (MASK ? 16 : 0);
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
                             kRecFull = kScEmpty + 8 * kScRing, kRecEmpty = kRecFull + 8 * kRecRing,
@@ -298,20 +302,43 @@ __device__ __forceinline__ Segment first_segment(const PrefixArgs& a) {
 }
 
 // Positions of the prefix to records of the pool.
+// MASK: positions from `lo` on only.
+template <bool MASK>
 struct Records {
   const int32_t* blocks;
   int64_t num_slots;
-  int bsz, shift, len, H, h;
+  int bsz, shift, len, H, h, lo = 0;
   bool pow2;
+  __device__ __forceinline__ bool in(int p) const { return p < len && (!MASK || p >= lo); }
   __device__ __forceinline__ int block_of(int p) const { return pow2 ? p >> shift : p / bsz; }
   // block id of position p, -1 past the prefix
-  __device__ __forceinline__ int lookup(int p) const { return p < len ? __ldg(blocks + block_of(p)) : -1; }
+  __device__ __forceinline__ int lookup(int p) const { return in(p) ? __ldg(blocks + block_of(p)) : -1; }
   // record of position p in block blk, -1: none
   __device__ __forceinline__ int record(int p, int blk) const {
     const int64_t slot = static_cast<int64_t>(blk) * bsz + (p - block_of(p) * bsz);
-    return (p < len && blk >= 0 && slot < num_slots) ? static_cast<int>(slot) * H + h : -1;
+    return (in(p) && blk >= 0 && slot < num_slots) ? static_cast<int>(slot) * H + h : -1;
   }
 };
+
+// A 16-bit value (its bits) that is not finite.
+template <bool BF16>
+__device__ __forceinline__ bool odd16(uint32_t x) {
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+  return (x & kExp) == kExp;
+}
+// Two 16-bit values with those that are not finite set to 0.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  return w & ((odd16<BF16>(w) ? 0u : 0x0000ffffu) | (odd16<BF16>(w >> 16) ? 0u : 0xffff0000u));
+}
+
+// E4M3 codes with the NaNs set to 0; not 0: there were any.
+__device__ __forceinline__ uint32_t drop_odd_e4m3(uint4& v) {
+  const uint32_t a = __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu), b = __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  const uint32_t c = __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu), d = __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  v.x &= ~a, v.y &= ~b, v.z &= ~c, v.w &= ~d;
+  return a | b | c | d;
+}
 
 // One operand's part of a block as the producers move it: ROWS keys of kBytes bytes each, from byte
 // `off` of the record on. Each warp of a group takes a quarter of the rows; a row is kLpr lanes of 16 B. In the slot,
@@ -336,6 +363,21 @@ struct Operand {
       cp_async16(slot + (ch >> 3) * kCol + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
                  cache + static_cast<uint64_t>(static_cast<uint32_t>(max(rk, 0))) * kGlobalRow + off + 16 * ch, rk >= 0 ? 16 : 0);
     }
+  }
+  // The lane's own copied chunks with the values that are not finite set to 0; whether there were any.
+  template <bool BF16>
+  static __device__ __forceinline__ bool drop_odd(uint32_t slot, int pw, int lane) {
+    const int ch = lane % kLpr;
+    bool any = false;
+#pragma unroll 4
+    for (int u = 0; u < kInstr; ++u) {
+      const int row = kWarpRows * pw + kPerInstr * u + lane / kLpr;
+      const uint32_t at = slot + (ch >> 3) * kCol + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+      const uint4 v = lds128(at);
+      const uint4 w = make_uint4(finite2<BF16>(v.x), finite2<BF16>(v.y), finite2<BF16>(v.z), finite2<BF16>(v.w));
+      if ((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) sts128(at, w), any = true;
+    }
+    return any;
   }
 };
 
@@ -413,10 +455,107 @@ __device__ __forceinline__ void convert_rows(uint32_t slot, const Rows& r, const
 __device__ __forceinline__ uint32_t k_slot(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ uint32_t v_slot(int j, int B) { return j == B - 1 ? 2 * B - 1 : 2 * j + 2; }
 
-template <int FMT, int HD, int NT, int CG>
-__global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umma_kernel(const PrefixArgs a) {
+// Scores of N columns in log2 units from their logits: x fac, capped and less the distance bias. The columns' positions are
+// base + k; `row` addresses the pair's nearest position and its slope.
+template <int N>
+__device__ __forceinline__ void adjust_scores(float (&x)[N], float fac, float cap, bool bias, uint32_t row, int base) {
+  const uint64_t fac2 = f2pack(fac, fac);
+#pragma unroll
+  for (int k = 0; k < N; k += 2) f2unpack(f2mul(f2pack(x[k], x[k + 1]), fac2), x[k], x[k + 1]);
+  if (cap > 0.f) {
+    const float up = cap * kLog2e;
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = up * tanh_of(x[k]);
+  }
+  if (bias) {
+    const uint2 v = lds64(row);
+    const float from = static_cast<float>(base - static_cast<int>(v.x)), slope = __uint_as_float(v.y);
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = fmaf(slope, fabsf(from + static_cast<float>(k)), x[k]);
+  }
+}
+
+// The values that are not finite which the producers of a masked segment left out of blocks that some rows do not see whole,
+// added to the thread's part of O (HD / kParts dims from d0 on) where its row sees their keys. `odd` addresses the SM's
+// record of such blocks; a pair's second SM has its own, since each converts half of the dims. Nearly always there are none.
+template <int FMT, int HD, int KB, int CG, typename REC, typename SEG>
+__device__ __forceinline__ void add_odd(const PrefixArgs& a, REC rc, const SEG& seg, int h, uint32_t odd, uint32_t range, uint32_t to,
+                                        int d0, bool in) {
   using F = Fmt<FMT>;
-  using U = Umma<FMT, HD, NT, CG>;
+  uint32_t bits = 0;
+  asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < CG; ++i) {
+    uint32_t x;
+    asm volatile("{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %1, %2;\n ld.volatile.shared::cluster.u32 %0, [ra];\n}\n" : "=r"(x) : "r"(odd), "r"(i));
+    bits |= x;
+  }
+  if (__builtin_expect(!__any_sync(0xffffffffu, bits != 0u), 1)) return;
+  const uint2 lim = lds64(range);
+  const int lo = static_cast<int>(lim.x), hi = in ? static_cast<int>(lim.y) : 0;
+  rc.h = h, rc.lo = seg.t.lo, rc.len = seg.t.hi;
+  rc.blocks = a.block_table + static_cast<int64_t>(seg.t.hi > 0 ? seg.t.seq : 0) * a.max_blocks;
+  for (int j = seg.b0; j < seg.b1; ++j) {
+    const int p0 = j * KB;
+    if (!((bits >> (j & 31)) & 1) || (p0 >= seg.t.all_lo && p0 + KB <= seg.t.all_hi)) continue;
+    for (int c = 0; c < HD / kParts; c += 16) {
+      float o[16];
+      tmem_load(to + c, o);
+      tmem_loaded(o);
+      for (int p = max(p0, seg.t.lo); p < min(p0 + KB, seg.t.hi); ++p) {
+        const int rec = rc.record(p, rc.lookup(p));
+        if (rec < 0 || p < lo || p >= hi) continue;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(rec)) * HD + d0 + c + k;
+          if (FMT == QKV_E4M3) {
+            if ((__ldg(a.v_cache + at) & 0x7f) == 0x7f) o[k] = NAN;
+          } else {
+            const uint32_t v = __ldg(reinterpret_cast<const uint16_t*>(a.v_cache) + at);
+            if (odd16<F::kBf16>(v)) o[k] += F::kBf16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+          }
+        }
+      }
+      __syncwarp();
+      uint32_t w[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k]);
+      tmem_st_x16(to + c, w);
+      tmem_wait_st();
+    }
+  }
+}
+
+// The segments of the prefix or of the masked rows, alike for the roles.
+template <bool MASK, int KB>
+struct Segments;
+template <int KB>
+struct Segments<false, KB> : Segment {
+  template <int CG>
+  __device__ __forceinline__ void begin(const PrefixArgs& a) { static_cast<Segment&>(*this) = first_segment<CG>(a); }
+  __device__ __forceinline__ int head(const PrefixArgs& a) const { return tile / a.umma_ptiles; }
+};
+template <int KB>
+struct Segments<true, KB> : MaskedSegment<KB> {
+  uint32_t team;
+  template <int CG>
+  __device__ __forceinline__ void begin(const PrefixArgs& a) {
+    team = blockIdx.x / CG;
+    MaskedSegment<KB>::begin(a, team);
+  }
+  __device__ __forceinline__ bool next(const PrefixArgs& a) { return MaskedSegment<KB>::next(a, team); }
+  __device__ __forceinline__ int head(const PrefixArgs&) const { return this->h_now; }
+};
+
+// MASK: qkv_masked_attn, with the work list of masked_tiles.cuh. What differs: the tile's keys lie in its sequence's row
+// of the block table, a block that not all of a warp's rows see whole is masked row by row, scores may be capped and get the
+// distance bias, and a tile that one team has whole is written out here. A value of V that is not finite in a
+// block that some row of the tile does not see whole is left out of the product (0 times it would not be 0) and added at
+// the end for the rows that see it.
+template <int FMT, int HD, int NT, int CG, bool MASK>
+__global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) prefix_umma_kernel(const PrefixArgs a) {
+  using F = Fmt<FMT>;
+  using U = Umma<FMT, HD, NT, CG, MASK>;
   constexpr int NS = U::kSlots, KB = U::KB;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -450,6 +589,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       bar_init(sb + U::kDrain, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
       sts32(flag, 0u);
+      if (MASK) sts32(sb + U::kOdd, 0u);
     }
     __syncwarp();
   }
@@ -458,8 +598,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   team_sync<CG>();
   tmem_fence_after_sync();
   const uint32_t tb = lds32(sb + U::kTmemSlot);
-  Segment seg = first_segment<CG>(a);
-  Records rc;
+  if (MASK) await_previous();  // the work list
+  Segments<MASK, KB> seg;
+  seg.template begin<CG>(a);
+  Records<MASK> rc;
   rc.blocks = a.prefix_blocks, rc.num_slots = a.num_slots, rc.bsz = a.block_size, rc.len = a.prefix_len, rc.H = H;
   rc.pow2 = (rc.bsz & (rc.bsz - 1)) == 0, rc.shift = __ffs(rc.bsz) - 1;
 
@@ -503,8 +645,34 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
       return done;
     };
     while (seg.next(a)) {
-      const int h = seg.tile / a.umma_ptiles;
-      const uint32_t flat0 = (static_cast<uint32_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
+      const int h = seg.head(a);
+      uint32_t flat0, flats = pairs;  // the thread's pair in tile 0, and how many there are (MASK: of the tile's rows)
+      const uint16_t* q0 = a.q;
+      if constexpr (MASK) {
+        flat0 = rank * kTileM + r, flats = static_cast<uint32_t>(seg.t.nrows * G);
+        q0 += seg.t.row0 * a.q_stride;
+        // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see
+#pragma unroll 1
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t flat = flat0 + t * CG * kTileM;
+          RowRange x = {kPadRow, 0, 0, 0, 0};
+          const uint32_t row = flat / G;
+          if (flat < flats) x = row_range(a, seg.t.row0 + static_cast<int64_t>(row), false);
+          const float slope = flat < flats && a.slopes != nullptr ? __ldg(a.slopes + h * G + (flat - row * G)) : 0.f;
+          if (wg == 0)
+            sts128(sb + U::kTab + 16 * (t * kTileM + r), make_uint4(x.lo, x.hi, x.near, __float_as_uint(-slope * kLog2e)));
+          const int lo = __reduce_max_sync(0xffffffffu, flat < flats ? x.lo : 0);
+          const int hi = __reduce_min_sync(0xffffffffu, flat < flats ? x.hi : INT_MAX);
+          if (lane == 0) {
+            sts32(sb + U::kAll + 8 * (t * U::kSoftWarps + warp), lo);
+            sts32(sb + U::kAll + 8 * (t * U::kSoftWarps + warp) + 4, hi);
+          }
+        }
+        __syncwarp();
+        if (vote(!ok)) break;  // the table is read from here on
+      } else {
+        flat0 = (static_cast<uint32_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
+      }
       // state of the tile at hand; with two tiles the other one's waits in the second element
       float M[2] = {-INFINITY, -INFINITY}, R[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, fac[NT] = {};
       int E[2] = {F::kInt8 ? -90 : 0, F::kInt8 ? -90 : 0};
@@ -527,10 +695,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
 #pragma unroll 1
       for (int t = 0; t < NT; ++t, other_tile()) {
         const uint32_t flat = flat0 + t * CG * kTileM;
-        const bool in = flat < pairs;
+        const bool in = flat < flats;
         const uint32_t row = in ? flat / G : 0;
         warp_in[0] = __any_sync(0xffffffffu, in);
-        const uint16_t* src = a.q + row * a.q_stride + static_cast<int64_t>(in ? h * G + (flat - row * G) : 0) * HD + d0;
+        const uint16_t* src = q0 + row * a.q_stride + static_cast<int64_t>(in ? h * G + (flat - row * G) : 0) * HD + d0;
         const uint32_t part = own_part + t * U::kQTile;
         uint4 v[kVec];
 #pragma unroll
@@ -546,7 +714,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           if (!F::kBytes && sign < 0.f) v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
           sts128(part + rr * 128 + (((c0 + lane % kVec) ^ (rr & 7)) << 4), v[i]);
         }
-        float fc = fabsf(a.softmax_scale) * kLog2e;
+        float fc = fabsf(a.softmax_scale) * (MASK && a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
         if (F::kBytes) {
           __syncwarp();
           uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
@@ -602,7 +770,19 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         tmem_fence_after_sync();
         if (warp_in[0]) {  // the same in the kParts warps
           const uint4 mw = lds128(sc + U::kScMask);
-          const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
+          bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
+          uint32_t seen = ~0u;  // MASK: the thread's columns that its row sees
+          const int base = (seg.b0 + i / NT) * KB + wg * HB;  // MASK: position of the thread's first column
+          if (MASK) {
+            const uint2 all = lds64(sb + U::kAll + 8 * (t * U::kSoftWarps + warp));
+            whole = whole && base - wg * HB >= static_cast<int>(all.x) && base - wg * HB + KB <= static_cast<int>(all.y);
+            if (!whole) {
+              const uint2 range = lds64(sb + U::kTab + 16 * (t * kTileM + r));
+              const int lo = min(max(static_cast<int>(range.x) - base, 0), HB), hi = min(max(static_cast<int>(range.y) - base, 0), HB);
+              seen = static_cast<uint32_t>((1ull << hi) - 1) & ~static_cast<uint32_t>((1ull << lo) - 1);
+              seen &= lds32(sc + U::kScMask + 4 * ((wg * HB) >> 5)) >> ((wg * HB) & 31);
+            }
+          }
           const float4* ksp = reinterpret_cast<const float4*>(smem + (sc - smem0)) + wg * (HB / 4);
           const float4* vsp = ksp + U::kScVs / 16;
           const uint32_t ts = tl + U::kS + KB * b + wg * HB;  // this thread's columns of S, and its half of P over them
@@ -611,15 +791,30 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           tmem_load(ts, x);
           tmem_loaded(x);
           if (F::kInt8) scale_by(x, ksp);
-          if (__builtin_expect(!whole, 0)) mask_by(x, lds32(sc + U::kScMask + 4 * ((wg * HB) >> 5)) >> ((wg * HB) & 31));
+          float fc = fac[0];
+          if (MASK && (a.softcap > 0.f || a.slopes != nullptr)) {
+            adjust_scores<HB>(x, fc, a.softcap, a.slopes != nullptr, sb + U::kTab + 16 * (t * kTileM + r) + 8, base);
+            fc = 1.f;  // x holds the scores, in log2 units
+          }
+          if (__builtin_expect(!whole, 0)) mask_by(x, MASK ? seen : lds32(sc + U::kScMask + 4 * ((wg * HB) >> 5)) >> ((wg * HB) & 31));
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, all[kParts];
 #pragma unroll
           for (int k = 0; k < HB; k += 2) m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], x[k], x[k + 1]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          float tm = mx == -INFINITY ? mx : mx * fac[0];
+          float tm = mx == -INFINITY ? mx : mx * fc;
           int En = E[0];
           if (F::kInt8) {
-            const int e = min(98, static_cast<int>(lds32(sc + U::kScVmax) >> 23) - 126);  // largest V scale < 2^e
+            uint32_t vmax = lds32(sc + U::kScVmax);
+            if (MASK && !whole) {  // of the keys that the row sees: the others' scales may be anything
+              vmax = 0;
+#pragma unroll
+              for (int k = 0; k < HB; ++k)
+                if ((seen >> k) & 1) vmax = max(vmax, __float_as_uint(reinterpret_cast<const float*>(vsp)[k]) & 0x7fffffffu);
+              if (!exchange(__uint_as_float(vmax), all)) break;
+#pragma unroll
+              for (int k = 0; k < kParts; ++k) vmax = max(vmax, __float_as_uint(all[k]));
+            }
+            const int e = min(98, static_cast<int>(vmax >> 23) - 126);  // largest V scale < 2^e
             if (e > En) En = e + U::kHeadroom;
           }
           // most blocks need no more than the answer that no thread's columns pass the reference by too much
@@ -646,7 +841,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
             M[0] = Mn, R[0] = Rn, E[0] = En;
           }
           // ---- p = 2^(y - R), its sum, and (times the V scale) the operand
-          const uint64_t fac2 = f2pack(fac[0], fac[0]), ref2 = f2pack(-R[0], -R[0]);
+          const uint64_t fac2 = f2pack(fc, fc), ref2 = f2pack(-R[0], -R[0]);
           uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int k = 0; k < HB; k += 2) {
@@ -656,7 +851,14 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
             x[k + 1] = fast_exp2(y1);
             sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
           }
-          if (F::kInt8) scale_by(x, vsp);  // a masked key's scale is 0
+          if (F::kInt8) {
+            scale_by(x, vsp);  // a missing key's scale is 0
+            if (MASK && !whole) {
+#pragma unroll
+              for (int k = 0; k < HB; ++k)
+                if (!((seen >> k) & 1)) x[k] = 0.f;
+            }
+          }
           uint32_t p[HB / 2];
 #pragma unroll
           for (int k = 0; k < HB; k += 2) p[k / 2] = F::kBf16 ? pack_bf162(x[k], x[k + 1]) : pack_half2(x[k], x[k + 1]);
@@ -699,13 +901,62 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         float all[kParts];
         if (!exchange(l[0], all)) break;
         const uint32_t flat = flat0 + t * CG * kTileM;
-        const bool in = flat < pairs;
+        const bool in = flat < flats;
         const uint32_t row = in ? flat / G : 0;
         const float sum = (all[0] + all[1]) + (all[2] + all[3]);
         const bool any = sum != 0.f;  // NaN too
-        const float inv = any ? 1.f / sum : 0.f;
-        const int64_t part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
-        const int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
+        float inv = any ? 1.f / sum : 0.f;
+        int64_t part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
+        int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
+        if constexpr (MASK) {
+          if (!F::kInt8) add_odd<FMT, HD, KB, CG>(a, rc, seg, h, sb + U::kOdd, sb + U::kTab + 16 * (t * kTileM + r), tl + U::kO + t * HD + d0, d0, in);
+          if (seg.part < 0) {
+            at += seg.t.row0 * a.num_q_heads;
+            if (in && wg == 0 && a.lse != nullptr) {
+              float far = 0.f;
+              if (a.slopes != nullptr && any) {
+                const RowRange x = row_range(a, seg.t.row0 + static_cast<int64_t>(row), false);
+                if (x.pos != x.near) far = -__ldg(a.slopes + h * G + (flat - row * G)) * fabsf(static_cast<float>(x.pos - x.near));
+              }
+              a.lse[at] = any ? (R[0] + log2f(sum)) * kLn2 + far : -INFINITY;
+            }
+            // the tile is the team's own: 32 rows x 32 dims at a time, rounded; four lanes write 64 B of a row
+            inv = any ? inv * a.merge_scale : 0.f;
+            const int to = in ? at : -1;
+            const uint32_t part = own_part + t * U::kQTile;
+#pragma unroll 1
+            for (int c = 0; c < HD / kParts; c += 32) {
+              float o[32];
+              tmem_load(tl + U::kO + t * HD + d0 + c, o);
+              tmem_loaded(o);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  const float* y = o + 8 * k + 4 * m;
+                  float z[4] = {y[0], F::kInt8 ? y[2] : y[1], F::kInt8 ? y[1] : y[2], y[3]};
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) z[n] = any ? z[n] * inv : 0.f;
+                  w[2 * m] = round2(a.q_f16, z[0], z[1]), w[2 * m + 1] = round2(a.q_f16, z[2], z[3]);
+                }
+                sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int rr = 8 * k + (lane >> 3) + (lane & 4);
+                const int rr_to = __shfl_sync(0xffffffffu, to, rr);
+                const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
+                if (rr_to >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(rr_to) * HD + d0 + c + 8 * (lane & 3)) = x;
+              }
+              __syncwarp();
+            }
+            continue;
+          }
+          part_at = static_cast<int64_t>(seg.part) * (NT * CG * kTileM);
+          at = static_cast<int>(flat);
+        }
         if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
         // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer
         // needs: four lanes write 64 B of a row
@@ -763,6 +1014,15 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     };
     while (ok && seg.next(a)) {
       const int B = seg.b1 - seg.b0;
+      // MASK: whether some row of the tile does not see slot e's block whole; values that are not finite are left out then
+      auto in_part = [&](int e, auto is_v, auto block_of) -> bool {
+        if constexpr (MASK) {
+          if (F::kInt8 || !is_v(e)) return false;
+          const int p = (seg.b0 + block_of(e)) * KB;
+          return p < seg.t.all_lo || p + KB > seg.t.all_hi;
+        }
+        return false;
+      };
       // what the segment's slot e holds
       auto is_v = [&](int e) -> bool { return e == 2 * B - 1 || (e > 0 && !(e & 1)); };
       auto block_of = [&](int e) -> int { return is_v(e) ? (e == 2 * B - 1 ? B - 1 : e / 2 - 1) : (e + 1) / 2; };
@@ -793,6 +1053,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         for (int e = pg; ok && e < 2 * B; e += 2) {
           const uint32_t n = base + e;
           if (!(ok = await(n))) break;
+          if (MASK && FMT == QKV_E4M3 && in_part(e, is_v, block_of)) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int u = 0; u < N; ++u) odd |= drop_odd_e4m3(raw[u]);
+            if (odd) asm volatile("red.shared::cta.or.b32 [%0], %1;\n" ::"r"(sb + U::kOdd), "r"(1u << ((seg.b0 + block_of(e)) & 31)) : "memory");
+          }
           convert_rows<FMT, N>(sb + U::kRing + (n % NS) * U::kSlotBytes, is_v(e) ? vr : kr, raw);
           hand_over(n);
           ok = load(e + 2);
@@ -806,6 +1072,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
           free_records(e);
           cp_async_commit();
           cp_async_wait<0>();
+          if (MASK && in_part(e, is_v, block_of) && VOp::template drop_odd<F::kBf16>(slot, pw, lane))
+            asm volatile("red.shared::cta.or.b32 [%0], %1;\n" ::"r"(sb + U::kOdd), "r"(1u << ((seg.b0 + block_of(e)) & 31)) : "memory");
           hand_over(n);
         }
       }
@@ -817,7 +1085,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
     uint32_t jb = 0;
     bool ok = true;
     while (ok && seg.next(a)) {
-      rc.h = seg.tile / a.umma_ptiles;
+      rc.h = seg.head(a);
+      if constexpr (MASK) rc.lo = seg.t.lo, rc.len = seg.t.hi, rc.blocks = a.block_table + static_cast<int64_t>(seg.t.hi > 0 ? seg.t.seq : 0) * a.max_blocks;
       int blk[KB / 32];
 #pragma unroll
       for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup(seg.b0 * KB + 32 * i + lane);
@@ -828,7 +1097,18 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
         for (int i = 0; i < KB / 32; ++i) {
           const int p = j * KB + 32 * i + lane;
           rec[i] = rc.record(p, blk[i]);
-          if (rec[i] < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+          if constexpr (MASK) {
+            if (rec[i] < 0 && rc.in(p) && a.dev_status != nullptr) {  // missing: flagged where a row sees it
+              bool sees = false;
+              for (int k = 0; k < seg.t.nrows && !sees; ++k) {
+                const RowRange x = row_range(a, seg.t.row0 + static_cast<int64_t>(k), false);
+                sees = p >= x.lo && p < x.hi;
+              }
+              if (sees) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+            }
+          } else {
+            if (rec[i] < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+          }
           blk[i] = j + 1 < seg.b1 ? rc.lookup(p + KB) : -1;  // the next block's, a block ahead of its use
         }
         if (jb >= kRecRing) {
@@ -972,10 +1252,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG>::kThreads, 1) prefix_umm
   if (tid == 0 && lds32(flag) != 0u && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_TIMEOUT);
 }
 
-template <int FMT, int HD, int NT, int CG>
+template <int FMT, int HD, int NT, int CG, bool MASK>
 cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
-  using U = Umma<FMT, HD, NT, CG>;
-  auto kern = prefix_umma_kernel<FMT, HD, NT, CG>;
+  using U = Umma<FMT, HD, NT, CG, MASK>;
+  auto kern = prefix_umma_kernel<FMT, HD, NT, CG, MASK>;
   static std::atomic<bool> done[64] = {};
   cudaError_t e = allow_smem(kern, U::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -984,17 +1264,25 @@ cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(U::kThreads);
   cfg.dynamicSmemBytes = U::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
   cfg.attrs = at;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.numAttrs = 0;
+  if (CG > 1) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  if (MASK) {  // starts while the work list is made
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int FMT>
+template <int FMT, bool MASK = false>
 cudaError_t launch_umma(PrefixArgs a, cudaStream_t stream) {
   // Test of the lost-wait path: QKV_TEST_PREFIX_DROP_HANDOFF=<block> makes the records' warp leave out the hand-off of
   // that block in each CTA (read at each launch; unset in any other use).
@@ -1003,9 +1291,9 @@ cudaError_t launch_umma(PrefixArgs a, cudaStream_t stream) {
     const long n = std::strtol(t, &end, 10);
     if (end != t && n >= 0 && n < (1 << 30)) a.umma_drop = static_cast<uint32_t>(n);
   }
-  if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2>(a, stream) : launch_umma<FMT, 256, 1, 1>(a, stream);
-  if (a.umma_cg == 2) return launch_umma<FMT, 128, 2, 2>(a, stream);
-  return launch_umma<FMT, 128, 1, 1>(a, stream);
+  if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2, MASK>(a, stream) : launch_umma<FMT, 256, 1, 1, MASK>(a, stream);
+  if (a.umma_cg == 2) return launch_umma<FMT, 128, 2, 2, MASK>(a, stream);
+  return launch_umma<FMT, 128, 1, 1, MASK>(a, stream);
 }
 
 }  // namespace prefix

@@ -233,26 +233,39 @@ struct PrefixArgs {
   int window = 0;                      // 0: none
   float softcap = 0.f;                 // 0: none
   const float* slopes = nullptr;       // [Hq], null: no bias
+  // its tcgen05 tiles: the work list, the rows of a tile and the keys of a block
+  void* plan = nullptr;
+  int tile_rows = 0;
+  int block_keys = 0;
 };
 // the mma.sync tiles of (row, head) pairs over prefix_items ranges of the prefix and own_items of the
 // keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
 cudaError_t launch_prefix_mma_bf16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_masked_mma_bf16(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_umma_bf16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_bf16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_f16(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_masked_mma_f16(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_umma_f16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_f16(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_int8_side(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_masked_mma_int8_side(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_umma_int8_side(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_int8_side(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_int8_inline(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_masked_mma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_umma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_int8_inline(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_mma_e4m3(const PrefixArgs& a, bool overlaps, cudaStream_t stream);
 cudaError_t launch_masked_mma_e4m3(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_masked_merge(const PrefixArgs& a, cudaStream_t stream);
+// the work list of the tcgen05 tiles, and the join of the tiles that teams share
+size_t masked_plan_bytes(int64_t rows);
+cudaError_t launch_masked_plan(const PrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_masked_join(const PrefixArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device helpers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
