@@ -899,7 +899,7 @@ namespace {
 struct MaskedPlan {
   int64_t tiles;  // mma.sync tiles
   int parts;      // ranges of their keys
-  int umma_cg, umma_pairs, tile_rows, block_keys;
+  int umma_cg, umma_pairs, tile_rows, block_keys, tile_cost;
   uint32_t umma_teams;
   int64_t rows, rows_heads;
   int head_dim;
@@ -907,8 +907,8 @@ struct MaskedPlan {
   // itself; a team of SMs leaves at most two partial tiles.
   int64_t part_rows() const { return umma_cg > 0 ? 2 * static_cast<int64_t>(umma_teams) * umma_pairs : parts > 1 ? parts * rows_heads : 0; }
   size_t o_bytes() const { return static_cast<size_t>(part_rows()) * head_dim * 4; }
-  size_t list_at() const { return o_bytes() + (static_cast<size_t>(part_rows()) * 4 + 15) / 16 * 16; }
-  size_t bytes() const { return list_at() + (umma_cg > 0 ? qkv::masked_plan_bytes(rows) : 0); }
+  size_t list_at() const { return o_bytes() + (static_cast<size_t>(part_rows()) * 4 + 31) / 32 * 32; }
+  size_t bytes() const { return list_at() + (umma_cg > 0 ? qkv::masked_plan_bytes(rows, tile_rows) : 0); }
 };
 
 qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
@@ -919,6 +919,8 @@ qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, in
 
 // Pairs of a sequence, on average, from which a masked call runs on tcgen05 tiles.
 constexpr int64_t kMaskedUmmaPairs = 64;
+// What a tile costs besides its key blocks, in blocks.
+constexpr int kMaskedTileCost = 6;
 
 qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                        int max_row_end, int window, MaskedPlan* p) {
@@ -932,16 +934,17 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   const int64_t keys = window > 0 && window < max_row_end - 16 ? window + 16 : max_row_end;
   p->parts = key_parts(p->tiles, static_cast<int>(keys > 0 ? keys : 1), row_bytes_of(fmt, head_dim), sms);
   p->rows = rows;
-  p->umma_cg = 0, p->umma_pairs = 0, p->tile_rows = 0, p->block_keys = 0, p->umma_teams = 0;
+  p->umma_cg = 0, p->umma_pairs = 0, p->tile_rows = 0, p->block_keys = 0, p->tile_cost = 0, p->umma_teams = 0;
   const int64_t pairs = rows * G / num_seqs;  // of a sequence
   if (pairs >= kMaskedUmmaPairs && max_row_end <= (1 << 27)) {
-    p->umma_cg = pairs > (head_dim == 128 ? 256 : 128) ? 2 : 1;
-    p->umma_pairs = p->umma_cg == 1 ? 128 : head_dim == 128 ? 512 : 256;
+    p->umma_cg = pairs > 128 ? 2 : 1;
+    p->umma_pairs = 128 * p->umma_cg;
     p->tile_rows = p->umma_pairs / G;
     p->block_keys = head_dim == 256 && p->umma_cg == 1 ? 64 : 128;
     p->umma_teams = static_cast<uint32_t>(sms / p->umma_cg);
-    // a team's share is counted in 32 bits, however the rows are cut into tiles
-    const int64_t blocks = max_row_end / p->block_keys + 2;
+    p->tile_cost = kMaskedTileCost;
+    // a team's share is counted in 32 bits, however the rows are cut into tiles, and a chunk's work is
+    const int64_t blocks = max_row_end / p->block_keys + 2 + p->tile_cost;
     if (rows > (int64_t(1) << 31) / blocks / num_kv_heads * p->umma_teams) p->umma_cg = 0;
   }
   if (p->umma_cg == 0 && p->tiles * p->parts > INT32_MAX) return QKV_ERR_ARG;
@@ -1063,6 +1066,9 @@ qkv_status qkv_masked_attn(const qkv_masked_desc* d, void* stream) {
     a.umma_teams = p.umma_teams;
     a.tile_rows = p.tile_rows;
     a.block_keys = p.block_keys;
+    a.tile_cost = p.tile_cost;
+    a.plan_tiles_at = static_cast<int64_t>(qkv::masked_plan_tiles_at(d->rows, p.tile_rows));
+    a.plan_chunks = qkv::masked_plan_chunks(d->rows, p.tile_rows);
     e = qkv::launch_masked_plan(a, s);
     if (e == cudaSuccess) e = launch_masked_umma(a, d->fmt, s);
     if (e == cudaSuccess) e = qkv::launch_masked_join(a, s);

@@ -5,7 +5,7 @@ namespace qkv {
 namespace prefix {
 namespace {
 
-constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Inclusive sum over the block's threads; `total` is the last one's.
 __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* sums, uint32_t& total) {
@@ -33,70 +33,65 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* sums, uint32_t& t
   return x;
 }
 
-// One block; a thread per row, as many whole groups of tile_rows rows at a time as it has threads.
+// A chunk of rows per block, a thread per row.
 __global__ void __launch_bounds__(kPlanThreads) masked_plan_kernel(const PrefixArgs a) {
   __shared__ int sSeq[kPlanThreads], sLo[kPlanThreads], sHi[kPlanThreads];
   __shared__ int tLo[kPlanThreads], tHi[kPlanThreads], tAllLo[kPlanThreads], tAllHi[kPlanThreads], tRow[kPlanThreads], tRows[kPlanThreads];
   __shared__ uint32_t sums[kPlanWarps];
   let_next_start();
-  const int tid = threadIdx.x, T = a.tile_rows, KB = a.block_keys, step = kPlanThreads / T * T;
-  MaskedHead* head = static_cast<MaskedHead*>(a.plan);
-  MaskedTile* tiles = reinterpret_cast<MaskedTile*>(head + 1);
-  uint64_t units = 0;
-  uint32_t count = 0;
-  for (int64_t r0 = 0; r0 < a.rows; r0 += step) {
-    const int64_t row = r0 + tid;
-    const bool there = tid < step && row < a.rows;
-    RowRange x = {kPadRow, 0, 0, 0, 0};
-    int seq = -1;
-    if (there) x = row_range(a, row, true), seq = __ldg(a.row_seq + row);
-    const bool live = x.state != kPadRow, sees = x.lo < x.hi;
-    sSeq[tid] = live ? seq : -1, sLo[tid] = x.lo, sHi[tid] = x.hi;
-    tLo[tid] = INT_MAX, tHi[tid] = 0, tAllLo[tid] = 0, tAllHi[tid] = INT_MAX, tRows[tid] = 0;
-    __syncthreads();
-    bool first = live;
-    if (live && tid % T != 0) {
-      const int lo = sLo[tid - 1], hi = sHi[tid - 1];
-      const bool apart = sees && lo < hi && max(lo, x.lo) > min(hi, x.hi);
-      first = sSeq[tid - 1] != seq || apart;  // a padding row before: another sequence (-1)
-    }
-    uint32_t n;
-    const uint32_t i = scan(first ? 1 : 0, sums, n) - 1;  // the row's tile of these
-    // a tile's rows of the warp to the first of them, and from there into the tile
-    const int tile = live ? static_cast<int>(i) : -1, lane = tid & 31;
-    int rows = 1, lo = sees ? x.lo : INT_MAX, hi = x.hi, all_lo = x.lo, all_hi = sees ? x.hi : INT_MAX;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o_tile = __shfl_down_sync(0xffffffffu, tile, off), o_rows = __shfl_down_sync(0xffffffffu, rows, off);
-      const int o_lo = __shfl_down_sync(0xffffffffu, lo, off), o_hi = __shfl_down_sync(0xffffffffu, hi, off);
-      const int o_all_lo = __shfl_down_sync(0xffffffffu, all_lo, off), o_all_hi = __shfl_down_sync(0xffffffffu, all_hi, off);
-      if (lane + off < 32 && o_tile == tile) {
-        rows += o_rows, lo = min(lo, o_lo), hi = max(hi, o_hi), all_lo = max(all_lo, o_all_lo), all_hi = min(all_hi, o_all_hi);
-      }
-    }
-    const int before = __shfl_up_sync(0xffffffffu, tile, 1);
-    if (live && first) tRow[i] = static_cast<int>(row);
-    if (live && (lane == 0 || before != tile)) {
-      atomicAdd(tRows + i, rows);
-      atomicMin(tLo + i, lo), atomicMax(tHi + i, hi);
-      atomicMax(tAllLo + i, all_lo), atomicMin(tAllHi + i, all_hi);
-    }
-    __syncthreads();
-    MaskedTile t = {};
-    uint32_t blocks = 0, sum;
-    if (tid < n) {
-      t.row0 = tRow[tid], t.nrows = tRows[tid], t.seq = sSeq[t.row0 - r0];
-      if (tHi[tid] > 0) t.lo = tLo[tid], t.hi = tHi[tid], t.all_lo = tAllLo[tid], t.all_hi = tAllHi[tid];
-      blocks = max(1, (t.hi + KB - 1) / KB - t.lo / KB);  // rows that see nothing have a block without keys
-    }
-    t.first = units + scan(blocks, sums, sum) - blocks;  // the host keeps 1024 tiles' blocks below 2^32
-    if (tid < n) tiles[count + tid] = t;
-    count += n;
-    units += sum;
+  const int tid = threadIdx.x, T = a.tile_rows, KB = a.block_keys, step = static_cast<int>(plan_chunk_rows(T));
+  MaskedChunk* chunk = static_cast<MaskedChunk*>(a.plan) + blockIdx.x;
+  MaskedTile* tiles = const_cast<MaskedTile*>(plan_tiles(a, static_cast<int>(blockIdx.x)));
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * step, row = r0 + tid;
+  const bool there = tid < step && row < a.rows;
+  RowRange x = {kPadRow, 0, 0, 0, 0};
+  int seq = -1;
+  if (there) x = row_range(a, row, true), seq = __ldg(a.row_seq + row);
+  const bool live = x.state != kPadRow, sees = x.lo < x.hi;
+  sSeq[tid] = live ? seq : -1, sLo[tid] = x.lo, sHi[tid] = x.hi;
+  tLo[tid] = INT_MAX, tHi[tid] = 0, tAllLo[tid] = 0, tAllHi[tid] = INT_MAX, tRows[tid] = 0;
+  __syncthreads();
+  bool first = live;
+  if (live && tid % T != 0) {
+    const int lo = sLo[tid - 1], hi = sHi[tid - 1];
+    const bool apart = sees && lo < hi && max(lo, x.lo) > min(hi, x.hi);
+    first = sSeq[tid - 1] != seq || apart;  // a padding row before: another sequence (-1)
   }
+  uint32_t n;
+  const uint32_t i = scan(first ? 1 : 0, sums, n) - 1;  // the row's tile of these
+  // a tile's rows of the warp to the first of them, and from there into the tile
+  const int tile = live ? static_cast<int>(i) : -1, lane = tid & 31;
+  int rows = 1, lo = sees ? x.lo : INT_MAX, hi = x.hi, all_lo = x.lo, all_hi = sees ? x.hi : INT_MAX;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o_tile = __shfl_down_sync(0xffffffffu, tile, off), o_rows = __shfl_down_sync(0xffffffffu, rows, off);
+    const int o_lo = __shfl_down_sync(0xffffffffu, lo, off), o_hi = __shfl_down_sync(0xffffffffu, hi, off);
+    const int o_all_lo = __shfl_down_sync(0xffffffffu, all_lo, off), o_all_hi = __shfl_down_sync(0xffffffffu, all_hi, off);
+    if (lane + off < 32 && o_tile == tile) {
+      rows += o_rows, lo = min(lo, o_lo), hi = max(hi, o_hi), all_lo = max(all_lo, o_all_lo), all_hi = min(all_hi, o_all_hi);
+    }
+  }
+  const int before = __shfl_up_sync(0xffffffffu, tile, 1);
+  if (live && first) tRow[i] = static_cast<int>(row);
+  if (live && (lane == 0 || before != tile)) {
+    atomicAdd(tRows + i, rows);
+    atomicMin(tLo + i, lo), atomicMax(tHi + i, hi);
+    atomicMax(tAllLo + i, all_lo), atomicMin(tAllHi + i, all_hi);
+  }
+  __syncthreads();
+  MaskedTile t = {};
+  uint32_t cost = 0, sum;
+  if (tid < n) {
+    t.row0 = tRow[tid], t.nrows = tRows[tid], t.seq = sSeq[t.row0 - r0];
+    if (tHi[tid] > 0) t.lo = tLo[tid], t.hi = tHi[tid], t.all_lo = tAllLo[tid], t.all_hi = tAllHi[tid];
+    // rows that see nothing have a block without keys
+    cost = a.tile_cost + max(1, (t.hi + KB - 1) / KB - t.lo / KB);
+  }
+  t.first = scan(cost, sums, sum) - cost;  // the host keeps a chunk's work below 2^32
+  if (tid < n) tiles[tid] = t;
   if (tid == 0) {
-    tiles[count].first = units;
-    head->units = units, head->tiles = count;
+    tiles[n].first = sum;
+    chunk->work = sum, chunk->tiles = n;
   }
 }
 
@@ -107,23 +102,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) masked_join_kernel(const Pref
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   await_previous();
   // the tile that team blockIdx.x begins and does not finish
-  const MaskedHead head = *plan_head(a);
-  const MaskedTile* tiles = plan_tiles(a);
-  const Shares s(head.units * a.num_kv_heads, a.umma_teams);
+  const uint64_t work = plan_work(a);
+  const Shares s(work * a.num_kv_heads, a.umma_teams);
   const uint32_t team = blockIdx.x;
   const uint64_t from = s.first(team), end = from + s.of(team);
-  if (end == from || end == head.units * a.num_kv_heads) return;
-  const int h = static_cast<int>((end - 1) / head.units);
-  const uint64_t h0 = h * head.units, rem = end - 1 - h0;
-  int lo = 0, hi = static_cast<int>(head.tiles);
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tiles[mid].first <= rem) lo = mid;
-    else hi = mid;
-  }
-  const MaskedTile t = tiles[lo];
-  const uint64_t begin = h0 + t.first, stop = h0 + tiles[lo + 1].first;
-  if (begin < from || stop <= end) return;  // begun by a team before, or finished
+  if (end == from || end == work * a.num_kv_heads) return;
+  const int h = static_cast<int>((end - 1) / work);
+  const PlanPlace p = plan_find(a, end - 1 - h * work);
+  const MaskedTile t = plan_tiles(a, p.chunk)[p.tile];
+  const uint64_t begin = h * work + p.before + t.first, stop = h * work + p.before + plan_tiles(a, p.chunk)[p.tile + 1].first;
+  // its first block is another team's, or it is finished
+  if (begin + a.tile_cost < from || begin + a.tile_cost >= end || stop <= end) return;
   uint32_t parts = 1;
   for (uint64_t u = end; u < stop; ++parts) u += s.of(team + parts);
   const int G = a.num_q_heads / a.num_kv_heads;
@@ -195,11 +184,16 @@ cudaError_t launch_join(const PrefixArgs& a, cudaStream_t stream) {
 }  // namespace
 }  // namespace prefix
 
-size_t masked_plan_bytes(int64_t rows) {
-  return sizeof(prefix::MaskedHead) + static_cast<size_t>(rows + 1) * sizeof(prefix::MaskedTile);
+size_t masked_plan_tiles_at(int64_t rows, int tile_rows) {
+  return (static_cast<size_t>(prefix::plan_chunks(rows, tile_rows)) * sizeof(prefix::MaskedChunk) + 31) / 32 * 32;
 }
+size_t masked_plan_bytes(int64_t rows, int tile_rows) {
+  return masked_plan_tiles_at(rows, tile_rows) +
+         static_cast<size_t>(prefix::plan_chunks(rows, tile_rows)) * (prefix::kPlanThreads + 1) * sizeof(prefix::MaskedTile);
+}
+int masked_plan_chunks(int64_t rows, int tile_rows) { return static_cast<int>(prefix::plan_chunks(rows, tile_rows)); }
 cudaError_t launch_masked_plan(const PrefixArgs& a, cudaStream_t stream) {
-  prefix::masked_plan_kernel<<<1, prefix::kPlanThreads, 0, stream>>>(a);
+  prefix::masked_plan_kernel<<<static_cast<unsigned>(a.plan_chunks), prefix::kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_masked_join(const PrefixArgs& a, cudaStream_t stream) {

@@ -310,6 +310,10 @@ struct Records {
   int bsz, shift, len, H, h, lo = 0;
   bool pow2;
   __device__ __forceinline__ bool in(int p) const { return p < len && (!MASK || p >= lo); }
+  __device__ __forceinline__ void of_tile(const PrefixArgs& a, const MaskedTile& t) {
+    lo = t.lo, len = t.hi;
+    blocks = a.block_table + static_cast<int64_t>(t.hi > 0 ? t.seq : 0) * a.max_blocks;  // no keys: no sequence either
+  }
   __device__ __forceinline__ int block_of(int p) const { return pow2 ? p >> shift : p / bsz; }
   // block id of position p, -1 past the prefix
   __device__ __forceinline__ int lookup(int p) const { return in(p) ? __ldg(blocks + block_of(p)) : -1; }
@@ -475,34 +479,40 @@ __device__ __forceinline__ void adjust_scores(float (&x)[N], float fac, float ca
   }
 }
 
+// Record of both SMs (each has half of the dims, and all rows) that block j holds values that were left out. It is there
+// before the block's hand-over, which the product and its readers wait for.
+template <int CG>
+__device__ __forceinline__ void note_odd(uint32_t odd, int j) {
+#pragma unroll
+  for (int i = 0; i < CG; ++i)
+    asm volatile("{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n red.relaxed.cluster.shared::cluster.or.b32 [ra], %2;\n}\n" ::"r"(odd), "r"(i),
+                 "r"(1u << (j & 31))
+                 : "memory");
+  asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+}
+
 // The values that are not finite which the producers of a masked segment left out of blocks that some rows do not see whole,
-// added to the thread's part of O (HD / kParts dims from d0 on) where its row sees their keys. `odd` addresses the SM's
-// record of such blocks; a pair's second SM has its own, since each converts half of the dims. Nearly always there are none.
-template <int FMT, int HD, int KB, int CG, typename REC, typename SEG>
+// added to the thread's part of O (HD / kParts dims from d0 on) where its row sees their keys. `odd` addresses the record of
+// such blocks. Nearly always there are none.
+template <int FMT, int HD, int KB, typename REC, typename SEG>
 __device__ __forceinline__ void add_odd(const PrefixArgs& a, REC rc, const SEG& seg, int h, uint32_t odd, uint32_t range, uint32_t to,
                                         int d0, bool in) {
   using F = Fmt<FMT>;
-  uint32_t bits = 0;
-  asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < CG; ++i) {
-    uint32_t x;
-    asm volatile("{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %1, %2;\n ld.volatile.shared::cluster.u32 %0, [ra];\n}\n" : "=r"(x) : "r"(odd), "r"(i));
-    bits |= x;
-  }
+  const uint32_t bits = lds32(odd);
   if (__builtin_expect(!__any_sync(0xffffffffu, bits != 0u), 1)) return;
   const uint2 lim = lds64(range);
   const int lo = static_cast<int>(lim.x), hi = in ? static_cast<int>(lim.y) : 0;
-  rc.h = h, rc.lo = seg.t.lo, rc.len = seg.t.hi;
-  rc.blocks = a.block_table + static_cast<int64_t>(seg.t.hi > 0 ? seg.t.seq : 0) * a.max_blocks;
+  const MaskedTile tile = seg.tile(a);
+  rc.h = h;
+  rc.of_tile(a, tile);
   for (int j = seg.b0; j < seg.b1; ++j) {
     const int p0 = j * KB;
-    if (!((bits >> (j & 31)) & 1) || (p0 >= seg.t.all_lo && p0 + KB <= seg.t.all_hi)) continue;
+    if (!((bits >> (j & 31)) & 1) || (p0 >= tile.all_lo && p0 + KB <= tile.all_hi)) continue;
     for (int c = 0; c < HD / kParts; c += 16) {
       float o[16];
       tmem_load(to + c, o);
       tmem_loaded(o);
-      for (int p = max(p0, seg.t.lo); p < min(p0 + KB, seg.t.hi); ++p) {
+      for (int p = max(p0, tile.lo); p < min(p0 + KB, tile.hi); ++p) {
         const int rec = rc.record(p, rc.lookup(p));
         if (rec < 0 || p < lo || p >= hi) continue;
 #pragma unroll
@@ -544,7 +554,7 @@ struct Segments<true, KB> : MaskedSegment<KB> {
     MaskedSegment<KB>::begin(a, team);
   }
   __device__ __forceinline__ bool next(const PrefixArgs& a) { return MaskedSegment<KB>::next(a, team); }
-  __device__ __forceinline__ int head(const PrefixArgs&) const { return this->h_now; }
+  __device__ __forceinline__ int head(const PrefixArgs&) const { return MaskedSegment<KB>::head; }
 };
 
 // MASK: qkv_masked_attn, with the work list of masked_tiles.cuh. What differs: the tile's keys lie in its sequence's row
@@ -649,15 +659,16 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       uint32_t flat0, flats = pairs;  // the thread's pair in tile 0, and how many there are (MASK: of the tile's rows)
       const uint16_t* q0 = a.q;
       if constexpr (MASK) {
-        flat0 = rank * kTileM + r, flats = static_cast<uint32_t>(seg.t.nrows * G);
-        q0 += seg.t.row0 * a.q_stride;
+        flat0 = rank * kTileM + r, flats = static_cast<uint32_t>(seg.tile(a).nrows * G);
+        const int64_t row0 = seg.tile(a).row0;
+        q0 += row0 * a.q_stride;
         // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see
 #pragma unroll 1
         for (int t = 0; t < NT; ++t) {
           const uint32_t flat = flat0 + t * CG * kTileM;
           RowRange x = {kPadRow, 0, 0, 0, 0};
           const uint32_t row = flat / G;
-          if (flat < flats) x = row_range(a, seg.t.row0 + static_cast<int64_t>(row), false);
+          if (flat < flats) x = row_range(a, row0 + row, false);
           const float slope = flat < flats && a.slopes != nullptr ? __ldg(a.slopes + h * G + (flat - row * G)) : 0.f;
           if (wg == 0)
             sts128(sb + U::kTab + 16 * (t * kTileM + r), make_uint4(x.lo, x.hi, x.near, __float_as_uint(-slope * kLog2e)));
@@ -894,6 +905,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       }
       jb += seg.b1 - seg.b0;
       // ---- the segment's partial results
+      int row0 = 0;
+      if constexpr (MASK) row0 = seg.tile(a).row0, flats = static_cast<uint32_t>(seg.tile(a).nrows * G);
 #pragma unroll 1
       for (int t = 0; t < NT; ++t, other_tile()) {
         ok = ok && await_pv((jb - 1) * NT + t);
@@ -909,46 +922,38 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
         int64_t part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
         int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
         if constexpr (MASK) {
-          if (!F::kInt8) add_odd<FMT, HD, KB, CG>(a, rc, seg, h, sb + U::kOdd, sb + U::kTab + 16 * (t * kTileM + r), tl + U::kO + t * HD + d0, d0, in);
+          if (!F::kInt8) add_odd<FMT, HD, KB>(a, rc, seg, h, sb + U::kOdd, sb + U::kTab + 16 * (t * kTileM + r), tl + U::kO + t * HD + d0, d0, in);
           if (seg.part < 0) {
-            at += seg.t.row0 * a.num_q_heads;
+            at += row0 * a.num_q_heads;
             if (in && wg == 0 && a.lse != nullptr) {
               float far = 0.f;
               if (a.slopes != nullptr && any) {
-                const RowRange x = row_range(a, seg.t.row0 + static_cast<int64_t>(row), false);
+                const RowRange x = row_range(a, row0 + static_cast<int64_t>(row), false);
                 if (x.pos != x.near) far = -__ldg(a.slopes + h * G + (flat - row * G)) * fabsf(static_cast<float>(x.pos - x.near));
               }
               a.lse[at] = any ? (R[0] + log2f(sum)) * kLn2 + far : -INFINITY;
             }
-            // the tile is the team's own: 32 rows x 32 dims at a time, rounded; four lanes write 64 B of a row
+            // the tile is the team's own: 32 dims at a time, rounded, straight from the thread's registers
             inv = any ? inv * a.merge_scale : 0.f;
-            const int to = in ? at : -1;
-            const uint32_t part = own_part + t * U::kQTile;
+            uint16_t* to = a.out + static_cast<int64_t>(at) * HD + d0;
 #pragma unroll 1
             for (int c = 0; c < HD / kParts; c += 32) {
               float o[32];
               tmem_load(tl + U::kO + t * HD + d0 + c, o);
               tmem_loaded(o);
+              uint32_t w[16];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t w[4];
+              for (int k = 0; k < 8; ++k) {
+                // int8: the producers store dims 0, 2, 1, 3 of each four
+                float z[4] = {o[4 * k], F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], F::kInt8 ? o[4 * k + 1] : o[4 * k + 2], o[4 * k + 3]};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  const float* y = o + 8 * k + 4 * m;
-                  float z[4] = {y[0], F::kInt8 ? y[2] : y[1], F::kInt8 ? y[1] : y[2], y[3]};
-#pragma unroll
-                  for (int n = 0; n < 4; ++n) z[n] = any ? z[n] * inv : 0.f;
-                  w[2 * m] = round2(a.q_f16, z[0], z[1]), w[2 * m + 1] = round2(a.q_f16, z[2], z[3]);
-                }
-                sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                for (int n = 0; n < 4; ++n) z[n] = any ? z[n] * inv : 0.f;
+                w[2 * k] = round2(a.q_f16, z[0], z[1]), w[2 * k + 1] = round2(a.q_f16, z[2], z[3]);
               }
-              __syncwarp();
+              if (in) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int rr = 8 * k + (lane >> 3) + (lane & 4);
-                const int rr_to = __shfl_sync(0xffffffffu, to, rr);
-                const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
-                if (rr_to >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(rr_to) * HD + d0 + c + 8 * (lane & 3)) = x;
+                for (int k = 0; k < 4; ++k)
+                  *reinterpret_cast<uint4*>(to + c + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
               }
               __syncwarp();
             }
@@ -1014,12 +1019,14 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
     };
     while (ok && seg.next(a)) {
       const int B = seg.b1 - seg.b0;
+      int all_lo = 0, all_hi = 0;
+      if constexpr (MASK) all_lo = seg.tile(a).all_lo, all_hi = seg.tile(a).all_hi;
       // MASK: whether some row of the tile does not see slot e's block whole; values that are not finite are left out then
       auto in_part = [&](int e, auto is_v, auto block_of) -> bool {
         if constexpr (MASK) {
           if (F::kInt8 || !is_v(e)) return false;
           const int p = (seg.b0 + block_of(e)) * KB;
-          return p < seg.t.all_lo || p + KB > seg.t.all_hi;
+          return p < all_lo || p + KB > all_hi;
         }
         return false;
       };
@@ -1057,7 +1064,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
             uint32_t odd = 0;
 #pragma unroll
             for (int u = 0; u < N; ++u) odd |= drop_odd_e4m3(raw[u]);
-            if (odd) asm volatile("red.shared::cta.or.b32 [%0], %1;\n" ::"r"(sb + U::kOdd), "r"(1u << ((seg.b0 + block_of(e)) & 31)) : "memory");
+            if (odd) note_odd<CG>(sb + U::kOdd, seg.b0 + block_of(e));
           }
           convert_rows<FMT, N>(sb + U::kRing + (n % NS) * U::kSlotBytes, is_v(e) ? vr : kr, raw);
           hand_over(n);
@@ -1073,7 +1080,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           cp_async_commit();
           cp_async_wait<0>();
           if (MASK && in_part(e, is_v, block_of) && VOp::template drop_odd<F::kBf16>(slot, pw, lane))
-            asm volatile("red.shared::cta.or.b32 [%0], %1;\n" ::"r"(sb + U::kOdd), "r"(1u << ((seg.b0 + block_of(e)) & 31)) : "memory");
+            note_odd<CG>(sb + U::kOdd, seg.b0 + block_of(e));
           hand_over(n);
         }
       }
@@ -1086,7 +1093,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
     bool ok = true;
     while (ok && seg.next(a)) {
       rc.h = seg.head(a);
-      if constexpr (MASK) rc.lo = seg.t.lo, rc.len = seg.t.hi, rc.blocks = a.block_table + static_cast<int64_t>(seg.t.hi > 0 ? seg.t.seq : 0) * a.max_blocks;
+      if constexpr (MASK) rc.of_tile(a, seg.tile(a));
       int blk[KB / 32];
 #pragma unroll
       for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup(seg.b0 * KB + 32 * i + lane);
@@ -1100,8 +1107,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           if constexpr (MASK) {
             if (rec[i] < 0 && rc.in(p) && a.dev_status != nullptr) {  // missing: flagged where a row sees it
               bool sees = false;
-              for (int k = 0; k < seg.t.nrows && !sees; ++k) {
-                const RowRange x = row_range(a, seg.t.row0 + static_cast<int64_t>(k), false);
+              for (int k = 0; k < seg.tile(a).nrows && !sees; ++k) {
+                const RowRange x = row_range(a, seg.tile(a).row0 + static_cast<int64_t>(k), false);
                 sees = p >= x.lo && p < x.hi;
               }
               if (sees) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
@@ -1292,7 +1299,7 @@ cudaError_t launch_umma(PrefixArgs a, cudaStream_t stream) {
     if (end != t && n >= 0 && n < (1 << 30)) a.umma_drop = static_cast<uint32_t>(n);
   }
   if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2, MASK>(a, stream) : launch_umma<FMT, 256, 1, 1, MASK>(a, stream);
-  if (a.umma_cg == 2) return launch_umma<FMT, 128, 2, 2, MASK>(a, stream);
+  if (a.umma_cg == 2) return launch_umma<FMT, 128, MASK ? 1 : 2, 2, MASK>(a, stream);
   return launch_umma<FMT, 128, 1, 1, MASK>(a, stream);
 }
 

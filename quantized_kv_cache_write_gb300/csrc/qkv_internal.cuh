@@ -233,10 +233,14 @@ struct PrefixArgs {
   int window = 0;                      // 0: none
   float softcap = 0.f;                 // 0: none
   const float* slopes = nullptr;       // [Hq], null: no bias
-  // its tcgen05 tiles: the work list, the rows of a tile and the keys of a block
+  // its tcgen05 tiles: the work list, its chunks and where its tiles begin; the rows of a tile, the keys of a block, and what
+  // a tile costs besides its blocks, in blocks
   void* plan = nullptr;
+  int64_t plan_tiles_at = 0;
+  int plan_chunks = 0;
   int tile_rows = 0;
   int block_keys = 0;
+  int tile_cost = 0;
 };
 // the mma.sync tiles of (row, head) pairs over prefix_items ranges of the prefix and own_items of the
 // keys behind it (overlaps: the call's previous kernel may still run); the tcgen05 tiles over the prefix
@@ -263,7 +267,9 @@ cudaError_t launch_prefix_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_masked_merge(const PrefixArgs& a, cudaStream_t stream);
 // the work list of the tcgen05 tiles, and the join of the tiles that teams share
-size_t masked_plan_bytes(int64_t rows);
+size_t masked_plan_bytes(int64_t rows, int tile_rows);
+size_t masked_plan_tiles_at(int64_t rows, int tile_rows);
+int masked_plan_chunks(int64_t rows, int tile_rows);
 cudaError_t launch_masked_plan(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_masked_join(const PrefixArgs& a, cudaStream_t stream);
 
