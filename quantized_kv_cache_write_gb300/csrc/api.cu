@@ -936,7 +936,7 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   p->rows = rows;
   p->umma_cg = 0, p->umma_pairs = 0, p->tile_rows = 0, p->block_keys = 0, p->tile_cost = 0, p->umma_teams = 0;
   const int64_t pairs = rows * G / num_seqs;  // of a sequence
-  if (pairs >= kMaskedUmmaPairs && max_row_end <= (1 << 27)) {
+  if (pairs >= kMaskedUmmaPairs && max_row_end <= (1 << 27) && num_kv_heads <= 0xffff) {
     p->umma_cg = pairs > 128 ? 2 : 1;
     p->umma_pairs = 128 * p->umma_cg;
     p->tile_rows = p->umma_pairs / G;

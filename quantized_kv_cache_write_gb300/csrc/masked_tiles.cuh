@@ -94,49 +94,71 @@ __device__ __forceinline__ PlanPlace plan_find(const PrefixArgs& a, uint64_t rem
   return p;
 }
 
-// A team's next segment: its part of the blocks of one tile of one KV head. Blocks are numbered from position 0. The tile's
-// entry is read where it is needed: it stays in L1, and its fields would cost the roles registers through their loops.
+// A team's next segment: its part of the blocks of one tile of one KV head. Blocks are numbered from position 0. What the
+// roles' loops do not need sits in shared memory, a copy of its own for each warp (kSegWords words at `at`), and the
+// tile's entry is read where it is needed, from L1: in registers they cost the softmax its columns.
+constexpr int kSegWords = 8;
 template <int KB>
 struct MaskedSegment {
-  uint32_t left;         // work still to do
-  uint32_t skip;         // work of the next tile that a team before has
-  int chunk, i, h;       // the next tile and its KV head
-  int now_chunk, now_i;  // the segment's tile
-  int head;              // and KV head
-  int b0, b1, part;
-  __device__ __forceinline__ const MaskedTile& tile(const PrefixArgs& a) const { return plan_tiles(a, now_chunk)[now_i]; }
-  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t team) {
+  uint32_t at;
+  int b0, b1;
+  // words: work still to do; work of the next tile that a team before has; the next tile's chunk, number and KV head;
+  // this one's chunk and number; its KV head and part (-1: whole) in one
+  __device__ __forceinline__ uint32_t word(int i) const { return lds32(at + 4 * i); }
+  __device__ __forceinline__ const MaskedTile& tile(const PrefixArgs& a) const {
+    return plan_tiles(a, static_cast<int>(word(5)))[word(6)];
+  }
+  __device__ __forceinline__ int head() const { return static_cast<int>(word(7) >> 16); }
+  __device__ __forceinline__ int part() const { return static_cast<int>(word(7) & 0xffffu) - 1; }
+  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t team, uint32_t words) {
+    at = words;
     const uint64_t work = plan_work(a);
     const Shares s(work * a.num_kv_heads, a.umma_teams);
-    left = static_cast<uint32_t>(s.of(team));  // the host keeps a share below 2^32
-    skip = 0, chunk = 0, i = 0, h = 0;
-    if (left == 0) return;
-    const uint64_t u = s.first(team);
-    h = static_cast<int>(u / work);
-    const PlanPlace p = plan_find(a, u - h * work);
-    chunk = p.chunk, i = p.tile, skip = p.into;
+    const uint32_t left = static_cast<uint32_t>(s.of(team));  // the host keeps a share below 2^32
+    PlanPlace p = {0, 0, 0, 0};
+    int h = 0;
+    if (left != 0) {
+      const uint64_t u = s.first(team);
+      h = static_cast<int>(u / work);
+      p = plan_find(a, u - h * work);
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      sts128(at, make_uint4(left, p.into, p.chunk, p.tile));
+      sts32(at + 16, h);
+    }
+    __syncwarp();
   }
   __device__ __forceinline__ bool next(const PrefixArgs& a, uint32_t team) {
-    while (left != 0) {
+    __syncwarp();
+    const uint4 w = lds128(at);
+    uint32_t left = w.x, skip = w.y;
+    int chunk = static_cast<int>(w.z), i = static_cast<int>(w.w), h = static_cast<int>(word(4));
+    bool found = false;
+    while (left != 0 && !found) {
       while (i >= static_cast<int>(plan_chunk(a)[chunk].tiles)) {  // there is work left, so there is a tile
         i = 0;
         if (++chunk == a.plan_chunks) chunk = 0, ++h;
       }
-      now_chunk = chunk, now_i = i, head = h;
       const MaskedTile* t = plan_tiles(a, chunk) + i;
       const uint32_t cost = t[1].first - t[0].first, extra = a.tile_cost, n = min(left, cost - skip);
       const uint32_t from = max(skip, extra) - extra, to = max(skip + n, extra) - extra;
       left -= n;
       skip = 0;
-      ++i;
       if (to > from) {
         b0 = t->lo / KB + static_cast<int>(from);
         b1 = t->lo / KB + static_cast<int>(to);
-        part = to - from == cost - extra ? -1 : static_cast<int>(2 * team + (from > 0 ? 0 : 1));
-        return true;
+        const uint32_t part = to - from == cost - extra ? 0 : 2 * team + (from > 0 ? 0 : 1) + 1;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) sts32(at + 20, chunk), sts32(at + 24, i), sts32(at + 28, static_cast<uint32_t>(h) << 16 | part);
+        found = true;
       }
+      ++i;
     }
-    return false;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sts128(at, make_uint4(left, skip, chunk, i)), sts32(at + 16, h);
+    __syncwarp();
+    return found;
   }
 };
 

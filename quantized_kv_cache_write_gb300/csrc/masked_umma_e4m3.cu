@@ -3,6 +3,6 @@
 
 namespace qkv {
 
-cudaError_t launch_masked_umma_e4m3(const PrefixArgs& a, cudaStream_t stream) { return prefix::launch_umma<QKV_E4M3, true>(a, stream); }
+cudaError_t launch_masked_umma_e4m3(const PrefixArgs& a, cudaStream_t stream) { return prefix::launch_masked_umma<QKV_E4M3>(a, stream); }
 
 }  // namespace qkv

@@ -3,6 +3,6 @@
 
 namespace qkv {
 
-cudaError_t launch_masked_umma_int8_side(const PrefixArgs& a, cudaStream_t stream) { return prefix::launch_umma<QKV_INT8_SIDE, true>(a, stream); }
+cudaError_t launch_masked_umma_int8_side(const PrefixArgs& a, cudaStream_t stream) { return prefix::launch_masked_umma<QKV_INT8_SIDE>(a, stream); }
 
 }  // namespace qkv

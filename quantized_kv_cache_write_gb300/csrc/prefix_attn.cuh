@@ -139,16 +139,17 @@ __device__ __forceinline__ RowRange row_range(const PrefixArgs& a, int64_t r, bo
   }
   return x;
 }
-// tanh, off by less than 2^-20 of itself: near 0 its series (the first term left out is below 2^-23 of the value),
-// elsewhere one exponential and one reciprocal, 1 - 2 / (1 + e^2z), off by less than 2^-21, with the limits at infinities.
-constexpr float kTanhSmall = 0.4f;
+// tanh, off by less than 2^-20 of itself: up to kTanhSmall a polynomial in z^2 fitted to tanh(z) / z by least squares on the
+// relative error (2^-22.6 with fp32 steps), elsewhere one exponential and one reciprocal, 1 - 2 / (1 + e^2z), off by less
+// than 2^-21, with the limits at infinities.
+constexpr float kTanhSmall = 0.75f;
+__device__ constexpr float kTanh[6] = {1.0f, -0.33332958817481995f, 0.1332540661096573f, -0.05334442853927612f, 0.01958290860056877f, -0.004716257099062204f};
 __device__ __forceinline__ float tanh_series(float z) {
   const float x = z * z;
-  float s = fmaf(x, -8.8632355e-3f, 2.1869488e-2f);  // -1382 / 155925, 62 / 2835
-  s = fmaf(x, s, -5.3968254e-2f);                    // -17 / 315
-  s = fmaf(x, s, 1.3333333e-1f);                     // 2 / 15
-  s = fmaf(x, s, -3.3333333e-1f);                    // -1 / 3
-  return fmaf(x * s, z, z);
+  float s = kTanh[5];
+#pragma unroll
+  for (int i = 4; i >= 0; --i) s = fmaf(x, s, kTanh[i]);
+  return z * s;
 }
 __device__ __forceinline__ float tanh_exp(float z) {
   float r;
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   const bool pow2 = (bsz & (bsz - 1)) == 0, runs = bsz % TK == 0;  // runs: a tile never leaves its block
   const int shift = __ffs(bsz) - 1;
   auto block_of = [&](int pos) -> int { return pow2 ? pos >> shift : pos / bsz; };
-  auto tile_pos = [&](int i) -> int { return a0 + (warp + kWarps * i) * TK; };
+  // MASK: from the last tile to the first, so that the nearest keys, whose bias is smallest, set the reference at once
+  auto tile_pos = [&](int i) -> int { return a0 + (MASK ? ntiles - 1 - warp - kWarps * i : warp + kWarps * i) * TK; };
   // block id of key `lane` of this warp's tile i (loaded a tile ahead of its use)
   auto load_blk = [&](int i) -> int {
     const int pos = tile_pos(i) + lane;

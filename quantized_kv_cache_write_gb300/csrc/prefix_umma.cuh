@@ -80,7 +80,8 @@ struct Umma {
   // MASK: each pair's range, nearest position and slope; each softmax warp's positions that all its rows see; blocks whose
   // values that are not finite were left out (a bit for each block modulo 32)
   static constexpr uint32_t kTab = kRow + 2 * kParts * 4 * kTileM, kAll = kTab + (MASK ? NT * kTileM * 16 : 0);
-  static constexpr uint32_t kOdd = kAll + (MASK ? NT * kSoftWarps * 8 : 0);
+  static constexpr uint32_t kSeg = kAll + (MASK ? NT * kSoftWarps * 8 : 0);  // and each warp's segment
+  static constexpr uint32_t kOdd = kSeg + (MASK ? 4 * kSegWords * (kMmaWarp + 1) : 0);
   static constexpr uint32_t kBar = kOdd + (MASK ? 16 : 0);
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
@@ -243,6 +244,15 @@ __device__ __forceinline__ void scale_by(float (&v)[N], const float4* src) {
   }
 }
 template <int N>
+__device__ __forceinline__ void scale_by(float (&v)[N], uint32_t at) {
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k) {
+    const uint4 f = lds128(at + 16 * k);
+    f2scale(v + 4 * k, f2pack(__uint_as_float(f.x), __uint_as_float(f.y)));
+    f2scale(v + 4 * k + 2, f2pack(__uint_as_float(f.z), __uint_as_float(f.w)));
+  }
+}
+template <int N>
 __device__ __forceinline__ void mask_by(float (&v)[N], uint32_t mask) {
 #pragma unroll
   for (int k = 0; k < N; ++k)
@@ -310,6 +320,10 @@ struct Records {
   int bsz, shift, len, H, h, lo = 0;
   bool pow2;
   __device__ __forceinline__ bool in(int p) const { return p < len && (!MASK || p >= lo); }
+  __device__ __forceinline__ void init(const PrefixArgs& a, int head) {
+    blocks = a.prefix_blocks, num_slots = a.num_slots, bsz = a.block_size, len = a.prefix_len, H = a.num_kv_heads, h = head;
+    pow2 = (bsz & (bsz - 1)) == 0, shift = __ffs(bsz) - 1;
+  }
   __device__ __forceinline__ void of_tile(const PrefixArgs& a, const MaskedTile& t) {
     lo = t.lo, len = t.hi;
     blocks = a.block_table + static_cast<int64_t>(t.hi > 0 ? t.seq : 0) * a.max_blocks;  // no keys: no sequence either
@@ -460,22 +474,60 @@ __device__ __forceinline__ uint32_t k_slot(int j) { return j == 0 ? 0 : 2 * j - 
 __device__ __forceinline__ uint32_t v_slot(int j, int B) { return j == B - 1 ? 2 * B - 1 : 2 * j + 2; }
 
 // Scores of N columns in log2 units from their logits: x fac, capped and less the distance bias. The columns' positions are
-// base + k; `row` addresses the pair's nearest position and its slope.
+// base + k; `row` addresses the pair's nearest position and its slope. Where the warp's logits are all small against the cap,
+// as they nearly always are, tanh is its polynomial, two columns at a time; the bias is linear where no row of the warp has
+// its nearest position inside the columns. 2048 rows x 32 heads of 128 behind 20000 bf16 keys, us: 1036 without either; with
+// the cap 1831 while each column chose for itself.
 template <int N>
 __device__ __forceinline__ void adjust_scores(float (&x)[N], float fac, float cap, bool bias, uint32_t row, int base) {
-  const uint64_t fac2 = f2pack(fac, fac);
-#pragma unroll
-  for (int k = 0; k < N; k += 2) f2unpack(f2mul(f2pack(x[k], x[k + 1]), fac2), x[k], x[k + 1]);
   if (cap > 0.f) {
+    const uint64_t fac2 = f2pack(fac, fac);
     const float up = cap * kLog2e;
+    float big = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = up * tanh_of(x[k]);
+    for (int k = 0; k < N; k += 2) {
+      f2unpack(f2mul(f2pack(x[k], x[k + 1]), fac2), x[k], x[k + 1]);
+      big = max3(big, fabsf(x[k]), fabsf(x[k + 1]));
+    }
+    if (__all_sync(0xffffffffu, big < kTanhSmall)) {
+      uint64_t c[6];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) c[i] = f2pack(up * kTanh[i], up * kTanh[i]);
+#pragma unroll
+      for (int k = 0; k < N; k += 2) {
+        const uint64_t z = f2pack(x[k], x[k + 1]), z2 = f2mul(z, z);
+        uint64_t s = c[5];
+#pragma unroll
+        for (int i = 4; i >= 0; --i) s = f2fma(z2, s, c[i]);
+        f2unpack(f2mul(z, s), x[k], x[k + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float e = tanh_exp(x[k]), s = tanh_series(x[k]);
+        x[k] = up * (fabsf(x[k]) < kTanhSmall ? s : e);
+      }
+    }
+    fac = 1.f;
   }
   if (bias) {
+    const uint64_t fac2 = f2pack(fac, fac);
     const uint2 v = lds64(row);
-    const float from = static_cast<float>(base - static_cast<int>(v.x)), slope = __uint_as_float(v.y);
+    const int at = base - static_cast<int>(v.x);
+    const float from = static_cast<float>(at), slope = __uint_as_float(v.y);
+    if (__all_sync(0xffffffffu, at >= 0 || at + N <= 1)) {
+      const float s = at >= 0 ? slope : -slope;
+      const uint64_t s2 = f2pack(s, s), from2 = f2pack(s * from, s * from), two = f2pack(2.f, 2.f);
+      uint64_t k2 = f2pack(0.f, 1.f);
 #pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = fmaf(slope, fabsf(from + static_cast<float>(k)), x[k]);
+      for (int k = 0; k < N; k += 2) {
+        f2unpack(f2fma(f2pack(x[k], x[k + 1]), fac2, f2fma(s2, k2, from2)), x[k], x[k + 1]);
+        k2 = f2add(k2, two);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = fmaf(slope, fabsf(from + static_cast<float>(k)), x[k] * fac);
+    }
   }
 }
 
@@ -494,8 +546,8 @@ __device__ __forceinline__ void note_odd(uint32_t odd, int j) {
 // The values that are not finite which the producers of a masked segment left out of blocks that some rows do not see whole,
 // added to the thread's part of O (HD / kParts dims from d0 on) where its row sees their keys. `odd` addresses the record of
 // such blocks. Nearly always there are none.
-template <int FMT, int HD, int KB, typename REC, typename SEG>
-__device__ __forceinline__ void add_odd(const PrefixArgs& a, REC rc, const SEG& seg, int h, uint32_t odd, uint32_t range, uint32_t to,
+template <int FMT, int HD, int KB, typename SEG>
+__device__ __forceinline__ void add_odd(const PrefixArgs& a, const SEG& seg, int h, uint32_t odd, uint32_t range, uint32_t to,
                                         int d0, bool in) {
   using F = Fmt<FMT>;
   const uint32_t bits = lds32(odd);
@@ -503,7 +555,8 @@ __device__ __forceinline__ void add_odd(const PrefixArgs& a, REC rc, const SEG& 
   const uint2 lim = lds64(range);
   const int lo = static_cast<int>(lim.x), hi = in ? static_cast<int>(lim.y) : 0;
   const MaskedTile tile = seg.tile(a);
-  rc.h = h;
+  Records<true> rc;
+  rc.init(a, h);
   rc.of_tile(a, tile);
   for (int j = seg.b0; j < seg.b1; ++j) {
     const int p0 = j * KB;
@@ -542,28 +595,32 @@ struct Segments;
 template <int KB>
 struct Segments<false, KB> : Segment {
   template <int CG>
-  __device__ __forceinline__ void begin(const PrefixArgs& a) { static_cast<Segment&>(*this) = first_segment<CG>(a); }
-  __device__ __forceinline__ int head(const PrefixArgs& a) const { return tile / a.umma_ptiles; }
+  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t) { static_cast<Segment&>(*this) = first_segment<CG>(a); }
+  template <int CG>
+  __device__ __forceinline__ bool next_of(const PrefixArgs& a) { return next(a); }
+  __device__ __forceinline__ int head_of(const PrefixArgs& a) const { return tile / a.umma_ptiles; }
 };
 template <int KB>
 struct Segments<true, KB> : MaskedSegment<KB> {
-  uint32_t team;
   template <int CG>
-  __device__ __forceinline__ void begin(const PrefixArgs& a) {
-    team = blockIdx.x / CG;
-    MaskedSegment<KB>::begin(a, team);
-  }
-  __device__ __forceinline__ bool next(const PrefixArgs& a) { return MaskedSegment<KB>::next(a, team); }
-  __device__ __forceinline__ int head(const PrefixArgs&) const { return MaskedSegment<KB>::head; }
+  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t words) { MaskedSegment<KB>::begin(a, blockIdx.x / CG, words); }
+  template <int CG>
+  __device__ __forceinline__ bool next_of(const PrefixArgs& a) { return MaskedSegment<KB>::next(a, blockIdx.x / CG); }
+  __device__ __forceinline__ int head_of(const PrefixArgs&) const { return this->head(); }
 };
 
 // MASK: qkv_masked_attn, with the work list of masked_tiles.cuh. What differs: the tile's keys lie in its sequence's row
 // of the block table, a block that not all of a warp's rows see whole is masked row by row, scores may be capped and get the
 // distance bias, and a tile that one team has whole is written out here. A value of V that is not finite in a
 // block that some row of the tile does not see whole is left out of the product (0 times it would not be 0) and added at
-// the end for the rows that see it.
-template <int FMT, int HD, int NT, int CG, bool MASK>
-__global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) prefix_umma_kernel(const PrefixArgs a) {
+// the end for the rows that see it. A segment's
+// blocks are taken from the last to the first: a row's nearest keys, whose bias is smallest, then set its reference at once.
+// MODE: kPrefix, kMasked, or kAdjusted, which is masked with capped scores or a bias (their code takes registers that the
+// others' softmax would spill).
+constexpr int kPrefix = 0, kMasked = 1, kAdjusted = 2;
+template <int FMT, int HD, int NT, int CG, int MODE>
+__global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThreads, 1) prefix_umma_kernel(const PrefixArgs a) {
+  constexpr bool MASK = MODE != kPrefix;
   using F = Fmt<FMT>;
   using U = Umma<FMT, HD, NT, CG, MASK>;
   constexpr int NS = U::kSlots, KB = U::KB;
@@ -610,10 +667,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
   const uint32_t tb = lds32(sb + U::kTmemSlot);
   if (MASK) await_previous();  // the work list
   Segments<MASK, KB> seg;
-  seg.template begin<CG>(a);
+  seg.template begin<CG>(a, sb + U::kSeg + 4 * kSegWords * warp);
   Records<MASK> rc;
-  rc.blocks = a.prefix_blocks, rc.num_slots = a.num_slots, rc.bsz = a.block_size, rc.len = a.prefix_len, rc.H = H;
-  rc.pow2 = (rc.bsz & (rc.bsz - 1)) == 0, rc.shift = __ffs(rc.bsz) - 1;
+  if (!MASK) rc.init(a, 0);
 
   if (warp < U::kSoftWarps) {
     // ================================================================ softmax: kParts threads per pair
@@ -654,8 +710,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       tmem_fence_after_sync();
       return done;
     };
-    while (seg.next(a)) {
-      const int h = seg.head(a);
+    while (seg.template next_of<CG>(a)) {
+      int h = seg.head_of(a);
       uint32_t flat0, flats = pairs;  // the thread's pair in tile 0, and how many there are (MASK: of the tile's rows)
       const uint16_t* q0 = a.q;
       if constexpr (MASK) {
@@ -725,7 +781,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           if (!F::kBytes && sign < 0.f) v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
           sts128(part + rr * 128 + (((c0 + lane % kVec) ^ (rr & 7)) << 4), v[i]);
         }
-        float fc = fabsf(a.softmax_scale) * (MASK && a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
+        float fc = fabsf(a.softmax_scale) * (MODE == kAdjusted && a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
         if (F::kBytes) {
           __syncwarp();
           uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
@@ -769,11 +825,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
 
-      const int subs = (seg.b1 - seg.b0) * NT;
+      int from = MASK ? (seg.b1 - 1) * KB : 0;  // MASK: the block's first position
+      const uint32_t end = (jb + (seg.b1 - seg.b0)) * NT;
 #pragma unroll 1
-      for (int i = 0; i < subs; ++i) {
-        const int t = NT == 2 ? i & 1 : 0;
-        const uint32_t blk = jb + i / NT, n = jb * NT + i, b = n & 1;
+      for (uint32_t n = jb * NT; n != end; ++n) {
+        const int t = NT == 2 ? n & 1 : 0;
+        const uint32_t blk = n / NT, b = n & 1;
         const uint32_t sc = sb + U::kSc + (blk & (kScRing - 1)) * U::kScStage;
         if (t == 0) ok = ok && bar_wait(sb + U::kScFull + 8 * (blk & (kScRing - 1)), (blk / kScRing) & 1, flag);
         ok = ok && bar_wait(sb + U::kSFull + 8 * b, (n >> 1) & 1, flag);
@@ -783,10 +840,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           const uint4 mw = lds128(sc + U::kScMask);
           bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
           uint32_t seen = ~0u;  // MASK: the thread's columns that its row sees
-          const int base = (seg.b0 + i / NT) * KB + wg * HB;  // MASK: position of the thread's first column
+          const int base = from + wg * HB;  // MASK: position of the thread's first column
           if (MASK) {
             const uint2 all = lds64(sb + U::kAll + 8 * (t * U::kSoftWarps + warp));
-            whole = whole && base - wg * HB >= static_cast<int>(all.x) && base - wg * HB + KB <= static_cast<int>(all.y);
+            whole = whole && from >= static_cast<int>(all.x) && from + KB <= static_cast<int>(all.y);
             if (!whole) {
               const uint2 range = lds64(sb + U::kTab + 16 * (t * kTileM + r));
               const int lo = min(max(static_cast<int>(range.x) - base, 0), HB), hi = min(max(static_cast<int>(range.y) - base, 0), HB);
@@ -801,9 +858,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           float x[HB];
           tmem_load(ts, x);
           tmem_loaded(x);
-          if (F::kInt8) scale_by(x, ksp);
+          if (F::kInt8) {
+            if (MASK) scale_by(x, sc + 4 * wg * HB);
+            else scale_by(x, ksp);
+          }
           float fc = fac[0];
-          if (MASK && (a.softcap > 0.f || a.slopes != nullptr)) {
+          if (MODE == kAdjusted) {
             adjust_scores<HB>(x, fc, a.softcap, a.slopes != nullptr, sb + U::kTab + 16 * (t * kTileM + r) + 8, base);
             fc = 1.f;  // x holds the scores, in log2 units
           }
@@ -820,7 +880,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
               vmax = 0;
 #pragma unroll
               for (int k = 0; k < HB; ++k)
-                if ((seen >> k) & 1) vmax = max(vmax, __float_as_uint(reinterpret_cast<const float*>(vsp)[k]) & 0x7fffffffu);
+                if ((seen >> k) & 1) vmax = max(vmax, lds32(sc + U::kScVs + 4 * (wg * HB + k)) & 0x7fffffffu);
               if (!exchange(__uint_as_float(vmax), all)) break;
 #pragma unroll
               for (int k = 0; k < kParts; ++k) vmax = max(vmax, __float_as_uint(all[k]));
@@ -863,7 +923,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
             sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
           }
           if (F::kInt8) {
-            scale_by(x, vsp);  // a missing key's scale is 0
+            if (MASK) scale_by(x, sc + U::kScVs + 4 * wg * HB);
+            else scale_by(x, vsp);  // a missing key's scale is 0
             if (MASK && !whole) {
 #pragma unroll
               for (int k = 0; k < HB; ++k)
@@ -877,7 +938,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           float s0, s1;
           f2unpack(f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3])), s0, s1);
           l[0] += s0 + s1;
-          if (raise && i >= NT) {
+          // MASK: f is 1 in a segment's first block
+          if (MASK ? __any_sync(0xffffffffu, raise && f != 1.f) : raise && n >= (jb + 1) * NT) {
             // O of the blocks before, once their P V is done (with two tiles S was issued after it); last, when the
             // columns' registers are free for a part of the dims at once
             if (NT == 1) ok = await_pv(n - 1);
@@ -902,11 +964,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           if (t == NT - 1) bar_arrive(sb + U::kScEmpty + 8 * (blk & (kScRing - 1)));
         }
         other_tile();
+        if (MASK && t == NT - 1) from -= KB;
       }
-      jb += seg.b1 - seg.b0;
+      jb = end / NT;
       // ---- the segment's partial results
       int row0 = 0;
-      if constexpr (MASK) row0 = seg.tile(a).row0, flats = static_cast<uint32_t>(seg.tile(a).nrows * G);
+      if constexpr (MASK) row0 = seg.tile(a).row0, flats = static_cast<uint32_t>(seg.tile(a).nrows * G), h = seg.head();
 #pragma unroll 1
       for (int t = 0; t < NT; ++t, other_tile()) {
         ok = ok && await_pv((jb - 1) * NT + t);
@@ -919,11 +982,13 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
         const float sum = (all[0] + all[1]) + (all[2] + all[3]);
         const bool any = sum != 0.f;  // NaN too
         float inv = any ? 1.f / sum : 0.f;
-        int64_t part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
+        int64_t part_at = 0;
         int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
-        if constexpr (MASK) {
-          if (!F::kInt8) add_odd<FMT, HD, KB>(a, rc, seg, h, sb + U::kOdd, sb + U::kTab + 16 * (t * kTileM + r), tl + U::kO + t * HD + d0, d0, in);
-          if (seg.part < 0) {
+        if constexpr (!MASK) {
+          part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
+        } else {
+          if (!F::kInt8) add_odd<FMT, HD, KB>(a, seg, h, sb + U::kOdd, sb + U::kTab + 16 * (t * kTileM + r), tl + U::kO + t * HD + d0, d0, in);
+          if (seg.part() < 0) {
             at += row0 * a.num_q_heads;
             if (in && wg == 0 && a.lse != nullptr) {
               float far = 0.f;
@@ -959,7 +1024,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
             }
             continue;
           }
-          part_at = static_cast<int64_t>(seg.part) * (NT * CG * kTileM);
+          part_at = static_cast<int64_t>(seg.part()) * (NT * CG * kTileM);
           at = static_cast<int>(flat);
         }
         if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
@@ -1017,7 +1082,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kFull + 8 * (s % NS));
     };
-    while (ok && seg.next(a)) {
+    while (ok && seg.template next_of<CG>(a)) {
       const int B = seg.b1 - seg.b0;
       int all_lo = 0, all_hi = 0;
       if constexpr (MASK) all_lo = seg.tile(a).all_lo, all_hi = seg.tile(a).all_hi;
@@ -1025,7 +1090,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       auto in_part = [&](int e, auto is_v, auto block_of) -> bool {
         if constexpr (MASK) {
           if (F::kInt8 || !is_v(e)) return false;
-          const int p = (seg.b0 + block_of(e)) * KB;
+          const int p = (seg.b1 - 1 - block_of(e)) * KB;
           return p < all_lo || p + KB > all_hi;
         }
         return false;
@@ -1064,7 +1129,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
             uint32_t odd = 0;
 #pragma unroll
             for (int u = 0; u < N; ++u) odd |= drop_odd_e4m3(raw[u]);
-            if (odd) note_odd<CG>(sb + U::kOdd, seg.b0 + block_of(e));
+            if (odd) note_odd<CG>(sb + U::kOdd, seg.b1 - 1 - block_of(e));
           }
           convert_rows<FMT, N>(sb + U::kRing + (n % NS) * U::kSlotBytes, is_v(e) ? vr : kr, raw);
           hand_over(n);
@@ -1080,7 +1145,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           cp_async_commit();
           cp_async_wait<0>();
           if (MASK && in_part(e, is_v, block_of) && VOp::template drop_odd<F::kBf16>(slot, pw, lane))
-            note_odd<CG>(sb + U::kOdd, seg.b0 + block_of(e));
+            note_odd<CG>(sb + U::kOdd, seg.b1 - 1 - block_of(e));
           hand_over(n);
         }
       }
@@ -1089,20 +1154,21 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
     }
   } else if (warp == U::kRecWarp) {
     // ================================================================ records
+    if (MASK) rc.init(a, 0);
     uint32_t jb = 0;
     bool ok = true;
-    while (ok && seg.next(a)) {
-      rc.h = seg.head(a);
+    while (ok && seg.template next_of<CG>(a)) {
+      rc.h = seg.head_of(a);
       if constexpr (MASK) rc.of_tile(a, seg.tile(a));
       int blk[KB / 32];
 #pragma unroll
-      for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup(seg.b0 * KB + 32 * i + lane);
+      for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup((MASK ? seg.b1 - 1 : seg.b0) * KB + 32 * i + lane);
       for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
         const uint32_t n = jb % kRecRing;
         int rec[KB / 32];
 #pragma unroll
         for (int i = 0; i < KB / 32; ++i) {
-          const int p = j * KB + 32 * i + lane;
+          const int p = (MASK ? seg.b1 - 1 - (j - seg.b0) : j) * KB + 32 * i + lane;
           rec[i] = rc.record(p, blk[i]);
           if constexpr (MASK) {
             if (rec[i] < 0 && rc.in(p) && a.dev_status != nullptr) {  // missing: flagged where a row sees it
@@ -1116,7 +1182,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
           } else {
             if (rec[i] < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
           }
-          blk[i] = j + 1 < seg.b1 ? rc.lookup(p + KB) : -1;  // the next block's, a block ahead of its use
+          blk[i] = j + 1 < seg.b1 ? rc.lookup(MASK ? p - KB : p + KB) : -1;  // the next block's, a block ahead of its use
         }
         if (jb >= kRecRing) {
           ok = __all_sync(0xffffffffu, bar_wait(sb + U::kRecEmpty + 8 * n, (jb / kRecRing - 1) & 1, flag));
@@ -1132,7 +1198,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
     // ================================================================ scales and masks
     uint32_t jb = 0;
     bool ok = true;
-    while (ok && seg.next(a)) {
+    while (ok && seg.template next_of<CG>(a)) {
       for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
         const uint32_t n = jb & (kScRing - 1), sc = sb + U::kSc + n * U::kScStage, rn = jb % kRecRing;
         float ks[KB / 32], vs[KB / 32];
@@ -1224,7 +1290,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
       }
       __syncwarp();
     };
-    while (ok && seg.next(a)) {
+    while (ok && seg.template next_of<CG>(a)) {
       const int B = seg.b1 - seg.b0;
       ok = wait(sb + U::kQFull, segs & 1);
       ++segs;
@@ -1259,10 +1325,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MASK>::kThreads, 1) pref
   if (tid == 0 && lds32(flag) != 0u && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_TIMEOUT);
 }
 
-template <int FMT, int HD, int NT, int CG, bool MASK>
+template <int FMT, int HD, int NT, int CG, int MODE>
 cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
-  using U = Umma<FMT, HD, NT, CG, MASK>;
-  auto kern = prefix_umma_kernel<FMT, HD, NT, CG, MASK>;
+  using U = Umma<FMT, HD, NT, CG, MODE != kPrefix>;
+  auto kern = prefix_umma_kernel<FMT, HD, NT, CG, MODE>;
   static std::atomic<bool> done[64] = {};
   cudaError_t e = allow_smem(kern, U::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -1281,7 +1347,7 @@ cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
     at[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
   }
-  if (MASK) {  // starts while the work list is made
+  if (MODE != kPrefix) {  // starts while the work list is made
     at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
@@ -1289,7 +1355,7 @@ cudaError_t launch_umma(const PrefixArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int FMT, bool MASK = false>
+template <int FMT, int MODE = kPrefix>
 cudaError_t launch_umma(PrefixArgs a, cudaStream_t stream) {
   // Test of the lost-wait path: QKV_TEST_PREFIX_DROP_HANDOFF=<block> makes the records' warp leave out the hand-off of
   // that block in each CTA (read at each launch; unset in any other use).
@@ -1298,9 +1364,15 @@ cudaError_t launch_umma(PrefixArgs a, cudaStream_t stream) {
     const long n = std::strtol(t, &end, 10);
     if (end != t && n >= 0 && n < (1 << 30)) a.umma_drop = static_cast<uint32_t>(n);
   }
-  if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2, MASK>(a, stream) : launch_umma<FMT, 256, 1, 1, MASK>(a, stream);
-  if (a.umma_cg == 2) return launch_umma<FMT, 128, MASK ? 1 : 2, 2, MASK>(a, stream);
-  return launch_umma<FMT, 128, 1, 1, MASK>(a, stream);
+  if (a.head_dim == 256) return a.umma_cg == 2 ? launch_umma<FMT, 256, 1, 2, MODE>(a, stream) : launch_umma<FMT, 256, 1, 1, MODE>(a, stream);
+  // masked: one tile of 256 pairs, not two: half of the work at a tile's ends, and no second tile's state
+  if (a.umma_cg == 2) return launch_umma<FMT, 128, MODE == kPrefix ? 2 : 1, 2, MODE>(a, stream);
+  return launch_umma<FMT, 128, 1, 1, MODE>(a, stream);
+}
+
+template <int FMT>
+cudaError_t launch_masked_umma(const PrefixArgs& a, cudaStream_t stream) {
+  return a.softcap > 0.f || a.slopes != nullptr ? launch_umma<FMT, kAdjusted>(a, stream) : launch_umma<FMT, kMasked>(a, stream);
 }
 
 }  // namespace prefix
