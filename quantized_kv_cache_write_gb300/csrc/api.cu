@@ -917,8 +917,14 @@ qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, in
   return check_prefix_shape(fmt, rows, num_q_heads, num_kv_heads, head_dim, 0, max_row_end);
 }
 
-// Pairs of a sequence, on average, from which a masked call runs on tcgen05 tiles.
-constexpr int64_t kMaskedUmmaPairs = 64;
+// Where a masked call runs on tcgen05 tiles: a sequence brings at least this many pairs on average, and tiles of 16
+// pairs would read at least so many bytes of keys and values, most of them from L2 (a tcgen05 call costs some 16 us more at its
+// ends). In us, mma.sync | tcgen05: 16 heads of 256, int8: 8 sequences x 5 rows behind 1000 keys (20 MB) 24 | 38, behind
+// 8000 (164 MB) 72 | 53; 64 x 4 behind 1000 (131 MB) 54 | 49; 4 x 16 behind 1000 (33 MB) 25 | 38, behind 8000 96 | 51. 8
+// heads of 128 in groups of 8, e4m3: 8 x 5 behind 1000 (49 MB) 26 | 41, behind 8000 (393 MB) 109 | 90; 64 x 4 behind
+// 8000 420 | 395; 64 x 1 behind 8000 209 | 389. Groups of 4: 64 x 4 behind 8000 (16 pairs) 269 | 391.
+constexpr int64_t kMaskedUmmaPairs = 32;
+constexpr int64_t kMaskedUmmaBytes = 100 << 20;
 // What a tile costs besides its key blocks, in blocks.
 constexpr int kMaskedTileCost = 6;
 
@@ -936,7 +942,9 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   p->rows = rows;
   p->umma_cg = 0, p->umma_pairs = 0, p->tile_rows = 0, p->block_keys = 0, p->tile_cost = 0, p->umma_teams = 0;
   const int64_t pairs = rows * G / num_seqs;  // of a sequence
-  if (pairs >= kMaskedUmmaPairs && max_row_end <= (1 << 27) && num_kv_heads <= 0xffff) {
+  const int64_t tiles16 = ceil_div(rows * G, 16) * num_kv_heads;
+  const bool large = keys > 0 && tiles16 >= kMaskedUmmaBytes / (keys * 2 * row_bytes_of(fmt, head_dim));
+  if (pairs >= kMaskedUmmaPairs && large && max_row_end <= (1 << 27) && num_kv_heads <= 0xffff) {
     p->umma_cg = pairs > 128 ? 2 : 1;
     p->umma_pairs = 128 * p->umma_cg;
     p->tile_rows = p->umma_pairs / G;

@@ -502,11 +502,16 @@ __device__ __forceinline__ void adjust_scores(float (&x)[N], float fac, float ca
         f2unpack(f2mul(z, s), x[k], x[k + 1]);
       }
     } else {
+      // column by column, the large ones first: both forms of all columns at once would spill
+      uint32_t small = 0;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float e = tanh_exp(x[k]), s = tanh_series(x[k]);
-        x[k] = up * (fabsf(x[k]) < kTanhSmall ? s : e);
+        if (fabsf(x[k]) < kTanhSmall) small |= 1u << k;
+        else x[k] = tanh_exp(x[k]);
       }
+      asm volatile("" : "+r"(small));
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = up * ((small >> k) & 1 ? tanh_series(x[k]) : x[k]);
     }
     fac = 1.f;
   }
