@@ -94,73 +94,32 @@ __device__ __forceinline__ PlanPlace plan_find(const PrefixArgs& a, uint64_t rem
   return p;
 }
 
-// A team's next segment: its part of the blocks of one tile of one KV head. Blocks are numbered from position 0. What the
-// roles' loops do not need sits in shared memory, a copy of its own for each warp (kSegWords words at `at`), and the
-// tile's entry is read where it is needed, from L1: in registers they cost the softmax its columns.
-constexpr int kSegWords = 8;
-template <int KB>
-struct MaskedSegment {
-  uint32_t at;
-  int b0, b1;
-  // words: work still to do; work of the next tile that a team before has; the next tile's chunk, number and KV head;
-  // this one's chunk and number; its KV head and part (-1: whole) in one
-  __device__ __forceinline__ uint32_t word(int i) const { return lds32(at + 4 * i); }
-  __device__ __forceinline__ const MaskedTile& tile(const PrefixArgs& a) const {
-    return plan_tiles(a, static_cast<int>(word(5)))[word(6)];
-  }
-  __device__ __forceinline__ int head() const { return static_cast<int>(word(7) >> 16); }
-  __device__ __forceinline__ int part() const { return static_cast<int>(word(7) & 0xffffu) - 1; }
-  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t team, uint32_t words) {
-    at = words;
+// A team's walk through its share, a segment at a time: its part of the blocks of one tile of one KV head. One warp of each
+// SM walks and publishes the segments to the other roles (SegWord); a walk in every role costs each of them a thousand
+// cycles of loads per segment, and the instruction cache a copy.
+struct MaskedWalk {
+  uint32_t left;    // work still to do
+  uint32_t skip;    // work of the next tile that a team before has
+  int chunk, i, h;  // the next tile and its KV head
+  uint32_t team;
+  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t of_team) {
+    team = of_team;
     const uint64_t work = plan_work(a);
     const Shares s(work * a.num_kv_heads, a.umma_teams);
-    const uint32_t left = static_cast<uint32_t>(s.of(team));  // the host keeps a share below 2^32
-    PlanPlace p = {0, 0, 0, 0};
-    int h = 0;
-    if (left != 0) {
-      const uint64_t u = s.first(team);
-      h = static_cast<int>(u / work);
-      p = plan_find(a, u - h * work);
-    }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      sts128(at, make_uint4(left, p.into, p.chunk, p.tile));
-      sts32(at + 16, h);
-    }
-    __syncwarp();
-  }
-  __device__ __forceinline__ bool next(const PrefixArgs& a, uint32_t team) {
-    __syncwarp();
-    const uint4 w = lds128(at);
-    uint32_t left = w.x, skip = w.y;
-    int chunk = static_cast<int>(w.z), i = static_cast<int>(w.w), h = static_cast<int>(word(4));
-    bool found = false;
-    while (left != 0 && !found) {
-      while (i >= static_cast<int>(plan_chunk(a)[chunk].tiles)) {  // there is work left, so there is a tile
-        i = 0;
-        if (++chunk == a.plan_chunks) chunk = 0, ++h;
-      }
-      const MaskedTile* t = plan_tiles(a, chunk) + i;
-      const uint32_t cost = t[1].first - t[0].first, extra = a.tile_cost, n = min(left, cost - skip);
-      const uint32_t from = max(skip, extra) - extra, to = max(skip + n, extra) - extra;
-      left -= n;
-      skip = 0;
-      if (to > from) {
-        b0 = t->lo / KB + static_cast<int>(from);
-        b1 = t->lo / KB + static_cast<int>(to);
-        const uint32_t part = to - from == cost - extra ? 0 : 2 * team + (from > 0 ? 0 : 1) + 1;
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) sts32(at + 20, chunk), sts32(at + 24, i), sts32(at + 28, static_cast<uint32_t>(h) << 16 | part);
-        found = true;
-      }
-      ++i;
-    }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) sts128(at, make_uint4(left, skip, chunk, i)), sts32(at + 16, h);
-    __syncwarp();
-    return found;
+    left = static_cast<uint32_t>(s.of(team));  // the host keeps a share below 2^32
+    skip = 0, chunk = 0, i = 0, h = 0;
+    if (left == 0) return;
+    const uint64_t u = s.first(team);
+    h = static_cast<int>(u / work);
+    const PlanPlace p = plan_find(a, u - h * work);
+    chunk = p.chunk, i = p.tile, skip = p.into;
   }
 };
+// A published segment, in shared memory: its first block and the last one's next (equal: there is none; blocks are numbered
+// from position 0), the tile's rows, its KV head, its place among the partial results (-1: the tile is whole), what all
+// of its rows see, and where the tile's entry is.
+enum SegWord { kSegB0, kSegB1, kSegRow0, kSegRows, kSegHead, kSegPart, kSegAllLo, kSegAllHi, kSegChunk, kSegTile, kSegWords = 12 };
+constexpr int kSegRing = 4;  // the softmax holds a segment while it asks for the next one
 
 }  // namespace prefix
 }  // namespace qkv

@@ -80,9 +80,10 @@ struct Umma {
   // MASK: each pair's range, nearest position and slope; each softmax warp's positions that all its rows see; blocks whose
   // values that are not finite were left out (a bit for each block modulo 32)
   static constexpr uint32_t kTab = kRow + 2 * kParts * 4 * kTileM, kAll = kTab + (MASK ? NT * kTileM * 16 : 0);
-  static constexpr uint32_t kSeg = kAll + (MASK ? NT * kSoftWarps * 8 : 0);  // and each warp's segment
-  static constexpr uint32_t kOdd = kSeg + (MASK ? 4 * kSegWords * (kMmaWarp + 1) : 0);
-  static constexpr uint32_t kBar = kOdd + (MASK ? 16 : 0);
+  static constexpr uint32_t kSeg = kAll + (MASK ? NT * kSoftWarps * 8 : 0);  // the published segments
+  static constexpr uint32_t kOdd = kSeg + (MASK ? 4 * kSegWords * kSegRing : 0);
+  static constexpr uint32_t kSegFull = kOdd + (MASK ? 16 : 0), kSegEmpty = kSegFull + (MASK ? 8 * kSegRing : 0);
+  static constexpr uint32_t kBar = kSegEmpty + (MASK ? 8 * kSegRing : 0);
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
                             kRecFull = kScEmpty + 8 * kScRing, kRecEmpty = kRecFull + 8 * kRecRing,
@@ -257,6 +258,16 @@ __device__ __forceinline__ void mask_by(float (&v)[N], uint32_t mask) {
 #pragma unroll
   for (int k = 0; k < N; ++k)
     if (!((mask >> k) & 1)) v[k] = -INFINITY;
+}
+// 16 bytes, or zeros; issued here, however late they are used.
+__device__ __forceinline__ uint4 load_if(const uint4* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      " @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<uint32_t>(there)));
+  return v;
 }
 // 16 or 32 columns of this thread's tensor-memory lane; 8 or 16 packed ones
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
@@ -549,21 +560,26 @@ __device__ __forceinline__ void note_odd(uint32_t odd, int j) {
 }
 
 // The values that are not finite which the producers of a masked segment left out of blocks that some rows do not see whole,
-// added to the thread's part of O (HD / kParts dims from d0 on) where its row sees their keys. `odd` addresses the record of
-// such blocks. Nearly always there are none.
-template <int FMT, int HD, int KB, typename SEG>
-__device__ __forceinline__ void add_odd(const PrefixArgs& a, const SEG& seg, int h, uint32_t odd, uint32_t range, uint32_t to,
-                                        int d0, bool in) {
+// added to the thread's part of O (HD / kParts dims from d0 on) where its row sees their keys. Nearly always there are
+// none.
+struct Odd {
+  const MaskedTile* tile;
+  int b0, b1;       // the segment's blocks
+  uint32_t bits;    // address of the record of such blocks
+  uint32_t range;   // and of the pair's range
+};
+template <int FMT, int HD, int KB>
+__device__ __forceinline__ void add_odd(const PrefixArgs& a, const Odd& odd, int h, uint32_t to, int d0, bool in) {
   using F = Fmt<FMT>;
-  const uint32_t bits = lds32(odd);
+  const uint32_t bits = lds32(odd.bits);
   if (__builtin_expect(!__any_sync(0xffffffffu, bits != 0u), 1)) return;
-  const uint2 lim = lds64(range);
+  const uint2 lim = lds64(odd.range);
   const int lo = static_cast<int>(lim.x), hi = in ? static_cast<int>(lim.y) : 0;
-  const MaskedTile tile = seg.tile(a);
+  const MaskedTile tile = *odd.tile;
   Records<true> rc;
   rc.init(a, h);
   rc.of_tile(a, tile);
-  for (int j = seg.b0; j < seg.b1; ++j) {
+  for (int j = odd.b0; j < odd.b1; ++j) {
     const int p0 = j * KB;
     if (!((bits >> (j & 31)) & 1) || (p0 >= tile.all_lo && p0 + KB <= tile.all_hi)) continue;
     for (int c = 0; c < HD / kParts; c += 16) {
@@ -594,25 +610,89 @@ __device__ __forceinline__ void add_odd(const PrefixArgs& a, const SEG& seg, int
   }
 }
 
-// The segments of the prefix or of the masked rows, alike for the roles.
-template <bool MASK, int KB>
+// The segments of the prefix, or the published ones of the masked rows, alike for the roles.
+template <bool MASK, typename U, int CG>
 struct Segments;
-template <int KB>
-struct Segments<false, KB> : Segment {
-  template <int CG>
+template <typename U, int CG>
+struct Segments<false, U, CG> : Segment {
   __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t) { static_cast<Segment&>(*this) = first_segment<CG>(a); }
-  template <int CG>
-  __device__ __forceinline__ bool next_of(const PrefixArgs& a) { return next(a); }
-  __device__ __forceinline__ int head_of(const PrefixArgs& a) const { return tile / a.umma_ptiles; }
+  __device__ __forceinline__ int head(const PrefixArgs& a) const { return tile / a.umma_ptiles; }
+  __device__ __forceinline__ void done() const {}
 };
-template <int KB>
-struct Segments<true, KB> : MaskedSegment<KB> {
-  template <int CG>
-  __device__ __forceinline__ void begin(const PrefixArgs& a, uint32_t words) { MaskedSegment<KB>::begin(a, blockIdx.x / CG, words); }
-  template <int CG>
-  __device__ __forceinline__ bool next_of(const PrefixArgs& a) { return MaskedSegment<KB>::next(a, blockIdx.x / CG); }
-  __device__ __forceinline__ int head_of(const PrefixArgs&) const { return this->head(); }
+template <typename U, int CG>
+struct Segments<true, U, CG> {
+  uint32_t sb, count;
+  int b0, b1;
+  bool lost;  // the wait for a segment ran out
+  __device__ __forceinline__ void begin(const PrefixArgs&, uint32_t base) { sb = base, count = 0, lost = false; }
+  __device__ __forceinline__ uint32_t at(uint32_t n) const { return sb + U::kSeg + 4 * kSegWords * (n % kSegRing); }
+  __device__ __forceinline__ int word(SegWord w) const { return static_cast<int>(lds32(at(count - 1) + 4 * w)); }
+  __device__ __forceinline__ int head(const PrefixArgs&) const { return word(kSegHead); }
+  __device__ __forceinline__ bool next(const PrefixArgs&) {
+    const uint32_t n = count % kSegRing;
+    lost = !__all_sync(0xffffffffu, bar_wait(sb + U::kSegFull + 8 * n, (count / kSegRing) & 1, sb + U::kFlag));
+    if (lost) return false;
+    take();
+    return b1 > b0;
+  }
+  __device__ __forceinline__ void take() {
+    ++count;
+    b0 = word(kSegB0), b1 = word(kSegB1);
+  }
+  // the warp is done with segment n, or the one at hand
+  __device__ __forceinline__ void release(uint32_t n) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(sb + U::kSegEmpty + 8 * (n % kSegRing));
+  }
+  __device__ __forceinline__ void done() const { release(count - 1); }
 };
+// The walk's next segment into the ring as number n, or the mark that there is none; whether there is one.
+template <int KB, typename U>
+__device__ __forceinline__ bool publish(const PrefixArgs& a, MaskedWalk& w, uint32_t sb, uint32_t n) {
+  bool found = false;
+  int b0 = 0, b1 = 0, part = -1, chunk = 0, i = 0, h = 0;
+  MaskedTile t = {};
+  while (w.left != 0 && !found) {
+    while (w.i >= static_cast<int>(plan_chunk(a)[w.chunk].tiles)) {  // there is work left, so there is a tile
+      w.i = 0;
+      if (++w.chunk == a.plan_chunks) w.chunk = 0, ++w.h;
+    }
+    chunk = w.chunk, i = w.i, h = w.h;
+    t = plan_tiles(a, chunk)[i];
+    const uint32_t cost = plan_tiles(a, chunk)[i + 1].first - t.first, extra = a.tile_cost, took = min(w.left, cost - w.skip);
+    const uint32_t from = max(w.skip, extra) - extra, to = max(w.skip + took, extra) - extra;
+    w.left -= took;
+    w.skip = 0;
+    ++w.i;
+    found = to > from;
+    b0 = t.lo / KB + static_cast<int>(from), b1 = t.lo / KB + static_cast<int>(to);
+    part = to - from == cost - extra ? -1 : static_cast<int>(2 * w.team + (from > 0 ? 0 : 1));
+  }
+  if (!found) b0 = b1 = 0, t.nrows = 0, t.row0 = 0;
+  if (n >= kSegRing && !__all_sync(0xffffffffu, bar_wait(sb + U::kSegEmpty + 8 * (n % kSegRing), (n / kSegRing - 1) & 1, sb + U::kFlag)))
+    return false;
+  if ((threadIdx.x & 31) == 0) {
+    const uint32_t at = sb + U::kSeg + 4 * kSegWords * (n % kSegRing);
+    sts128(at, make_uint4(b0, b1, t.row0, t.nrows));
+    sts128(at + 16, make_uint4(h, part, t.all_lo, t.all_hi));
+    sts128(at + 32, make_uint4(chunk, i, 0, 0));
+    bar_arrive(sb + U::kSegFull + 8 * (n % kSegRing));
+  }
+  __syncwarp();
+  return found;
+}
+// Missing keys are flagged where a row of the tile sees them.
+static __device__ __noinline__ void flag_if_seen(const int32_t* start, const int32_t* end, const int32_t* pos, int window, int max_end, int rows, int p,
+                                          uint32_t* status) {
+  for (int k = 0; k < rows; ++k) {
+    const int e = __ldg(end + k), b = start != nullptr ? __ldg(start + k) : 0, at = pos != nullptr ? __ldg(pos + k) : e - 1;
+    if (e > max_end || b < 0 || at < 0 || at > kMaxRowPos) continue;  // an invalid row, which sees nothing
+    if (p < e && p >= (window > 0 ? max(b, at - window + 1) : b)) {
+      atomicOr(status, QKV_DEV_BAD_INDEX);
+      return;
+    }
+  }
+}
 
 // MASK: qkv_masked_attn, with the work list of masked_tiles.cuh. What differs: the tile's keys lie in its sequence's row
 // of the block table, a block that not all of a warp's rows see whole is masked row by row, scores may be capped and get the
@@ -658,6 +738,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         bar_init(sb + U::kRecEmpty + 8 * s, 2 * kProdWarps + 1);  // a K and a V group, and scales
       }
       bar_init(sb + U::kQFull, U::kSoftWarps * CG);
+      for (int s = 0; MASK && s < kSegRing; ++s) {
+        bar_init(sb + U::kSegFull + 8 * s, 1);
+        // the softmax, two groups of producers, the scales and, in the team's first SM, the MMAs
+        bar_init(sb + U::kSegEmpty + 8 * s, U::kSoftWarps + 2 * kProdWarps + 1 + (rank == 0 ? 1 : 0));
+      }
       bar_init(sb + U::kDrain, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
       sts32(flag, 0u);
@@ -671,8 +756,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
   tmem_fence_after_sync();
   const uint32_t tb = lds32(sb + U::kTmemSlot);
   if (MASK) await_previous();  // the work list
-  Segments<MASK, KB> seg;
-  seg.template begin<CG>(a, sb + U::kSeg + 4 * kSegWords * warp);
+  Segments<MASK, U, CG> seg;
+  seg.begin(a, sb);
   Records<MASK> rc;
   if (!MASK) rc.init(a, 0);
 
@@ -715,71 +800,199 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
       tmem_fence_after_sync();
       return done;
     };
-    while (seg.template next_of<CG>(a)) {
-      int h = seg.head_of(a);
-      uint32_t flat0, flats = pairs;  // the thread's pair in tile 0, and how many there are (MASK: of the tile's rows)
-      const uint16_t* q0 = a.q;
+    static_assert(!MASK || NT == 1, "masked segments have one tile");
+    const uint32_t mask_flat = rank * kTileM + r;  // MASK: the thread's pair in the tile
+    int h = 0, row0 = 0;                           // MASK: the segment's KV head and first row
+    uint32_t flat0 = mask_flat, flats = pairs;     // the thread's pair in tile 0, and how many there are (MASK: of the tile's rows)
+    uint4 asked[MASK ? kVec : 1];                  // MASK: query rows, as loaded
+    RowRange range = {kPadRow, 0, 0, 0, 0};        // MASK: the pair's
+    float slope = 0.f;
+    // kVec lanes fetch the part of a row's dims that a thread has together, 32 / kVec rows at a time
+    auto load_query = [&](uint32_t flat, uint4* v) {
+      const bool in = flat < flats;
+      const uint32_t row = in ? flat / G : 0;
+      const uint16_t* src = a.q + (row0 + static_cast<int64_t>(row)) * a.q_stride + static_cast<int64_t>(in ? h * G + (flat - row * G) : 0) * HD + d0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int rr = 32 / kVec * i + lane / kVec;
+        const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), rr);
+        const bool there = __shfl_sync(0xffffffffu, in, rr);
+        if (MASK) v[i] = load_if(reinterpret_cast<const uint4*>(at) + lane % kVec, there);
+        else v[i] = there ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kVec) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    bool more = true, begun = false;
+    // MASK: what a segment needs from global memory, asked for while the one before ends (if there is none: nothing)
+    auto fetch = [&]() {
       if constexpr (MASK) {
-        flat0 = rank * kTileM + r, flats = static_cast<uint32_t>(seg.tile(a).nrows * G);
-        const int64_t row0 = seg.tile(a).row0;
-        q0 += row0 * a.q_stride;
-        // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see
-#pragma unroll 1
-        for (int t = 0; t < NT; ++t) {
-          const uint32_t flat = flat0 + t * CG * kTileM;
-          RowRange x = {kPadRow, 0, 0, 0, 0};
-          const uint32_t row = flat / G;
-          if (flat < flats) x = row_range(a, row0 + row, false);
-          const float slope = flat < flats && a.slopes != nullptr ? __ldg(a.slopes + h * G + (flat - row * G)) : 0.f;
-          if (wg == 0)
-            sts128(sb + U::kTab + 16 * (t * kTileM + r), make_uint4(x.lo, x.hi, x.near, __float_as_uint(-slope * kLog2e)));
-          const int lo = __reduce_max_sync(0xffffffffu, flat < flats ? x.lo : 0);
-          const int hi = __reduce_min_sync(0xffffffffu, flat < flats ? x.hi : INT_MAX);
-          if (lane == 0) {
-            sts32(sb + U::kAll + 8 * (t * U::kSoftWarps + warp), lo);
-            sts32(sb + U::kAll + 8 * (t * U::kSoftWarps + warp) + 4, hi);
-          }
+        h = seg.word(kSegHead), row0 = seg.word(kSegRow0), flats = more ? static_cast<uint32_t>(seg.word(kSegRows) * G) : 0;
+        load_query(mask_flat, asked);
+        range = RowRange{kPadRow, 0, 0, 0, 0}, slope = 0.f;
+        if (mask_flat < flats) {
+          const uint32_t row = mask_flat / G;
+          if (MODE == kAdjusted && a.slopes != nullptr) slope = __ldg(a.slopes + h * G + (mask_flat - row * G));
+          range = row_range(a, row0 + static_cast<int64_t>(row), false);
         }
+      }
+    };
+    // state of the tile at hand; with two tiles the other one's waits in the second element
+    float M[2], R[2], l[2], fac[NT];
+    int E[2];
+    bool warp_in[NT];
+    auto other_tile = [&]() {
+      if (NT == 2) {
+        float x;
+        x = M[0], M[0] = M[1], M[1] = x;
+        x = R[0], R[0] = R[1], R[1] = x;
+        x = l[0], l[0] = l[1], l[1] = x;
+        x = fac[0], fac[0] = fac[NT - 1], fac[NT - 1] = x;
+        const int e = E[0];
+        E[0] = E[1], E[1] = e;
+        const bool w = warp_in[0];
+        warp_in[0] = warp_in[NT - 1], warp_in[NT - 1] = w;
+      }
+    };
+    // ---- the segment's partial results, or (MASK) the output of a tile that is the team's own
+    auto finish = [&](int out_h, int out_row0, uint32_t out_flats, int out_part, const Odd& odd) {
+#pragma unroll 1
+      for (int t = 0; t < NT; ++t, other_tile()) {
+        ok = ok && await_pv((jb - 1) * NT + t);
+        if (!warp_in[0]) continue;
+        float all[kParts];
+        if (!exchange(l[0], all)) break;
+        const uint32_t flat = flat0 + t * CG * kTileM;
+        const bool in = flat < out_flats;
+        const uint32_t row = in ? flat / G : 0;
+        const float sum = (all[0] + all[1]) + (all[2] + all[3]);
+        const bool any = sum != 0.f;  // NaN too
+        float inv = any ? 1.f / sum : 0.f;
+        int64_t part_at = 0;
+        int at = static_cast<int>(row * a.num_q_heads + out_h * G + (flat - row * G));
+        if constexpr (!MASK) {
+          part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
+        } else {
+          if (!F::kInt8) add_odd<FMT, HD, KB>(a, odd, out_h, tl + U::kO + d0, d0, in);
+          if (out_part < 0) {
+            at += out_row0 * a.num_q_heads;
+            if (in && wg == 0 && a.lse != nullptr) {
+              float far = 0.f;
+              if (MODE == kAdjusted && a.slopes != nullptr && any) {
+                const RowRange x = row_range(a, out_row0 + static_cast<int64_t>(row), false);
+                if (x.pos != x.near) far = -__ldg(a.slopes + out_h * G + (flat - row * G)) * fabsf(static_cast<float>(x.pos - x.near));
+              }
+              a.lse[at] = any ? (R[0] + log2f(sum)) * kLn2 + far : -INFINITY;
+            }
+            // 32 rows x 32 dims at a time, rounded, through the warp's place in the query tile: four lanes write 64 B of a
+            // row. A thread that writes its own row touches a line of its own with each store: 3300 cycles a tile, not 1000.
+            inv = any ? inv * a.merge_scale : 0.f;
+            const int to = in ? at : -1;
+#pragma unroll 1
+            for (int c = 0; c < HD / kParts; c += 32) {
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                float o[16];
+                tmem_load(tl + U::kO + d0 + c + 16 * half, o);
+                tmem_loaded(o);
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  // int8: the producers store dims 0, 2, 1, 3 of each four
+                  float z[4] = {o[4 * k], F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], F::kInt8 ? o[4 * k + 1] : o[4 * k + 2], o[4 * k + 3]};
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) z[n] = any ? z[n] * inv : 0.f;
+                  w[2 * k] = round2(a.q_f16, z[0], z[1]), w[2 * k + 1] = round2(a.q_f16, z[2], z[3]);
+                }
+                sts128(own_part + lane * 128 + (((c0 + 2 * half) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                sts128(own_part + lane * 128 + (((c0 + 2 * half + 1) ^ (lane & 7)) << 4), make_uint4(w[4], w[5], w[6], w[7]));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int rr = 8 * k + (lane >> 3) + (lane & 4);
+                const int rr_to = __shfl_sync(0xffffffffu, to, rr);
+                const uint4 x = lds128(own_part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
+                if (rr_to >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(rr_to) * HD + d0 + c + 8 * (lane & 3)) = x;
+              }
+              __syncwarp();
+            }
+            continue;
+          }
+          part_at = static_cast<int64_t>(out_part) * (NT * CG * kTileM);
+          at = static_cast<int>(flat);
+        }
+        if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
+        // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer
+        // needs: four lanes write 64 B of a row
+        const int to = in && any ? at : -1;
+        const uint32_t part = own_part + t * U::kQTile;
+#pragma unroll 1
+        for (int c = 0; c < HD / kParts; c += 16) {
+          float o[16];
+          tmem_load(tl + U::kO + t * HD + d0 + c, o);
+          tmem_loaded(o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // int8: the producers store dims 0, 2, 1, 3 of each four
+            const float x1 = F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], x2 = F::kInt8 ? o[4 * k + 1] : o[4 * k + 2];
+            sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(o[4 * k] * inv), __float_as_uint(x1 * inv), __float_as_uint(x2 * inv),
+                              __float_as_uint(o[4 * k + 3] * inv)));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 8 * k + (lane >> 3) + (lane & 4);
+            const int rr_to = __shfl_sync(0xffffffffu, to, rr);
+            const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
+            if (rr_to >= 0) *reinterpret_cast<uint4*>(a.o_part + (part_at + rr_to) * HD + d0 + c + 4 * (lane & 3)) = x;
+          }
+          __syncwarp();
+        }
+        }
+      tmem_fence_before_sync();  // ordered before the next segment's first arrival
+    };
+    while (true) {
+      if constexpr (MASK) {
+        const int out_h = h, out_row0 = row0, out_part = begun ? seg.word(kSegPart) : 0;
+        const uint32_t out_flats = flats, used = seg.count - 1;
+        Odd odd = {};
+        if (!F::kInt8 && begun)
+          odd = Odd{plan_tiles(a, seg.word(kSegChunk)) + seg.word(kSegTile), seg.b0, seg.b1, sb + U::kOdd, sb + U::kTab + 16 * r};
+        more = ok && seg.next(a);
+        if (seg.lost) ok = false;
+        if (seg.count > 0) fetch();
+        if (begun) finish(out_h, out_row0, out_flats, out_part, odd);
+        if (vote(!ok)) break;
+        if (begun) seg.release(used);
+        if (!more) break;
+        begun = true;
+        // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see
+        if (wg == 0) sts128(sb + U::kTab + 16 * r, make_uint4(range.lo, range.hi, range.near, __float_as_uint(-slope * kLog2e)));
+        const int lo = __reduce_max_sync(0xffffffffu, mask_flat < flats ? range.lo : 0);
+        const int hi = __reduce_min_sync(0xffffffffu, mask_flat < flats ? range.hi : INT_MAX);
+        if (lane == 0) sts32(sb + U::kAll + 8 * warp, lo), sts32(sb + U::kAll + 8 * warp + 4, hi);
         __syncwarp();
         if (vote(!ok)) break;  // the table is read from here on
       } else {
+        if (!seg.next(a)) break;
+        h = seg.head(a);
         flat0 = (static_cast<uint32_t>(seg.tile - h * a.umma_ptiles) * NT * CG + rank) * kTileM + r;
       }
-      // state of the tile at hand; with two tiles the other one's waits in the second element
-      float M[2] = {-INFINITY, -INFINITY}, R[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, fac[NT] = {};
-      int E[2] = {F::kInt8 ? -90 : 0, F::kInt8 ? -90 : 0};
-      bool warp_in[NT] = {};
-      auto other_tile = [&]() {
-        if (NT == 2) {
-          float x;
-          x = M[0], M[0] = M[1], M[1] = x;
-          x = R[0], R[0] = R[1], R[1] = x;
-          x = l[0], l[0] = l[1], l[1] = x;
-          x = fac[0], fac[0] = fac[NT - 1], fac[NT - 1] = x;
-          const int e = E[0];
-          E[0] = E[1], E[1] = e;
-          const bool w = warp_in[0];
-          warp_in[0] = warp_in[NT - 1], warp_in[NT - 1] = w;
-        }
-      };
+#pragma unroll
+      for (int i = 0; i < 2; ++i) M[i] = -INFINITY, R[i] = 0.f, l[i] = 0.f, E[i] = F::kInt8 ? -90 : 0;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) fac[i] = 0.f, warp_in[i] = false;
       // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), a part of the
-      // dims by each of a row's threads; kVec lanes fetch a row's part together, 32 / kVec rows at a time
+      // dims by each of a row's threads
 #pragma unroll 1
       for (int t = 0; t < NT; ++t, other_tile()) {
         const uint32_t flat = flat0 + t * CG * kTileM;
-        const bool in = flat < flats;
-        const uint32_t row = in ? flat / G : 0;
-        warp_in[0] = __any_sync(0xffffffffu, in);
-        const uint16_t* src = q0 + row * a.q_stride + static_cast<int64_t>(in ? h * G + (flat - row * G) : 0) * HD + d0;
+        warp_in[0] = __any_sync(0xffffffffu, flat < flats);
         const uint32_t part = own_part + t * U::kQTile;
         uint4 v[kVec];
+        if (!MASK) load_query(flat, v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const int rr = 32 / kVec * i + lane / kVec;
-          const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), rr);
-          const bool there = __shfl_sync(0xffffffffu, in, rr);
-          v[i] = there ? __ldg(reinterpret_cast<const uint4*>(from) + lane % kVec) : make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; MASK && i < kVec; ++i) v[i] = asked[MASK ? i : 0];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           const int rr = 32 / kVec * i + lane / kVec;
@@ -972,97 +1185,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         if (MASK && t == NT - 1) from -= KB;
       }
       jb = end / NT;
-      // ---- the segment's partial results
-      int row0 = 0;
-      if constexpr (MASK) row0 = seg.tile(a).row0, flats = static_cast<uint32_t>(seg.tile(a).nrows * G), h = seg.head();
-#pragma unroll 1
-      for (int t = 0; t < NT; ++t, other_tile()) {
-        ok = ok && await_pv((jb - 1) * NT + t);
-        if (!warp_in[0]) continue;
-        float all[kParts];
-        if (!exchange(l[0], all)) break;
-        const uint32_t flat = flat0 + t * CG * kTileM;
-        const bool in = flat < flats;
-        const uint32_t row = in ? flat / G : 0;
-        const float sum = (all[0] + all[1]) + (all[2] + all[3]);
-        const bool any = sum != 0.f;  // NaN too
-        float inv = any ? 1.f / sum : 0.f;
-        int64_t part_at = 0;
-        int at = static_cast<int>(row * a.num_q_heads + h * G + (flat - row * G));
-        if constexpr (!MASK) {
-          part_at = static_cast<int64_t>(seg.part) * a.rows * a.num_q_heads;
-        } else {
-          if (!F::kInt8) add_odd<FMT, HD, KB>(a, seg, h, sb + U::kOdd, sb + U::kTab + 16 * (t * kTileM + r), tl + U::kO + t * HD + d0, d0, in);
-          if (seg.part() < 0) {
-            at += row0 * a.num_q_heads;
-            if (in && wg == 0 && a.lse != nullptr) {
-              float far = 0.f;
-              if (a.slopes != nullptr && any) {
-                const RowRange x = row_range(a, row0 + static_cast<int64_t>(row), false);
-                if (x.pos != x.near) far = -__ldg(a.slopes + h * G + (flat - row * G)) * fabsf(static_cast<float>(x.pos - x.near));
-              }
-              a.lse[at] = any ? (R[0] + log2f(sum)) * kLn2 + far : -INFINITY;
-            }
-            // the tile is the team's own: 32 dims at a time, rounded, straight from the thread's registers
-            inv = any ? inv * a.merge_scale : 0.f;
-            uint16_t* to = a.out + static_cast<int64_t>(at) * HD + d0;
-#pragma unroll 1
-            for (int c = 0; c < HD / kParts; c += 32) {
-              float o[32];
-              tmem_load(tl + U::kO + t * HD + d0 + c, o);
-              tmem_loaded(o);
-              uint32_t w[16];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                // int8: the producers store dims 0, 2, 1, 3 of each four
-                float z[4] = {o[4 * k], F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], F::kInt8 ? o[4 * k + 1] : o[4 * k + 2], o[4 * k + 3]};
-#pragma unroll
-                for (int n = 0; n < 4; ++n) z[n] = any ? z[n] * inv : 0.f;
-                w[2 * k] = round2(a.q_f16, z[0], z[1]), w[2 * k + 1] = round2(a.q_f16, z[2], z[3]);
-              }
-              if (in) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  *reinterpret_cast<uint4*>(to + c + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-              }
-              __syncwarp();
-            }
-            continue;
-          }
-          part_at = static_cast<int64_t>(seg.part()) * (NT * CG * kTileM);
-          at = static_cast<int>(flat);
-        }
-        if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
-        // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer
-        // needs: four lanes write 64 B of a row
-        const int to = in && any ? at : -1;
-        const uint32_t part = own_part + t * U::kQTile;
-#pragma unroll 1
-        for (int c = 0; c < HD / kParts; c += 16) {
-          float o[16];
-          tmem_load(tl + U::kO + t * HD + d0 + c, o);
-          tmem_loaded(o);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // int8: the producers store dims 0, 2, 1, 3 of each four
-            const float x1 = F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], x2 = F::kInt8 ? o[4 * k + 1] : o[4 * k + 2];
-            sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4),
-                   make_uint4(__float_as_uint(o[4 * k] * inv), __float_as_uint(x1 * inv), __float_as_uint(x2 * inv),
-                              __float_as_uint(o[4 * k + 3] * inv)));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = 8 * k + (lane >> 3) + (lane & 4);
-            const int rr_to = __shfl_sync(0xffffffffu, to, rr);
-            const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
-            if (rr_to >= 0) *reinterpret_cast<uint4*>(a.o_part + (part_at + rr_to) * HD + d0 + c + 4 * (lane & 3)) = x;
-          }
-          __syncwarp();
-        }
+      if constexpr (!MASK) {
+        finish(h, 0, flats, 0, Odd{});
+        if (vote(!ok)) break;
       }
-      tmem_fence_before_sync();  // ordered before the next segment's first arrival
-      if (vote(!ok)) break;
     }
   } else if (warp < U::kRecWarp) {
     // ================================================================ producers
@@ -1087,10 +1213,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
       __syncwarp();
       if (lane == 0) lead_arrive<CG>(sb + U::kFull + 8 * (s % NS));
     };
-    while (ok && seg.template next_of<CG>(a)) {
+    while (ok && seg.next(a)) {
       const int B = seg.b1 - seg.b0;
       int all_lo = 0, all_hi = 0;
-      if constexpr (MASK) all_lo = seg.tile(a).all_lo, all_hi = seg.tile(a).all_hi;
+      if constexpr (MASK) all_lo = seg.word(kSegAllLo), all_hi = seg.word(kSegAllHi);
       // MASK: whether some row of the tile does not see slot e's block whole; values that are not finite are left out then
       auto in_part = [&](int e, auto is_v, auto block_of) -> bool {
         if constexpr (MASK) {
@@ -1156,15 +1282,27 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
       }
       base += 2 * B;
       jb += B;
+      seg.done();
     }
   } else if (warp == U::kRecWarp) {
     // ================================================================ records
     if (MASK) rc.init(a, 0);
     uint32_t jb = 0;
     bool ok = true;
-    while (ok && seg.template next_of<CG>(a)) {
-      rc.h = seg.head_of(a);
-      if constexpr (MASK) rc.of_tile(a, seg.tile(a));
+    [[maybe_unused]] MaskedWalk walk;
+    if constexpr (MASK) walk.begin(a, blockIdx.x / CG);
+    auto next_segment = [&]() -> bool {
+      if constexpr (MASK) {
+        if (!publish<KB, U>(a, walk, sb, seg.count)) return false;
+        seg.take();
+        return true;
+      } else {
+        return seg.next(a);
+      }
+    };
+    while (ok && next_segment()) {
+      rc.h = seg.head(a);
+      if constexpr (MASK) rc.of_tile(a, plan_tiles(a, seg.word(kSegChunk))[seg.word(kSegTile)]);
       int blk[KB / 32];
 #pragma unroll
       for (int i = 0; i < KB / 32; ++i) blk[i] = rc.lookup((MASK ? seg.b1 - 1 : seg.b0) * KB + 32 * i + lane);
@@ -1176,13 +1314,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           const int p = (MASK ? seg.b1 - 1 - (j - seg.b0) : j) * KB + 32 * i + lane;
           rec[i] = rc.record(p, blk[i]);
           if constexpr (MASK) {
-            if (rec[i] < 0 && rc.in(p) && a.dev_status != nullptr) {  // missing: flagged where a row sees it
-              bool sees = false;
-              for (int k = 0; k < seg.tile(a).nrows && !sees; ++k) {
-                const RowRange x = row_range(a, seg.tile(a).row0 + static_cast<int64_t>(k), false);
-                sees = p >= x.lo && p < x.hi;
-              }
-              if (sees) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
+            if (rec[i] < 0 && rc.in(p) && a.dev_status != nullptr) {
+              const int row = seg.word(kSegRow0);
+              flag_if_seen(a.row_start != nullptr ? a.row_start + row : nullptr, a.row_len + row, a.row_pos != nullptr ? a.row_pos + row : nullptr,
+                           a.window, a.max_row_len, seg.word(kSegRows), p, a.dev_status);
             }
           } else {
             if (rec[i] < 0 && p < a.prefix_len && a.dev_status != nullptr) atomicOr(a.dev_status, QKV_DEV_BAD_INDEX);
@@ -1203,7 +1338,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
     // ================================================================ scales and masks
     uint32_t jb = 0;
     bool ok = true;
-    while (ok && seg.template next_of<CG>(a)) {
+    while (ok && seg.next(a)) {
       for (int j = seg.b0; j < seg.b1; ++j, ++jb) {
         const uint32_t n = jb & (kScRing - 1), sc = sb + U::kSc + n * U::kScStage, rn = jb % kRecRing;
         float ks[KB / 32], vs[KB / 32];
@@ -1248,6 +1383,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         __syncwarp();
         if (lane == 0) bar_arrive(sb + U::kScFull + 8 * n);
       }
+      seg.done();
     }
   } else if (rank == 0) {
     // ================================================================ MMA issuer
@@ -1295,7 +1431,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
       }
       __syncwarp();
     };
-    while (ok && seg.template next_of<CG>(a)) {
+    while (ok && seg.next(a)) {
       const int B = seg.b1 - seg.b0;
       ok = wait(sb + U::kQFull, segs & 1);
       ++segs;
@@ -1313,6 +1449,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
       }
       jb += B;
       base += 2 * B;
+      seg.done();
     }
     if (lead) commit_to<CG>(sb + U::kDrain);
     __syncwarp();
