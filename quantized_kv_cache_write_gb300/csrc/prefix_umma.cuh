@@ -521,8 +521,15 @@ __device__ __forceinline__ void adjust_scores(float (&x)[N], float fac, float ca
         else x[k] = tanh_exp(x[k]);
       }
       asm volatile("" : "+r"(small));
+      // the polynomial step by step as above, so that a score does not depend on the rows that share its warp
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = up * ((small >> k) & 1 ? tanh_series(x[k]) : x[k]);
+      for (int k = 0; k < N; ++k) {
+        const float z2 = x[k] * x[k];
+        float s = up * kTanh[5];
+#pragma unroll
+        for (int i = 4; i >= 0; --i) s = fmaf(z2, s, up * kTanh[i]);
+        x[k] *= (small >> k) & 1 ? s : up;
+      }
     }
     fac = 1.f;
   }
@@ -948,7 +955,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           }
           __syncwarp();
         }
-        }
+      }
       tmem_fence_before_sync();  // ordered before the next segment's first arrival
     };
     while (true) {
@@ -1058,10 +1065,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           const uint4 mw = lds128(sc + U::kScMask);
           bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xffffffffu;
           uint32_t seen = ~0u;  // MASK: the thread's columns that its row sees
+          bool ranged = false;  // MASK: some row of the warp does not see all of the block's positions
           const int base = from + wg * HB;  // MASK: position of the thread's first column
           if (MASK) {
             const uint2 all = lds64(sb + U::kAll + 8 * (t * U::kSoftWarps + warp));
-            whole = whole && from >= static_cast<int>(all.x) && from + KB <= static_cast<int>(all.y);
+            ranged = from < static_cast<int>(all.x) || from + KB > static_cast<int>(all.y);
+            whole = whole && !ranged;
             if (!whole) {
               const uint2 range = lds64(sb + U::kTab + 16 * (t * kTileM + r));
               const int lo = min(max(static_cast<int>(range.x) - base, 0), HB), hi = min(max(static_cast<int>(range.y) - base, 0), HB);
@@ -1094,7 +1103,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           int En = E[0];
           if (F::kInt8) {
             uint32_t vmax = lds32(sc + U::kScVmax);
-            if (MASK && !whole) {  // of the keys that the row sees: the others' scales may be anything
+            // Of the keys that the row sees: the others' scales may be anything. (Missing keys count as 0 anyway, so that the
+            // warps meet here by their rows' ranges alone, on which they agree even when a wait ran out.)
+            if (MASK && ranged) {
               vmax = 0;
 #pragma unroll
               for (int k = 0; k < HB; ++k)

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a, co
 template <int FMT, int HD, bool PAIRS, int kRows>
 __global__ void __launch_bounds__(kReadThreads) read_turned_kernel(const ReadArgs a) {
   constexpr int W = HD / 8, kPerWarp = 32 / W;
-  constexpr bool kInt8 = FMT == QKV_INT8_SIDE || FMT == QKV_INT8_INLINE, k16 = FMT == QKV_BF16 || FMT == QKV_F16;
+  constexpr bool k16 = FMT == QKV_BF16 || FMT == QKV_F16;
   constexpr int kRecord = FMT == QKV_INT8_INLINE ? HD + 4 : k16 ? 2 * HD : HD;
   const int lane = threadIdx.x & 31, j = lane & (W - 1), sub = lane / W;
   const int hk = a.k_out != nullptr ? a.num_kv_heads : 0, rows = hk + (a.v_out != nullptr ? a.num_kv_heads : 0);
