@@ -69,12 +69,13 @@ typedef enum {
 #define QKV_DEV_TIMEOUT 4u   /* a gather CTA's bounded wait for its own copies or tensor-core
                                 work ran out (not expected on a healthy GPU): the CTA stopped
                                 early, its outputs are incomplete; the kernel returns instead of
-                                hanging. Only the tcgen05 engine and qkv_prefix_attn's tcgen05
-                                tiles wait. Tests make it happen:
+                                hanging. Only the tcgen05 engine and the tcgen05 tiles of
+                                qkv_prefix_attn and qkv_masked_attn wait. Tests make it happen:
                                 QKV_TEST_TCGEN05_DROP_HANDOFF=<block> in the environment drops
                                 that block's hand-off inside each CTA of the engine,
                                 QKV_TEST_PREFIX_DROP_HANDOFF=<block> inside each CTA of the tiles
-                                (never set them otherwise) */
+                                (never set them otherwise, nor QKV_TEST_MASKED_TILES, with which
+                                tests run qkv_masked_attn on tcgen05 or mma tiles at any size) */
 
 /*
  * qkv_write_int8 -- quantize new K/V tokens to int8 with one absmax scale per (token, head)

@@ -4,6 +4,8 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 
 #include "qkv_internal.cuh"
 
@@ -944,7 +946,10 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   const int64_t pairs = rows * G / num_seqs;  // of a sequence
   const int64_t tiles16 = ceil_div(rows * G, 16) * num_kv_heads;
   const bool large = keys > 0 && tiles16 >= kMaskedUmmaBytes / (keys * 2 * row_bytes_of(fmt, head_dim));
-  if (pairs >= kMaskedUmmaPairs && large && max_row_end <= (1 << 27) && num_kv_heads <= 0xffff) {
+  bool umma = pairs >= kMaskedUmmaPairs && large;
+  // Test of each kind of tiles at any size: QKV_TEST_MASKED_TILES=tcgen05 or mma (read at each call; unset in any other use).
+  if (const char* t = std::getenv("QKV_TEST_MASKED_TILES")) umma = std::strcmp(t, "tcgen05") == 0 || (umma && std::strcmp(t, "mma") != 0);
+  if (umma && max_row_end <= (1 << 27) && num_kv_heads <= 0xffff) {
     p->umma_cg = pairs > 128 ? 2 : 1;
     p->umma_pairs = 128 * p->umma_cg;
     p->tile_rows = p->umma_pairs / G;

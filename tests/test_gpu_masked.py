@@ -12,6 +12,13 @@ from masked_harness import Pool, Seqs, call, check, chunk_rows, dev16, query
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True, params=["mma", "tcgen05"])
+def tiles(request, monkeypatch):
+    """Each kind of tiles, whatever the call would choose at these sizes."""
+    monkeypatch.setenv("QKV_TEST_MASKED_TILES", request.param)
+
+
 FMTS = [("bf16", "bf16"), ("f16", "f16"), ("int8_side", "bf16"), ("int8_side", "f16"), ("int8_inline", "bf16"),
         ("e4m3", "f16"), ("e4m3", "bf16")]
 SLOPES = lambda n: 2.0 ** (-8.0 * np.arange(1, n + 1) / n)  # noqa: E731

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("fmt,act,D,G,new,block", [("e4m3", "bf16", 128, 8, 200, 0), ("int8_side", "bf16", 256, 16, 90, 2),
                                                    ("bf16", "bf16", 256, 2, 40, 1), ("int8_inline", "f16", 128, 4, 300, 3)])
-def test_a_lost_handoff_times_out_and_the_context_stays_usable(fmt, act, D, G, new, block):
+def test_a_lost_handoff_times_out_and_the_context_stays_usable(fmt, act, D, G, new, block, monkeypatch):
     import quantized_kv_cache_write_gb300 as qkv
     assert ENV not in os.environ
     rng = np.random.default_rng(block)
@@ -27,6 +27,7 @@ def test_a_lost_handoff_times_out_and_the_context_stays_usable(fmt, act, D, G, n
     rows = chunk_rows(lengths, (new, new))
     q = query(rng, len(rows), 2 * G, D, act)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("QKV_TEST_MASKED_TILES", "tcgen05")
     started = time.monotonic()
     os.environ[ENV] = str(block)
     try:
