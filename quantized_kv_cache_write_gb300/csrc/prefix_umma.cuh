@@ -198,6 +198,16 @@ __device__ __forceinline__ bool bar_try(uint32_t mbar, uint32_t parity) {
       : "memory");
   return ok != 0u;
 }
+// Whether the phase of the given parity is over, without waiting for it.
+__device__ __forceinline__ bool bar_test(uint32_t mbar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(mbar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
 __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
@@ -686,6 +696,13 @@ __device__ __forceinline__ bool publish(const PrefixArgs& a, MaskedWalk& w, uint
     bar_arrive(sb + U::kSegFull + 8 * (n % kSegRing));
   }
   __syncwarp();
+  // its queries into L2, a segment ahead of their loads
+  const int G = a.num_q_heads / a.num_kv_heads;
+  for (int k = threadIdx.x & 31; k < t.nrows; k += 32)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(a.q + (t.row0 + static_cast<int64_t>(k)) * a.q_stride +
+                                                                   static_cast<int64_t>(h) * G * a.head_dim),
+                 "r"(static_cast<uint32_t>(2 * G * a.head_dim))
+                 : "memory");
   return found;
 }
 // Missing keys are flagged where a row of the tile sees them.
@@ -1278,18 +1295,39 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           ok = load(e + 2);
         }
       } else {
+        // A slot is handed over when its copies have arrived; with a long ring after those of the group's next one have
+        // been asked for -- unless that one's place is still taken: what frees it may be waiting for this slot. 2048 rows
+        // behind 30000 bf16 keys, us, at once | one ahead: 32 heads of 128 (eight slots) 1224 | 1097, 16 heads of 256 (four
+        // slots) 743 | 807.
+        constexpr bool kOneAhead = NS >= 8;
+        int last = -1;  // the slot whose copies are on their way
+        auto arrived = [&](int e) {
+          const uint32_t n = base + e;
+          if (MASK && in_part(e, is_v, block_of) && VOp::template drop_odd<F::kBf16>(sb + U::kRing + (n % NS) * U::kSlotBytes, pw, lane))
+            note_odd<CG>(sb + U::kOdd, seg.b1 - 1 - block_of(e));
+          hand_over(n);
+        };
         for (int e = pg; ok && e < 2 * B; e += 2) {
           const uint32_t n = base + e, slot = sb + U::kRing + (n % NS) * U::kSlotBytes;
+          const bool ahead = kOneAhead && (n < NS || __all_sync(0xffffffffu, bar_test(sb + U::kEmpty + 8 * (n % NS), (n / NS - 1) & 1)));
+          if (last >= 0 && !ahead) {
+            cp_async_wait<0>();
+            arrived(last);
+            last = -1;
+          }
           if (!(ok = await_records(e)) || !(ok = await(n))) break;
           if (is_v(e)) VOp::copy(slot, a.v_cache, pw, lane, rec + vrow, voff);
           else KOp::copy(slot, a.k_cache, pw, lane, rec + krow, 0);
           free_records(e);
           cp_async_commit();
-          cp_async_wait<0>();
-          if (MASK && in_part(e, is_v, block_of) && VOp::template drop_odd<F::kBf16>(slot, pw, lane))
-            note_odd<CG>(sb + U::kOdd, seg.b1 - 1 - block_of(e));
-          hand_over(n);
+          if (last >= 0) {
+            cp_async_wait<1>();
+            arrived(last);
+          }
+          last = e;
         }
+        cp_async_wait<0>();
+        if (ok && last >= 0) arrived(last);
       }
       base += 2 * B;
       jb += B;
