@@ -1440,6 +1440,10 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
     bool ok = true;
     const uint32_t lead = elect_one();
     const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);  // warp-uniform
+    // This warp's path from a barrier to the next MMA is part of every block: what is probably there already (a slot's
+    // values) is awaited first, ahead of what the tensor cores and the softmax have just been asked for. All lanes agree on
+    // every wait: with each lane's own answer the descriptors leave the uniform registers (256 rows x 16 heads behind 65536
+    // int8 keys 235 -> 250 us).
     auto wait = [&](uint32_t bar, uint32_t ph) -> bool { return __all_sync(0xffffffffu, bar_wait(bar, ph, flag)); };
     auto await_full = [&](uint32_t s) -> bool { return wait(sb + U::kFull + 8 * (s % NS), (s / NS) & 1); };
     // S of sub-iteration n (of tile t) into its buffer, from the K slot s (awaited by the first tile, freed by the
@@ -1447,8 +1451,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
     // they have the same shape and accumulator, which S and O are not, so that P V has to be over first.
     auto qk = [&](int t, uint32_t n, uint32_t s) {
       const uint32_t b = n & 1;
-      if (n >= 2 && !(ok = wait(sb + U::kPvDone + 8 * b, ((n >> 1) - 1) & 1))) return;
       if (t == 0 && !(ok = await_full(s))) return;
+      if (n >= 2 && !(ok = wait(sb + U::kPvDone + 8 * b, ((n >> 1) - 1) & 1))) return;
       tmem_fence_after_sync();
       const uint32_t d = tu + U::kS + KB * b;
       const uint64_t qd = sw128_desc(sb + U::kQ + t * U::kQTile, 16, 1024);
@@ -1465,8 +1469,8 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
     };
     // O of tile t += P (in buffer b) times the V slot s
     auto pv = [&](int t, uint32_t b, uint32_t ph, uint32_t s, bool first) {
-      if (!(ok = wait(sb + U::kPFull + 8 * b, ph))) return;
       if (t == 0 && !(ok = await_full(s))) return;
+      if (!(ok = wait(sb + U::kPFull + 8 * b, ph))) return;
       tmem_fence_after_sync();
       constexpr int kPer = KB / kParts / 16;  // 16 keys a step
       const uint32_t d = tu + U::kO + t * HD, p = tu + U::kS + KB * b;
@@ -1488,12 +1492,15 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
 #pragma unroll 1
       for (int j = -1; ok && j < B; ++j) {
         const uint32_t n = jb + j;
+        if constexpr (NT == 1) {
+          if (j + 1 < B) qk(0, n + 1, base + k_slot(j + 1));
+          if (ok && j >= 0) pv(0, n & 1, (n >> 1) & 1, base + v_slot(j, B), j == 0);
+        } else {
 #pragma unroll 1
-        for (int i = 0; ok && i < 2; ++i) {
-          const int t = NT == 2 ? i : 0;
-          if (j >= 0 && (NT == 2 || i == 1))
-            pv(t, (n * NT + t) & 1, ((n * NT + t) >> 1) & 1, base + v_slot(j, B), j == 0);
-          if (ok && j + 1 < B && (NT == 2 || i == 0)) qk(t, (n + 1) * NT + t, base + k_slot(j + 1));
+          for (int t = 0; ok && t < NT; ++t) {
+            if (j >= 0) pv(t, (n * NT + t) & 1, ((n * NT + t) >> 1) & 1, base + v_slot(j, B), j == 0);
+            if (ok && j + 1 < B) qk(t, (n + 1) * NT + t, base + k_slot(j + 1));
+          }
         }
       }
       jb += B;
