@@ -1295,11 +1295,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           ok = load(e + 2);
         }
       } else {
-        // A slot is handed over when its copies have arrived; with a long ring after those of the group's next one have
-        // been asked for -- unless that one's place is still taken: what frees it may be waiting for this slot. 2048 rows
-        // behind 30000 bf16 keys, us, at once | one ahead: 32 heads of 128 (eight slots) 1224 | 1097, 16 heads of 256 (four
-        // slots) 743 | 807.
-        constexpr bool kOneAhead = NS >= 8;
+        // A slot is handed over when its copies have arrived; with a ring of five or more after those of the group's next
+        // one have been asked for -- unless that one's place is still taken: what frees it may be waiting for this slot.
+        // bf16, us, at once | one ahead: 2048 rows behind 30000 keys, 32 heads of 128 (eight slots) 1224 | 1097, 16 heads
+        // of 256 (four slots) 743 | 807; 64 x 4 rows x 64 heads of 128 behind 8000 (five slots) 437 | 403.
+        constexpr bool kOneAhead = NS >= 5;
         int last = -1;  // the slot whose copies are on their way
         auto arrived = [&](int e) {
           const uint32_t n = base + e;
