@@ -806,7 +806,7 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* desc, void* stream);
 /*
  * qkv_masked_attn -- dense attention over a paged pool whose scores may be capped, get a bias that depends on distance, and
  * are masked to a range of keys per row: a causal prompt or a chunk of one, a sliding window, packed documents, a prefix that
- * its own tokens see whole, and single tokens of any of these. Prompts run on tcgen05 tiles that take up to 512
+ * its own tokens see whole, and single tokens of any of these. Prompts run on tcgen05 tiles that take up to 256
  * (row, head) pairs of one sequence, single tokens on tiles of 16 or 8 whose keys are split over the GPU.
  * The pages attend to selected slots only; this is the dense operator over the same pool, scales and block tables
  * [HOIST-PR §Changes: scale hoisting; E4M3-PR §Implementation scope: paged storage].

@@ -12,7 +12,7 @@
 // often per MMA as with one SM.
 //
 // Warps: sixteen for the softmax (four threads per pair, a quarter of a block's columns each), two groups of four
-// producers, one for the records, one for the scales, one MMA issuer (of the team's first SM). Slots
+// producers, one for the records, one for the scales, one for the MMAs (of the team's first SM). Slots
 // (rows of 128 B, 128 B swizzle) pass from the producers to the MMA warp in the order
 // K_0 K_1 V_0 K_2 V_1 ..., one group every second one; K is K-major, V MN-major, and both are stored alike, one
 // 128 B row per key and 64 dims.
@@ -21,7 +21,7 @@
 //     free; then the registers take the group's next slot. 16-bit pools are copied straight into the slot
 //     (cp.async).
 //   scales: K and V scales, the mask of the block's keys and the largest V scale into a small ring.
-//   MMA: one thread. P is the A operand in tensor memory, in the columns of the S it was made from.
+//   MMA: one warp, of which an elected lane issues. P is the A operand in tensor memory, in the columns of the S it was made from.
 //   softmax: y = S ks fac (log2 units). Reference R = M + E - kShift: M follows the row's maximum lazily
 //     (raised when a logit passes it by 2^kRaise), E is a power-of-two bound on the V scales, so p vs 2^-R
 //     stays below fp16's range; l and O both carry 2^-R, and a raise of R rescales both. The thread's columns

@@ -34,6 +34,11 @@ flush (a 256 MiB write), and synchronises. Profile the last launch with
                      behind 65536 keys), e4m3 (64 rows x 64 heads of 128, 8 KV heads, 32768 keys) or
                      bf16 (128 rows x 32 heads of 128, 4 KV heads, 8191 keys, up to 2048 of their own)
   dense_e4m3         the same call without a prefix: 64 rows x 64 heads of 128, up to 8192 keys each
+  append_axes        qkv_append_axes of 8192 patches with three axes: 32 + 8 heads of 128, bf16
+  read_int8          qkv_read of 131072 tokens of an int8 side pool (one head of 256) to bf16
+  masked_<what>      qkv_masked_attn: prompt (4096 causal rows x 16 heads of 256, int8 side, capped), documents (8192
+                     packed rows x 32 heads of 128, 4 KV heads, bf16) or decode (64 rows x 64 heads of 128, 8 KV heads,
+                     up to 8192 e4m3 keys each, capped)
 """
 
 from __future__ import annotations
@@ -54,7 +59,8 @@ from gen import (chunked_prefill, e4m3_splitk_layer, long_context_decode, mixed_
 CASES = ["page1_int8_side", "page1_int8_inline", "page1_e4m3", "page1_bf16", "page1_tcgen05", "page1_gqa32",
          "page1_hd128", "e4m3_layer", "long_context", "mixed_default", "mixed_persistent", "chunked_prefill",
          "write_int8_fill", "write_e4m3_fill", "merge_e4m3_layer", "append_int8", "append_bf16", "prefix_int8",
-         "prefix_e4m3", "prefix_bf16", "dense_e4m3"]
+         "prefix_e4m3", "prefix_bf16", "dense_e4m3", "append_axes", "read_int8", "masked_prompt", "masked_documents",
+         "masked_decode"]
 
 
 def _dev(bits):
@@ -138,6 +144,67 @@ def _prefix(case: str):
                      device="cuda")
     return lambda: q.qkv_prefix_attn(qd, q.FORMATS[fmt], kc, vc, table, seq, ln, block, D ** -0.5, max_row_len=max(lens),
                                      num_kv_heads=H, prefix_blocks=ids[:shared], prefix_len=P, out=out, workspace=ws,
+                                     **kw)
+
+
+def _append_axes():
+    T, Hq, H, D, S = 8192, 32, 8, 128, 65536
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    packed = torch.randn((T, Hq + 2 * H, D), device="cuda", generator=gen).to(torch.bfloat16)
+    ang = torch.arange(131072, device="cuda", dtype=torch.float64)[:, None] * 1e6 ** (
+        -torch.arange(D // 2, device="cuda", dtype=torch.float64) / (D // 2))
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    t = torch.arange(T, device="cuda")
+    axis_pos = torch.stack([t // 1024, t // 32 % 32, t % 32]).int()  # frames of 32 x 32 patches
+    slots = torch.randperm(S, device="cuda", generator=gen)[:T]
+    kc = torch.zeros((S, H, D), dtype=torch.bfloat16, device="cuda")
+    vc, q_out = torch.zeros_like(kc), torch.empty((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    pair_axis = [0] * 16 + [1] * 24 + [2] * 24
+    return lambda: q.qkv_append_axes(packed[:, Hq:Hq + H], packed[:, Hq + H:], q.QKV_BF16, kc, vc, cs, axis_pos, pair_axis,
+                                     q=packed[:, :Hq], q_out=q_out, slot_mapping=slots)
+
+
+def _read_int8():
+    T, H, D, S = 131072, 1, 256, 262144
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    kc, vc = (torch.randint(-127, 128, (S, H, D), device="cuda", generator=gen, dtype=torch.int8) for _ in "kv")
+    ks, vs = (torch.rand((S, H), device="cuda", generator=gen) * 0.02 for _ in "kv")
+    slots = torch.randperm(S, device="cuda", generator=gen)[:T]
+    k_out, v_out = (torch.empty((T, H, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    return lambda: q.qkv_read(q.QKV_INT8_SIDE, kc, vc, k_out=k_out, v_out=v_out, slot_mapping=slots, k_scale=ks, v_scale=vs)
+
+
+def _masked(case: str):
+    fmt, seqs, rows, keys, Hq, H, D, block, cap = {
+        "masked_prompt": ("int8_side", 1, 4096, 4096, 16, 1, 256, 16, 30.0),
+        "masked_documents": ("bf16", 4, 2048, 2048, 32, 4, 128, 16, 0.0),
+        "masked_decode": ("e4m3", 64, 1, 8192, 64, 8, 128, 16, 50.0)}[case]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    wide = keys // block
+    S = seqs * wide * block
+    table = torch.randperm(seqs * wide, device="cuda", generator=gen).int().view(seqs, wide)
+    row_seq = torch.arange(seqs, device="cuda").int().repeat_interleave(rows)
+    row_end = torch.arange(1, rows + 1, device="cuda").int().repeat(seqs)
+    start = None
+    if case == "masked_documents":
+        start = (row_end - 1) // 256 * 256
+    if rows == 1:
+        row_end = torch.randint(1, keys + 1, (seqs,), device="cuda", generator=gen).int()
+    kw = {}
+    if fmt == "bf16":
+        kc, vc = (torch.randn((S, H, D), device="cuda", generator=gen).to(torch.bfloat16) for _ in "kv")
+    elif fmt == "e4m3":
+        kc, vc = (torch.randn((S, H, D), device="cuda", generator=gen).to(torch.float8_e4m3fn).view(torch.uint8)
+                  for _ in "kv")
+    else:
+        kc, vc = (torch.randint(-127, 128, (S, H, D), device="cuda", generator=gen, dtype=torch.int8) for _ in "kv")
+        kw = {n: torch.full((S, H), 0.02, device="cuda") for n in ("k_scale_tok", "v_scale_tok")}
+    qd = torch.randn((seqs * rows, Hq, D), device="cuda", generator=gen).to(torch.bfloat16)
+    out = torch.empty_like(qd)
+    ws = torch.empty(q.qkv_masked_attn_workspace(q.FORMATS[fmt], seqs * rows, seqs, Hq, H, D, keys), dtype=torch.uint8,
+                     device="cuda")
+    return lambda: q.qkv_masked_attn(qd, q.FORMATS[fmt], kc, vc, table, row_seq, row_end, block, D ** -0.5,
+                                     max_row_end=keys, num_kv_heads=H, row_start=start, softcap=cap, out=out, workspace=ws,
                                      **kw)
 
 
@@ -229,6 +296,12 @@ def build(case: str):
         return _append(case)
     if case in ("prefix_int8", "prefix_e4m3", "prefix_bf16", "dense_e4m3"):
         return _prefix(case)
+    if case == "append_axes":
+        return _append_axes()
+    if case == "read_int8":
+        return _read_int8()
+    if case in ("masked_prompt", "masked_documents", "masked_decode"):
+        return _masked(case)
     raise SystemExit(f"unknown case {case!r}; one of {', '.join(CASES)}")
 
 
