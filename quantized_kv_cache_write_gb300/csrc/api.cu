@@ -910,7 +910,7 @@ struct MaskedPlan {
   int64_t part_rows() const { return umma_cg > 0 ? 2 * static_cast<int64_t>(umma_teams) * umma_pairs : parts > 1 ? parts * rows_heads : 0; }
   size_t o_bytes() const { return static_cast<size_t>(part_rows()) * head_dim * 4; }
   size_t list_at() const { return o_bytes() + (static_cast<size_t>(part_rows()) * 4 + 31) / 32 * 32; }
-  size_t bytes() const { return list_at() + (umma_cg > 0 ? qkv::masked_plan_bytes(rows, tile_rows) : 0); }
+  size_t bytes() const { return list_at() + (umma_cg > 0 ? qkv::masked_plan_bytes(rows, tile_rows, umma_teams) : 0); }
 };
 
 qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
@@ -1080,7 +1080,7 @@ qkv_status qkv_masked_attn(const qkv_masked_desc* d, void* stream) {
     a.tile_rows = p.tile_rows;
     a.block_keys = p.block_keys;
     a.tile_cost = p.tile_cost;
-    a.plan_tiles_at = static_cast<int64_t>(qkv::masked_plan_tiles_at(d->rows, p.tile_rows));
+    a.plan_tiles_at = static_cast<int64_t>(qkv::masked_plan_tiles_at(d->rows, p.tile_rows, p.umma_teams));
     a.plan_chunks = qkv::masked_plan_chunks(d->rows, p.tile_rows);
     e = qkv::launch_masked_plan(a, s);
     if (e == cudaSuccess) e = launch_masked_umma(a, d->fmt, s);

@@ -95,30 +95,32 @@ __global__ void __launch_bounds__(kPlanThreads) masked_plan_kernel(const PrefixA
   }
 }
 
+// Four values of a part, or zeros; issued here, however late they are used.
+__device__ __forceinline__ float4 load_part(const float4* p, uint32_t there) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      " @p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
+      : "l"(p), "r"(there)
+      : "memory");
+  return v;
+}
+
 // A tile that teams share: its (row, head) pairs, one warp each, from the parts that the teams left.
 constexpr int kJoinWarps = 8;
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) masked_join_kernel(const PrefixArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   await_previous();
-  // the tile that team blockIdx.x begins and does not finish
-  const uint64_t work = plan_work(a);
-  const Shares s(work * a.num_kv_heads, a.umma_teams);
   const uint32_t team = blockIdx.x;
-  const uint64_t from = s.first(team), end = from + s.of(team);
-  if (end == from || end == work * a.num_kv_heads) return;
-  const int h = static_cast<int>((end - 1) / work);
-  const PlanPlace p = plan_find(a, end - 1 - h * work);
-  const MaskedTile t = plan_tiles(a, p.chunk)[p.tile];
-  const uint64_t begin = h * work + p.before + t.first, stop = h * work + p.before + plan_tiles(a, p.chunk)[p.tile + 1].first;
-  // its first block is another team's, or it is finished
-  if (begin + a.tile_cost < from || begin + a.tile_cost >= end || stop <= end) return;
-  uint32_t parts = 1;
-  for (uint64_t u = end; u < stop; ++parts) u += s.of(team + parts);
+  const int4 t = __ldcg(reinterpret_cast<const int4*>(plan_join(a, team)));
+  const int row0 = t.x, nrows = t.y, h = t.z;
+  const uint32_t parts = static_cast<uint32_t>(t.w);
   const int G = a.num_q_heads / a.num_kv_heads;
   const int flat = static_cast<int>(blockIdx.y) * kJoinWarps + warp;
-  if (flat >= t.nrows * G) return;
-  const int64_t row = t.row0 + flat / G, at = row * a.num_q_heads + h * G + flat % G;
+  if (parts == 0 || flat >= nrows * G) return;
+  const int64_t row = row0 + flat / G, at = row * a.num_q_heads + h * G + flat % G;
   // part i: place 1 of the team that begins, place 0 of those after it
   auto place = [&](uint32_t i) -> int64_t { return static_cast<int64_t>(i == 0 ? 2 * team + 1 : 2 * (team + i)) * a.umma_pairs + flat; };
   float m = -INFINITY;
@@ -138,22 +140,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) masked_join_kernel(const Pref
   float sum = 0.f;
   const bool any = m != -INFINITY || nan;
   const float ref = m == -INFINITY ? 0.f : m;
-  if (any) {
-#pragma unroll 4
-    for (uint32_t i = 0; i < parts; ++i) {
-      const float l = __ldcg(a.lse_part + place(i));
-      const bool none = l == -INFINITY;  // a part without keys wrote no values; one with keys counts, its values may be NaN
-      const float w = none ? 0.f : expf(l - ref);
-      sum += w;
-      const float4* src = reinterpret_cast<const float4*>(a.o_part + place(i) * HD);
+  // a part without keys wrote no values; one with keys counts, its values may be NaN. Eight parts' values are in flight at
+  // once
+  constexpr uint32_t kAtOnce = 8;
+  for (uint32_t i0 = 0; any && i0 < parts; i0 += 32) {
+    const float l = i0 + lane < parts ? __ldcg(a.lse_part + place(i0 + lane)) : -INFINITY;
+    const uint32_t some = __ballot_sync(0xffffffffu, l != -INFINITY);
+    const float w = l != -INFINITY ? expf(l - ref) : 0.f;
+    sum += w;
+    for (uint32_t i = 0; i < min(parts - i0, 32u); i += kAtOnce) {
+      float4 x[kAtOnce][kVec];
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!none) x = __ldcg(src + lane + 32 * v);
-        acc[v].x += w * x.x, acc[v].y += w * x.y, acc[v].z += w * x.z, acc[v].w += w * x.w;
+      for (uint32_t k = 0; k < kAtOnce; ++k) {
+        const float4* src = reinterpret_cast<const float4*>(a.o_part + place(i0 + i + k) * HD);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) x[k][v] = load_part(src + lane + 32 * v, (some >> (i + k)) & 1);
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < kAtOnce; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, i + k);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) acc[v].x += wk * x[k][v].x, acc[v].y += wk * x[k][v].y, acc[v].z += wk * x[k][v].z, acc[v].w += wk * x[k][v].w;
       }
     }
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   const float f = any ? a.merge_scale / sum : 0.f;
 #pragma unroll
   for (int v = 0; v < kVec; ++v)
@@ -184,11 +196,11 @@ cudaError_t launch_join(const PrefixArgs& a, cudaStream_t stream) {
 }  // namespace
 }  // namespace prefix
 
-size_t masked_plan_tiles_at(int64_t rows, int tile_rows) {
-  return (static_cast<size_t>(prefix::plan_chunks(rows, tile_rows)) * sizeof(prefix::MaskedChunk) + 31) / 32 * 32;
+size_t masked_plan_tiles_at(int64_t rows, int tile_rows, uint32_t teams) {
+  return (static_cast<size_t>(prefix::plan_chunks(rows, tile_rows)) * sizeof(prefix::MaskedChunk) + teams * sizeof(prefix::MaskedJoin) + 31) / 32 * 32;
 }
-size_t masked_plan_bytes(int64_t rows, int tile_rows) {
-  return masked_plan_tiles_at(rows, tile_rows) +
+size_t masked_plan_bytes(int64_t rows, int tile_rows, uint32_t teams) {
+  return masked_plan_tiles_at(rows, tile_rows, teams) +
          static_cast<size_t>(prefix::plan_chunks(rows, tile_rows)) * (prefix::kPlanThreads + 1) * sizeof(prefix::MaskedTile);
 }
 int masked_plan_chunks(int64_t rows, int tile_rows) { return static_cast<int>(prefix::plan_chunks(rows, tile_rows)); }

@@ -29,6 +29,12 @@ struct MaskedTile {
 struct MaskedChunk {
   uint32_t work, tiles;
 };
+// What the tile kernel leaves for the join, one for each team: the tile that it begins and does not finish, and the teams that
+// have a part of it (0: there is none).
+struct MaskedJoin {
+  int row0, nrows, h;
+  uint32_t parts;
+};
 __host__ __device__ inline int64_t plan_chunk_rows(int tile_rows) { return kPlanThreads / tile_rows * tile_rows; }
 __host__ __device__ inline int64_t plan_chunks(int64_t rows, int tile_rows) {
   return (rows + plan_chunk_rows(tile_rows) - 1) / plan_chunk_rows(tile_rows);
@@ -36,6 +42,10 @@ __host__ __device__ inline int64_t plan_chunks(int64_t rows, int tile_rows) {
 __device__ __forceinline__ const MaskedChunk* plan_chunk(const PrefixArgs& a) { return static_cast<const MaskedChunk*>(a.plan); }
 __device__ __forceinline__ const MaskedTile* plan_tiles(const PrefixArgs& a, int chunk) {
   return reinterpret_cast<const MaskedTile*>(static_cast<const uint8_t*>(a.plan) + a.plan_tiles_at) + static_cast<int64_t>(chunk) * (kPlanThreads + 1);
+}
+// The joins lie before the tiles.
+__device__ __forceinline__ MaskedJoin* plan_join(const PrefixArgs& a, uint32_t team) {
+  return reinterpret_cast<MaskedJoin*>(static_cast<uint8_t*>(a.plan) + a.plan_tiles_at) - a.umma_teams + team;
 }
 
 // The teams' shares: each of the first `extra` has one unit of work more.
@@ -57,11 +67,11 @@ __device__ __forceinline__ uint64_t plan_work(const PrefixArgs& a) {
 // The tile that holds unit `rem` of a KV head's work (0 <= rem < plan_work), and its place in it; the warp's lanes together.
 struct PlanPlace {
   int chunk, tile;
-  uint32_t into;     // units of the tile before
-  uint64_t before;   // units of the chunks before
+  uint32_t into;  // units of the tile before
 };
 __device__ __forceinline__ PlanPlace plan_find(const PrefixArgs& a, uint64_t rem) {
-  PlanPlace p = {0, 0, 0, 0};
+  PlanPlace p = {0, 0, 0};
+  uint64_t before = 0;  // units of the chunks before
   const int lane = threadIdx.x & 31;
   uint64_t base = 0;
   for (int c0 = 0; c0 < a.plan_chunks; c0 += 32) {
@@ -76,18 +86,19 @@ __device__ __forceinline__ PlanPlace plan_find(const PrefixArgs& a, uint64_t rem
     if (past != 0) {
       const int at = __ffs(past) - 1;
       p.chunk = c0 + at;
-      p.before = base + __shfl_sync(0xffffffffu, sum - own, at);
+      before = base + __shfl_sync(0xffffffffu, sum - own, at);
       break;
     }
     base += __shfl_sync(0xffffffffu, sum, 31);
   }
   const MaskedTile* tiles = plan_tiles(a, p.chunk);
-  const uint32_t in = static_cast<uint32_t>(rem - p.before);
-  int lo = 0, hi = static_cast<int>(plan_chunk(a)[p.chunk].tiles);  // the last tile that starts there or before
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tiles[mid].first <= in) lo = mid;
-    else hi = mid;
+  const uint32_t in = static_cast<uint32_t>(rem - before);
+  const int n = static_cast<int>(plan_chunk(a)[p.chunk].tiles);
+  // the last tile that starts there or before, in two steps of 32 (a chunk has at most 1024): ten dependent loads by halves
+  int lo = 0;
+  for (int step = 32; step > 0; step /= 32) {
+    const int at = lo + lane * step;
+    lo += step * (31 - __clz(__ballot_sync(0xffffffffu, at < n && tiles[min(at, n - 1)].first <= in)));
   }
   p.tile = lo;
   p.into = in - tiles[lo].first;
@@ -99,6 +110,7 @@ __device__ __forceinline__ PlanPlace plan_find(const PrefixArgs& a, uint64_t rem
 // cycles of loads per segment, and the instruction cache a copy.
 struct MaskedWalk {
   uint32_t left;    // work still to do
+  uint32_t share, extra;  // the teams' shares
   uint32_t skip;    // work of the next tile that a team before has
   int chunk, i, h;  // the next tile and its KV head
   uint32_t team;
@@ -107,12 +119,19 @@ struct MaskedWalk {
     const uint64_t work = plan_work(a);
     const Shares s(work * a.num_kv_heads, a.umma_teams);
     left = static_cast<uint32_t>(s.of(team));  // the host keeps a share below 2^32
+    share = static_cast<uint32_t>(s.share), extra = static_cast<uint32_t>(s.extra);
     skip = 0, chunk = 0, i = 0, h = 0;
     if (left == 0) return;
     const uint64_t u = s.first(team);
     h = static_cast<int>(u / work);
     const PlanPlace p = plan_find(a, u - h * work);
     chunk = p.chunk, i = p.tile, skip = p.into;
+  }
+  // how many of the teams after this one `rest` units of work go to
+  __device__ __forceinline__ uint32_t teams_of(uint32_t rest) const {
+    const uint32_t more = max(extra, team + 1) - (team + 1);  // of them have a unit more
+    const uint64_t theirs = static_cast<uint64_t>(more) * (share + 1);
+    return rest <= theirs ? (rest + share) / (share + 1) : more + (rest - static_cast<uint32_t>(theirs) + share - 1) / share;
   }
 };
 // A published segment, in shared memory: its first block and the last one's next (equal: there is none; blocks are numbered

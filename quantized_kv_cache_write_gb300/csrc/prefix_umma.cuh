@@ -664,10 +664,11 @@ struct Segments<true, U, CG> {
   __device__ __forceinline__ void done() const { release(count - 1); }
 };
 // The walk's next segment into the ring as number n, or the mark that there is none; whether there is one.
-template <int KB, typename U>
+template <int KB, int CG, typename U>
 __device__ __forceinline__ bool publish(const PrefixArgs& a, MaskedWalk& w, uint32_t sb, uint32_t n) {
   bool found = false;
   int b0 = 0, b1 = 0, part = -1, chunk = 0, i = 0, h = 0;
+  uint32_t rest = 0;  // of the tile's blocks, those of the teams after this one
   MaskedTile t = {};
   while (w.left != 0 && !found) {
     while (w.i >= static_cast<int>(plan_chunk(a)[w.chunk].tiles)) {  // there is work left, so there is a tile
@@ -684,6 +685,7 @@ __device__ __forceinline__ bool publish(const PrefixArgs& a, MaskedWalk& w, uint
     found = to > from;
     b0 = t.lo / KB + static_cast<int>(from), b1 = t.lo / KB + static_cast<int>(to);
     part = to - from == cost - extra ? -1 : static_cast<int>(2 * w.team + (from > 0 ? 0 : 1));
+    rest = cost - extra - to;
   }
   if (!found) b0 = b1 = 0, t.nrows = 0, t.row0 = 0;
   if (n >= kSegRing && !__all_sync(0xffffffffu, bar_wait(sb + U::kSegEmpty + 8 * (n % kSegRing), (n / kSegRing - 1) & 1, sb + U::kFlag)))
@@ -694,6 +696,9 @@ __device__ __forceinline__ bool publish(const PrefixArgs& a, MaskedWalk& w, uint
     sts128(at + 16, make_uint4(h, part, t.all_lo, t.all_hi));
     sts128(at + 32, make_uint4(chunk, i, 0, 0));
     bar_arrive(sb + U::kSegFull + 8 * (n % kSegRing));
+    // begun and not finished, the team's last segment: one SM notes it for the join
+    if (found && part == static_cast<int>(2 * w.team + 1) && blockIdx.x % CG == 0)
+      *reinterpret_cast<int4*>(plan_join(a, w.team)) = make_int4(t.row0, t.nrows, h, static_cast<int>(1 + w.teams_of(rest)));
   }
   __syncwarp();
   // its queries into L2, a segment ahead of their loads
@@ -1339,10 +1344,13 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
     uint32_t jb = 0;
     bool ok = true;
     [[maybe_unused]] MaskedWalk walk;
-    if constexpr (MASK) walk.begin(a, blockIdx.x / CG);
+    if constexpr (MASK) {
+      walk.begin(a, blockIdx.x / CG);
+      if (lane == 0 && rank == 0) *reinterpret_cast<int4*>(plan_join(a, walk.team)) = make_int4(0, 0, 0, 0);
+    }
     auto next_segment = [&]() -> bool {
       if constexpr (MASK) {
-        if (!publish<KB, U>(a, walk, sb, seg.count)) return false;
+        if (!publish<KB, CG, U>(a, walk, sb, seg.count)) return false;
         seg.take();
         return true;
       } else {

@@ -267,8 +267,8 @@ cudaError_t launch_prefix_umma_e4m3(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_masked_merge(const PrefixArgs& a, cudaStream_t stream);
 // the work list of the tcgen05 tiles, and the join of the tiles that teams share
-size_t masked_plan_bytes(int64_t rows, int tile_rows);
-size_t masked_plan_tiles_at(int64_t rows, int tile_rows);
+size_t masked_plan_bytes(int64_t rows, int tile_rows, uint32_t teams);
+size_t masked_plan_tiles_at(int64_t rows, int tile_rows, uint32_t teams);
 int masked_plan_chunks(int64_t rows, int tile_rows);
 cudaError_t launch_masked_plan(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_masked_join(const PrefixArgs& a, cudaStream_t stream);
