@@ -920,14 +920,17 @@ qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, in
 }
 
 // Where a masked call runs on tcgen05 tiles: a sequence brings at least this many pairs on average, and tiles of 16
-// pairs would read at least so many bytes of keys and values, most of them from L2 (a tcgen05 call costs some 16 us more at its
-// ends). In us, mma.sync | tcgen05: 16 heads of 256, int8: 8 sequences x 5 rows behind 1000 keys (20 MB) 24 | 38, behind
-// 8000 (164 MB) 72 | 53; 64 x 4 behind 1000 (131 MB) 54 | 49; 4 x 16 behind 1000 (33 MB) 25 | 38, behind 8000 96 | 51. 8
-// heads of 128 in groups of 8, e4m3: 8 x 5 behind 1000 (49 MB) 26 | 41, behind 8000 (393 MB) 109 | 90; 64 x 4 behind
-// 8000 420 | 395; 64 x 1 behind 8000 209 | 389. Groups of 4: 64 x 4 behind 8000 (16 pairs) 269 | 391.
+// pairs would read at least so many bytes of keys and values, most of them from L2 (a tcgen05 call costs some 8 us more at its
+// ends). In us, mma.sync | tcgen05: 16 heads of 256, int8: 8 sequences x 5 rows behind 1000 keys (20 MB) 23 | 32, behind
+// 4000 (78 MB) 46 | 38, behind 8000 71 | 43; 64 x 4 behind 500 (62 MB) 29 | 40, behind 1000 54 | 46; 4 x 16 behind 2000
+// (62 MB) 32 | 39, behind 4000 54 | 39. 64 heads of 128 in groups of 8, e4m3: 8 x 5 behind 1000 (39 MB) 25 | 32, behind
+// 2000 (78 MB) 42 | 40, behind 8000 109 | 74; 64 x 4 (32 pairs) behind 1000 97 | 100, behind 8000 420 | 384; 64 x 2
+// behind 4000 (16 pairs, 500 MB) 152 | 217. Groups of 4: 64 x 4 behind 8000 (16 pairs, 2 GB) 360 | 391.
 constexpr int64_t kMaskedUmmaPairs = 32;
-constexpr int64_t kMaskedUmmaBytes = 100 << 20;
-// What a tile costs besides its key blocks, in blocks.
+constexpr int64_t kMaskedUmmaBytes = 64 << 20;
+// What a tile costs besides its key blocks, in blocks: with 0 | 3 | 6 | 12 of them prompts of documents of about 700 bf16
+// rows took 278 | 248 | 252 | 256 us, three prompts of 77 to 1501 rows under a prefix mask 134 | 125 | 116 | 119, 2048 rows
+// behind 8000 int8 keys 323 | 324 | 320 | 325.
 constexpr int kMaskedTileCost = 6;
 
 qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
@@ -950,6 +953,9 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   // Test of each kind of tiles at any size: QKV_TEST_MASKED_TILES=tcgen05 or mma (read at each call; unset in any other use).
   if (const char* t = std::getenv("QKV_TEST_MASKED_TILES")) umma = std::strcmp(t, "tcgen05") == 0 || (umma && std::strcmp(t, "mma") != 0);
   if (umma && max_row_end <= (1 << 27) && num_kv_heads <= 0xffff) {
+    // Tiles of 256 pairs on a pair of SMs where a sequence has more than one of 128. In us, 128 | 256: 16 sequences x 18
+    // rows x 64 heads of 128 in groups of 8 behind 8000 bf16 keys (144 pairs) 217 | 172, 16 rows each (128) 140 | 176; 16 x
+    // 150 rows x 8 heads of 256, each its own group, 157 | 120, 100 rows each 159 | 170.
     p->umma_cg = pairs > 128 ? 2 : 1;
     p->umma_pairs = 128 * p->umma_cg;
     p->tile_rows = p->umma_pairs / G;

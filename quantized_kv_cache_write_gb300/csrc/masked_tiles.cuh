@@ -1,6 +1,6 @@
-// The work list of qkv_masked_attn's tcgen05 tiles. A tile is up to tile_rows consecutive rows of one sequence (cut at
-// multiples of tile_rows, where the sequence changes, and between rows whose ranges lie apart) and the key blocks that any of
-// them sees. A KV head's work is its tiles' costs: a tile's blocks, and tile_cost more for what it costs besides them (its
+// The work list of qkv_masked_attn's tcgen05 tiles. A tile is up to tile_rows consecutive rows of one sequence (cut every
+// tile_rows rows from where the sequence changes or a row's range lies apart from that of the row before) and the key blocks
+// that any of them sees. A KV head's work is its tiles' costs: a tile's blocks, and tile_cost more for what it costs besides them (its
 // queries, its first and last products, its output). The kernel that makes the list runs first, a block for each chunk of
 // rows; the teams of the tile kernel then each take an equal contiguous share of all heads' work, so that causal, ragged and
 // windowed rows balance without the host knowing them. A tile that one team has whole is written out by it; of one that
@@ -15,7 +15,7 @@
 namespace qkv {
 namespace prefix {
 
-constexpr int kPlanThreads = 1024;  // rows of a chunk, at most: whole groups of tile_rows
+constexpr int kPlanThreads = 1024;  // rows of a chunk, at most: a multiple of tile_rows
 
 struct MaskedTile {
   uint32_t first;      // its work within its chunk
