@@ -82,7 +82,10 @@ struct Umma {
   static constexpr uint32_t kTab = kRow + 2 * kParts * 4 * kTileM, kAll = kTab + (MASK ? NT * kTileM * 16 : 0);
   static constexpr uint32_t kSeg = kAll + (MASK ? NT * kSoftWarps * 8 : 0);  // the published segments
   static constexpr uint32_t kOdd = kSeg + (MASK ? 4 * kSegWords * kSegRing : 0);
-  static constexpr uint32_t kSegFull = kOdd + (MASK ? 16 : 0), kSegEmpty = kSegFull + (MASK ? 8 * kSegRing : 0);
+  // each softmax warp's place for a tile's output on its way out: 32 rows of 64 B, of 32 B where there is no room for those
+  static constexpr uint32_t kOut = kOdd + (MASK ? 16 : 0);
+  static constexpr uint32_t kOutRow = kOut + kSoftWarps * 32 * 64 + 2048 <= 232448 ? 64 : 32;
+  static constexpr uint32_t kSegFull = kOut + (MASK ? kSoftWarps * 32 * kOutRow : 0), kSegEmpty = kSegFull + (MASK ? 8 * kSegRing : 0);
   static constexpr uint32_t kBar = kSegEmpty + (MASK ? 8 * kSegRing : 0);
   static constexpr uint32_t kFull = kBar, kEmpty = kFull + 8 * kSlots, kSFull = kEmpty + 8 * kSlots, kPFull = kSFull + 16,
                             kPvDone = kPFull + 16, kScFull = kPvDone + 16, kScEmpty = kScFull + 8 * kScRing,
@@ -850,11 +853,13 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         else v[i] = there ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kVec) : make_uint4(0, 0, 0, 0);
       }
     };
-    bool more = true, begun = false;
-    // MASK: what a segment needs from global memory, asked for while the one before ends (if there is none: nothing)
+    bool begun = false;
+    [[maybe_unused]] float next_fac = 0.f;  // MASK: the next segment's factor, and whether the warp has pairs of it
+    [[maybe_unused]] bool next_in = false;
+    // MASK: what a segment needs from global memory
     auto fetch = [&]() {
       if constexpr (MASK) {
-        h = seg.word(kSegHead), row0 = seg.word(kSegRow0), flats = more ? static_cast<uint32_t>(seg.word(kSegRows) * G) : 0;
+        h = seg.word(kSegHead), row0 = seg.word(kSegRow0), flats = static_cast<uint32_t>(seg.word(kSegRows) * G);
         load_query(mask_flat, asked);
         range = RowRange{kPadRow, 0, 0, 0, 0}, slope = 0.f;
         if (mask_flat < flats) {
@@ -880,6 +885,82 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         const bool w = warp_in[0];
         warp_in[0] = warp_in[NT - 1], warp_in[NT - 1] = w;
       }
+    };
+    // the pairs' query rows into tile t (bytes pools: fp16, pre-scaled by a power of two), a part of the dims by each of a
+    // row's threads; and the factor from products to log2 units
+    auto put_queries = [&](int t, uint32_t flat, float& factor) -> bool {
+      const uint32_t part = own_part + t * U::kQTile;
+      uint4 v[kVec];
+      if (!MASK) load_query(flat, v);
+#pragma unroll
+      for (int i = 0; MASK && i < kVec; ++i) v[i] = asked[MASK ? i : 0];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int rr = 32 / kVec * i + lane / kVec;
+        if (!F::kBytes && sign < 0.f) v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
+        sts128(part + rr * 128 + (((c0 + lane % kVec) ^ (rr & 7)) << 4), v[i]);
+      }
+      float fc = fabsf(a.softmax_scale) * (MODE == kAdjusted && a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
+      if (F::kBytes) {
+        __syncwarp();
+        uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          v[i] = lds128(part + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4));
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+        }
+        float all[kParts];
+        if (!exchange(__uint_as_float(mb), all)) return false;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) mb = max(mb, __float_as_uint(all[i]));
+        const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
+        int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
+        e = max(-112, min(126, e));
+        const float up = sign * pow2f(e);
+        fc *= pow2f(-e);
+        if (FMT == QKV_E4M3) fc *= a.k_scale_layer;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
+            x[2 * k] = f.x * up;
+            x[2 * k + 1] = f.y * up;
+          }
+          // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
+          v[i] = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
+                          : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+          sts128(part + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4), v[i]);
+        }
+      }
+      factor = fmaxf(fc, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
+      return true;
+    };
+    auto queries_there = [&]() {
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
+    };
+    // MASK: a chunk of 16 B of a row in the warp's place for output (eight rows' same chunk, and eight chunks in a row, are in
+    // different banks), and what the warp stored there to its rows' `to` (-1: nowhere)
+    constexpr int kOutChunks = U::kOutRow / 16, kOutTurn = 8 / kOutChunks;
+    auto out_chunk = [&](int row, int c) -> uint32_t {
+      return sb + U::kOut + (32 * warp + row) * U::kOutRow + ((c ^ ((row / kOutTurn) & (kOutChunks - 1))) << 4);
+    };
+    auto write_rows = [&](int to, auto write) {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kOutChunks; ++k) {
+        const int rr = 32 / kOutChunks * k + lane / kOutChunks;
+        const int rr_to = __shfl_sync(0xffffffffu, to, rr);
+        const uint4 x = lds128(out_chunk(rr, lane % kOutChunks));
+        if (rr_to >= 0) write(rr_to, lane % kOutChunks, x);
+      }
+      __syncwarp();
     };
     // ---- the segment's partial results, or (MASK) the output of a tile that is the team's own
     auto finish = [&](int out_h, int out_row0, uint32_t out_flats, int out_part, const Odd& odd) {
@@ -911,14 +992,14 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
               }
               a.lse[at] = any ? (R[0] + log2f(sum)) * kLn2 + far : -INFINITY;
             }
-            // 32 rows x 32 dims at a time, rounded, through the warp's place in the query tile: four lanes write 64 B of a
-            // row. A thread that writes its own row touches a line of its own with each store: 3300 cycles a tile, not 1000.
+            // 32 rows x 16 or 32 dims at a time, rounded, through the warp's own place: two or four lanes write 32 or 64 B of
+            // a row. A thread that writes its own row touches a line of its own with each store: 3300 cycles a tile, not 1000.
             inv = any ? inv * a.merge_scale : 0.f;
             const int to = in ? at : -1;
 #pragma unroll 1
-            for (int c = 0; c < HD / kParts; c += 32) {
+            for (int c = 0; c < HD / kParts; c += 8 * kOutChunks) {
 #pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
+              for (int half = 0; half < kOutChunks / 2; ++half) {
                 float o[16];
                 tmem_load(tl + U::kO + d0 + c + 16 * half, o);
                 tmem_loaded(o);
@@ -931,18 +1012,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
                   for (int n = 0; n < 4; ++n) z[n] = any ? z[n] * inv : 0.f;
                   w[2 * k] = round2(a.q_f16, z[0], z[1]), w[2 * k + 1] = round2(a.q_f16, z[2], z[3]);
                 }
-                sts128(own_part + lane * 128 + (((c0 + 2 * half) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-                sts128(own_part + lane * 128 + (((c0 + 2 * half + 1) ^ (lane & 7)) << 4), make_uint4(w[4], w[5], w[6], w[7]));
+                sts128(out_chunk(lane, 2 * half), make_uint4(w[0], w[1], w[2], w[3]));
+                sts128(out_chunk(lane, 2 * half + 1), make_uint4(w[4], w[5], w[6], w[7]));
               }
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int rr = 8 * k + (lane >> 3) + (lane & 4);
-                const int rr_to = __shfl_sync(0xffffffffu, to, rr);
-                const uint4 x = lds128(own_part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
-                if (rr_to >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(rr_to) * HD + d0 + c + 8 * (lane & 3)) = x;
-              }
-              __syncwarp();
+              write_rows(to, [&](int row_to, int ch, const uint4& x) {
+                *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row_to) * HD + d0 + c + 8 * ch) = x;
+              });
             }
             continue;
           }
@@ -959,14 +1034,25 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           float o[16];
           tmem_load(tl + U::kO + t * HD + d0 + c, o);
           tmem_loaded(o);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          auto four = [&](int k) {
             // int8: the producers store dims 0, 2, 1, 3 of each four
             const float x1 = F::kInt8 ? o[4 * k + 2] : o[4 * k + 1], x2 = F::kInt8 ? o[4 * k + 1] : o[4 * k + 2];
-            sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4),
-                   make_uint4(__float_as_uint(o[4 * k] * inv), __float_as_uint(x1 * inv), __float_as_uint(x2 * inv),
-                              __float_as_uint(o[4 * k + 3] * inv)));
+            return make_uint4(__float_as_uint(o[4 * k] * inv), __float_as_uint(x1 * inv), __float_as_uint(x2 * inv),
+                              __float_as_uint(o[4 * k + 3] * inv));
+          };
+          if constexpr (MASK) {
+#pragma unroll
+            for (int k0 = 0; k0 < 4; k0 += kOutChunks) {
+#pragma unroll
+              for (int k = 0; k < kOutChunks; ++k) sts128(out_chunk(lane, k), four(k0 + k));
+              write_rows(to, [&](int row_to, int ch, const uint4& x) {
+                *reinterpret_cast<uint4*>(a.o_part + (part_at + row_to) * HD + d0 + c + 4 * (k0 + ch)) = x;
+              });
+            }
+            continue;
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4), four(k));
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -987,12 +1073,22 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         Odd odd = {};
         if (!F::kInt8 && begun)
           odd = Odd{plan_tiles(a, seg.word(kSegChunk)) + seg.word(kSegTile), seg.b0, seg.b1, sb + U::kOdd, sb + U::kTab + 16 * r};
-        more = ok && seg.next(a);
+        const bool more = ok && seg.next(a);
         if (seg.lost) ok = false;
-        if (seg.count > 0) fetch();
-        if (begun) finish(out_h, out_row0, out_flats, out_part, odd);
-        if (vote(!ok)) break;
-        if (begun) seg.release(used);
+        if (vote(!ok)) break;  // from here on the row's threads do the same
+        // the next segment's queries first, so that its first products run under the output of the one before: prompts of
+        // documents of about 700 bf16 rows 243 -> 0 us
+        if (more) {
+          fetch();
+          next_in = __any_sync(0xffffffffu, mask_flat < flats);
+          if (!put_queries(0, mask_flat, next_fac)) break;
+          queries_there();
+        }
+        if (begun) {
+          finish(out_h, out_row0, out_flats, out_part, odd);
+          if (vote(!ok)) break;
+          seg.release(used);
+        }
         if (!more) break;
         begun = true;
         // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see
@@ -1011,66 +1107,18 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
       for (int i = 0; i < 2; ++i) M[i] = -INFINITY, R[i] = 0.f, l[i] = 0.f, E[i] = F::kInt8 ? -90 : 0;
 #pragma unroll
       for (int i = 0; i < NT; ++i) fac[i] = 0.f, warp_in[i] = false;
-      // ---- the pairs' query rows into the tiles (bytes pools: fp16, pre-scaled by a power of two), a part of the
-      // dims by each of a row's threads
+      if constexpr (!MASK) {
 #pragma unroll 1
-      for (int t = 0; t < NT; ++t, other_tile()) {
-        const uint32_t flat = flat0 + t * CG * kTileM;
-        warp_in[0] = __any_sync(0xffffffffu, flat < flats);
-        const uint32_t part = own_part + t * U::kQTile;
-        uint4 v[kVec];
-        if (!MASK) load_query(flat, v);
-#pragma unroll
-        for (int i = 0; MASK && i < kVec; ++i) v[i] = asked[MASK ? i : 0];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const int rr = 32 / kVec * i + lane / kVec;
-          if (!F::kBytes && sign < 0.f) v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
-          sts128(part + rr * 128 + (((c0 + lane % kVec) ^ (rr & 7)) << 4), v[i]);
+        for (int t = 0; t < NT; ++t, other_tile()) {
+          const uint32_t flat = flat0 + t * CG * kTileM;
+          warp_in[0] = __any_sync(0xffffffffu, flat < flats);
+          if (!put_queries(t, flat, fac[0])) break;
         }
-        float fc = fabsf(a.softmax_scale) * (MODE == kAdjusted && a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
-        if (F::kBytes) {
-          __syncwarp();
-          uint32_t mb = 0;  // largest magnitude, as bits of the 16-bit type (magnitudes order like their bits)
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            v[i] = lds128(part + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4));
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mb = max(mb, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-          }
-          float all[kParts];
-          if (!exchange(__uint_as_float(mb), all)) break;
-#pragma unroll
-          for (int i = 0; i < kParts; ++i) mb = max(mb, __float_as_uint(all[i]));
-          const float m = a.q_f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mb))) : __uint_as_float(mb << 16);
-          int e = m > 0.f ? 14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127) : 0;
-          e = max(-112, min(126, e));
-          const float up = sign * pow2f(e);
-          fc *= pow2f(-e);
-          if (FMT == QKV_E4M3) fc *= a.k_scale_layer;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16lo(w[k]), bf16hi(w[k]));
-              x[2 * k] = f.x * up;
-              x[2 * k + 1] = f.y * up;
-            }
-            // int8: dims (0, 2), (1, 3) of each four, the order in which the producers store K
-            v[i] = F::kInt8 ? make_uint4(pack_half2(x[0], x[2]), pack_half2(x[1], x[3]), pack_half2(x[4], x[6]), pack_half2(x[5], x[7]))
-                            : make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
-            sts128(part + lane * 128 + (((c0 + i) ^ (lane & 7)) << 4), v[i]);
-          }
-        }
-        fac[0] = fmaxf(fc, 1e-37f);  // a scale of 0: a missing key's -inf stays -inf
+        if (!ok) break;
+        queries_there();
+      } else {
+        fac[0] = next_fac, warp_in[0] = next_in;
       }
-      if (!ok) break;
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) lead_arrive<CG>(sb + U::kQFull);
 
       int from = MASK ? (seg.b1 - 1) * KB : 0;  // MASK: the block's first position
       const uint32_t end = (jb + (seg.b1 - seg.b0)) * NT;
