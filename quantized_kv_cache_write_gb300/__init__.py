@@ -726,7 +726,7 @@ def _axes(axis_pos, pair_axis, rot: int, T: int):
     app = _plain("axis_pos", axis_pos, _int32, shape[0] * T)
     if pair_axis is None:
         return app, shape[0], 0, None
-    held = bytearray(pair_axis)  # a value that is no byte: ValueError
+    held = bytearray(iter(pair_axis))  # a value that is no byte: ValueError; one number is no sequence: TypeError
     if len(held) != rot // 2 or not held:
         raise ValueError(f"pair_axis must hold an axis for each of the {rot // 2} pairs, got {len(held)}")
     return app, shape[0], ctypes.addressof(ctypes.c_char.from_buffer(held)), held
@@ -795,6 +795,8 @@ def qkv_read(fmt: int, k_cache, v_cache, *, k_out=None, v_out=None, slot_mapping
     held = None
     if (cos_sin is None) != (axis_pos is None):
         raise ValueError("cos_sin and axis_pos come together")
+    if cos_sin is None and pair_axis is not None:
+        raise ValueError("pair_axis without cos_sin: nothing is turned back")
     if cos_sin is not None:
         if len(cos_sin.shape) != 2:
             raise ValueError("cos_sin must be [positions, rotary_dim]")

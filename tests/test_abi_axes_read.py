@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 
+import numpy as np
 import pytest
 import torch
 
@@ -155,6 +156,19 @@ def test_read_binding_refuses(lib, change, match):  # noqa: F811
     kw.update(change)
     with pytest.raises(ValueError, match=match):
         lib.qkv_read(kw.pop("fmt"), kw.pop("k_cache"), kw.pop("v_cache"), **kw)
+
+
+def test_pair_axis_is_a_sequence_and_needs_angles(lib):  # noqa: F811
+    axis_pos = torch.zeros((3, 4), dtype=torch.int32)
+    with pytest.raises(TypeError):
+        lib._axes(axis_pos, 32, 64, 4)  # a number of pairs is no list of axes
+    want = bytes([i % 3 for i in range(32)])
+    for given in (list(want), want, torch.tensor(list(want)), np.array(list(want))):
+        assert bytes(lib._axes(axis_pos, given, 64, 4)[3]) == want
+    with pytest.raises(ValueError, match="pair_axis"):
+        lib.qkv_read(1, torch.zeros((9, 2, 128), dtype=torch.int8), torch.zeros((9, 2, 128), dtype=torch.int8),
+                     k_out=torch.zeros((4, 2, 128)), slot_mapping=torch.zeros(4, dtype=torch.int64), k_scale=torch.zeros((9, 2)),
+                     v_scale=torch.zeros((9, 2)), pair_axis=[0] * 32)
 
 
 def header_fields(name):
