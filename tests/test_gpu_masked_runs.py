@@ -74,3 +74,18 @@ def test_prompts_by_the_rule(fmt, act, H, G, D, mask, window, cap):
     rows = chunk_rows(lengths, new, mask, doc=311)
     pick = np.unique(np.concatenate([rng.integers(0, len(rows), 120), [0, 1, 2002, 2003, len(rows) - 1]]))
     _sampled(fmt, act, rng, seqs, pool, rows, H, G, D, pick, window=window, softcap=cap)
+
+
+@pytest.mark.parametrize("tiles", ["mma", "tcgen05"])
+@pytest.mark.parametrize("fmt,act,G,D", [("int8_side", "bf16", 16, 256), ("bf16", "bf16", 8, 128)])
+@pytest.mark.parametrize("new", [1, 50])
+def test_slopes_of_either_sign_and_any_size(monkeypatch, tiles, fmt, act, G, D, new):
+    """A negative slope prefers far keys, a large one leaves the nearest (or the farthest) alone."""
+    monkeypatch.setenv("QKV_TEST_MASKED_TILES", tiles)
+    rng = np.random.default_rng(G + new)
+    seqs = Seqs(rng, [700, 333], 16)
+    pool = Pool(rng, fmt, act, seqs.live, seqs.num_slots, 1, D)
+    rows = chunk_rows([700, 333], [new, new])
+    rows[::3, 3] = 350  # in the middle of what these rows see
+    slopes = np.resize([0.0, -0.01, 0.5, -0.5, 300.0, -300.0, 1e-6, 0.03], G)
+    check(pool, fmt, act, query(rng, len(rows), G, D, act), seqs, rows, 1, D ** -0.5, slopes=slopes, softcap=20.0)
