@@ -247,6 +247,11 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+template <typename T>
+__device__ __forceinline__ void swap_places(T& a, T& b) {
+  const T x = a;
+  a = b, b = x;
+}
 // N columns times their scales; N columns whose key is missing to -inf.
 template <int N>
 __device__ __forceinline__ void scale_by(float (&v)[N], const float4* src) {
@@ -874,16 +879,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
     int E[2];
     bool warp_in[NT];
     auto other_tile = [&]() {
-      if (NT == 2) {
-        float x;
-        x = M[0], M[0] = M[1], M[1] = x;
-        x = R[0], R[0] = R[1], R[1] = x;
-        x = l[0], l[0] = l[1], l[1] = x;
-        x = fac[0], fac[0] = fac[NT - 1], fac[NT - 1] = x;
-        const int e = E[0];
-        E[0] = E[1], E[1] = e;
-        const bool w = warp_in[0];
-        warp_in[0] = warp_in[NT - 1], warp_in[NT - 1] = w;
+      if constexpr (NT == 2) {
+        swap_places(M[0], M[1]), swap_places(R[0], R[1]), swap_places(l[0], l[1]), swap_places(E[0], E[1]);
+        swap_places(fac[0], fac[NT - 1]), swap_places(warp_in[0], warp_in[NT - 1]);
       }
     };
     // A value as if it were new, so that what a tile's ends compute from it does not stay in registers through the block
@@ -1032,7 +1030,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         }
         if (in && wg == 0) a.lse_part[part_at + at] = any ? (R[0] + log2f(sum)) * kLn2 : -INFINITY;
         // 32 rows x 16 dims at a time through the warp's place in the query tile, which the segment no longer
-        // needs: four lanes write 64 B of a row
+        // needs (MASK: the warp's own place): four lanes write 64 B of a row
         const int to = in && any ? at : -1;
         const uint32_t part = own_part + t * U::kQTile;
 #pragma unroll 1
@@ -1055,27 +1053,33 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
                 *reinterpret_cast<uint4*>(a.o_part + (part_at + row_to) * HD + d0 + c + 4 * (k0 + ch)) = x;
               });
             }
-            continue;
-          }
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4), four(k));
-          __syncwarp();
+            for (int k = 0; k < 4; ++k) sts128(part + lane * 128 + (((c0 + k) ^ (lane & 7)) << 4), four(k));
+            __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = 8 * k + (lane >> 3) + (lane & 4);
-            const int rr_to = __shfl_sync(0xffffffffu, to, rr);
-            const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
-            if (rr_to >= 0) *reinterpret_cast<uint4*>(a.o_part + (part_at + rr_to) * HD + d0 + c + 4 * (lane & 3)) = x;
+            for (int k = 0; k < 4; ++k) {
+              const int rr = 8 * k + (lane >> 3) + (lane & 4);
+              const int rr_to = __shfl_sync(0xffffffffu, to, rr);
+              const uint4 x = lds128(part + rr * 128 + (((c0 + (lane & 3)) ^ (rr & 7)) << 4));
+              if (rr_to >= 0) *reinterpret_cast<uint4*>(a.o_part + (part_at + rr_to) * HD + d0 + c + 4 * (lane & 3)) = x;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       tmem_fence_before_sync();  // ordered before the next segment's first arrival
     };
     while (true) {
       if constexpr (MASK) {
-        const int out_h = h, out_row0 = row0, out_part = begun ? seg.word(kSegPart) : 0;
-        const uint32_t out_flats = flats, used = seg.count - 1;
+        // the segment at hand, whose words stay until it is released
+        int out_h = 0, out_row0 = 0, out_part = 0;
+        uint32_t out_flats = 0;
+        const uint32_t used = seg.count - 1;
+        if (begun) {
+          out_h = seg.word(kSegHead), out_row0 = seg.word(kSegRow0), out_part = seg.word(kSegPart);
+          out_flats = static_cast<uint32_t>(seg.word(kSegRows) * G);
+        }
         Odd odd = {};
         if (!F::kInt8 && begun)
           odd = Odd{plan_tiles(a, seg.word(kSegChunk)) + seg.word(kSegTile), seg.b0, seg.b1, sb + U::kOdd, sb + U::kTab + 16 * r};
@@ -1162,7 +1166,9 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           tmem_load(ts, x);
           tmem_loaded(x);
           if (F::kInt8) {
-            if (MASK) scale_by(x, sc + 4 * wg * HB);
+            // the compiler may ask for the scales early where it has registers for them: 2048 rows x 16 heads of 256 behind
+            // 30000 keys 964 us, 1015 with every load at its place; capped, 4096 causal rows, 237 and 235
+            if (MODE == kAdjusted) scale_by(x, sc + 4 * wg * HB);
             else scale_by(x, ksp);
           }
           float fc = fac[0];
@@ -1228,7 +1234,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
             sum[(k >> 1) & 3] = f2add(sum[(k >> 1) & 3], f2pack(x[k], x[k + 1]));
           }
           if (F::kInt8) {
-            if (MASK) scale_by(x, sc + U::kScVs + 4 * wg * HB);
+            if (MODE == kAdjusted) scale_by(x, sc + U::kScVs + 4 * wg * HB);
             else scale_by(x, vsp);  // a missing key's scale is 0
             if (MASK && !whole) {
 #pragma unroll
