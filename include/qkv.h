@@ -842,7 +842,11 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* desc, void* stream);
  *   Numbers: as for qkv_prefix_attn. A capped score is off by up to 2^-19 of itself besides. The bias
  *   counts from the seen key that is nearest to p (only differences matter to the weights), so that a row far from its keys
  *   loses no bits; a key at distance d from that one has a score off by up to 2^-23 slopes[g] d. A value that is not finite
- *   in a key that a row does not see leaves that row as it was.
+ *   in a key that a row does not see leaves that row as it was. In one that it sees: a NaN in K (or in an int8 key's scale)
+ *   makes the row's out and lse NaN for the KV head's query heads, and so does a score of +infinity; one of -infinity gives the
+ *   key no weight; under a cap they are softcap and -softcap. (An int8 key's scale multiplies the sum of its codes' products
+ *   with the query: an infinite one leaves that sum's sign.) In V it shows in its own dim (an int8 scale: in every dim), as it
+ *   is or as NaN, and lse does not know of it.
  * Results do not depend on other rows of the batch, up to rounding; calls with the same arguments on the same device give the
  * same bits.
  *
