@@ -841,7 +841,8 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* desc, void* stream);
  *   Limits as for qkv_prefix_attn: rows * num_q_heads and num_slots * num_kv_heads at most 2^31 - 1.
  *   Numbers: as for qkv_prefix_attn. A capped score is off by up to 2^-19 of itself besides. The bias
  *   counts from the seen key that is nearest to p (only differences matter to the weights), so that a row far from its keys
- *   loses no bits; a key at distance d from that one has a score off by up to 2^-23 slopes[g] d. A value that is not finite
+ *   loses no bits; a key at distance d from that one has a score off by up to 2^-21 |slopes[g]| max(d, 32) (the slope in
+ *   log2 units, its product, the sum over a block's columns and the score's own rounding). A value that is not finite
  *   in a key that a row does not see leaves that row as it was. In one that it sees: a NaN in K (or in an int8 key's scale)
  *   makes the row's out and lse NaN for the KV head's query heads, and so does a score of +infinity; one of -infinity gives the
  *   key no weight; under a cap they are softcap and -softcap. (An int8 key's scale multiplies the sum of its codes' products
