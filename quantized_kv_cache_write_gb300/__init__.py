@@ -905,7 +905,8 @@ def qkv_masked_attn(q, fmt: int, k_cache, v_cache, block_table, row_seq, row_end
 
     q bf16 or fp16 [R, Hq, D]; row r is a token of sequence row_seq[r] (int32 [R], -1 padding) and sees
     positions row_start[r] (None: 0) .. row_end[r] - 1, with a window only those less than `window`
-    before row_pos[r] (None: row_end - 1); slopes fp32 [Hq]; block_table int32 [num_seqs, max_blocks].
+    before row_pos[r] (None: row_end - 1); slopes fp32 [Hq]; block_table int32 [num_seqs, max_blocks],
+    cut to the batch's sequences (rows / num_seqs chooses the tiles).
     out is [R, Hq, D] in q's type; workspace any contiguous tensor of at least
     qkv_masked_attn_workspace bytes.
     """

@@ -922,7 +922,8 @@ qkv_status check_masked_shape(qkv_format fmt, int64_t rows, int64_t num_seqs, in
   return check_prefix_shape(fmt, rows, num_q_heads, num_kv_heads, head_dim, 0, max_row_end);
 }
 
-// Where a masked call runs on tcgen05 tiles: a sequence brings at least this many pairs on average, and tiles of 16
+// Where a masked call runs on tcgen05 tiles: a sequence brings at least this many pairs on average (over the table's
+// sequences, or the rows if those are fewer: where the rows lie is known on the device alone), and tiles of 16
 // pairs would read at least so many bytes of keys and values, most of them from L2 (a tcgen05 call costs some 8 us more at its
 // ends). In us, mma.sync | tcgen05: 16 heads of 256, int8: 8 sequences x 5 rows behind 1000 keys (20 MB) 23 | 32, behind
 // 4000 (78 MB) 46 | 38, behind 8000 71 | 43; 64 x 4 behind 500 (62 MB) 29 | 40, behind 1000 54 | 46; 4 x 16 behind 2000
@@ -941,6 +942,8 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   const int sms = sm_count();
   if (sms < 1) return QKV_ERR_CUDA;
   const int G = num_q_heads / num_kv_heads;
+  // The sequences that have rows, as far as the host knows: the table may hold more, but no more than there are rows.
+  const int64_t seqs = rows < num_seqs ? (rows > 0 ? rows : 1) : num_seqs;
   p->rows_heads = rows * num_q_heads;
   p->head_dim = head_dim;
   p->tiles = rows * ceil_div(G, 16) * num_kv_heads;
@@ -951,10 +954,10 @@ qkv_status plan_masked(qkv_format fmt, int64_t rows, int64_t num_seqs, int num_q
   // even out), are cut down to one. 1 row x 4 heads of 128 behind 60000 e4m3 keys in 118 parts 31 us, in 102 24; 8 heads: 48,
   // in 51 35; 3 rows x 16 heads of 256, int8: 52, in 91 39.
   const int64_t wave = 9 * resident_slots(row_bytes_of(fmt, head_dim), sms) / 10, ctas = p->tiles * p->parts;
-  if (ctas > wave && (ctas < 2 * wave || num_seqs == 1) && p->tiles < wave) p->parts = static_cast<int>(wave / p->tiles);
+  if (ctas > wave && (ctas < 2 * wave || seqs == 1) && p->tiles < wave) p->parts = static_cast<int>(wave / p->tiles);
   p->rows = rows;
   p->umma_cg = 0, p->umma_pairs = 0, p->tile_rows = 0, p->block_keys = 0, p->tile_cost = 0, p->umma_teams = 0;
-  const int64_t pairs = rows * G / num_seqs;  // of a sequence
+  const int64_t pairs = rows * G / seqs;  // of a sequence, on average
   const int64_t tiles16 = ceil_div(rows * G, 16) * num_kv_heads;
   const bool large = keys > 0 && tiles16 >= kMaskedUmmaBytes / (keys * 2 * row_bytes_of(fmt, head_dim));
   bool umma = pairs >= kMaskedUmmaPairs && large;
