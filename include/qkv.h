@@ -831,14 +831,14 @@ qkv_status qkv_prefix_attn(const qkv_prefix_desc* desc, void* stream);
  *   row_start     int32 [rows], at least 0, or NULL: 0. row_start >= row_end: the row sees nothing (o = 0, lse = -inf).
  *   row_end       int32 [rows] in [0, max_row_end].
  *   row_pos       int32 [rows] in [0, 2^30], or NULL: row_end - 1. Looked at for the window and the bias only, and not for
- *                 rows that see nothing.
+ *                 rows with row_start >= row_end.
  *   max_row_end   no row ends later; 0 <= max_row_end <= max_blocks * block_size and at most 2^30, else QKV_ERR_ARG. With
  *                 num_seqs and window it sizes the launch (a captured graph keeps it).
  *   window        0: none; else at least 1.
  *   softcap       0: none; else in [2^-20, 2^20] (else QKV_ERR_ARG).
  *   slopes        fp32 [num_q_heads], 4 B-aligned, or NULL: no bias.
- *   Flagged with QKV_DEV_BAD_INDEX: a row_seq outside [-1, num_seqs), a row_start, row_end or row_pos outside its range (the
- *   row is empty), and an unallocated block (id < 0) or a slot >= num_slots among the keys that a row sees (the key is masked).
+ *   Flagged with QKV_DEV_BAD_INDEX: a row_seq outside [-1, num_seqs), a row_start, row_end or (where it is looked at) row_pos
+ *   outside its range (the row is empty), and an unallocated block (id < 0) or a slot >= num_slots among the keys that a row sees (the key is masked).
  *   Blocks that no row sees may hold anything in the table.
  *   workspace     device scratch of workspace_bytes, 16 B-aligned; its contents need not be set. Too small a workspace is
  *                 QKV_ERR_ARG. Calls that overlap on the GPU -- on two streams, or replays of two captured graphs -- must

@@ -1074,7 +1074,7 @@ qkv_status qkv_masked_attn(const qkv_masked_desc* d, void* stream) {
   a.row_len = d->row_end;
   a.max_row_len = d->max_row_end;
   a.row_start = d->row_start;
-  a.row_pos = d->row_pos;
+  a.row_pos = d->window > 0 || d->slopes ? d->row_pos : nullptr;  // nothing else asks for positions
   a.window = d->window;
   a.softcap = d->softcap;
   a.slopes = d->slopes;
