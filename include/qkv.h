@@ -652,7 +652,8 @@ qkv_status qkv_append_axes(const qkv_append_axes_desc* desc, void* stream);
  *   value = code * scale in fp32 (E4M3: the layer's scale; 16-bit pools: the value itself); turned back, for pair i of
  *   token t (paired as for qkv_append_rope) with c, s of cos_sin at p = axis_pos[pair_axis[i], t]:
  *     a' = fl(fl(a c) + fl(b s)),  b' = fl(fl(b c) - fl(a s));
- *   then rounded once to the output's type. A 16-bit pool's rows into their own type are copied bit for bit.
+ *   then rounded once to the output's type. A 16-bit pool's values that are not turned are copied bit for bit into their own
+ *   type.
  *
  *   size          sizeof(qkv_read_desc), for the layout check (else QKV_ERR_ARG).
  *   fmt, k_cache, v_cache, k_scale, v_scale, k_scale_layer, v_scale_layer, num_slots, num_kv_heads, head_dim

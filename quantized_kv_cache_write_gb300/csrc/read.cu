@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kReadThreads) read_turned_kernel(const ReadArg
       uint2 p = a.out_type == QKV_OUT_F16 ? round4<true>(x) : round4<false>(x);
       uint2 q = a.out_type == QKV_OUT_F16 ? round4<true>(x + 4) : round4<false>(x + 4);
       const bool same = k16 && (FMT == QKV_F16) == (a.out_type == QKV_OUT_F16);
-      if (same && !is_k) p = lo[i], q = hi[i];
+      if (same && !(is_k && turns0)) p = lo[i];  // not turned: the bits as they are, a NaN's payload too
+      if (same && !(is_k && turns1)) q = hi[i];
       *reinterpret_cast<uint2*>(dst + d0) = p;
       *reinterpret_cast<uint2*>(dst + d1) = q;
     }
