@@ -491,7 +491,7 @@ qkv_status check_append(const qkv_append_desc* d, bool axes = false) {
   if (d->fmt == QKV_E4M3 && (!finite_positive(d->k_scale_layer) || !finite_positive(d->v_scale_layer)))
     return QKV_ERR_SCALE;
   if (d->num_tokens == 0) return QKV_OK;
-  // A launch of one row per lane group has at most append.cu's kSmallWarps warps; one of four rows T ceil(rows / 4) or
+  // A launch of one row per lane group has at most append.cuh's kSmallWarps warps; one of four rows T ceil(rows / 4) or
   // fewer, which is at most T rows / 2 (rows is 3 or more, or 2: one unit), so 2^32 warps, 2^30 blocks of four.
   const int64_t rows = static_cast<int64_t>(hq) + 2 * static_cast<int64_t>(d->num_kv_heads);
   if (rows > INT32_MAX || d->num_tokens > (int64_t(1) << 33) / rows) return QKV_ERR_ARG;

@@ -141,7 +141,7 @@ __device__ __forceinline__ RowRange row_range(const PrefixArgs& a, int64_t r, bo
 }
 // tanh, off by less than 2^-20 of itself: up to kTanhSmall a polynomial in z^2 fitted to tanh(z) / z by least squares on the
 // relative error (2^-22.6 with fp32 steps), elsewhere one exponential and one reciprocal, 1 - 2 / (1 + e^2z), off by less
-// than 2^-21, with the limits at infinities.
+// than 2^-21, with the limits at infinities. Both are far below the 2^-11 (bf16 pools 2^-8) that a weight is rounded by.
 constexpr float kTanhSmall = 0.75f;
 __device__ constexpr float kTanh[6] = {1.0f, -0.33332958817481995f, 0.1332540661096573f, -0.05334442853927612f, 0.01958290860056877f, -0.004716257099062204f};
 __device__ __forceinline__ float tanh_series(float z) {
@@ -701,7 +701,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
           S(n, p, k) = e;
         }
     }
-    // kWide: the A operand, pairs by keys; else the B operand, keys by pairs (a lane's pairs were the columns)
+    // kWide: the A operand, pairs by keys; else the B operand, keys by pairs (a lane's pairs were the columns). Rounded once, to
+    // the 16 bits of the MMA's operands (bf16 for a bf16 pool, whose values pass fp16's range); their sum is of them unrounded.
     uint32_t pa[NH][2 * KL];
 #pragma unroll
     for (int n = 0; n < 2 * NH; ++n)

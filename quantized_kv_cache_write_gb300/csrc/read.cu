@@ -13,7 +13,8 @@
 //
 // Bound by memory: a record in and 2 or 4 B out per value. Measured: 131072 tokens of an int8 side pool, one head of 256, to
 // bf16 45 us (4.5 TB/s); with 4 B loads and a warp per row 58. 65536 such tokens turned back, with 64 MB of angles, 58
-// us (angles asked for with the rows: the same, and bf16 in 8 heads of 128 56 -> 62).
+// us, 2.3 times the bytes' time (angles asked for with the rows: the same, and bf16 in 8 heads of 128 56 -> 62): a lane's 4 B
+// loads, and two dependent loads (positions, angles) per row before its stores.
 #include "rope.cuh"
 
 namespace qkv {
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kReadThreads) read_turned_kernel(const ReadArg
 // replayed from a graph (warps with one): int8 side, one head of 256: 1024 (1024) 2.6 | 4.2, 16384 (16384) 6.1 | 6.7, 32768
 // (32768) 9.9 | 10.4; turned back: 16384 (32768) 14.3 | 14.3, 32768 (65536) 26.1 | 25.1; bf16, 8 heads of 128: 2048 (16384)
 // 5.2 | 5.4, 8192 (65536) 15.1 | 14.2, 32768 73 | 60.
-constexpr int64_t kSmallWarps = 32768;
+constexpr int64_t kSmallReadWarps = 32768;
 
 template <int FMT, int HD>
 cudaError_t launch(const ReadArgs& a, cudaStream_t stream) {
@@ -243,7 +244,7 @@ cudaError_t launch(const ReadArgs& a, cudaStream_t stream) {
   const bool turned = a.cos_sin != nullptr && a.k_out != nullptr;
   const int lanes = turned ? HD / 8 : FMT == QKV_BF16 || FMT == QKV_F16 ? HD / 8 : HD / 16;  // of a row
   const int64_t single = (rows * lanes + 31) / 32;
-  const bool one = single <= kSmallWarps;
+  const bool one = single <= kSmallReadWarps;
   const unsigned grid = static_cast<unsigned>(((one ? single : (single + 3) / 4) * 32 + kReadThreads - 1) / kReadThreads);
   if (!turned) {
     auto off = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
