@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
   if (MASK) {
     const bool sees = my_lo < my_hi;
     const int lo = __reduce_min_sync(0xffffffffu, sees ? my_lo : INT_MAX), hi = __reduce_max_sync(0xffffffffu, my_hi);
-    own_min = __reduce_min_sync(0xffffffffu, my_row >= 0 ? my_hi : INT_MAX);
+    own_min = __reduce_min_sync(0xffffffffu, sees ? my_hi : INT_MAX);  // of the rows that see anything
     own_max = __reduce_max_sync(0xffffffffu, my_lo);
     const int first = lo < hi ? lo & ~(TK - 1) : 0, np = static_cast<int>(parts);
     const int per = ((hi - first + np - 1) / np + TK * kWarps - 1) / (TK * kWarps) * (TK * kWarps);
@@ -861,7 +861,8 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
         const bool none = sM[w][lane] == -INFINITY && sL[w][lane] == 0.f;
         sW[w][lane] = none ? -1.f : F::kInt8 ? al * pow2f(max(sEu[w][lane] - top, -126)) : al;
       }
-      const bool any = state != kEmptyRow && (m != -INFINITY || sum != sum);
+      // MASK: tiles that all rows with keys see whole are not masked for those without
+      const bool any = state != kEmptyRow && !(MASK && my_own == kEmptyRow) && (m != -INFINITY || sum != sum);
       sInv[lane] = any ? (direct && FMT == QKV_E4M3 ? a.v_scale_layer : 1.f) / sum : 0.f;
       if (state != kPadRow) {
         const int64_t part_at = static_cast<int64_t>(own_part ? a.prefix_parts + part : part) * a.rows * a.num_q_heads + pair;

@@ -978,7 +978,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         const bool in = flat < out_flats;
         const uint32_t row = in ? flat / G : 0;
         const float sum = (all[0] + all[1]) + (all[2] + all[3]);
-        const bool any = sum != 0.f;  // NaN too
+        bool any = sum != 0.f;  // NaN too
+        if (MASK) {  // blocks that all rows with keys see whole are not masked for those without
+          const uint2 lim = lds64(sb + U::kTab + 16 * r);
+          any = any && static_cast<int>(lim.x) < static_cast<int>(lim.y);
+        }
         float inv = any ? 1.f / sum : 0.f;
         int64_t part_at = 0;
         int at = static_cast<int>(row * a.num_q_heads + out_h * G + (flat - row * G));
@@ -1101,10 +1105,11 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         }
         if (!more) break;
         begun = true;
-        // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see
+        // ---- the pairs' masks: of each row once (by the first part's threads), and what all of a warp's rows see that see
+        // anything
         if (wg == 0) sts128(sb + U::kTab + 16 * r, make_uint4(range.lo, range.hi, range.near, __float_as_uint(-slope * kLog2e)));
         const int lo = __reduce_max_sync(0xffffffffu, mask_flat < flats ? range.lo : 0);
-        const int hi = __reduce_min_sync(0xffffffffu, mask_flat < flats ? range.hi : INT_MAX);
+        const int hi = __reduce_min_sync(0xffffffffu, mask_flat < flats && range.lo < range.hi ? range.hi : INT_MAX);
         if (lane == 0) sts32(sb + U::kAll + 8 * warp, lo), sts32(sb + U::kAll + 8 * warp + 4, hi);
         __syncwarp();
         if (vote(!ok)) break;  // the table is read from here on
