@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, Geom<FMT, HD, NP>::kMinBlocks) prefi
       const int near = __shfl_sync(0xffffffffu, range.near, t & 31), pos = __shfl_sync(0xffffffffu, range.pos, t & 31);
       if (my_row < 0) my_lo = my_hi = 0;
       if (warp == 0 && lane < NP) {
-        const float slope = my_row >= 0 && a.slopes != nullptr ? __ldg(a.slopes + h * G + my_g) : 0.f;
+        const float slope = my_lo < my_hi && a.slopes != nullptr ? __ldg(a.slopes + h * G + my_g) : 0.f;
         sLo[lane] = my_lo, sHi[lane] = my_hi, sNear[lane] = near;
         sSlope[lane] = -slope * kLog2e;
         sFar[lane] = near == pos ? 0.f : -slope * fabsf(static_cast<float>(pos - near));

@@ -871,6 +871,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
           const uint32_t row = mask_flat / G;
           if (MODE == kAdjusted && a.slopes != nullptr) slope = __ldg(a.slopes + h * G + (mask_flat - row * G));
           range = row_range(a, row0 + static_cast<int64_t>(row), false);
+          if (range.lo >= range.hi) slope = 0.f;  // no bias that rises from block to block, and the reference with it
         }
       }
     };
@@ -977,12 +978,12 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         const uint32_t flat = flat0 + t * CG * kTileM;
         const bool in = flat < out_flats;
         const uint32_t row = in ? flat / G : 0;
-        const float sum = (all[0] + all[1]) + (all[2] + all[3]);
-        bool any = sum != 0.f;  // NaN too
+        float sum = (all[0] + all[1]) + (all[2] + all[3]);
         if (MASK) {  // blocks that all rows with keys see whole are not masked for those without
-          const uint2 lim = lds64(sb + U::kTab + 16 * r);
-          any = any && static_cast<int>(lim.x) < static_cast<int>(lim.y);
+          const uint2 lim = lds64(here(sb) + U::kTab + 16 * (here(threadIdx.x) & 127));
+          if (lim.x >= lim.y) sum = 0.f;
         }
+        const bool any = sum != 0.f;  // NaN too
         float inv = any ? 1.f / sum : 0.f;
         int64_t part_at = 0;
         int at = static_cast<int>(row * a.num_q_heads + out_h * G + (flat - row * G));
@@ -1109,7 +1110,7 @@ __global__ void __launch_bounds__(Umma<FMT, HD, NT, CG, MODE != kPrefix>::kThrea
         // anything
         if (wg == 0) sts128(sb + U::kTab + 16 * r, make_uint4(range.lo, range.hi, range.near, __float_as_uint(-slope * kLog2e)));
         const int lo = __reduce_max_sync(0xffffffffu, mask_flat < flats ? range.lo : 0);
-        const int hi = __reduce_min_sync(0xffffffffu, mask_flat < flats && range.lo < range.hi ? range.hi : INT_MAX);
+        const int hi = __reduce_min_sync(0xffffffffu, range.lo < range.hi ? range.hi : INT_MAX);
         if (lane == 0) sts32(sb + U::kAll + 8 * warp, lo), sts32(sb + U::kAll + 8 * warp + 4, hi);
         __syncwarp();
         if (vote(!ok)) break;  // the table is read from here on
